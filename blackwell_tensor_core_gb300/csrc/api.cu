@@ -23,6 +23,7 @@
 #include "../../include/bwgemm.h"
 #include "layout.h"
 #include "params.h"
+#include "runtime.h"
 
 namespace bwg {
 cudaError_t set_gemm_attributes(size_t smem);
@@ -1107,6 +1108,31 @@ bwg_status run_small_m_noalloc(const void* A, const void* B, void* D, int M, int
 }
 
 }  // namespace
+
+namespace bwg {
+
+bwg_status runtime_device(Runtime* out) {
+  DeviceState* st = nullptr;
+  const bwg_status s = ensure_device(&st);
+  if (s != BWG_OK) return s;
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) {
+    cudaGetLastError();
+    return BWG_ERR_CUDA;
+  }
+  *out = Runtime{dev, st->sm_count, st->max_smem, st->err, g_timeout_ns.load()};
+  return BWG_OK;
+}
+
+bool runtime_map(CUtensorMap* m, const void* ptr, CUtensorMapDataType dtype, int rank,
+                 const uint64_t* dims, const uint64_t* strides, const uint32_t* box,
+                 CUtensorMapSwizzle swizzle) {
+  return get_map_nd(m, ptr, dtype, rank, dims, strides, box, swizzle);
+}
+
+bwg_status runtime_status(cudaError_t e) { return launch_status(e); }
+
+}  // namespace bwg
 
 // ================================================================ C ABI ====
 

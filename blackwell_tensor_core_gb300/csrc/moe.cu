@@ -1,0 +1,600 @@
+// The routed rows' way to their experts and back: a stable counting sort of
+// the (token, expert) pairs, the dispatch of token rows into expert order,
+// the weighted combine into token order, and the gradient of each.
+//
+// With T tokens, k experts a token and pairs p = t * k + j:
+//   sort      order[r] = the pair at sorted row r, position[p] = its inverse,
+//             offsets[e] = the first row of expert e (offsets[E] = n, the rows
+//             that have an expert; pairs without one are sorted behind them)
+//   dispatch  rows[position[p]] = x[t], zero where position[p] >= n
+//   combine   y[t] = sum_j w[p] rows[position[p]] over position[p] < n
+// and, d for the gradient of a scalar loss,
+//   dispatch' dx[t] = sum_j d_rows[position[p]]   (combine without weights)
+//   combine'  d_rows[position[p]] = w[p] dy[t],  dw[p] = <dy[t], rows[position[p]]>
+// A pair without an expert takes part in none of the sums, whatever its row
+// holds (NaN included), and its d_rows and dw are zero.
+//
+// Every kernel walks the pairs in token order, so that a token's row is read
+// once for all its k copies, and adds in the order j = 0 .. k-1 in FP32:
+// there are no atomics and results do not depend on the launch.
+#include <algorithm>
+#include <cstdint>
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+
+#include "../../include/bwgemm.h"
+#include "params.h"
+#include "ptx.cuh"
+#include "runtime.h"
+
+namespace bwg {
+namespace {
+
+constexpr int kMaxExperts = 1024;
+
+// The int at `p` (this CTA's shared memory) in the shared memory of CTA `rank`.
+__device__ __forceinline__ int ld_cluster(const int* p, uint32_t rank) {
+  return static_cast<int>(ld_shared_cluster_u32(mapa_shared(smem_u32(p), rank)));
+}
+
+// A position outside [0, pairs) is not followed; it is reported through the
+// device error word, with the kind of a broken offsets array.
+__device__ __forceinline__ void record_bad_position(unsigned long long* err) {
+  atomicCAS(err, 0ull, (kFaultBadOffsets << 56) | (static_cast<unsigned long long>(blockIdx.x & 0xFFFFFFu) << 16));
+}
+
+// ------------------------------------------------------------------ sort ----
+// One cluster of C CTAs of W warps; warp g of all C * W takes the g-th
+// contiguous run of pairs.  Pass 1 counts each warp's pairs per expert in a
+// shared-memory row of its own (lanes with the same expert are found with
+// match.any and counted by one of them, so no two lanes write one counter);
+// the counts become starts by prefix sums over warps, over CTAs (through
+// distributed shared memory) and over experts; pass 2 hands out the rows in
+// pair order.
+// What bounds it: latency.  The ids are 0.3 MB for the 4096 x 8 layer; one
+// launch with its counts on chip replaces three passes through global memory.
+constexpr int kSortMaxWarps = 32;
+constexpr int kSortAhead = 4;  // id loads in flight per lane
+
+template <class ID>
+__global__ void __launch_bounds__(kSortMaxWarps * 32)
+    moe_sort_kernel(const ID* __restrict__ ids, int pairs, int E, int n_cta, int* __restrict__ offsets,
+                    int* __restrict__ order, int* __restrict__ position) {
+  extern __shared__ int sm[];
+  const int W = static_cast<int>(blockDim.x >> 5);
+  const int buckets = E + 1;         // bucket E: pairs without an expert
+  int* hist = sm;                    // [W][buckets]
+  int* total = sm + W * buckets;     // [buckets] this CTA's counts
+  int* start = total + buckets;      // [buckets] this CTA's first row in each bucket
+  int* part = start + buckets;       // [32] scan partials, [32] = rows with an expert
+  const int lane = static_cast<int>(threadIdx.x & 31u);
+  const int warp = static_cast<int>(threadIdx.x >> 5);
+  const uint32_t rank = n_cta > 1 ? cluster_ctarank() : 0u;
+
+  for (int i = static_cast<int>(threadIdx.x); i < W * buckets; i += static_cast<int>(blockDim.x)) hist[i] = 0;
+  __syncthreads();
+
+  const long long runs = static_cast<long long>(n_cta) * W;
+  const long long per = ((pairs + runs - 1) / runs + 31) / 32 * 32;
+  const long long first = (static_cast<long long>(rank) * W + warp) * per;
+  const long long last = first + per < pairs ? first + per : pairs;
+  int* mine = hist + warp * buckets;
+  const unsigned below = (1u << lane) - 1u;
+
+  auto load = [&](long long p) -> int {
+    if (p >= last) return -1;
+    const ID v = ids[p];
+    return v >= 0 && v < static_cast<ID>(E) ? static_cast<int>(v) : E;
+  };
+  for (long long p0 = first; p0 < last; p0 += 32 * kSortAhead) {
+    int key[kSortAhead];
+#pragma unroll
+    for (int a = 0; a < kSortAhead; ++a) key[a] = load(p0 + 32 * a + lane);
+#pragma unroll
+    for (int a = 0; a < kSortAhead; ++a) {
+      const unsigned same = __match_any_sync(0xffffffffu, key[a]);
+      if (key[a] >= 0 && (same & below) == 0) mine[key[a]] += __popc(same);
+      __syncwarp();
+    }
+  }
+  __syncthreads();
+  // warps' counts -> each warp's start inside the CTA's share of the bucket
+  for (int b = static_cast<int>(threadIdx.x); b < buckets; b += static_cast<int>(blockDim.x)) {
+    int run = 0;
+    for (int w = 0; w < W; ++w) {
+      const int c = hist[w * buckets + b];
+      hist[w * buckets + b] = run;
+      run += c;
+    }
+    total[b] = run;
+  }
+  if (n_cta > 1)
+    cluster_sync_all();
+  else
+    __syncthreads();
+  // every CTA: all CTAs' counts, the part of lower ranks, and the exclusive
+  // sum over experts, blockDim.x experts at a time
+  int carry = 0;
+  for (int b0 = 0; b0 < E; b0 += static_cast<int>(blockDim.x)) {
+    const int b = b0 + static_cast<int>(threadIdx.x);
+    int all = 0, before = 0;
+    if (b < E) {
+      for (int c = 0; c < n_cta; ++c) {
+        const int v = n_cta > 1 ? ld_cluster(total + b, static_cast<uint32_t>(c)) : total[b];
+        if (c < static_cast<int>(rank)) before += v;
+        all += v;
+      }
+    }
+    int incl = all;
+    for (int d = 1; d < 32; d <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, incl, d);
+      if (lane >= d) incl += y;
+    }
+    if (lane == 31) part[warp] = incl;
+    __syncthreads();
+    if (warp == 0) {
+      int v = lane < W ? part[lane] : 0;
+      for (int d = 1; d < 32; d <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, v, d);
+        if (lane >= d) v += y;
+      }
+      part[lane] = v;
+    }
+    __syncthreads();
+    const int excl = carry + (warp > 0 ? part[warp - 1] : 0) + incl - all;
+    if (b < E) {
+      start[b] = excl + before;
+      if (rank == 0) offsets[b] = excl;
+    }
+    carry += part[31];
+    __syncthreads();
+  }
+  if (threadIdx.x == 0) {
+    int before = 0;
+    for (int c = 0; c < static_cast<int>(rank); ++c) before += ld_cluster(total + E, static_cast<uint32_t>(c));
+    start[E] = carry + before;
+    if (rank == 0) offsets[E] = carry;
+  }
+  __syncthreads();
+  for (long long p0 = first; p0 < last; p0 += 32 * kSortAhead) {
+    int key[kSortAhead];
+#pragma unroll
+    for (int a = 0; a < kSortAhead; ++a) key[a] = load(p0 + 32 * a + lane);
+#pragma unroll
+    for (int a = 0; a < kSortAhead; ++a) {
+      const unsigned same = __match_any_sync(0xffffffffu, key[a]);
+      if (key[a] >= 0) {
+        const int at = start[key[a]] + mine[key[a]] + __popc(same & below);
+        const int p = static_cast<int>(p0 + 32 * a + lane);
+        position[p] = at;
+        order[at] = p;
+      }
+      __syncwarp();
+      if (key[a] >= 0 && (same & below) == 0) mine[key[a]] += __popc(same);
+      __syncwarp();
+    }
+  }
+  // a CTA's counts may be read by its peers until all have passed their sums
+  if (n_cta > 1) cluster_sync_all();
+}
+
+// ------------------------------------------------------------------ rows ----
+
+struct MoeRows {
+  const void* src;      // dispatch: x; combine: rows; combine gradient: dy
+  const void* rows_in;  // combine gradient: rows
+  void* dst;            // dispatch: rows; combine: y; combine gradient: d_rows
+  const float* weights; // combine: [pairs] or nullptr (all 1)
+  float* d_weights;
+  const int* position;
+  const int* kept;      // &offsets[E]
+  long long ld_src, ld_rows, ld_dst;  // in elements
+  int T, k, vecs;       // vecs: vectors a row
+  int pairs;            // T * k: rows of the expert order
+  unsigned long long* err;
+};
+
+// A vector of VB bytes of elements T, as FP32 values and back.
+template <int VB>
+struct Raw;
+template <>
+struct Raw<16> {
+  using type = uint4;
+};
+template <>
+struct Raw<8> {
+  using type = uint2;
+};
+template <>
+struct Raw<4> {
+  using type = uint32_t;
+};
+template <>
+struct Raw<2> {
+  using type = uint16_t;
+};
+
+template <class T, int VB>
+union Vec {
+  typename Raw<VB>::type raw;
+  T e[VB / sizeof(T)];
+  __device__ Vec() {}
+};
+
+__device__ __forceinline__ float to_f32(float v) { return v; }
+__device__ __forceinline__ float to_f32(__nv_bfloat16 v) { return __bfloat162float(v); }
+__device__ __forceinline__ float to_f32(__half v) { return __half2float(v); }
+__device__ __forceinline__ void from_f32(float& d, float v) { d = v; }
+__device__ __forceinline__ void from_f32(__nv_bfloat16& d, float v) { d = __float2bfloat16_rn(v); }
+__device__ __forceinline__ void from_f32(__half& d, float v) { d = __float2half_rn(v); }
+
+constexpr int kPairsAhead = 8;  // pairs of a token handled together
+
+// Block (t, chunk): a vector of token t per thread, stored to its k rows.
+template <int VB>
+__global__ void moe_dispatch_kernel(const __grid_constant__ MoeRows p, int chunks, int elt) {
+  using R = typename Raw<VB>::type;
+  const int t = static_cast<int>(blockIdx.x / static_cast<unsigned>(chunks));
+  const int v = static_cast<int>(blockIdx.x % static_cast<unsigned>(chunks)) * static_cast<int>(blockDim.x) +
+                static_cast<int>(threadIdx.x);
+  if (v >= p.vecs) return;
+  const R x = reinterpret_cast<const R*>(static_cast<const char*>(p.src) + t * p.ld_src * elt)[v];
+  const int kept = *p.kept;
+  const int* pos = p.position + static_cast<long long>(t) * p.k;
+  for (int j = 0; j < p.k; ++j) {
+    const int r = pos[j];
+    if (static_cast<unsigned>(r) >= static_cast<unsigned>(p.pairs)) {
+      if (threadIdx.x == 0) record_bad_position(p.err);
+      continue;
+    }
+    R out = x;
+    if (r >= kept) out = R{};
+    reinterpret_cast<R*>(static_cast<char*>(p.dst) + r * p.ld_dst * elt)[v] = out;
+  }
+}
+
+// Block (t, chunk): a vector of y[t] per thread, from its k rows.
+template <class T, int VB>
+__global__ void moe_combine_kernel(const __grid_constant__ MoeRows p, int chunks) {
+  using R = typename Raw<VB>::type;
+  constexpr int N = VB / static_cast<int>(sizeof(T));
+  const int t = static_cast<int>(blockIdx.x / static_cast<unsigned>(chunks));
+  const int v = static_cast<int>(blockIdx.x % static_cast<unsigned>(chunks)) * static_cast<int>(blockDim.x) +
+                static_cast<int>(threadIdx.x);
+  if (v >= p.vecs) return;
+  const int kept = min(*p.kept, p.pairs);
+  const long long p0 = static_cast<long long>(t) * p.k;
+  float acc[N];
+#pragma unroll
+  for (int i = 0; i < N; ++i) acc[i] = 0.f;
+  for (int j0 = 0; j0 < p.k; j0 += kPairsAhead) {
+    Vec<T, VB> x[kPairsAhead];
+    float w[kPairsAhead];
+    bool has[kPairsAhead];
+#pragma unroll
+    for (int a = 0; a < kPairsAhead; ++a) {
+      const int j = j0 + a;
+      const int r = j < p.k ? p.position[p0 + j] : kept;
+      if (static_cast<unsigned>(r) > static_cast<unsigned>(p.pairs) && threadIdx.x == 0) record_bad_position(p.err);
+      has[a] = r >= 0 && r < kept;
+      if (has[a]) {
+        x[a].raw = reinterpret_cast<const R*>(static_cast<const T*>(p.src) + r * p.ld_src)[v];
+        w[a] = p.weights != nullptr ? p.weights[p0 + j] : 1.f;
+      }
+    }
+#pragma unroll
+    for (int a = 0; a < kPairsAhead; ++a)
+      if (has[a]) {
+#pragma unroll
+        for (int i = 0; i < N; ++i) acc[i] = fmaf(w[a], to_f32(x[a].e[i]), acc[i]);
+      }
+  }
+  Vec<T, VB> y;
+#pragma unroll
+  for (int i = 0; i < N; ++i) from_f32(y.e[i], acc[i]);
+  reinterpret_cast<R*>(static_cast<T*>(p.dst) + t * p.ld_dst)[v] = y.raw;
+}
+
+constexpr int kGradThreads = 256;
+
+// Block t: d_rows of token t's k rows and the k inner products, the row kept
+// in no more than one vector per thread and pair at a time.
+template <class T, int VB>
+__global__ void __launch_bounds__(kGradThreads) moe_combine_grad_kernel(const __grid_constant__ MoeRows p) {
+  using R = typename Raw<VB>::type;
+  constexpr int N = VB / static_cast<int>(sizeof(T));
+  __shared__ float sums[kGradThreads / 32][kPairsAhead];
+  const int t = static_cast<int>(blockIdx.x);
+  const int kept = min(*p.kept, p.pairs);
+  const long long p0 = static_cast<long long>(t) * p.k;
+  const R* dy = reinterpret_cast<const R*>(static_cast<const T*>(p.src) + t * p.ld_src);
+  for (int j0 = 0; j0 < p.k; j0 += kPairsAhead) {
+    int row[kPairsAhead];
+    float w[kPairsAhead], dot[kPairsAhead];
+#pragma unroll
+    for (int a = 0; a < kPairsAhead; ++a) {
+      const bool in = j0 + a < p.k;
+      row[a] = in ? p.position[p0 + j0 + a] : -1;
+      if (in && static_cast<unsigned>(row[a]) >= static_cast<unsigned>(p.pairs)) {
+        if (threadIdx.x == 0) record_bad_position(p.err);
+        row[a] = -1;
+      }
+      w[a] = row[a] >= 0 && row[a] < kept ? p.weights[p0 + j0 + a] : 0.f;
+      dot[a] = 0.f;
+    }
+    for (int v = static_cast<int>(threadIdx.x); v < p.vecs; v += kGradThreads) {
+      Vec<T, VB> g;
+      g.raw = dy[v];
+      Vec<T, VB> x[kPairsAhead];
+#pragma unroll
+      for (int a = 0; a < kPairsAhead; ++a)
+        if (row[a] >= 0 && row[a] < kept)
+          x[a].raw = reinterpret_cast<const R*>(static_cast<const T*>(p.rows_in) + row[a] * p.ld_rows)[v];
+#pragma unroll
+      for (int a = 0; a < kPairsAhead; ++a) {
+        if (row[a] < 0) continue;
+        Vec<T, VB> d;
+        if (row[a] < kept) {
+#pragma unroll
+          for (int i = 0; i < N; ++i) {
+            dot[a] = fmaf(to_f32(x[a].e[i]), to_f32(g.e[i]), dot[a]);
+            from_f32(d.e[i], w[a] * to_f32(g.e[i]));
+          }
+        } else {
+          d.raw = R{};
+        }
+        reinterpret_cast<R*>(static_cast<T*>(p.dst) + row[a] * p.ld_dst)[v] = d.raw;
+      }
+    }
+#pragma unroll
+    for (int a = 0; a < kPairsAhead; ++a) {
+      for (int d = 16; d > 0; d >>= 1) dot[a] += __shfl_xor_sync(0xffffffffu, dot[a], d);
+      if ((threadIdx.x & 31u) == 0) sums[threadIdx.x >> 5][a] = dot[a];
+    }
+    __syncthreads();
+    const int a = static_cast<int>(threadIdx.x);
+    if (a < kPairsAhead && j0 + a < p.k) {
+      float s = 0.f;
+      for (int w2 = 0; w2 < kGradThreads / 32; ++w2) s += sums[w2][a];
+      p.d_weights[p0 + j0 + a] = s;
+    }
+    __syncthreads();
+  }
+}
+
+// Widest vector (16, 8, 4 or 2 bytes, at least an element) in which every
+// row of H elements can be read and written whole.
+int vector_bytes(int H, int elt, std::initializer_list<const void*> ptrs, std::initializer_list<long long> lds) {
+  uintptr_t bits = static_cast<uintptr_t>(static_cast<long long>(H) * elt);
+  for (const void* q : ptrs) bits |= reinterpret_cast<uintptr_t>(q);
+  for (long long ld : lds) bits |= static_cast<uintptr_t>(ld * elt);
+  for (int vb = 16; vb > elt; vb >>= 1)
+    if ((bits & static_cast<uintptr_t>(vb - 1)) == 0) return vb;
+  return elt;
+}
+
+int elt_bytes(int dtype) { return dtype == BWG_OUT_FP32 ? 4 : 2; }
+
+bool dtype_ok(int dtype) { return dtype == BWG_OUT_BF16 || dtype == BWG_OUT_FP16 || dtype == BWG_OUT_FP32; }
+
+bool elt_aligned(const void* q, int elt) { return (reinterpret_cast<uintptr_t>(q) & static_cast<uintptr_t>(elt - 1)) == 0; }
+
+// Arguments that the row kernels share; *empty: nothing to do.
+bwg_status check_rows(int dtype, int T, int H, int k, int E, const int* position, const int* offsets, bool* empty) {
+  *empty = false;
+  if (!dtype_ok(dtype) || T < 0 || H < 0 || k < 1 || E < 1) return BWG_ERR_INVALID_ARG;
+  if (E > kMaxExperts || static_cast<long long>(T) * k > 0x7fffffffLL) return BWG_ERR_UNSUPPORTED;
+  if (T == 0 || H == 0) {
+    *empty = true;
+    return BWG_OK;
+  }
+  if (position == nullptr || offsets == nullptr) return BWG_ERR_INVALID_ARG;
+  return BWG_OK;
+}
+
+// Threads of a row block and blocks a row: enough threads for one vector each.
+void row_shape(int vecs, int* threads, int* chunks) {
+  *threads = vecs >= 256 ? 256 : (vecs + 31) / 32 * 32;
+  *chunks = (vecs + *threads - 1) / *threads;
+}
+
+template <class T>
+cudaError_t launch_combine(const MoeRows& p, int vb, unsigned blocks, int threads, int chunks, cudaStream_t s) {
+  switch (vb) {
+    case 16: moe_combine_kernel<T, 16><<<blocks, threads, 0, s>>>(p, chunks); break;
+    case 8: moe_combine_kernel<T, 8><<<blocks, threads, 0, s>>>(p, chunks); break;
+    case 4: moe_combine_kernel<T, 4><<<blocks, threads, 0, s>>>(p, chunks); break;
+    default:
+      if constexpr (sizeof(T) == 2) moe_combine_kernel<T, 2><<<blocks, threads, 0, s>>>(p, chunks);
+  }
+  return cudaGetLastError();
+}
+
+template <class T>
+cudaError_t launch_combine_grad(const MoeRows& p, int vb, cudaStream_t s) {
+  const unsigned blocks = static_cast<unsigned>(p.T);
+  switch (vb) {
+    case 16: moe_combine_grad_kernel<T, 16><<<blocks, kGradThreads, 0, s>>>(p); break;
+    case 8: moe_combine_grad_kernel<T, 8><<<blocks, kGradThreads, 0, s>>>(p); break;
+    case 4: moe_combine_grad_kernel<T, 4><<<blocks, kGradThreads, 0, s>>>(p); break;
+    default:
+      if constexpr (sizeof(T) == 2) moe_combine_grad_kernel<T, 2><<<blocks, kGradThreads, 0, s>>>(p);
+  }
+  return cudaGetLastError();
+}
+
+bwg_status run_combine(const void* rows, int dtype, int T, int H, int ldr, int k, const float* weights,
+                       const int* position, const int* offsets, int E, void* Y, int ldy, cudaStream_t s) {
+  bool empty;
+  bwg_status st = check_rows(dtype, T, H, k, E, position, offsets, &empty);
+  if (st != BWG_OK || empty) return st;
+  if (rows == nullptr || Y == nullptr || ldr < H || ldy < H) return BWG_ERR_INVALID_ARG;
+  const int elt = elt_bytes(dtype);
+  if (!elt_aligned(rows, elt) || !elt_aligned(Y, elt)) return BWG_ERR_ALIGNMENT;
+  Runtime rt;
+  if ((st = runtime_device(&rt)) != BWG_OK) return st;
+  const int vb = vector_bytes(H, elt, {rows, Y}, {ldr, ldy});
+  MoeRows p = {};
+  p.src = rows;
+  p.dst = Y;
+  p.weights = weights;
+  p.position = position;
+  p.kept = offsets + E;
+  p.ld_src = ldr;
+  p.ld_dst = ldy;
+  p.T = T;
+  p.k = k;
+  p.pairs = T * k;
+  p.err = rt.err;
+  p.vecs = static_cast<int>(static_cast<long long>(H) * elt / vb);
+  int threads, chunks;
+  row_shape(p.vecs, &threads, &chunks);
+  const long long blocks = static_cast<long long>(T) * chunks;
+  if (blocks > 0x7fffffffLL) return BWG_ERR_UNSUPPORTED;
+  const unsigned b = static_cast<unsigned>(blocks);
+  const cudaError_t e = dtype == BWG_OUT_FP32   ? launch_combine<float>(p, vb, b, threads, chunks, s)
+                        : dtype == BWG_OUT_BF16 ? launch_combine<__nv_bfloat16>(p, vb, b, threads, chunks, s)
+                                                : launch_combine<__half>(p, vb, b, threads, chunks, s);
+  return runtime_status(e);
+}
+
+template <class ID>
+cudaError_t launch_sort(const void* ids, int pairs, int E, int* offsets, int* order, int* position, cudaStream_t s) {
+  // One CTA up to 4096 pairs, a warp for each 128 of them; a cluster of 8
+  // beyond, whose 256 warps then have at least 16 pairs each.
+  const int n_cta = pairs <= 4096 ? 1 : 8;
+  const int warps = n_cta > 1 ? kSortMaxWarps : std::min(kSortMaxWarps, std::max(4, (pairs + 127) / 128));
+  const size_t smem = (static_cast<size_t>(warps + 2) * (E + 1) + 33) * sizeof(int);
+  if (smem > 48 * 1024) {
+    const cudaError_t a = cudaFuncSetAttribute(moe_sort_kernel<ID>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                               static_cast<int>(smem));
+    if (a != cudaSuccess) return a;
+  }
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(n_cta), 1, 1);
+  cfg.blockDim = dim3(static_cast<unsigned>(warps * 32), 1, 1);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = static_cast<unsigned>(n_cta);
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, moe_sort_kernel<ID>, static_cast<const ID*>(ids), pairs, E, n_cta, offsets, order,
+                            position);
+}
+
+}  // namespace
+}  // namespace bwg
+
+using namespace bwg;
+
+extern "C" {
+
+bwg_status moe_sort(const void* expert_ids, int id_bytes, int pairs, int E, int* offsets, int* order, int* position,
+                    void* stream) {
+  if ((id_bytes != 4 && id_bytes != 8) || pairs < 0 || E < 1 || offsets == nullptr) return BWG_ERR_INVALID_ARG;
+  if (E > kMaxExperts) return BWG_ERR_UNSUPPORTED;
+  if (pairs > 0 && (expert_ids == nullptr || order == nullptr || position == nullptr)) return BWG_ERR_INVALID_ARG;
+  if (!elt_aligned(expert_ids, id_bytes)) return BWG_ERR_ALIGNMENT;
+  Runtime rt;
+  const bwg_status st = runtime_device(&rt);
+  if (st != BWG_OK) return st;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  return runtime_status(id_bytes == 8 ? launch_sort<long long>(expert_ids, pairs, E, offsets, order, position, s)
+                                      : launch_sort<int>(expert_ids, pairs, E, offsets, order, position, s));
+}
+
+bwg_status moe_dispatch(const void* X, int dtype, int T, int H, int ldx, int k, const int* position,
+                        const int* offsets, int E, void* rows, int ldr, void* stream) {
+  bool empty;
+  bwg_status st = check_rows(dtype, T, H, k, E, position, offsets, &empty);
+  if (st != BWG_OK || empty) return st;
+  if (X == nullptr || rows == nullptr || ldx < H || ldr < H) return BWG_ERR_INVALID_ARG;
+  const int elt = elt_bytes(dtype);
+  if (!elt_aligned(X, elt) || !elt_aligned(rows, elt)) return BWG_ERR_ALIGNMENT;
+  Runtime rt;
+  if ((st = runtime_device(&rt)) != BWG_OK) return st;
+  const int vb = vector_bytes(H, elt, {X, rows}, {ldx, ldr});
+  MoeRows p = {};
+  p.src = X;
+  p.dst = rows;
+  p.position = position;
+  p.kept = offsets + E;
+  p.ld_src = ldx;
+  p.ld_dst = ldr;
+  p.T = T;
+  p.k = k;
+  p.pairs = T * k;
+  p.err = rt.err;
+  p.vecs = static_cast<int>(static_cast<long long>(H) * elt / vb);
+  int threads, chunks;
+  row_shape(p.vecs, &threads, &chunks);
+  const long long blocks = static_cast<long long>(T) * chunks;
+  if (blocks > 0x7fffffffLL) return BWG_ERR_UNSUPPORTED;
+  const unsigned b = static_cast<unsigned>(blocks);
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  switch (vb) {
+    case 16: moe_dispatch_kernel<16><<<b, threads, 0, s>>>(p, chunks, elt); break;
+    case 8: moe_dispatch_kernel<8><<<b, threads, 0, s>>>(p, chunks, elt); break;
+    case 4: moe_dispatch_kernel<4><<<b, threads, 0, s>>>(p, chunks, elt); break;
+    default: moe_dispatch_kernel<2><<<b, threads, 0, s>>>(p, chunks, elt); break;
+  }
+  return runtime_status(cudaGetLastError());
+}
+
+bwg_status moe_dispatch_grad(const void* d_rows, int dtype, int T, int H, int ldr, int k, const int* position,
+                             const int* offsets, int E, void* dX, int ldx, void* stream) {
+  return run_combine(d_rows, dtype, T, H, ldr, k, nullptr, position, offsets, E, dX, ldx,
+                     static_cast<cudaStream_t>(stream));
+}
+
+bwg_status moe_combine(const void* rows, int dtype, int T, int H, int ldr, int k, const float* weights,
+                       const int* position, const int* offsets, int E, void* Y, int ldy, void* stream) {
+  if (T > 0 && H > 0 && weights == nullptr) return BWG_ERR_INVALID_ARG;
+  return run_combine(rows, dtype, T, H, ldr, k, weights, position, offsets, E, Y, ldy,
+                     static_cast<cudaStream_t>(stream));
+}
+
+bwg_status moe_combine_grad(const void* dY, const void* rows, int dtype, int T, int H, int ldy, int ldr, int k,
+                            const float* weights, const int* position, const int* offsets, int E, void* d_rows,
+                            int ld_dr, float* d_weights, void* stream) {
+  bool empty;
+  bwg_status st = check_rows(dtype, T, H < 1 ? 1 : H, k, E, position, offsets, &empty);
+  if (H < 0) return BWG_ERR_INVALID_ARG;
+  if (st != BWG_OK || empty) return st;
+  if (weights == nullptr || d_weights == nullptr) return BWG_ERR_INVALID_ARG;
+  if (H > 0 && (dY == nullptr || rows == nullptr || d_rows == nullptr || ldy < H || ldr < H || ld_dr < H))
+    return BWG_ERR_INVALID_ARG;
+  const int elt = elt_bytes(dtype);
+  if (!elt_aligned(dY, elt) || !elt_aligned(rows, elt) || !elt_aligned(d_rows, elt)) return BWG_ERR_ALIGNMENT;
+  Runtime rt;
+  if ((st = runtime_device(&rt)) != BWG_OK) return st;
+  const int vb = vector_bytes(H, elt, {dY, rows, d_rows}, {ldy, ldr, ld_dr});
+  MoeRows p = {};
+  p.src = dY;
+  p.rows_in = rows;
+  p.dst = d_rows;
+  p.weights = weights;
+  p.d_weights = d_weights;
+  p.position = position;
+  p.kept = offsets + E;
+  p.ld_src = ldy;
+  p.ld_rows = ldr;
+  p.ld_dst = ld_dr;
+  p.T = T;
+  p.k = k;
+  p.pairs = T * k;
+  p.err = rt.err;
+  p.vecs = static_cast<int>(static_cast<long long>(H) * elt / vb);
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  const cudaError_t e = dtype == BWG_OUT_FP32   ? launch_combine_grad<float>(p, vb, s)
+                        : dtype == BWG_OUT_BF16 ? launch_combine_grad<__nv_bfloat16>(p, vb, s)
+                                                : launch_combine_grad<__half>(p, vb, s);
+  return runtime_status(e);
+}
+
+}  // extern "C"

@@ -11,6 +11,7 @@ from __future__ import annotations
 import ctypes
 import os
 import threading
+from typing import NamedTuple
 
 import torch
 
@@ -69,6 +70,14 @@ def lib() -> ctypes.CDLL:
                          "grouped_gemm_swiglu_bf16_nt", "grouped_gemm_swiglu_fp16_nt"):
                 f = getattr(L, name)
                 f.argtypes = [vp, ctypes.POINTER(vp), vp, vp, i, i, i, i, vp]
+                f.restype = i
+            for name, args in (("moe_sort", [vp, i, i, i, vp, vp, vp, vp]),
+                               ("moe_dispatch", [vp, i, i, i, i, i, vp, vp, i, vp, i, vp]),
+                               ("moe_dispatch_grad", [vp, i, i, i, i, i, vp, vp, i, vp, i, vp]),
+                               ("moe_combine", [vp, i, i, i, i, i, vp, vp, vp, i, vp, i, vp]),
+                               ("moe_combine_grad", [vp, vp, i, i, i, i, i, i, vp, vp, vp, i, vp, i, vp, vp])):
+                f = getattr(L, name)
+                f.argtypes = args
                 f.restype = i
             L.gemm_bf16_host.argtypes = [vp, vp, vp, i, i, i, i, vp, vp, vp, vp]
             L.gemm_bf16_host.restype = i
@@ -374,3 +383,127 @@ def grouped_gemm_swiglu_bf16_nt(A_ptr, B_ptrs, H_ptr, offsets_ptr, G, M_total, N
 def grouped_gemm_swiglu_fp16_nt(A_ptr, B_ptrs, H_ptr, offsets_ptr, G, M_total, N, K, stream) -> None:
     _grouped_call("grouped_gemm_swiglu_fp16_nt", A_ptr, B_ptrs, H_ptr, offsets_ptr, G, M_total, N, K,
                   stream)
+
+
+# ------------------------------------------------------------ routed rows ---
+
+
+class Routing(NamedTuple):
+    """What moe_sort makes of the experts' ids: the order of the rows that the
+    grouped products read, and the way back."""
+
+    offsets: torch.Tensor   # int32 [E + 1]: first row of each expert, then the rows that have one
+    order: torch.Tensor     # int32 [T * k]: the pair t * k + j at each row
+    position: torch.Tensor  # int32 [T, k]: the row of each pair
+
+
+def moe_sort(expert_ids: torch.Tensor, num_experts: int, stream=None) -> Routing:
+    """Stable sort of the (token, expert) pairs by expert.  ``expert_ids`` is a
+    CUDA int32 or int64 tensor [T, k]; an id outside 0 .. num_experts - 1 marks
+    a pair without an expert, sorted behind all others."""
+    if expert_ids.dim() != 2 or expert_ids.dtype not in (torch.int32, torch.int64):
+        raise ValueError("expert_ids must be an int32 or int64 tensor [T, k]")
+    if not expert_ids.is_cuda or not expert_ids.is_contiguous():
+        raise ValueError("expert_ids must be a dense CUDA tensor")
+    num_experts = int(num_experts)
+    if num_experts < 1:
+        raise ValueError("num_experts must be at least 1")
+    dev = expert_ids.device
+    pairs = expert_ids.numel()
+    offsets = torch.empty(num_experts + 1, dtype=torch.int32, device=dev)
+    order = torch.empty(pairs, dtype=torch.int32, device=dev)
+    position = torch.empty(expert_ids.shape, dtype=torch.int32, device=dev)
+    _check(lib().moe_sort(expert_ids.data_ptr(), expert_ids.element_size(), pairs, num_experts, offsets.data_ptr(),
+                          order.data_ptr(), position.data_ptr(), _stream_handle(stream, dev)), "moe_sort")
+    return Routing(offsets, order, position)
+
+
+def _routing(r: Routing, dev) -> tuple[int, int, int]:
+    """(T, k, E) of a routing whose tensors the kernels can read on `dev`."""
+    offsets, position = r.offsets, r.position
+    for name, t in (("offsets", offsets), ("position", position)):
+        if t.dtype != torch.int32 or not t.is_contiguous() or t.device != dev:
+            raise ValueError("routing.%s must be a dense int32 tensor on %s" % (name, dev))
+    if position.dim() != 2 or offsets.dim() != 1 or offsets.shape[0] < 2 or position.shape[1] < 1:
+        raise ValueError("routing must hold offsets [E + 1] and position [T, k]")
+    return position.shape[0], position.shape[1], offsets.shape[0] - 1
+
+
+def _rows(t: torch.Tensor, name: str, rows: int) -> int:
+    """Leading dimension of a row matrix with `rows` rows."""
+    if t.dtype not in _OUT_CODES:
+        raise TypeError("%s must be bfloat16, float16 or float32" % name)
+    ld = _matrix(t, name)
+    if t.shape[0] != rows:
+        raise ValueError("%s must have %d rows, got %d" % (name, rows, t.shape[0]))
+    if rows > 1 and ld < t.shape[1]:
+        raise ValueError("%s must not be a broadcast view: its rows overlap" % name)
+    return max(ld, t.shape[1])  # torch gives a single row any stride
+
+
+def _rows_like(out, like: torch.Tensor, rows: int, name: str) -> torch.Tensor:
+    if out is None:
+        return torch.empty((rows, like.shape[1]), dtype=like.dtype, device=like.device)
+    if tuple(out.shape) != (rows, like.shape[1]) or out.dtype != like.dtype or out.device != like.device:
+        raise ValueError("%s must be [%d, %d] of the input's dtype and device" % (name, rows, like.shape[1]))
+    return out
+
+
+def _pair_weights(w: torch.Tensor, T: int, k: int, dev) -> None:
+    if w.dtype != torch.float32 or tuple(w.shape) != (T, k) or not w.is_contiguous() or w.device != dev:
+        raise ValueError("weights must be a dense float32 tensor [%d, %d] on %s" % (T, k, dev))
+
+
+def moe_dispatch(x: torch.Tensor, routing: Routing, out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """Token rows [T, H] in expert order, [T * k, H]; zeros in the rows of
+    pairs without an expert (from row routing.offsets[-1] on)."""
+    T, k, E = _routing(routing, x.device)
+    ldx = _rows(x, "x", T)
+    out = _rows_like(out, x, T * k, "out")
+    _check(lib().moe_dispatch(x.data_ptr(), _OUT_CODES[x.dtype], T, x.shape[1], ldx, k, routing.position.data_ptr(),
+                              routing.offsets.data_ptr(), E, out.data_ptr(), _rows(out, "out", T * k),
+                              _stream_handle(stream, x.device)), "moe_dispatch")
+    return out
+
+
+def moe_dispatch_grad(d_rows: torch.Tensor, routing: Routing, out: torch.Tensor | None = None,
+                      stream=None) -> torch.Tensor:
+    """Gradient of moe_dispatch: [T * k, H] -> [T, H], each token's rows summed."""
+    T, k, E = _routing(routing, d_rows.device)
+    ldr = _rows(d_rows, "d_rows", T * k)
+    out = _rows_like(out, d_rows, T, "out")
+    _check(lib().moe_dispatch_grad(d_rows.data_ptr(), _OUT_CODES[d_rows.dtype], T, d_rows.shape[1], ldr, k,
+                                   routing.position.data_ptr(), routing.offsets.data_ptr(), E, out.data_ptr(),
+                                   _rows(out, "out", T), _stream_handle(stream, d_rows.device)), "moe_dispatch_grad")
+    return out
+
+
+def moe_combine(rows: torch.Tensor, routing: Routing, weights: torch.Tensor, out: torch.Tensor | None = None,
+                stream=None) -> torch.Tensor:
+    """Rows in expert order [T * k, H] back to token order [T, H], each token's
+    rows summed with its float32 weights [T, k]."""
+    T, k, E = _routing(routing, rows.device)
+    ldr = _rows(rows, "rows", T * k)
+    _pair_weights(weights, T, k, rows.device)
+    out = _rows_like(out, rows, T, "out")
+    _check(lib().moe_combine(rows.data_ptr(), _OUT_CODES[rows.dtype], T, rows.shape[1], ldr, k, weights.data_ptr(),
+                             routing.position.data_ptr(), routing.offsets.data_ptr(), E, out.data_ptr(),
+                             _rows(out, "out", T), _stream_handle(stream, rows.device)), "moe_combine")
+    return out
+
+
+def moe_combine_grad(d_out: torch.Tensor, rows: torch.Tensor, routing: Routing, weights: torch.Tensor,
+                     stream=None) -> tuple[torch.Tensor, torch.Tensor]:
+    """Gradient of moe_combine: (d_rows [T * k, H], d_weights float32 [T, k])."""
+    T, k, E = _routing(routing, rows.device)
+    ldr, ldy = _rows(rows, "rows", T * k), _rows(d_out, "d_out", T)
+    if d_out.dtype != rows.dtype or d_out.shape[1] != rows.shape[1] or d_out.device != rows.device:
+        raise ValueError("d_out must have the dtype, columns and device of rows")
+    _pair_weights(weights, T, k, rows.device)
+    d_rows = torch.empty((T * k, rows.shape[1]), dtype=rows.dtype, device=rows.device)
+    d_weights = torch.empty((T, k), dtype=torch.float32, device=rows.device)
+    _check(lib().moe_combine_grad(d_out.data_ptr(), rows.data_ptr(), _OUT_CODES[rows.dtype], T, rows.shape[1], ldy,
+                                  ldr, k, weights.data_ptr(), routing.position.data_ptr(),
+                                  routing.offsets.data_ptr(), E, d_rows.data_ptr(), rows.shape[1],
+                                  d_weights.data_ptr(), _stream_handle(stream, rows.device)), "moe_combine_grad")
+    return d_rows, d_weights

@@ -214,13 +214,61 @@ bwg_status gemm_bf16_small_m_noalloc(const void* A, const void* B, void* D, int 
 bwg_status gemm_bf16_host(const void* A_host, const void* B_host, void* D_host, int M, int N, int K,
                           int out_dtype, void* dA, void* dB, void* dD, void* stream);
 
+/* ---------------------------------------------------------------------
+ * Routed rows: from token order into expert order and back.
+ *
+ * The grouped products above want the rows of A sorted by expert and int32
+ * offsets.  With T tokens, k experts a token and E experts, pair
+ * p = t * k + j is token t's j-th expert.  All pointers are device pointers;
+ * nothing synchronises and the library keeps no pointer.
+ *
+ * moe_sort: a stable counting sort of the pairs by expert.
+ *   expert_ids: int32 (id_bytes 4) or int64 (8), `pairs` = T * k of them; an
+ *     id outside [0, E) marks a pair without an expert (a dropped token).
+ *   offsets [E + 1]: first row of each expert, offsets[E] = n, the rows that
+ *     have one.  order [pairs]: the pair at each sorted row, position [pairs]
+ *     its inverse.  Pairs without an expert are sorted behind all others
+ *     (rows n ..), so order and position are whole permutations.
+ *   E <= 1024, else BWG_ERR_UNSUPPORTED.  offsets honours the contract of the
+ *   grouped products for M_total = n.
+ *
+ * The row operators take X, Y, rows in one element type, `dtype` (a
+ * bwg_out_dtype), row-major with leading dimensions in elements.  Any H and
+ * any leading dimension >= H; pointers aligned to the element.  Rows whose
+ * start and length are multiples of 16 bytes move fastest.
+ * moe_dispatch:      rows[position[p]] = X[t]; zero where position[p] >= n.
+ * moe_dispatch_grad: dX[t] = sum_j d_rows[position[p]] over position[p] < n.
+ * moe_combine:       Y[t] = sum_j weights[p] rows[position[p]], the same pairs.
+ * moe_combine_grad:  d_rows[position[p]] = weights[p] dY[t] and d_weights[p] =
+ *   <dY[t], rows[position[p]]>; both zero for a pair without an expert.
+ *   weights and d_weights are FP32 [pairs].  Sums are FP32 in the order of j,
+ *   rounded once; a row of a pair without an expert is not read.
+ * `rows` and `d_rows` have T * k rows.  T, H or k * T of zero is a no-op
+ * (moe_combine_grad with H = 0 writes d_weights = 0).  A position outside
+ * [0, T * k) is skipped and reported through the device error word (kind 2).
+ * The outputs must not overlap the inputs.
+ * ------------------------------------------------------------------- */
+bwg_status moe_sort(const void* expert_ids, int id_bytes, int pairs, int E, int* offsets, int* order,
+                    int* position, void* stream);
+bwg_status moe_dispatch(const void* X, int dtype, int T, int H, int ldx, int k, const int* position,
+                        const int* offsets, int E, void* rows, int ldr, void* stream);
+bwg_status moe_dispatch_grad(const void* d_rows, int dtype, int T, int H, int ldr, int k,
+                             const int* position, const int* offsets, int E, void* dX, int ldx,
+                             void* stream);
+bwg_status moe_combine(const void* rows, int dtype, int T, int H, int ldr, int k, const float* weights,
+                       const int* position, const int* offsets, int E, void* Y, int ldy, void* stream);
+bwg_status moe_combine_grad(const void* dY, const void* rows, int dtype, int T, int H, int ldy, int ldr,
+                            int k, const float* weights, const int* position, const int* offsets, int E,
+                            void* d_rows, int ld_dr, float* d_weights, void* stream);
+
 /* Human-readable name of a status code (static string). */
 const char* bwg_status_string(int status);
 
 /*
  * Synchronises `stream`, then reads and clears the device error word of the
  * current device.  *info receives the raw word (0 if no fault):
- *   bits 56..63 kind (1 barrier wait timed out, 2 invalid group offsets),
+ *   bits 56..63 kind (1 barrier wait timed out, 2 invalid group offsets or
+ *   row positions),
  *   48..55 role (0 TMA producer, 1 MMA issuer, 2 epilogue),
  *   40..47 barrier (0 stage full, 1 stage empty, 2 accumulator full,
  *   3 accumulator empty), 16..39 block index, 8..15 stage, 0..7 phase.
