@@ -23,7 +23,8 @@ ROOT = os.path.dirname(PKG)
 BUILD_DIR = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libbwgemm.so")
 HEADER = os.path.join(ROOT, "include", "bwgemm.h")
-SOURCES = ["api.cu", "gemm_tc.cu", "gemm_small_m.cu", "moe.cu", "probes.cu"]
+SOURCES = ["api.cu", "gemm_tc.cu", "gemm_small_m.cu", "moe.cu", "fp4.cu", "gemm_fp4.cu",
+           "probes.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

@@ -1,0 +1,711 @@
+// Products of microscaled 4-bit matrices on tcgen05 tensor cores (sm_103a):
+//   D[i, n] = alpha sum_k A[i, k] B[n, k]
+// with A the activations [M, K] and B the weights [N, K] (or one [N, K] per
+// group of rows of A), both e2m1 with a scale per block of 16 or 32 columns
+// (fp4.h), FP32 accumulation, alpha the product of the matrices' FP32 scales.
+//
+// The kernel computes D^T: 128 weight rows per CTA are the M of an
+// instruction and the activations' rows its N, which may be any multiple of
+// 16 up to 192.  So a ragged end of a group costs what it has rows, not a
+// 256-row tile.  A CTA pair (cta_group::2) takes NC x 256 weight rows x 192
+// activation rows; each CTA stages its own weight rows and half of the
+// activation rows.
+//
+// Scales travel as their 512-byte tiles: TMA brings them beside the operands
+// and tcgen05.cp puts them into TMEM, four columns a tile, in order with the
+// MMAs of the same thread.  Activation tiles start at multiples of 192 rows,
+// so a tile's first scale row is a multiple of 64: the MMA reads the scales
+// of its N from the TMEM column of that row's group of 32.
+#include <algorithm>
+#include <cstdint>
+#include <cstdlib>
+#include <cstring>
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <mutex>
+#include <type_traits>
+
+#include "../../include/bwgemm.h"
+#include "fp4.h"
+#include "params.h"
+#include "ptx.cuh"
+#include "runtime.h"
+
+namespace bwg {
+namespace {
+
+constexpr int kFp4MaxGroups = 1024;
+constexpr int kTok = 192;          // activation rows of a tile: the MMA's N
+constexpr int kKBytes = 128;       // one stage: 256 columns, one swizzle row
+constexpr int kKCols = 256;
+constexpr uint32_t kWBytes = 128 * kKBytes;        // a CTA's weight rows of one consumer
+constexpr uint32_t kTokBytes = (kTok / 2) * kKBytes;  // a CTA's half of the activation rows
+
+struct Fp4GemmParams {
+  CUtensorMap map_w;   // weights {K/2 bytes, N, G}, box {128, 128, 1}, 128B swizzle
+  CUtensorMap map_a;   // activations {K/2 bytes, M}, box {128, 96}, 128B swizzle
+  CUtensorMap map_ws;  // weight scales {128 words, K tiles, row blocks}, box {128, 4 or 2, 1}
+  CUtensorMap map_as;  // activation scales, the same with a box of 2 row blocks
+  unsigned long long* err;
+  unsigned long long timeout_ns;
+  const int* offsets;      // [G + 1] or nullptr: one group of all M rows
+  const float* a_global;   // nullptr: 1
+  const float* b_global;   // nullptr: 1
+  void* d;
+  long long ldd;
+  int M, N, G;             // N: output columns (SwiGLU: half of the weights' rows)
+  int b_globals;           // 1 or G
+  int num_k_blocks, last_steps;  // stages, and 64-column steps of the last one
+  int num_w_tiles;         // tiles along the weights
+  int w_blocks;            // scale row blocks of one group's weights
+  int swiglu_up;           // SwiGLU: first weight row of the up half
+  int stages, out_dtype, group_m;
+};
+
+enum : uint32_t { kRoleProducer = 0, kRoleMma = 1, kRoleEpilogue = 2 };
+enum : uint32_t { kBarFull = 0, kBarEmpty = 1, kBarAccFull = 2, kBarAccEmpty = 3 };
+
+__device__ __forceinline__ void record_fault(unsigned long long* err, unsigned long long kind, uint32_t role,
+                                             uint32_t bar, uint32_t stage, uint32_t phase) {
+  const unsigned long long code = (kind << 56) | (static_cast<unsigned long long>(role) << 48) |
+                                  (static_cast<unsigned long long>(bar) << 40) |
+                                  (static_cast<unsigned long long>(blockIdx.x & 0xFFFFFFu) << 16) |
+                                  ((stage & 0xFFu) << 8) | (phase & 0xFFu);
+  atomicCAS(err, 0ull, code);
+}
+
+// Group tables in shared memory: rows of each group (lo[g] .. lo[g + 1], from
+// the offsets clamped into [0, M] and made non-decreasing), its first scale
+// row and the tiles before it.  Built by one warp.
+struct Tables {
+  int* lo;      // [G + 1]
+  int* prefix;  // [G + 1]
+  int* sf;      // [G]
+};
+
+__device__ bool build_tables(const Fp4GemmParams& p, const Tables& t) {
+  const int lane = static_cast<int>(threadIdx.x & 31u);
+  int run = 0, carry_t = 0, carry_s = 0;
+  bool bad = false;
+  for (int g0 = 0; g0 < p.G; g0 += 32) {
+    const int g = g0 + lane;
+    const bool in = g < p.G;
+    const int a = !in ? 0 : p.offsets != nullptr ? p.offsets[g] : 0;
+    const int b = !in ? 0 : p.offsets != nullptr ? p.offsets[g + 1] : p.M;
+    if (in && ((g == 0 && a != 0) || b < a || a < 0 || b > p.M)) bad = true;
+    int m = in ? max(a, b) : run;
+    for (int d = 1; d < 32; d <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, m, d);
+      if (lane >= d) m = max(m, y);
+    }
+    const int hi = min(max(m, run), p.M);
+    int lo = __shfl_up_sync(0xffffffffu, hi, 1);
+    if (lane == 0) lo = run;
+    const int rows = in ? hi - lo : 0;
+    const int tiles = (rows + kTok - 1) / kTok * p.num_w_tiles;
+    int it = tiles, is = pad128(rows);
+    for (int d = 1; d < 32; d <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, it, d);
+      const int z = __shfl_up_sync(0xffffffffu, is, d);
+      if (lane >= d) {
+        it += y;
+        is += z;
+      }
+    }
+    if (in) {
+      t.lo[g] = lo;
+      t.lo[g + 1] = hi;
+      t.prefix[g] = carry_t + it - tiles;
+      t.prefix[g + 1] = carry_t + it;
+      t.sf[g] = carry_s + is - pad128(rows);
+    }
+    carry_t += __shfl_sync(0xffffffffu, it, 31);
+    carry_s += __shfl_sync(0xffffffffu, is, 31);
+    run = __shfl_sync(0xffffffffu, hi, 31);
+    __syncwarp();
+  }
+  return !__any_sync(0xffffffffu, bad);
+}
+
+struct Tile {
+  int g;
+  int w0;       // first weight row (of the gate half for SwiGLU)
+  int t0;       // first activation row
+  int tokens;   // rows, 1 .. kTok
+  int n;        // tokens rounded up to 16
+  int srow;     // scale row of t0 in the activation scales
+};
+
+template <int W_ROWS>
+__device__ __forceinline__ Tile tile_at(const Fp4GemmParams& p, const Tables& t, int u) {
+  int g = 0, top = p.G - 1;
+  while (g < top) {
+    const int mid = (g + top + 1) >> 1;
+    if (t.prefix[mid] <= u)
+      g = mid;
+    else
+      top = mid - 1;
+  }
+  const int rows = t.lo[g + 1] - t.lo[g];
+  int tt, wt;
+  raster_tile(u - t.prefix[g], (rows + kTok - 1) / kTok, p.num_w_tiles, p.group_m, &tt, &wt);
+  Tile r;
+  r.g = g;
+  r.w0 = wt * W_ROWS;
+  r.t0 = t.lo[g] + tt * kTok;
+  r.tokens = min(kTok, rows - tt * kTok);
+  r.n = (r.tokens + 15) & ~15;
+  r.srow = t.sf[g] + tt * kTok;
+  return r;
+}
+
+__device__ __forceinline__ float silu_mul(float g, float u) { return g * rcp_approx(1.0f + __expf(-g)) * u; }
+
+constexpr int threads_of(int nc) { return nc == 1 ? 192 : 384; }
+
+// Shared memory: stage s holds [NC weight blocks][activation rows][scales].
+template <int NC>
+struct Layout {
+  static constexpr uint32_t kScaleTiles = 4;  // K tiles of a stage with blocks of 16 (2 with blocks of 32)
+  static constexpr uint32_t kStageW = NC * kWBytes;
+  static constexpr uint32_t kSfBlock = kScaleTiles * kScaleTileBytes;  // scales of 128 rows of one stage
+  static constexpr uint32_t kStageSf = (NC + 2) * kSfBlock;
+  static constexpr uint32_t kStage = kStageW + kTokBytes + kStageSf;
+  static_assert(kStage % 1024 == 0, "swizzled tiles start on 1024 bytes");
+};
+
+// NC weight blocks of 128 rows per CTA.  NC == 1: two accumulators, so that
+// the epilogue of a tile runs beside the MMAs of the next.  NC == 2: one
+// accumulator per block; fewer bytes staged per instruction.  SW: the blocks
+// are the gate and the up rows of the same 256 output columns.
+template <int NC, int FMT, bool SW>
+__global__ void __launch_bounds__(threads_of(NC), 1) fp4_pair_kernel(const __grid_constant__ Fp4GemmParams p) {
+  static_assert(!SW || NC == 2, "SwiGLU pairs a gate block with an up block");
+  using L = Layout<NC>;
+  constexpr int kVec = FMT == kNvfp4 ? 16 : 32;
+  constexpr int kTilesK = FMT == kNvfp4 ? 4 : 2;     // scale tiles of a stage along K
+  constexpr uint32_t kSfBytes = kTilesK * kScaleTileBytes;
+  constexpr uint32_t kStageTx = 2u * (L::kStageW + kTokBytes + (NC + 2) * kSfBytes);
+  constexpr int kWRows = SW ? 256 : 256 * NC;        // output columns of a tile
+  constexpr uint32_t kEpi0 = NC == 1 ? 2u : 4u;
+  constexpr uint32_t kAccCols = kTok;
+  constexpr uint32_t kSfCol0 = 2 * kTok;             // scales start after the two accumulators
+  constexpr uint32_t kSfCols = (NC + 2) * kTilesK * 4;  // TMEM columns of one stage's scales
+  static_assert(kSfCol0 + 2 * kSfCols <= kTmemCols, "two accumulators and two stages of scales");
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
+  const uint32_t warp = threadIdx.x >> 5;
+  const uint32_t lane = threadIdx.x & 31u;
+  const uint32_t rank = cluster_ctarank();
+  const int S = p.stages;
+  const uint32_t bars = base + static_cast<uint32_t>(S) * L::kStage;
+  auto full_bar = [&](int s) { return bars + 8u * s; };
+  auto empty_bar = [&](int s) { return bars + 8u * (S + s); };
+  auto acc_full = [&](int a) { return bars + 8u * (2 * S + a); };
+  auto acc_empty = [&](int a) { return bars + 8u * (2 * S + 2 + a); };
+  const uint32_t tmem_slot = bars + 8u * (2 * S + 4);
+  int* tab = reinterpret_cast<int*>(smem_raw + (tmem_slot + 16u - smem_u32(smem_raw)));
+  const Tables tb{tab, tab + p.G + 1, tab + 2 * p.G + 2};
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < S; ++s) {
+      mbar_init(full_bar(s), 1);
+      mbar_init(empty_bar(s), 1);
+    }
+    for (int a = 0; a < 2; ++a) {
+      mbar_init(acc_full(a), 1);
+      // epilogue warps of both CTAs that read this accumulator
+      mbar_init(acc_empty(a), SW ? 16 : 8);
+    }
+    fence_mbarrier_init();
+  }
+  if (warp == 2) {
+    const bool ok = build_tables(p, tb);
+    if (!ok && blockIdx.x == 0 && lane == 0) record_fault(p.err, kFaultBadOffsets, 0, 0, 0, 0);
+  }
+  if (warp == 0 && lane == 0) {
+    prefetch_tensormap(&p.map_w);
+    prefetch_tensormap(&p.map_a);
+    prefetch_tensormap(&p.map_ws);
+    prefetch_tensormap(&p.map_as);
+  }
+  if (warp == 1) {
+    tmem_alloc<2>(tmem_slot, kTmemCols);
+    tmem_relinquish<2>();
+  }
+  tc_fence_before();
+  cluster_sync_all();
+  tc_fence_after();
+  const uint32_t tmem = ld_shared_u32(tmem_slot);
+  const int first = static_cast<int>(cluster_id_x());
+  const int stride = static_cast<int>(num_clusters_x());
+  const int total = tb.prefix[p.G];
+  bool aborted = false;
+
+  if (warp == 0) {
+    // ---- TMA producer -------------------------------------------------------
+    if (lane == 0) {
+      int s = 0;
+      uint32_t ph = 0;
+      for (int u = first; u < total && !aborted; u += stride) {
+        const Tile tl = tile_at<kWRows>(p, tb, u);
+        const int w_row = tl.w0 + static_cast<int>(rank) * 128;
+        const int a_row = tl.t0 + static_cast<int>(rank) * (tl.n / 2);
+        for (int kb = 0; kb < p.num_k_blocks; ++kb) {
+          if (!mbar_wait(empty_bar(s), ph ^ 1u, p.timeout_ns)) {
+            record_fault(p.err, kFaultTimeout, kRoleProducer, kBarEmpty, s, ph ^ 1u);
+            aborted = true;
+            break;
+          }
+          const uint32_t st = base + static_cast<uint32_t>(s) * L::kStage;
+          if (rank == 0) mbar_arrive_expect_tx(full_bar(s), kStageTx);
+          const uint32_t fb = mapa_shared(full_bar(s), 0);
+#pragma unroll
+          for (int c = 0; c < NC; ++c) {
+            const int row = SW ? w_row + c * p.swiglu_up : w_row + c * 256;
+            tma_load_3d_pair(st + c * kWBytes, &p.map_w, fb, kb * kKBytes, row, tl.g);
+            tma_load_3d_pair(st + L::kStageW + kTokBytes + c * L::kSfBlock, &p.map_ws, fb, 0, kb * kTilesK,
+                             tl.g * p.w_blocks + row / 128);
+          }
+          tma_load_2d_pair(st + L::kStageW, &p.map_a, fb, kb * kKBytes, a_row);
+          // both CTAs need the scales of all of the instruction's N; a box
+          // of two row blocks (the second may lie past the end: zeros)
+          tma_load_3d_pair(st + L::kStageW + kTokBytes + NC * L::kSfBlock, &p.map_as, fb, 0, kb * kTilesK,
+                           tl.srow / 128);
+          if (++s == S) {
+            s = 0;
+            ph ^= 1u;
+          }
+        }
+      }
+    }
+    __syncwarp();
+  } else if (warp == 1) {
+    // ---- MMA issuer (CTA 0 of the pair) ------------------------------------
+    if (rank == 0) {
+      int s = 0;
+      uint32_t ph = 0, acc_ph = 0, sf_buf = 0;
+      int acc = 0;
+      for (int u = first; u < total && !aborted; u += stride) {
+        const Tile tl = tile_at<kWRows>(p, tb, u);
+        for (int a = 0; a < NC; ++a) {
+          const int slot = NC == 1 ? acc : a;
+          if (!warp_wait_all(acc_empty(slot), acc_ph ^ 1u, p.timeout_ns)) {
+            if (lane == 0) record_fault(p.err, kFaultTimeout, kRoleMma, kBarAccEmpty, slot, acc_ph ^ 1u);
+            aborted = true;
+          }
+        }
+        if (aborted) break;
+        tc_fence_after();
+        const uint32_t shift = static_cast<uint32_t>(tl.srow & 127) / 32u;
+        const bool two_blocks = shift * 32u + static_cast<uint32_t>(tl.n) > 128u;
+        const uint32_t idesc0 = make_idesc_fp4(FMT, 256, static_cast<uint32_t>(tl.n), 0);
+        for (int kb = 0; kb < p.num_k_blocks; ++kb) {
+          if (!warp_wait_all(full_bar(s), ph, p.timeout_ns)) {
+            if (lane == 0) record_fault(p.err, kFaultTimeout, kRoleMma, kBarFull, s, ph);
+            aborted = true;
+            break;
+          }
+          tc_fence_after();
+          if (elect_one()) {
+            const uint32_t st = base + static_cast<uint32_t>(s) * L::kStage;
+            const uint32_t sf = st + L::kStageW + kTokBytes;
+            const uint32_t sf_tmem = tmem + kSfCol0 + sf_buf * kSfCols;
+            const int steps = kb == p.num_k_blocks - 1 ? p.last_steps : 4;
+            // scales: block c's tile j to columns (c * kTilesK + j) * 4, the
+            // activations' two row blocks of tile j side by side
+#pragma unroll
+            for (int j = 0; j < kTilesK; ++j) {
+#pragma unroll
+              for (int c = 0; c < NC; ++c)
+                tmem_copy_scales<2>(sf_tmem + (c * kTilesK + j) * 4,
+                                    make_smem_desc(sf + c * L::kSfBlock + j * kScaleTileBytes, 16, 128, kSwizzleNone));
+              const uint32_t sfb = sf + NC * L::kSfBlock + j * kScaleTileBytes;
+              const uint32_t col = sf_tmem + (NC * kTilesK + 2 * j) * 4;
+              tmem_copy_scales<2>(col, make_smem_desc(sfb, 16, 128, kSwizzleNone));
+              if (two_blocks)
+                tmem_copy_scales<2>(col + 4, make_smem_desc(sfb + kSfBytes, 16, 128, kSwizzleNone));
+            }
+            const uint64_t b_desc = make_smem_desc(st + L::kStageW, 16, 1024, kSwizzle128B);
+#pragma unroll
+            for (int kk = 0; kk < 4; ++kk) {
+              if (kk < steps) {
+                const int j = FMT == kNvfp4 ? kk : kk / 2;
+                const uint32_t idesc =
+                    FMT == kNvfp4 ? idesc0 : (idesc0 | (static_cast<uint32_t>(kk & 1) << 5) |
+                                              (static_cast<uint32_t>(kk & 1) << 30));
+                const uint32_t sfb_col = sf_tmem + (NC * kTilesK + 2 * j) * 4 + shift;
+#pragma unroll
+                for (int c = 0; c < NC; ++c) {
+                  const uint64_t a_desc = make_smem_desc(st + c * kWBytes, 16, 1024, kSwizzle128B);
+                  const uint32_t d = tmem + static_cast<uint32_t>(NC == 1 ? acc : c) * kAccCols;
+                  mma_fp4<2, kVec>(d, a_desc + kk * 2, b_desc + kk * 2, idesc, sf_tmem + (c * kTilesK + j) * 4,
+                                   sfb_col, (kb | kk) != 0 ? 1u : 0u);
+                }
+              }
+            }
+            mma_commit_pair_mc(empty_bar(s), 0x3);
+          }
+          __syncwarp();
+          sf_buf ^= 1u;
+          if (++s == S) {
+            s = 0;
+            ph ^= 1u;
+          }
+        }
+        if (aborted) break;
+        if (elect_one()) {
+          if constexpr (NC == 1) {
+            mma_commit_pair_mc(acc_full(acc), 0x3);
+          } else {
+            mma_commit_pair_mc(acc_full(0), 0x3);
+            mma_commit_pair_mc(acc_full(1), 0x3);
+          }
+        }
+        __syncwarp();
+        if constexpr (NC == 1) {
+          acc ^= 1;
+          if (acc == 0) acc_ph ^= 1u;
+        } else {
+          acc_ph ^= 1u;
+        }
+      }
+    }
+    __syncwarp();
+  } else if (warp >= kEpi0) {
+    // ---- epilogue: TMEM lane = output column, TMEM column = row of D --------
+    const uint32_t q = warp & 3u;
+    const int grp = static_cast<int>((warp - kEpi0) >> 2);  // NC == 2: 0 or 1
+    const uint32_t acc_empty0 = mapa_shared(acc_empty(0), 0);
+    const float ga = p.a_global != nullptr ? __ldg(p.a_global) : 1.f;
+    const bool out32 = p.out_dtype == kOutF32;
+    const bool outbf = p.out_dtype == kOutBF16;
+    int acc = SW ? 0 : (NC == 1 ? 0 : grp);
+    uint32_t acc_ph = 0;
+    for (int u = first; u < total; u += stride) {
+      const Tile tl = tile_at<kWRows>(p, tb, u);
+      bool ok = warp_wait_all(acc_full(acc), acc_ph, p.timeout_ns);
+      if (SW) ok = ok && warp_wait_all(acc_full(1), acc_ph, p.timeout_ns);
+      if (!ok) {
+        if (lane == 0) record_fault(p.err, kFaultTimeout, kRoleEpilogue, kBarAccFull, acc, acc_ph);
+        aborted = true;
+        break;
+      }
+      tc_fence_after();
+      const float alpha = p.b_global != nullptr ? ga * __ldg(p.b_global + (p.b_globals > 1 ? tl.g : 0)) : ga;
+      const uint32_t t_lane = tmem + ((q * 32u) << 16);
+      const int col = tl.w0 + (SW ? 0 : grp * 256) + static_cast<int>(rank * 128u + q * 32u + lane);
+      const bool col_ok = col < p.N;
+      auto release = [&]() {
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive_cluster_relaxed(acc_empty0 + 8u * acc);
+          if (SW) mbar_arrive_cluster_relaxed(acc_empty0 + 8u);
+        }
+      };
+      const int elt = out32 ? 4 : 2;
+      uint8_t* const dcol = static_cast<uint8_t*>(p.d) + (static_cast<long long>(tl.t0) * p.ldd + col) * elt;
+      const long long row_bytes = p.ldd * elt;
+      // SwiGLU: the two warpgroups take alternate chunks of 32 rows
+      const int c_first = SW ? grp * 32 : 0, c_step = SW ? 64 : 32;
+      if (c_first >= tl.tokens) release();
+      for (int c0 = c_first; c0 < tl.tokens; c0 += c_step) {
+        uint32_t v[32];
+        tmem_ld_32x32b_x32(t_lane + static_cast<uint32_t>(SW ? 0 : acc) * kAccCols + c0, v);
+        if constexpr (SW) {
+          uint32_t w[32];
+          tmem_ld_32x32b_x32(t_lane + kAccCols + c0, w);
+          tmem_wait_ld();
+          if (c0 + c_step >= tl.tokens) release();
+#pragma unroll
+          for (int j = 0; j < 32; ++j)
+            v[j] = __float_as_uint(silu_mul(alpha * __uint_as_float(v[j]), alpha * __uint_as_float(w[j])));
+        } else {
+          tmem_wait_ld();
+          if (c0 + c_step >= tl.tokens) release();
+#pragma unroll
+          for (int j = 0; j < 32; ++j) v[j] = __float_as_uint(alpha * __uint_as_float(v[j]));
+        }
+        if (col_ok) {
+          uint8_t* dst = dcol + c0 * row_bytes;
+#pragma unroll
+          for (int j = 0; j < 32; ++j) {
+            if (c0 + j < tl.tokens) {
+              const float x = __uint_as_float(v[j]);
+              if (out32)
+                *reinterpret_cast<float*>(dst) = x;
+              else
+                *reinterpret_cast<uint16_t*>(dst) = outbf ? cvt_rn_bf16(x) : cvt_rn_f16(x);
+            }
+            dst += row_bytes;
+          }
+        }
+      }
+      if constexpr (NC == 1) {
+        acc ^= 1;
+        if (acc == 0) acc_ph ^= 1u;
+      } else {
+        acc_ph ^= 1u;
+      }
+    }
+    __syncwarp();
+  }
+
+  // ---- teardown -------------------------------------------------------------
+  if (__syncthreads_or(aborted ? 1 : 0)) {
+    // a wait gave up: let copies in flight land before their memory goes
+    const uint64_t t0 = globaltimer_ns();
+    while (globaltimer_ns() - t0 < 200000ull) nanosleep_ns(1000);
+  }
+  tc_fence_before();
+  cluster_sync_all();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc<2>(tmem, kTmemCols);
+  }
+}
+
+// SwiGLU of FP32 rows [gate | up], for halves that the fused epilogue cannot
+// pair (it needs both to start on a tile of scales): rows before *last only.
+template <class T>
+__global__ void fp4_swiglu_kernel(const float* __restrict__ x, const int* __restrict__ last, int n_out, long long ldd,
+                                  T* __restrict__ h) {
+  const int row = static_cast<int>(blockIdx.x);
+  if (row >= *last) return;
+  const float* r = x + static_cast<long long>(row) * 2 * n_out;
+  for (int c = static_cast<int>(threadIdx.x); c < n_out; c += static_cast<int>(blockDim.x)) {
+    const float y = silu_mul(r[c], r[n_out + c]);
+    if constexpr (std::is_same<T, float>::value)
+      h[row * ldd + c] = y;
+    else if constexpr (std::is_same<T, __half>::value)
+      h[row * ldd + c] = __float2half_rn(y);
+    else
+      h[row * ldd + c] = __float2bfloat16_rn(y);
+  }
+}
+
+template <int NC>
+int pair_smem(int stages, int G) {
+  return 1024 + stages * static_cast<int>(Layout<NC>::kStage) + 8 * (2 * stages + 4) + 16 + 4 * (3 * G + 2);
+}
+
+using PairKernel = void (*)(Fp4GemmParams);
+
+PairKernel pick_pair(int nc, int format, bool sw) {
+  if (sw) return format == kNvfp4 ? fp4_pair_kernel<2, kNvfp4, true> : fp4_pair_kernel<2, kMxfp4, true>;
+  if (nc == 2) return format == kNvfp4 ? fp4_pair_kernel<2, kNvfp4, false> : fp4_pair_kernel<2, kMxfp4, false>;
+  return format == kNvfp4 ? fp4_pair_kernel<1, kNvfp4, false> : fp4_pair_kernel<1, kMxfp4, false>;
+}
+
+// Co-resident pairs of a kernel at the largest shared memory, and its
+// attribute set, once per device.
+bwg_status pair_clusters(PairKernel k, int nc, const Runtime& rt, int* clusters) {
+  struct Key {
+    PairKernel k;
+    int dev;
+  };
+  static std::mutex mu;
+  static struct {
+    Key key;
+    int clusters;
+  } seen[64 * 6];
+  static int n_seen = 0;
+  std::lock_guard<std::mutex> lock(mu);
+  for (int i = 0; i < n_seen; ++i)
+    if (seen[i].key.k == k && seen[i].key.dev == rt.device) {
+      *clusters = seen[i].clusters;
+      return BWG_OK;
+    }
+  const void* fn = reinterpret_cast<const void*>(k);
+  if (cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, rt.max_smem) != cudaSuccess) {
+    cudaGetLastError();
+    return BWG_ERR_CUDA;
+  }
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(2, 1, 1);
+  cfg.blockDim = dim3(static_cast<unsigned>(threads_of(nc)), 1, 1);
+  cfg.dynamicSmemBytes = static_cast<size_t>(rt.max_smem);
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = 2;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  int n = 0;
+  if (cudaOccupancyMaxActiveClusters(&n, fn, &cfg) != cudaSuccess || n <= 0) {
+    cudaGetLastError();
+    n = rt.sm_count / 2;
+  }
+  if (n_seen < static_cast<int>(sizeof(seen) / sizeof(seen[0]))) {
+    seen[n_seen].key = Key{k, rt.device};
+    seen[n_seen].clusters = n;
+    ++n_seen;
+  }
+  *clusters = n;
+  return BWG_OK;
+}
+
+struct Fp4Operand {
+  const void* codes;
+  const void* scales;
+  const float* global;
+  int n_global;
+};
+
+bool fp4_maps(Fp4GemmParams* p, const Fp4Operand& a, const Fp4Operand& b, int M, int N_w, int K, int format, int G,
+              int a_row_blocks) {
+  const uint64_t row = static_cast<uint64_t>(K / 2);
+  const CUtensorMapDataType u8 = CU_TENSOR_MAP_DATA_TYPE_UINT8, u32 = CU_TENSOR_MAP_DATA_TYPE_UINT32;
+  const uint64_t kt = static_cast<uint64_t>(fp4_k_tiles(K, format));
+  const uint32_t kbox = format == kNvfp4 ? 4 : 2;
+  const uint64_t wd[3] = {row, static_cast<uint64_t>(N_w), static_cast<uint64_t>(G)};
+  const uint64_t ws[2] = {row, row * static_cast<uint64_t>(N_w)};
+  const uint32_t wb[3] = {kKBytes, 128, 1};
+  const uint64_t ad[2] = {row, static_cast<uint64_t>(M)};
+  const uint32_t ab[2] = {kKBytes, kTok / 2};
+  const uint64_t sd[3] = {128, kt, static_cast<uint64_t>(G) * static_cast<uint64_t>(p->w_blocks)};
+  const uint64_t ss[2] = {kScaleTileBytes, kt * kScaleTileBytes};
+  const uint32_t sb[3] = {128, kbox, 1};
+  const uint64_t asd[3] = {128, kt, static_cast<uint64_t>(a_row_blocks)};
+  const uint32_t asb[3] = {128, kbox, 2};
+  return runtime_map(&p->map_w, b.codes, u8, 3, wd, ws, wb, CU_TENSOR_MAP_SWIZZLE_128B) &&
+         runtime_map(&p->map_a, a.codes, u8, 2, ad, &row, ab, CU_TENSOR_MAP_SWIZZLE_128B) &&
+         runtime_map(&p->map_ws, b.scales, u32, 3, sd, ss, sb, CU_TENSOR_MAP_SWIZZLE_NONE) &&
+         runtime_map(&p->map_as, a.scales, u32, 3, asd, ss, asb, CU_TENSOR_MAP_SWIZZLE_NONE);
+}
+
+bool aligned16(const void* q) { return (reinterpret_cast<uintptr_t>(q) & 15u) == 0; }
+
+bwg_status run_fp4_gemm(const Fp4Operand& a, const Fp4Operand& b, void* D, int M, int N, int K, int ldd, int format,
+                        const int* offsets, int G, int out_dtype, bool swiglu, cudaStream_t stream) {
+  if (out_dtype != BWG_OUT_BF16 && out_dtype != BWG_OUT_FP32 && out_dtype != BWG_OUT_FP16) return BWG_ERR_INVALID_ARG;
+  if (format != kNvfp4 && format != kMxfp4) return BWG_ERR_INVALID_ARG;
+  if (M < 0 || N < 0 || K < 0 || G < 0) return BWG_ERR_INVALID_ARG;
+  if (K % 32 != 0) return BWG_ERR_ALIGNMENT;
+  if (M == 0 || N == 0 || G == 0) return BWG_OK;
+  const int n_out = swiglu ? N / 2 : N;
+  if (D == nullptr || ldd < n_out) return BWG_ERR_INVALID_ARG;
+  if (format == kMxfp4 && (a.global != nullptr || b.global != nullptr)) return BWG_ERR_INVALID_ARG;
+  if (b.global != nullptr && b.n_global != 1 && b.n_global != G) return BWG_ERR_INVALID_ARG;
+  if (reinterpret_cast<uintptr_t>(D) & (out_dtype == BWG_OUT_FP32 ? 3u : 1u)) return BWG_ERR_ALIGNMENT;
+  if (K > 0) {
+    if (a.codes == nullptr || a.scales == nullptr || b.codes == nullptr || b.scales == nullptr)
+      return BWG_ERR_INVALID_ARG;
+    if (!aligned16(a.codes) || !aligned16(a.scales) || !aligned16(b.codes) || !aligned16(b.scales))
+      return BWG_ERR_ALIGNMENT;
+  }
+  if (G > kFp4MaxGroups) return BWG_ERR_UNSUPPORTED;
+  Runtime rt;
+  bwg_status st = runtime_device(&rt);
+  if (st != BWG_OK) return st;
+  if (K == 0) return runtime_status(launch_zero_fill(D, M, n_out, ldd, out_dtype == BWG_OUT_FP32 ? 4 : 2, stream));
+  Fp4GemmParams p;
+  std::memset(&p, 0, sizeof(p));
+  // Two weight blocks a CTA unless that leaves pairs without a tile.
+  // BWG_FP4_NC overrides.
+  const long long tok_tiles = (M + kTok - 1LL) / kTok + (offsets != nullptr ? G : 0);
+  const char* nc_env = std::getenv("BWG_FP4_NC");
+  const int nc = swiglu                                               ? 2
+                 : nc_env != nullptr && (*nc_env == '1' || *nc_env == '2') ? *nc_env - '0'
+                 : tok_tiles * ((n_out + 511) / 512) < rt.sm_count / 2 ? 1
+                                                                      : 2;
+  p.w_blocks = pad128(N) / 128;
+  const int a_rows = offsets != nullptr ? static_cast<int>((M + 127LL * std::min(G, M)) / 128) : pad128(M) / 128;
+  if (!fp4_maps(&p, a, b, M, N, K, format, G, a_rows)) return BWG_ERR_CUDA;
+  p.err = rt.err;
+  p.timeout_ns = rt.timeout_ns;
+  p.offsets = offsets;
+  p.a_global = a.global;
+  p.b_global = b.global;
+  p.b_globals = b.n_global;
+  p.d = D;
+  p.ldd = ldd;
+  p.M = M;
+  p.N = n_out;
+  p.G = G;
+  p.num_k_blocks = (K + kKCols - 1) / kKCols;
+  p.last_steps = (K - (p.num_k_blocks - 1) * kKCols + 63) / 64;
+  const int w_rows = swiglu ? 256 : 256 * nc;
+  p.num_w_tiles = (n_out + w_rows - 1) / w_rows;
+  p.swiglu_up = n_out;
+  p.out_dtype = out_dtype;
+  p.group_m = 8;
+  p.stages = nc == 2 ? 4 : 6;
+  const int smem = nc == 2 ? pair_smem<2>(p.stages, G) : pair_smem<1>(p.stages, G);
+  if (smem > rt.max_smem) return BWG_ERR_UNSUPPORTED;
+  const PairKernel k = pick_pair(nc, format, swiglu);
+  int clusters = 0;
+  if ((st = pair_clusters(k, nc, rt, &clusters)) != BWG_OK) return st;
+  // every group adds at most one partial tile of rows
+  const long long most = tok_tiles * p.num_w_tiles;
+  const int grid = 2 * static_cast<int>(std::min<long long>(most, clusters));
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(grid), 1, 1);
+  cfg.blockDim = dim3(static_cast<unsigned>(threads_of(nc)), 1, 1);
+  cfg.dynamicSmemBytes = static_cast<size_t>(smem);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = 2;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return runtime_status(cudaLaunchKernelEx(&cfg, k, p));
+}
+
+// Grouped product with SwiGLU where the up half starts inside a tile of
+// scales: the FP32 product into the workspace, then the activation.
+bwg_status run_swiglu_two_steps(const Fp4Operand& a, const Fp4Operand& b, void* H, int M, int N, int K, int ldh,
+                                int format, const int* offsets, int G, int out_dtype, void* workspace,
+                                cudaStream_t stream) {
+  if (out_dtype != BWG_OUT_BF16 && out_dtype != BWG_OUT_FP32 && out_dtype != BWG_OUT_FP16) return BWG_ERR_INVALID_ARG;
+  if (M < 0 || N < 0 || N % 2 != 0 || K < 0 || G < 0) return BWG_ERR_INVALID_ARG;
+  if (M == 0 || N == 0 || G == 0) return BWG_OK;
+  if (H == nullptr || workspace == nullptr || ldh < N / 2) return BWG_ERR_INVALID_ARG;
+  if (!aligned16(workspace) || (reinterpret_cast<uintptr_t>(H) & (out_dtype == BWG_OUT_FP32 ? 3u : 1u)))
+    return BWG_ERR_ALIGNMENT;
+  const bwg_status st =
+      run_fp4_gemm(a, b, workspace, M, N, K, N, format, offsets, G, BWG_OUT_FP32, false, stream);
+  if (st != BWG_OK) return st;
+  const float* x = static_cast<const float*>(workspace);
+  const int n = N / 2, threads = std::min(256, (n + 31) / 32 * 32);
+  const unsigned blocks = static_cast<unsigned>(M);
+  if (out_dtype == BWG_OUT_FP32)
+    fp4_swiglu_kernel<<<blocks, threads, 0, stream>>>(x, offsets + G, n, ldh, static_cast<float*>(H));
+  else if (out_dtype == BWG_OUT_FP16)
+    fp4_swiglu_kernel<<<blocks, threads, 0, stream>>>(x, offsets + G, n, ldh, static_cast<__half*>(H));
+  else
+    fp4_swiglu_kernel<<<blocks, threads, 0, stream>>>(x, offsets + G, n, ldh, static_cast<__nv_bfloat16*>(H));
+  return runtime_status(cudaGetLastError());
+}
+
+}  // namespace
+}  // namespace bwg
+
+using namespace bwg;
+
+extern "C" {
+
+bwg_status gemm_fp4(const void* A, const void* A_scales, const float* A_global, const void* B, const void* B_scales,
+                    const float* B_global, int format, void* D, int M, int N, int K, int ldd, int out_dtype,
+                    void* stream) {
+  return run_fp4_gemm(Fp4Operand{A, A_scales, A_global, 1}, Fp4Operand{B, B_scales, B_global, 1}, D, M, N, K, ldd,
+                      format, nullptr, 1, out_dtype, false, static_cast<cudaStream_t>(stream));
+}
+
+bwg_status grouped_gemm_fp4(const void* A, const void* A_scales, const float* A_global, const void* B,
+                            const void* B_scales, const float* B_global, int n_global, int format, void* D,
+                            const int* group_offsets, int G, int M_total, int N, int K, int ldd, int out_dtype,
+                            int swiglu, void* workspace, void* stream) {
+  if (M_total > 0 && N > 0 && G > 0 && group_offsets == nullptr) return BWG_ERR_INVALID_ARG;
+  const Fp4Operand a{A, A_scales, A_global, 1}, b{B, B_scales, B_global, n_global};
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (swiglu && N % 256 != 0)
+    return run_swiglu_two_steps(a, b, D, M_total, N, K, ldd, format, group_offsets, G, out_dtype, workspace, s);
+  return run_fp4_gemm(a, b, D, M_total, N, K, ldd, format, group_offsets, G, out_dtype, swiglu != 0, s);
+}
+
+}  // extern "C"

@@ -75,6 +75,11 @@ def lib() -> ctypes.CDLL:
                                ("moe_dispatch", [vp, i, i, i, i, i, vp, vp, i, vp, i, vp]),
                                ("moe_dispatch_grad", [vp, i, i, i, i, i, vp, vp, i, vp, i, vp]),
                                ("moe_combine", [vp, i, i, i, i, i, vp, vp, vp, i, vp, i, vp]),
+                               ("quantize_fp4", [vp, i, i, i, i, i, vp, i, vp, i, vp, vp, vp]),
+                               ("dequantize_fp4", [vp, vp, i, vp, i, vp, i, vp, i, i, i, i, vp]),
+                               ("gemm_fp4", [vp, vp, vp, vp, vp, vp, i, vp, i, i, i, i, i, vp]),
+                               ("grouped_gemm_fp4", [vp, vp, vp, vp, vp, vp, i, i, vp, vp, i, i, i, i, i, i, i, vp,
+                                                     vp]),
                                ("moe_combine_grad", [vp, vp, i, i, i, i, i, i, vp, vp, vp, i, vp, i, vp, vp])):
                 f = getattr(L, name)
                 f.argtypes = args
@@ -131,6 +136,12 @@ def lib() -> ctypes.CDLL:
             L.bwg_streamk_tiles.restype = i
             L.bwg_unit_part.argtypes = [i, i, i, i, ip, ip, ip]
             L.bwg_unit_part.restype = None
+            L.bwg_fp4_scale_bytes.argtypes = [i, i, i, i, i]
+            L.bwg_fp4_scale_bytes.restype = ctypes.c_longlong
+            L.bwg_fp4_scale_offset.argtypes = [ctypes.c_longlong, i, i, i]
+            L.bwg_fp4_scale_offset.restype = ctypes.c_longlong
+            L.bwg_idesc_fp4.argtypes = [i, i, i, i]
+            L.bwg_idesc_fp4.restype = u32
             L.bwg_version.argtypes = []
             L.bwg_version.restype = ctypes.c_char_p
             _lib = L
@@ -507,3 +518,202 @@ def moe_combine_grad(d_out: torch.Tensor, rows: torch.Tensor, routing: Routing, 
                                   routing.offsets.data_ptr(), E, d_rows.data_ptr(), rows.shape[1],
                                   d_weights.data_ptr(), _stream_handle(stream, rows.device)), "moe_combine_grad")
     return d_rows, d_weights
+
+
+# ------------------------------------------------- 4-bit floating point ---
+
+_FP4_CODES = {"nvfp4": 0, "mxfp4": 1}
+
+
+class Fp4Matrix:
+    """A matrix [rows, K] in microscaled 4-bit floating point.
+
+    codes         uint8 [rows, K / 2], two e2m1 values a byte
+    scales        uint8, in tiles of 128 rows x 4 blocks (see the C header)
+    format        "nvfp4" (blocks of 16, e4m3 scales) or "mxfp4" (blocks of 32, e8m0)
+    global_scale  float32 [1] or [groups] (nvfp4), or None
+    group_offsets int32 [groups + 1] of ragged groups of rows, or None
+    groups        without offsets: the number of equal groups of rows
+    """
+
+    __slots__ = ("codes", "scales", "format", "global_scale", "group_offsets", "groups")
+
+    def __init__(self, codes, scales, format, global_scale=None, group_offsets=None, groups=1):
+        self.codes = codes
+        self.scales = scales
+        self.format = format
+        self.global_scale = global_scale
+        self.group_offsets = group_offsets
+        self.groups = groups if group_offsets is None else group_offsets.shape[0] - 1
+
+    @property
+    def shape(self):
+        return self.codes.shape[0], self.codes.shape[1] * 2
+
+    @property
+    def device(self):
+        return self.codes.device
+
+
+def _fp4_format(fmt: str) -> int:
+    if fmt not in _FP4_CODES:
+        raise ValueError("format must be 'nvfp4' or 'mxfp4', got %r" % (fmt,))
+    return _FP4_CODES[fmt]
+
+
+def _fp4_global(g, fmt: int, groups: int, dev) -> tuple:
+    if g is None:
+        return None, 1
+    if fmt == 1:
+        raise ValueError("mxfp4 has no global scale")
+    if g.dtype != torch.float32 or not g.is_contiguous() or g.device != dev or g.numel() not in (1, groups):
+        raise ValueError("global_scale must be a dense float32 tensor of 1 or %d values on %s" % (groups, dev))
+    return g.data_ptr(), g.numel()
+
+
+def _fp4_offsets(off, dev):
+    if off is None:
+        return None
+    if off.dtype != torch.int32 or off.dim() != 1 or off.shape[0] < 2 or not off.is_contiguous() or off.device != dev:
+        raise ValueError("group_offsets must be a dense int32 tensor [groups + 1] on %s" % dev)
+    return off.data_ptr()
+
+
+def _fp4_check(q: Fp4Matrix, name: str) -> int:
+    """Format code of an Fp4Matrix whose buffers are as large as the kernels take them."""
+    fmt = _fp4_format(q.format)
+    codes, scales = q.codes, q.scales
+    if codes.dtype != torch.uint8 or codes.dim() != 2 or not codes.is_contiguous() or not codes.is_cuda:
+        raise ValueError("%s.codes must be a dense CUDA uint8 tensor [rows, K / 2]" % name)
+    rows, K = q.shape
+    need = lib().bwg_fp4_scale_bytes(rows, K, fmt, q.groups, 0 if q.group_offsets is None else 1)
+    if need < 0:
+        raise ValueError("%s: %d rows do not make %d equal groups" % (name, rows, q.groups))
+    if scales.dtype != torch.uint8 or not scales.is_contiguous() or scales.device != codes.device \
+            or scales.numel() < need:
+        raise ValueError("%s.scales must be a dense uint8 tensor of at least %d bytes on %s"
+                         % (name, need, codes.device))
+    return fmt
+
+
+def quantize_fp4(x: torch.Tensor, format: str = "nvfp4", global_scale: torch.Tensor | None = None,
+                 group_offsets: torch.Tensor | None = None, groups: int = 1, stream=None) -> Fp4Matrix:
+    """x [rows, K] (or stacked weights [groups, N, K]) into 4 bits.  For the
+    routed rows of a grouped product give the routing's offsets."""
+    fmt = _fp4_format(format)
+    if x.dim() == 3:
+        if group_offsets is not None or not x.is_contiguous():
+            raise ValueError("stacked weights must be dense [groups, N, K], without group_offsets")
+        groups = x.shape[0]
+        x = x.reshape(-1, x.shape[2])
+    if x.dtype not in _OUT_CODES:
+        raise TypeError("x must be bfloat16, float16 or float32")
+    rows, K = x.shape
+    ldx = _rows(x, "x", rows)
+    dev = x.device
+    if K % 32:
+        raise ValueError("K must be a multiple of 32, got %d" % K)
+    off = _fp4_offsets(group_offsets, dev)
+    if off is not None:
+        groups = group_offsets.shape[0] - 1
+    elif groups < 1 or rows % groups:
+        raise ValueError("%d rows do not make %d equal groups" % (rows, groups))
+    g, n_global = _fp4_global(global_scale, fmt, groups, dev)
+    L = lib()
+    codes = torch.empty((rows, K // 2), dtype=torch.uint8, device=dev)
+    scales = torch.empty(L.bwg_fp4_scale_bytes(rows, K, fmt, groups, 0 if off is None else 1), dtype=torch.uint8,
+                         device=dev)
+    _check(L.quantize_fp4(x.data_ptr(), _OUT_CODES[x.dtype], rows, K, ldx, fmt, g, n_global, off, groups,
+                          codes.data_ptr(), scales.data_ptr(), _stream_handle(stream, dev)), "quantize_fp4")
+    return Fp4Matrix(codes, scales, format, global_scale, group_offsets, groups)
+
+
+def dequantize_fp4(q: Fp4Matrix, out_dtype: torch.dtype = torch.bfloat16, out: torch.Tensor | None = None,
+                   stream=None) -> torch.Tensor:
+    """The values of q, [rows, K], computed in FP32 and rounded once."""
+    fmt = _fp4_check(q, "q")
+    dev = q.codes.device
+    rows, K = q.shape
+    off = _fp4_offsets(q.group_offsets, dev)
+    g, n_global = _fp4_global(q.global_scale, fmt, q.groups, dev)
+    if out is None:
+        if out_dtype not in _OUT_CODES:
+            raise TypeError("out_dtype must be bfloat16, float16 or float32")
+        out = torch.empty((rows, K), dtype=out_dtype, device=dev)
+    elif tuple(out.shape) != (rows, K) or out.device != dev:
+        raise ValueError("out must be [%d, %d] on %s" % (rows, K, dev))
+    _check(lib().dequantize_fp4(q.codes.data_ptr(), q.scales.data_ptr(), fmt, g, n_global, off, q.groups,
+                                out.data_ptr(), _OUT_CODES[out.dtype], rows, K, _rows(out, "out", rows),
+                                _stream_handle(stream, dev)), "dequantize_fp4")
+    return out
+
+
+def _fp4_pair(A: Fp4Matrix, B: Fp4Matrix) -> int:
+    fmt = _fp4_check(A, "A")
+    if _fp4_check(B, "B") != fmt:
+        raise ValueError("A and B must have the same format")
+    if A.codes.shape[1] != B.codes.shape[1]:
+        raise ValueError("inner dimensions differ: %s x %s" % (A.shape, B.shape))
+    if A.codes.device != B.codes.device:
+        raise ValueError("A and B must be on the same device")
+    return fmt
+
+
+def _fp4_out(out, out_dtype, M: int, N: int, dev) -> torch.Tensor:
+    if out is None:
+        if out_dtype not in _OUT_CODES:
+            raise TypeError("output dtype must be bfloat16, float16 or float32")
+        return torch.empty((M, N), dtype=out_dtype, device=dev)
+    if tuple(out.shape) != (M, N) or out.device != dev:
+        raise ValueError("out must be [%d, %d] on %s" % (M, N, dev))
+    return out
+
+
+def gemm_fp4(A: Fp4Matrix, B: Fp4Matrix, out: torch.Tensor | None = None,
+             out_dtype: torch.dtype = torch.bfloat16, stream=None) -> torch.Tensor:
+    """D = A @ B.T of the values of A [M, K] and B [N, K], FP32 accumulation."""
+    fmt = _fp4_pair(A, B)
+    if A.group_offsets is not None or B.group_offsets is not None or A.groups != 1 or B.groups != 1:
+        raise ValueError("gemm_fp4 takes matrices without groups of rows; see grouped_gemm_fp4")
+    dev = A.codes.device
+    M, K = A.shape
+    N = B.codes.shape[0]
+    out = _fp4_out(out, out_dtype, M, N, dev)
+    ga, _ = _fp4_global(A.global_scale, fmt, 1, dev)
+    gb, _ = _fp4_global(B.global_scale, fmt, 1, dev)
+    _check(lib().gemm_fp4(A.codes.data_ptr(), A.scales.data_ptr(), ga, B.codes.data_ptr(), B.scales.data_ptr(), gb,
+                          fmt, out.data_ptr(), M, N, K, _rows(out, "out", M), _OUT_CODES[out.dtype],
+                          _stream_handle(stream, dev)), "gemm_fp4")
+    return out
+
+
+def grouped_gemm_fp4(A: Fp4Matrix, B: Fp4Matrix, swiglu: bool = False, out: torch.Tensor | None = None,
+                     out_dtype: torch.dtype = torch.bfloat16, stream=None) -> torch.Tensor:
+    """Grouped expert product in 4 bits: rows of A's group g (its group_offsets)
+    times B's group g ([groups * N, K], equal groups) transposed.  With
+    ``swiglu`` each B[g] is [gate; up] along N and the result silu(gate) * up."""
+    fmt = _fp4_pair(A, B)
+    if A.group_offsets is None or B.group_offsets is not None:
+        raise ValueError("A must have ragged groups (group_offsets), B equal ones")
+    if A.groups != B.groups:
+        raise ValueError("A has %d groups, B %d" % (A.groups, B.groups))
+    dev = A.codes.device
+    off = _fp4_offsets(A.group_offsets, dev)
+    M, K = A.shape
+    G = B.groups
+    N = B.codes.shape[0] // G
+    if swiglu and N % 2:
+        raise ValueError("swiglu needs an even number of weight rows, got %d" % N)
+    n_out = N // 2 if swiglu else N
+    out = _fp4_out(out, out_dtype, M, n_out, dev)
+    ga, na = _fp4_global(A.global_scale, fmt, 1, dev)
+    gb, n_global = _fp4_global(B.global_scale, fmt, G, dev)
+    work = torch.empty((M, N), dtype=torch.float32, device=dev) if swiglu and N % 256 else None
+    if work is not None and stream is not None:
+        work.record_stream(stream)
+    _check(lib().grouped_gemm_fp4(A.codes.data_ptr(), A.scales.data_ptr(), ga, B.codes.data_ptr(),
+                                  B.scales.data_ptr(), gb, n_global, fmt, out.data_ptr(), off, G, M, N, K,
+                                  _rows(out, "out", M), _OUT_CODES[out.dtype], 1 if swiglu else 0,
+                                  None if work is None else work.data_ptr(), _stream_handle(stream, dev)),
+           "grouped_gemm_fp4")
+    return out

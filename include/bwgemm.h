@@ -261,6 +261,67 @@ bwg_status moe_combine_grad(const void* dY, const void* rows, int dtype, int T, 
                             int k, const float* weights, const int* position, const int* offsets, int E,
                             void* d_rows, int ld_dr, float* d_weights, void* stream);
 
+/* ---------------------------------------------------------------------
+ * Microscaled 4-bit floating point: quantisation and products.
+ *
+ * Values are e2m1 (0, .5, 1, 1.5, 2, 3, 4, 6 with a sign), two a byte (the
+ * even column in the low half); a matrix [R, K] is row-major, K / 2 bytes a
+ * row, K a multiple of 32.  One scale byte per block of a row:
+ *   BWG_NVFP4: blocks of 16 columns, e4m3 scales, and an FP32 scale g for the
+ *              whole matrix (or for each group);  value = code * scale * g
+ *   BWG_MXFP4: blocks of 32 columns, e8m0 scales;  value = code * scale
+ * Scales lie in tiles of 128 rows x 4 blocks, 512 bytes a tile, tiles along K
+ * first: block b of row r is byte (r % 32) * 16 + (r / 32 % 4) * 4 + b % 4 of
+ * tile (r / 128, b / 4) (bwg_fp4_scale_offset).  Bytes for blocks past K in
+ * the last tile are zero; rows past the last are not read into any result.
+ *
+ * A matrix may hold G groups of rows (experts), each of which starts a new
+ * row of scale tiles: with group_offsets (DEVICE int32 [G + 1], as for the
+ * grouped products) group g's rows are group_offsets[g] .., without them
+ * every group has R / G rows.  Codes stay where their row is.
+ * bwg_fp4_scale_bytes says how many bytes of scales to allocate for rows
+ * grouped so (ragged: with group_offsets), -1 for invalid arguments.
+ *
+ * quantize_fp4: X [M, K] (dtype: a bwg_out_dtype; any ldx >= K) into codes
+ *   and scales.  With amax a block's largest magnitude,
+ *     NVFP4: scale = e4m3(min(amax / (6 g), 448)), code = e2m1(x / (scale g))
+ *     MXFP4: scale = 2^max(floor(log2 amax) - 2, -127), code = e2m1(x / scale)
+ *   each rounded to nearest, ties to even, saturating.  A block that holds an
+ *   infinity or a NaN gets a NaN scale: all of it reads back as NaN.
+ *   global_scale: device, n_global = 1 or G floats g > 0, NULL for 1 (and
+ *   always for MXFP4).  amax(X) / 2688 uses the whole range.
+ * dequantize_fp4: the values, computed in FP32 and rounded once to dtype.
+ * Rows of no group (from group_offsets[G] on) are neither read nor written.
+ *
+ * gemm_fp4: D[M, N] = A x B^T for A [M, K] and B [N, K] in the same format,
+ *   FP32 accumulation, D in out_dtype with any ldd >= N.
+ * grouped_gemm_fp4: D[r, :] = A[r, :] x B[g]^T for r in group g.  A is
+ *   [M_total, K] in ragged groups, B [G * N, K] in G groups of N rows; B_global
+ *   has n_global = 1 or G floats.  group_offsets[G] may be below M_total: D's
+ *   rows from there on are not written.  Offsets that break the contract are
+ *   clamped and reported through the device error word (kind 2).  G <= 1024.
+ *   With swiglu, B[g] = [gate; up] along N and D[M_total, N / 2] = silu(gate)
+ *   * up, evaluated in FP32; N must be even.  If N is no multiple of 256, the
+ *   up half starts inside a scale tile: the product then goes through
+ *   `workspace` (M_total * N * 4 bytes, 16-byte aligned; else unused).
+ * Codes and scales must be 16-byte aligned.  K = 0 gives D = 0.
+ * ------------------------------------------------------------------- */
+typedef enum { BWG_NVFP4 = 0, BWG_MXFP4 = 1 } bwg_fp4_format;
+
+bwg_status quantize_fp4(const void* X, int dtype, int M, int K, int ldx, int format,
+                        const float* global_scale, int n_global, const int* group_offsets, int G,
+                        void* codes, void* scales, void* stream);
+bwg_status dequantize_fp4(const void* codes, const void* scales, int format, const float* global_scale,
+                          int n_global, const int* group_offsets, int G, void* Y, int dtype, int M, int K,
+                          int ldy, void* stream);
+bwg_status gemm_fp4(const void* A, const void* A_scales, const float* A_global, const void* B,
+                    const void* B_scales, const float* B_global, int format, void* D, int M, int N, int K,
+                    int ldd, int out_dtype, void* stream);
+bwg_status grouped_gemm_fp4(const void* A, const void* A_scales, const float* A_global, const void* B,
+                            const void* B_scales, const float* B_global, int n_global, int format, void* D,
+                            const int* group_offsets, int G, int M_total, int N, int K, int ldd,
+                            int out_dtype, int swiglu, void* workspace, void* stream);
+
 /* Human-readable name of a status code (static string). */
 const char* bwg_status_string(int status);
 
@@ -363,6 +424,7 @@ void bwg_debug_set_trace(void* buffer);
  *                      evict-last (default 2; 0 with the cluster split)
  *   BWG_GROUPED_1C     1: grouped kernels with one MMA consumer (256-row units)
  *   BWG_GROUPED_SWAP   1: swapped-operand group ends (one-consumer grouped kernel)
+ *   BWG_FP4_NC         1 / 2: 4-bit products with 256 / 512 weight rows a CTA pair
  *   BWG_B_ONE_BOX      0: dense pair kernels load a CTA's B stage as two
  *                      64-column boxes (default: one load where N % 64 == 0
  *                      or B is [N, K])
@@ -441,6 +503,15 @@ bwg_status bwg_check_gemm_args(const void* A, const void* B, const void* D, int 
 /* tcgen05 instruction descriptor, kind::f16 with FP32 accumulation
  * (bf16 != 0: BF16 inputs, else FP16; *_mn_major != 0: operand MN-major). */
 uint32_t bwg_idesc_f16(int bf16, int a_mn_major, int b_mn_major, int m, int n);
+
+/* Bytes of scales of an [M, K] matrix in G groups of rows, and the byte of
+ * block `block` of scale row `row` (see quantize_fp4). */
+long long bwg_fp4_scale_bytes(int M, int K, int format, int G, int ragged);
+long long bwg_fp4_scale_offset(long long row, int block, int K, int format);
+
+/* tcgen05 instruction descriptor of the 4-bit block-scaled kinds (format: a
+ * bwg_fp4_format; scale_id: first of a word's four scales that is used). */
+uint32_t bwg_idesc_fp4(int format, int m, int n, int scale_id);
 
 /* tcgen05 shared-memory matrix descriptor (swizzle: 0 none, 2 = 128-byte). */
 uint64_t bwg_smem_desc(uint32_t smem_addr, uint32_t lbo_bytes, uint32_t sbo_bytes, int swizzle);
