@@ -54,6 +54,8 @@ class PlanInfo(ctypes.Structure):
 def lib() -> ctypes.CDLL:
     """The loaded C library (raises if it is not built)."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is None:
             if not os.path.exists(LIB_PATH):
@@ -167,7 +169,10 @@ def _check(status: int, what: str) -> None:
 
 def _stream_handle(stream, device) -> int:
     if stream is None:
-        stream = torch.cuda.current_stream(device)
+        # the handle of torch.cuda.current_stream(device), without the Stream
+        # object around it (7 us of a 20 us call)
+        index = device if isinstance(device, int) else device.index
+        return torch._C._cuda_getCurrentRawStream(index)
     return int(stream.cuda_stream)
 
 
@@ -445,19 +450,23 @@ def _rows(t: torch.Tensor, name: str, rows: int) -> int:
     if t.dtype not in _OUT_CODES:
         raise TypeError("%s must be bfloat16, float16 or float32" % name)
     ld = _matrix(t, name)
-    if t.shape[0] != rows:
-        raise ValueError("%s must have %d rows, got %d" % (name, rows, t.shape[0]))
-    if rows > 1 and ld < t.shape[1]:
+    have, cols = t.shape
+    if have != rows:
+        raise ValueError("%s must have %d rows, got %d" % (name, rows, have))
+    if ld >= cols:
+        return ld
+    if rows > 1:
         raise ValueError("%s must not be a broadcast view: its rows overlap" % name)
-    return max(ld, t.shape[1])  # torch gives a single row any stride
+    return cols  # torch gives a single row any stride
 
 
-def _rows_like(out, like: torch.Tensor, rows: int, name: str) -> torch.Tensor:
+def _out_rows(out, rows: int, cols: int, dtype, dev, name: str = "out") -> tuple:
+    """(output matrix, leading dimension): a new one, or the caller's checked."""
     if out is None:
-        return torch.empty((rows, like.shape[1]), dtype=like.dtype, device=like.device)
-    if tuple(out.shape) != (rows, like.shape[1]) or out.dtype != like.dtype or out.device != like.device:
-        raise ValueError("%s must be [%d, %d] of the input's dtype and device" % (name, rows, like.shape[1]))
-    return out
+        return torch.empty((rows, cols), dtype=dtype, device=dev), cols
+    if tuple(out.shape) != (rows, cols) or out.dtype != dtype or out.device != dev:
+        raise ValueError("%s must be a [%d, %d] %s tensor on %s" % (name, rows, cols, dtype, dev))
+    return out, _rows(out, name, rows)
 
 
 def _pair_weights(w: torch.Tensor, T: int, k: int, dev) -> None:
@@ -470,10 +479,11 @@ def moe_dispatch(x: torch.Tensor, routing: Routing, out: torch.Tensor | None = N
     pairs without an expert (from row routing.offsets[-1] on)."""
     T, k, E = _routing(routing, x.device)
     ldx = _rows(x, "x", T)
-    out = _rows_like(out, x, T * k, "out")
-    _check(lib().moe_dispatch(x.data_ptr(), _OUT_CODES[x.dtype], T, x.shape[1], ldx, k, routing.position.data_ptr(),
-                              routing.offsets.data_ptr(), E, out.data_ptr(), _rows(out, "out", T * k),
-                              _stream_handle(stream, x.device)), "moe_dispatch")
+    H, dtype, dev = x.shape[1], x.dtype, x.device
+    out, ldo = _out_rows(out, T * k, H, dtype, dev)
+    _check(lib().moe_dispatch(x.data_ptr(), _OUT_CODES[dtype], T, H, ldx, k, routing.position.data_ptr(),
+                              routing.offsets.data_ptr(), E, out.data_ptr(), ldo, _stream_handle(stream, dev)),
+           "moe_dispatch")
     return out
 
 
@@ -482,10 +492,11 @@ def moe_dispatch_grad(d_rows: torch.Tensor, routing: Routing, out: torch.Tensor 
     """Gradient of moe_dispatch: [T * k, H] -> [T, H], each token's rows summed."""
     T, k, E = _routing(routing, d_rows.device)
     ldr = _rows(d_rows, "d_rows", T * k)
-    out = _rows_like(out, d_rows, T, "out")
-    _check(lib().moe_dispatch_grad(d_rows.data_ptr(), _OUT_CODES[d_rows.dtype], T, d_rows.shape[1], ldr, k,
-                                   routing.position.data_ptr(), routing.offsets.data_ptr(), E, out.data_ptr(),
-                                   _rows(out, "out", T), _stream_handle(stream, d_rows.device)), "moe_dispatch_grad")
+    H, dtype, dev = d_rows.shape[1], d_rows.dtype, d_rows.device
+    out, ldo = _out_rows(out, T, H, dtype, dev)
+    _check(lib().moe_dispatch_grad(d_rows.data_ptr(), _OUT_CODES[dtype], T, H, ldr, k, routing.position.data_ptr(),
+                                   routing.offsets.data_ptr(), E, out.data_ptr(), ldo, _stream_handle(stream, dev)),
+           "moe_dispatch_grad")
     return out
 
 
@@ -495,11 +506,12 @@ def moe_combine(rows: torch.Tensor, routing: Routing, weights: torch.Tensor, out
     rows summed with its float32 weights [T, k]."""
     T, k, E = _routing(routing, rows.device)
     ldr = _rows(rows, "rows", T * k)
-    _pair_weights(weights, T, k, rows.device)
-    out = _rows_like(out, rows, T, "out")
-    _check(lib().moe_combine(rows.data_ptr(), _OUT_CODES[rows.dtype], T, rows.shape[1], ldr, k, weights.data_ptr(),
-                             routing.position.data_ptr(), routing.offsets.data_ptr(), E, out.data_ptr(),
-                             _rows(out, "out", T), _stream_handle(stream, rows.device)), "moe_combine")
+    H, dtype, dev = rows.shape[1], rows.dtype, rows.device
+    _pair_weights(weights, T, k, dev)
+    out, ldo = _out_rows(out, T, H, dtype, dev)
+    _check(lib().moe_combine(rows.data_ptr(), _OUT_CODES[dtype], T, H, ldr, k, weights.data_ptr(),
+                             routing.position.data_ptr(), routing.offsets.data_ptr(), E, out.data_ptr(), ldo,
+                             _stream_handle(stream, dev)), "moe_combine")
     return out
 
 
@@ -579,14 +591,25 @@ def _fp4_offsets(off, dev):
     return off.data_ptr()
 
 
+def _fp4_scale_bytes(M: int, K: int, fmt: int, G: int, ragged: bool) -> int:
+    """bwg_fp4_scale_bytes without the call."""
+    if ragged:
+        tile_rows = (M + 127 * min(G, M)) // 128
+    elif G < 1 or M % G:
+        return -1
+    else:
+        tile_rows = G * (-(-(M // G) // 128))
+    return tile_rows * -(-K // (64 if fmt == 0 else 128)) * 512
+
+
 def _fp4_check(q: Fp4Matrix, name: str) -> int:
     """Format code of an Fp4Matrix whose buffers are as large as the kernels take them."""
     fmt = _fp4_format(q.format)
-    codes, scales = q.codes, q.scales
+    codes, scales, ragged = q.codes, q.scales, q.group_offsets is not None
     if codes.dtype != torch.uint8 or codes.dim() != 2 or not codes.is_contiguous() or not codes.is_cuda:
         raise ValueError("%s.codes must be a dense CUDA uint8 tensor [rows, K / 2]" % name)
-    rows, K = q.shape
-    need = lib().bwg_fp4_scale_bytes(rows, K, fmt, q.groups, 0 if q.group_offsets is None else 1)
+    rows, half = codes.shape
+    need = _fp4_scale_bytes(rows, 2 * half, fmt, q.groups, ragged)
     if need < 0:
         raise ValueError("%s: %d rows do not make %d equal groups" % (name, rows, q.groups))
     if scales.dtype != torch.uint8 or not scales.is_contiguous() or scales.device != codes.device \
@@ -621,8 +644,7 @@ def quantize_fp4(x: torch.Tensor, format: str = "nvfp4", global_scale: torch.Ten
     g, n_global = _fp4_global(global_scale, fmt, groups, dev)
     L = lib()
     codes = torch.empty((rows, K // 2), dtype=torch.uint8, device=dev)
-    scales = torch.empty(L.bwg_fp4_scale_bytes(rows, K, fmt, groups, 0 if off is None else 1), dtype=torch.uint8,
-                         device=dev)
+    scales = torch.empty(_fp4_scale_bytes(rows, K, fmt, groups, off is not None), dtype=torch.uint8, device=dev)
     _check(L.quantize_fp4(x.data_ptr(), _OUT_CODES[x.dtype], rows, K, ldx, fmt, g, n_global, off, groups,
                           codes.data_ptr(), scales.data_ptr(), _stream_handle(stream, dev)), "quantize_fp4")
     return Fp4Matrix(codes, scales, format, global_scale, group_offsets, groups)
@@ -636,14 +658,9 @@ def dequantize_fp4(q: Fp4Matrix, out_dtype: torch.dtype = torch.bfloat16, out: t
     rows, K = q.shape
     off = _fp4_offsets(q.group_offsets, dev)
     g, n_global = _fp4_global(q.global_scale, fmt, q.groups, dev)
-    if out is None:
-        if out_dtype not in _OUT_CODES:
-            raise TypeError("out_dtype must be bfloat16, float16 or float32")
-        out = torch.empty((rows, K), dtype=out_dtype, device=dev)
-    elif tuple(out.shape) != (rows, K) or out.device != dev:
-        raise ValueError("out must be [%d, %d] on %s" % (rows, K, dev))
+    out, ldo = _fp4_out(out, out_dtype, rows, K, dev)
     _check(lib().dequantize_fp4(q.codes.data_ptr(), q.scales.data_ptr(), fmt, g, n_global, off, q.groups,
-                                out.data_ptr(), _OUT_CODES[out.dtype], rows, K, _rows(out, "out", rows),
+                                out.data_ptr(), _OUT_CODES[out.dtype], rows, K, ldo,
                                 _stream_handle(stream, dev)), "dequantize_fp4")
     return out
 
@@ -659,14 +676,12 @@ def _fp4_pair(A: Fp4Matrix, B: Fp4Matrix) -> int:
     return fmt
 
 
-def _fp4_out(out, out_dtype, M: int, N: int, dev) -> torch.Tensor:
-    if out is None:
-        if out_dtype not in _OUT_CODES:
-            raise TypeError("output dtype must be bfloat16, float16 or float32")
-        return torch.empty((M, N), dtype=out_dtype, device=dev)
-    if tuple(out.shape) != (M, N) or out.device != dev:
-        raise ValueError("out must be [%d, %d] on %s" % (M, N, dev))
-    return out
+def _fp4_out(out, out_dtype, M: int, N: int, dev) -> tuple:
+    if out is not None:
+        out_dtype = out.dtype
+    if out_dtype not in _OUT_CODES:
+        raise TypeError("output dtype must be bfloat16, float16 or float32")
+    return _out_rows(out, M, N, out_dtype, dev)
 
 
 def gemm_fp4(A: Fp4Matrix, B: Fp4Matrix, out: torch.Tensor | None = None,
@@ -678,11 +693,11 @@ def gemm_fp4(A: Fp4Matrix, B: Fp4Matrix, out: torch.Tensor | None = None,
     dev = A.codes.device
     M, K = A.shape
     N = B.codes.shape[0]
-    out = _fp4_out(out, out_dtype, M, N, dev)
+    out, ldo = _fp4_out(out, out_dtype, M, N, dev)
     ga, _ = _fp4_global(A.global_scale, fmt, 1, dev)
     gb, _ = _fp4_global(B.global_scale, fmt, 1, dev)
     _check(lib().gemm_fp4(A.codes.data_ptr(), A.scales.data_ptr(), ga, B.codes.data_ptr(), B.scales.data_ptr(), gb,
-                          fmt, out.data_ptr(), M, N, K, _rows(out, "out", M), _OUT_CODES[out.dtype],
+                          fmt, out.data_ptr(), M, N, K, ldo, _OUT_CODES[out.dtype],
                           _stream_handle(stream, dev)), "gemm_fp4")
     return out
 
@@ -705,7 +720,7 @@ def grouped_gemm_fp4(A: Fp4Matrix, B: Fp4Matrix, swiglu: bool = False, out: torc
     if swiglu and N % 2:
         raise ValueError("swiglu needs an even number of weight rows, got %d" % N)
     n_out = N // 2 if swiglu else N
-    out = _fp4_out(out, out_dtype, M, n_out, dev)
+    out, ldo = _fp4_out(out, out_dtype, M, n_out, dev)
     ga, na = _fp4_global(A.global_scale, fmt, 1, dev)
     gb, n_global = _fp4_global(B.global_scale, fmt, G, dev)
     work = torch.empty((M, N), dtype=torch.float32, device=dev) if swiglu and N % 256 else None
@@ -713,7 +728,7 @@ def grouped_gemm_fp4(A: Fp4Matrix, B: Fp4Matrix, swiglu: bool = False, out: torc
         work.record_stream(stream)
     _check(lib().grouped_gemm_fp4(A.codes.data_ptr(), A.scales.data_ptr(), ga, B.codes.data_ptr(),
                                   B.scales.data_ptr(), gb, n_global, fmt, out.data_ptr(), off, G, M, N, K,
-                                  _rows(out, "out", M), _OUT_CODES[out.dtype], 1 if swiglu else 0,
+                                  ldo, _OUT_CODES[out.dtype], 1 if swiglu else 0,
                                   None if work is None else work.data_ptr(), _stream_handle(stream, dev)),
            "grouped_gemm_fp4")
     return out

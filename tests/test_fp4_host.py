@@ -39,6 +39,10 @@ def test_scale_bytes_hold_every_grouping(lib):
         need = int(sum(-(-c // 128) for c in counts)) * 512 * 3  # K = 160 in nvfp4: three tiles
         assert need <= lib.bwg_fp4_scale_bytes(M, 160, 0, G, 1) <= (M // 128 + min(G, M)) * 512 * 3 + 511
     assert lib.bwg_fp4_scale_bytes(600, 128, 1, 3, 0) == 3 * 2 * 512
+    from blackwell_tensor_core_gb300 import ops
+    for M, K, fmt, G, ragged in ((0, 64, 0, 1, 0), (7, 96, 1, 1, 0), (600, 1056, 0, 3, 0), (10, 64, 0, 3, 0),
+                                 (5, 64, 1, 900, 1), (1000, 4096, 0, 32, 1), (0, 32, 0, 4, 1)):
+        assert ops._fp4_scale_bytes(M, K, fmt, G, bool(ragged)) == lib.bwg_fp4_scale_bytes(M, K, fmt, G, ragged)
     for bad in ((-1, 64, 0, 1, 0), (8, -32, 0, 1, 0), (8, 64, 2, 1, 0), (8, 64, 0, 0, 0), (8, 64, 0, 3, 0)):
         assert lib.bwg_fp4_scale_bytes(*bad) == -1
 
