@@ -9,13 +9,14 @@
 // has zero codes; a block holding an infinity or a NaN gets a NaN scale and
 // zero codes, so that all of it reads back as NaN.
 //
-// What bounds these kernels: HBM.  One pass: a thread owns a block, so that
-// its maximum needs no exchange between threads.
+// What bounds these kernels: HBM.  One pass: a lane owns a block, so that its
+// maximum needs no exchange between lanes.
 #include <algorithm>
 #include <cstdint>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
+#include <type_traits>
 
 #include "../../include/bwgemm.h"
 #include "fp4.h"
@@ -40,19 +41,21 @@ struct Fp4Params {
   long long ldx;         // elements
   int M, K, G;
   int n_global;          // 1 or G
-  int k_tiles;
+  int k_tiles;           // scale tiles along K
   int nb;                // blocks a row
-  int lanes_per_row;     // blocks a row rounded up to whole warps
+  int chunks;            // units along K: U scale tiles each
+  int row_blocks;        // 128-row blocks of scales; with offsets, at most that many
 };
 
 // Group tables of a ragged matrix in shared memory: first row of each group
 // (clamped into [0, M], non-decreasing) and its first scale row.
 struct Groups {
   int* lo;  // [G + 1]
-  int* sf;  // [G]
+  int* sf;  // [G + 1]
 };
 
-__device__ void build_groups(const Fp4Params& p, const Groups& t) {
+// Returns the 128-row blocks of scales that the groups fill.
+__device__ int build_groups(const Fp4Params& p, const Groups& t) {
   if (threadIdx.x < 32) {
     const int lane = static_cast<int>(threadIdx.x);
     int run = 0, carry = 0;
@@ -85,34 +88,41 @@ __device__ void build_groups(const Fp4Params& p, const Groups& t) {
       carry += __shfl_sync(0xffffffffu, incl, 31);
       run = __shfl_sync(0xffffffffu, hi, 31);
     }
+    if (lane == 0) t.sf[p.G] = carry;
     if (__any_sync(0xffffffffu, bad) && lane == 0 && blockIdx.x == 0) atomicCAS(p.err, 0ull, kFaultBadOffsets << 56);
   }
   __syncthreads();
+  return t.sf[p.G] >> 7;
 }
 
-// Group and scale row of matrix row r; false: r lies in no group.
-__device__ __forceinline__ bool locate(const Fp4Params& p, const Groups& t, int r, int* g, long long* row) {
+// The rows of one 128-row block of scales: [row, end) of group g, fewer than
+// 128 at a group's end; false: the block holds none.
+struct RowBlock {
+  int g, row, end;
+};
+
+__device__ __forceinline__ bool row_block(const Fp4Params& p, const Groups& t, int rb, RowBlock* o) {
   if (p.offsets != nullptr) {
-    if (r >= t.lo[p.G]) return false;
+    // the last group whose scales start at or before this block: it holds
+    // the block, as empty groups share their start with the next
     int a = 0, b = p.G - 1;
-    while (a < b) {  // the last group that starts at or before r
+    while (a < b) {
       const int mid = (a + b + 1) >> 1;
-      if (t.lo[mid] <= r)
+      if (t.sf[mid] <= rb * 128)
         a = mid;
       else
         b = mid - 1;
     }
-    *g = a;
-    *row = static_cast<long long>(t.sf[a]) + (r - t.lo[a]);
-  } else if (p.G > 1) {
-    const int per = p.M / p.G;
-    *g = r / per;
-    *row = static_cast<long long>(*g) * pad128(per) + (r - *g * per);
+    o->g = a;
+    o->row = t.lo[a] + (rb * 128 - t.sf[a]);
+    o->end = min(t.lo[a + 1], o->row + 128);
   } else {
-    *g = 0;
-    *row = r;
+    const int per = p.M / p.G, per_blocks = pad128(per) >> 7;
+    o->g = rb / per_blocks;
+    o->row = o->g * per + (rb - o->g * per_blocks) * 128;
+    o->end = min((o->g + 1) * per, o->row + 128);
   }
-  return true;
+  return o->row < o->end;
 }
 
 template <class T>
@@ -126,61 +136,94 @@ __device__ __forceinline__ float bits_to_f32<__half>(uint32_t half) {
   return __half2float(__ushort_as_half(static_cast<unsigned short>(half)));
 }
 
-// Block of B elements of type T into FP32 and its largest magnitude.
-template <class T, int B, bool VEC>
-__device__ __forceinline__ float load_block(const T* src, float (&v)[B]) {
-  float amax = 0.f;
-  bool odd = false;  // an infinity or a NaN
-  if constexpr (sizeof(T) == 4) {
-    uint32_t m = 0;
-    if constexpr (VEC) {
+// 32 bytes in one access (sm_100 and later).
+__device__ __forceinline__ void ld32(const void* p, uint32_t (&w)[8]) {
+  asm("ld.global.nc.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+      : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]), "=r"(w[4]), "=r"(w[5]), "=r"(w[6]), "=r"(w[7])
+      : "l"(p));
+}
+__device__ __forceinline__ void st32(void* p, const uint32_t* w) {
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(w[0]), "r"(w[1]), "r"(w[2]),
+               "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+               : "memory");
+}
+
+// Words of a block of elements of E bytes, in accesses of VB bytes.
+template <int E, int VB, int W>
+__device__ __forceinline__ void load_words(const void* src, uint32_t (&w)[W]) {
+  if constexpr (VB == 32) {
 #pragma unroll
-      for (int i = 0; i < B / 4; ++i) {
-        const float4 q = __ldg(reinterpret_cast<const float4*>(src) + i);
-        v[4 * i] = q.x;
-        v[4 * i + 1] = q.y;
-        v[4 * i + 2] = q.z;
-        v[4 * i + 3] = q.w;
-      }
-    } else {
+    for (int i = 0; i < W / 8; ++i)
+      ld32(static_cast<const char*>(src) + 32 * i, *reinterpret_cast<uint32_t(*)[8]>(&w[8 * i]));
+  } else if constexpr (VB == 16) {
 #pragma unroll
-      for (int i = 0; i < B; ++i) v[i] = __ldg(reinterpret_cast<const float*>(src) + i);
+    for (int i = 0; i < W / 4; ++i) {
+      const uint4 q = __ldg(static_cast<const uint4*>(src) + i);
+      w[4 * i] = q.x;
+      w[4 * i + 1] = q.y;
+      w[4 * i + 2] = q.z;
+      w[4 * i + 3] = q.w;
     }
+  } else if constexpr (E == 4) {
 #pragma unroll
-    for (int i = 0; i < B; ++i) m = max(m, __float_as_uint(v[i]) & 0x7fffffffu);
-    odd = m >= 0x7f800000u;
+    for (int i = 0; i < W; ++i) w[i] = __ldg(static_cast<const uint32_t*>(src) + i);
+  } else {
+    const unsigned short* s = static_cast<const unsigned short*>(src);
+#pragma unroll
+    for (int i = 0; i < W; ++i) w[i] = __ldg(s + 2 * i) | (static_cast<uint32_t>(__ldg(s + 2 * i + 1)) << 16);
+  }
+}
+
+template <int E, int VB, int W>
+__device__ __forceinline__ void store_words(void* dst, const uint32_t (&w)[W]) {
+  if constexpr (VB == 32) {
+#pragma unroll
+    for (int i = 0; i < W / 8; ++i) st32(static_cast<char*>(dst) + 32 * i, &w[8 * i]);
+  } else if constexpr (VB == 16) {
+#pragma unroll
+    for (int i = 0; i < W / 4; ++i)
+      static_cast<uint4*>(dst)[i] = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+  } else if constexpr (E == 4) {
+#pragma unroll
+    for (int i = 0; i < W; ++i) static_cast<uint32_t*>(dst)[i] = w[i];
+  } else {
+#pragma unroll
+    for (int i = 0; i < 2 * W; ++i)
+      static_cast<unsigned short*>(dst)[i] = static_cast<unsigned short>(w[i / 2] >> (16 * (i & 1)));
+  }
+}
+
+// A block's words as FP32 values (NEG: negated), and its largest magnitude
+// (NaN where it holds an infinity or a NaN).  Magnitudes of floats order like
+// their bits.
+template <class T, int B, bool NEG>
+__device__ __forceinline__ float unpack_block(const uint32_t* w, float (&v)[B]) {
+  uint32_t m = 0, inf;
+  float amax;
+  if constexpr (sizeof(T) == 4) {
+#pragma unroll
+    for (int i = 0; i < B; ++i) {
+      m = max(m, w[i] & 0x7fffffffu);
+      v[i] = NEG ? -__uint_as_float(w[i]) : __uint_as_float(w[i]);
+    }
+    inf = 0x7f800000u;
     amax = __uint_as_float(m);
   } else {
-    uint32_t w[B / 2];
-    if constexpr (VEC) {
-#pragma unroll
-      for (int i = 0; i < B / 8; ++i) {
-        const uint4 q = __ldg(reinterpret_cast<const uint4*>(src) + i);
-        w[4 * i] = q.x;
-        w[4 * i + 1] = q.y;
-        w[4 * i + 2] = q.z;
-        w[4 * i + 3] = q.w;
-      }
-    } else {
-      const unsigned short* s = reinterpret_cast<const unsigned short*>(src);
-#pragma unroll
-      for (int i = 0; i < B / 2; ++i) w[i] = __ldg(s + 2 * i) | (static_cast<uint32_t>(__ldg(s + 2 * i + 1)) << 16);
-    }
-    // magnitudes of 16-bit floats order like their bits
-    uint32_t m = 0;
-#pragma unroll
-    for (int i = 0; i < B / 2; ++i) m = __vmaxu2(m, w[i] & 0x7fff7fffu);
-    m = max(m & 0xffffu, m >> 16);
-    constexpr uint32_t kInf = std::is_same<T, __half>::value ? 0x7c00u : 0x7f80u;
-    odd = m >= kInf;
-    amax = bits_to_f32<T>(m);
 #pragma unroll
     for (int i = 0; i < B / 2; ++i) {
-      v[2 * i] = bits_to_f32<T>(w[i] & 0xffffu);
-      v[2 * i + 1] = bits_to_f32<T>(w[i] >> 16);
+      m = __vmaxu2(m, w[i] & 0x7fff7fffu);
+      const uint32_t x = NEG ? w[i] ^ 0x80008000u : w[i];
+      v[2 * i] = bits_to_f32<T>(x & 0xffffu);
+      if constexpr (std::is_same<T, __half>::value)
+        v[2 * i + 1] = bits_to_f32<T>(x >> 16);
+      else
+        v[2 * i + 1] = __uint_as_float(x & 0xffff0000u);
     }
+    m = max(m & 0xffffu, m >> 16);
+    inf = std::is_same<T, __half>::value ? 0x7c00u : 0x7f80u;
+    amax = bits_to_f32<T>(m);
   }
-  return odd ? __int_as_float(0x7fffffff) : amax;
+  return m >= inf ? __int_as_float(0x7fffffff) : amax;
 }
 
 // 8 FP32 values as 8 e2m1 codes (nearest even, saturating).
@@ -209,83 +252,165 @@ __device__ __forceinline__ float e4m3_to_f32(uint32_t b) {
   return __half2float(__ushort_as_half(static_cast<unsigned short>(h2 & 0xffffu)));
 }
 
-// Scales the block to codes; returns the scale byte.
+// Two FP32 operations in one instruction (sm_100 and later).
+__device__ __forceinline__ uint64_t pair_of(float lo, float hi) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+
+// The matrix's (or group's) scale and what a block's scale is computed from.
+struct GlobalScale {
+  float g, c, rc;  // g, 6 g and about 1 / (6 g)
+  bool fast;       // 6 g far from the ends of FP32
+};
+__device__ __forceinline__ GlobalScale global_scale(const float* p) {
+  GlobalScale s;
+  s.g = p != nullptr ? __ldg(p) : 1.f;
+  s.c = __fmul_rn(6.f, s.g);
+  s.rc = rcp_approx(s.c);
+  s.fast = s.c > 1e-25f && s.c < 1e25f;
+  return s;
+}
+
+// Scales the block to what its codes are rounded from (v holds -x for nvfp4,
+// x for mxfp4) and stores the scale byte in *sb; false: left to slow_block.
+//
+// nvfp4's quotients are FP32's x / d from an approximate reciprocal r of d:
+// q0 = x r is a few units in the last place off, its remainder x - q0 d is
+// exact in an FMA, and q0 plus the remainder times r rounds to the quotient
+// (Markstein, 1990).  From -x, with e = q0 d - x, every factor is a constant
+// and a zero keeps its sign, also for a zero scale (r = 0).  What could
+// overflow or lose the remainder's bits goes to slow_block, out of line, which
+// leaves registers for four blocks of threads an SM: 58 us for 32768 x 4096
+// BF16 (5.8 TB/s) against 75 us with that code here, 69 us with it out of
+// line but three blocks, and 84 us with divisions, one value at a time.
 template <int FMT, int B>
-__device__ __forceinline__ uint32_t quantize_block(float (&v)[B], float amax, float g) {
-  if (!(amax <= 3.4028235e38f)) {  // infinity or NaN in the block
-#pragma unroll
-    for (int i = 0; i < B; ++i) v[i] = 0.f;
-    return FMT == kNvfp4 ? 0x7fu : 0xffu;
-  }
+__device__ __forceinline__ bool quantize_block(float (&v)[B], float amax, const GlobalScale& gs, uint32_t* sb) {
   if constexpr (FMT == kMxfp4) {
-    const int e = static_cast<int>(__float_as_uint(amax) >> 23) - 2;
-    const uint32_t s = static_cast<uint32_t>(max(e, 0));
+    const uint32_t s = static_cast<uint32_t>(max(static_cast<int>(__float_as_uint(amax) >> 23) - 2, 0));
     const float inv = __uint_as_float((254u - s) << 23);  // 2^(127 - s): exact
 #pragma unroll
     for (int i = 0; i < B; ++i) v[i] *= inv;
-    return s;
+    *sb = s;
+    return amax <= 3.4028235e38f;
   } else {
-    const uint32_t sb = cvt_e4m3(fminf(__fdiv_rn(amax, __fmul_rn(6.f, g)), 448.f));
-    const float step = __fmul_rn(e4m3_to_f32(sb), g);
-    if (!(step > 0.f)) {
-      // zero scale: codes are zeros of x's sign
+    const float t0 = amax * gs.rc;
+    const uint32_t s = cvt_e4m3(fminf(fmaf(fmaf(-t0, gs.c, amax), gs.rc, t0), 448.f));
+    const float step = __fmul_rn(e4m3_to_f32(s), gs.g);
+    const float r = step > 0.f ? rcp_approx(step) : 0.f;
+    const uint64_t r2 = pair_of(-r, -r), s2 = pair_of(step, step);
 #pragma unroll
-      for (int i = 0; i < B; ++i) v[i] = copysignf(0.f, v[i]);
-    } else if (const float r = __frcp_rn(step); step > 1e-30f && step < 1e30f && amax * r < 1e30f) {
-      // x / step in FP32 from the rounded reciprocal r: q0 = x r, then one
-      // correction by the exact remainder (Markstein, 1990); nothing here
-      // overflows or loses the remainder's bits
-#pragma unroll
-      for (int i = 0; i < B; ++i) {
-        const float q0 = v[i] * r;
-        v[i] = copysignf(fmaf(fmaf(-q0, step, v[i]), r, q0), v[i]);
-      }
-    } else {
-#pragma unroll
-      for (int i = 0; i < B; ++i) v[i] = __fdiv_rn(v[i], step);
+    for (int i = 0; i < B; i += 2) {
+      const uint64_t x2 = pair_of(v[i], v[i + 1]);
+      const uint64_t q0 = mul2(x2, r2);
+      const uint64_t q = fma2(fma2(q0, s2, x2), r2, q0);
+      asm("mov.b64 {%0, %1}, %2;" : "=f"(v[i]), "=f"(v[i + 1]) : "l"(q));
     }
-    return sb;
+    *sb = s;
+    return gs.fast && t0 < 1e30f;
   }
 }
 
-// Warp w of the grid takes 32 consecutive blocks of one row, a lane each.
-template <class T, int FMT, bool VEC>
-__global__ void __launch_bounds__(kFp4Threads) quantize_kernel(const __grid_constant__ Fp4Params p) {
+// One block, value by value: an infinity or a NaN in it, or magnitudes near
+// the ends of FP32.  Returns the scale byte.
+template <class T, int FMT>
+__device__ __noinline__ uint32_t slow_block(const T* src, float g, uint8_t* codes) {
   constexpr int B = FMT == kNvfp4 ? 16 : 32;
+  float amax = 0.f;
+  bool finite = true;
+  for (int i = 0; i < B; ++i) {
+    const float a = fabsf(static_cast<float>(src[i]));
+    finite = finite && a <= 3.4028235e38f;
+    amax = fmaxf(amax, a);
+  }
+  uint32_t s;
+  float step;
+  if constexpr (FMT == kNvfp4) {
+    s = finite ? cvt_e4m3(fminf(__fdiv_rn(amax, __fmul_rn(6.f, g)), 448.f)) : 0x7fu;
+    step = __fmul_rn(e4m3_to_f32(s), g);
+  } else {
+    s = finite ? static_cast<uint32_t>(max(static_cast<int>(__float_as_uint(amax) >> 23) - 2, 0)) : 0xffu;
+    step = 0.f;  // only blocks that are not finite come here
+  }
+  for (int i = 0; i < B; i += 8) {
+    float q[8];
+    for (int j = 0; j < 8; ++j) {
+      const float x = static_cast<float>(src[i + j]);
+      q[j] = !finite ? 0.f : step > 0.f ? __fdiv_rn(x, step) : copysignf(0.f, x);
+    }
+    *reinterpret_cast<uint32_t*>(codes + i / 2) = pack_e2m1x8(q);
+  }
+  return s;
+}
+
+// A unit is one 128-row block of scales x U scale tiles along K, for 8 warps.
+// A warp takes rows 2 i, 2 i + 1 of each group of 32 rows (8 rows) and the 4
+// blocks of a tile: its 32 scales are one 32-byte sector of the tile, its
+// loads and code stores whole sectors.  All U loads of a lane are issued
+// before the first is used.
+template <class T, int FMT, int VB, int U>
+__global__ void __launch_bounds__(kFp4Threads, 4) quantize_kernel(const __grid_constant__ Fp4Params p) {
+  constexpr int B = FMT == kNvfp4 ? 16 : 32;
+  constexpr int W = B * static_cast<int>(sizeof(T)) / 4;
   extern __shared__ int tab[];
   const Groups t{tab, tab + p.G + 1};
-  if (p.offsets != nullptr) build_groups(p, t);
-  const int per_row = p.lanes_per_row >> 5;
-  const long long items = static_cast<long long>(p.M) * per_row;
+  int row_blocks = p.row_blocks;
+  if (p.offsets != nullptr) row_blocks = build_groups(p, t);
   const int lane = static_cast<int>(threadIdx.x & 31u);
-  const long long stride = static_cast<long long>(gridDim.x) * (kFp4Threads / 32);
-  for (long long w = static_cast<long long>(blockIdx.x) * (kFp4Threads / 32) + (threadIdx.x >> 5); w < items;
-       w += stride) {
-    const int r = static_cast<int>(w / per_row);
-    const int b = static_cast<int>(w % per_row) * 32 + lane;
-    int g;
-    long long srow;
-    const bool has = locate(p, t, r, &g, &srow);
-    uint32_t sb = 0;  // blocks past the row's last: the tile's padding
-    if (has && b < p.nb) {
-      float v[B];
-      const float amax = load_block<T, B, VEC>(static_cast<const T*>(p.x) + r * p.ldx + static_cast<long long>(b) * B, v);
-      const float gs = p.global != nullptr ? __ldg(p.global + (p.n_global > 1 ? g : 0)) : 1.f;
-      sb = quantize_block<FMT, B>(v, amax, gs);
-      uint32_t c[B / 8];
+  const int q = lane >> 3, h = (lane >> 2) & 1, bl = lane & 3;
+  const long long units = static_cast<long long>(row_blocks) * p.chunks;
+  for (long long u = blockIdx.x; u < units; u += gridDim.x) {
+    const int rb = static_cast<int>(u / p.chunks);
+    const int kt0 = static_cast<int>(u - static_cast<long long>(rb) * p.chunks) * U;
+    RowBlock r;
+    if (!row_block(p, t, rb, &r)) continue;
+    const GlobalScale gs = global_scale(p.global != nullptr ? p.global + (p.n_global > 1 ? r.g : 0) : nullptr);
 #pragma unroll
-      for (int i = 0; i < B / 8; ++i) c[i] = pack_e2m1x8(v + 8 * i);
-      uint8_t* dst = p.codes + static_cast<long long>(r) * (p.K / 2) + static_cast<long long>(b) * (B / 2);
-      if constexpr (B == 16)
-        *reinterpret_cast<uint2*>(dst) = make_uint2(c[0], c[1]);
-      else
-        *reinterpret_cast<uint4*>(dst) = make_uint4(c[0], c[1], c[2], c[3]);
+    for (int half = 0; half < 2; ++half) {
+      const int in32 = (half * (kFp4Threads / 32) + static_cast<int>(threadIdx.x >> 5)) * 2 + h;
+      const int row = r.row + q * 32 + in32;
+      if (row >= r.end) continue;
+      const T* src = static_cast<const T*>(p.x) + row * p.ldx;
+      uint32_t w[U][W];
+#pragma unroll
+      for (int i = 0; i < U; ++i) {
+        const int b = (kt0 + i) * 4 + bl;
+        if (b < p.nb) load_words<sizeof(T), VB, W>(src + static_cast<long long>(b) * B, w[i]);
+      }
+#pragma unroll
+      for (int i = 0; i < U; ++i) {
+        const int b = (kt0 + i) * 4 + bl;
+        uint32_t sb = 0;  // blocks past the row's last: the tile's padding
+        if (b < p.nb) {
+          float v[B];
+          const float amax = unpack_block<T, B, FMT == kNvfp4>(w[i], v);
+          const bool done = quantize_block<FMT, B>(v, amax, gs, &sb);
+          uint32_t c[B / 8];
+#pragma unroll
+          for (int j = 0; j < B / 8; ++j) c[j] = pack_e2m1x8(v + 8 * j);
+          uint8_t* dst = p.codes + static_cast<long long>(row) * (p.K / 2) + static_cast<long long>(b) * (B / 2);
+          if constexpr (B == 16)
+            *reinterpret_cast<uint2*>(dst) = make_uint2(c[0], c[1]);
+          else
+            *reinterpret_cast<uint4*>(dst) = make_uint4(c[0], c[1], c[2], c[3]);
+          if (!done) sb = slow_block<T, FMT>(src + static_cast<long long>(b) * B, gs.g, dst);
+        }
+        if (kt0 + i < p.k_tiles)
+          p.scales[(static_cast<long long>(rb) * p.k_tiles + kt0 + i) * kScaleTileBytes + in32 * 16 + q * 4 + bl] =
+              static_cast<uint8_t>(sb);
+      }
     }
-    // four neighbours' scales are one word of a tile
-    sb |= __shfl_down_sync(0xffffffffu, sb, 1) << 8;
-    sb |= __shfl_down_sync(0xffffffffu, sb, 2) << 16;
-    if (has && (lane & 3) == 0 && (b >> 2) < p.k_tiles)
-      *reinterpret_cast<uint32_t*>(p.scales + fp4_scale_offset(srow, b, p.k_tiles)) = sb;
   }
 }
 
@@ -300,75 +425,78 @@ __device__ __forceinline__ uint32_t pack2<__half>(float a, float b) {
   return pack_f16x2(a, b);
 }
 
-template <class T, int FMT, bool VEC>
+// The same units and lanes, from codes and scales to values.
+template <class T, int FMT, int VB, int U>
 __global__ void __launch_bounds__(kFp4Threads) dequantize_kernel(const __grid_constant__ Fp4Params p) {
   constexpr int B = FMT == kNvfp4 ? 16 : 32;
+  constexpr int W = B * static_cast<int>(sizeof(T)) / 4;
   extern __shared__ int tab[];
   const Groups t{tab, tab + p.G + 1};
-  if (p.offsets != nullptr) build_groups(p, t);
-  const int per_row = p.lanes_per_row >> 5;
-  const long long items = static_cast<long long>(p.M) * per_row;
+  int row_blocks = p.row_blocks;
+  if (p.offsets != nullptr) row_blocks = build_groups(p, t);
   const int lane = static_cast<int>(threadIdx.x & 31u);
-  const long long stride = static_cast<long long>(gridDim.x) * (kFp4Threads / 32);
-  for (long long w = static_cast<long long>(blockIdx.x) * (kFp4Threads / 32) + (threadIdx.x >> 5); w < items;
-       w += stride) {
-    const int r = static_cast<int>(w / per_row);
-    const int b = static_cast<int>(w % per_row) * 32 + lane;
-    int g;
-    long long srow;
-    if (b >= p.nb || !locate(p, t, r, &g, &srow)) continue;
-    const uint8_t* src = p.codes + static_cast<long long>(r) * (p.K / 2) + static_cast<long long>(b) * (B / 2);
-    uint32_t c[B / 8];
-    if constexpr (B == 16) {
-      const uint2 q = __ldg(reinterpret_cast<const uint2*>(src));
-      c[0] = q.x;
-      c[1] = q.y;
-    } else {
-      const uint4 q = __ldg(reinterpret_cast<const uint4*>(src));
-      c[0] = q.x;
-      c[1] = q.y;
-      c[2] = q.z;
-      c[3] = q.w;
-    }
-    const uint32_t sb = __ldg(p.scales + fp4_scale_offset(srow, b, p.k_tiles));
-    float s;
-    if constexpr (FMT == kNvfp4)
-      s = e4m3_to_f32(sb);
-    else
-      s = sb == 0xffu ? __int_as_float(0x7fffffff) : sb == 0 ? __uint_as_float(0x00400000u) : __uint_as_float(sb << 23);
-    const float gs = p.global != nullptr ? __ldg(p.global + (p.n_global > 1 ? g : 0)) : 1.f;
-    float v[B];
+  const int q = lane >> 3, h = (lane >> 2) & 1, bl = lane & 3;
+  const long long units = static_cast<long long>(row_blocks) * p.chunks;
+  for (long long u = blockIdx.x; u < units; u += gridDim.x) {
+    const int rb = static_cast<int>(u / p.chunks);
+    const int kt0 = static_cast<int>(u - static_cast<long long>(rb) * p.chunks) * U;
+    RowBlock r;
+    if (!row_block(p, t, rb, &r)) continue;
+    const float gs = p.global != nullptr ? __ldg(p.global + (p.n_global > 1 ? r.g : 0)) : 1.f;
 #pragma unroll
-    for (int i = 0; i < B / 2; ++i) {
-      uint32_t h2;
-      const uint16_t byte = static_cast<uint16_t>((c[i / 4] >> (8 * (i % 4))) & 0xffu);
-      asm("{\n\t.reg .b8 lo, hi;\n\tmov.b16 {lo, hi}, %1;\n\tcvt.rn.f16x2.e2m1x2 %0, lo;\n\t}" : "=r"(h2) : "h"(byte));
-      const __half2 h = *reinterpret_cast<const __half2*>(&h2);
-      v[2 * i] = __low2float(h) * s * gs;
-      v[2 * i + 1] = __high2float(h) * s * gs;
-    }
-    T* dst = static_cast<T*>(p.y) + r * p.ldx + static_cast<long long>(b) * B;
-    if constexpr (sizeof(T) == 4) {
-      if constexpr (VEC) {
+    for (int half = 0; half < 2; ++half) {
+      const int in32 = (half * (kFp4Threads / 32) + static_cast<int>(threadIdx.x >> 5)) * 2 + h;
+      const int row = r.row + q * 32 + in32;
+      if (row >= r.end) continue;
+      uint32_t c[U][B / 8];
+      uint32_t sb[U];
 #pragma unroll
-        for (int i = 0; i < B / 4; ++i)
-          reinterpret_cast<float4*>(dst)[i] = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
-      } else {
-#pragma unroll
-        for (int i = 0; i < B; ++i) reinterpret_cast<float*>(dst)[i] = v[i];
+      for (int i = 0; i < U; ++i) {
+        const int b = (kt0 + i) * 4 + bl;
+        if (b >= p.nb) continue;
+        const uint8_t* src = p.codes + static_cast<long long>(row) * (p.K / 2) + static_cast<long long>(b) * (B / 2);
+        if constexpr (B == 16) {
+          const uint2 x = __ldg(reinterpret_cast<const uint2*>(src));
+          c[i][0] = x.x;
+          c[i][1] = x.y;
+        } else {
+          const uint4 x = __ldg(reinterpret_cast<const uint4*>(src));
+          c[i][0] = x.x;
+          c[i][1] = x.y;
+          c[i][2] = x.z;
+          c[i][3] = x.w;
+        }
+        sb[i] = __ldg(p.scales + (static_cast<long long>(rb) * p.k_tiles + kt0 + i) * kScaleTileBytes + in32 * 16 +
+                      q * 4 + bl);
       }
-    } else {
-      uint32_t o[B / 2];
 #pragma unroll
-      for (int i = 0; i < B / 2; ++i) o[i] = pack2<T>(v[2 * i], v[2 * i + 1]);
-      if constexpr (VEC) {
+      for (int i = 0; i < U; ++i) {
+        const int b = (kt0 + i) * 4 + bl;
+        if (b >= p.nb) continue;
+        float s;
+        if constexpr (FMT == kNvfp4)
+          s = e4m3_to_f32(sb[i]);
+        else
+          s = sb[i] == 0xffu ? __int_as_float(0x7fffffff)
+                             : sb[i] == 0 ? __uint_as_float(0x00400000u) : __uint_as_float(sb[i] << 23);
+        uint32_t o[W];
 #pragma unroll
-        for (int i = 0; i < B / 8; ++i)
-          reinterpret_cast<uint4*>(dst)[i] = make_uint4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
-      } else {
-#pragma unroll
-        for (int i = 0; i < B; ++i)
-          reinterpret_cast<unsigned short*>(dst)[i] = static_cast<unsigned short>(o[i / 2] >> (16 * (i & 1)));
+        for (int j = 0; j < B / 2; ++j) {
+          uint32_t h2;
+          const uint16_t byte = static_cast<uint16_t>((c[i][j / 4] >> (8 * (j % 4))) & 0xffu);
+          asm("{\n\t.reg .b8 lo, hi;\n\tmov.b16 {lo, hi}, %1;\n\tcvt.rn.f16x2.e2m1x2 %0, lo;\n\t}"
+              : "=r"(h2)
+              : "h"(byte));
+          const __half2 v2 = *reinterpret_cast<const __half2*>(&h2);
+          const float lo = __low2float(v2) * s * gs, hi = __high2float(v2) * s * gs;
+          if constexpr (sizeof(T) == 4) {
+            o[2 * j] = __float_as_uint(lo);
+            o[2 * j + 1] = __float_as_uint(hi);
+          } else {
+            o[j] = pack2<T>(lo, hi);
+          }
+        }
+        store_words<sizeof(T), VB, W>(static_cast<T*>(p.y) + row * p.ldx + static_cast<long long>(b) * B, o);
       }
     }
   }
@@ -413,16 +541,42 @@ Fp4Params make_params(const void* x, void* y, int M, int K, int ldx, int format,
   p.G = G;
   p.k_tiles = fp4_k_tiles(K, format);
   p.nb = K / fp4_block(format);
-  p.lanes_per_row = (p.nb + 31) / 32 * 32;
+  p.row_blocks = offsets != nullptr ? static_cast<int>((M + 127LL * std::min(G, M)) / 128)
+                                    : static_cast<int>(static_cast<long long>(G) * pad128(M / G) / 128);
   return p;
 }
 
 using Fp4Kernel = void (*)(Fp4Params);
 
-template <class T, bool VEC>
-Fp4Kernel pick(bool quant, int format) {
-  if (quant) return format == kNvfp4 ? quantize_kernel<T, kNvfp4, VEC> : quantize_kernel<T, kMxfp4, VEC>;
-  return format == kNvfp4 ? dequantize_kernel<T, kNvfp4, VEC> : dequantize_kernel<T, kMxfp4, VEC>;
+// Scale tiles of a unit: 128 bytes of 16-bit input a lane, half of it on the
+// larger types' side; 1 where that leaves SMs idle.
+template <class T, int FMT>
+constexpr int unit_tiles() {
+  return (FMT == kNvfp4 ? 4 : 2) / (sizeof(T) == 4 ? 2 : 1);
+}
+
+template <class T, int FMT, int VB>
+Fp4Kernel pick_unit(bool quant, bool wide) {
+  constexpr int U = unit_tiles<T, FMT>();
+  if (quant) return wide ? quantize_kernel<T, FMT, VB, U> : quantize_kernel<T, FMT, VB, 1>;
+  return wide ? dequantize_kernel<T, FMT, VB, U> : dequantize_kernel<T, FMT, VB, 1>;
+}
+
+template <class T, int FMT>
+Fp4Kernel pick_access(bool quant, bool wide, int vb) {
+  return vb == 32   ? pick_unit<T, FMT, 32>(quant, wide)
+         : vb == 16 ? pick_unit<T, FMT, 16>(quant, wide)
+                    : pick_unit<T, FMT, 0>(quant, wide);
+}
+
+template <class T>
+Fp4Kernel pick(bool quant, bool wide, int format, int vb) {
+  return format == kNvfp4 ? pick_access<T, kNvfp4>(quant, wide, vb) : pick_access<T, kMxfp4>(quant, wide, vb);
+}
+
+template <class T>
+int tiles_of(int format) {
+  return format == kNvfp4 ? unit_tiles<T, kNvfp4>() : unit_tiles<T, kMxfp4>();
 }
 
 bwg_status run_fp4(bool quant, const void* x, void* y, int dtype, int M, int K, int ldx, int format,
@@ -434,17 +588,23 @@ bwg_status run_fp4(bool quant, const void* x, void* y, int dtype, int M, int K, 
   if (st != BWG_OK || empty) return st;
   Runtime rt;
   if ((st = runtime_device(&rt)) != BWG_OK) return st;
-  const Fp4Params p = make_params(x, y, M, K, ldx, format, global, n_global, offsets, G, codes, scales, rt);
+  Fp4Params p = make_params(x, y, M, K, ldx, format, global, n_global, offsets, G, codes, scales, rt);
   const int elt = dtype == BWG_OUT_FP32 ? 4 : 2;
-  const bool vec = (reinterpret_cast<uintptr_t>(mat) & 15u) == 0 && (static_cast<long long>(ldx) * elt) % 16 == 0;
-  const Fp4Kernel k = dtype == BWG_OUT_FP32   ? (vec ? pick<float, true>(quant, format) : pick<float, false>(quant, format))
-                      : dtype == BWG_OUT_BF16 ? (vec ? pick<__nv_bfloat16, true>(quant, format)
-                                                     : pick<__nv_bfloat16, false>(quant, format))
-                                              : (vec ? pick<__half, true>(quant, format)
-                                                     : pick<__half, false>(quant, format));
-  const long long warps = static_cast<long long>(M) * (p.lanes_per_row / 32);
-  const long long blocks = std::min<long long>((warps + kFp4Threads / 32 - 1) / (kFp4Threads / 32), rt.sm_count * 8LL);
-  const size_t smem = offsets != nullptr ? (2 * static_cast<size_t>(G) + 1) * sizeof(int) : 0;
+  const uintptr_t bits = reinterpret_cast<uintptr_t>(mat) | static_cast<uintptr_t>(static_cast<long long>(ldx) * elt);
+  const int vb = (bits & 31u) == 0 ? 32 : (bits & 15u) == 0 ? 16 : 0;
+  const int tiles = dtype == BWG_OUT_FP32   ? tiles_of<float>(format)
+                    : dtype == BWG_OUT_BF16 ? tiles_of<__nv_bfloat16>(format)
+                                            : tiles_of<__half>(format);
+  const long long wide_units = static_cast<long long>(p.row_blocks) * ((p.k_tiles + tiles - 1) / tiles);
+  const bool wide = wide_units >= 2LL * rt.sm_count;
+  const int U = wide ? tiles : 1;
+  p.chunks = (p.k_tiles + U - 1) / U;
+  const Fp4Kernel k = dtype == BWG_OUT_FP32   ? pick<float>(quant, wide, format, vb)
+                      : dtype == BWG_OUT_BF16 ? pick<__nv_bfloat16>(quant, wide, format, vb)
+                                              : pick<__half>(quant, wide, format, vb);
+  const long long units = static_cast<long long>(p.row_blocks) * p.chunks;
+  const long long blocks = std::min<long long>(units, rt.sm_count * 8LL);
+  const size_t smem = offsets != nullptr ? (2 * static_cast<size_t>(G) + 2) * sizeof(int) : 0;
   k<<<static_cast<unsigned>(blocks), kFp4Threads, smem, s>>>(p);
   return runtime_status(cudaGetLastError());
 }
