@@ -59,7 +59,7 @@ struct Fp4GemmParams {
   int num_w_tiles;         // tiles along the weights
   int w_blocks;            // scale row blocks of one group's weights
   int swiglu_up;           // SwiGLU: first weight row of the up half
-  int stages, out_dtype, group_m;
+  int out_dtype, group_m;
 };
 
 enum : uint32_t { kRoleProducer = 0, kRoleMma = 1, kRoleEpilogue = 2 };
@@ -161,7 +161,11 @@ __device__ __forceinline__ Tile tile_at(const Fp4GemmParams& p, const Tables& t,
 
 __device__ __forceinline__ float silu_mul(float g, float u) { return g * rcp_approx(1.0f + __expf(-g)) * u; }
 
-constexpr int threads_of(int nc) { return nc == 1 ? 192 : 384; }
+// Warps 0, 2 and 3 load, warp 1 issues the MMAs, warps 4.. are the epilogue.
+constexpr int threads_of(int nc) { return nc == 1 ? 256 : 384; }
+// Ring depth: the MMA loop is unrolled over it, so that every stage's
+// addresses are constants.
+constexpr int stages_of(int nc) { return nc == 1 ? 6 : 4; }
 
 // Shared memory: stage s holds [NC weight blocks][activation rows][scales].
 template <int NC>
@@ -187,17 +191,17 @@ __global__ void __launch_bounds__(threads_of(NC), 1) fp4_pair_kernel(const __gri
   constexpr uint32_t kSfBytes = kTilesK * kScaleTileBytes;
   constexpr uint32_t kStageTx = 2u * (L::kStageW + kTokBytes + (NC + 2) * kSfBytes);
   constexpr int kWRows = SW ? 256 : 256 * NC;        // output columns of a tile
-  constexpr uint32_t kEpi0 = NC == 1 ? 2u : 4u;
+  constexpr uint32_t kEpi0 = 4u;
   constexpr uint32_t kAccCols = kTok;
   constexpr uint32_t kSfCol0 = 2 * kTok;             // scales start after the two accumulators
   constexpr uint32_t kSfCols = (NC + 2) * kTilesK * 4;  // TMEM columns of one stage's scales
-  static_assert(kSfCol0 + 2 * kSfCols <= kTmemCols, "two accumulators and two stages of scales");
+  static_assert(kSfCol0 + kSfCols <= kTmemCols, "two accumulators and a stage's scales");
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
   const uint32_t warp = threadIdx.x >> 5;
   const uint32_t lane = threadIdx.x & 31u;
   const uint32_t rank = cluster_ctarank();
-  const int S = p.stages;
+  constexpr int S = stages_of(NC);
   const uint32_t bars = base + static_cast<uint32_t>(S) * L::kStage;
   auto full_bar = [&](int s) { return bars + 8u * s; };
   auto empty_bar = [&](int s) { return bars + 8u * (S + s); };
@@ -219,7 +223,7 @@ __global__ void __launch_bounds__(threads_of(NC), 1) fp4_pair_kernel(const __gri
     }
     fence_mbarrier_init();
   }
-  if (warp == 2) {
+  if (warp == 4) {
     const bool ok = build_tables(p, tb);
     if (!ok && blockIdx.x == 0 && lane == 0) record_fault(p.err, kFaultBadOffsets, 0, 0, 0, 0);
   }
@@ -242,36 +246,43 @@ __global__ void __launch_bounds__(threads_of(NC), 1) fp4_pair_kernel(const __gri
   const int total = tb.prefix[p.G];
   bool aborted = false;
 
-  if (warp == 0) {
-    // ---- TMA producer -------------------------------------------------------
-    if (lane == 0) {
+  if (warp < 4 && warp != 1) {
+    // ---- TMA producers --------------------------------------------------------
+    // One warp for each weight block and one for the activations (NC == 1: the
+    // third has none).  A stage takes 6 loads; one diverged thread issuing
+    // them needs about 900 clocks, more than the stage's MMAs (768).  Warps
+    // that stay together and elect a lane need about 50 clocks a load, and
+    // three of them share the loads.
+    const int job = warp == 0 ? 0 : static_cast<int>(warp) - 1;  // 0, 1: weight block, 2: activations
+    if (job == 2 || job < NC) {
       int s = 0;
       uint32_t ph = 0;
       for (int u = first; u < total && !aborted; u += stride) {
         const Tile tl = tile_at<kWRows>(p, tb, u);
-        const int w_row = tl.w0 + static_cast<int>(rank) * 128;
-        const int a_row = tl.t0 + static_cast<int>(rank) * (tl.n / 2);
+        const int row = job == 2 ? tl.t0 + static_cast<int>(rank) * (tl.n / 2)
+                                 : tl.w0 + static_cast<int>(rank) * 128 + job * (SW ? p.swiglu_up : 256);
+        const int sf_row = job == 2 ? tl.srow / 128 : tl.g * p.w_blocks + row / 128;
         for (int kb = 0; kb < p.num_k_blocks; ++kb) {
-          if (!mbar_wait(empty_bar(s), ph ^ 1u, p.timeout_ns)) {
-            record_fault(p.err, kFaultTimeout, kRoleProducer, kBarEmpty, s, ph ^ 1u);
+          if (!warp_wait_cta(empty_bar(s), ph ^ 1u, p.timeout_ns)) {
+            if (lane == 0) record_fault(p.err, kFaultTimeout, kRoleProducer, kBarEmpty, s, ph ^ 1u);
             aborted = true;
             break;
           }
-          const uint32_t st = base + static_cast<uint32_t>(s) * L::kStage;
-          if (rank == 0) mbar_arrive_expect_tx(full_bar(s), kStageTx);
-          const uint32_t fb = mapa_shared(full_bar(s), 0);
-#pragma unroll
-          for (int c = 0; c < NC; ++c) {
-            const int row = SW ? w_row + c * p.swiglu_up : w_row + c * 256;
-            tma_load_3d_pair(st + c * kWBytes, &p.map_w, fb, kb * kKBytes, row, tl.g);
-            tma_load_3d_pair(st + L::kStageW + kTokBytes + c * L::kSfBlock, &p.map_ws, fb, 0, kb * kTilesK,
-                             tl.g * p.w_blocks + row / 128);
+          if (elect_one()) {
+            const uint32_t st = base + static_cast<uint32_t>(s) * L::kStage;
+            const uint32_t fb = mapa_shared(full_bar(s), 0);
+            if (job == 2) {
+              tma_load_2d_pair(st + L::kStageW, &p.map_a, fb, kb * kKBytes, row);
+              // both CTAs need the scales of all of the instruction's N; a
+              // box of two row blocks (the second may lie past the end: zeros)
+              tma_load_3d_pair(st + L::kStageW + kTokBytes + NC * L::kSfBlock, &p.map_as, fb, 0, kb * kTilesK, sf_row);
+            } else {
+              if (job == 0 && rank == 0) mbar_arrive_expect_tx(full_bar(s), kStageTx);
+              tma_load_3d_pair(st + job * kWBytes, &p.map_w, fb, kb * kKBytes, row, tl.g);
+              tma_load_3d_pair(st + L::kStageW + kTokBytes + job * L::kSfBlock, &p.map_ws, fb, 0, kb * kTilesK, sf_row);
+            }
           }
-          tma_load_2d_pair(st + L::kStageW, &p.map_a, fb, kb * kKBytes, a_row);
-          // both CTAs need the scales of all of the instruction's N; a box
-          // of two row blocks (the second may lie past the end: zeros)
-          tma_load_3d_pair(st + L::kStageW + kTokBytes + NC * L::kSfBlock, &p.map_as, fb, 0, kb * kTilesK,
-                           tl.srow / 128);
+          __syncwarp();
           if (++s == S) {
             s = 0;
             ph ^= 1u;
@@ -282,35 +293,48 @@ __global__ void __launch_bounds__(threads_of(NC), 1) fp4_pair_kernel(const __gri
     __syncwarp();
   } else if (warp == 1) {
     // ---- MMA issuer (CTA 0 of the pair) ------------------------------------
-    if (rank == 0) {
-      int s = 0;
-      uint32_t ph = 0, acc_ph = 0, sf_buf = 0;
-      int acc = 0;
-      for (int u = first; u < total && !aborted; u += stride) {
-        const Tile tl = tile_at<kWRows>(p, tb, u);
-        for (int a = 0; a < NC; ++a) {
-          const int slot = NC == 1 ? acc : a;
-          if (!warp_wait_all(acc_empty(slot), acc_ph ^ 1u, p.timeout_ns)) {
-            if (lane == 0) record_fault(p.err, kFaultTimeout, kRoleMma, kBarAccEmpty, slot, acc_ph ^ 1u);
-            aborted = true;
+    // A stage is 16 or 24 tcgen05 instructions and their issue, not the
+    // tensor cores, can set the pace: the operands are kept uniform (the ring
+    // unrolled, tile values through a warp reduction, TMEM addresses constant:
+    // all 512 columns are allocated, so they start at 0), and a stage's full
+    // barrier is asked before the stage before it is issued.
+    if (rank == 0 && first < total) {
+      uint32_t ph = 0, acc_ph = 0;
+      int acc = 0, u = first, kb = 0;
+      uint32_t shift = 0, idesc0 = 0;
+      bool two_blocks = false, ready = false, more = true;
+      while (more) {
+#pragma unroll
+        for (int s = 0; s < S; ++s) {
+          if (!more) break;
+          if (kb == 0) {
+            const Tile tl = tile_at<kWRows>(p, tb, u);
+            const uint32_t n = __reduce_max_sync(0xffffffffu, static_cast<uint32_t>(tl.n));
+            shift = __reduce_max_sync(0xffffffffu, static_cast<uint32_t>(tl.srow & 127)) / 32u;
+            two_blocks = shift * 32u + n > 128u;
+            idesc0 = make_idesc_fp4(FMT, 256, n, 0);
+            for (int a = 0; a < NC; ++a) {
+              const int slot = NC == 1 ? acc : a;
+              if (!warp_wait_all(acc_empty(slot), acc_ph ^ 1u, p.timeout_ns)) {
+                if (lane == 0) record_fault(p.err, kFaultTimeout, kRoleMma, kBarAccEmpty, slot, acc_ph ^ 1u);
+                aborted = true;
+              }
+            }
+            tc_fence_after();
           }
-        }
-        if (aborted) break;
-        tc_fence_after();
-        const uint32_t shift = static_cast<uint32_t>(tl.srow & 127) / 32u;
-        const bool two_blocks = shift * 32u + static_cast<uint32_t>(tl.n) > 128u;
-        const uint32_t idesc0 = make_idesc_fp4(FMT, 256, static_cast<uint32_t>(tl.n), 0);
-        for (int kb = 0; kb < p.num_k_blocks; ++kb) {
-          if (!warp_wait_all(full_bar(s), ph, p.timeout_ns)) {
+          if (!ready && !warp_wait_cta(full_bar(s), ph, p.timeout_ns)) {
             if (lane == 0) record_fault(p.err, kFaultTimeout, kRoleMma, kBarFull, s, ph);
             aborted = true;
+          }
+          if (aborted) {
+            more = false;
             break;
           }
           tc_fence_after();
+          const bool ask = mbar_test_wait_cta(full_bar(s + 1 == S ? 0 : s + 1), s + 1 == S ? ph ^ 1u : ph);
           if (elect_one()) {
             const uint32_t st = base + static_cast<uint32_t>(s) * L::kStage;
             const uint32_t sf = st + L::kStageW + kTokBytes;
-            const uint32_t sf_tmem = tmem + kSfCol0 + sf_buf * kSfCols;
             const int steps = kb == p.num_k_blocks - 1 ? p.last_steps : 4;
             // scales: block c's tile j to columns (c * kTilesK + j) * 4, the
             // activations' two row blocks of tile j side by side
@@ -318,10 +342,10 @@ __global__ void __launch_bounds__(threads_of(NC), 1) fp4_pair_kernel(const __gri
             for (int j = 0; j < kTilesK; ++j) {
 #pragma unroll
               for (int c = 0; c < NC; ++c)
-                tmem_copy_scales<2>(sf_tmem + (c * kTilesK + j) * 4,
+                tmem_copy_scales<2>(kSfCol0 + (c * kTilesK + j) * 4,
                                     make_smem_desc(sf + c * L::kSfBlock + j * kScaleTileBytes, 16, 128, kSwizzleNone));
               const uint32_t sfb = sf + NC * L::kSfBlock + j * kScaleTileBytes;
-              const uint32_t col = sf_tmem + (NC * kTilesK + 2 * j) * 4;
+              const uint32_t col = kSfCol0 + (NC * kTilesK + 2 * j) * 4;
               tmem_copy_scales<2>(col, make_smem_desc(sfb, 16, 128, kSwizzleNone));
               if (two_blocks)
                 tmem_copy_scales<2>(col + 4, make_smem_desc(sfb + kSfBytes, 16, 128, kSwizzleNone));
@@ -334,41 +358,36 @@ __global__ void __launch_bounds__(threads_of(NC), 1) fp4_pair_kernel(const __gri
                 const uint32_t idesc =
                     FMT == kNvfp4 ? idesc0 : (idesc0 | (static_cast<uint32_t>(kk & 1) << 5) |
                                               (static_cast<uint32_t>(kk & 1) << 30));
-                const uint32_t sfb_col = sf_tmem + (NC * kTilesK + 2 * j) * 4 + shift;
+                const uint32_t sfb_col = kSfCol0 + (NC * kTilesK + 2 * j) * 4 + shift;
 #pragma unroll
                 for (int c = 0; c < NC; ++c) {
                   const uint64_t a_desc = make_smem_desc(st + c * kWBytes, 16, 1024, kSwizzle128B);
-                  const uint32_t d = tmem + static_cast<uint32_t>(NC == 1 ? acc : c) * kAccCols;
-                  mma_fp4<2, kVec>(d, a_desc + kk * 2, b_desc + kk * 2, idesc, sf_tmem + (c * kTilesK + j) * 4,
-                                   sfb_col, (kb | kk) != 0 ? 1u : 0u);
+                  mma_fp4<2, kVec>(static_cast<uint32_t>(NC == 1 ? acc : c) * kAccCols, a_desc + kk * 2, b_desc + kk * 2,
+                                   idesc, kSfCol0 + (c * kTilesK + j) * 4, sfb_col, (kb | kk) != 0 ? 1u : 0u);
                 }
               }
             }
             mma_commit_pair_mc(empty_bar(s), 0x3);
+            if (kb + 1 == p.num_k_blocks) {
+              mma_commit_pair_mc(acc_full(NC == 1 ? acc : 0), 0x3);
+              if (NC == 2) mma_commit_pair_mc(acc_full(1), 0x3);
+            }
           }
           __syncwarp();
-          sf_buf ^= 1u;
-          if (++s == S) {
-            s = 0;
-            ph ^= 1u;
+          ready = __all_sync(0xffffffffu, ask);
+          if (++kb == p.num_k_blocks) {
+            kb = 0;
+            u += stride;
+            more = u < total;
+            if constexpr (NC == 1) {
+              acc ^= 1;
+              if (acc == 0) acc_ph ^= 1u;
+            } else {
+              acc_ph ^= 1u;
+            }
           }
         }
-        if (aborted) break;
-        if (elect_one()) {
-          if constexpr (NC == 1) {
-            mma_commit_pair_mc(acc_full(acc), 0x3);
-          } else {
-            mma_commit_pair_mc(acc_full(0), 0x3);
-            mma_commit_pair_mc(acc_full(1), 0x3);
-          }
-        }
-        __syncwarp();
-        if constexpr (NC == 1) {
-          acc ^= 1;
-          if (acc == 0) acc_ph ^= 1u;
-        } else {
-          acc_ph ^= 1u;
-        }
+        ph ^= 1u;
       }
     }
     __syncwarp();
@@ -486,8 +505,9 @@ __global__ void fp4_swiglu_kernel(const float* __restrict__ x, const int* __rest
 }
 
 template <int NC>
-int pair_smem(int stages, int G) {
-  return 1024 + stages * static_cast<int>(Layout<NC>::kStage) + 8 * (2 * stages + 4) + 16 + 4 * (3 * G + 2);
+int pair_smem(int G) {
+  constexpr int S = stages_of(NC);
+  return 1024 + S * static_cast<int>(Layout<NC>::kStage) + 8 * (2 * S + 4) + 16 + 4 * (3 * G + 2);
 }
 
 using PairKernel = void (*)(Fp4GemmParams);
@@ -632,8 +652,7 @@ bwg_status run_fp4_gemm(const Fp4Operand& a, const Fp4Operand& b, void* D, int M
   p.swiglu_up = n_out;
   p.out_dtype = out_dtype;
   p.group_m = 8;
-  p.stages = nc == 2 ? 4 : 6;
-  const int smem = nc == 2 ? pair_smem<2>(p.stages, G) : pair_smem<1>(p.stages, G);
+  const int smem = nc == 2 ? pair_smem<2>(G) : pair_smem<1>(G);
   if (smem > rt.max_smem) return BWG_ERR_UNSUPPORTED;
   const PairKernel k = pick_pair(nc, format, swiglu);
   int clusters = 0;
