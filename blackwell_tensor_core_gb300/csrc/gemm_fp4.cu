@@ -159,6 +159,50 @@ __device__ __forceinline__ Tile tile_at(const Fp4GemmParams& p, const Tables& t,
   return r;
 }
 
+// The tiles of one cluster, u = first, first + stride, .., looked up 32 at a
+// time, a lane each: the divisions and the group search of a tile switch
+// then cost a warp once in 32 tiles.
+template <int W_ROWS>
+struct TileWindow {
+  const Fp4GemmParams& p;
+  const Tables& tb;
+  int first, stride, count;
+  int base;  // tile of lane 0, -1 before the first
+  Tile mine;
+
+  __device__ TileWindow(const Fp4GemmParams& p_, const Tables& tb_, int first_, int stride_, int total)
+      : p(p_), tb(tb_), first(first_), stride(stride_), base(-32) {
+    count = first < total ? (total - first + stride - 1) / stride : 0;
+  }
+  __device__ bool have(int i) const { return i < count; }
+  __device__ void seek(int i) {
+    if (i - base < 32) return;
+    base = i;
+    const int at = i + static_cast<int>(threadIdx.x & 31u);
+    mine = tile_at<W_ROWS>(p, tb, first + (at < count ? at : i) * stride);
+  }
+  __device__ Tile at(int i) {
+    seek(i);
+    Tile t;
+    t.g = __shfl_sync(0xffffffffu, mine.g, i - base);
+    t.w0 = __shfl_sync(0xffffffffu, mine.w0, i - base);
+    t.t0 = __shfl_sync(0xffffffffu, mine.t0, i - base);
+    t.tokens = __shfl_sync(0xffffffffu, mine.tokens, i - base);
+    t.srow = __shfl_sync(0xffffffffu, mine.srow, i - base);
+    t.n = (t.tokens + 15) & ~15;
+    return t;
+  }
+  // N and the column shift of the activation scales (n << 2 | shift), as a
+  // value the compiler knows to be the same in every lane.
+  __device__ uint32_t mma_values(int i) {
+    seek(i);
+    const bool me = static_cast<int>(threadIdx.x & 31u) == i - base;
+    return __reduce_max_sync(0xffffffffu, me ? (static_cast<uint32_t>(mine.n) << 2) |
+                                                   (static_cast<uint32_t>(mine.srow & 127) / 32u)
+                                             : 0u);
+  }
+};
+
 __device__ __forceinline__ float silu_mul(float g, float u) { return g * rcp_approx(1.0f + __expf(-g)) * u; }
 
 // Warps 0, 2 and 3 load, warp 1 issues the MMAs, warps 4.. are the epilogue.
@@ -257,8 +301,9 @@ __global__ void __launch_bounds__(threads_of(NC), 1) fp4_pair_kernel(const __gri
     if (job == 2 || job < NC) {
       int s = 0;
       uint32_t ph = 0;
-      for (int u = first; u < total && !aborted; u += stride) {
-        const Tile tl = tile_at<kWRows>(p, tb, u);
+      TileWindow<kWRows> win(p, tb, first, stride, total);
+      for (int i = 0; win.have(i) && !aborted; ++i) {
+        const Tile tl = win.at(i);
         const int row = job == 2 ? tl.t0 + static_cast<int>(rank) * (tl.n / 2)
                                  : tl.w0 + static_cast<int>(rank) * 128 + job * (SW ? p.swiglu_up : 256);
         const int sf_row = job == 2 ? tl.srow / 128 : tl.g * p.w_blocks + row / 128;
@@ -293,116 +338,122 @@ __global__ void __launch_bounds__(threads_of(NC), 1) fp4_pair_kernel(const __gri
     __syncwarp();
   } else if (warp == 1) {
     // ---- MMA issuer (CTA 0 of the pair) ------------------------------------
-    // A stage is 16 or 24 tcgen05 instructions and their issue, not the
-    // tensor cores, can set the pace: the operands are kept uniform (the ring
-    // unrolled, tile values through a warp reduction, TMEM addresses constant:
-    // all 512 columns are allocated, so they start at 0), and a stage's full
-    // barrier is asked before the stage before it is issued.
-    if (rank == 0 && first < total) {
+    // A stage is 10 to 24 tcgen05 instructions, and their issue, not the
+    // tensor cores, can set the pace.  So the operands are kept uniform (the
+    // ring unrolled, tile values through a warp reduction, TMEM addresses
+    // constant: all 512 columns are allocated, so they start at 0; the
+    // operations predicated instead of issued in a branch), and a stage's
+    // full barrier is asked before the stage before it is issued.
+    if (rank == 0) {
+      int s = 0, acc = 0;
       uint32_t ph = 0, acc_ph = 0;
-      int acc = 0, u = first, kb = 0;
-      uint32_t shift = 0, idesc0 = 0;
-      bool two_blocks = false, ready = false, more = true;
-      while (more) {
-#pragma unroll
-        for (int s = 0; s < S; ++s) {
-          if (!more) break;
-          if (kb == 0) {
-            const Tile tl = tile_at<kWRows>(p, tb, u);
-            const uint32_t n = __reduce_max_sync(0xffffffffu, static_cast<uint32_t>(tl.n));
-            shift = __reduce_max_sync(0xffffffffu, static_cast<uint32_t>(tl.srow & 127)) / 32u;
-            two_blocks = shift * 32u + n > 128u;
-            idesc0 = make_idesc_fp4(FMT, 256, n, 0);
-            for (int a = 0; a < NC; ++a) {
-              const int slot = NC == 1 ? acc : a;
-              if (!warp_wait_all(acc_empty(slot), acc_ph ^ 1u, p.timeout_ns)) {
-                if (lane == 0) record_fault(p.err, kFaultTimeout, kRoleMma, kBarAccEmpty, slot, acc_ph ^ 1u);
-                aborted = true;
-              }
-            }
-            tc_fence_after();
-          }
-          if (!ready && !warp_wait_cta(full_bar(s), ph, p.timeout_ns)) {
-            if (lane == 0) record_fault(p.err, kFaultTimeout, kRoleMma, kBarFull, s, ph);
+      bool ready = false;
+      TileWindow<kWRows> win(p, tb, first, stride, total);
+      for (int i = 0; win.have(i) && !aborted; ++i) {
+        const uint32_t packed = win.mma_values(i);
+        const uint32_t shift = packed & 3u;
+        const uint32_t idesc0 = make_idesc_fp4(FMT, 256, packed >> 2, 0);
+        for (int a = 0; a < NC; ++a) {
+          const int slot = NC == 1 ? acc : a;
+          if (!warp_wait_all(acc_empty(slot), acc_ph ^ 1u, p.timeout_ns)) {
+            if (lane == 0) record_fault(p.err, kFaultTimeout, kRoleMma, kBarAccEmpty, slot, acc_ph ^ 1u);
             aborted = true;
           }
-          if (aborted) {
-            more = false;
-            break;
+        }
+        if (aborted) break;
+        tc_fence_after();
+        int kb = 0;
+        // one k-block, in stage st; returns false after the tile's last
+        auto k_block = [&](auto stage_c) {
+          constexpr int st = decltype(stage_c)::value;
+          if (!ready && !warp_wait_cta(full_bar(st), ph, p.timeout_ns)) {
+            if (lane == 0) record_fault(p.err, kFaultTimeout, kRoleMma, kBarFull, st, ph);
+            aborted = true;
+            return false;
           }
           tc_fence_after();
-          const bool ask = mbar_test_wait_cta(full_bar(s + 1 == S ? 0 : s + 1), s + 1 == S ? ph ^ 1u : ph);
-          if (elect_one()) {
-            const uint32_t st = base + static_cast<uint32_t>(s) * L::kStage;
-            const uint32_t sf = st + L::kStageW + kTokBytes;
-            const int steps = kb == p.num_k_blocks - 1 ? p.last_steps : 4;
-            // scales: block c's tile j to columns (c * kTilesK + j) * 4, the
-            // activations' two row blocks of tile j side by side
+          constexpr int next = st + 1 == S ? 0 : st + 1;
+          const bool ask = mbar_test_wait_cta(full_bar(next), next == 0 ? ph ^ 1u : ph);
+          const uint32_t mem = base + static_cast<uint32_t>(st) * L::kStage;
+          const uint32_t sf = mem + L::kStageW + kTokBytes;
+          const int steps = kb + 1 == p.num_k_blocks ? p.last_steps : 4;
+          const bool on = elect_one();
+          // scales: block c's tile j to columns (c * kTilesK + j) * 4, the
+          // activations' two row blocks of tile j side by side
 #pragma unroll
-            for (int j = 0; j < kTilesK; ++j) {
+          for (int j = 0; j < kTilesK; ++j) {
 #pragma unroll
-              for (int c = 0; c < NC; ++c)
-                tmem_copy_scales<2>(kSfCol0 + (c * kTilesK + j) * 4,
+            for (int c = 0; c < NC; ++c)
+              tmem_copy_scales_pair(on, kSfCol0 + (c * kTilesK + j) * 4,
                                     make_smem_desc(sf + c * L::kSfBlock + j * kScaleTileBytes, 16, 128, kSwizzleNone));
-              const uint32_t sfb = sf + NC * L::kSfBlock + j * kScaleTileBytes;
-              const uint32_t col = kSfCol0 + (NC * kTilesK + 2 * j) * 4;
-              tmem_copy_scales<2>(col, make_smem_desc(sfb, 16, 128, kSwizzleNone));
-              if (two_blocks)
-                tmem_copy_scales<2>(col + 4, make_smem_desc(sfb + kSfBytes, 16, 128, kSwizzleNone));
-            }
-            const uint64_t b_desc = make_smem_desc(st + L::kStageW, 16, 1024, kSwizzle128B);
+            const uint32_t sfb = sf + NC * L::kSfBlock + j * kScaleTileBytes;
+            constexpr uint32_t kSfb = kSfCol0 + NC * kTilesK * 4;
+            tmem_copy_scales_pair(on, kSfb + 8 * j, make_smem_desc(sfb, 16, 128, kSwizzleNone));
+            tmem_copy_scales_pair(on, kSfb + 8 * j + 4, make_smem_desc(sfb + kSfBytes, 16, 128, kSwizzleNone));
+          }
+          const uint64_t b_desc = make_smem_desc(mem + L::kStageW, 16, 1024, kSwizzle128B);
 #pragma unroll
-            for (int kk = 0; kk < 4; ++kk) {
-              if (kk < steps) {
-                const int j = FMT == kNvfp4 ? kk : kk / 2;
-                const uint32_t idesc =
-                    FMT == kNvfp4 ? idesc0 : (idesc0 | (static_cast<uint32_t>(kk & 1) << 5) |
-                                              (static_cast<uint32_t>(kk & 1) << 30));
-                const uint32_t sfb_col = kSfCol0 + (NC * kTilesK + 2 * j) * 4 + shift;
+          for (int kk = 0; kk < 4; ++kk) {
+            const int j = FMT == kNvfp4 ? kk : kk / 2;
+            const uint32_t idesc = FMT == kNvfp4 ? idesc0
+                                                 : (idesc0 | (static_cast<uint32_t>(kk & 1) << 5) |
+                                                    (static_cast<uint32_t>(kk & 1) << 30));
 #pragma unroll
-                for (int c = 0; c < NC; ++c) {
-                  const uint64_t a_desc = make_smem_desc(st + c * kWBytes, 16, 1024, kSwizzle128B);
-                  mma_fp4<2, kVec>(static_cast<uint32_t>(NC == 1 ? acc : c) * kAccCols, a_desc + kk * 2, b_desc + kk * 2,
-                                   idesc, kSfCol0 + (c * kTilesK + j) * 4, sfb_col, (kb | kk) != 0 ? 1u : 0u);
-                }
-              }
-            }
-            mma_commit_pair_mc(empty_bar(s), 0x3);
-            if (kb + 1 == p.num_k_blocks) {
-              mma_commit_pair_mc(acc_full(NC == 1 ? acc : 0), 0x3);
-              if (NC == 2) mma_commit_pair_mc(acc_full(1), 0x3);
+            for (int c = 0; c < NC; ++c) {
+              const uint64_t a_desc = make_smem_desc(mem + static_cast<uint32_t>(c) * kWBytes, 16, 1024, kSwizzle128B);
+              mma_fp4_pair<kVec>(on && kk < steps, static_cast<uint32_t>(NC == 1 ? acc : c) * kAccCols, a_desc + kk * 2,
+                                 b_desc + kk * 2, idesc, kSfCol0 + (c * kTilesK + j) * 4,
+                                 kSfCol0 + (NC * kTilesK + 2 * j) * 4 + shift, (kb | kk) != 0 ? 1u : 0u);
             }
           }
-          __syncwarp();
+          mma_commit_pair_mc_if(on, empty_bar(st), 0x3);
           ready = __all_sync(0xffffffffu, ask);
-          if (++kb == p.num_k_blocks) {
-            kb = 0;
-            u += stride;
-            more = u < total;
-            if constexpr (NC == 1) {
-              acc ^= 1;
-              if (acc == 0) acc_ph ^= 1u;
-            } else {
-              acc_ph ^= 1u;
-            }
+          s = next;
+          if (next == 0) ph ^= 1u;
+          return ++kb < p.num_k_blocks;
+        };
+        while (true) {
+          if (s == 0 && !k_block(std::integral_constant<int, 0>{})) break;
+          if (s == 1 && !k_block(std::integral_constant<int, 1>{})) break;
+          if (s == 2 && !k_block(std::integral_constant<int, 2>{})) break;
+          if (s == 3 && !k_block(std::integral_constant<int, 3>{})) break;
+          if constexpr (S > 4) {
+            if (s == 4 && !k_block(std::integral_constant<int, 4>{})) break;
+            if (s == 5 && !k_block(std::integral_constant<int, 5>{})) break;
           }
         }
-        ph ^= 1u;
+        if (aborted) break;
+        const bool on = elect_one();
+        mma_commit_pair_mc_if(on, acc_full(NC == 1 ? acc : 0), 0x3);
+        if (NC == 2) mma_commit_pair_mc_if(on, acc_full(1), 0x3);
+        if constexpr (NC == 1) {
+          acc ^= 1;
+          if (acc == 0) acc_ph ^= 1u;
+        } else {
+          acc_ph ^= 1u;
+        }
       }
     }
     __syncwarp();
   } else if (warp >= kEpi0) {
     // ---- epilogue: TMEM lane = output column, TMEM column = row of D --------
     const uint32_t q = warp & 3u;
-    const int grp = static_cast<int>((warp - kEpi0) >> 2);  // NC == 2: 0 or 1
+    const int grp = static_cast<int>((warp - 4u) >> 2);  // NC == 2: 0 or 1
     const uint32_t acc_empty0 = mapa_shared(acc_empty(0), 0);
     const float ga = p.a_global != nullptr ? __ldg(p.a_global) : 1.f;
     const bool out32 = p.out_dtype == kOutF32;
     const bool outbf = p.out_dtype == kOutBF16;
-    int acc = SW ? 0 : (NC == 1 ? 0 : grp);
+    const int elt = out32 ? 4 : 2;
+    const long long row_bytes = p.ldd * elt;
+    int acc = SW || NC == 1 ? 0 : grp;
     uint32_t acc_ph = 0;
-    for (int u = first; u < total; u += stride) {
-      const Tile tl = tile_at<kWRows>(p, tb, u);
+    TileWindow<kWRows> win(p, tb, first, stride, total);
+    for (int i = 0; win.have(i); ++i) {
+      const Tile tl = win.at(i);
+      const float alpha = p.b_global != nullptr ? ga * __ldg(p.b_global + (p.b_globals > 1 ? tl.g : 0)) : ga;
+      const uint32_t t_lane = tmem + ((q * 32u) << 16);
+      const int col = tl.w0 + (SW ? 0 : grp * 256) + static_cast<int>(rank * 128u + q * 32u + lane);
+      uint8_t* const dcol = static_cast<uint8_t*>(p.d) + (static_cast<long long>(tl.t0) * p.ldd + col) * elt;
       bool ok = warp_wait_all(acc_full(acc), acc_ph, p.timeout_ns);
       if (SW) ok = ok && warp_wait_all(acc_full(1), acc_ph, p.timeout_ns);
       if (!ok) {
@@ -411,10 +462,6 @@ __global__ void __launch_bounds__(threads_of(NC), 1) fp4_pair_kernel(const __gri
         break;
       }
       tc_fence_after();
-      const float alpha = p.b_global != nullptr ? ga * __ldg(p.b_global + (p.b_globals > 1 ? tl.g : 0)) : ga;
-      const uint32_t t_lane = tmem + ((q * 32u) << 16);
-      const int col = tl.w0 + (SW ? 0 : grp * 256) + static_cast<int>(rank * 128u + q * 32u + lane);
-      const bool col_ok = col < p.N;
       auto release = [&]() {
         tc_fence_before();
         __syncwarp();
@@ -423,41 +470,107 @@ __global__ void __launch_bounds__(threads_of(NC), 1) fp4_pair_kernel(const __gri
           if (SW) mbar_arrive_cluster_relaxed(acc_empty0 + 8u);
         }
       };
-      const int elt = out32 ? 4 : 2;
-      uint8_t* const dcol = static_cast<uint8_t*>(p.d) + (static_cast<long long>(tl.t0) * p.ldd + col) * elt;
-      const long long row_bytes = p.ldd * elt;
-      // SwiGLU: the two warpgroups take alternate chunks of 32 rows
-      const int c_first = SW ? grp * 32 : 0, c_step = SW ? 64 : 32;
-      if (c_first >= tl.tokens) release();
-      for (int c0 = c_first; c0 < tl.tokens; c0 += c_step) {
-        uint32_t v[32];
-        tmem_ld_32x32b_x32(t_lane + static_cast<uint32_t>(SW ? 0 : acc) * kAccCols + c0, v);
-        if constexpr (SW) {
-          uint32_t w[32];
-          tmem_ld_32x32b_x32(t_lane + kAccCols + c0, w);
-          tmem_wait_ld();
-          if (c0 + c_step >= tl.tokens) release();
+      auto pack = [&](float lo, float hi) { return outbf ? pack_bf16x2(lo, hi) : pack_f16x2(lo, hi); };
+      // stores rows c0 .. c0 + 31 of this lane's column, two packed a register
+      auto store16 = [&](int c0, const uint32_t* v) {
+        uint8_t* dst = dcol + c0 * row_bytes;
+        if (c0 + 32 <= tl.tokens) {
 #pragma unroll
-          for (int j = 0; j < 32; ++j)
-            v[j] = __float_as_uint(silu_mul(alpha * __uint_as_float(v[j]), alpha * __uint_as_float(w[j])));
+          for (int j = 0; j < 16; ++j) {
+            *reinterpret_cast<uint16_t*>(dst) = static_cast<uint16_t>(v[j]);
+            *reinterpret_cast<uint16_t*>(dst + row_bytes) = static_cast<uint16_t>(v[j] >> 16);
+            dst += 2 * row_bytes;
+          }
         } else {
-          tmem_wait_ld();
-          if (c0 + c_step >= tl.tokens) release();
 #pragma unroll
-          for (int j = 0; j < 32; ++j) v[j] = __float_as_uint(alpha * __uint_as_float(v[j]));
+          for (int j = 0; j < 16; ++j) {
+            if (c0 + 2 * j < tl.tokens) *reinterpret_cast<uint16_t*>(dst) = static_cast<uint16_t>(v[j]);
+            if (c0 + 2 * j + 1 < tl.tokens) *reinterpret_cast<uint16_t*>(dst + row_bytes) = static_cast<uint16_t>(v[j] >> 16);
+            dst += 2 * row_bytes;
+          }
         }
-        if (col_ok) {
-          uint8_t* dst = dcol + c0 * row_bytes;
+      };
+      const uint32_t t_acc = t_lane + static_cast<uint32_t>(SW ? 0 : acc) * kAccCols;
+      if (!out32 && NC == 2) {
+        // The whole slice is read, packed to 16 bits and the accumulator
+        // handed back before the first store.
+        if constexpr (SW) {
+          // the two warpgroups take alternate chunks of 32 rows
+          uint32_t pk[3][16];
 #pragma unroll
-          for (int j = 0; j < 32; ++j) {
-            if (c0 + j < tl.tokens) {
-              const float x = __uint_as_float(v[j]);
-              if (out32)
-                *reinterpret_cast<float*>(dst) = x;
-              else
-                *reinterpret_cast<uint16_t*>(dst) = outbf ? cvt_rn_bf16(x) : cvt_rn_f16(x);
+          for (int i = 0; i < 3; ++i) {
+            const int c0 = grp * 32 + i * 64;
+            if (c0 < tl.tokens) {
+              uint32_t g[32], w[32];
+              tmem_ld_32x32b_x32(t_acc + c0, g);
+              tmem_ld_32x32b_x32(t_acc + kAccCols + c0, w);
+              tmem_wait_ld();
+#pragma unroll
+              for (int j = 0; j < 16; ++j)
+                pk[i][j] = pack(silu_mul(alpha * __uint_as_float(g[2 * j]), alpha * __uint_as_float(w[2 * j])),
+                                silu_mul(alpha * __uint_as_float(g[2 * j + 1]), alpha * __uint_as_float(w[2 * j + 1])));
             }
-            dst += row_bytes;
+          }
+          release();
+          if (col < p.N) {
+#pragma unroll
+            for (int i = 0; i < 3; ++i)
+              if (grp * 32 + i * 64 < tl.tokens) store16(grp * 32 + i * 64, pk[i]);
+          }
+        } else {
+          uint32_t pk[6][16];
+#pragma unroll
+          for (int i = 0; i < 6; ++i) {
+            if (32 * i < tl.tokens) {
+              uint32_t v[32];
+              tmem_ld_32x32b_x32(t_acc + 32 * i, v);
+              tmem_wait_ld();
+#pragma unroll
+              for (int j = 0; j < 16; ++j)
+                pk[i][j] = pack(alpha * __uint_as_float(v[2 * j]), alpha * __uint_as_float(v[2 * j + 1]));
+            }
+          }
+          release();
+          if (col < p.N) {
+#pragma unroll
+            for (int i = 0; i < 6; ++i)
+              if (32 * i < tl.tokens) store16(32 * i, pk[i]);
+          }
+        }
+      } else {
+        const int c_first = SW ? grp * 32 : 0, c_step = SW ? 64 : 32;
+        if (c_first >= tl.tokens) release();
+        for (int c0 = c_first; c0 < tl.tokens; c0 += c_step) {
+          uint32_t v[32];
+          tmem_ld_32x32b_x32(t_acc + c0, v);
+          if constexpr (SW) {
+            uint32_t w[32];
+            tmem_ld_32x32b_x32(t_acc + kAccCols + c0, w);
+            tmem_wait_ld();
+            if (c0 + c_step >= tl.tokens) release();
+#pragma unroll
+            for (int j = 0; j < 32; ++j)
+              v[j] = __float_as_uint(silu_mul(alpha * __uint_as_float(v[j]), alpha * __uint_as_float(w[j])));
+          } else {
+            tmem_wait_ld();
+            if (c0 + c_step >= tl.tokens) release();
+#pragma unroll
+            for (int j = 0; j < 32; ++j) v[j] = __float_as_uint(alpha * __uint_as_float(v[j]));
+          }
+          if (col < p.N) {
+            if (out32) {
+              uint8_t* dst = dcol + c0 * row_bytes;
+#pragma unroll
+              for (int j = 0; j < 32; ++j) {
+                if (c0 + j < tl.tokens) *reinterpret_cast<uint32_t*>(dst) = v[j];
+                dst += row_bytes;
+              }
+            } else {
+              uint32_t pk[16];
+#pragma unroll
+              for (int j = 0; j < 16; ++j) pk[j] = pack(__uint_as_float(v[2 * j]), __uint_as_float(v[2 * j + 1]));
+              store16(c0, pk);
+            }
           }
         }
       }
