@@ -7,7 +7,7 @@
 // The kernel computes D^T: 128 weight rows per CTA are the M of an
 // instruction and the activations' rows its N, which may be any multiple of
 // 16 up to 192.  So a ragged end of a group costs what it has rows, not a
-// 256-row tile.  A CTA pair (cta_group::2) takes NC x 256 weight rows x 192
+// 256-row tile.  A CTA pair (cta_group::2) takes 256 output columns x 192
 // activation rows; each CTA stages its own weight rows and half of the
 // activation rows.
 //
@@ -18,7 +18,6 @@
 // of its N from the TMEM column of that row's group of 32.
 #include <algorithm>
 #include <cstdint>
-#include <cstdlib>
 #include <cstring>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -211,6 +210,10 @@ constexpr int threads_of(int nc) { return nc == 1 ? 256 : 384; }
 // addresses are constants.
 constexpr int stages_of(int nc) { return nc == 1 ? 6 : 4; }
 
+// SwiGLU: registers per thread after set-up, out of 168 x 384 at launch.
+constexpr uint32_t kRegsControlSw = 56, kRegsEpilogueSw = 224;
+static_assert(kRegsControlSw * 128 + kRegsEpilogueSw * 256 <= 168 * 384, "the register split must fit");
+
 // Shared memory: stage s holds [NC weight blocks][activation rows][scales].
 template <int NC>
 struct Layout {
@@ -222,20 +225,22 @@ struct Layout {
   static_assert(kStage % 1024 == 0, "swizzled tiles start on 1024 bytes");
 };
 
-// NC weight blocks of 128 rows per CTA.  NC == 1: two accumulators, so that
-// the epilogue of a tile runs beside the MMAs of the next.  NC == 2: one
-// accumulator per block; fewer bytes staged per instruction.  SW: the blocks
-// are the gate and the up rows of the same 256 output columns.
-template <int NC, int FMT, bool SW>
-__global__ void __launch_bounds__(threads_of(NC), 1) fp4_pair_kernel(const __grid_constant__ Fp4GemmParams p) {
-  static_assert(!SW || NC == 2, "SwiGLU pairs a gate block with an up block");
+// A tile is 256 output columns (128 a CTA) x up to 192 rows.  Plain: one block
+// of weight rows a CTA and two accumulators, so that the epilogue of a tile
+// runs beside the MMAs of the next.  SW: the gate and the up rows of the same
+// columns, one accumulator each.  (Two blocks a CTA for the plain product too,
+// which stages a quarter fewer bytes per instruction, took 165 us against 160
+// for 8192^3: its one accumulator per block leaves the tensor cores idle at
+// each tile's end.)
+template <int FMT, bool SW>
+__global__ void __launch_bounds__(threads_of(SW ? 2 : 1), 1) fp4_pair_kernel(const __grid_constant__ Fp4GemmParams p) {
+  constexpr int NC = SW ? 2 : 1;
   using L = Layout<NC>;
   constexpr int kVec = FMT == kNvfp4 ? 16 : 32;
   constexpr int kTilesK = FMT == kNvfp4 ? 4 : 2;     // scale tiles of a stage along K
   constexpr uint32_t kSfBytes = kTilesK * kScaleTileBytes;
   constexpr uint32_t kStageTx = 2u * (L::kStageW + kTokBytes + (NC + 2) * kSfBytes);
-  constexpr int kWRows = SW ? 256 : 256 * NC;        // output columns of a tile
-  constexpr uint32_t kEpi0 = 4u;
+  constexpr int kWRows = 256;                        // output columns of a tile
   constexpr uint32_t kAccCols = kTok;
   constexpr uint32_t kSfCol0 = 2 * kTok;             // scales start after the two accumulators
   constexpr uint32_t kSfCols = (NC + 2) * kTilesK * 4;  // TMEM columns of one stage's scales
@@ -284,13 +289,15 @@ __global__ void __launch_bounds__(threads_of(NC), 1) fp4_pair_kernel(const __gri
   tc_fence_before();
   cluster_sync_all();
   tc_fence_after();
-  const uint32_t tmem = ld_shared_u32(tmem_slot);
   const int first = static_cast<int>(cluster_id_x());
   const int stride = static_cast<int>(num_clusters_x());
   const int total = tb.prefix[p.G];
   bool aborted = false;
 
-  if (warp < 4 && warp != 1) {
+  if (warp < 4) {
+    // the epilogue warpgroups hold both accumulators' slices
+    if constexpr (SW) setmaxnreg_dec<kRegsControlSw>();
+    if (warp != 1) {
     // ---- TMA producers --------------------------------------------------------
     // One warp for each weight block and one for the activations (NC == 1: the
     // third has none).  A stage takes 6 loads; one diverged thread issuing
@@ -305,7 +312,7 @@ __global__ void __launch_bounds__(threads_of(NC), 1) fp4_pair_kernel(const __gri
       for (int i = 0; win.have(i) && !aborted; ++i) {
         const Tile tl = win.at(i);
         const int row = job == 2 ? tl.t0 + static_cast<int>(rank) * (tl.n / 2)
-                                 : tl.w0 + static_cast<int>(rank) * 128 + job * (SW ? p.swiglu_up : 256);
+                                 : tl.w0 + static_cast<int>(rank) * 128 + job * p.swiglu_up;
         const int sf_row = job == 2 ? tl.srow / 128 : tl.g * p.w_blocks + row / 128;
         for (int kb = 0; kb < p.num_k_blocks; ++kb) {
           if (!warp_wait_cta(empty_bar(s), ph ^ 1u, p.timeout_ns)) {
@@ -335,8 +342,7 @@ __global__ void __launch_bounds__(threads_of(NC), 1) fp4_pair_kernel(const __gri
         }
       }
     }
-    __syncwarp();
-  } else if (warp == 1) {
+    } else {
     // ---- MMA issuer (CTA 0 of the pair) ------------------------------------
     // A stage is 10 to 24 tcgen05 instructions, and their issue, not the
     // tensor cores, can set the pace.  So the operands are kept uniform (the
@@ -374,7 +380,8 @@ __global__ void __launch_bounds__(threads_of(NC), 1) fp4_pair_kernel(const __gri
           tc_fence_after();
           constexpr int next = st + 1 == S ? 0 : st + 1;
           const bool ask = mbar_test_wait_cta(full_bar(next), next == 0 ? ph ^ 1u : ph);
-          const uint32_t mem = base + static_cast<uint32_t>(st) * L::kStage;
+          uint32_t mem = base + static_cast<uint32_t>(st) * L::kStage;
+          asm volatile("" : "+r"(mem));
           const uint32_t sf = mem + L::kStageW + kTokBytes;
           const int steps = kb + 1 == p.num_k_blocks ? p.last_steps : 4;
           const bool on = elect_one();
@@ -434,151 +441,119 @@ __global__ void __launch_bounds__(threads_of(NC), 1) fp4_pair_kernel(const __gri
         }
       }
     }
+    }
     __syncwarp();
-  } else if (warp >= kEpi0) {
+  } else {
+    if constexpr (SW) setmaxnreg_inc<kRegsEpilogueSw>();
     // ---- epilogue: TMEM lane = output column, TMEM column = row of D --------
     const uint32_t q = warp & 3u;
-    const int grp = static_cast<int>((warp - 4u) >> 2);  // NC == 2: 0 or 1
+    const int grp = static_cast<int>((warp - 4u) >> 2);  // SwiGLU: warpgroup 0 or 1
     const uint32_t acc_empty0 = mapa_shared(acc_empty(0), 0);
     const float ga = p.a_global != nullptr ? __ldg(p.a_global) : 1.f;
     const bool out32 = p.out_dtype == kOutF32;
     const bool outbf = p.out_dtype == kOutBF16;
-    const int elt = out32 ? 4 : 2;
-    const long long row_bytes = p.ldd * elt;
-    int acc = SW || NC == 1 ? 0 : grp;
-    uint32_t acc_ph = 0;
-    TileWindow<kWRows> win(p, tb, first, stride, total);
-    for (int i = 0; win.have(i); ++i) {
-      const Tile tl = win.at(i);
-      const float alpha = p.b_global != nullptr ? ga * __ldg(p.b_global + (p.b_globals > 1 ? tl.g : 0)) : ga;
-      const uint32_t t_lane = tmem + ((q * 32u) << 16);
-      const int col = tl.w0 + (SW ? 0 : grp * 256) + static_cast<int>(rank * 128u + q * 32u + lane);
-      uint8_t* const dcol = static_cast<uint8_t*>(p.d) + (static_cast<long long>(tl.t0) * p.ldd + col) * elt;
-      bool ok = warp_wait_all(acc_full(acc), acc_ph, p.timeout_ns);
-      if (SW) ok = ok && warp_wait_all(acc_full(1), acc_ph, p.timeout_ns);
-      if (!ok) {
-        if (lane == 0) record_fault(p.err, kFaultTimeout, kRoleEpilogue, kBarAccFull, acc, acc_ph);
-        aborted = true;
-        break;
+    const uint32_t t_lane = (q * 32u) << 16;
+    auto wait_acc_full = [&](int slot, uint32_t phase) {
+      if (warp_wait_all(acc_full(slot), phase, p.timeout_ns)) return true;
+      if (lane == 0) record_fault(p.err, kFaultTimeout, kRoleEpilogue, kBarAccFull, slot, phase);
+      return false;
+    };
+    auto release = [&](int slot) {
+      if (lane == 0) mbar_arrive_cluster_relaxed(acc_empty0 + 8u * slot);
+    };
+    auto alpha_of = [&](int g) {
+      return p.b_global != nullptr ? ga * __ldg(p.b_global + (p.b_globals > 1 ? g : 0)) : ga;
+    };
+    // values of rows c0 .. c0 + 31 of the tile, this lane's column: 32 lanes
+    // write 32 adjacent columns of one row at a time
+    auto store = [&](const Tile& tl, int c0, const uint32_t (&v)[32]) {
+      const int rows = tl.tokens - c0;
+      const int col = tl.w0 + static_cast<int>(rank * 128u + q * 32u + lane);
+      if (col >= p.N || rows <= 0) return;
+      const int elt = out32 ? 4 : 2;
+      const long long row_bytes = p.ldd * elt;
+      uint8_t* dst = static_cast<uint8_t*>(p.d) + (static_cast<long long>(tl.t0 + c0) * p.ldd + col) * elt;
+      if (out32) {
+#pragma unroll
+        for (int j = 0; j < 32; ++j) {
+          if (j < rows) *reinterpret_cast<uint32_t*>(dst) = v[j];
+          dst += row_bytes;
+        }
+        return;
       }
-      tc_fence_after();
-      auto release = [&]() {
+#pragma unroll
+      for (int j = 0; j < 32; j += 2) {
+        const float lo = __uint_as_float(v[j]), hi = __uint_as_float(v[j + 1]);
+        const uint32_t pk = outbf ? pack_bf16x2(lo, hi) : pack_f16x2(lo, hi);
+        if (j < rows) *reinterpret_cast<uint16_t*>(dst) = static_cast<uint16_t>(pk);
+        if (j + 1 < rows) *reinterpret_cast<uint16_t*>(dst + row_bytes) = static_cast<uint16_t>(pk >> 16);
+        dst += 2 * row_bytes;
+      }
+    };
+    TileWindow<kWRows> win(p, tb, first, stride, total);
+    if constexpr (SW) {
+      // The two warpgroups take alternate chunks of 32 rows, three each.  All
+      // of a warp's gate and up values (192 registers) are read and both
+      // accumulators handed back before the first silu: its exponentials
+      // would hold the accumulators for about 2000 clocks longer.
+      uint32_t acc_ph = 0;
+      for (int i = 0; win.have(i); ++i) {
+        if (!wait_acc_full(0, acc_ph) || !wait_acc_full(1, acc_ph)) {
+          aborted = true;
+          break;
+        }
+        acc_ph ^= 1u;
+        tc_fence_after();
+        const uint32_t col0 = t_lane + static_cast<uint32_t>(grp) * 32u;
+        uint32_t gate[3][32], up[3][32];
+#pragma unroll
+        for (int c = 0; c < 3; ++c) {
+          // columns past the tile's rows lie inside the accumulators
+          tmem_ld_32x32b_x32(col0 + c * 64, gate[c]);
+          tmem_ld_32x32b_x32(col0 + kAccCols + c * 64, up[c]);
+        }
+        tmem_wait_ld();
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) {
-          mbar_arrive_cluster_relaxed(acc_empty0 + 8u * acc);
-          if (SW) mbar_arrive_cluster_relaxed(acc_empty0 + 8u);
-        }
-      };
-      auto pack = [&](float lo, float hi) { return outbf ? pack_bf16x2(lo, hi) : pack_f16x2(lo, hi); };
-      // stores rows c0 .. c0 + 31 of this lane's column, two packed a register
-      auto store16 = [&](int c0, const uint32_t* v) {
-        uint8_t* dst = dcol + c0 * row_bytes;
-        if (c0 + 32 <= tl.tokens) {
+        release(0);
+        release(1);
+        const Tile tl = win.at(i);
+        const float alpha = alpha_of(tl.g);
 #pragma unroll
-          for (int j = 0; j < 16; ++j) {
-            *reinterpret_cast<uint16_t*>(dst) = static_cast<uint16_t>(v[j]);
-            *reinterpret_cast<uint16_t*>(dst + row_bytes) = static_cast<uint16_t>(v[j] >> 16);
-            dst += 2 * row_bytes;
-          }
-        } else {
+        for (int c = 0; c < 3; ++c) {
 #pragma unroll
-          for (int j = 0; j < 16; ++j) {
-            if (c0 + 2 * j < tl.tokens) *reinterpret_cast<uint16_t*>(dst) = static_cast<uint16_t>(v[j]);
-            if (c0 + 2 * j + 1 < tl.tokens) *reinterpret_cast<uint16_t*>(dst + row_bytes) = static_cast<uint16_t>(v[j] >> 16);
-            dst += 2 * row_bytes;
-          }
-        }
-      };
-      const uint32_t t_acc = t_lane + static_cast<uint32_t>(SW ? 0 : acc) * kAccCols;
-      if (!out32 && NC == 2) {
-        // The whole slice is read, packed to 16 bits and the accumulator
-        // handed back before the first store.
-        if constexpr (SW) {
-          // the two warpgroups take alternate chunks of 32 rows
-          uint32_t pk[3][16];
-#pragma unroll
-          for (int i = 0; i < 3; ++i) {
-            const int c0 = grp * 32 + i * 64;
-            if (c0 < tl.tokens) {
-              uint32_t g[32], w[32];
-              tmem_ld_32x32b_x32(t_acc + c0, g);
-              tmem_ld_32x32b_x32(t_acc + kAccCols + c0, w);
-              tmem_wait_ld();
-#pragma unroll
-              for (int j = 0; j < 16; ++j)
-                pk[i][j] = pack(silu_mul(alpha * __uint_as_float(g[2 * j]), alpha * __uint_as_float(w[2 * j])),
-                                silu_mul(alpha * __uint_as_float(g[2 * j + 1]), alpha * __uint_as_float(w[2 * j + 1])));
-            }
-          }
-          release();
-          if (col < p.N) {
-#pragma unroll
-            for (int i = 0; i < 3; ++i)
-              if (grp * 32 + i * 64 < tl.tokens) store16(grp * 32 + i * 64, pk[i]);
-          }
-        } else {
-          uint32_t pk[6][16];
-#pragma unroll
-          for (int i = 0; i < 6; ++i) {
-            if (32 * i < tl.tokens) {
-              uint32_t v[32];
-              tmem_ld_32x32b_x32(t_acc + 32 * i, v);
-              tmem_wait_ld();
-#pragma unroll
-              for (int j = 0; j < 16; ++j)
-                pk[i][j] = pack(alpha * __uint_as_float(v[2 * j]), alpha * __uint_as_float(v[2 * j + 1]));
-            }
-          }
-          release();
-          if (col < p.N) {
-#pragma unroll
-            for (int i = 0; i < 6; ++i)
-              if (32 * i < tl.tokens) store16(32 * i, pk[i]);
-          }
-        }
-      } else {
-        const int c_first = SW ? grp * 32 : 0, c_step = SW ? 64 : 32;
-        if (c_first >= tl.tokens) release();
-        for (int c0 = c_first; c0 < tl.tokens; c0 += c_step) {
-          uint32_t v[32];
-          tmem_ld_32x32b_x32(t_acc + c0, v);
-          if constexpr (SW) {
-            uint32_t w[32];
-            tmem_ld_32x32b_x32(t_acc + kAccCols + c0, w);
-            tmem_wait_ld();
-            if (c0 + c_step >= tl.tokens) release();
-#pragma unroll
-            for (int j = 0; j < 32; ++j)
-              v[j] = __float_as_uint(silu_mul(alpha * __uint_as_float(v[j]), alpha * __uint_as_float(w[j])));
-          } else {
-            tmem_wait_ld();
-            if (c0 + c_step >= tl.tokens) release();
-#pragma unroll
-            for (int j = 0; j < 32; ++j) v[j] = __float_as_uint(alpha * __uint_as_float(v[j]));
-          }
-          if (col < p.N) {
-            if (out32) {
-              uint8_t* dst = dcol + c0 * row_bytes;
-#pragma unroll
-              for (int j = 0; j < 32; ++j) {
-                if (c0 + j < tl.tokens) *reinterpret_cast<uint32_t*>(dst) = v[j];
-                dst += row_bytes;
-              }
-            } else {
-              uint32_t pk[16];
-#pragma unroll
-              for (int j = 0; j < 16; ++j) pk[j] = pack(__uint_as_float(v[2 * j]), __uint_as_float(v[2 * j + 1]));
-              store16(c0, pk);
-            }
-          }
+          for (int j = 0; j < 32; ++j)
+            gate[c][j] =
+                __float_as_uint(silu_mul(alpha * __uint_as_float(gate[c][j]), alpha * __uint_as_float(up[c][j])));
+          store(tl, grp * 32 + c * 64, gate[c]);
         }
       }
-      if constexpr (NC == 1) {
+    } else {
+      int acc = 0;
+      uint32_t acc_ph = 0;
+      for (int i = 0; win.have(i); ++i) {
+        const Tile tl = win.at(i);
+        const float alpha = alpha_of(tl.g);
+        if (!wait_acc_full(acc, acc_ph)) {
+          aborted = true;
+          break;
+        }
+        tc_fence_after();
+        for (int c0 = 0; c0 < tl.tokens; c0 += 32) {
+          uint32_t v[32];
+          tmem_ld_32x32b_x32(t_lane + static_cast<uint32_t>(acc) * kAccCols + c0, v);
+          tmem_wait_ld();
+          if (c0 + 32 >= tl.tokens) {
+            tc_fence_before();
+            __syncwarp();
+            release(acc);
+          }
+#pragma unroll
+          for (int j = 0; j < 32; ++j) v[j] = __float_as_uint(alpha * __uint_as_float(v[j]));
+          store(tl, c0, v);
+        }
         acc ^= 1;
         if (acc == 0) acc_ph ^= 1u;
-      } else {
-        acc_ph ^= 1u;
       }
     }
     __syncwarp();
@@ -594,7 +569,7 @@ __global__ void __launch_bounds__(threads_of(NC), 1) fp4_pair_kernel(const __gri
   cluster_sync_all();
   if (warp == 1) {
     tc_fence_after();
-    tmem_dealloc<2>(tmem, kTmemCols);
+    tmem_dealloc<2>(0, kTmemCols);
   }
 }
 
@@ -625,10 +600,9 @@ int pair_smem(int G) {
 
 using PairKernel = void (*)(Fp4GemmParams);
 
-PairKernel pick_pair(int nc, int format, bool sw) {
-  if (sw) return format == kNvfp4 ? fp4_pair_kernel<2, kNvfp4, true> : fp4_pair_kernel<2, kMxfp4, true>;
-  if (nc == 2) return format == kNvfp4 ? fp4_pair_kernel<2, kNvfp4, false> : fp4_pair_kernel<2, kMxfp4, false>;
-  return format == kNvfp4 ? fp4_pair_kernel<1, kNvfp4, false> : fp4_pair_kernel<1, kMxfp4, false>;
+PairKernel pick_pair(int format, bool sw) {
+  if (sw) return format == kNvfp4 ? fp4_pair_kernel<kNvfp4, true> : fp4_pair_kernel<kMxfp4, true>;
+  return format == kNvfp4 ? fp4_pair_kernel<kNvfp4, false> : fp4_pair_kernel<kMxfp4, false>;
 }
 
 // Co-resident pairs of a kernel at the largest shared memory, and its
@@ -642,7 +616,7 @@ bwg_status pair_clusters(PairKernel k, int nc, const Runtime& rt, int* clusters)
   static struct {
     Key key;
     int clusters;
-  } seen[64 * 6];
+  } seen[64 * 4];
   static int n_seen = 0;
   std::lock_guard<std::mutex> lock(mu);
   for (int i = 0; i < n_seen; ++i)
@@ -666,6 +640,15 @@ bwg_status pair_clusters(PairKernel k, int nc, const Runtime& rt, int* clusters)
   attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
+  cudaFuncAttributes fa;
+  if (cudaFuncGetAttributes(&fa, fn) != cudaSuccess) {
+    cudaGetLastError();
+    return BWG_ERR_CUDA;
+  }
+  // the SwiGLU kernel's register split only completes if the CTA was launched
+  // with at least the registers that it hands out
+  if (nc == 2 && static_cast<uint32_t>(fa.numRegs) * threads_of(2) < kRegsControlSw * 128u + kRegsEpilogueSw * 256u)
+    return BWG_ERR_UNSUPPORTED;
   int n = 0;
   if (cudaOccupancyMaxActiveClusters(&n, fn, &cfg) != cudaSuccess || n <= 0) {
     cudaGetLastError();
@@ -736,14 +719,8 @@ bwg_status run_fp4_gemm(const Fp4Operand& a, const Fp4Operand& b, void* D, int M
   if (K == 0) return runtime_status(launch_zero_fill(D, M, n_out, ldd, out_dtype == BWG_OUT_FP32 ? 4 : 2, stream));
   Fp4GemmParams p;
   std::memset(&p, 0, sizeof(p));
-  // Two weight blocks a CTA unless that leaves pairs without a tile.
-  // BWG_FP4_NC overrides.
+  const int nc = swiglu ? 2 : 1;
   const long long tok_tiles = (M + kTok - 1LL) / kTok + (offsets != nullptr ? G : 0);
-  const char* nc_env = std::getenv("BWG_FP4_NC");
-  const int nc = swiglu                                               ? 2
-                 : nc_env != nullptr && (*nc_env == '1' || *nc_env == '2') ? *nc_env - '0'
-                 : tok_tiles * ((n_out + 511) / 512) < rt.sm_count / 2 ? 1
-                                                                      : 2;
   p.w_blocks = pad128(N) / 128;
   const int a_rows = offsets != nullptr ? static_cast<int>((M + 127LL * std::min(G, M)) / 128) : pad128(M) / 128;
   if (!fp4_maps(&p, a, b, M, N, K, format, G, a_rows)) return BWG_ERR_CUDA;
@@ -760,14 +737,13 @@ bwg_status run_fp4_gemm(const Fp4Operand& a, const Fp4Operand& b, void* D, int M
   p.G = G;
   p.num_k_blocks = (K + kKCols - 1) / kKCols;
   p.last_steps = (K - (p.num_k_blocks - 1) * kKCols + 63) / 64;
-  const int w_rows = swiglu ? 256 : 256 * nc;
-  p.num_w_tiles = (n_out + w_rows - 1) / w_rows;
+  p.num_w_tiles = (n_out + 255) / 256;
   p.swiglu_up = n_out;
   p.out_dtype = out_dtype;
   p.group_m = 8;
   const int smem = nc == 2 ? pair_smem<2>(G) : pair_smem<1>(G);
   if (smem > rt.max_smem) return BWG_ERR_UNSUPPORTED;
-  const PairKernel k = pick_pair(nc, format, swiglu);
+  const PairKernel k = pick_pair(format, swiglu);
   int clusters = 0;
   if ((st = pair_clusters(k, nc, rt, &clusters)) != BWG_OK) return st;
   // every group adds at most one partial tile of rows

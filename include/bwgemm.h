@@ -424,7 +424,6 @@ void bwg_debug_set_trace(void* buffer);
  *                      evict-last (default 2; 0 with the cluster split)
  *   BWG_GROUPED_1C     1: grouped kernels with one MMA consumer (256-row units)
  *   BWG_GROUPED_SWAP   1: swapped-operand group ends (one-consumer grouped kernel)
- *   BWG_FP4_NC         1 / 2: 4-bit products with 256 / 512 weight rows a CTA pair
  *   BWG_B_ONE_BOX      0: dense pair kernels load a CTA's B stage as two
  *                      64-column boxes (default: one load where N % 64 == 0
  *                      or B is [N, K])

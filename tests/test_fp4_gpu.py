@@ -224,9 +224,7 @@ DENSE = [(1, 8, 32), (1, 128, 64), (16, 128, 256), (17, 200, 96), (64, 256, 512)
 
 @pytest.mark.parametrize("fmt", FMTS)
 @pytest.mark.parametrize("M,N,K", DENSE)
-@pytest.mark.parametrize("nc", ["", "1", "2"])
-def test_gemm_integers_are_exact(ops, M, N, K, fmt, nc, monkeypatch):
-    monkeypatch.setenv("BWG_FP4_NC", nc)
+def test_gemm_integers_are_exact(ops, M, N, K, fmt):
     rng = np.random.default_rng(M + N + K)
     a, A = random_fp4(ops, M, K, fmt, rng, integers=True)
     b, B = random_fp4(ops, N, K, fmt, rng, integers=True)
