@@ -436,21 +436,26 @@ def moe_sort(expert_ids: torch.Tensor, num_experts: int, stream=None) -> Routing
 
 def _routing(r: Routing, dev) -> tuple[int, int, int]:
     """(T, k, E) of a routing whose tensors the kernels can read on `dev`."""
-    offsets, position = r.offsets, r.position
-    for name, t in (("offsets", offsets), ("position", position)):
-        if t.dtype != torch.int32 or not t.is_contiguous() or t.device != dev:
-            raise ValueError("routing.%s must be a dense int32 tensor on %s" % (name, dev))
-    if position.dim() != 2 or offsets.dim() != 1 or offsets.shape[0] < 2 or position.shape[1] < 1:
+    offsets, _, position = r
+    if not (position.dtype is torch.int32 and offsets.dtype is torch.int32 and position.is_contiguous()
+            and offsets.is_contiguous() and position.device == dev and offsets.device == dev):
+        raise ValueError("routing must hold dense int32 tensors on %s" % dev)
+    ps, os_ = position.shape, offsets.shape
+    if len(ps) != 2 or len(os_) != 1 or os_[0] < 2 or ps[1] < 1:
         raise ValueError("routing must hold offsets [E + 1] and position [T, k]")
-    return position.shape[0], position.shape[1], offsets.shape[0] - 1
+    return ps[0], ps[1], os_[0] - 1
 
 
 def _rows(t: torch.Tensor, name: str, rows: int) -> int:
     """Leading dimension of a row matrix with `rows` rows."""
     if t.dtype not in _OUT_CODES:
         raise TypeError("%s must be bfloat16, float16 or float32" % name)
-    ld = _matrix(t, name)
+    if t.dim() != 2 or not t.is_cuda:
+        raise ValueError("%s must be a 2-D CUDA tensor" % name)
     have, cols = t.shape
+    ld, unit = t.stride()
+    if unit != 1:
+        raise ValueError("%s must be row-major with unit column stride" % name)
     if have != rows:
         raise ValueError("%s must have %d rows, got %d" % (name, rows, have))
     if ld >= cols:
@@ -464,13 +469,13 @@ def _out_rows(out, rows: int, cols: int, dtype, dev, name: str = "out") -> tuple
     """(output matrix, leading dimension): a new one, or the caller's checked."""
     if out is None:
         return torch.empty((rows, cols), dtype=dtype, device=dev), cols
-    if tuple(out.shape) != (rows, cols) or out.dtype != dtype or out.device != dev:
+    if out.shape != (rows, cols) or out.dtype is not dtype or out.device != dev:
         raise ValueError("%s must be a [%d, %d] %s tensor on %s" % (name, rows, cols, dtype, dev))
     return out, _rows(out, name, rows)
 
 
 def _pair_weights(w: torch.Tensor, T: int, k: int, dev) -> None:
-    if w.dtype != torch.float32 or tuple(w.shape) != (T, k) or not w.is_contiguous() or w.device != dev:
+    if w.dtype is not torch.float32 or w.shape != (T, k) or not w.is_contiguous() or w.device != dev:
         raise ValueError("weights must be a dense float32 tensor [%d, %d] on %s" % (T, k, dev))
 
 
