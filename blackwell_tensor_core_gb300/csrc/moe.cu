@@ -54,8 +54,12 @@ __device__ __forceinline__ void record_bad_position(unsigned long long* err) {
 // pair order.
 // What bounds it: latency.  The ids are 0.3 MB for the 4096 x 8 layer; one
 // launch with its counts on chip replaces three passes through global memory.
+// 32768 ids of 32 experts: 10.6 us, against 11.6 with a loop over the
+// warps' counts and over the CTAs' totals in their place (one shared-memory or
+// distributed load after the other).
 constexpr int kSortMaxWarps = 32;
-constexpr int kSortAhead = 4;  // id loads in flight per lane
+constexpr int kSortAhead = 4;    // id loads in flight per lane
+constexpr int kSortCtas = 8;     // of the cluster
 
 template <class ID>
 __global__ void __launch_bounds__(kSortMaxWarps * 32)
@@ -64,22 +68,20 @@ __global__ void __launch_bounds__(kSortMaxWarps * 32)
   extern __shared__ int sm[];
   const int W = static_cast<int>(blockDim.x >> 5);
   const int buckets = E + 1;         // bucket E: pairs without an expert
-  int* hist = sm;                    // [W][buckets]
-  int* total = sm + W * buckets;     // [buckets] this CTA's counts
+  const int pitch = buckets | 1;     // odd: the lanes of a column read different banks
+  int* hist = sm;                    // [W][pitch]
+  int* total = sm + W * pitch;       // [buckets] this CTA's counts
   int* start = total + buckets;      // [buckets] this CTA's first row in each bucket
-  int* part = start + buckets;       // [32] scan partials, [32] = rows with an expert
+  int* part = start + buckets;       // [32] scan partials
   const int lane = static_cast<int>(threadIdx.x & 31u);
   const int warp = static_cast<int>(threadIdx.x >> 5);
   const uint32_t rank = n_cta > 1 ? cluster_ctarank() : 0u;
-
-  for (int i = static_cast<int>(threadIdx.x); i < W * buckets; i += static_cast<int>(blockDim.x)) hist[i] = 0;
-  __syncthreads();
 
   const long long runs = static_cast<long long>(n_cta) * W;
   const long long per = ((pairs + runs - 1) / runs + 31) / 32 * 32;
   const long long first = (static_cast<long long>(rank) * W + warp) * per;
   const long long last = first + per < pairs ? first + per : pairs;
-  int* mine = hist + warp * buckets;
+  int* mine = hist + warp * pitch;
   const unsigned below = (1u << lane) - 1u;
 
   auto load = [&](long long p) -> int {
@@ -87,10 +89,16 @@ __global__ void __launch_bounds__(kSortMaxWarps * 32)
     const ID v = ids[p];
     return v >= 0 && v < static_cast<ID>(E) ? static_cast<int>(v) : E;
   };
-  for (long long p0 = first; p0 < last; p0 += 32 * kSortAhead) {
-    int key[kSortAhead];
+  int key[kSortAhead];
 #pragma unroll
-    for (int a = 0; a < kSortAhead; ++a) key[a] = load(p0 + 32 * a + lane);
+  for (int a = 0; a < kSortAhead; ++a) key[a] = load(first + 32 * a + lane);
+  for (int b = lane; b < buckets; b += 32) mine[b] = 0;
+  __syncwarp();
+  for (long long p0 = first; p0 < last; p0 += 32 * kSortAhead) {
+    if (p0 != first) {
+#pragma unroll
+      for (int a = 0; a < kSortAhead; ++a) key[a] = load(p0 + 32 * a + lane);
+    }
 #pragma unroll
     for (int a = 0; a < kSortAhead; ++a) {
       const unsigned same = __match_any_sync(0xffffffffu, key[a]);
@@ -99,31 +107,40 @@ __global__ void __launch_bounds__(kSortMaxWarps * 32)
     }
   }
   __syncthreads();
-  // warps' counts -> each warp's start inside the CTA's share of the bucket
-  for (int b = static_cast<int>(threadIdx.x); b < buckets; b += static_cast<int>(blockDim.x)) {
-    int run = 0;
-    for (int w = 0; w < W; ++w) {
-      const int c = hist[w * buckets + b];
-      hist[w * buckets + b] = run;
-      run += c;
+  // warps' counts -> each warp's start inside the CTA's share of the bucket:
+  // a warp a bucket, a lane a row of counts
+  for (int b = warp; b < buckets; b += W) {
+    const int c = lane < W ? hist[lane * pitch + b] : 0;
+    int incl = c;
+    for (int d = 1; d < 32; d <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, incl, d);
+      if (lane >= d) incl += y;
     }
-    total[b] = run;
+    if (lane < W) hist[lane * pitch + b] = incl - c;
+    if (lane == 31) total[b] = incl;
   }
   if (n_cta > 1)
     cluster_sync_all();
   else
     __syncthreads();
   // every CTA: all CTAs' counts, the part of lower ranks, and the exclusive
-  // sum over experts, blockDim.x experts at a time
+  // sum over buckets, blockDim.x buckets at a time
   int carry = 0;
-  for (int b0 = 0; b0 < E; b0 += static_cast<int>(blockDim.x)) {
+  for (int b0 = 0; b0 < buckets; b0 += static_cast<int>(blockDim.x)) {
     const int b = b0 + static_cast<int>(threadIdx.x);
     int all = 0, before = 0;
-    if (b < E) {
-      for (int c = 0; c < n_cta; ++c) {
-        const int v = n_cta > 1 ? ld_cluster(total + b, static_cast<uint32_t>(c)) : total[b];
-        if (c < static_cast<int>(rank)) before += v;
-        all += v;
+    if (b < buckets) {
+      if (n_cta > 1) {
+        int v[kSortCtas];
+#pragma unroll
+        for (int c = 0; c < kSortCtas; ++c) v[c] = ld_cluster(total + b, static_cast<uint32_t>(c));
+#pragma unroll
+        for (int c = 0; c < kSortCtas; ++c) {
+          if (c < static_cast<int>(rank)) before += v[c];
+          all += v[c];
+        }
+      } else {
+        all = total[b];
       }
     }
     int incl = all;
@@ -143,24 +160,18 @@ __global__ void __launch_bounds__(kSortMaxWarps * 32)
     }
     __syncthreads();
     const int excl = carry + (warp > 0 ? part[warp - 1] : 0) + incl - all;
-    if (b < E) {
+    if (b < buckets) {
       start[b] = excl + before;
-      if (rank == 0) offsets[b] = excl;
+      if (rank == 0) offsets[b] = excl;  // for bucket E: the rows that have an expert
     }
     carry += part[31];
     __syncthreads();
   }
-  if (threadIdx.x == 0) {
-    int before = 0;
-    for (int c = 0; c < static_cast<int>(rank); ++c) before += ld_cluster(total + E, static_cast<uint32_t>(c));
-    start[E] = carry + before;
-    if (rank == 0) offsets[E] = carry;
-  }
-  __syncthreads();
   for (long long p0 = first; p0 < last; p0 += 32 * kSortAhead) {
-    int key[kSortAhead];
+    if (per > 32 * kSortAhead) {  // else the keys are still there
 #pragma unroll
-    for (int a = 0; a < kSortAhead; ++a) key[a] = load(p0 + 32 * a + lane);
+      for (int a = 0; a < kSortAhead; ++a) key[a] = load(p0 + 32 * a + lane);
+    }
 #pragma unroll
     for (int a = 0; a < kSortAhead; ++a) {
       const unsigned same = __match_any_sync(0xffffffffu, key[a]);
@@ -203,10 +214,6 @@ struct Raw<16> {
   using type = uint4;
 };
 template <>
-struct Raw<8> {
-  using type = uint2;
-};
-template <>
 struct Raw<4> {
   using type = uint32_t;
 };
@@ -228,8 +235,6 @@ __device__ __forceinline__ float to_f32(__half v) { return __half2float(v); }
 __device__ __forceinline__ void from_f32(float& d, float v) { d = v; }
 __device__ __forceinline__ void from_f32(__nv_bfloat16& d, float v) { d = __float2bfloat16_rn(v); }
 __device__ __forceinline__ void from_f32(__half& d, float v) { d = __float2half_rn(v); }
-
-constexpr int kPairsAhead = 8;  // pairs of a token handled together
 
 // Block (t, chunk): a vector of token t per thread, stored to its k rows.
 template <int VB>
@@ -254,124 +259,167 @@ __global__ void moe_dispatch_kernel(const __grid_constant__ MoeRows p, int chunk
   }
 }
 
-// Block (t, chunk): a vector of y[t] per thread, from its k rows.
-template <class T, int VB>
-__global__ void moe_combine_kernel(const __grid_constant__ MoeRows p, int chunks) {
-  using R = typename Raw<VB>::type;
-  constexpr int N = VB / static_cast<int>(sizeof(T));
-  const int t = static_cast<int>(blockIdx.x / static_cast<unsigned>(chunks));
-  const int v = static_cast<int>(blockIdx.x % static_cast<unsigned>(chunks)) * static_cast<int>(blockDim.x) +
-                static_cast<int>(threadIdx.x);
-  if (v >= p.vecs) return;
-  const int kept = min(*p.kept, p.pairs);
-  const long long p0 = static_cast<long long>(t) * p.k;
-  float acc[N];
-#pragma unroll
-  for (int i = 0; i < N; ++i) acc[i] = 0.f;
-  for (int j0 = 0; j0 < p.k; j0 += kPairsAhead) {
-    Vec<T, VB> x[kPairsAhead];
-    float w[kPairsAhead];
-    bool has[kPairsAhead];
-#pragma unroll
-    for (int a = 0; a < kPairsAhead; ++a) {
-      const int j = j0 + a;
-      const int r = j < p.k ? p.position[p0 + j] : kept;
-      if (static_cast<unsigned>(r) > static_cast<unsigned>(p.pairs) && threadIdx.x == 0) record_bad_position(p.err);
-      has[a] = r >= 0 && r < kept;
-      if (has[a]) {
-        x[a].raw = reinterpret_cast<const R*>(static_cast<const T*>(p.src) + r * p.ld_src)[v];
-        w[a] = p.weights != nullptr ? p.weights[p0 + j] : 1.f;
-      }
-    }
-#pragma unroll
-    for (int a = 0; a < kPairsAhead; ++a)
-      if (has[a]) {
-#pragma unroll
-        for (int i = 0; i < N; ++i) acc[i] = fmaf(w[a], to_f32(x[a].e[i]), acc[i]);
-      }
-  }
-  Vec<T, VB> y;
-#pragma unroll
-  for (int i = 0; i < N; ++i) from_f32(y.e[i], acc[i]);
-  reinterpret_cast<R*>(static_cast<T*>(p.dst) + t * p.ld_dst)[v] = y.raw;
+// Loads in flight decide how near these two kernels come to the memory's rate,
+// so a thread takes P pairs (k rounded up to 1, 2, 4 or 8; more in turns) of V
+// vectors and issues all P * V loads before it uses the first.  Measured for
+// 4096 tokens x 8 experts, H = 4096 BF16: the combine 46.9 us (6.4 TB/s) with 8
+// loads of 16 bytes a thread and 128 threads a block, 60 with 16 loads, 47.7
+// with 256 threads; the gradient 87.2 us (6.5 TB/s) with 16 loads, 90.7 with 8,
+// 92.3 with 256 threads.  Narrower vectors: 32 loads for the combine (2049 x 8
+// rows of 2047 FP32: 26 us, 30 with 16), 16 for the gradient (51.4, 52.2 with
+// 32).  Checks of the positions between the loads cost the combine 15 us.
+constexpr int kRowThreads = 128;
+template <int VB, int P, bool GRAD>
+constexpr int vectors_of() {
+  return (GRAD ? 16 : VB == 16 ? 8 : 32) / P;
 }
 
-constexpr int kGradThreads = 256;
-
-// Block t: d_rows of token t's k rows and the k inner products, the row kept
-// in no more than one vector per thread and pair at a time.
-template <class T, int VB>
-__global__ void __launch_bounds__(kGradThreads) moe_combine_grad_kernel(const __grid_constant__ MoeRows p) {
+// Block (t, chunk): V vectors of y[t] per thread, blockDim.x apart, from its k rows.
+template <class T, int VB, int P>
+__global__ void __launch_bounds__(kRowThreads) moe_combine_kernel(const __grid_constant__ MoeRows p, int chunks) {
   using R = typename Raw<VB>::type;
   constexpr int N = VB / static_cast<int>(sizeof(T));
-  __shared__ float sums[kGradThreads / 32][kPairsAhead];
+  constexpr int V = vectors_of<VB, P, false>();
+  const int t = static_cast<int>(blockIdx.x / static_cast<unsigned>(chunks));
+  const int step = static_cast<int>(blockDim.x);
+  const int v0 = static_cast<int>(blockIdx.x % static_cast<unsigned>(chunks)) * step * V + static_cast<int>(threadIdx.x);
+  const int kept = min(*p.kept, p.pairs);
+  const long long p0 = static_cast<long long>(t) * p.k;
+  float acc[V][N];
+#pragma unroll
+  for (int m = 0; m < V; ++m)
+#pragma unroll
+    for (int i = 0; i < N; ++i) acc[m][i] = 0.f;
+  for (int j0 = 0; j0 < p.k; j0 += P) {
+    Vec<T, VB> x[P][V];
+    float w[P];
+    int row[P];
+    bool has[P], bad = false;
+    // all positions and weights, then all rows: nothing between the loads
+#pragma unroll
+    for (int a = 0; a < P; ++a) {
+      row[a] = j0 + a < p.k ? p.position[p0 + j0 + a] : kept;
+      w[a] = p.weights != nullptr && j0 + a < p.k ? p.weights[p0 + j0 + a] : 1.f;
+    }
+#pragma unroll
+    for (int a = 0; a < P; ++a) {
+      bad |= static_cast<unsigned>(row[a]) > static_cast<unsigned>(p.pairs);
+      has[a] = row[a] >= 0 && row[a] < kept;
+      const R* src = reinterpret_cast<const R*>(static_cast<const T*>(p.src) + (has[a] ? row[a] : 0) * p.ld_src);
+#pragma unroll
+      for (int m = 0; m < V; ++m)
+        if (has[a] && v0 + m * step < p.vecs) x[a][m].raw = __ldg(src + v0 + m * step);
+    }
+    if (bad && threadIdx.x == 0) record_bad_position(p.err);
+#pragma unroll
+    for (int a = 0; a < P; ++a)
+      if (has[a]) {
+#pragma unroll
+        for (int m = 0; m < V; ++m)
+#pragma unroll
+          for (int i = 0; i < N; ++i) acc[m][i] = fmaf(w[a], to_f32(x[a][m].e[i]), acc[m][i]);
+      }
+  }
+  R* dst = reinterpret_cast<R*>(static_cast<T*>(p.dst) + t * p.ld_dst);
+#pragma unroll
+  for (int m = 0; m < V; ++m) {
+    if (v0 + m * step < p.vecs) {
+      Vec<T, VB> y;
+#pragma unroll
+      for (int i = 0; i < N; ++i) from_f32(y.e[i], acc[m][i]);
+      dst[v0 + m * step] = y.raw;
+    }
+  }
+}
+
+// Block t: d_rows of token t's k rows and the k inner products.
+template <class T, int VB, int P>
+__global__ void __launch_bounds__(kRowThreads) moe_combine_grad_kernel(const __grid_constant__ MoeRows p) {
+  using R = typename Raw<VB>::type;
+  constexpr int N = VB / static_cast<int>(sizeof(T));
+  constexpr int V = vectors_of<VB, P, true>();
+  __shared__ float sums[kRowThreads / 32][P];
   const int t = static_cast<int>(blockIdx.x);
+  const int step = static_cast<int>(blockDim.x);
   const int kept = min(*p.kept, p.pairs);
   const long long p0 = static_cast<long long>(t) * p.k;
   const R* dy = reinterpret_cast<const R*>(static_cast<const T*>(p.src) + t * p.ld_src);
-  for (int j0 = 0; j0 < p.k; j0 += kPairsAhead) {
-    int row[kPairsAhead];
-    float w[kPairsAhead], dot[kPairsAhead];
+  for (int j0 = 0; j0 < p.k; j0 += P) {
+    int row[P];
+    float w[P], dot[P];
+    bool bad = false;
 #pragma unroll
-    for (int a = 0; a < kPairsAhead; ++a) {
+    for (int a = 0; a < P; ++a) {
       const bool in = j0 + a < p.k;
       row[a] = in ? p.position[p0 + j0 + a] : -1;
-      if (in && static_cast<unsigned>(row[a]) >= static_cast<unsigned>(p.pairs)) {
-        if (threadIdx.x == 0) record_bad_position(p.err);
+      w[a] = in ? p.weights[p0 + j0 + a] : 0.f;
+    }
+#pragma unroll
+    for (int a = 0; a < P; ++a) {
+      if (static_cast<unsigned>(row[a]) >= static_cast<unsigned>(p.pairs)) {
+        bad |= j0 + a < p.k;
         row[a] = -1;
       }
-      w[a] = row[a] >= 0 && row[a] < kept ? p.weights[p0 + j0 + a] : 0.f;
       dot[a] = 0.f;
     }
-    for (int v = static_cast<int>(threadIdx.x); v < p.vecs; v += kGradThreads) {
-      Vec<T, VB> g;
-      g.raw = dy[v];
-      Vec<T, VB> x[kPairsAhead];
+    if (bad && threadIdx.x == 0) record_bad_position(p.err);
+    for (int v = static_cast<int>(threadIdx.x); v < p.vecs; v += step * V) {
+      Vec<T, VB> g[V], x[P][V];
 #pragma unroll
-      for (int a = 0; a < kPairsAhead; ++a)
-        if (row[a] >= 0 && row[a] < kept)
-          x[a].raw = reinterpret_cast<const R*>(static_cast<const T*>(p.rows_in) + row[a] * p.ld_rows)[v];
+      for (int m = 0; m < V; ++m)
+        if (v + m * step < p.vecs) g[m].raw = __ldg(dy + v + m * step);
 #pragma unroll
-      for (int a = 0; a < kPairsAhead; ++a) {
-        if (row[a] < 0) continue;
-        Vec<T, VB> d;
-        if (row[a] < kept) {
+      for (int a = 0; a < P; ++a)
+        if (row[a] >= 0 && row[a] < kept) {
+          const R* src = reinterpret_cast<const R*>(static_cast<const T*>(p.rows_in) + row[a] * p.ld_rows);
 #pragma unroll
-          for (int i = 0; i < N; ++i) {
-            dot[a] = fmaf(to_f32(x[a].e[i]), to_f32(g.e[i]), dot[a]);
-            from_f32(d.e[i], w[a] * to_f32(g.e[i]));
-          }
-        } else {
-          d.raw = R{};
+          for (int m = 0; m < V; ++m)
+            if (v + m * step < p.vecs) x[a][m].raw = __ldg(src + v + m * step);
         }
-        reinterpret_cast<R*>(static_cast<T*>(p.dst) + row[a] * p.ld_dst)[v] = d.raw;
+#pragma unroll
+      for (int a = 0; a < P; ++a) {
+        if (row[a] < 0) continue;
+        R* dst = reinterpret_cast<R*>(static_cast<T*>(p.dst) + row[a] * p.ld_dst);
+#pragma unroll
+        for (int m = 0; m < V; ++m) {
+          if (v + m * step >= p.vecs) continue;
+          Vec<T, VB> d;
+          if (row[a] < kept) {
+#pragma unroll
+            for (int i = 0; i < N; ++i) {
+              dot[a] = fmaf(to_f32(x[a][m].e[i]), to_f32(g[m].e[i]), dot[a]);
+              from_f32(d.e[i], w[a] * to_f32(g[m].e[i]));
+            }
+          } else {
+            d.raw = R{};
+          }
+          dst[v + m * step] = d.raw;
+        }
       }
     }
 #pragma unroll
-    for (int a = 0; a < kPairsAhead; ++a) {
+    for (int a = 0; a < P; ++a) {
       for (int d = 16; d > 0; d >>= 1) dot[a] += __shfl_xor_sync(0xffffffffu, dot[a], d);
       if ((threadIdx.x & 31u) == 0) sums[threadIdx.x >> 5][a] = dot[a];
     }
     __syncthreads();
     const int a = static_cast<int>(threadIdx.x);
-    if (a < kPairsAhead && j0 + a < p.k) {
-      float s = 0.f;
-      for (int w2 = 0; w2 < kGradThreads / 32; ++w2) s += sums[w2][a];
-      p.d_weights[p0 + j0 + a] = s;
+    if (a < P && j0 + a < p.k) {
+      float total = 0.f;
+      for (int w2 = 0; w2 < step / 32; ++w2) total += sums[w2][a];
+      p.d_weights[p0 + j0 + a] = total;
     }
     __syncthreads();
   }
 }
 
-// Widest vector (16, 8, 4 or 2 bytes, at least an element) in which every
+// Widest vector (16, 4 or 2 bytes, at least an element) in which every
 // row of H elements can be read and written whole.
 int vector_bytes(int H, int elt, std::initializer_list<const void*> ptrs, std::initializer_list<long long> lds) {
   uintptr_t bits = static_cast<uintptr_t>(static_cast<long long>(H) * elt);
   for (const void* q : ptrs) bits |= reinterpret_cast<uintptr_t>(q);
   for (long long ld : lds) bits |= static_cast<uintptr_t>(ld * elt);
-  for (int vb = 16; vb > elt; vb >>= 1)
-    if ((bits & static_cast<uintptr_t>(vb - 1)) == 0) return vb;
-  return elt;
+  return (bits & 15u) == 0 ? 16 : (bits & 3u) == 0 ? 4 : elt;
 }
 
 int elt_bytes(int dtype) { return dtype == BWG_OUT_FP32 ? 4 : 2; }
@@ -393,35 +441,57 @@ bwg_status check_rows(int dtype, int T, int H, int k, int E, const int* position
   return BWG_OK;
 }
 
-// Threads of a row block and blocks a row: enough threads for one vector each.
-void row_shape(int vecs, int* threads, int* chunks) {
-  *threads = vecs >= 256 ? 256 : (vecs + 31) / 32 * 32;
-  *chunks = (vecs + *threads - 1) / *threads;
+// Threads of a row block (at most `most`, whole warps) and blocks a row, for
+// `per` vectors a thread, the row shared out evenly.
+void row_shape(int vecs, int per, int most, int* threads, int* chunks) {
+  *chunks = std::max(1, (vecs + most * per - 1) / (most * per));
+  const int each = (vecs + *chunks * per - 1) / (*chunks * per);
+  *threads = std::max(32, (each + 31) / 32 * 32);
 }
 
-template <class T>
-cudaError_t launch_combine(const MoeRows& p, int vb, unsigned blocks, int threads, int chunks, cudaStream_t s) {
-  switch (vb) {
-    case 16: moe_combine_kernel<T, 16><<<blocks, threads, 0, s>>>(p, chunks); break;
-    case 8: moe_combine_kernel<T, 8><<<blocks, threads, 0, s>>>(p, chunks); break;
-    case 4: moe_combine_kernel<T, 4><<<blocks, threads, 0, s>>>(p, chunks); break;
-    default:
-      if constexpr (sizeof(T) == 2) moe_combine_kernel<T, 2><<<blocks, threads, 0, s>>>(p, chunks);
-  }
+template <class T, int VB, int P>
+cudaError_t launch_combine_as(const MoeRows& p, cudaStream_t s) {
+  int threads, chunks;
+  row_shape(p.vecs, vectors_of<VB, P, false>(), kRowThreads, &threads, &chunks);
+  const long long blocks = static_cast<long long>(p.T) * chunks;
+  if (blocks > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
+  moe_combine_kernel<T, VB, P><<<static_cast<unsigned>(blocks), threads, 0, s>>>(p, chunks);
   return cudaGetLastError();
 }
 
-template <class T>
-cudaError_t launch_combine_grad(const MoeRows& p, int vb, cudaStream_t s) {
-  const unsigned blocks = static_cast<unsigned>(p.T);
-  switch (vb) {
-    case 16: moe_combine_grad_kernel<T, 16><<<blocks, kGradThreads, 0, s>>>(p); break;
-    case 8: moe_combine_grad_kernel<T, 8><<<blocks, kGradThreads, 0, s>>>(p); break;
-    case 4: moe_combine_grad_kernel<T, 4><<<blocks, kGradThreads, 0, s>>>(p); break;
-    default:
-      if constexpr (sizeof(T) == 2) moe_combine_grad_kernel<T, 2><<<blocks, kGradThreads, 0, s>>>(p);
-  }
+template <class T, int VB, int P>
+cudaError_t launch_grad_as(const MoeRows& p, cudaStream_t s) {
+  int threads, chunks;
+  row_shape(p.vecs, vectors_of<VB, P, true>(), kRowThreads, &threads, &chunks);
+  moe_combine_grad_kernel<T, VB, P><<<static_cast<unsigned>(p.T), threads, 0, s>>>(p);
   return cudaGetLastError();
+}
+
+template <class T, int VB>
+cudaError_t launch_pairs(bool grad, const MoeRows& p, cudaStream_t s) {
+  if (grad)
+    return p.k > 4   ? launch_grad_as<T, VB, 8>(p, s)
+           : p.k > 2 ? launch_grad_as<T, VB, 4>(p, s)
+           : p.k > 1 ? launch_grad_as<T, VB, 2>(p, s)
+                     : launch_grad_as<T, VB, 1>(p, s);
+  return p.k > 4   ? launch_combine_as<T, VB, 8>(p, s)
+         : p.k > 2 ? launch_combine_as<T, VB, 4>(p, s)
+         : p.k > 1 ? launch_combine_as<T, VB, 2>(p, s)
+                   : launch_combine_as<T, VB, 1>(p, s);
+}
+
+template <class T>
+cudaError_t launch_vectors(bool grad, const MoeRows& p, int vb, cudaStream_t s) {
+  if (vb == 16) return launch_pairs<T, 16>(grad, p, s);
+  if (vb == 4) return launch_pairs<T, 4>(grad, p, s);
+  if constexpr (sizeof(T) == 2) return launch_pairs<T, 2>(grad, p, s);
+  return cudaErrorInvalidValue;
+}
+
+cudaError_t launch_weighted(bool grad, const MoeRows& p, int dtype, int vb, cudaStream_t s) {
+  return dtype == BWG_OUT_FP32   ? launch_vectors<float>(grad, p, vb, s)
+         : dtype == BWG_OUT_BF16 ? launch_vectors<__nv_bfloat16>(grad, p, vb, s)
+                                 : launch_vectors<__half>(grad, p, vb, s);
 }
 
 bwg_status run_combine(const void* rows, int dtype, int T, int H, int ldr, int k, const float* weights,
@@ -448,24 +518,16 @@ bwg_status run_combine(const void* rows, int dtype, int T, int H, int ldr, int k
   p.pairs = T * k;
   p.err = rt.err;
   p.vecs = static_cast<int>(static_cast<long long>(H) * elt / vb);
-  int threads, chunks;
-  row_shape(p.vecs, &threads, &chunks);
-  const long long blocks = static_cast<long long>(T) * chunks;
-  if (blocks > 0x7fffffffLL) return BWG_ERR_UNSUPPORTED;
-  const unsigned b = static_cast<unsigned>(blocks);
-  const cudaError_t e = dtype == BWG_OUT_FP32   ? launch_combine<float>(p, vb, b, threads, chunks, s)
-                        : dtype == BWG_OUT_BF16 ? launch_combine<__nv_bfloat16>(p, vb, b, threads, chunks, s)
-                                                : launch_combine<__half>(p, vb, b, threads, chunks, s);
-  return runtime_status(e);
+  return runtime_status(launch_weighted(false, p, dtype, vb, s));
 }
 
 template <class ID>
 cudaError_t launch_sort(const void* ids, int pairs, int E, int* offsets, int* order, int* position, cudaStream_t s) {
   // One CTA up to 4096 pairs, a warp for each 128 of them; a cluster of 8
   // beyond, whose 256 warps then have at least 16 pairs each.
-  const int n_cta = pairs <= 4096 ? 1 : 8;
+  const int n_cta = pairs <= 4096 ? 1 : kSortCtas;
   const int warps = n_cta > 1 ? kSortMaxWarps : std::min(kSortMaxWarps, std::max(4, (pairs + 127) / 128));
-  const size_t smem = (static_cast<size_t>(warps + 2) * (E + 1) + 33) * sizeof(int);
+  const size_t smem = (static_cast<size_t>(warps) * ((E + 1) | 1) + 2 * (E + 1) + 32) * sizeof(int);
   if (smem > 48 * 1024) {
     const cudaError_t a = cudaFuncSetAttribute(moe_sort_kernel<ID>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                                static_cast<int>(smem));
@@ -532,14 +594,13 @@ bwg_status moe_dispatch(const void* X, int dtype, int T, int H, int ldx, int k, 
   p.err = rt.err;
   p.vecs = static_cast<int>(static_cast<long long>(H) * elt / vb);
   int threads, chunks;
-  row_shape(p.vecs, &threads, &chunks);
+  row_shape(p.vecs, 1, 256, &threads, &chunks);
   const long long blocks = static_cast<long long>(T) * chunks;
   if (blocks > 0x7fffffffLL) return BWG_ERR_UNSUPPORTED;
   const unsigned b = static_cast<unsigned>(blocks);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   switch (vb) {
     case 16: moe_dispatch_kernel<16><<<b, threads, 0, s>>>(p, chunks, elt); break;
-    case 8: moe_dispatch_kernel<8><<<b, threads, 0, s>>>(p, chunks, elt); break;
     case 4: moe_dispatch_kernel<4><<<b, threads, 0, s>>>(p, chunks, elt); break;
     default: moe_dispatch_kernel<2><<<b, threads, 0, s>>>(p, chunks, elt); break;
   }
@@ -591,10 +652,7 @@ bwg_status moe_combine_grad(const void* dY, const void* rows, int dtype, int T, 
   p.err = rt.err;
   p.vecs = static_cast<int>(static_cast<long long>(H) * elt / vb);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  const cudaError_t e = dtype == BWG_OUT_FP32   ? launch_combine_grad<float>(p, vb, s)
-                        : dtype == BWG_OUT_BF16 ? launch_combine_grad<__nv_bfloat16>(p, vb, s)
-                                                : launch_combine_grad<__half>(p, vb, s);
-  return runtime_status(e);
+  return runtime_status(launch_weighted(true, p, dtype, vb, s));
 }
 
 }  // extern "C"

@@ -157,6 +157,15 @@ def test_combine_grad_against_its_formula(ops, T, k, E, H, how, dtype):
     assert bool((err <= (H + 16) * 2.0 ** -24 * prod.abs().sum(2) * kept).all())
 
 
+def test_no_columns(ops):
+    r = ops.moe_sort(make_ids(5, 3, 4, 2), 4)
+    w = torch.rand(5, 3, device="cuda")
+    x, rows = torch.empty(5, 0, device="cuda"), torch.empty(15, 0, device="cuda")
+    assert ops.moe_dispatch(x, r).shape == (15, 0) and ops.moe_combine(rows, r, w).shape == (5, 0)
+    d_rows, d_w = ops.moe_combine_grad(x, rows, r, w)
+    assert d_rows.shape == (15, 0) and bool((d_w == 0).all())
+
+
 def test_gradients_against_differences(ops):
     """The combine is linear in rows and in weights, so central differences of
     it with steps of powers of two carry only its FP32 rounding."""
