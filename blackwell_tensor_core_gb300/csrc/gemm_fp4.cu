@@ -391,12 +391,12 @@ __global__ void __launch_bounds__(threads_of(SW ? 2 : 1), 1) fp4_pair_kernel(con
           for (int j = 0; j < kTilesK; ++j) {
 #pragma unroll
             for (int c = 0; c < NC; ++c)
-              tmem_copy_scales_pair(on, kSfCol0 + (c * kTilesK + j) * 4,
+              tmem_copy_scales_if<2>(on, kSfCol0 + (c * kTilesK + j) * 4,
                                     make_smem_desc(sf + c * L::kSfBlock + j * kScaleTileBytes, 16, 128, kSwizzleNone));
             const uint32_t sfb = sf + NC * L::kSfBlock + j * kScaleTileBytes;
             constexpr uint32_t kSfb = kSfCol0 + NC * kTilesK * 4;
-            tmem_copy_scales_pair(on, kSfb + 8 * j, make_smem_desc(sfb, 16, 128, kSwizzleNone));
-            tmem_copy_scales_pair(on, kSfb + 8 * j + 4, make_smem_desc(sfb + kSfBytes, 16, 128, kSwizzleNone));
+            tmem_copy_scales_if<2>(on, kSfb + 8 * j, make_smem_desc(sfb, 16, 128, kSwizzleNone));
+            tmem_copy_scales_if<2>(on, kSfb + 8 * j + 4, make_smem_desc(sfb + kSfBytes, 16, 128, kSwizzleNone));
           }
           const uint64_t b_desc = make_smem_desc(mem + L::kStageW, 16, 1024, kSwizzle128B);
 #pragma unroll
@@ -408,7 +408,7 @@ __global__ void __launch_bounds__(threads_of(SW ? 2 : 1), 1) fp4_pair_kernel(con
 #pragma unroll
             for (int c = 0; c < NC; ++c) {
               const uint64_t a_desc = make_smem_desc(mem + static_cast<uint32_t>(c) * kWBytes, 16, 1024, kSwizzle128B);
-              mma_fp4_pair<kVec>(on && kk < steps, static_cast<uint32_t>(NC == 1 ? acc : c) * kAccCols, a_desc + kk * 2,
+              mma_fp4_if<2, kVec>(on && kk < steps, static_cast<uint32_t>(NC == 1 ? acc : c) * kAccCols, a_desc + kk * 2,
                                  b_desc + kk * 2, idesc, kSfCol0 + (c * kTilesK + j) * 4,
                                  kSfCol0 + (NC * kTilesK + 2 * j) * 4 + shift, (kb | kk) != 0 ? 1u : 0u);
             }
@@ -573,6 +573,262 @@ __global__ void __launch_bounds__(threads_of(SW ? 2 : 1), 1) fp4_pair_kernel(con
   }
 }
 
+// ---------------------------------------------------------- few rows -------
+// At most 128 rows of A: the weights' bytes are the time.  One CTA a tile of
+// 128 output columns, the rows (rounded up to 16) as N.  Where there are too
+// few tiles to keep the memory busy, a cluster of `split` CTAs shares a
+// tile's k-blocks and sums its FP32 partials through distributed shared
+// memory, in rank order; else the CTAs walk the tiles.
+// What bounds it: HBM, and at a few MB of weights the latency of a launch and
+// of the first loads.
+constexpr int kSmallMaxRows = 128;
+constexpr int kSmallThreads = 256;
+constexpr int kSmallMaxStages = 8;
+constexpr int kSmallMaxSplit = 8;
+
+struct Fp4SmallParams {
+  CUtensorMap map_w, map_a, map_ws, map_as;  // as above; activations in boxes of n rows, scales of one row block
+  unsigned long long* err;
+  unsigned long long timeout_ns;
+  const float* a_global;
+  const float* b_global;
+  void* d;
+  long long ldd;
+  int M, N, n;             // n: M rounded up to 16
+  int num_k_blocks, last_steps;
+  int tiles, split, stages, out_dtype;
+};
+
+BWG_HD uint32_t small_stage_bytes(int n) {
+  return kWBytes + static_cast<uint32_t>(n) * kKBytes + 2u * 4u * kScaleTileBytes;
+}
+
+template <int FMT>
+__global__ void __launch_bounds__(kSmallThreads, 1) fp4_small_kernel(const __grid_constant__ Fp4SmallParams p) {
+  constexpr int kVec = FMT == kNvfp4 ? 16 : 32;
+  constexpr int kTilesK = FMT == kNvfp4 ? 4 : 2;
+  constexpr uint32_t kSfSlot = 4 * kScaleTileBytes;
+  constexpr uint32_t kSfBytes = kTilesK * kScaleTileBytes;
+  constexpr uint32_t kAcc = kSmallMaxRows;       // columns of one of two accumulators
+  constexpr uint32_t kSfCol0 = 2 * kAcc;
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
+  const uint32_t warp = threadIdx.x >> 5;
+  const uint32_t lane = threadIdx.x & 31u;
+  const int S = p.stages;
+  const uint32_t stage_bytes = small_stage_bytes(p.n);
+  const uint32_t a_bytes = static_cast<uint32_t>(p.n) * kKBytes;
+  const uint32_t bars = base + static_cast<uint32_t>(S) * stage_bytes;
+  auto full_bar = [&](int s) { return bars + 8u * s; };
+  auto empty_bar = [&](int s) { return bars + 8u * (S + s); };
+  auto acc_full = [&](int a) { return bars + 8u * (2 * S + a); };
+  auto acc_empty = [&](int a) { return bars + 8u * (2 * S + 2 + a); };
+  const uint32_t tmem_slot = bars + 8u * (2 * S + 4);
+  const int rank = p.split > 1 ? static_cast<int>(cluster_ctarank()) : 0;
+  const int first = p.split > 1 ? static_cast<int>(cluster_id_x()) : static_cast<int>(blockIdx.x);
+  const int stride = p.split > 1 ? p.tiles : static_cast<int>(gridDim.x);  // a cluster has one tile
+  const int kb0 = p.num_k_blocks * rank / p.split, kb1 = p.num_k_blocks * (rank + 1) / p.split;
+  bool aborted = false;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < S; ++s) {
+      mbar_init(full_bar(s), 1);
+      mbar_init(empty_bar(s), 1);
+    }
+    for (int a = 0; a < 2; ++a) {
+      mbar_init(acc_full(a), 1);
+      mbar_init(acc_empty(a), 4);
+    }
+    fence_mbarrier_init();
+  }
+  if (warp == 0 && lane == 0) {
+    prefetch_tensormap(&p.map_w);
+    prefetch_tensormap(&p.map_a);
+    prefetch_tensormap(&p.map_ws);
+    prefetch_tensormap(&p.map_as);
+  }
+  if (warp == 1) {
+    tmem_alloc<1>(tmem_slot, kTmemCols);  // all columns: they start at 0
+    tmem_relinquish<1>();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+
+  if (warp == 0 || warp == 2) {
+    // ---- TMA producers: weights, activations ---------------------------------
+    const bool weights = warp == 0;
+    const uint64_t stream_once = l2_policy_evict_first();
+    int s = 0;
+    uint32_t ph = 0;
+    for (int t = first; t < p.tiles && !aborted; t += stride) {
+      for (int kb = kb0; kb < kb1; ++kb) {
+        if (!warp_wait_cta(empty_bar(s), ph ^ 1u, p.timeout_ns)) {
+          if (lane == 0) record_fault(p.err, kFaultTimeout, kRoleProducer, kBarEmpty, s, ph ^ 1u);
+          aborted = true;
+          break;
+        }
+        if (elect_one()) {
+          const uint32_t st = base + static_cast<uint32_t>(s) * stage_bytes;
+          const uint32_t sf = st + kWBytes + a_bytes;
+          if (weights) {
+            mbar_arrive_expect_tx(full_bar(s), kWBytes + a_bytes + 2u * kSfBytes);
+            tma_load_3d_hint(st, &p.map_w, full_bar(s), kb * kKBytes, t * 128, 0, stream_once);
+            tma_load_3d_hint(sf, &p.map_ws, full_bar(s), 0, kb * kTilesK, t, stream_once);
+          } else {
+            tma_load_2d(st + kWBytes, &p.map_a, full_bar(s), kb * kKBytes, 0);
+            tma_load_3d(sf + kSfSlot, &p.map_as, full_bar(s), 0, kb * kTilesK, 0);
+          }
+        }
+        __syncwarp();
+        if (++s == S) {
+          s = 0;
+          ph ^= 1u;
+        }
+      }
+    }
+  } else if (warp == 1) {
+    // ---- MMA issuer ------------------------------------------------------------
+    int s = 0, acc = 0;
+    uint32_t ph = 0, acc_ph = 0;
+    const uint32_t idesc0 = make_idesc_fp4(FMT, 128, static_cast<uint32_t>(p.n), 0);
+    for (int t = first; t < p.tiles && !aborted; t += stride) {
+      if (!warp_wait_all(acc_empty(acc), acc_ph ^ 1u, p.timeout_ns)) {
+        if (lane == 0) record_fault(p.err, kFaultTimeout, kRoleMma, kBarAccEmpty, acc, acc_ph ^ 1u);
+        aborted = true;
+        break;
+      }
+      tc_fence_after();
+      for (int kb = kb0; kb < kb1; ++kb) {
+        if (!warp_wait_cta(full_bar(s), ph, p.timeout_ns)) {
+          if (lane == 0) record_fault(p.err, kFaultTimeout, kRoleMma, kBarFull, s, ph);
+          aborted = true;
+          break;
+        }
+        tc_fence_after();
+        const uint32_t st = base + static_cast<uint32_t>(s) * stage_bytes;
+        const uint32_t sf = st + kWBytes + a_bytes;
+        const int steps = kb + 1 == p.num_k_blocks ? p.last_steps : 4;
+        const bool on = elect_one();
+#pragma unroll
+        for (int j = 0; j < kTilesK; ++j) {
+          tmem_copy_scales_if<1>(on, kSfCol0 + j * 4,
+                                 make_smem_desc(sf + j * kScaleTileBytes, 16, 128, kSwizzleNone));
+          tmem_copy_scales_if<1>(on, kSfCol0 + (kTilesK + j) * 4,
+                                 make_smem_desc(sf + kSfSlot + j * kScaleTileBytes, 16, 128, kSwizzleNone));
+        }
+        const uint64_t a_desc = make_smem_desc(st, 16, 1024, kSwizzle128B);
+        const uint64_t b_desc = make_smem_desc(st + kWBytes, 16, 1024, kSwizzle128B);
+#pragma unroll
+        for (int kk = 0; kk < 4; ++kk) {
+          const int j = FMT == kNvfp4 ? kk : kk / 2;
+          const uint32_t idesc = FMT == kNvfp4 ? idesc0
+                                               : (idesc0 | (static_cast<uint32_t>(kk & 1) << 5) |
+                                                  (static_cast<uint32_t>(kk & 1) << 30));
+          mma_fp4_if<1, kVec>(on && kk < steps, static_cast<uint32_t>(acc) * kAcc, a_desc + kk * 2, b_desc + kk * 2,
+                              idesc, kSfCol0 + j * 4, kSfCol0 + (kTilesK + j) * 4, kb != kb0 || kk != 0 ? 1u : 0u);
+        }
+        mma_commit_1cta_if(on, empty_bar(s));
+        if (kb + 1 == kb1) mma_commit_1cta_if(on, acc_full(acc));
+        __syncwarp();
+        if (++s == S) {
+          s = 0;
+          ph ^= 1u;
+        }
+      }
+      acc ^= 1;
+      if (acc == 0) acc_ph ^= 1u;
+    }
+  } else if (warp >= 4) {
+    // ---- epilogue: TMEM lane = output column, TMEM column = row of D ---------
+    const uint32_t q = warp & 3u;
+    const bool out32 = p.out_dtype == kOutF32, outbf = p.out_dtype == kOutBF16;
+    const float alpha = (p.a_global != nullptr ? __ldg(p.a_global) : 1.f) * (p.b_global != nullptr ? __ldg(p.b_global) : 1.f);
+    int acc = 0;
+    uint32_t acc_ph = 0;
+    for (int t = first; t < p.tiles; t += stride) {
+      if (!warp_wait_all(acc_full(acc), acc_ph, p.timeout_ns)) {
+        if (lane == 0) record_fault(p.err, kFaultTimeout, kRoleEpilogue, kBarAccFull, acc, acc_ph);
+        aborted = true;
+        break;
+      }
+      tc_fence_after();
+      const int ch = static_cast<int>(q * 32u + lane);
+      const int col = t * 128 + ch;
+      for (int c0 = 0; c0 < p.M; c0 += 32) {
+        uint32_t v[32];
+        tmem_ld_32x32b_x32(((q * 32u) << 16) + static_cast<uint32_t>(acc) * kAcc + c0, v);
+        tmem_wait_ld();
+        if (c0 + 32 >= p.M) {
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive_local(acc_empty(acc));
+        }
+        if (p.split > 1) {
+          // the ring is idle: every load of this CTA has been used
+#pragma unroll
+          for (int j = 0; j < 32; ++j)
+            if (c0 + j < p.M) st_shared_u32(base + static_cast<uint32_t>((c0 + j) * 128 + ch) * 4u, v[j]);
+        } else if (col < p.N) {
+          const int elt = out32 ? 4 : 2;
+          uint8_t* dst = static_cast<uint8_t*>(p.d) + (static_cast<long long>(c0) * p.ldd + col) * elt;
+#pragma unroll
+          for (int j = 0; j < 32; ++j) {
+            if (c0 + j < p.M) {
+              const float x = alpha * __uint_as_float(v[j]);
+              if (out32)
+                *reinterpret_cast<float*>(dst) = x;
+              else
+                *reinterpret_cast<uint16_t*>(dst) = outbf ? cvt_rn_bf16(x) : cvt_rn_f16(x);
+            }
+            dst += p.ldd * elt;
+          }
+        }
+      }
+      acc ^= 1;
+      if (acc == 0) acc_ph ^= 1u;
+    }
+  }
+  __syncwarp();
+
+  if (p.split > 1) {
+    // ---- partials: rank r sums rows r, r + split, .. of the tile ---------------
+    cluster_sync_all();
+    const bool out32 = p.out_dtype == kOutF32, outbf = p.out_dtype == kOutBF16;
+    const float alpha = (p.a_global != nullptr ? __ldg(p.a_global) : 1.f) * (p.b_global != nullptr ? __ldg(p.b_global) : 1.f);
+    const int ch = static_cast<int>(threadIdx.x & 127u);
+    const int col = first * 128 + ch;
+    for (int j = rank + p.split * static_cast<int>(threadIdx.x >> 7); j < p.M; j += 2 * p.split) {
+      const uint32_t at = base + static_cast<uint32_t>(j * 128 + ch) * 4u;
+      float part[kSmallMaxSplit];
+#pragma unroll
+      for (int c = 0; c < kSmallMaxSplit; ++c)
+        part[c] = c < p.split ? __uint_as_float(ld_shared_cluster_u32(mapa_shared(at, static_cast<uint32_t>(c)))) : 0.f;
+      float x = part[0];
+#pragma unroll
+      for (int c = 1; c < kSmallMaxSplit; ++c)
+        if (c < p.split) x += part[c];
+      x *= alpha;
+      if (col < p.N) {
+        uint8_t* dst = static_cast<uint8_t*>(p.d) + (static_cast<long long>(j) * p.ldd + col) * (out32 ? 4 : 2);
+        if (out32)
+          *reinterpret_cast<float*>(dst) = x;
+        else
+          *reinterpret_cast<uint16_t*>(dst) = outbf ? cvt_rn_bf16(x) : cvt_rn_f16(x);
+      }
+    }
+  }
+  if (__syncthreads_or(aborted ? 1 : 0)) {
+    const uint64_t t0 = globaltimer_ns();
+    while (globaltimer_ns() - t0 < 200000ull) nanosleep_ns(1000);
+  }
+  if (p.split > 1) cluster_sync_all();  // peers may still read this CTA's partials
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc<1>(0, kTmemCols);
+  }
+}
+
 // SwiGLU of FP32 rows [gate | up], for halves that the fused epilogue cannot
 // pair (it needs both to start on a tile of scales): rows before *last only.
 template <class T>
@@ -692,6 +948,103 @@ bool fp4_maps(Fp4GemmParams* p, const Fp4Operand& a, const Fp4Operand& b, int M,
          runtime_map(&p->map_as, a.scales, u32, 3, asd, ss, asb, CU_TENSOR_MAP_SWIZZLE_NONE);
 }
 
+// Cluster size of a few-rows call: the one that keeps the most SMs loading,
+// with all clusters co-resident and two k-blocks a CTA at least; 1 where the
+// tiles alone fill half of the SMs.
+int small_split(int tiles, int kb, int sm_count, const int* clusters) {
+  if (2 * tiles > sm_count) return 1;
+  int best = 1;
+  for (int f = 2; f <= kSmallMaxSplit; ++f)
+    if (tiles <= clusters[f] && kb >= 2 * f) best = f;
+  return best;
+}
+
+bwg_status run_small(const Fp4Operand& a, const Fp4Operand& b, void* D, int M, int N, int K, int ldd, int format,
+                     int out_dtype, const Runtime& rt, cudaStream_t stream) {
+  using Kernel = void (*)(Fp4SmallParams);
+  const Kernel k = format == kNvfp4 ? fp4_small_kernel<kNvfp4> : fp4_small_kernel<kMxfp4>;
+  // co-resident clusters by size, once per device (every call of this kernel
+  // takes more than half of an SM's shared memory)
+  static std::mutex mu;
+  static struct {
+    bool ready;
+    int clusters[kSmallMaxSplit + 1];
+  } seen[64][2];
+  if (rt.device >= 64) return BWG_ERR_UNSUPPORTED;
+  cudaLaunchConfig_t cfg = {};
+  cfg.blockDim = dim3(kSmallThreads, 1, 1);
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  auto& info = seen[rt.device][format];
+  {
+    std::lock_guard<std::mutex> lock(mu);
+    if (!info.ready) {
+      const void* fn = reinterpret_cast<const void*>(k);
+      if (cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, rt.max_smem) != cudaSuccess) {
+        cudaGetLastError();
+        return BWG_ERR_CUDA;
+      }
+      for (int f = 2; f <= kSmallMaxSplit; ++f) {
+        cfg.gridDim = dim3(static_cast<unsigned>(f), 1, 1);
+        cfg.dynamicSmemBytes = static_cast<size_t>(rt.max_smem);
+        attr[0].val.clusterDim.x = static_cast<unsigned>(f);
+        int n = 0;
+        if (cudaOccupancyMaxActiveClusters(&n, fn, &cfg) != cudaSuccess) {
+          cudaGetLastError();
+          n = 0;
+        }
+        info.clusters[f] = n;
+      }
+      info.ready = true;
+    }
+  }
+  Fp4SmallParams p;
+  std::memset(&p, 0, sizeof(p));
+  p.n = (M + 15) & ~15;
+  const uint64_t row = static_cast<uint64_t>(K / 2);
+  const uint64_t kt = static_cast<uint64_t>(fp4_k_tiles(K, format));
+  const uint32_t kbox = format == kNvfp4 ? 4 : 2;
+  const CUtensorMapDataType u8 = CU_TENSOR_MAP_DATA_TYPE_UINT8, u32 = CU_TENSOR_MAP_DATA_TYPE_UINT32;
+  const uint64_t wd[3] = {row, static_cast<uint64_t>(N), 1}, ws[2] = {row, row * static_cast<uint64_t>(N)};
+  const uint32_t wb[3] = {kKBytes, 128, 1};
+  const uint64_t ad[2] = {row, static_cast<uint64_t>(M)};
+  const uint32_t ab[2] = {kKBytes, static_cast<uint32_t>(p.n)};
+  const uint64_t ss[2] = {kScaleTileBytes, kt * kScaleTileBytes};
+  const uint64_t wsd[3] = {128, kt, static_cast<uint64_t>(pad128(N) / 128)}, asd[3] = {128, kt, 1};
+  const uint32_t sb[3] = {128, kbox, 1};
+  if (!runtime_map(&p.map_w, b.codes, u8, 3, wd, ws, wb, CU_TENSOR_MAP_SWIZZLE_128B) ||
+      !runtime_map(&p.map_a, a.codes, u8, 2, ad, &row, ab, CU_TENSOR_MAP_SWIZZLE_128B) ||
+      !runtime_map(&p.map_ws, b.scales, u32, 3, wsd, ss, sb, CU_TENSOR_MAP_SWIZZLE_NONE) ||
+      !runtime_map(&p.map_as, a.scales, u32, 3, asd, ss, sb, CU_TENSOR_MAP_SWIZZLE_NONE))
+    return BWG_ERR_CUDA;
+  p.err = rt.err;
+  p.timeout_ns = rt.timeout_ns;
+  p.a_global = a.global;
+  p.b_global = b.global;
+  p.d = D;
+  p.ldd = ldd;
+  p.M = M;
+  p.N = N;
+  p.num_k_blocks = (K + kKCols - 1) / kKCols;
+  p.last_steps = (K - (p.num_k_blocks - 1) * kKCols + 63) / 64;
+  p.tiles = (N + 127) / 128;
+  p.split = small_split(p.tiles, p.num_k_blocks, rt.sm_count, info.clusters);
+  p.out_dtype = out_dtype;
+  const int stage = static_cast<int>(small_stage_bytes(p.n));
+  const int tail = 1024 + 8 * (2 * kSmallMaxStages + 4) + 16;
+  p.stages = std::min(kSmallMaxStages, (rt.max_smem - tail) / stage);
+  if (p.stages < 2) return BWG_ERR_UNSUPPORTED;
+  cfg.gridDim = dim3(static_cast<unsigned>(p.split > 1 ? p.tiles * p.split : std::min(p.tiles, rt.sm_count)), 1, 1);
+  cfg.dynamicSmemBytes = static_cast<size_t>(p.stages * stage + tail);
+  cfg.stream = stream;
+  attr[0].val.clusterDim.x = static_cast<unsigned>(p.split);
+  return runtime_status(cudaLaunchKernelEx(&cfg, k, p));
+}
+
 bool aligned16(const void* q) { return (reinterpret_cast<uintptr_t>(q) & 15u) == 0; }
 
 bwg_status run_fp4_gemm(const Fp4Operand& a, const Fp4Operand& b, void* D, int M, int N, int K, int ldd, int format,
@@ -717,6 +1070,8 @@ bwg_status run_fp4_gemm(const Fp4Operand& a, const Fp4Operand& b, void* D, int M
   bwg_status st = runtime_device(&rt);
   if (st != BWG_OK) return st;
   if (K == 0) return runtime_status(launch_zero_fill(D, M, n_out, ldd, out_dtype == BWG_OUT_FP32 ? 4 : 2, stream));
+  if (offsets == nullptr && G == 1 && M <= kSmallMaxRows)
+    return run_small(a, b, D, M, N, K, ldd, format, out_dtype, rt, stream);
   Fp4GemmParams p;
   std::memset(&p, 0, sizeof(p));
   const int nc = swiglu ? 2 : 1;

@@ -47,16 +47,15 @@ __device__ __forceinline__ void record_bad_position(unsigned long long* err) {
 // ------------------------------------------------------------------ sort ----
 // One cluster of C CTAs of W warps; warp g of all C * W takes the g-th
 // contiguous run of pairs.  Pass 1 counts each warp's pairs per expert in a
-// shared-memory row of its own (lanes with the same expert are found with
-// match.any and counted by one of them, so no two lanes write one counter);
+// shared-memory row of its own (lanes with the same expert are found by votes
+// and counted by one of them, so no two lanes write one counter);
 // the counts become starts by prefix sums over warps, over CTAs (through
 // distributed shared memory) and over experts; pass 2 hands out the rows in
 // pair order.
 // What bounds it: latency.  The ids are 0.3 MB for the 4096 x 8 layer; one
 // launch with its counts on chip replaces three passes through global memory.
-// 32768 ids of 32 experts: 10.6 us, against 11.6 with a loop over the
-// warps' counts and over the CTAs' totals in their place (one shared-memory or
-// distributed load after the other).
+// 32768 ids of 32 experts: 8.2 us, 11.6 with match.any and with sums over the
+// warps' counts and the CTAs' totals that wait for one load after the other.
 constexpr int kSortMaxWarps = 32;
 constexpr int kSortAhead = 4;    // id loads in flight per lane
 constexpr int kSortCtas = 8;     // of the cluster
@@ -68,9 +67,8 @@ __global__ void __launch_bounds__(kSortMaxWarps * 32)
   extern __shared__ int sm[];
   const int W = static_cast<int>(blockDim.x >> 5);
   const int buckets = E + 1;         // bucket E: pairs without an expert
-  const int pitch = buckets | 1;     // odd: the lanes of a column read different banks
-  int* hist = sm;                    // [W][pitch]
-  int* total = sm + W * pitch;       // [buckets] this CTA's counts
+  int* hist = sm;                    // [W][buckets]
+  int* total = sm + W * buckets;       // [buckets] this CTA's counts
   int* start = total + buckets;      // [buckets] this CTA's first row in each bucket
   int* part = start + buckets;       // [32] scan partials
   const int lane = static_cast<int>(threadIdx.x & 31u);
@@ -81,13 +79,25 @@ __global__ void __launch_bounds__(kSortMaxWarps * 32)
   const long long per = ((pairs + runs - 1) / runs + 31) / 32 * 32;
   const long long first = (static_cast<long long>(rank) * W + warp) * per;
   const long long last = first + per < pairs ? first + per : pairs;
-  int* mine = hist + warp * pitch;
+  int* mine = hist + warp * buckets;
   const unsigned below = (1u << lane) - 1u;
 
   auto load = [&](long long p) -> int {
     if (p >= last) return -1;
     const ID v = ids[p];
     return v >= 0 && v < static_cast<ID>(E) ? static_cast<int>(v) : E;
+  };
+  // The lanes with this lane's bucket, bit by bit of the bucket's number: 6
+  // votes for 32 experts take less time than one match.any (131072 pairs
+  // 21 us, with match.any 29).
+  const int bits = 32 - __clz(E);
+  auto same_bucket = [&](int key) -> unsigned {
+    unsigned same = __ballot_sync(0xffffffffu, key >= 0);
+    for (int b = 0; b < bits; ++b) {
+      const unsigned set = __ballot_sync(0xffffffffu, (key >> b) & 1);
+      same &= (key >> b) & 1 ? set : ~set;
+    }
+    return same;
   };
   int key[kSortAhead];
 #pragma unroll
@@ -101,23 +111,28 @@ __global__ void __launch_bounds__(kSortMaxWarps * 32)
     }
 #pragma unroll
     for (int a = 0; a < kSortAhead; ++a) {
-      const unsigned same = __match_any_sync(0xffffffffu, key[a]);
+      if (p0 + 32 * a >= last) break;
+      const unsigned same = same_bucket(key[a]);
       if (key[a] >= 0 && (same & below) == 0) mine[key[a]] += __popc(same);
       __syncwarp();
     }
   }
   __syncthreads();
-  // warps' counts -> each warp's start inside the CTA's share of the bucket:
-  // a warp a bucket, a lane a row of counts
-  for (int b = warp; b < buckets; b += W) {
-    const int c = lane < W ? hist[lane * pitch + b] : 0;
-    int incl = c;
-    for (int d = 1; d < 32; d <<= 1) {
-      const int y = __shfl_up_sync(0xffffffffu, incl, d);
-      if (lane >= d) incl += y;
+  // warps' counts -> each warp's start inside the CTA's share of the bucket,
+  // a thread a bucket, 8 loads ahead
+  for (int b = static_cast<int>(threadIdx.x); b < buckets; b += static_cast<int>(blockDim.x)) {
+    int run = 0;
+    for (int w0 = 0; w0 < W; w0 += 8) {
+      int c[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) c[i] = w0 + i < W ? hist[(w0 + i) * buckets + b] : 0;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        if (w0 + i < W) hist[(w0 + i) * buckets + b] = run;
+        run += c[i];
+      }
     }
-    if (lane < W) hist[lane * pitch + b] = incl - c;
-    if (lane == 31) total[b] = incl;
+    total[b] = run;
   }
   if (n_cta > 1)
     cluster_sync_all();
@@ -174,7 +189,8 @@ __global__ void __launch_bounds__(kSortMaxWarps * 32)
     }
 #pragma unroll
     for (int a = 0; a < kSortAhead; ++a) {
-      const unsigned same = __match_any_sync(0xffffffffu, key[a]);
+      if (p0 + 32 * a >= last) break;
+      const unsigned same = same_bucket(key[a]);
       if (key[a] >= 0) {
         const int at = start[key[a]] + mine[key[a]] + __popc(same & below);
         const int p = static_cast<int>(p0 + 32 * a + lane);
@@ -523,11 +539,11 @@ bwg_status run_combine(const void* rows, int dtype, int T, int H, int ldr, int k
 
 template <class ID>
 cudaError_t launch_sort(const void* ids, int pairs, int E, int* offsets, int* order, int* position, cudaStream_t s) {
-  // One CTA up to 4096 pairs, a warp for each 128 of them; a cluster of 8
-  // beyond, whose 256 warps then have at least 16 pairs each.
-  const int n_cta = pairs <= 4096 ? 1 : kSortCtas;
+  // One CTA up to 2048 pairs (256 experts: 5.6 us), a warp for each 128 of
+  // them; a cluster of 8 beyond (8192 pairs: 6.2 us, one CTA 4096 in 7.7).
+  const int n_cta = pairs <= 2048 ? 1 : kSortCtas;
   const int warps = n_cta > 1 ? kSortMaxWarps : std::min(kSortMaxWarps, std::max(4, (pairs + 127) / 128));
-  const size_t smem = (static_cast<size_t>(warps) * ((E + 1) | 1) + 2 * (E + 1) + 32) * sizeof(int);
+  const size_t smem = (static_cast<size_t>(warps + 2) * (E + 1) + 32) * sizeof(int);
   if (smem > 48 * 1024) {
     const cudaError_t a = cudaFuncSetAttribute(moe_sort_kernel<ID>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                                static_cast<int>(smem));

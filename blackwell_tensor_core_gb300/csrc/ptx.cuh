@@ -514,21 +514,35 @@ BWG_DEV void mma_f16(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t
 
 // D[tmem] (+)= (A x scale_A) x (B x scale_B), e2m1 operands with one scale per
 // block of 16 (VEC = 16, four a 64-column step) or 32 (two) columns, the
-// scales in TMEM; FP32 accumulator; CTA pair.
-template <int VEC>
-BWG_DEV void mma_fp4_pair(bool on, uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+// scales in TMEM; FP32 accumulator; CTA pair (CG = 2) or one CTA.
+template <int CG, int VEC>
+BWG_DEV void mma_fp4_if(bool on, uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
                           uint32_t sfa_tmem, uint32_t sfb_tmem, uint32_t accumulate) {
-  if constexpr (VEC == 16)
+  if constexpr (CG == 2 && VEC == 16)
     asm volatile(
         "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %6, 0;\n\tsetp.ne.b32 q, %7, 0;\n\t"
         "@q tcgen05.mma.cta_group::2.kind::mxf4nvf4.block_scale.scale_vec::4X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(
             d_tmem),
         "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(sfa_tmem), "r"(sfb_tmem), "r"(accumulate), "r"(on ? 1u : 0u)
         : "memory");
-  else
+  else if constexpr (CG == 2)
     asm volatile(
         "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %6, 0;\n\tsetp.ne.b32 q, %7, 0;\n\t"
         "@q tcgen05.mma.cta_group::2.kind::mxf4nvf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(
+            d_tmem),
+        "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(sfa_tmem), "r"(sfb_tmem), "r"(accumulate), "r"(on ? 1u : 0u)
+        : "memory");
+  else if constexpr (VEC == 16)
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %6, 0;\n\tsetp.ne.b32 q, %7, 0;\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::mxf4nvf4.block_scale.scale_vec::4X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(
+            d_tmem),
+        "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(sfa_tmem), "r"(sfb_tmem), "r"(accumulate), "r"(on ? 1u : 0u)
+        : "memory");
+  else
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %6, 0;\n\tsetp.ne.b32 q, %7, 0;\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::mxf4nvf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(
             d_tmem),
         "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(sfa_tmem), "r"(sfb_tmem), "r"(accumulate), "r"(on ? 1u : 0u)
         : "memory");
@@ -536,13 +550,29 @@ BWG_DEV void mma_fp4_pair(bool on, uint32_t d_tmem, uint64_t a_desc, uint64_t b_
 
 // Copy 32 rows of 128 bits from shared memory (unswizzled core matrices, see
 // the descriptor) to four TMEM columns of 32 lanes, repeated for each of the
-// four lane quarters, in both CTAs of a pair, each from its own shared
-// memory.  Runs in order with the MMAs of the same thread.
-BWG_DEV void tmem_copy_scales_pair(bool on, uint32_t taddr, uint64_t s_desc) {
+// four lane quarters; with CG = 2 in both CTAs of a pair, each from its own
+// shared memory.  Runs in order with the MMAs of the same thread.
+template <int CG>
+BWG_DEV void tmem_copy_scales_if(bool on, uint32_t taddr, uint64_t s_desc) {
+  if constexpr (CG == 2)
+    asm volatile(
+        "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %2, 0;\n\t"
+        "@q tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;\n\t}" ::"r"(taddr),
+        "l"(s_desc), "r"(on ? 1u : 0u)
+        : "memory");
+  else
+    asm volatile(
+        "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %2, 0;\n\t"
+        "@q tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;\n\t}" ::"r"(taddr),
+        "l"(s_desc), "r"(on ? 1u : 0u)
+        : "memory");
+}
+
+BWG_DEV void mma_commit_1cta_if(bool on, uint32_t bar) {
   asm volatile(
-      "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %2, 0;\n\t"
-      "@q tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;\n\t}" ::"r"(taddr),
-      "l"(s_desc), "r"(on ? 1u : 0u)
+      "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %1, 0;\n\t"
+      "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(bar),
+      "r"(on ? 1u : 0u)
       : "memory");
 }
 

@@ -219,7 +219,8 @@ def test_quantize_nothing(ops):
 # ---------------------------------------------------------- dense product ---
 
 DENSE = [(1, 8, 32), (1, 128, 64), (16, 128, 256), (17, 200, 96), (64, 256, 512), (72, 520, 1056), (128, 130, 320),
-         (129, 256, 256), (192, 512, 768), (193, 513, 544), (300, 1000, 416), (385, 1024, 2048), (1000, 300, 7168)]
+         (129, 256, 256), (192, 512, 768), (193, 513, 544), (300, 1000, 416), (385, 1024, 2048), (1000, 300, 7168),
+         (1, 2048, 7168), (5, 300, 7168), (128, 1024, 4096), (97, 4100, 2080), (33, 20000, 512), (100, 19600, 256)]
 
 
 @pytest.mark.parametrize("fmt", FMTS)
