@@ -7,7 +7,7 @@
 // The kernel computes D^T: 128 weight rows per CTA are the M of an
 // instruction and the activations' rows its N, which may be any multiple of
 // 16 up to 192.  So a ragged end of a group costs what it has rows, not a
-// 256-row tile.  A CTA pair (cta_group::2) takes 256 output columns x 192
+// 256-row tile.  A CTA pair (cta_group::2) takes 256 or 512 weight rows x 192
 // activation rows; each CTA stages its own weight rows and half of the
 // activation rows.
 //
@@ -211,8 +211,8 @@ constexpr int threads_of(int nc) { return nc == 1 ? 256 : 384; }
 constexpr int stages_of(int nc) { return nc == 1 ? 6 : 4; }
 
 // SwiGLU: registers per thread after set-up, out of 168 x 384 at launch.
-constexpr uint32_t kRegsControlSw = 56, kRegsEpilogueSw = 224;
-static_assert(kRegsControlSw * 128 + kRegsEpilogueSw * 256 <= 168 * 384, "the register split must fit");
+constexpr uint32_t kRegsControl = 56, kRegsEpilogue = 224;
+static_assert(kRegsControl * 128 + kRegsEpilogue * 256 <= 168 * 384, "the register split must fit");
 
 // Shared memory: stage s holds [NC weight blocks][activation rows][scales].
 template <int NC>
@@ -225,22 +225,26 @@ struct Layout {
   static_assert(kStage % 1024 == 0, "swizzled tiles start on 1024 bytes");
 };
 
-// A tile is 256 output columns (128 a CTA) x up to 192 rows.  Plain: one block
-// of weight rows a CTA and two accumulators, so that the epilogue of a tile
-// runs beside the MMAs of the next.  SW: the gate and the up rows of the same
-// columns, one accumulator each.  (Two blocks a CTA for the plain product too,
-// which stages a quarter fewer bytes per instruction, took 165 us against 160
-// for 8192^3: its one accumulator per block leaves the tensor cores idle at
-// each tile's end.)
-template <int FMT, bool SW>
-__global__ void __launch_bounds__(threads_of(SW ? 2 : 1), 1) fp4_pair_kernel(const __grid_constant__ Fp4GemmParams p) {
-  constexpr int NC = SW ? 2 : 1;
+// NC weight blocks of 128 rows a CTA x up to 192 rows of A.  NC == 1: two
+// accumulators, so that the epilogue of a tile runs beside the MMAs of the
+// next.  NC == 2: one accumulator a block; fewer bytes staged and fewer
+// instructions issued per tile, but the tensor cores idle about 1600 clocks at
+// a tile's end.  SW: the two blocks are the gate and the up rows of the same
+// 256 output columns.
+// What bounds it: with random data the power limit (8192^3 NVFP4 160 us in a
+// short run at 2070 MHz, 182 back to back at 1.87-1.95 GHz and 1370 W); at full
+// clock the MMA warp's issue and the staging: a k-block of an NC == 2 tile
+// takes 0.42 us (0.39 MXFP4) where its MMAs need 0.371, one of an NC == 1 tile
+// 0.24 (0.21) for 0.186.
+template <int NC, int FMT, bool SW>
+__global__ void __launch_bounds__(threads_of(NC), 1) fp4_pair_kernel(const __grid_constant__ Fp4GemmParams p) {
+  static_assert(!SW || NC == 2, "SwiGLU pairs a gate block with an up block");
   using L = Layout<NC>;
   constexpr int kVec = FMT == kNvfp4 ? 16 : 32;
   constexpr int kTilesK = FMT == kNvfp4 ? 4 : 2;     // scale tiles of a stage along K
   constexpr uint32_t kSfBytes = kTilesK * kScaleTileBytes;
   constexpr uint32_t kStageTx = 2u * (L::kStageW + kTokBytes + (NC + 2) * kSfBytes);
-  constexpr int kWRows = 256;                        // output columns of a tile
+  constexpr int kWRows = SW ? 256 : 256 * NC;        // output columns of a tile
   constexpr uint32_t kAccCols = kTok;
   constexpr uint32_t kSfCol0 = 2 * kTok;             // scales start after the two accumulators
   constexpr uint32_t kSfCols = (NC + 2) * kTilesK * 4;  // TMEM columns of one stage's scales
@@ -296,7 +300,7 @@ __global__ void __launch_bounds__(threads_of(SW ? 2 : 1), 1) fp4_pair_kernel(con
 
   if (warp < 4) {
     // the epilogue warpgroups hold both accumulators' slices
-    if constexpr (SW) setmaxnreg_dec<kRegsControlSw>();
+    if constexpr (NC == 2) setmaxnreg_dec<kRegsControl>();
     if (warp != 1) {
     // ---- TMA producers --------------------------------------------------------
     // One warp for each weight block and one for the activations (NC == 1: the
@@ -312,7 +316,7 @@ __global__ void __launch_bounds__(threads_of(SW ? 2 : 1), 1) fp4_pair_kernel(con
       for (int i = 0; win.have(i) && !aborted; ++i) {
         const Tile tl = win.at(i);
         const int row = job == 2 ? tl.t0 + static_cast<int>(rank) * (tl.n / 2)
-                                 : tl.w0 + static_cast<int>(rank) * 128 + job * p.swiglu_up;
+                                 : tl.w0 + static_cast<int>(rank) * 128 + job * (SW ? p.swiglu_up : 256);
         const int sf_row = job == 2 ? tl.srow / 128 : tl.g * p.w_blocks + row / 128;
         for (int kb = 0; kb < p.num_k_blocks; ++kb) {
           if (!warp_wait_cta(empty_bar(s), ph ^ 1u, p.timeout_ns)) {
@@ -444,7 +448,7 @@ __global__ void __launch_bounds__(threads_of(SW ? 2 : 1), 1) fp4_pair_kernel(con
     }
     __syncwarp();
   } else {
-    if constexpr (SW) setmaxnreg_inc<kRegsEpilogueSw>();
+    if constexpr (NC == 2) setmaxnreg_inc<kRegsEpilogue>();
     // ---- epilogue: TMEM lane = output column, TMEM column = row of D --------
     const uint32_t q = warp & 3u;
     const int grp = static_cast<int>((warp - 4u) >> 2);  // SwiGLU: warpgroup 0 or 1
@@ -468,7 +472,7 @@ __global__ void __launch_bounds__(threads_of(SW ? 2 : 1), 1) fp4_pair_kernel(con
     // write 32 adjacent columns of one row at a time
     auto store = [&](const Tile& tl, int c0, const uint32_t (&v)[32]) {
       const int rows = tl.tokens - c0;
-      const int col = tl.w0 + static_cast<int>(rank * 128u + q * 32u + lane);
+      const int col = tl.w0 + (NC == 2 && !SW ? grp * 256 : 0) + static_cast<int>(rank * 128u + q * 32u + lane);
       if (col >= p.N || rows <= 0) return;
       const int elt = out32 ? 4 : 2;
       const long long row_bytes = p.ldd * elt;
@@ -526,6 +530,32 @@ __global__ void __launch_bounds__(threads_of(SW ? 2 : 1), 1) fp4_pair_kernel(con
             gate[c][j] =
                 __float_as_uint(silu_mul(alpha * __uint_as_float(gate[c][j]), alpha * __uint_as_float(up[c][j])));
           store(tl, grp * 32 + c * 64, gate[c]);
+        }
+      }
+    } else if constexpr (NC == 2) {
+      // each warpgroup its block's accumulator, all of it before the hand-back
+      uint32_t acc_ph = 0;
+      for (int i = 0; win.have(i); ++i) {
+        if (!wait_acc_full(grp, acc_ph)) {
+          aborted = true;
+          break;
+        }
+        acc_ph ^= 1u;
+        tc_fence_after();
+        uint32_t v[6][32];
+#pragma unroll
+        for (int c = 0; c < 6; ++c) tmem_ld_32x32b_x32(t_lane + static_cast<uint32_t>(grp) * kAccCols + c * 32, v[c]);
+        tmem_wait_ld();
+        tc_fence_before();
+        __syncwarp();
+        release(grp);
+        const Tile tl = win.at(i);
+        const float alpha = alpha_of(tl.g);
+#pragma unroll
+        for (int c = 0; c < 6; ++c) {
+#pragma unroll
+          for (int j = 0; j < 32; ++j) v[c][j] = __float_as_uint(alpha * __uint_as_float(v[c][j]));
+          store(tl, c * 32, v[c]);
         }
       }
     } else {
@@ -856,9 +886,10 @@ int pair_smem(int G) {
 
 using PairKernel = void (*)(Fp4GemmParams);
 
-PairKernel pick_pair(int format, bool sw) {
-  if (sw) return format == kNvfp4 ? fp4_pair_kernel<kNvfp4, true> : fp4_pair_kernel<kMxfp4, true>;
-  return format == kNvfp4 ? fp4_pair_kernel<kNvfp4, false> : fp4_pair_kernel<kMxfp4, false>;
+PairKernel pick_pair(int nc, int format, bool sw) {
+  if (sw) return format == kNvfp4 ? fp4_pair_kernel<2, kNvfp4, true> : fp4_pair_kernel<2, kMxfp4, true>;
+  if (nc == 2) return format == kNvfp4 ? fp4_pair_kernel<2, kNvfp4, false> : fp4_pair_kernel<2, kMxfp4, false>;
+  return format == kNvfp4 ? fp4_pair_kernel<1, kNvfp4, false> : fp4_pair_kernel<1, kMxfp4, false>;
 }
 
 // Co-resident pairs of a kernel at the largest shared memory, and its
@@ -872,7 +903,7 @@ bwg_status pair_clusters(PairKernel k, int nc, const Runtime& rt, int* clusters)
   static struct {
     Key key;
     int clusters;
-  } seen[64 * 4];
+  } seen[64 * 6];
   static int n_seen = 0;
   std::lock_guard<std::mutex> lock(mu);
   for (int i = 0; i < n_seen; ++i)
@@ -903,7 +934,7 @@ bwg_status pair_clusters(PairKernel k, int nc, const Runtime& rt, int* clusters)
   }
   // the SwiGLU kernel's register split only completes if the CTA was launched
   // with at least the registers that it hands out
-  if (nc == 2 && static_cast<uint32_t>(fa.numRegs) * threads_of(2) < kRegsControlSw * 128u + kRegsEpilogueSw * 256u)
+  if (nc == 2 && static_cast<uint32_t>(fa.numRegs) * threads_of(2) < kRegsControl * 128u + kRegsEpilogue * 256u)
     return BWG_ERR_UNSUPPORTED;
   int n = 0;
   if (cudaOccupancyMaxActiveClusters(&n, fn, &cfg) != cudaSuccess || n <= 0) {
@@ -917,6 +948,19 @@ bwg_status pair_clusters(PairKernel k, int nc, const Runtime& rt, int* clusters)
   }
   *clusters = n;
   return BWG_OK;
+}
+
+// Weight blocks a CTA for a plain product.  A tile of two blocks takes 1.9
+// times as long as one of one block, but a pair's last round of tiles is then
+// twice as coarse.  Back to back at the power limit, 8192^3 NVFP4: 182 us with
+// two blocks (10 rounds), 190 with one (19); 32 experts' FC1 without SwiGLU 217
+// and 228; 4096^3 (3 and 5 rounds) 31.0 and 27.5.
+int plain_blocks(int M, int N, int groups, int pairs) {
+  // a ragged group ends on half a tile on average
+  const long long rows = (M + kTok - 1LL) / kTok + groups / 2;
+  const long long one = (rows * ((N + 255) / 256) + pairs - 1) / pairs;
+  const long long two = (rows * ((N + 511) / 512) + pairs - 1) / pairs;
+  return 19 * two <= 10 * one ? 2 : 1;
 }
 
 struct Fp4Operand {
@@ -1074,8 +1118,8 @@ bwg_status run_fp4_gemm(const Fp4Operand& a, const Fp4Operand& b, void* D, int M
     return run_small(a, b, D, M, N, K, ldd, format, out_dtype, rt, stream);
   Fp4GemmParams p;
   std::memset(&p, 0, sizeof(p));
-  const int nc = swiglu ? 2 : 1;
-  const long long tok_tiles = (M + kTok - 1LL) / kTok + (offsets != nullptr ? G : 0);
+  const long long tok_tiles = (M + kTok - 1LL) / kTok + (offsets != nullptr ? G : 0);  // at most
+  const int nc = swiglu ? 2 : plain_blocks(M, n_out, offsets != nullptr ? G : 0, rt.sm_count / 2);
   p.w_blocks = pad128(N) / 128;
   const int a_rows = offsets != nullptr ? static_cast<int>((M + 127LL * std::min(G, M)) / 128) : pad128(M) / 128;
   if (!fp4_maps(&p, a, b, M, N, K, format, G, a_rows)) return BWG_ERR_CUDA;
@@ -1092,13 +1136,14 @@ bwg_status run_fp4_gemm(const Fp4Operand& a, const Fp4Operand& b, void* D, int M
   p.G = G;
   p.num_k_blocks = (K + kKCols - 1) / kKCols;
   p.last_steps = (K - (p.num_k_blocks - 1) * kKCols + 63) / 64;
-  p.num_w_tiles = (n_out + 255) / 256;
+  const int w_rows = swiglu ? 256 : 256 * nc;
+  p.num_w_tiles = (n_out + w_rows - 1) / w_rows;
   p.swiglu_up = n_out;
   p.out_dtype = out_dtype;
   p.group_m = 8;
   const int smem = nc == 2 ? pair_smem<2>(G) : pair_smem<1>(G);
   if (smem > rt.max_smem) return BWG_ERR_UNSUPPORTED;
-  const PairKernel k = pick_pair(format, swiglu);
+  const PairKernel k = pick_pair(nc, format, swiglu);
   int clusters = 0;
   if ((st = pair_clusters(k, nc, rt, &clusters)) != BWG_OK) return st;
   // every group adds at most one partial tile of rows

@@ -220,7 +220,8 @@ def test_quantize_nothing(ops):
 
 DENSE = [(1, 8, 32), (1, 128, 64), (16, 128, 256), (17, 200, 96), (64, 256, 512), (72, 520, 1056), (128, 130, 320),
          (129, 256, 256), (192, 512, 768), (193, 513, 544), (300, 1000, 416), (385, 1024, 2048), (1000, 300, 7168),
-         (1, 2048, 7168), (5, 300, 7168), (128, 1024, 4096), (97, 4100, 2080), (33, 20000, 512), (100, 19600, 256)]
+         (1, 2048, 7168), (5, 300, 7168), (128, 1024, 4096), (97, 4100, 2080), (33, 20000, 512), (100, 19600, 256),
+         (1150, 5000, 544), (1150, 5000, 1792)]  # two weight blocks a CTA
 
 
 @pytest.mark.parametrize("fmt", FMTS)
@@ -310,7 +311,7 @@ GROUPS = [[5], [0, 0, 3], [300, 0, 256, 1, 0, 191, 37, 193, 530], [192, 384], [1
 
 @pytest.mark.parametrize("fmt", FMTS)
 @pytest.mark.parametrize("counts", GROUPS)
-@pytest.mark.parametrize("N,K", [(200, 96), (512, 512), (768, 1120)])
+@pytest.mark.parametrize("N,K", [(200, 96), (512, 512), (768, 1120), (2600, 352)])
 def test_grouped_integers_are_exact(ops, counts, N, K, fmt):
     rng = np.random.default_rng(sum(counts) + N)
     off = np.concatenate([[0], np.cumsum(counts)]).astype(np.int32)
