@@ -210,7 +210,7 @@ constexpr int threads_of(int nc) { return nc == 1 ? 256 : 384; }
 // addresses are constants.
 constexpr int stages_of(int nc) { return nc == 1 ? 6 : 4; }
 
-// SwiGLU: registers per thread after set-up, out of 168 x 384 at launch.
+// Two blocks: registers per thread after set-up, out of 168 x 384 at launch.
 constexpr uint32_t kRegsControl = 56, kRegsEpilogue = 224;
 static_assert(kRegsControl * 128 + kRegsEpilogue * 256 <= 168 * 384, "the register split must fit");
 
@@ -299,152 +299,154 @@ __global__ void __launch_bounds__(threads_of(NC), 1) fp4_pair_kernel(const __gri
   bool aborted = false;
 
   if (warp < 4) {
-    // the epilogue warpgroups hold both accumulators' slices
+    // the epilogue warpgroups hold whole slices of accumulators
     if constexpr (NC == 2) setmaxnreg_dec<kRegsControl>();
     if (warp != 1) {
-    // ---- TMA producers --------------------------------------------------------
-    // One warp for each weight block and one for the activations (NC == 1: the
-    // third has none).  A stage takes 6 loads; one diverged thread issuing
-    // them needs about 900 clocks, more than the stage's MMAs (768).  Warps
-    // that stay together and elect a lane need about 50 clocks a load, and
-    // three of them share the loads.
-    const int job = warp == 0 ? 0 : static_cast<int>(warp) - 1;  // 0, 1: weight block, 2: activations
-    if (job == 2 || job < NC) {
-      int s = 0;
-      uint32_t ph = 0;
-      TileWindow<kWRows> win(p, tb, first, stride, total);
-      for (int i = 0; win.have(i) && !aborted; ++i) {
-        const Tile tl = win.at(i);
-        const int row = job == 2 ? tl.t0 + static_cast<int>(rank) * (tl.n / 2)
-                                 : tl.w0 + static_cast<int>(rank) * 128 + job * (SW ? p.swiglu_up : 256);
-        const int sf_row = job == 2 ? tl.srow / 128 : tl.g * p.w_blocks + row / 128;
-        for (int kb = 0; kb < p.num_k_blocks; ++kb) {
-          if (!warp_wait_cta(empty_bar(s), ph ^ 1u, p.timeout_ns)) {
-            if (lane == 0) record_fault(p.err, kFaultTimeout, kRoleProducer, kBarEmpty, s, ph ^ 1u);
-            aborted = true;
-            break;
-          }
-          if (elect_one()) {
-            const uint32_t st = base + static_cast<uint32_t>(s) * L::kStage;
-            const uint32_t fb = mapa_shared(full_bar(s), 0);
-            if (job == 2) {
-              tma_load_2d_pair(st + L::kStageW, &p.map_a, fb, kb * kKBytes, row);
-              // both CTAs need the scales of all of the instruction's N; a
-              // box of two row blocks (the second may lie past the end: zeros)
-              tma_load_3d_pair(st + L::kStageW + kTokBytes + NC * L::kSfBlock, &p.map_as, fb, 0, kb * kTilesK, sf_row);
-            } else {
-              if (job == 0 && rank == 0) mbar_arrive_expect_tx(full_bar(s), kStageTx);
-              tma_load_3d_pair(st + job * kWBytes, &p.map_w, fb, kb * kKBytes, row, tl.g);
-              tma_load_3d_pair(st + L::kStageW + kTokBytes + job * L::kSfBlock, &p.map_ws, fb, 0, kb * kTilesK, sf_row);
+      // ---- TMA producers --------------------------------------------------------
+      // One warp for each weight block and one for the activations.  A stage of
+      // two blocks takes 6 loads; one diverged thread needs about 900 clocks to
+      // issue them, more than the stage's MMAs (768).  Warps that stay together
+      // and elect a lane need about 50 clocks a load, and three share them.
+      const int job = warp == 0 ? 0 : static_cast<int>(warp) - 1;  // 0, 1: weight block, 2: activations
+      if (job == 2 || job < NC) {
+        int s = 0;
+        uint32_t ph = 0;
+        TileWindow<kWRows> win(p, tb, first, stride, total);
+        for (int i = 0; win.have(i) && !aborted; ++i) {
+          const Tile tl = win.at(i);
+          const int row = job == 2 ? tl.t0 + static_cast<int>(rank) * (tl.n / 2)
+                                   : tl.w0 + static_cast<int>(rank) * 128 + job * (SW ? p.swiglu_up : 256);
+          const int sf_row = job == 2 ? tl.srow / 128 : tl.g * p.w_blocks + row / 128;
+          for (int kb = 0; kb < p.num_k_blocks; ++kb) {
+            if (!warp_wait_cta(empty_bar(s), ph ^ 1u, p.timeout_ns)) {
+              if (lane == 0) record_fault(p.err, kFaultTimeout, kRoleProducer, kBarEmpty, s, ph ^ 1u);
+              aborted = true;
+              break;
             }
-          }
-          __syncwarp();
-          if (++s == S) {
-            s = 0;
-            ph ^= 1u;
+            if (elect_one()) {
+              const uint32_t st = base + static_cast<uint32_t>(s) * L::kStage;
+              const uint32_t fb = mapa_shared(full_bar(s), 0);
+              if (job == 2) {
+                tma_load_2d_pair(st + L::kStageW, &p.map_a, fb, kb * kKBytes, row);
+                // both CTAs need the scales of all of the instruction's N; a
+                // box of two row blocks (the second may lie past the end: zeros)
+                tma_load_3d_pair(st + L::kStageW + kTokBytes + NC * L::kSfBlock, &p.map_as, fb, 0, kb * kTilesK, sf_row);
+              } else {
+                if (job == 0 && rank == 0) mbar_arrive_expect_tx(full_bar(s), kStageTx);
+                tma_load_3d_pair(st + job * kWBytes, &p.map_w, fb, kb * kKBytes, row, tl.g);
+                tma_load_3d_pair(st + L::kStageW + kTokBytes + job * L::kSfBlock, &p.map_ws, fb, 0, kb * kTilesK, sf_row);
+              }
+            }
+            __syncwarp();
+            if (++s == S) {
+              s = 0;
+              ph ^= 1u;
+            }
           }
         }
       }
-    }
     } else {
-    // ---- MMA issuer (CTA 0 of the pair) ------------------------------------
-    // A stage is 10 to 24 tcgen05 instructions, and their issue, not the
-    // tensor cores, can set the pace.  So the operands are kept uniform (the
-    // ring unrolled, tile values through a warp reduction, TMEM addresses
-    // constant: all 512 columns are allocated, so they start at 0; the
-    // operations predicated instead of issued in a branch), and a stage's
-    // full barrier is asked before the stage before it is issued.
-    if (rank == 0) {
-      int s = 0, acc = 0;
-      uint32_t ph = 0, acc_ph = 0;
-      bool ready = false;
-      TileWindow<kWRows> win(p, tb, first, stride, total);
-      for (int i = 0; win.have(i) && !aborted; ++i) {
-        const uint32_t packed = win.mma_values(i);
-        const uint32_t shift = packed & 3u;
-        const uint32_t idesc0 = make_idesc_fp4(FMT, 256, packed >> 2, 0);
-        for (int a = 0; a < NC; ++a) {
-          const int slot = NC == 1 ? acc : a;
-          if (!warp_wait_all(acc_empty(slot), acc_ph ^ 1u, p.timeout_ns)) {
-            if (lane == 0) record_fault(p.err, kFaultTimeout, kRoleMma, kBarAccEmpty, slot, acc_ph ^ 1u);
-            aborted = true;
-          }
-        }
-        if (aborted) break;
-        tc_fence_after();
-        int kb = 0;
-        // one k-block, in stage st; returns false after the tile's last
-        auto k_block = [&](auto stage_c) {
-          constexpr int st = decltype(stage_c)::value;
-          if (!ready && !warp_wait_cta(full_bar(st), ph, p.timeout_ns)) {
-            if (lane == 0) record_fault(p.err, kFaultTimeout, kRoleMma, kBarFull, st, ph);
-            aborted = true;
-            return false;
-          }
-          tc_fence_after();
-          constexpr int next = st + 1 == S ? 0 : st + 1;
-          const bool ask = mbar_test_wait_cta(full_bar(next), next == 0 ? ph ^ 1u : ph);
-          uint32_t mem = base + static_cast<uint32_t>(st) * L::kStage;
-          asm volatile("" : "+r"(mem));
-          const uint32_t sf = mem + L::kStageW + kTokBytes;
-          const int steps = kb + 1 == p.num_k_blocks ? p.last_steps : 4;
-          const bool on = elect_one();
-          // scales: block c's tile j to columns (c * kTilesK + j) * 4, the
-          // activations' two row blocks of tile j side by side
-#pragma unroll
-          for (int j = 0; j < kTilesK; ++j) {
-#pragma unroll
-            for (int c = 0; c < NC; ++c)
-              tmem_copy_scales_if<2>(on, kSfCol0 + (c * kTilesK + j) * 4,
-                                    make_smem_desc(sf + c * L::kSfBlock + j * kScaleTileBytes, 16, 128, kSwizzleNone));
-            const uint32_t sfb = sf + NC * L::kSfBlock + j * kScaleTileBytes;
-            constexpr uint32_t kSfb = kSfCol0 + NC * kTilesK * 4;
-            tmem_copy_scales_if<2>(on, kSfb + 8 * j, make_smem_desc(sfb, 16, 128, kSwizzleNone));
-            tmem_copy_scales_if<2>(on, kSfb + 8 * j + 4, make_smem_desc(sfb + kSfBytes, 16, 128, kSwizzleNone));
-          }
-          const uint64_t b_desc = make_smem_desc(mem + L::kStageW, 16, 1024, kSwizzle128B);
-#pragma unroll
-          for (int kk = 0; kk < 4; ++kk) {
-            const int j = FMT == kNvfp4 ? kk : kk / 2;
-            const uint32_t idesc = FMT == kNvfp4 ? idesc0
-                                                 : (idesc0 | (static_cast<uint32_t>(kk & 1) << 5) |
-                                                    (static_cast<uint32_t>(kk & 1) << 30));
-#pragma unroll
-            for (int c = 0; c < NC; ++c) {
-              const uint64_t a_desc = make_smem_desc(mem + static_cast<uint32_t>(c) * kWBytes, 16, 1024, kSwizzle128B);
-              mma_fp4_if<2, kVec>(on && kk < steps, static_cast<uint32_t>(NC == 1 ? acc : c) * kAccCols, a_desc + kk * 2,
-                                 b_desc + kk * 2, idesc, kSfCol0 + (c * kTilesK + j) * 4,
-                                 kSfCol0 + (NC * kTilesK + 2 * j) * 4 + shift, (kb | kk) != 0 ? 1u : 0u);
+      // ---- MMA issuer (CTA 0 of the pair) ------------------------------------
+      // A stage is 10 to 24 tcgen05 instructions, and their issue, not the
+      // tensor cores, can set the pace.  So the operands are kept uniform (the
+      // ring unrolled, tile values through a warp reduction, TMEM addresses
+      // constant: all 512 columns are allocated, so they start at 0; the
+      // operations predicated instead of issued in a branch), and a stage's
+      // full barrier is asked before the stage before it is issued.
+      if (rank == 0) {
+        int s = 0, acc = 0;
+        uint32_t ph = 0, acc_ph = 0;
+        bool ready = false;
+        TileWindow<kWRows> win(p, tb, first, stride, total);
+        for (int i = 0; win.have(i) && !aborted; ++i) {
+          const uint32_t packed = win.mma_values(i);
+          const uint32_t shift = packed & 3u;
+          const uint32_t idesc0 = make_idesc_fp4(FMT, 256, packed >> 2, 0);
+          for (int a = 0; a < NC; ++a) {
+            const int slot = NC == 1 ? acc : a;
+            if (!warp_wait_all(acc_empty(slot), acc_ph ^ 1u, p.timeout_ns)) {
+              if (lane == 0) record_fault(p.err, kFaultTimeout, kRoleMma, kBarAccEmpty, slot, acc_ph ^ 1u);
+              aborted = true;
             }
           }
-          mma_commit_pair_mc_if(on, empty_bar(st), 0x3);
-          ready = __all_sync(0xffffffffu, ask);
-          s = next;
-          if (next == 0) ph ^= 1u;
-          return ++kb < p.num_k_blocks;
-        };
-        while (true) {
-          if (s == 0 && !k_block(std::integral_constant<int, 0>{})) break;
-          if (s == 1 && !k_block(std::integral_constant<int, 1>{})) break;
-          if (s == 2 && !k_block(std::integral_constant<int, 2>{})) break;
-          if (s == 3 && !k_block(std::integral_constant<int, 3>{})) break;
-          if constexpr (S > 4) {
-            if (s == 4 && !k_block(std::integral_constant<int, 4>{})) break;
-            if (s == 5 && !k_block(std::integral_constant<int, 5>{})) break;
+          if (aborted) break;
+          tc_fence_after();
+          int kb = 0;
+          // one k-block, in stage st; returns false after the tile's last
+          auto k_block = [&](auto stage_c) {
+            constexpr int st = decltype(stage_c)::value;
+            if (!ready && !warp_wait_cta(full_bar(st), ph, p.timeout_ns)) {
+              if (lane == 0) record_fault(p.err, kFaultTimeout, kRoleMma, kBarFull, st, ph);
+              aborted = true;
+              return false;
+            }
+            tc_fence_after();
+            constexpr int next = st + 1 == S ? 0 : st + 1;
+            const bool ask = mbar_test_wait_cta(full_bar(next), next == 0 ? ph ^ 1u : ph);
+            uint32_t mem = base + static_cast<uint32_t>(st) * L::kStage;
+            // the stage's descriptors are computed here, not kept in registers
+            // for all stages (80 registers instead of 120, and no spills with
+            // the SwiGLU kernel's register split)
+            asm volatile("" : "+r"(mem));
+            const uint32_t sf = mem + L::kStageW + kTokBytes;
+            const int steps = kb + 1 == p.num_k_blocks ? p.last_steps : 4;
+            const bool on = elect_one();
+            // scales: block c's tile j to columns (c * kTilesK + j) * 4, the
+            // activations' two row blocks of tile j side by side
+#pragma unroll
+            for (int j = 0; j < kTilesK; ++j) {
+#pragma unroll
+              for (int c = 0; c < NC; ++c)
+                tmem_copy_scales_if<2>(on, kSfCol0 + (c * kTilesK + j) * 4,
+                                      make_smem_desc(sf + c * L::kSfBlock + j * kScaleTileBytes, 16, 128, kSwizzleNone));
+              const uint32_t sfb = sf + NC * L::kSfBlock + j * kScaleTileBytes;
+              constexpr uint32_t kSfb = kSfCol0 + NC * kTilesK * 4;
+              tmem_copy_scales_if<2>(on, kSfb + 8 * j, make_smem_desc(sfb, 16, 128, kSwizzleNone));
+              tmem_copy_scales_if<2>(on, kSfb + 8 * j + 4, make_smem_desc(sfb + kSfBytes, 16, 128, kSwizzleNone));
+            }
+            const uint64_t b_desc = make_smem_desc(mem + L::kStageW, 16, 1024, kSwizzle128B);
+#pragma unroll
+            for (int kk = 0; kk < 4; ++kk) {
+              const int j = FMT == kNvfp4 ? kk : kk / 2;
+              const uint32_t idesc = FMT == kNvfp4 ? idesc0
+                                                   : (idesc0 | (static_cast<uint32_t>(kk & 1) << 5) |
+                                                      (static_cast<uint32_t>(kk & 1) << 30));
+#pragma unroll
+              for (int c = 0; c < NC; ++c) {
+                const uint64_t a_desc = make_smem_desc(mem + static_cast<uint32_t>(c) * kWBytes, 16, 1024, kSwizzle128B);
+                mma_fp4_if<2, kVec>(on && kk < steps, static_cast<uint32_t>(NC == 1 ? acc : c) * kAccCols, a_desc + kk * 2,
+                                   b_desc + kk * 2, idesc, kSfCol0 + (c * kTilesK + j) * 4,
+                                   kSfCol0 + (NC * kTilesK + 2 * j) * 4 + shift, (kb | kk) != 0 ? 1u : 0u);
+              }
+            }
+            mma_commit_pair_mc_if(on, empty_bar(st), 0x3);
+            ready = __all_sync(0xffffffffu, ask);
+            s = next;
+            if (next == 0) ph ^= 1u;
+            return ++kb < p.num_k_blocks;
+          };
+          while (true) {
+            if (s == 0 && !k_block(std::integral_constant<int, 0>{})) break;
+            if (s == 1 && !k_block(std::integral_constant<int, 1>{})) break;
+            if (s == 2 && !k_block(std::integral_constant<int, 2>{})) break;
+            if (s == 3 && !k_block(std::integral_constant<int, 3>{})) break;
+            if constexpr (S > 4) {
+              if (s == 4 && !k_block(std::integral_constant<int, 4>{})) break;
+              if (s == 5 && !k_block(std::integral_constant<int, 5>{})) break;
+            }
+          }
+          if (aborted) break;
+          const bool on = elect_one();
+          mma_commit_pair_mc_if(on, acc_full(NC == 1 ? acc : 0), 0x3);
+          if (NC == 2) mma_commit_pair_mc_if(on, acc_full(1), 0x3);
+          if constexpr (NC == 1) {
+            acc ^= 1;
+            if (acc == 0) acc_ph ^= 1u;
+          } else {
+            acc_ph ^= 1u;
           }
         }
-        if (aborted) break;
-        const bool on = elect_one();
-        mma_commit_pair_mc_if(on, acc_full(NC == 1 ? acc : 0), 0x3);
-        if (NC == 2) mma_commit_pair_mc_if(on, acc_full(1), 0x3);
-        if constexpr (NC == 1) {
-          acc ^= 1;
-          if (acc == 0) acc_ph ^= 1u;
-        } else {
-          acc_ph ^= 1u;
-        }
       }
-    }
     }
     __syncwarp();
   } else {
@@ -932,8 +934,8 @@ bwg_status pair_clusters(PairKernel k, int nc, const Runtime& rt, int* clusters)
     cudaGetLastError();
     return BWG_ERR_CUDA;
   }
-  // the SwiGLU kernel's register split only completes if the CTA was launched
-  // with at least the registers that it hands out
+  // the register split only completes if the CTA was launched with at least the
+  // registers that it hands out
   if (nc == 2 && static_cast<uint32_t>(fa.numRegs) * threads_of(2) < kRegsControl * 128u + kRegsEpilogue * 256u)
     return BWG_ERR_UNSUPPORTED;
   int n = 0;

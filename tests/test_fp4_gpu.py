@@ -255,6 +255,19 @@ def test_gemm_within_bound(ops, M, N, K, fmt, out_dtype):
 
 
 @pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("M,N,K", [(2000, 5000, 8192), (1500, 2600, 8000)])
+def test_many_tiles_are_exact(ops, M, N, K, fmt):
+    """Several tiles a CTA pair and many k-blocks: scales and operands of one
+    stage are overwritten by the next while the tensor cores run."""
+    rng = np.random.default_rng(M)
+    a, A = random_fp4(ops, M, K, fmt, rng, integers=True)
+    b, B = random_fp4(ops, N, K, fmt, rng, integers=True)
+    want = dev(A) @ dev(B).t()  # in 64 bits
+    for _ in range(5):
+        assert torch.equal(ops.gemm_fp4(a, b, out_dtype=torch.float32).double(), want)
+
+
+@pytest.mark.parametrize("fmt", FMTS)
 def test_gemm_into_a_wider_matrix(ops, fmt):
     rng = np.random.default_rng(8)
     M, N, K = 200, 300, 192
