@@ -22,6 +22,7 @@
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
+#include <mutex>
 
 #include "../../include/bwgemm.h"
 #include "params.h"
@@ -54,11 +55,11 @@ __device__ __forceinline__ void record_bad_position(unsigned long long* err) {
 // pair order.
 // What bounds it: latency.  The ids are 0.3 MB for the 4096 x 8 layer; one
 // launch with its counts on chip replaces three passes through global memory.
-// 32768 ids of 32 experts: 8.2 us, 11.6 with match.any and with sums over the
+// 32768 ids of 32 experts: 6.4 us; with 8 CTAs 8.1, and 11.6 with match.any and with sums over the
 // warps' counts and the CTAs' totals that wait for one load after the other.
 constexpr int kSortMaxWarps = 32;
 constexpr int kSortAhead = 4;    // id loads in flight per lane
-constexpr int kSortCtas = 8;     // of the cluster
+constexpr int kSortCtas = 16;    // of the cluster, where the device has room for it; else 8
 
 template <class ID>
 __global__ void __launch_bounds__(kSortMaxWarps * 32)
@@ -148,7 +149,7 @@ __global__ void __launch_bounds__(kSortMaxWarps * 32)
       if (n_cta > 1) {
         int v[kSortCtas];
 #pragma unroll
-        for (int c = 0; c < kSortCtas; ++c) v[c] = ld_cluster(total + b, static_cast<uint32_t>(c));
+        for (int c = 0; c < kSortCtas; ++c) v[c] = c < n_cta ? ld_cluster(total + b, static_cast<uint32_t>(c)) : 0;
 #pragma unroll
         for (int c = 0; c < kSortCtas; ++c) {
           if (c < static_cast<int>(rank)) before += v[c];
@@ -289,7 +290,7 @@ __global__ void __launch_bounds__(256) moe_dispatch_kernel(const __grid_constant
 }
 
 // Loads in flight decide how near these two kernels come to the memory's rate,
-// so a thread takes P pairs (k rounded up to 1, 2, 4 or 8; more in turns) of V
+// so a thread takes P pairs (k, 5 as 6 and 7 as 8; more in turns of 8) of V
 // vectors and issues all P * V loads before it uses the first.  Measured for
 // 4096 tokens x 8 experts, H = 4096 BF16: the combine 46.9 us (6.4 TB/s) with 8
 // loads of 16 bytes a thread and 128 threads a block, 60 with 16 loads, 47.7
@@ -498,15 +499,14 @@ cudaError_t launch_grad_as(const MoeRows& p, cudaStream_t s) {
 
 template <class T, int VB>
 cudaError_t launch_pairs(bool grad, const MoeRows& p, cudaStream_t s) {
-  if (grad)
-    return p.k > 4   ? launch_grad_as<T, VB, 8>(p, s)
-           : p.k > 2 ? launch_grad_as<T, VB, 4>(p, s)
-           : p.k > 1 ? launch_grad_as<T, VB, 2>(p, s)
-                     : launch_grad_as<T, VB, 1>(p, s);
-  return p.k > 4   ? launch_combine_as<T, VB, 8>(p, s)
-         : p.k > 2 ? launch_combine_as<T, VB, 4>(p, s)
-         : p.k > 1 ? launch_combine_as<T, VB, 2>(p, s)
-                   : launch_combine_as<T, VB, 1>(p, s);
+  switch (p.k > 6 ? 8 : p.k > 4 ? 6 : p.k) {
+    case 1: return grad ? launch_grad_as<T, VB, 1>(p, s) : launch_combine_as<T, VB, 1>(p, s);
+    case 2: return grad ? launch_grad_as<T, VB, 2>(p, s) : launch_combine_as<T, VB, 2>(p, s);
+    case 3: return grad ? launch_grad_as<T, VB, 3>(p, s) : launch_combine_as<T, VB, 3>(p, s);
+    case 4: return grad ? launch_grad_as<T, VB, 4>(p, s) : launch_combine_as<T, VB, 4>(p, s);
+    case 6: return grad ? launch_grad_as<T, VB, 6>(p, s) : launch_combine_as<T, VB, 6>(p, s);
+    default: return grad ? launch_grad_as<T, VB, 8>(p, s) : launch_combine_as<T, VB, 8>(p, s);
+  }
 }
 
 template <class T>
@@ -550,22 +550,60 @@ bwg_status run_combine(const void* rows, int dtype, int T, int H, int ldr, int k
   return runtime_status(launch_weighted(false, p, dtype, vb, s));
 }
 
+size_t sort_smem(int warps, int E) { return (static_cast<size_t>(warps + 2) * (E + 1) + 32) * sizeof(int); }
+
+// CTAs of the sort's cluster on this device: 16 (beyond the portable size) if
+// one such cluster fits with the most shared memory a call takes, else 8.
 template <class ID>
-cudaError_t launch_sort(const void* ids, int pairs, int E, int* offsets, int* order, int* position, cudaStream_t s) {
-  // One CTA up to 2048 pairs (256 experts: 5.6 us), a warp for each 128 of
-  // them; a cluster of 8 beyond (8192 pairs: 6.2 us, one CTA 4096 in 7.7).
-  const int n_cta = pairs <= 2048 ? 1 : kSortCtas;
-  const int warps = n_cta > 1 ? kSortMaxWarps : std::min(kSortMaxWarps, std::max(4, (pairs + 127) / 128));
-  const size_t smem = (static_cast<size_t>(warps + 2) * (E + 1) + 32) * sizeof(int);
-  if (smem > 48 * 1024) {
-    const cudaError_t a = cudaFuncSetAttribute(moe_sort_kernel<ID>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                               static_cast<int>(smem));
-    if (a != cudaSuccess) return a;
+cudaError_t sort_ctas(int device, int* n) {
+  static std::mutex mu;
+  static int known[64];
+  if (device >= 64) return cudaErrorInvalidDevice;
+  std::lock_guard<std::mutex> lock(mu);
+  if (known[device] == 0) {
+    const void* fn = reinterpret_cast<const void*>(moe_sort_kernel<ID>);
+    const size_t smem = sort_smem(kSortMaxWarps, kMaxExperts);
+    cudaError_t e =
+        cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+    if (e == cudaSuccess) e = cudaFuncSetAttribute(fn, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    if (e != cudaSuccess) return e;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(kSortCtas, 1, 1);
+    cfg.blockDim = dim3(kSortMaxWarps * 32, 1, 1);
+    cfg.dynamicSmemBytes = smem;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = kSortCtas;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    int clusters = 0;
+    if (cudaOccupancyMaxActiveClusters(&clusters, fn, &cfg) != cudaSuccess) {
+      cudaGetLastError();
+      clusters = 0;
+    }
+    known[device] = clusters > 0 ? kSortCtas : 8;
   }
+  *n = known[device];
+  return cudaSuccess;
+}
+
+template <class ID>
+cudaError_t launch_sort(const void* ids, int pairs, int E, int* offsets, int* order, int* position, int device,
+                        cudaStream_t s) {
+  // One CTA up to 2048 pairs (256 experts: 5.6 us), a warp for each 128 of
+  // them; a cluster beyond (8192 pairs with 8 CTAs: 6.2 us, one CTA takes 7.7
+  // for 4096; 32768 pairs with 16 CTAs 6.4 us, with 8 8.1).
+  int n_cta = 1;
+  const cudaError_t known = sort_ctas<ID>(device, &n_cta);
+  if (known != cudaSuccess) return known;
+  if (pairs <= 2048) n_cta = 1;
+  const int warps = n_cta > 1 ? kSortMaxWarps : std::min(kSortMaxWarps, std::max(4, (pairs + 127) / 128));
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(n_cta), 1, 1);
   cfg.blockDim = dim3(static_cast<unsigned>(warps * 32), 1, 1);
-  cfg.dynamicSmemBytes = smem;
+  cfg.dynamicSmemBytes = sort_smem(warps, E);
   cfg.stream = s;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -595,8 +633,8 @@ bwg_status moe_sort(const void* expert_ids, int id_bytes, int pairs, int E, int*
   const bwg_status st = runtime_device(&rt);
   if (st != BWG_OK) return st;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  return runtime_status(id_bytes == 8 ? launch_sort<long long>(expert_ids, pairs, E, offsets, order, position, s)
-                                      : launch_sort<int>(expert_ids, pairs, E, offsets, order, position, s));
+  return runtime_status(id_bytes == 8 ? launch_sort<long long>(expert_ids, pairs, E, offsets, order, position, rt.device, s)
+                                      : launch_sort<int>(expert_ids, pairs, E, offsets, order, position, rt.device, s));
 }
 
 bwg_status moe_dispatch(const void* X, int dtype, int T, int H, int ldx, int k, const int* position,
