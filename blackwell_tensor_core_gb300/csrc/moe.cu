@@ -262,6 +262,21 @@ constexpr int dispatch_vectors() {
   return VB == 16 ? 1 : VB == 4 ? 4 : 8;
 }
 
+// Vectors of 4 bytes: the threads of a warp take those that fill one aligned
+// line of 128 bytes of the row they store to, whatever its start, so that no
+// store splits a sector with another warp's (2049 x 8 rows of 2047 FP32: 29.0 us,
+// 32.1 without; with 2 bytes, or in the combine's gradient, whose vectors of dy
+// would then be read once a pair, it costs more than it gives).  Vectors to
+// skip at row `dst`.
+template <int VB>
+__device__ __forceinline__ int line_skew(const void* dst) {
+  return VB == 4 ? static_cast<int>((reinterpret_cast<uintptr_t>(dst) & 127u) / VB) : 0;
+}
+template <int VB>
+constexpr int most_skew() {
+  return VB == 4 ? 128 / VB - 1 : 0;
+}
+
 template <int VB>
 __global__ void __launch_bounds__(256) moe_dispatch_kernel(const __grid_constant__ MoeRows p, int chunks, int elt) {
   using R = typename Raw<VB>::type;
@@ -271,9 +286,11 @@ __global__ void __launch_bounds__(256) moe_dispatch_kernel(const __grid_constant
   const int v0 = static_cast<int>(blockIdx.x % static_cast<unsigned>(chunks)) * step * V + static_cast<int>(threadIdx.x);
   const R* src = reinterpret_cast<const R*>(static_cast<const char*>(p.src) + t * p.ld_src * elt);
   R x[V];
+  if constexpr (VB != 4) {
 #pragma unroll
-  for (int m = 0; m < V; ++m)
-    if (v0 + m * step < p.vecs) x[m] = __ldg(src + v0 + m * step);
+    for (int m = 0; m < V; ++m)
+      if (v0 + m * step < p.vecs) x[m] = __ldg(src + v0 + m * step);
+  }
   const int kept = *p.kept;
   const int* pos = p.position + static_cast<long long>(t) * p.k;
   for (int j = 0; j < p.k; ++j) {
@@ -283,9 +300,15 @@ __global__ void __launch_bounds__(256) moe_dispatch_kernel(const __grid_constant
       continue;
     }
     R* dst = reinterpret_cast<R*>(static_cast<char*>(p.dst) + r * p.ld_dst * elt);
+    const int v = v0 - line_skew<VB>(dst);
+    if constexpr (VB == 4) {
+#pragma unroll
+      for (int m = 0; m < V; ++m)
+        if (static_cast<unsigned>(v + m * step) < static_cast<unsigned>(p.vecs)) x[m] = __ldg(src + v + m * step);
+    }
 #pragma unroll
     for (int m = 0; m < V; ++m)
-      if (v0 + m * step < p.vecs) dst[v0 + m * step] = r < kept ? x[m] : R{};
+      if (static_cast<unsigned>(v + m * step) < static_cast<unsigned>(p.vecs)) dst[v + m * step] = r < kept ? x[m] : R{};
   }
 }
 
@@ -294,7 +317,7 @@ __global__ void __launch_bounds__(256) moe_dispatch_kernel(const __grid_constant
 // vectors and issues all P * V loads before it uses the first.  Measured for
 // 4096 tokens x 8 experts, H = 4096 BF16: the combine 46.9 us (6.4 TB/s) with 8
 // loads of 16 bytes a thread and 128 threads a block, 60 with 16 loads, 47.7
-// with 256 threads; the gradient 87.2 us (6.5 TB/s) with 16 loads, 90.7 with 8,
+// with 256 threads; the gradient 87.0 us (6.6 TB/s) with 16 loads, 90.7 with 8,
 // 92.3 with 256 threads.  Narrower vectors: 32 loads for the combine (2049 x 8
 // rows of 2047 FP32: 26 us, 30 with 16), 16 for the gradient (51.4, 52.2 with
 // 32).  Checks of the positions between the loads cost the combine 15 us.
@@ -393,37 +416,43 @@ __global__ void __launch_bounds__(kRowThreads) moe_combine_grad_kernel(const __g
       dot[a] = 0.f;
     }
     if (bad && threadIdx.x == 0) record_bad_position(p.err);
+    const R* from[P];
+    R* to[P];
+#pragma unroll
+    for (int a = 0; a < P; ++a) {
+      const int r = max(row[a], 0);
+      from[a] = reinterpret_cast<const R*>(static_cast<const T*>(p.rows_in) + r * p.ld_rows);
+      to[a] = reinterpret_cast<R*>(static_cast<T*>(p.dst) + r * p.ld_dst);
+    }
     for (int v = static_cast<int>(threadIdx.x); v < p.vecs; v += step * V) {
       Vec<T, VB> g[V], x[P][V];
+      auto in = [&](int m) { return v + m * step < p.vecs; };
 #pragma unroll
       for (int m = 0; m < V; ++m)
-        if (v + m * step < p.vecs) g[m].raw = __ldg(dy + v + m * step);
+        if (in(m)) g[m].raw = __ldg(dy + v + m * step);
 #pragma unroll
       for (int a = 0; a < P; ++a)
-        if (row[a] >= 0 && row[a] < kept) {
-          const R* src = reinterpret_cast<const R*>(static_cast<const T*>(p.rows_in) + row[a] * p.ld_rows);
 #pragma unroll
-          for (int m = 0; m < V; ++m)
-            if (v + m * step < p.vecs) x[a][m].raw = __ldg(src + v + m * step);
-        }
+        for (int m = 0; m < V; ++m)
+          if (row[a] >= 0 && row[a] < kept && in(m)) x[a][m].raw = __ldg(from[a] + v + m * step);
 #pragma unroll
       for (int a = 0; a < P; ++a) {
         if (row[a] < 0) continue;
-        R* dst = reinterpret_cast<R*>(static_cast<T*>(p.dst) + row[a] * p.ld_dst);
 #pragma unroll
         for (int m = 0; m < V; ++m) {
-          if (v + m * step >= p.vecs) continue;
+          if (!in(m)) continue;
           Vec<T, VB> d;
           if (row[a] < kept) {
 #pragma unroll
             for (int i = 0; i < N; ++i) {
-              dot[a] = fmaf(to_f32(x[a][m].e[i]), to_f32(g[m].e[i]), dot[a]);
-              from_f32(d.e[i], w[a] * to_f32(g[m].e[i]));
+              const float y = to_f32(g[m].e[i]);
+              dot[a] = fmaf(to_f32(x[a][m].e[i]), y, dot[a]);
+              from_f32(d.e[i], w[a] * y);
             }
           } else {
             d.raw = R{};
           }
-          dst[v + m * step] = d.raw;
+          to[a][v + m * step] = d.raw;
         }
       }
     }
@@ -661,8 +690,9 @@ bwg_status moe_dispatch(const void* X, int dtype, int T, int H, int ldx, int k, 
   p.err = rt.err;
   p.vecs = static_cast<int>(static_cast<long long>(H) * elt / vb);
   int threads, chunks;
-  row_shape(p.vecs, vb == 16 ? dispatch_vectors<16>() : vb == 4 ? dispatch_vectors<4>() : dispatch_vectors<2>(), 256,
-            &threads, &chunks);
+  row_shape(p.vecs + (vb == 4 ? most_skew<4>() : 0),
+            vb == 16 ? dispatch_vectors<16>() : vb == 4 ? dispatch_vectors<4>() : dispatch_vectors<2>(), 256, &threads,
+            &chunks);
   const long long blocks = static_cast<long long>(T) * chunks;
   if (blocks > 0x7fffffffLL) return BWG_ERR_UNSUPPORTED;
   const unsigned b = static_cast<unsigned>(blocks);
