@@ -176,6 +176,15 @@ def _stream_handle(stream, device) -> int:
     return int(stream.cuda_stream)
 
 
+def _new(shape, dtype, dev, stream) -> torch.Tensor:
+    """A tensor for the kernels on `stream`, taken from that stream's memory:
+    what the allocator hands out may still be in use on the current one."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=dev)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=dev)
+
+
 def _matrix(t: torch.Tensor, name: str) -> int:
     if t.dim() != 2:
         raise ValueError("%s must be 2-D" % name)
@@ -426,9 +435,9 @@ def moe_sort(expert_ids: torch.Tensor, num_experts: int, stream=None) -> Routing
         raise ValueError("num_experts must be at least 1")
     dev = expert_ids.device
     pairs = expert_ids.numel()
-    offsets = torch.empty(num_experts + 1, dtype=torch.int32, device=dev)
-    order = torch.empty(pairs, dtype=torch.int32, device=dev)
-    position = torch.empty(expert_ids.shape, dtype=torch.int32, device=dev)
+    offsets = _new((num_experts + 1,), torch.int32, dev, stream)
+    order = _new((pairs,), torch.int32, dev, stream)
+    position = _new(expert_ids.shape, torch.int32, dev, stream)
     _check(lib().moe_sort(expert_ids.data_ptr(), expert_ids.element_size(), pairs, num_experts, offsets.data_ptr(),
                           order.data_ptr(), position.data_ptr(), _stream_handle(stream, dev)), "moe_sort")
     return Routing(offsets, order, position)
@@ -465,13 +474,13 @@ def _rows(t: torch.Tensor, name: str, rows: int) -> int:
     return cols  # torch gives a single row any stride
 
 
-def _out_rows(out, rows: int, cols: int, dtype, dev, name: str = "out") -> tuple:
+def _out_rows(out, rows: int, cols: int, dtype, dev, stream) -> tuple:
     """(output matrix, leading dimension): a new one, or the caller's checked."""
     if out is None:
-        return torch.empty((rows, cols), dtype=dtype, device=dev), cols
+        return _new((rows, cols), dtype, dev, stream), cols
     if out.shape != (rows, cols) or out.dtype is not dtype or out.device != dev:
-        raise ValueError("%s must be a [%d, %d] %s tensor on %s" % (name, rows, cols, dtype, dev))
-    return out, _rows(out, name, rows)
+        raise ValueError("out must be a [%d, %d] %s tensor on %s" % (rows, cols, dtype, dev))
+    return out, _rows(out, "out", rows)
 
 
 def _pair_weights(w: torch.Tensor, T: int, k: int, dev) -> None:
@@ -485,7 +494,7 @@ def moe_dispatch(x: torch.Tensor, routing: Routing, out: torch.Tensor | None = N
     T, k, E = _routing(routing, x.device)
     ldx = _rows(x, "x", T)
     H, dtype, dev = x.shape[1], x.dtype, x.device
-    out, ldo = _out_rows(out, T * k, H, dtype, dev)
+    out, ldo = _out_rows(out, T * k, H, dtype, dev, stream)
     _check(lib().moe_dispatch(x.data_ptr(), _OUT_CODES[dtype], T, H, ldx, k, routing.position.data_ptr(),
                               routing.offsets.data_ptr(), E, out.data_ptr(), ldo, _stream_handle(stream, dev)),
            "moe_dispatch")
@@ -498,7 +507,7 @@ def moe_dispatch_grad(d_rows: torch.Tensor, routing: Routing, out: torch.Tensor 
     T, k, E = _routing(routing, d_rows.device)
     ldr = _rows(d_rows, "d_rows", T * k)
     H, dtype, dev = d_rows.shape[1], d_rows.dtype, d_rows.device
-    out, ldo = _out_rows(out, T, H, dtype, dev)
+    out, ldo = _out_rows(out, T, H, dtype, dev, stream)
     _check(lib().moe_dispatch_grad(d_rows.data_ptr(), _OUT_CODES[dtype], T, H, ldr, k, routing.position.data_ptr(),
                                    routing.offsets.data_ptr(), E, out.data_ptr(), ldo, _stream_handle(stream, dev)),
            "moe_dispatch_grad")
@@ -513,7 +522,7 @@ def moe_combine(rows: torch.Tensor, routing: Routing, weights: torch.Tensor, out
     ldr = _rows(rows, "rows", T * k)
     H, dtype, dev = rows.shape[1], rows.dtype, rows.device
     _pair_weights(weights, T, k, dev)
-    out, ldo = _out_rows(out, T, H, dtype, dev)
+    out, ldo = _out_rows(out, T, H, dtype, dev, stream)
     _check(lib().moe_combine(rows.data_ptr(), _OUT_CODES[dtype], T, H, ldr, k, weights.data_ptr(),
                              routing.position.data_ptr(), routing.offsets.data_ptr(), E, out.data_ptr(), ldo,
                              _stream_handle(stream, dev)), "moe_combine")
@@ -528,8 +537,8 @@ def moe_combine_grad(d_out: torch.Tensor, rows: torch.Tensor, routing: Routing, 
     if d_out.dtype != rows.dtype or d_out.shape[1] != rows.shape[1] or d_out.device != rows.device:
         raise ValueError("d_out must have the dtype, columns and device of rows")
     _pair_weights(weights, T, k, rows.device)
-    d_rows = torch.empty((T * k, rows.shape[1]), dtype=rows.dtype, device=rows.device)
-    d_weights = torch.empty((T, k), dtype=torch.float32, device=rows.device)
+    d_rows = _new((T * k, rows.shape[1]), rows.dtype, rows.device, stream)
+    d_weights = _new((T, k), torch.float32, rows.device, stream)
     _check(lib().moe_combine_grad(d_out.data_ptr(), rows.data_ptr(), _OUT_CODES[rows.dtype], T, rows.shape[1], ldy,
                                   ldr, k, weights.data_ptr(), routing.position.data_ptr(),
                                   routing.offsets.data_ptr(), E, d_rows.data_ptr(), rows.shape[1],
@@ -648,8 +657,8 @@ def quantize_fp4(x: torch.Tensor, format: str = "nvfp4", global_scale: torch.Ten
         raise ValueError("%d rows do not make %d equal groups" % (rows, groups))
     g, n_global = _fp4_global(global_scale, fmt, groups, dev)
     L = lib()
-    codes = torch.empty((rows, K // 2), dtype=torch.uint8, device=dev)
-    scales = torch.empty(_fp4_scale_bytes(rows, K, fmt, groups, off is not None), dtype=torch.uint8, device=dev)
+    codes = _new((rows, K // 2), torch.uint8, dev, stream)
+    scales = _new((_fp4_scale_bytes(rows, K, fmt, groups, off is not None),), torch.uint8, dev, stream)
     _check(L.quantize_fp4(x.data_ptr(), _OUT_CODES[x.dtype], rows, K, ldx, fmt, g, n_global, off, groups,
                           codes.data_ptr(), scales.data_ptr(), _stream_handle(stream, dev)), "quantize_fp4")
     return Fp4Matrix(codes, scales, format, global_scale, group_offsets, groups)
@@ -663,7 +672,7 @@ def dequantize_fp4(q: Fp4Matrix, out_dtype: torch.dtype = torch.bfloat16, out: t
     rows, K = q.shape
     off = _fp4_offsets(q.group_offsets, dev)
     g, n_global = _fp4_global(q.global_scale, fmt, q.groups, dev)
-    out, ldo = _fp4_out(out, out_dtype, rows, K, dev)
+    out, ldo = _fp4_out(out, out_dtype, rows, K, dev, stream)
     _check(lib().dequantize_fp4(q.codes.data_ptr(), q.scales.data_ptr(), fmt, g, n_global, off, q.groups,
                                 out.data_ptr(), _OUT_CODES[out.dtype], rows, K, ldo,
                                 _stream_handle(stream, dev)), "dequantize_fp4")
@@ -681,12 +690,12 @@ def _fp4_pair(A: Fp4Matrix, B: Fp4Matrix) -> int:
     return fmt
 
 
-def _fp4_out(out, out_dtype, M: int, N: int, dev) -> tuple:
+def _fp4_out(out, out_dtype, M: int, N: int, dev, stream) -> tuple:
     if out is not None:
         out_dtype = out.dtype
     if out_dtype not in _OUT_CODES:
         raise TypeError("output dtype must be bfloat16, float16 or float32")
-    return _out_rows(out, M, N, out_dtype, dev)
+    return _out_rows(out, M, N, out_dtype, dev, stream)
 
 
 def gemm_fp4(A: Fp4Matrix, B: Fp4Matrix, out: torch.Tensor | None = None,
@@ -698,7 +707,7 @@ def gemm_fp4(A: Fp4Matrix, B: Fp4Matrix, out: torch.Tensor | None = None,
     dev = A.codes.device
     M, K = A.shape
     N = B.codes.shape[0]
-    out, ldo = _fp4_out(out, out_dtype, M, N, dev)
+    out, ldo = _fp4_out(out, out_dtype, M, N, dev, stream)
     ga, _ = _fp4_global(A.global_scale, fmt, 1, dev)
     gb, _ = _fp4_global(B.global_scale, fmt, 1, dev)
     _check(lib().gemm_fp4(A.codes.data_ptr(), A.scales.data_ptr(), ga, B.codes.data_ptr(), B.scales.data_ptr(), gb,
@@ -725,12 +734,10 @@ def grouped_gemm_fp4(A: Fp4Matrix, B: Fp4Matrix, swiglu: bool = False, out: torc
     if swiglu and N % 2:
         raise ValueError("swiglu needs an even number of weight rows, got %d" % N)
     n_out = N // 2 if swiglu else N
-    out, ldo = _fp4_out(out, out_dtype, M, n_out, dev)
+    out, ldo = _fp4_out(out, out_dtype, M, n_out, dev, stream)
     ga, na = _fp4_global(A.global_scale, fmt, 1, dev)
     gb, n_global = _fp4_global(B.global_scale, fmt, G, dev)
-    work = torch.empty((M, N), dtype=torch.float32, device=dev) if swiglu and N % 256 else None
-    if work is not None and stream is not None:
-        work.record_stream(stream)
+    work = _new((M, N), torch.float32, dev, stream) if swiglu and N % 256 else None
     _check(lib().grouped_gemm_fp4(A.codes.data_ptr(), A.scales.data_ptr(), ga, B.codes.data_ptr(),
                                   B.scales.data_ptr(), gb, n_global, fmt, out.data_ptr(), off, G, M, N, K,
                                   ldo, _OUT_CODES[out.dtype], 1 if swiglu else 0,

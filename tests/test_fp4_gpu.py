@@ -433,6 +433,59 @@ def test_products_on_a_stream_of_their_own(ops):
     assert torch.equal(got, want)
 
 
+@pytest.mark.parametrize("fmt", FMTS)
+def test_matrices_past_32_bits(ops, fmt):
+    """More than 2^31 elements to quantise, to read back and in a product."""
+    M, K = 70000, 32768
+    assert M * K > 1 << 31
+    x = torch.randn(1, K, device="cuda").bfloat16().expand(M, K).contiguous()
+    tail = torch.randn(130, K, device="cuda").bfloat16()
+    x[-130:] = tail
+    q = ops.quantize_fp4(x, fmt)
+    assert torch.equal(q.codes[-130:], ops.quantize_fp4(tail, fmt).codes)
+    assert torch.equal(q.codes[0], q.codes[-131])
+    y = ops.dequantize_fp4(q, out=x)
+    assert torch.equal(y[-130:], ops.dequantize_fp4(ops.quantize_fp4(tail, fmt)))
+    del q, x, y
+    a = ops.quantize_fp4(torch.randn(M, 64, device="cuda"), fmt)
+    b = ops.quantize_fp4(torch.randn(K, 64, device="cuda"), fmt)
+    D = ops.gemm_fp4(a, b)
+    for rows in (slice(0, 200), slice(M - 200, M)):
+        part = ops.quantize_fp4(ops.dequantize_fp4(a, torch.float32)[rows].contiguous(), fmt)
+        assert torch.equal(D[rows], ops.gemm_fp4(part, b))
+
+
+def test_captured_into_a_graph(ops):
+    """The layer's calls replayed from a CUDA graph on new inputs."""
+    T, k, E, H = 64, 2, 8, 256
+    ids = torch.randint(0, E, (T, k), device="cuda")
+    x = torch.randn(T, H, device="cuda").bfloat16()
+    w = torch.rand(T, k, device="cuda")
+    w1 = ops.quantize_fp4(torch.randn(E, 512, H, device="cuda") * 0.06, "mxfp4")
+
+    def layer():
+        r = ops.moe_sort(ids, E)
+        q = ops.quantize_fp4(ops.moe_dispatch(x, r), "mxfp4", group_offsets=r.offsets)
+        return ops.moe_combine(ops.grouped_gemm_fp4(q, w1, swiglu=True), r, w)
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        layer()
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        y = layer()
+    for seed in range(3):
+        g = torch.Generator(device="cuda").manual_seed(seed)
+        x.copy_(torch.randn(T, H, generator=g, device="cuda"))
+        ids.copy_(torch.randint(-1, E, (T, k), generator=g, device="cuda"))
+        graph.replay()
+        torch.cuda.synchronize()
+        got = y.clone()
+        assert torch.equal(got, layer())
+
+
 def test_python_refusals(ops):
     x = torch.randn(8, 64, device="cuda")
     q = ops.quantize_fp4(x)
