@@ -20,6 +20,7 @@
 
 #include "../../include/bwgemm.h"
 #include "fp4.h"
+#include "launch.h"
 #include "params.h"
 #include "ptx.cuh"
 #include "runtime.h"
@@ -364,6 +365,7 @@ __global__ void __launch_bounds__(kFp4Threads, 4) quantize_kernel(const __grid_c
   constexpr int B = FMT == kNvfp4 ? 16 : 32;
   constexpr int W = B * static_cast<int>(sizeof(T)) / 4;
   extern __shared__ int tab[];
+  grid_dependents_launch();
   const Groups t{tab, tab + p.G + 1};
   int row_blocks = p.row_blocks;
   if (p.offsets != nullptr) row_blocks = build_groups(p, t);
@@ -431,6 +433,7 @@ __global__ void __launch_bounds__(kFp4Threads) dequantize_kernel(const __grid_co
   constexpr int B = FMT == kNvfp4 ? 16 : 32;
   constexpr int W = B * static_cast<int>(sizeof(T)) / 4;
   extern __shared__ int tab[];
+  grid_dependents_launch();
   const Groups t{tab, tab + p.G + 1};
   int row_blocks = p.row_blocks;
   if (p.offsets != nullptr) row_blocks = build_groups(p, t);
@@ -605,6 +608,9 @@ bwg_status run_fp4(bool quant, const void* x, void* y, int dtype, int M, int K, 
   const long long units = static_cast<long long>(p.row_blocks) * p.chunks;
   const long long blocks = std::min<long long>(units, rt.sm_count * 8LL);
   const size_t smem = offsets != nullptr ? (2 * static_cast<size_t>(G) + 2) * sizeof(int) : 0;
+  // A plain launch: blocks that start while the work before still holds some SMs
+  // gather on the others, and these grids are a round or two of blocks only
+  // (quantise before the experts' FC1: 275 us for both so, 260 plain).
   k<<<static_cast<unsigned>(blocks), kFp4Threads, smem, s>>>(p);
   return runtime_status(cudaGetLastError());
 }

@@ -26,6 +26,7 @@
 
 #include "../../include/bwgemm.h"
 #include "fp4.h"
+#include "launch.h"
 #include "params.h"
 #include "ptx.cuh"
 #include "runtime.h"
@@ -276,10 +277,6 @@ __global__ void __launch_bounds__(threads_of(NC), 1) fp4_pair_kernel(const __gri
     }
     fence_mbarrier_init();
   }
-  if (warp == 4) {
-    const bool ok = build_tables(p, tb);
-    if (!ok && blockIdx.x == 0 && lane == 0) record_fault(p.err, kFaultBadOffsets, 0, 0, 0, 0);
-  }
   if (warp == 0 && lane == 0) {
     prefetch_tensormap(&p.map_w);
     prefetch_tensormap(&p.map_a);
@@ -289,6 +286,11 @@ __global__ void __launch_bounds__(threads_of(NC), 1) fp4_pair_kernel(const __gri
   if (warp == 1) {
     tmem_alloc<2>(tmem_slot, kTmemCols);
     tmem_relinquish<2>();
+  }
+  grid_dependency_wait();
+  if (warp == 4) {
+    const bool ok = build_tables(p, tb);
+    if (!ok && blockIdx.x == 0 && lane == 0) record_fault(p.err, kFaultBadOffsets, 0, 0, 0, 0);
   }
   tc_fence_before();
   cluster_sync_all();
@@ -592,6 +594,7 @@ __global__ void __launch_bounds__(threads_of(NC), 1) fp4_pair_kernel(const __gri
   }
 
   // ---- teardown -------------------------------------------------------------
+  grid_dependents_launch();
   if (__syncthreads_or(aborted ? 1 : 0)) {
     // a wait gave up: let copies in flight land before their memory goes
     const uint64_t t0 = globaltimer_ns();
@@ -683,6 +686,7 @@ __global__ void __launch_bounds__(kSmallThreads, 1) fp4_small_kernel(const __gri
     tmem_alloc<1>(tmem_slot, kTmemCols);  // all columns: they start at 0
     tmem_relinquish<1>();
   }
+  grid_dependency_wait();
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -823,6 +827,7 @@ __global__ void __launch_bounds__(kSmallThreads, 1) fp4_small_kernel(const __gri
   }
   __syncwarp();
 
+  grid_dependents_launch();
   if (p.split > 1) {
     // ---- partials: rank r sums rows r, r + split, .. of the tile ---------------
     cluster_sync_all();
@@ -866,6 +871,7 @@ __global__ void __launch_bounds__(kSmallThreads, 1) fp4_small_kernel(const __gri
 template <class T>
 __global__ void fp4_swiglu_kernel(const float* __restrict__ x, const int* __restrict__ last, int n_out, long long ldd,
                                   T* __restrict__ h) {
+  grid_dependency_wait();
   const int row = static_cast<int>(blockIdx.x);
   if (row >= *last) return;
   const float* r = x + static_cast<long long>(row) * 2 * n_out;
@@ -1017,14 +1023,6 @@ bwg_status run_small(const Fp4Operand& a, const Fp4Operand& b, void* D, int M, i
     int clusters[kSmallMaxSplit + 1];
   } seen[64][2];
   if (rt.device >= 64) return BWG_ERR_UNSUPPORTED;
-  cudaLaunchConfig_t cfg = {};
-  cfg.blockDim = dim3(kSmallThreads, 1, 1);
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.y = 1;
-  attr[0].val.clusterDim.z = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
   auto& info = seen[rt.device][format];
   {
     std::lock_guard<std::mutex> lock(mu);
@@ -1034,6 +1032,14 @@ bwg_status run_small(const Fp4Operand& a, const Fp4Operand& b, void* D, int M, i
         cudaGetLastError();
         return BWG_ERR_CUDA;
       }
+      cudaLaunchConfig_t cfg = {};
+      cfg.blockDim = dim3(kSmallThreads, 1, 1);
+      cudaLaunchAttribute attr[1];
+      attr[0].id = cudaLaunchAttributeClusterDimension;
+      attr[0].val.clusterDim.y = 1;
+      attr[0].val.clusterDim.z = 1;
+      cfg.attrs = attr;
+      cfg.numAttrs = 1;
       for (int f = 2; f <= kSmallMaxSplit; ++f) {
         cfg.gridDim = dim3(static_cast<unsigned>(f), 1, 1);
         cfg.dynamicSmemBytes = static_cast<size_t>(rt.max_smem);
@@ -1084,11 +1090,10 @@ bwg_status run_small(const Fp4Operand& a, const Fp4Operand& b, void* D, int M, i
   const int tail = 1024 + 8 * (2 * kSmallMaxStages + 4) + 16;
   p.stages = std::min(kSmallMaxStages, (rt.max_smem - tail) / stage);
   if (p.stages < 2) return BWG_ERR_UNSUPPORTED;
-  cfg.gridDim = dim3(static_cast<unsigned>(p.split > 1 ? p.tiles * p.split : std::min(p.tiles, rt.sm_count)), 1, 1);
-  cfg.dynamicSmemBytes = static_cast<size_t>(p.stages * stage + tail);
-  cfg.stream = stream;
-  attr[0].val.clusterDim.x = static_cast<unsigned>(p.split);
-  return runtime_status(cudaLaunchKernelEx(&cfg, k, p));
+  const int grid = p.split > 1 ? p.tiles * p.split : std::min(p.tiles, rt.sm_count);
+  return runtime_status(launch_overlapped(k, static_cast<unsigned>(grid), kSmallThreads,
+                                          static_cast<size_t>(p.stages * stage + tail), stream,
+                                          static_cast<unsigned>(p.split), p));
 }
 
 bool aligned16(const void* q) { return (reinterpret_cast<uintptr_t>(q) & 15u) == 0; }
@@ -1151,19 +1156,8 @@ bwg_status run_fp4_gemm(const Fp4Operand& a, const Fp4Operand& b, void* D, int M
   // every group adds at most one partial tile of rows
   const long long most = tok_tiles * p.num_w_tiles;
   const int grid = 2 * static_cast<int>(std::min<long long>(most, clusters));
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(grid), 1, 1);
-  cfg.blockDim = dim3(static_cast<unsigned>(threads_of(nc)), 1, 1);
-  cfg.dynamicSmemBytes = static_cast<size_t>(smem);
-  cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = 2;
-  attr[0].val.clusterDim.y = 1;
-  attr[0].val.clusterDim.z = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return runtime_status(cudaLaunchKernelEx(&cfg, k, p));
+  return runtime_status(launch_overlapped(k, static_cast<unsigned>(grid), static_cast<unsigned>(threads_of(nc)),
+                                          static_cast<size_t>(smem), stream, 2, p));
 }
 
 // Grouped product with SwiGLU where the up half starts inside a tile of
@@ -1183,13 +1177,17 @@ bwg_status run_swiglu_two_steps(const Fp4Operand& a, const Fp4Operand& b, void* 
   const float* x = static_cast<const float*>(workspace);
   const int n = N / 2, threads = std::min(256, (n + 31) / 32 * 32);
   const unsigned blocks = static_cast<unsigned>(M);
+  cudaError_t e;
   if (out_dtype == BWG_OUT_FP32)
-    fp4_swiglu_kernel<<<blocks, threads, 0, stream>>>(x, offsets + G, n, ldh, static_cast<float*>(H));
+    e = launch_overlapped(fp4_swiglu_kernel<float>, blocks, static_cast<unsigned>(threads), 0, stream, 1, x, offsets + G, n,
+                          static_cast<long long>(ldh), static_cast<float*>(H));
   else if (out_dtype == BWG_OUT_FP16)
-    fp4_swiglu_kernel<<<blocks, threads, 0, stream>>>(x, offsets + G, n, ldh, static_cast<__half*>(H));
+    e = launch_overlapped(fp4_swiglu_kernel<__half>, blocks, static_cast<unsigned>(threads), 0, stream, 1, x, offsets + G, n,
+                          static_cast<long long>(ldh), static_cast<__half*>(H));
   else
-    fp4_swiglu_kernel<<<blocks, threads, 0, stream>>>(x, offsets + G, n, ldh, static_cast<__nv_bfloat16*>(H));
-  return runtime_status(cudaGetLastError());
+    e = launch_overlapped(fp4_swiglu_kernel<__nv_bfloat16>, blocks, static_cast<unsigned>(threads), 0, stream, 1, x, offsets + G, n,
+                          static_cast<long long>(ldh), static_cast<__nv_bfloat16*>(H));
+  return runtime_status(e);
 }
 
 }  // namespace
