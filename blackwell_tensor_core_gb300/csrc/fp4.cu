@@ -194,37 +194,48 @@ __device__ __forceinline__ void store_words(void* dst, const uint32_t (&w)[W]) {
   }
 }
 
-// A block's words as FP32 values (NEG: negated), and its largest magnitude
-// (NaN where it holds an infinity or a NaN).  Magnitudes of floats order like
-// their bits.
-template <class T, int B, bool NEG>
+// Larger magnitude of each half of two words of 16-bit floats, NaN winning
+// (32768 x 4096 BF16 to mxfp4: 52 us; 57 on the words' bits).
+template <class T>
+__device__ __forceinline__ uint32_t max_abs2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  if constexpr (std::is_same<T, __half>::value)
+    asm("{\n\t.reg .b32 x, y;\n\tabs.f16x2 x, %1;\n\tabs.f16x2 y, %2;\n\tmax.NaN.f16x2 %0, x, y;\n\t}"
+        : "=r"(r)
+        : "r"(a), "r"(b));
+  else
+    asm("{\n\t.reg .b32 x, y;\n\tabs.bf16x2 x, %1;\n\tabs.bf16x2 y, %2;\n\tmax.NaN.bf16x2 %0, x, y;\n\t}"
+        : "=r"(r)
+        : "r"(a), "r"(b));
+  return r;
+}
+
+// A block's words as FP32 values, and its largest magnitude: infinite or NaN
+// where it holds an infinity or a NaN.
+template <class T, int B>
 __device__ __forceinline__ float unpack_block(const uint32_t* w, float (&v)[B]) {
-  uint32_t m = 0, inf;
-  float amax;
   if constexpr (sizeof(T) == 4) {
+    uint32_t m = 0;  // magnitudes of floats order like their bits, NaN above infinity
 #pragma unroll
     for (int i = 0; i < B; ++i) {
       m = max(m, w[i] & 0x7fffffffu);
-      v[i] = NEG ? -__uint_as_float(w[i]) : __uint_as_float(w[i]);
+      v[i] = __uint_as_float(w[i]);
     }
-    inf = 0x7f800000u;
-    amax = __uint_as_float(m);
+    return __uint_as_float(m);
   } else {
+    uint32_t m = 0;
 #pragma unroll
     for (int i = 0; i < B / 2; ++i) {
-      m = __vmaxu2(m, w[i] & 0x7fff7fffu);
-      const uint32_t x = NEG ? w[i] ^ 0x80008000u : w[i];
-      v[2 * i] = bits_to_f32<T>(x & 0xffffu);
+      m = max_abs2<T>(m, w[i]);
+      v[2 * i] = bits_to_f32<T>(w[i] & 0xffffu);
       if constexpr (std::is_same<T, __half>::value)
-        v[2 * i + 1] = bits_to_f32<T>(x >> 16);
+        v[2 * i + 1] = bits_to_f32<T>(w[i] >> 16);
       else
-        v[2 * i + 1] = __uint_as_float(x & 0xffff0000u);
+        v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
     }
-    m = max(m & 0xffffu, m >> 16);
-    inf = std::is_same<T, __half>::value ? 0x7c00u : 0x7f80u;
-    amax = bits_to_f32<T>(m);
+    m = max_abs2<T>(m, m >> 16);
+    return bits_to_f32<T>(m & 0xffffu);
   }
-  return m >= inf ? __int_as_float(0x7fffffff) : amax;
 }
 
 // 8 FP32 values as 8 e2m1 codes (nearest even, saturating).
@@ -284,18 +295,19 @@ __device__ __forceinline__ GlobalScale global_scale(const float* p) {
   return s;
 }
 
-// Scales the block to what its codes are rounded from (v holds -x for nvfp4,
-// x for mxfp4) and stores the scale byte in *sb; false: left to slow_block.
+// Scales the block to what its codes are rounded from (nvfp4: to its negative)
+// and stores the scale byte in *sb; false: left to slow_block.
 //
 // nvfp4's quotients are FP32's x / d from an approximate reciprocal r of d:
 // q0 = x r is a few units in the last place off, its remainder x - q0 d is
 // exact in an FMA, and q0 plus the remainder times r rounds to the quotient
-// (Markstein, 1990).  From -x, with e = q0 d - x, every factor is a constant
-// and a zero keeps its sign, also for a zero scale (r = 0).  What could
-// overflow or lose the remainder's bits goes to slow_block, out of line, which
-// leaves registers for four blocks of threads an SM: 58 us for 32768 x 4096
-// BF16 (5.8 TB/s) against 75 us with that code here, 69 us with it out of
-// line but three blocks, and 84 us with divisions, one value at a time.
+// (Markstein, 1990).  Computed as -q from -r, so that every factor is a constant
+// of the block and a zero gets the sign that a flip of the codes' signs turns
+// into its own, also for a zero scale (r = 0).  What could overflow or lose the
+// remainder's bits goes to slow_block, out of line, which leaves registers for
+// four blocks of threads an SM: 58 us for 32768 x 4096 BF16 (5.9 TB/s) against
+// 75 us with that code here, 69 us with it out of line but three blocks, and
+// 84 us with divisions, one value at a time.  mxfp4's multiplications: 51 us.
 template <int FMT, int B>
 __device__ __forceinline__ bool quantize_block(float (&v)[B], float amax, const GlobalScale& gs, uint32_t* sb) {
   if constexpr (FMT == kMxfp4) {
@@ -314,8 +326,8 @@ __device__ __forceinline__ bool quantize_block(float (&v)[B], float amax, const 
 #pragma unroll
     for (int i = 0; i < B; i += 2) {
       const uint64_t x2 = pair_of(v[i], v[i + 1]);
-      const uint64_t q0 = mul2(x2, r2);
-      const uint64_t q = fma2(fma2(q0, s2, x2), r2, q0);
+      const uint64_t q0 = mul2(x2, r2);                   // -q0
+      const uint64_t q = fma2(fma2(q0, s2, x2), r2, q0);  // -q0 - (x - q0 d) r
       asm("mov.b64 {%0, %1}, %2;" : "=f"(v[i]), "=f"(v[i + 1]) : "l"(q));
     }
     *sb = s;
@@ -396,11 +408,11 @@ __global__ void __launch_bounds__(kFp4Threads, 4) quantize_kernel(const __grid_c
         uint32_t sb = 0;  // blocks past the row's last: the tile's padding
         if (b < p.nb) {
           float v[B];
-          const float amax = unpack_block<T, B, FMT == kNvfp4>(w[i], v);
+          const float amax = unpack_block<T, B>(w[i], v);
           const bool done = quantize_block<FMT, B>(v, amax, gs, &sb);
           uint32_t c[B / 8];
 #pragma unroll
-          for (int j = 0; j < B / 8; ++j) c[j] = pack_e2m1x8(v + 8 * j);
+          for (int j = 0; j < B / 8; ++j) c[j] = pack_e2m1x8(v + 8 * j) ^ (FMT == kNvfp4 ? 0x88888888u : 0u);
           uint8_t* dst = p.codes + static_cast<long long>(row) * (p.K / 2) + static_cast<long long>(b) * (B / 2);
           if constexpr (B == 16)
             *reinterpret_cast<uint2*>(dst) = make_uint2(c[0], c[1]);
@@ -606,7 +618,11 @@ bwg_status run_fp4(bool quant, const void* x, void* y, int dtype, int M, int K, 
                       : dtype == BWG_OUT_BF16 ? pick<__nv_bfloat16>(quant, wide, format, vb)
                                               : pick<__half>(quant, wide, format, vb);
   const long long units = static_cast<long long>(p.row_blocks) * p.chunks;
-  const long long blocks = std::min<long long>(units, rt.sm_count * 8LL);
+  // A block a unit: SMs that finish early go on (32768 x 4096 NVFP4 read back
+  // as BF16 54 us against 58 with 8 blocks an SM that stride over the units,
+  // as FP32 91 against 97).  With ragged groups, whose tables every block
+  // builds, 8 an SM: there more or fewer made no difference.
+  const long long blocks = std::min<long long>(units, offsets != nullptr ? rt.sm_count * 8LL : 0x7fffffffLL);
   const size_t smem = offsets != nullptr ? (2 * static_cast<size_t>(G) + 2) * sizeof(int) : 0;
   // A plain launch: blocks that start while the work before still holds some SMs
   // gather on the others, and these grids are a round or two of blocks only
