@@ -638,6 +638,16 @@ BWG_HD uint32_t small_stage_bytes(int n) {
   return kWBytes + static_cast<uint32_t>(n) * kKBytes + 2u * 4u * kScaleTileBytes;
 }
 
+// Four FP32 values of a CTA's shared memory in the cluster.
+__device__ __forceinline__ float4 ld_cluster_v4(uint32_t cluster_addr) {
+  float4 v;
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+               : "r"(cluster_addr)
+               : "memory");
+  return v;
+}
+
 template <int FMT>
 __global__ void __launch_bounds__(kSmallThreads, 1) fp4_small_kernel(const __grid_constant__ Fp4SmallParams p) {
   constexpr int kVec = FMT == kNvfp4 ? 16 : 32;
@@ -833,25 +843,45 @@ __global__ void __launch_bounds__(kSmallThreads, 1) fp4_small_kernel(const __gri
     cluster_sync_all();
     const bool out32 = p.out_dtype == kOutF32, outbf = p.out_dtype == kOutBF16;
     const float alpha = (p.a_global != nullptr ? __ldg(p.a_global) : 1.f) * (p.b_global != nullptr ? __ldg(p.b_global) : 1.f);
-    const int ch = static_cast<int>(threadIdx.x & 127u);
+    const int ch = static_cast<int>(lane) * 4;
     const int col = first * 128 + ch;
-    for (int j = rank + p.split * static_cast<int>(threadIdx.x >> 7); j < p.M; j += 2 * p.split) {
+    const int elt = out32 ? 4 : 2;
+    const bool whole =
+        col + 4 <= p.N && ((reinterpret_cast<uintptr_t>(p.d) | static_cast<uintptr_t>(p.ldd * elt)) & (4 * elt - 1)) == 0;
+    for (int j = rank + p.split * static_cast<int>(warp); j < p.M; j += p.split * (kSmallThreads / 32)) {
       const uint32_t at = base + static_cast<uint32_t>(j * 128 + ch) * 4u;
-      float part[kSmallMaxSplit];
+      float4 part[kSmallMaxSplit];
 #pragma unroll
       for (int c = 0; c < kSmallMaxSplit; ++c)
-        part[c] = c < p.split ? __uint_as_float(ld_shared_cluster_u32(mapa_shared(at, static_cast<uint32_t>(c)))) : 0.f;
-      float x = part[0];
+        if (c < p.split) part[c] = ld_cluster_v4(mapa_shared(at, static_cast<uint32_t>(c)));
+      float x[4] = {part[0].x, part[0].y, part[0].z, part[0].w};
 #pragma unroll
       for (int c = 1; c < kSmallMaxSplit; ++c)
-        if (c < p.split) x += part[c];
-      x *= alpha;
-      if (col < p.N) {
-        uint8_t* dst = static_cast<uint8_t*>(p.d) + (static_cast<long long>(j) * p.ldd + col) * (out32 ? 4 : 2);
+        if (c < p.split) {
+          x[0] += part[c].x;
+          x[1] += part[c].y;
+          x[2] += part[c].z;
+          x[3] += part[c].w;
+        }
+      uint8_t* dst = static_cast<uint8_t*>(p.d) + (static_cast<long long>(j) * p.ldd + col) * elt;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) x[i] *= alpha;
+      if (whole) {
         if (out32)
-          *reinterpret_cast<float*>(dst) = x;
+          *reinterpret_cast<float4*>(dst) = make_float4(x[0], x[1], x[2], x[3]);
+        else if (outbf)
+          *reinterpret_cast<uint2*>(dst) = make_uint2(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]));
         else
-          *reinterpret_cast<uint16_t*>(dst) = outbf ? cvt_rn_bf16(x) : cvt_rn_f16(x);
+          *reinterpret_cast<uint2*>(dst) = make_uint2(pack_f16x2(x[0], x[1]), pack_f16x2(x[2], x[3]));
+      } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          if (col + i < p.N) {
+            if (out32)
+              reinterpret_cast<float*>(dst)[i] = x[i];
+            else
+              reinterpret_cast<uint16_t*>(dst)[i] = outbf ? cvt_rn_bf16(x[i]) : cvt_rn_f16(x[i]);
+          }
       }
     }
   }
