@@ -609,13 +609,15 @@ __global__ void __launch_bounds__(threads_of(NC), 1) fp4_pair_kernel(const __gri
 }
 
 // ---------------------------------------------------------- few rows -------
-// At most 128 rows of A: the weights' bytes are the time.  One CTA a tile of
-// 128 output columns, the rows (rounded up to 16) as N.  Where there are too
-// few tiles to keep the memory busy, a cluster of `split` CTAs shares a
-// tile's k-blocks and sums its FP32 partials through distributed shared
-// memory, in rank order; else the CTAs walk the tiles.
+// At most 128 rows of A, where the weights' bytes are the time, and more as long
+// as one round of its tiles covers them.  One CTA a tile of 128 output columns
+// and up to 128 rows (rounded up to 16) as N.  Where there are too few tiles to
+// keep the memory busy, a cluster of `split` CTAs shares a tile's k-blocks and
+// sums its FP32 partials through distributed shared memory, in rank order;
+// else the CTAs walk the tiles.
 // What bounds it: HBM, and at a few MB of weights the latency of a launch and
-// of the first loads.
+// of the first loads (one row of 4096 x 4096 NVFP4 4.7 us, 128 rows 7.0, 256
+// rows of 4096 x 7168 9.5).
 constexpr int kSmallMaxRows = 128;
 constexpr int kSmallThreads = 256;
 constexpr int kSmallMaxStages = 8;
@@ -629,9 +631,10 @@ struct Fp4SmallParams {
   const float* b_global;
   void* d;
   long long ldd;
-  int M, N, n;             // n: M rounded up to 16
+  int M, N, n;             // n: rows of a tile, a multiple of 16
   int num_k_blocks, last_steps;
   int tiles, split, stages, out_dtype;
+  int row_tiles;           // tiles of up to 128 rows of A; a tile's number runs over them first
 };
 
 BWG_HD uint32_t small_stage_bytes(int n) {
@@ -646,6 +649,56 @@ __device__ __forceinline__ float4 ld_cluster_v4(uint32_t cluster_addr) {
                : "r"(cluster_addr)
                : "memory");
   return v;
+}
+
+// Rank `rank` of F sums rows rank, rank + F, .. of a tile's partials (at `base`
+// in each CTA, 128 floats a row), a warp a row, in rank order, and stores them.
+// F loads of 16 bytes are in flight a lane; twice as many measured the same, 4
+// bytes a lane 0.3 (16 rows) to 3 us more (128 rows).
+template <int F>
+__device__ __forceinline__ void sum_partials(const Fp4SmallParams& p, uint32_t base, int rank, int row0, int rows,
+                                             int col0) {
+  const bool out32 = p.out_dtype == kOutF32, outbf = p.out_dtype == kOutBF16;
+  const float alpha = (p.a_global != nullptr ? __ldg(p.a_global) : 1.f) * (p.b_global != nullptr ? __ldg(p.b_global) : 1.f);
+  const int ch = static_cast<int>(threadIdx.x & 31u) * 4;
+  const int col = col0 + ch;
+  const int elt = out32 ? 4 : 2;
+  const bool whole =
+      col + 4 <= p.N && ((reinterpret_cast<uintptr_t>(p.d) | static_cast<uintptr_t>(p.ldd * elt)) & (4 * elt - 1)) == 0;
+  for (int j = rank + F * static_cast<int>(threadIdx.x >> 5); j < rows; j += F * (kSmallThreads / 32)) {
+    const uint32_t at = base + static_cast<uint32_t>(j * 128 + ch) * 4u;
+    float4 part[F];
+#pragma unroll
+    for (int c = 0; c < F; ++c) part[c] = ld_cluster_v4(mapa_shared(at, static_cast<uint32_t>(c)));
+    float x[4] = {part[0].x, part[0].y, part[0].z, part[0].w};
+#pragma unroll
+    for (int c = 1; c < F; ++c) {
+      x[0] += part[c].x;
+      x[1] += part[c].y;
+      x[2] += part[c].z;
+      x[3] += part[c].w;
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) x[i] *= alpha;
+    uint8_t* dst = static_cast<uint8_t*>(p.d) + (static_cast<long long>(row0 + j) * p.ldd + col) * elt;
+    if (whole) {
+      if (out32)
+        *reinterpret_cast<float4*>(dst) = make_float4(x[0], x[1], x[2], x[3]);
+      else if (outbf)
+        *reinterpret_cast<uint2*>(dst) = make_uint2(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]));
+      else
+        *reinterpret_cast<uint2*>(dst) = make_uint2(pack_f16x2(x[0], x[1]), pack_f16x2(x[2], x[3]));
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (col + i < p.N) {
+          if (out32)
+            reinterpret_cast<float*>(dst)[i] = x[i];
+          else
+            reinterpret_cast<uint16_t*>(dst)[i] = outbf ? cvt_rn_bf16(x[i]) : cvt_rn_f16(x[i]);
+        }
+    }
+  }
 }
 
 template <int FMT>
@@ -704,10 +757,11 @@ __global__ void __launch_bounds__(kSmallThreads, 1) fp4_small_kernel(const __gri
   if (warp == 0 || warp == 2) {
     // ---- TMA producers: weights, activations ---------------------------------
     const bool weights = warp == 0;
-    const uint64_t stream_once = l2_policy_evict_first();
+    const uint64_t policy = p.row_tiles == 1 ? l2_policy_evict_first() : l2_policy_evict_normal();
     int s = 0;
     uint32_t ph = 0;
     for (int t = first; t < p.tiles && !aborted; t += stride) {
+      const int ct = t / p.row_tiles, rt = t % p.row_tiles;
       for (int kb = kb0; kb < kb1; ++kb) {
         if (!warp_wait_cta(empty_bar(s), ph ^ 1u, p.timeout_ns)) {
           if (lane == 0) record_fault(p.err, kFaultTimeout, kRoleProducer, kBarEmpty, s, ph ^ 1u);
@@ -719,11 +773,11 @@ __global__ void __launch_bounds__(kSmallThreads, 1) fp4_small_kernel(const __gri
           const uint32_t sf = st + kWBytes + a_bytes;
           if (weights) {
             mbar_arrive_expect_tx(full_bar(s), kWBytes + a_bytes + 2u * kSfBytes);
-            tma_load_3d_hint(st, &p.map_w, full_bar(s), kb * kKBytes, t * 128, 0, stream_once);
-            tma_load_3d_hint(sf, &p.map_ws, full_bar(s), 0, kb * kTilesK, t, stream_once);
+            tma_load_3d_hint(st, &p.map_w, full_bar(s), kb * kKBytes, ct * 128, 0, policy);
+            tma_load_3d_hint(sf, &p.map_ws, full_bar(s), 0, kb * kTilesK, ct, policy);
           } else {
-            tma_load_2d(st + kWBytes, &p.map_a, full_bar(s), kb * kKBytes, 0);
-            tma_load_3d(sf + kSfSlot, &p.map_as, full_bar(s), 0, kb * kTilesK, 0);
+            tma_load_2d(st + kWBytes, &p.map_a, full_bar(s), kb * kKBytes, rt * 128);
+            tma_load_3d(sf + kSfSlot, &p.map_as, full_bar(s), 0, kb * kTilesK, rt);
           }
         }
         __syncwarp();
@@ -800,12 +854,13 @@ __global__ void __launch_bounds__(kSmallThreads, 1) fp4_small_kernel(const __gri
       }
       tc_fence_after();
       const int ch = static_cast<int>(q * 32u + lane);
-      const int col = t * 128 + ch;
-      for (int c0 = 0; c0 < p.M; c0 += 32) {
+      const int col = t / p.row_tiles * 128 + ch;
+      const int row0 = t % p.row_tiles * 128, rows = min(128, p.M - row0);
+      for (int c0 = 0; c0 < rows; c0 += 32) {
         uint32_t v[32];
         tmem_ld_32x32b_x32(((q * 32u) << 16) + static_cast<uint32_t>(acc) * kAcc + c0, v);
         tmem_wait_ld();
-        if (c0 + 32 >= p.M) {
+        if (c0 + 32 >= rows) {
           tc_fence_before();
           __syncwarp();
           if (lane == 0) mbar_arrive_local(acc_empty(acc));
@@ -814,13 +869,13 @@ __global__ void __launch_bounds__(kSmallThreads, 1) fp4_small_kernel(const __gri
           // the ring is idle: every load of this CTA has been used
 #pragma unroll
           for (int j = 0; j < 32; ++j)
-            if (c0 + j < p.M) st_shared_u32(base + static_cast<uint32_t>((c0 + j) * 128 + ch) * 4u, v[j]);
+            if (c0 + j < rows) st_shared_u32(base + static_cast<uint32_t>((c0 + j) * 128 + ch) * 4u, v[j]);
         } else if (col < p.N) {
           const int elt = out32 ? 4 : 2;
-          uint8_t* dst = static_cast<uint8_t*>(p.d) + (static_cast<long long>(c0) * p.ldd + col) * elt;
+          uint8_t* dst = static_cast<uint8_t*>(p.d) + (static_cast<long long>(row0 + c0) * p.ldd + col) * elt;
 #pragma unroll
           for (int j = 0; j < 32; ++j) {
-            if (c0 + j < p.M) {
+            if (c0 + j < rows) {
               const float x = alpha * __uint_as_float(v[j]);
               if (out32)
                 *reinterpret_cast<float*>(dst) = x;
@@ -839,50 +894,17 @@ __global__ void __launch_bounds__(kSmallThreads, 1) fp4_small_kernel(const __gri
 
   grid_dependents_launch();
   if (p.split > 1) {
+    const int row0 = first % p.row_tiles * 128, rows = min(128, p.M - row0), col0 = first / p.row_tiles * 128;
     // ---- partials: rank r sums rows r, r + split, .. of the tile ---------------
     cluster_sync_all();
-    const bool out32 = p.out_dtype == kOutF32, outbf = p.out_dtype == kOutBF16;
-    const float alpha = (p.a_global != nullptr ? __ldg(p.a_global) : 1.f) * (p.b_global != nullptr ? __ldg(p.b_global) : 1.f);
-    const int ch = static_cast<int>(lane) * 4;
-    const int col = first * 128 + ch;
-    const int elt = out32 ? 4 : 2;
-    const bool whole =
-        col + 4 <= p.N && ((reinterpret_cast<uintptr_t>(p.d) | static_cast<uintptr_t>(p.ldd * elt)) & (4 * elt - 1)) == 0;
-    for (int j = rank + p.split * static_cast<int>(warp); j < p.M; j += p.split * (kSmallThreads / 32)) {
-      const uint32_t at = base + static_cast<uint32_t>(j * 128 + ch) * 4u;
-      float4 part[kSmallMaxSplit];
-#pragma unroll
-      for (int c = 0; c < kSmallMaxSplit; ++c)
-        if (c < p.split) part[c] = ld_cluster_v4(mapa_shared(at, static_cast<uint32_t>(c)));
-      float x[4] = {part[0].x, part[0].y, part[0].z, part[0].w};
-#pragma unroll
-      for (int c = 1; c < kSmallMaxSplit; ++c)
-        if (c < p.split) {
-          x[0] += part[c].x;
-          x[1] += part[c].y;
-          x[2] += part[c].z;
-          x[3] += part[c].w;
-        }
-      uint8_t* dst = static_cast<uint8_t*>(p.d) + (static_cast<long long>(j) * p.ldd + col) * elt;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) x[i] *= alpha;
-      if (whole) {
-        if (out32)
-          *reinterpret_cast<float4*>(dst) = make_float4(x[0], x[1], x[2], x[3]);
-        else if (outbf)
-          *reinterpret_cast<uint2*>(dst) = make_uint2(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]));
-        else
-          *reinterpret_cast<uint2*>(dst) = make_uint2(pack_f16x2(x[0], x[1]), pack_f16x2(x[2], x[3]));
-      } else {
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-          if (col + i < p.N) {
-            if (out32)
-              reinterpret_cast<float*>(dst)[i] = x[i];
-            else
-              reinterpret_cast<uint16_t*>(dst)[i] = outbf ? cvt_rn_bf16(x[i]) : cvt_rn_f16(x[i]);
-          }
-      }
+    switch (p.split) {
+      case 2: sum_partials<2>(p, base, rank, row0, rows, col0); break;
+      case 3: sum_partials<3>(p, base, rank, row0, rows, col0); break;
+      case 4: sum_partials<4>(p, base, rank, row0, rows, col0); break;
+      case 5: sum_partials<5>(p, base, rank, row0, rows, col0); break;
+      case 6: sum_partials<6>(p, base, rank, row0, rows, col0); break;
+      case 7: sum_partials<7>(p, base, rank, row0, rows, col0); break;
+      default: sum_partials<8>(p, base, rank, row0, rows, col0); break;
     }
   }
   if (__syncthreads_or(aborted ? 1 : 0)) {
@@ -1030,14 +1052,28 @@ bool fp4_maps(Fp4GemmParams* p, const Fp4Operand& a, const Fp4Operand& b, int M,
          runtime_map(&p->map_as, a.scales, u32, 3, asd, ss, asb, CU_TENSOR_MAP_SWIZZLE_NONE);
 }
 
-// Cluster size of a few-rows call: the one that keeps the most SMs loading,
-// with all clusters co-resident and two k-blocks a CTA at least; 1 where the
-// tiles alone fill half of the SMs.
-int small_split(int tiles, int kb, int sm_count, const int* clusters) {
+// Whether the kernel above takes a product: up to 128 rows always, more where
+// its tiles are one round.  Its CTAs are ready and done 1.3 us sooner than pairs
+// with two accumulators, and can share a tile: 256 rows of 4096 x 7168 9.5 us
+// against 12.0, 8192 x 2048 (K x N) 8.0 against 12.5, 512 rows of 4096 x 1024
+// 4.9 against 6.8.
+bool few_rows(int M, int N, int sm_count) {
+  return M <= kSmallMaxRows || static_cast<long long>((M + 127) / 128) * ((N + 127) / 128) <= sm_count;
+}
+
+// Cluster size of a few-rows call, with all clusters co-resident; 1 where the
+// tiles alone fill half of the SMs.  A k-block is about 0.21 us, the sum of a
+// split tile's partials 0.7 us and 0.5 for each 100 rows.
+int small_split(int tiles, int rows, int kb, int sm_count, const int* clusters) {
   if (2 * tiles > sm_count) return 1;
-  int best = 1;
-  for (int f = 2; f <= kSmallMaxSplit; ++f)
-    if (tiles <= clusters[f] && kb >= 2 * f) best = f;
+  int best = 1, least = 21 * kb;
+  for (int f = 2; f <= kSmallMaxSplit; ++f) {
+    const int cost = 21 * ((kb + f - 1) / f) + 70 + rows / 2;
+    if (tiles <= clusters[f] && f <= kb && cost < least) {
+      best = f;
+      least = cost;
+    }
+  }
   return best;
 }
 
@@ -1086,7 +1122,8 @@ bwg_status run_small(const Fp4Operand& a, const Fp4Operand& b, void* D, int M, i
   }
   Fp4SmallParams p;
   std::memset(&p, 0, sizeof(p));
-  p.n = (M + 15) & ~15;
+  p.n = std::min(kSmallMaxRows, (M + 15) & ~15);
+  p.row_tiles = (M + kSmallMaxRows - 1) / kSmallMaxRows;
   const uint64_t row = static_cast<uint64_t>(K / 2);
   const uint64_t kt = static_cast<uint64_t>(fp4_k_tiles(K, format));
   const uint32_t kbox = format == kNvfp4 ? 4 : 2;
@@ -1096,7 +1133,7 @@ bwg_status run_small(const Fp4Operand& a, const Fp4Operand& b, void* D, int M, i
   const uint64_t ad[2] = {row, static_cast<uint64_t>(M)};
   const uint32_t ab[2] = {kKBytes, static_cast<uint32_t>(p.n)};
   const uint64_t ss[2] = {kScaleTileBytes, kt * kScaleTileBytes};
-  const uint64_t wsd[3] = {128, kt, static_cast<uint64_t>(pad128(N) / 128)}, asd[3] = {128, kt, 1};
+  const uint64_t wsd[3] = {128, kt, static_cast<uint64_t>(pad128(N) / 128)}, asd[3] = {128, kt, static_cast<uint64_t>(p.row_tiles)};
   const uint32_t sb[3] = {128, kbox, 1};
   if (!runtime_map(&p.map_w, b.codes, u8, 3, wd, ws, wb, CU_TENSOR_MAP_SWIZZLE_128B) ||
       !runtime_map(&p.map_a, a.codes, u8, 2, ad, &row, ab, CU_TENSOR_MAP_SWIZZLE_128B) ||
@@ -1113,8 +1150,8 @@ bwg_status run_small(const Fp4Operand& a, const Fp4Operand& b, void* D, int M, i
   p.N = N;
   p.num_k_blocks = (K + kKCols - 1) / kKCols;
   p.last_steps = (K - (p.num_k_blocks - 1) * kKCols + 63) / 64;
-  p.tiles = (N + 127) / 128;
-  p.split = small_split(p.tiles, p.num_k_blocks, rt.sm_count, info.clusters);
+  p.tiles = (N + 127) / 128 * p.row_tiles;
+  p.split = small_split(p.tiles, std::min(M, kSmallMaxRows), p.num_k_blocks, rt.sm_count, info.clusters);
   p.out_dtype = out_dtype;
   const int stage = static_cast<int>(small_stage_bytes(p.n));
   const int tail = 1024 + 8 * (2 * kSmallMaxStages + 4) + 16;
@@ -1151,7 +1188,7 @@ bwg_status run_fp4_gemm(const Fp4Operand& a, const Fp4Operand& b, void* D, int M
   bwg_status st = runtime_device(&rt);
   if (st != BWG_OK) return st;
   if (K == 0) return runtime_status(launch_zero_fill(D, M, n_out, ldd, out_dtype == BWG_OUT_FP32 ? 4 : 2, stream));
-  if (offsets == nullptr && G == 1 && M <= kSmallMaxRows)
+  if (offsets == nullptr && G == 1 && few_rows(M, N, rt.sm_count))
     return run_small(a, b, D, M, N, K, ldd, format, out_dtype, rt, stream);
   Fp4GemmParams p;
   std::memset(&p, 0, sizeof(p));

@@ -267,6 +267,43 @@ def test_many_tiles_are_exact(ops, M, N, K, fmt):
         assert torch.equal(ops.gemm_fp4(a, b, out_dtype=torch.float32).double(), want)
 
 
+# tiles of 128 rows whose k-blocks 1 to 8 CTAs share, up to one tile for each SM; then just too many tiles for that
+SHARED = [(129, 130, 2304), (200, 512, 8192), (257, 301, 4992), (1000, 128, 2080), (513, 1024, 7168), (640, 640, 4096),
+          (300, 1500, 1792), (260, 1280, 6144), (260, 896, 6144), (129, 9000, 1056), (512, 4096, 1024), (19400, 100, 320),
+          (129, 10000, 544), (193, 9800, 416), (385, 5000, 1184)]
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("M,N,K", SHARED)
+def test_shared_tiles_are_exact(ops, M, N, K, fmt):
+    rng = np.random.default_rng(M + N + K + 2)
+    a, A = random_fp4(ops, M, K, fmt, rng, integers=True)
+    b, B = random_fp4(ops, N, K, fmt, rng, integers=True)
+    want = dev(A) @ dev(B).t()  # in 64 bits
+    for _ in range(3):
+        D = ops.gemm_fp4(a, b, out_dtype=torch.float32)
+        torch.cuda.synchronize()
+        assert ops.last_device_error() == (0, 0)
+        assert torch.equal(D.double(), want)
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("pad,shift", [(0, 0), (4, 4), (2, 0), (1, 3)])
+def test_shared_tiles_into_a_wider_matrix(ops, fmt, dtype, pad, shift):
+    """Rows of D that start on 16 bytes and rows that do not."""
+    rng = np.random.default_rng(9)
+    M, N, K = 150, 260, 4096
+    a, _ = random_fp4(ops, M, K, fmt, rng)
+    b, _ = random_fp4(ops, N, K, fmt, rng)
+    if dtype == torch.float16:  # keep the sums inside FP16
+        a.scales -= torch.where(a.scales == 255, 0, 8).to(torch.uint8)
+    buf = torch.full((M, shift + N + pad), -5.0, device="cuda", dtype=dtype)
+    ops.gemm_fp4(a, b, out=buf[:, shift:shift + N])
+    assert torch.equal(buf[:, shift:shift + N], ops.gemm_fp4(a, b, out_dtype=torch.float32).to(dtype))
+    assert bool((buf[:, :shift] == -5.0).all()) and bool((buf[:, shift + N:] == -5.0).all())
+
+
 @pytest.mark.parametrize("fmt", FMTS)
 def test_gemm_into_a_wider_matrix(ops, fmt):
     rng = np.random.default_rng(8)
