@@ -503,7 +503,9 @@ __global__ void __launch_bounds__(threads_of(NC), 1) fp4_pair_kernel(const __gri
       // The two warpgroups take alternate chunks of 32 rows, three each.  All
       // of a warp's gate and up values (192 registers) are read and both
       // accumulators handed back before the first silu: its exponentials
-      // would hold the accumulators for about 2000 clocks longer.
+      // would hold the accumulators for about 2000 clocks longer.  Chunks past
+      // the tile's rows end there (8 pairs of 4096 x 4096 18.2 -> 17.4 us, of
+      // 512 x 512 7.4 -> 6.3).
       uint32_t acc_ph = 0;
       for (int i = 0; win.have(i); ++i) {
         if (!wait_acc_full(0, acc_ph) || !wait_acc_full(1, acc_ph)) {
@@ -529,6 +531,7 @@ __global__ void __launch_bounds__(threads_of(NC), 1) fp4_pair_kernel(const __gri
         const float alpha = alpha_of(tl.g);
 #pragma unroll
         for (int c = 0; c < 3; ++c) {
+          if (grp * 32 + c * 64 >= tl.tokens) break;
 #pragma unroll
           for (int j = 0; j < 32; ++j)
             gate[c][j] =
@@ -557,6 +560,7 @@ __global__ void __launch_bounds__(threads_of(NC), 1) fp4_pair_kernel(const __gri
         const float alpha = alpha_of(tl.g);
 #pragma unroll
         for (int c = 0; c < 6; ++c) {
+          if (c * 32 >= tl.tokens) break;
 #pragma unroll
           for (int j = 0; j < 32; ++j) v[c][j] = __float_as_uint(alpha * __uint_as_float(v[c][j]));
           store(tl, c * 32, v[c]);
