@@ -206,7 +206,7 @@ struct TileWindow {
 __device__ __forceinline__ float silu_mul(float g, float u) { return g * rcp_approx(1.0f + __expf(-g)) * u; }
 
 // Warps 0, 2 and 3 load, warp 1 issues the MMAs, warps 4.. are the epilogue.
-constexpr int threads_of(int nc) { return nc == 1 ? 256 : 384; }
+constexpr int kPairThreads = 384;
 // Ring depth: the MMA loop is unrolled over it, so that every stage's
 // addresses are constants.
 constexpr int stages_of(int nc) { return nc == 1 ? 6 : 4; }
@@ -238,7 +238,7 @@ struct Layout {
 // takes 0.42 us (0.39 MXFP4) where its MMAs need 0.371, one of an NC == 1 tile
 // 0.24 (0.21) for 0.186.
 template <int NC, int FMT, bool SW>
-__global__ void __launch_bounds__(threads_of(NC), 1) fp4_pair_kernel(const __grid_constant__ Fp4GemmParams p) {
+__global__ void __launch_bounds__(kPairThreads, 1) fp4_pair_kernel(const __grid_constant__ Fp4GemmParams p) {
   static_assert(!SW || NC == 2, "SwiGLU pairs a gate block with an up block");
   using L = Layout<NC>;
   constexpr int kVec = FMT == kNvfp4 ? 16 : 32;
@@ -273,7 +273,7 @@ __global__ void __launch_bounds__(threads_of(NC), 1) fp4_pair_kernel(const __gri
     for (int a = 0; a < 2; ++a) {
       mbar_init(acc_full(a), 1);
       // epilogue warps of both CTAs that read this accumulator
-      mbar_init(acc_empty(a), SW ? 16 : 8);
+      mbar_init(acc_empty(a), NC == 1 || SW ? 16 : 8);
     }
     fence_mbarrier_init();
   }
@@ -577,11 +577,13 @@ __global__ void __launch_bounds__(threads_of(NC), 1) fp4_pair_kernel(const __gri
           break;
         }
         tc_fence_after();
-        for (int c0 = 0; c0 < tl.tokens; c0 += 32) {
+        // the two warpgroups take alternate chunks of 32 rows (1900 rows of
+        // 4096 x 1024 10.3 us, 11.5 with one)
+        for (int c0 = grp * 32; c0 < tl.tokens; c0 += 64) {
           uint32_t v[32];
           tmem_ld_32x32b_x32(t_lane + static_cast<uint32_t>(acc) * kAccCols + c0, v);
           tmem_wait_ld();
-          if (c0 + 32 >= tl.tokens) {
+          if (c0 + 64 >= tl.tokens) {
             tc_fence_before();
             __syncwarp();
             release(acc);
@@ -590,6 +592,7 @@ __global__ void __launch_bounds__(threads_of(NC), 1) fp4_pair_kernel(const __gri
           for (int j = 0; j < 32; ++j) v[j] = __float_as_uint(alpha * __uint_as_float(v[j]));
           store(tl, c0, v);
         }
+        if (grp * 32 >= tl.tokens) release(acc);
         acc ^= 1;
         if (acc == 0) acc_ph ^= 1u;
       }
@@ -613,9 +616,9 @@ __global__ void __launch_bounds__(threads_of(NC), 1) fp4_pair_kernel(const __gri
 }
 
 // ---------------------------------------------------------- few rows -------
-// At most 128 rows of A, where the weights' bytes are the time, and more as long
-// as one round of its tiles covers them.  One CTA a tile of 128 output columns
-// and up to 128 rows (rounded up to 16) as N.  Where there are too few tiles to
+// At most 128 rows of A, where the weights' bytes are the time, and more where
+// few rounds of its tiles cover them.  One CTA a tile of 128 output columns and
+// up to 128 rows (rounded up to 16) as N.  Where there are too few tiles to
 // keep the memory busy, a cluster of `split` CTAs shares a tile's k-blocks and
 // sums its FP32 partials through distributed shared memory, in rank order;
 // else the CTAs walk the tiles.
@@ -623,7 +626,11 @@ __global__ void __launch_bounds__(threads_of(NC), 1) fp4_pair_kernel(const __gri
 // of the first loads (one row of 4096 x 4096 NVFP4 4.7 us, 128 rows 7.0, 256
 // rows of 4096 x 7168 9.5).
 constexpr int kSmallMaxRows = 128;
-constexpr int kSmallThreads = 256;
+constexpr int kSmallThreads = 384;
+// Threads of a launch: a second epilogue warpgroup where a tile has a second
+// chunk of 32 rows (128 rows 0.3 us sooner, one row 0.15 later).
+int small_threads(int rows) { return rows > 32 ? kSmallThreads : kSmallThreads - 128; }
+
 constexpr int kSmallMaxStages = 8;
 constexpr int kSmallMaxSplit = 8;
 
@@ -669,7 +676,7 @@ __device__ __forceinline__ void sum_partials(const Fp4SmallParams& p, uint32_t b
   const int elt = out32 ? 4 : 2;
   const bool whole =
       col + 4 <= p.N && ((reinterpret_cast<uintptr_t>(p.d) | static_cast<uintptr_t>(p.ldd * elt)) & (4 * elt - 1)) == 0;
-  for (int j = rank + F * static_cast<int>(threadIdx.x >> 5); j < rows; j += F * (kSmallThreads / 32)) {
+  for (int j = rank + F * static_cast<int>(threadIdx.x >> 5); j < rows; j += F * static_cast<int>(blockDim.x >> 5)) {
     const uint32_t at = base + static_cast<uint32_t>(j * 128 + ch) * 4u;
     float4 part[F];
 #pragma unroll
@@ -739,7 +746,7 @@ __global__ void __launch_bounds__(kSmallThreads, 1) fp4_small_kernel(const __gri
     }
     for (int a = 0; a < 2; ++a) {
       mbar_init(acc_full(a), 1);
-      mbar_init(acc_empty(a), 4);
+      mbar_init(acc_empty(a), (blockDim.x >> 5) - 4);
     }
     fence_mbarrier_init();
   }
@@ -860,11 +867,14 @@ __global__ void __launch_bounds__(kSmallThreads, 1) fp4_small_kernel(const __gri
       const int ch = static_cast<int>(q * 32u + lane);
       const int col = t / p.row_tiles * 128 + ch;
       const int row0 = t % p.row_tiles * 128, rows = min(128, p.M - row0);
-      for (int c0 = 0; c0 < rows; c0 += 32) {
+      // the warpgroups take alternate chunks of 32 rows
+      const int c_first = static_cast<int>((warp - 4u) >> 2) * 32, c_step = (static_cast<int>(blockDim.x >> 7) - 1) * 32;
+      if (c_first >= rows && lane == 0) mbar_arrive_local(acc_empty(acc));
+      for (int c0 = c_first; c0 < rows; c0 += c_step) {
         uint32_t v[32];
         tmem_ld_32x32b_x32(((q * 32u) << 16) + static_cast<uint32_t>(acc) * kAcc + c0, v);
         tmem_wait_ld();
-        if (c0 + 32 >= rows) {
+        if (c0 + c_step >= rows) {
           tc_fence_before();
           __syncwarp();
           if (lane == 0) mbar_arrive_local(acc_empty(acc));
@@ -982,7 +992,7 @@ bwg_status pair_clusters(PairKernel k, int nc, const Runtime& rt, int* clusters)
   }
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(2, 1, 1);
-  cfg.blockDim = dim3(static_cast<unsigned>(threads_of(nc)), 1, 1);
+  cfg.blockDim = dim3(kPairThreads, 1, 1);
   cfg.dynamicSmemBytes = static_cast<size_t>(rt.max_smem);
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -998,7 +1008,7 @@ bwg_status pair_clusters(PairKernel k, int nc, const Runtime& rt, int* clusters)
   }
   // the register split only completes if the CTA was launched with at least the
   // registers that it hands out
-  if (nc == 2 && static_cast<uint32_t>(fa.numRegs) * threads_of(2) < kRegsControl * 128u + kRegsEpilogue * 256u)
+  if (nc == 2 && static_cast<uint32_t>(fa.numRegs) * kPairThreads < kRegsControl * 128u + kRegsEpilogue * 256u)
     return BWG_ERR_UNSUPPORTED;
   int n = 0;
   if (cudaOccupancyMaxActiveClusters(&n, fn, &cfg) != cudaSuccess || n <= 0) {
@@ -1014,12 +1024,32 @@ bwg_status pair_clusters(PairKernel k, int nc, const Runtime& rt, int* clusters)
   return BWG_OK;
 }
 
-// Weight blocks a CTA for a plain product.  A tile of two blocks takes 1.9
-// times as long as one of one block, but a pair's last round of tiles is then
-// twice as coarse.  Back to back at the power limit, 8192^3 NVFP4: 182 us with
-// two blocks (10 rounds), 190 with one (19); 32 experts' FC1 without SwiGLU 217
-// and 228; 4096^3 (3 and 5 rounds) 31.0 and 27.5.
-int plain_blocks(int M, int N, int groups, int pairs) {
+// Kernel of a dense product: 0 the few-rows kernel, 1 or 2 pairs with as many
+// weight blocks a CTA.  Up to 128 rows the first; above, the one whose rounds of
+// tiles take the least time: a start, and for each round its k-blocks and a
+// tile's switch, or the epilogue where that is longer (in 10 ns, fitted to 132
+// sizes of 200 to 4096 rows, where the fastest is taken but for 0.2% on average).
+// The few-rows kernel is ready sooner and splits tiles: 200 rows of 4096 x 7168
+// 9.1 us against 11.6 and 18.2; 960 rows of 4096 x 2048 8.2, 9.6 and 10.5.  One
+// block has the shorter k-blocks (1900 rows of 4096 x 7168 32.4, 26.5 and 32.3),
+// two cost the least per product (4096 rows of 8192 x 8192 125, 88 and 85).
+int dense_kernel(int M, int N, int kb, int sm_count) {
+  if (M <= kSmallMaxRows) return 0;
+  auto rounds = [&](long long rows, long long cols, int workers) {
+    const long long tiles = (M + rows - 1) / rows * ((N + cols - 1) / cols);
+    return (tiles + workers - 1) / workers;
+  };
+  const long long few = 320 + rounds(128, 128, sm_count) * std::max(24 * kb + 45, 150);
+  const long long one = 470 + rounds(kTok, 256, sm_count / 2) * std::max(25 * kb + 55, 175);
+  const long long two = 520 + rounds(kTok, 512, sm_count / 2) * std::max(44 * kb + 180, 310);
+  return few <= one && few <= two ? 0 : one <= two ? 1 : 2;
+}
+
+// Weight blocks a CTA for a plain grouped product.  A tile of two blocks takes
+// 1.9 times as long as one of one block, but a pair's last round of tiles is
+// then twice as coarse (32 experts' FC1 without SwiGLU 217 us with two, 228
+// with one).
+int grouped_blocks(int M, int N, int groups, int pairs) {
   // a ragged group ends on half a tile on average
   const long long rows = (M + kTok - 1LL) / kTok + groups / 2;
   const long long one = (rows * ((N + 255) / 256) + pairs - 1) / pairs;
@@ -1056,23 +1086,14 @@ bool fp4_maps(Fp4GemmParams* p, const Fp4Operand& a, const Fp4Operand& b, int M,
          runtime_map(&p->map_as, a.scales, u32, 3, asd, ss, asb, CU_TENSOR_MAP_SWIZZLE_NONE);
 }
 
-// Whether the kernel above takes a product: up to 128 rows always, more where
-// its tiles are one round.  Its CTAs are ready and done 1.3 us sooner than pairs
-// with two accumulators, and can share a tile: 256 rows of 4096 x 7168 9.5 us
-// against 12.0, 8192 x 2048 (K x N) 8.0 against 12.5, 512 rows of 4096 x 1024
-// 4.9 against 6.8.
-bool few_rows(int M, int N, int sm_count) {
-  return M <= kSmallMaxRows || static_cast<long long>((M + 127) / 128) * ((N + 127) / 128) <= sm_count;
-}
-
 // Cluster size of a few-rows call, with all clusters co-resident; 1 where the
 // tiles alone fill half of the SMs.  A k-block is about 0.21 us, the sum of a
-// split tile's partials 0.7 us and 0.5 for each 100 rows.
+// split tile's partials 0.7 us and 1.25 for each 100 rows.
 int small_split(int tiles, int rows, int kb, int sm_count, const int* clusters) {
   if (2 * tiles > sm_count) return 1;
   int best = 1, least = 21 * kb;
   for (int f = 2; f <= kSmallMaxSplit; ++f) {
-    const int cost = 21 * ((kb + f - 1) / f) + 70 + rows / 2;
+    const int cost = 21 * ((kb + f - 1) / f) + 70 + rows * 5 / 4;
     if (tiles <= clusters[f] && f <= kb && cost < least) {
       best = f;
       least = cost;
@@ -1162,7 +1183,7 @@ bwg_status run_small(const Fp4Operand& a, const Fp4Operand& b, void* D, int M, i
   p.stages = std::min(kSmallMaxStages, (rt.max_smem - tail) / stage);
   if (p.stages < 2) return BWG_ERR_UNSUPPORTED;
   const int grid = p.split > 1 ? p.tiles * p.split : std::min(p.tiles, rt.sm_count);
-  return runtime_status(launch_overlapped(k, static_cast<unsigned>(grid), kSmallThreads,
+  return runtime_status(launch_overlapped(k, static_cast<unsigned>(grid), static_cast<unsigned>(small_threads(p.n)),
                                           static_cast<size_t>(p.stages * stage + tail), stream,
                                           static_cast<unsigned>(p.split), p));
 }
@@ -1192,12 +1213,14 @@ bwg_status run_fp4_gemm(const Fp4Operand& a, const Fp4Operand& b, void* D, int M
   bwg_status st = runtime_device(&rt);
   if (st != BWG_OK) return st;
   if (K == 0) return runtime_status(launch_zero_fill(D, M, n_out, ldd, out_dtype == BWG_OUT_FP32 ? 4 : 2, stream));
-  if (offsets == nullptr && G == 1 && few_rows(M, N, rt.sm_count))
+  const bool dense = offsets == nullptr && G == 1 && !swiglu;
+  const int kernel = dense ? dense_kernel(M, N, (K + kKCols - 1) / kKCols, rt.sm_count) : -1;
+  if (kernel == 0)
     return run_small(a, b, D, M, N, K, ldd, format, out_dtype, rt, stream);
   Fp4GemmParams p;
   std::memset(&p, 0, sizeof(p));
   const long long tok_tiles = (M + kTok - 1LL) / kTok + (offsets != nullptr ? G : 0);  // at most
-  const int nc = swiglu ? 2 : plain_blocks(M, n_out, offsets != nullptr ? G : 0, rt.sm_count / 2);
+  const int nc = dense ? kernel : swiglu ? 2 : grouped_blocks(M, n_out, offsets != nullptr ? G : 0, rt.sm_count / 2);
   p.w_blocks = pad128(N) / 128;
   const int a_rows = offsets != nullptr ? static_cast<int>((M + 127LL * std::min(G, M)) / 128) : pad128(M) / 128;
   if (!fp4_maps(&p, a, b, M, N, K, format, G, a_rows)) return BWG_ERR_CUDA;
@@ -1227,7 +1250,7 @@ bwg_status run_fp4_gemm(const Fp4Operand& a, const Fp4Operand& b, void* D, int M
   // every group adds at most one partial tile of rows
   const long long most = tok_tiles * p.num_w_tiles;
   const int grid = 2 * static_cast<int>(std::min<long long>(most, clusters));
-  return runtime_status(launch_overlapped(k, static_cast<unsigned>(grid), static_cast<unsigned>(threads_of(nc)),
+  return runtime_status(launch_overlapped(k, static_cast<unsigned>(grid), kPairThreads,
                                           static_cast<size_t>(smem), stream, 2, p));
 }
 

@@ -267,10 +267,12 @@ def test_many_tiles_are_exact(ops, M, N, K, fmt):
         assert torch.equal(ops.gemm_fp4(a, b, out_dtype=torch.float32).double(), want)
 
 
-# tiles of 128 rows whose k-blocks 1 to 8 CTAs share, up to one tile for each SM; then just too many tiles for that
+# tiles of 128 rows whose k-blocks 1 to 8 CTAs share, up to one tile for each SM; two rounds of them; pairs of CTAs
+# with one and with two weight blocks
 SHARED = [(129, 130, 2304), (200, 512, 8192), (257, 301, 4992), (1000, 128, 2080), (513, 1024, 7168), (640, 640, 4096),
           (300, 1500, 1792), (260, 1280, 6144), (260, 896, 6144), (129, 9000, 1056), (512, 4096, 1024), (19400, 100, 320),
-          (129, 10000, 544), (193, 9800, 416), (385, 5000, 1184)]
+          (129, 10000, 544), (193, 9800, 416), (385, 5000, 1184),
+          (385, 5001, 2592), (770, 7600, 5024), (580, 6001, 3104), (1151, 2999, 544)]
 
 
 @pytest.mark.parametrize("fmt", FMTS)
