@@ -662,11 +662,11 @@ __device__ __forceinline__ float4 ld_cluster_v4(uint32_t cluster_addr) {
   return v;
 }
 
-// Rank `rank` of F sums rows rank, rank + F, .. of a tile's partials (at `base`
-// in each CTA, 128 floats a row), a warp a row, in rank order, and stores them.
-// F loads of 16 bytes are in flight a lane; twice as many measured the same, 4
-// bytes a lane 0.3 (16 rows) to 3 us more (128 rows).
-template <int F>
+// Rank `rank` of p.split sums rows rank, rank + p.split, .. of a tile's partials
+// (at `base` in each CTA, 128 floats a row), a warp a row, in rank order, and
+// stores them.  All of a row's loads of 16 bytes are in flight; two rows at a
+// time, or code for each cluster size, measured the same, 4 bytes a lane 0.3
+// (16 rows) to 3 us more (128 rows).
 __device__ __forceinline__ void sum_partials(const Fp4SmallParams& p, uint32_t base, int rank, int row0, int rows,
                                              int col0) {
   const bool out32 = p.out_dtype == kOutF32, outbf = p.out_dtype == kOutBF16;
@@ -676,19 +676,22 @@ __device__ __forceinline__ void sum_partials(const Fp4SmallParams& p, uint32_t b
   const int elt = out32 ? 4 : 2;
   const bool whole =
       col + 4 <= p.N && ((reinterpret_cast<uintptr_t>(p.d) | static_cast<uintptr_t>(p.ldd * elt)) & (4 * elt - 1)) == 0;
-  for (int j = rank + F * static_cast<int>(threadIdx.x >> 5); j < rows; j += F * static_cast<int>(blockDim.x >> 5)) {
+  const int split = p.split;
+  for (int j = rank + split * static_cast<int>(threadIdx.x >> 5); j < rows; j += split * static_cast<int>(blockDim.x >> 5)) {
     const uint32_t at = base + static_cast<uint32_t>(j * 128 + ch) * 4u;
-    float4 part[F];
+    float4 part[kSmallMaxSplit];
 #pragma unroll
-    for (int c = 0; c < F; ++c) part[c] = ld_cluster_v4(mapa_shared(at, static_cast<uint32_t>(c)));
+    for (int c = 0; c < kSmallMaxSplit; ++c)
+      if (c < split) part[c] = ld_cluster_v4(mapa_shared(at, static_cast<uint32_t>(c)));
     float x[4] = {part[0].x, part[0].y, part[0].z, part[0].w};
 #pragma unroll
-    for (int c = 1; c < F; ++c) {
-      x[0] += part[c].x;
-      x[1] += part[c].y;
-      x[2] += part[c].z;
-      x[3] += part[c].w;
-    }
+    for (int c = 1; c < kSmallMaxSplit; ++c)
+      if (c < split) {
+        x[0] += part[c].x;
+        x[1] += part[c].y;
+        x[2] += part[c].z;
+        x[3] += part[c].w;
+      }
 #pragma unroll
     for (int i = 0; i < 4; ++i) x[i] *= alpha;
     uint8_t* dst = static_cast<uint8_t*>(p.d) + (static_cast<long long>(row0 + j) * p.ldd + col) * elt;
@@ -711,6 +714,18 @@ __device__ __forceinline__ void sum_partials(const Fp4SmallParams& p, uint32_t b
     }
   }
 }
+
+// Column and row tile of tile t.  Most calls have one row tile, and the division
+// would stand before their first loads.
+struct SmallTile {
+  int c, r;
+  __device__ SmallTile(const Fp4SmallParams& p, int t) : c(t), r(0) {
+    if (p.row_tiles > 1) {
+      c = t / p.row_tiles;
+      r = t - c * p.row_tiles;
+    }
+  }
+};
 
 template <int FMT>
 __global__ void __launch_bounds__(kSmallThreads, 1) fp4_small_kernel(const __grid_constant__ Fp4SmallParams p) {
@@ -772,7 +787,7 @@ __global__ void __launch_bounds__(kSmallThreads, 1) fp4_small_kernel(const __gri
     int s = 0;
     uint32_t ph = 0;
     for (int t = first; t < p.tiles && !aborted; t += stride) {
-      const int ct = t / p.row_tiles, rt = t % p.row_tiles;
+      const SmallTile tile(p, t);
       for (int kb = kb0; kb < kb1; ++kb) {
         if (!warp_wait_cta(empty_bar(s), ph ^ 1u, p.timeout_ns)) {
           if (lane == 0) record_fault(p.err, kFaultTimeout, kRoleProducer, kBarEmpty, s, ph ^ 1u);
@@ -784,11 +799,11 @@ __global__ void __launch_bounds__(kSmallThreads, 1) fp4_small_kernel(const __gri
           const uint32_t sf = st + kWBytes + a_bytes;
           if (weights) {
             mbar_arrive_expect_tx(full_bar(s), kWBytes + a_bytes + 2u * kSfBytes);
-            tma_load_3d_hint(st, &p.map_w, full_bar(s), kb * kKBytes, ct * 128, 0, policy);
-            tma_load_3d_hint(sf, &p.map_ws, full_bar(s), 0, kb * kTilesK, ct, policy);
+            tma_load_3d_hint(st, &p.map_w, full_bar(s), kb * kKBytes, tile.c * 128, 0, policy);
+            tma_load_3d_hint(sf, &p.map_ws, full_bar(s), 0, kb * kTilesK, tile.c, policy);
           } else {
-            tma_load_2d(st + kWBytes, &p.map_a, full_bar(s), kb * kKBytes, rt * 128);
-            tma_load_3d(sf + kSfSlot, &p.map_as, full_bar(s), 0, kb * kTilesK, rt);
+            tma_load_2d(st + kWBytes, &p.map_a, full_bar(s), kb * kKBytes, tile.r * 128);
+            tma_load_3d(sf + kSfSlot, &p.map_as, full_bar(s), 0, kb * kTilesK, tile.r);
           }
         }
         __syncwarp();
@@ -865,8 +880,9 @@ __global__ void __launch_bounds__(kSmallThreads, 1) fp4_small_kernel(const __gri
       }
       tc_fence_after();
       const int ch = static_cast<int>(q * 32u + lane);
-      const int col = t / p.row_tiles * 128 + ch;
-      const int row0 = t % p.row_tiles * 128, rows = min(128, p.M - row0);
+      const SmallTile tile(p, t);
+      const int col = tile.c * 128 + ch;
+      const int row0 = tile.r * 128, rows = min(128, p.M - row0);
       // the warpgroups take alternate chunks of 32 rows
       const int c_first = static_cast<int>((warp - 4u) >> 2) * 32, c_step = (static_cast<int>(blockDim.x >> 7) - 1) * 32;
       if (c_first >= rows && lane == 0) mbar_arrive_local(acc_empty(acc));
@@ -908,18 +924,11 @@ __global__ void __launch_bounds__(kSmallThreads, 1) fp4_small_kernel(const __gri
 
   grid_dependents_launch();
   if (p.split > 1) {
-    const int row0 = first % p.row_tiles * 128, rows = min(128, p.M - row0), col0 = first / p.row_tiles * 128;
+    const SmallTile tile(p, first);
+    const int row0 = tile.r * 128, rows = min(128, p.M - row0), col0 = tile.c * 128;
     // ---- partials: rank r sums rows r, r + split, .. of the tile ---------------
     cluster_sync_all();
-    switch (p.split) {
-      case 2: sum_partials<2>(p, base, rank, row0, rows, col0); break;
-      case 3: sum_partials<3>(p, base, rank, row0, rows, col0); break;
-      case 4: sum_partials<4>(p, base, rank, row0, rows, col0); break;
-      case 5: sum_partials<5>(p, base, rank, row0, rows, col0); break;
-      case 6: sum_partials<6>(p, base, rank, row0, rows, col0); break;
-      case 7: sum_partials<7>(p, base, rank, row0, rows, col0); break;
-      default: sum_partials<8>(p, base, rank, row0, rows, col0); break;
-    }
+    sum_partials(p, base, rank, row0, rows, col0);
   }
   if (__syncthreads_or(aborted ? 1 : 0)) {
     const uint64_t t0 = globaltimer_ns();
