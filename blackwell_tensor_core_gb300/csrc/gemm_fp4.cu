@@ -715,19 +715,22 @@ __device__ __forceinline__ void sum_partials(const Fp4SmallParams& p, uint32_t b
   }
 }
 
-// Column and row tile of tile t.  Most calls have one row tile, and the division
-// would stand before their first loads.
+// Column tile, first row and rows of tile t.  MANY: more than one row tile; its
+// division would stand before the first loads of a call that has one (0.2 us of
+// the 2.6 of 512 x 512, with what follows from it).
+template <bool MANY>
 struct SmallTile {
-  int c, r;
-  __device__ SmallTile(const Fp4SmallParams& p, int t) : c(t), r(0) {
-    if (p.row_tiles > 1) {
+  int c, row0, rows;
+  __device__ SmallTile(const Fp4SmallParams& p, int t) : c(t), row0(0), rows(p.M) {
+    if constexpr (MANY) {
       c = t / p.row_tiles;
-      r = t - c * p.row_tiles;
+      row0 = (t - c * p.row_tiles) * kSmallMaxRows;
+      rows = min(kSmallMaxRows, p.M - row0);
     }
   }
 };
 
-template <int FMT>
+template <int FMT, bool MANY>
 __global__ void __launch_bounds__(kSmallThreads, 1) fp4_small_kernel(const __grid_constant__ Fp4SmallParams p) {
   constexpr int kVec = FMT == kNvfp4 ? 16 : 32;
   constexpr int kTilesK = FMT == kNvfp4 ? 4 : 2;
@@ -783,11 +786,11 @@ __global__ void __launch_bounds__(kSmallThreads, 1) fp4_small_kernel(const __gri
   if (warp == 0 || warp == 2) {
     // ---- TMA producers: weights, activations ---------------------------------
     const bool weights = warp == 0;
-    const uint64_t policy = p.row_tiles == 1 ? l2_policy_evict_first() : l2_policy_evict_normal();
+    const uint64_t policy = MANY ? l2_policy_evict_normal() : l2_policy_evict_first();
     int s = 0;
     uint32_t ph = 0;
     for (int t = first; t < p.tiles && !aborted; t += stride) {
-      const SmallTile tile(p, t);
+      const SmallTile<MANY> tile(p, t);
       for (int kb = kb0; kb < kb1; ++kb) {
         if (!warp_wait_cta(empty_bar(s), ph ^ 1u, p.timeout_ns)) {
           if (lane == 0) record_fault(p.err, kFaultTimeout, kRoleProducer, kBarEmpty, s, ph ^ 1u);
@@ -802,8 +805,8 @@ __global__ void __launch_bounds__(kSmallThreads, 1) fp4_small_kernel(const __gri
             tma_load_3d_hint(st, &p.map_w, full_bar(s), kb * kKBytes, tile.c * 128, 0, policy);
             tma_load_3d_hint(sf, &p.map_ws, full_bar(s), 0, kb * kTilesK, tile.c, policy);
           } else {
-            tma_load_2d(st + kWBytes, &p.map_a, full_bar(s), kb * kKBytes, tile.r * 128);
-            tma_load_3d(sf + kSfSlot, &p.map_as, full_bar(s), 0, kb * kTilesK, tile.r);
+            tma_load_2d(st + kWBytes, &p.map_a, full_bar(s), kb * kKBytes, tile.row0);
+            tma_load_3d(sf + kSfSlot, &p.map_as, full_bar(s), 0, kb * kTilesK, tile.row0 / 128);
           }
         }
         __syncwarp();
@@ -880,9 +883,8 @@ __global__ void __launch_bounds__(kSmallThreads, 1) fp4_small_kernel(const __gri
       }
       tc_fence_after();
       const int ch = static_cast<int>(q * 32u + lane);
-      const SmallTile tile(p, t);
-      const int col = tile.c * 128 + ch;
-      const int row0 = tile.r * 128, rows = min(128, p.M - row0);
+      const SmallTile<MANY> tile(p, t);
+      const int col = tile.c * 128 + ch, row0 = tile.row0, rows = tile.rows;
       // the warpgroups take alternate chunks of 32 rows
       const int c_first = static_cast<int>((warp - 4u) >> 2) * 32, c_step = (static_cast<int>(blockDim.x >> 7) - 1) * 32;
       if (c_first >= rows && lane == 0) mbar_arrive_local(acc_empty(acc));
@@ -924,11 +926,10 @@ __global__ void __launch_bounds__(kSmallThreads, 1) fp4_small_kernel(const __gri
 
   grid_dependents_launch();
   if (p.split > 1) {
-    const SmallTile tile(p, first);
-    const int row0 = tile.r * 128, rows = min(128, p.M - row0), col0 = tile.c * 128;
+    const SmallTile<MANY> tile(p, first);
     // ---- partials: rank r sums rows r, r + split, .. of the tile ---------------
     cluster_sync_all();
-    sum_partials(p, base, rank, row0, rows, col0);
+    sum_partials(p, base, rank, tile.row0, tile.rows, tile.c * 128);
   }
   if (__syncthreads_or(aborted ? 1 : 0)) {
     const uint64_t t0 = globaltimer_ns();
@@ -1114,16 +1115,18 @@ int small_split(int tiles, int rows, int kb, int sm_count, const int* clusters) 
 bwg_status run_small(const Fp4Operand& a, const Fp4Operand& b, void* D, int M, int N, int K, int ldd, int format,
                      int out_dtype, const Runtime& rt, cudaStream_t stream) {
   using Kernel = void (*)(Fp4SmallParams);
-  const Kernel k = format == kNvfp4 ? fp4_small_kernel<kNvfp4> : fp4_small_kernel<kMxfp4>;
+  const bool many = M > kSmallMaxRows;
+  const Kernel k = format == kNvfp4 ? (many ? fp4_small_kernel<kNvfp4, true> : fp4_small_kernel<kNvfp4, false>)
+                                    : (many ? fp4_small_kernel<kMxfp4, true> : fp4_small_kernel<kMxfp4, false>);
   // co-resident clusters by size, once per device (every call of this kernel
   // takes more than half of an SM's shared memory)
   static std::mutex mu;
   static struct {
     bool ready;
     int clusters[kSmallMaxSplit + 1];
-  } seen[64][2];
+  } seen[64][2][2];
   if (rt.device >= 64) return BWG_ERR_UNSUPPORTED;
-  auto& info = seen[rt.device][format];
+  auto& info = seen[rt.device][format][many];
   {
     std::lock_guard<std::mutex> lock(mu);
     if (!info.ready) {
