@@ -185,6 +185,17 @@ def _new(shape, dtype, dev, stream) -> torch.Tensor:
         return torch.empty(shape, dtype=dtype, device=dev)
 
 
+# The library takes sizes and row strides as 32-bit ints.  ctypes keeps the
+# low 32 bits of what does not fit, so that 2^32 + 64 would pass for 64: every
+# size that a caller gives is checked here first.
+_INT_MAX = (1 << 31) - 1
+
+
+def _fits(what: str, *sizes: int) -> None:
+    if max(sizes) > _INT_MAX:
+        raise ValueError("%s: %d is past 2^31 - 1" % (what, max(sizes)))
+
+
 def _matrix(t: torch.Tensor, name: str) -> int:
     if t.dim() != 2:
         raise ValueError("%s must be 2-D" % name)
@@ -192,6 +203,7 @@ def _matrix(t: torch.Tensor, name: str) -> int:
         raise ValueError("%s must be row-major with unit column stride" % name)
     if not t.is_cuda:
         raise ValueError("%s must be a CUDA tensor" % name)
+    _fits("size or row stride of " + name, *t.shape, t.stride(0))
     return t.stride(0)
 
 
@@ -268,6 +280,7 @@ def grouped_gemm(A: torch.Tensor, Bs: list, group_offsets: torch.Tensor,
         raise ValueError("group_offsets must be a CUDA int32 tensor with G+1 entries")
     if not A.is_contiguous():
         raise ValueError("A must be dense [M_total, K]")
+    _fits("rows, columns or groups", M_total, K, N, G)
     n_out = N // 2 if swiglu else N
     if out is None:
         out = torch.empty((M_total, n_out), dtype=A.dtype, device=A.device)
@@ -324,6 +337,7 @@ def gemm_bf16_host(A_host: torch.Tensor, B_host: torch.Tensor, D_host: torch.Ten
     for name, t in (("A_host", A_host), ("B_host", B_host), ("D_host", D_host)):
         if t.is_cuda or not t.is_contiguous():
             raise ValueError("%s must be a dense host tensor" % name)
+        _fits("size of " + name, *t.shape)
     need = {"dA": M * K * 2, "dB": K * N * 2, "dD": M * N * D_host.element_size()}
     for name, t in (("dA", dA), ("dB", dB), ("dD", dD)):
         if not t.is_cuda or not t.is_contiguous() or t.numel() * t.element_size() < need[name]:
@@ -435,6 +449,7 @@ def moe_sort(expert_ids: torch.Tensor, num_experts: int, stream=None) -> Routing
         raise ValueError("num_experts must be at least 1")
     dev = expert_ids.device
     pairs = expert_ids.numel()
+    _fits("pairs or experts", pairs, num_experts)
     offsets = _new((num_experts + 1,), torch.int32, dev, stream)
     order = _new((pairs,), torch.int32, dev, stream)
     position = _new(expert_ids.shape, torch.int32, dev, stream)
@@ -452,6 +467,8 @@ def _routing(r: Routing, dev) -> tuple[int, int, int]:
     ps, os_ = position.shape, offsets.shape
     if len(ps) != 2 or len(os_) != 1 or os_[0] < 2 or ps[1] < 1:
         raise ValueError("routing must hold offsets [E + 1] and position [T, k]")
+    if ps[0] * ps[1] > _INT_MAX or os_[0] > _INT_MAX:
+        raise ValueError("routing has more than 2^31 - 1 pairs or experts")
     return ps[0], ps[1], os_[0] - 1
 
 
@@ -467,11 +484,13 @@ def _rows(t: torch.Tensor, name: str, rows: int) -> int:
         raise ValueError("%s must be row-major with unit column stride" % name)
     if have != rows:
         raise ValueError("%s must have %d rows, got %d" % (name, rows, have))
-    if ld >= cols:
-        return ld
-    if rows > 1:
+    if rows <= 1:
+        ld = cols  # torch gives a single row any stride
+    elif ld < cols:
         raise ValueError("%s must not be a broadcast view: its rows overlap" % name)
-    return cols  # torch gives a single row any stride
+    if ld > _INT_MAX or rows > _INT_MAX:
+        raise ValueError("%s: %d rows with a row stride of %d are past 2^31 - 1" % (name, rows, ld))
+    return ld
 
 
 def _out_rows(out, rows: int, cols: int, dtype, dev, stream) -> tuple:
@@ -602,6 +621,8 @@ def _fp4_offsets(off, dev):
         return None
     if off.dtype != torch.int32 or off.dim() != 1 or off.shape[0] < 2 or not off.is_contiguous() or off.device != dev:
         raise ValueError("group_offsets must be a dense int32 tensor [groups + 1] on %s" % dev)
+    if off.shape[0] > _INT_MAX:
+        raise ValueError("group_offsets has more than 2^31 - 1 groups")
     return off.data_ptr()
 
 
@@ -623,6 +644,8 @@ def _fp4_check(q: Fp4Matrix, name: str) -> int:
     if codes.dtype != torch.uint8 or codes.dim() != 2 or not codes.is_contiguous() or not codes.is_cuda:
         raise ValueError("%s.codes must be a dense CUDA uint8 tensor [rows, K / 2]" % name)
     rows, half = codes.shape
+    if rows > _INT_MAX or 2 * half > _INT_MAX or q.groups > _INT_MAX:
+        raise ValueError("%s: rows, columns or groups past 2^31 - 1" % name)
     need = _fp4_scale_bytes(rows, 2 * half, fmt, q.groups, ragged)
     if need < 0:
         raise ValueError("%s: %d rows do not make %d equal groups" % (name, rows, q.groups))
