@@ -173,7 +173,20 @@ def _stream_handle(stream, device) -> int:
         # object around it (7 us of a 20 us call)
         index = device if isinstance(device, int) else device.index
         return torch._C._cuda_getCurrentRawStream(index)
+    if not isinstance(device, int):
+        of = getattr(stream, "device", device)
+        if of != device:
+            raise ValueError("the stream is of %s, the tensors are on %s" % (of, device))
     return int(stream.cuda_stream)
+
+
+def _on(device, fn, *args):
+    """fn(*args) with `device` current: the library launches on the current
+    device, and the default stream of every device has the same handle."""
+    if device.index == torch._C._cuda_getDevice():
+        return fn(*args)
+    with torch.cuda.device(device):
+        return fn(*args)
 
 
 def _new(shape, dtype, dev, stream) -> torch.Tensor:
@@ -230,8 +243,8 @@ def gemm(A: torch.Tensor, B: torch.Tensor, out: torch.Tensor | None = None,
         fn = gemm_bf16_nt if A.dtype == torch.bfloat16 else gemm_fp16_nt
     else:
         fn = gemm_bf16 if A.dtype == torch.bfloat16 else gemm_fp16
-    fn(A.data_ptr(), B.data_ptr(), out.data_ptr(), M, N, K, lda, ldb, ldd, _OUT_CODES[out.dtype],
-       _stream_handle(stream, A.device))
+    _on(A.device, fn, A.data_ptr(), B.data_ptr(), out.data_ptr(), M, N, K, lda, ldb, ldd, _OUT_CODES[out.dtype],
+        _stream_handle(stream, A.device))
     return out
 
 
@@ -295,8 +308,8 @@ def grouped_gemm(A: torch.Tensor, Bs: list, group_offsets: torch.Tensor,
         fn = grouped_gemm_bf16_nt if bf else grouped_gemm_fp16_nt
     else:
         fn = grouped_gemm_bf16 if bf else grouped_gemm_fp16
-    fn(A.data_ptr(), [b.data_ptr() for b in Bs], out.data_ptr(), group_offsets.data_ptr(), G, M_total,
-       N, K, _stream_handle(stream, A.device))
+    _on(A.device, fn, A.data_ptr(), [b.data_ptr() for b in Bs], out.data_ptr(), group_offsets.data_ptr(), G,
+        M_total, N, K, _stream_handle(stream, A.device))
     return out
 
 
@@ -342,9 +355,9 @@ def gemm_bf16_host(A_host: torch.Tensor, B_host: torch.Tensor, D_host: torch.Ten
     for name, t in (("dA", dA), ("dB", dB), ("dD", dD)):
         if not t.is_cuda or not t.is_contiguous() or t.numel() * t.element_size() < need[name]:
             raise ValueError("%s must be a dense CUDA buffer of at least %d bytes" % (name, need[name]))
-    _check(lib().gemm_bf16_host(A_host.data_ptr(), B_host.data_ptr(), D_host.data_ptr(), M, N, K,
-                                _OUT_CODES[D_host.dtype], dA.data_ptr(), dB.data_ptr(), dD.data_ptr(),
-                                _stream_handle(stream, dA.device)), "gemm_bf16_host")
+    _check(_on(dA.device, lib().gemm_bf16_host, A_host.data_ptr(), B_host.data_ptr(), D_host.data_ptr(), M, N, K,
+               _OUT_CODES[D_host.dtype], dA.data_ptr(), dB.data_ptr(), dD.data_ptr(),
+               _stream_handle(stream, dA.device)), "gemm_bf16_host")
 
 
 def last_device_error(stream=None) -> tuple[int, int]:
@@ -453,8 +466,8 @@ def moe_sort(expert_ids: torch.Tensor, num_experts: int, stream=None) -> Routing
     offsets = _new((num_experts + 1,), torch.int32, dev, stream)
     order = _new((pairs,), torch.int32, dev, stream)
     position = _new(expert_ids.shape, torch.int32, dev, stream)
-    _check(lib().moe_sort(expert_ids.data_ptr(), expert_ids.element_size(), pairs, num_experts, offsets.data_ptr(),
-                          order.data_ptr(), position.data_ptr(), _stream_handle(stream, dev)), "moe_sort")
+    _check(_on(dev, lib().moe_sort, expert_ids.data_ptr(), expert_ids.element_size(), pairs, num_experts,
+               offsets.data_ptr(), order.data_ptr(), position.data_ptr(), _stream_handle(stream, dev)), "moe_sort")
     return Routing(offsets, order, position)
 
 
@@ -514,9 +527,8 @@ def moe_dispatch(x: torch.Tensor, routing: Routing, out: torch.Tensor | None = N
     ldx = _rows(x, "x", T)
     H, dtype, dev = x.shape[1], x.dtype, x.device
     out, ldo = _out_rows(out, T * k, H, dtype, dev, stream)
-    _check(lib().moe_dispatch(x.data_ptr(), _OUT_CODES[dtype], T, H, ldx, k, routing.position.data_ptr(),
-                              routing.offsets.data_ptr(), E, out.data_ptr(), ldo, _stream_handle(stream, dev)),
-           "moe_dispatch")
+    _check(_on(dev, lib().moe_dispatch, x.data_ptr(), _OUT_CODES[dtype], T, H, ldx, k, routing.position.data_ptr(),
+               routing.offsets.data_ptr(), E, out.data_ptr(), ldo, _stream_handle(stream, dev)), "moe_dispatch")
     return out
 
 
@@ -527,9 +539,9 @@ def moe_dispatch_grad(d_rows: torch.Tensor, routing: Routing, out: torch.Tensor 
     ldr = _rows(d_rows, "d_rows", T * k)
     H, dtype, dev = d_rows.shape[1], d_rows.dtype, d_rows.device
     out, ldo = _out_rows(out, T, H, dtype, dev, stream)
-    _check(lib().moe_dispatch_grad(d_rows.data_ptr(), _OUT_CODES[dtype], T, H, ldr, k, routing.position.data_ptr(),
-                                   routing.offsets.data_ptr(), E, out.data_ptr(), ldo, _stream_handle(stream, dev)),
-           "moe_dispatch_grad")
+    _check(_on(dev, lib().moe_dispatch_grad, d_rows.data_ptr(), _OUT_CODES[dtype], T, H, ldr, k,
+               routing.position.data_ptr(), routing.offsets.data_ptr(), E, out.data_ptr(), ldo,
+               _stream_handle(stream, dev)), "moe_dispatch_grad")
     return out
 
 
@@ -542,9 +554,9 @@ def moe_combine(rows: torch.Tensor, routing: Routing, weights: torch.Tensor, out
     H, dtype, dev = rows.shape[1], rows.dtype, rows.device
     _pair_weights(weights, T, k, dev)
     out, ldo = _out_rows(out, T, H, dtype, dev, stream)
-    _check(lib().moe_combine(rows.data_ptr(), _OUT_CODES[dtype], T, H, ldr, k, weights.data_ptr(),
-                             routing.position.data_ptr(), routing.offsets.data_ptr(), E, out.data_ptr(), ldo,
-                             _stream_handle(stream, dev)), "moe_combine")
+    _check(_on(dev, lib().moe_combine, rows.data_ptr(), _OUT_CODES[dtype], T, H, ldr, k, weights.data_ptr(),
+               routing.position.data_ptr(), routing.offsets.data_ptr(), E, out.data_ptr(), ldo,
+               _stream_handle(stream, dev)), "moe_combine")
     return out
 
 
@@ -558,10 +570,10 @@ def moe_combine_grad(d_out: torch.Tensor, rows: torch.Tensor, routing: Routing, 
     _pair_weights(weights, T, k, rows.device)
     d_rows = _new((T * k, rows.shape[1]), rows.dtype, rows.device, stream)
     d_weights = _new((T, k), torch.float32, rows.device, stream)
-    _check(lib().moe_combine_grad(d_out.data_ptr(), rows.data_ptr(), _OUT_CODES[rows.dtype], T, rows.shape[1], ldy,
-                                  ldr, k, weights.data_ptr(), routing.position.data_ptr(),
-                                  routing.offsets.data_ptr(), E, d_rows.data_ptr(), rows.shape[1],
-                                  d_weights.data_ptr(), _stream_handle(stream, rows.device)), "moe_combine_grad")
+    _check(_on(rows.device, lib().moe_combine_grad, d_out.data_ptr(), rows.data_ptr(), _OUT_CODES[rows.dtype], T,
+               rows.shape[1], ldy, ldr, k, weights.data_ptr(), routing.position.data_ptr(),
+               routing.offsets.data_ptr(), E, d_rows.data_ptr(), rows.shape[1], d_weights.data_ptr(),
+               _stream_handle(stream, rows.device)), "moe_combine_grad")
     return d_rows, d_weights
 
 
@@ -679,11 +691,10 @@ def quantize_fp4(x: torch.Tensor, format: str = "nvfp4", global_scale: torch.Ten
     elif groups < 1 or rows % groups:
         raise ValueError("%d rows do not make %d equal groups" % (rows, groups))
     g, n_global = _fp4_global(global_scale, fmt, groups, dev)
-    L = lib()
     codes = _new((rows, K // 2), torch.uint8, dev, stream)
     scales = _new((_fp4_scale_bytes(rows, K, fmt, groups, off is not None),), torch.uint8, dev, stream)
-    _check(L.quantize_fp4(x.data_ptr(), _OUT_CODES[x.dtype], rows, K, ldx, fmt, g, n_global, off, groups,
-                          codes.data_ptr(), scales.data_ptr(), _stream_handle(stream, dev)), "quantize_fp4")
+    _check(_on(dev, lib().quantize_fp4, x.data_ptr(), _OUT_CODES[x.dtype], rows, K, ldx, fmt, g, n_global, off,
+               groups, codes.data_ptr(), scales.data_ptr(), _stream_handle(stream, dev)), "quantize_fp4")
     return Fp4Matrix(codes, scales, format, global_scale, group_offsets, groups)
 
 
@@ -696,9 +707,8 @@ def dequantize_fp4(q: Fp4Matrix, out_dtype: torch.dtype = torch.bfloat16, out: t
     off = _fp4_offsets(q.group_offsets, dev)
     g, n_global = _fp4_global(q.global_scale, fmt, q.groups, dev)
     out, ldo = _fp4_out(out, out_dtype, rows, K, dev, stream)
-    _check(lib().dequantize_fp4(q.codes.data_ptr(), q.scales.data_ptr(), fmt, g, n_global, off, q.groups,
-                                out.data_ptr(), _OUT_CODES[out.dtype], rows, K, ldo,
-                                _stream_handle(stream, dev)), "dequantize_fp4")
+    _check(_on(dev, lib().dequantize_fp4, q.codes.data_ptr(), q.scales.data_ptr(), fmt, g, n_global, off, q.groups,
+               out.data_ptr(), _OUT_CODES[out.dtype], rows, K, ldo, _stream_handle(stream, dev)), "dequantize_fp4")
     return out
 
 
@@ -733,9 +743,9 @@ def gemm_fp4(A: Fp4Matrix, B: Fp4Matrix, out: torch.Tensor | None = None,
     out, ldo = _fp4_out(out, out_dtype, M, N, dev, stream)
     ga, _ = _fp4_global(A.global_scale, fmt, 1, dev)
     gb, _ = _fp4_global(B.global_scale, fmt, 1, dev)
-    _check(lib().gemm_fp4(A.codes.data_ptr(), A.scales.data_ptr(), ga, B.codes.data_ptr(), B.scales.data_ptr(), gb,
-                          fmt, out.data_ptr(), M, N, K, ldo, _OUT_CODES[out.dtype],
-                          _stream_handle(stream, dev)), "gemm_fp4")
+    _check(_on(dev, lib().gemm_fp4, A.codes.data_ptr(), A.scales.data_ptr(), ga, B.codes.data_ptr(),
+               B.scales.data_ptr(), gb, fmt, out.data_ptr(), M, N, K, ldo, _OUT_CODES[out.dtype],
+               _stream_handle(stream, dev)), "gemm_fp4")
     return out
 
 
@@ -761,9 +771,8 @@ def grouped_gemm_fp4(A: Fp4Matrix, B: Fp4Matrix, swiglu: bool = False, out: torc
     ga, na = _fp4_global(A.global_scale, fmt, 1, dev)
     gb, n_global = _fp4_global(B.global_scale, fmt, G, dev)
     work = _new((M, N), torch.float32, dev, stream) if swiglu and N % 256 else None
-    _check(lib().grouped_gemm_fp4(A.codes.data_ptr(), A.scales.data_ptr(), ga, B.codes.data_ptr(),
-                                  B.scales.data_ptr(), gb, n_global, fmt, out.data_ptr(), off, G, M, N, K,
-                                  ldo, _OUT_CODES[out.dtype], 1 if swiglu else 0,
-                                  None if work is None else work.data_ptr(), _stream_handle(stream, dev)),
+    _check(_on(dev, lib().grouped_gemm_fp4, A.codes.data_ptr(), A.scales.data_ptr(), ga, B.codes.data_ptr(),
+               B.scales.data_ptr(), gb, n_global, fmt, out.data_ptr(), off, G, M, N, K, ldo, _OUT_CODES[out.dtype],
+               1 if swiglu else 0, None if work is None else work.data_ptr(), _stream_handle(stream, dev)),
            "grouped_gemm_fp4")
     return out

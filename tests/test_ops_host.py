@@ -124,3 +124,89 @@ def test_sizes_past_32_bits_are_refused(rec):
         with pytest.raises(ValueError):
             call()
     assert rec.calls == []
+
+
+# ------------------------------------------------------------- devices ---
+
+def _every_call(dev):
+    f32 = dict(dtype=torch.float32, dev=dev)
+    i32 = dict(dtype=torch.int32, dev=dev)
+    r = routing(4, 2, 3, dev)
+    off = cuda(3, **i32)
+    return {
+        "moe_sort": lambda **s: ops.moe_sort(cuda(4, 2, **i32), 3, **s),
+        "moe_dispatch": lambda **s: ops.moe_dispatch(cuda(4, 64, dev=dev), r, **s),
+        "moe_dispatch_grad": lambda **s: ops.moe_dispatch_grad(cuda(8, 64, dev=dev), r, **s),
+        "moe_combine": lambda **s: ops.moe_combine(cuda(8, 64, dev=dev), r, cuda(4, 2, **f32), **s),
+        "moe_combine_grad": lambda **s: ops.moe_combine_grad(cuda(4, 64, dev=dev), cuda(8, 64, dev=dev), r,
+                                                             cuda(4, 2, **f32), **s),
+        "quantize_fp4": lambda **s: ops.quantize_fp4(cuda(4, 64, dev=dev), **s),
+        "dequantize_fp4": lambda **s: ops.dequantize_fp4(fp4(4, 64, dev=dev), **s),
+        "gemm_fp4": lambda **s: ops.gemm_fp4(fp4(4, 64, dev=dev), fp4(64, 64, dev=dev), **s),
+        "grouped_gemm_fp4": lambda **s: ops.grouped_gemm_fp4(fp4(4, 64, offsets=off, dev=dev),
+                                                             fp4(512, 64, groups=2, dev=dev), **s),
+        "gemm_bf16": lambda **s: ops.gemm(cuda(4, 64, dev=dev), cuda(64, 64, dev=dev), **s),
+        "gemm_bf16_nt": lambda **s: ops.gemm(cuda(4, 64, dev=dev), cuda(64, 64, dev=dev), b_transposed=True, **s),
+        "grouped_gemm_bf16": lambda **s: ops.grouped_gemm(cuda(4, 64, dev=dev), [cuda(64, 64, dev=dev)] * 2, off, **s),
+        "grouped_gemm_swiglu_bf16": lambda **s: ops.grouped_gemm(cuda(4, 64, dev=dev), [cuda(64, 64, dev=dev)] * 2,
+                                                                 off, swiglu=True, **s),
+    }
+
+
+CALLS = ["moe_sort", "moe_dispatch", "moe_dispatch_grad", "moe_combine", "moe_combine_grad", "quantize_fp4",
+         "dequantize_fp4", "gemm_fp4", "grouped_gemm_fp4", "gemm_bf16", "gemm_bf16_nt", "grouped_gemm_bf16",
+         "grouped_gemm_swiglu_bf16"]
+
+
+@pytest.fixture
+def devices(rec, monkeypatch):
+    """Which device is current, as torch.cuda.device would make it, and which
+    one was at each call of the library."""
+    now = [0]
+    seen = []
+
+    class Device:
+        def __init__(self, device):
+            self.index = device if isinstance(device, int) else device.index
+
+        def __enter__(self):
+            self.before, now[0] = now[0], self.index
+
+        def __exit__(self, *exc):
+            now[0] = self.before
+
+    monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: now[0], raising=False)
+    monkeypatch.setattr(torch.cuda, "device", Device)
+    inner = Recorder.__getattr__
+
+    def __getattr__(self, name):
+        call = inner(self, name)
+
+        def with_device(*args):
+            seen.append((name, now[0]))
+            return call(*args)
+        return with_device
+
+    monkeypatch.setattr(Recorder, "__getattr__", __getattr__)
+    return seen
+
+
+@pytest.mark.parametrize("name", CALLS)
+@pytest.mark.parametrize("index", [0, 1])
+def test_calls_run_on_their_tensors_device(devices, name, index):
+    """The library launches on the current device: on the tensors' one during
+    the call, and on the caller's again after it."""
+    _every_call("cuda:%d" % index)[name]()
+    assert devices == [(name, index)]
+    assert torch._C._cuda_getDevice() == 0
+
+
+@pytest.mark.parametrize("name", CALLS)
+def test_streams_of_another_device_are_refused(devices, name, monkeypatch):
+    import contextlib
+    monkeypatch.setattr(torch.cuda, "stream", lambda s: contextlib.nullcontext())
+    with pytest.raises(ValueError):
+        _every_call("cuda:0")[name](stream=types.SimpleNamespace(device=torch.device("cuda:1"), cuda_stream=7))
+    assert devices == []
+    _every_call("cuda:0")[name](stream=types.SimpleNamespace(device=torch.device("cuda:0"), cuda_stream=7))
+    assert devices == [(name, 0)]
