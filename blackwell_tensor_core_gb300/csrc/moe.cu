@@ -358,12 +358,12 @@ __global__ void __launch_bounds__(kRowThreads) moe_combine_kernel(const __grid_c
     // all positions and weights, then all rows: nothing between the loads
 #pragma unroll
     for (int a = 0; a < P; ++a) {
-      row[a] = j0 + a < p.k ? p.position[p0 + j0 + a] : kept;
+      row[a] = j0 + a < p.k ? p.position[p0 + j0 + a] : -1;
       w[a] = p.weights != nullptr && j0 + a < p.k ? p.weights[p0 + j0 + a] : 1.f;
     }
 #pragma unroll
     for (int a = 0; a < P; ++a) {
-      bad |= static_cast<unsigned>(row[a]) > static_cast<unsigned>(p.pairs);
+      bad |= j0 + a < p.k && static_cast<unsigned>(row[a]) >= static_cast<unsigned>(p.pairs);
       has[a] = row[a] >= 0 && row[a] < kept;
       const R* src = reinterpret_cast<const R*>(static_cast<const T*>(p.src) + (has[a] ? row[a] : 0) * p.ld_src);
 #pragma unroll
