@@ -677,7 +677,7 @@ def quantize_fp4(x: torch.Tensor, format: str = "nvfp4", global_scale: torch.Ten
         if group_offsets is not None or not x.is_contiguous():
             raise ValueError("stacked weights must be dense [groups, N, K], without group_offsets")
         groups = x.shape[0]
-        x = x.reshape(-1, x.shape[2])
+        x = x.reshape(groups * x.shape[1], x.shape[2])
     if x.dtype not in _OUT_CODES:
         raise TypeError("x must be bfloat16, float16 or float32")
     rows, K = x.shape

@@ -210,3 +210,10 @@ def test_streams_of_another_device_are_refused(devices, name, monkeypatch):
     assert devices == []
     _every_call("cuda:0")[name](stream=types.SimpleNamespace(device=torch.device("cuda:0"), cuda_stream=7))
     assert devices == [(name, 0)]
+
+
+def test_stacked_weights_without_columns(rec):
+    q = ops.quantize_fp4(cuda(3, 8, 0))
+    assert q.shape == (24, 0) and q.groups == 3
+    (name, args), = rec.calls
+    assert name == "quantize_fp4" and args[2:4] == (24, 0) and args[9] == 3
