@@ -942,14 +942,22 @@ __global__ void __launch_bounds__(kSmallThreads, 1) fp4_small_kernel(const __gri
   }
 }
 
+// Whether a row (the same in all of a block's threads) is one of a group's: the
+// clamped tables give it one where any of the offsets lies above it.
+__device__ __forceinline__ bool row_has_group(const int* offsets, int G, int row) {
+  bool above = false;
+  for (int i = static_cast<int>(threadIdx.x); i <= G; i += static_cast<int>(blockDim.x)) above |= offsets[i] > row;
+  return __syncthreads_or(above) != 0;
+}
+
 // SwiGLU of FP32 rows [gate | up], for halves that the fused epilogue cannot
-// pair (it needs both to start on a tile of scales): rows before *last only.
+// pair (it needs both to start on a tile of scales): the groups' rows only.
 template <class T>
-__global__ void fp4_swiglu_kernel(const float* __restrict__ x, const int* __restrict__ last, int n_out, long long ldd,
-                                  T* __restrict__ h) {
+__global__ void fp4_swiglu_kernel(const float* __restrict__ x, const int* __restrict__ offsets, int G, int n_out,
+                                  long long ldd, T* __restrict__ h) {
   grid_dependency_wait();
   const int row = static_cast<int>(blockIdx.x);
-  if (row >= *last) return;
+  if (!row_has_group(offsets, G, row)) return;
   const float* r = x + static_cast<long long>(row) * 2 * n_out;
   for (int c = static_cast<int>(threadIdx.x); c < n_out; c += static_cast<int>(blockDim.x)) {
     const float y = silu_mul(r[c], r[n_out + c]);
@@ -1285,13 +1293,13 @@ bwg_status run_swiglu_two_steps(const Fp4Operand& a, const Fp4Operand& b, void* 
   const unsigned blocks = static_cast<unsigned>(M);
   cudaError_t e;
   if (out_dtype == BWG_OUT_FP32)
-    e = launch_overlapped(fp4_swiglu_kernel<float>, blocks, static_cast<unsigned>(threads), 0, stream, 1, x, offsets + G, n,
+    e = launch_overlapped(fp4_swiglu_kernel<float>, blocks, static_cast<unsigned>(threads), 0, stream, 1, x, offsets, G, n,
                           static_cast<long long>(ldh), static_cast<float*>(H));
   else if (out_dtype == BWG_OUT_FP16)
-    e = launch_overlapped(fp4_swiglu_kernel<__half>, blocks, static_cast<unsigned>(threads), 0, stream, 1, x, offsets + G, n,
+    e = launch_overlapped(fp4_swiglu_kernel<__half>, blocks, static_cast<unsigned>(threads), 0, stream, 1, x, offsets, G, n,
                           static_cast<long long>(ldh), static_cast<__half*>(H));
   else
-    e = launch_overlapped(fp4_swiglu_kernel<__nv_bfloat16>, blocks, static_cast<unsigned>(threads), 0, stream, 1, x, offsets + G, n,
+    e = launch_overlapped(fp4_swiglu_kernel<__nv_bfloat16>, blocks, static_cast<unsigned>(threads), 0, stream, 1, x, offsets, G, n,
                           static_cast<long long>(ldh), static_cast<__nv_bfloat16*>(H));
   return runtime_status(e);
 }
