@@ -950,6 +950,24 @@ __device__ __forceinline__ bool row_has_group(const int* offsets, int G, int row
   return __syncthreads_or(above) != 0;
 }
 
+// A grouped product over no columns: zeros in the groups' rows, a block a row.
+// The first block checks the offsets as build_tables does.
+__global__ void fp4_zero_rows_kernel(const int* offsets, int G, int M, uint8_t* d, size_t ld_bytes, size_t row_bytes,
+                                     unsigned long long* err) {
+  grid_dependency_wait();
+  const int row = static_cast<int>(blockIdx.x);
+  if (row == 0) {
+    bool bad = false;
+    for (int g = static_cast<int>(threadIdx.x); g < G; g += static_cast<int>(blockDim.x)) {
+      const int a = offsets[g], b = offsets[g + 1];
+      bad |= (g == 0 && a != 0) || b < a || a < 0 || b > M;
+    }
+    if (bad) record_fault(err, kFaultBadOffsets, 0, 0, 0, 0);
+  }
+  if (!row_has_group(offsets, G, row)) return;
+  for (size_t i = threadIdx.x; i < row_bytes; i += blockDim.x) d[static_cast<size_t>(row) * ld_bytes + i] = 0;
+}
+
 // SwiGLU of FP32 rows [gate | up], for halves that the fused epilogue cannot
 // pair (it needs both to start on a tile of scales): the groups' rows only.
 template <class T>
@@ -1232,7 +1250,13 @@ bwg_status run_fp4_gemm(const Fp4Operand& a, const Fp4Operand& b, void* D, int M
   Runtime rt;
   bwg_status st = runtime_device(&rt);
   if (st != BWG_OK) return st;
-  if (K == 0) return runtime_status(launch_zero_fill(D, M, n_out, ldd, out_dtype == BWG_OUT_FP32 ? 4 : 2, stream));
+  if (K == 0) {
+    const int elt = out_dtype == BWG_OUT_FP32 ? 4 : 2;
+    if (offsets == nullptr) return runtime_status(launch_zero_fill(D, M, n_out, ldd, elt, stream));
+    return runtime_status(launch_overlapped(fp4_zero_rows_kernel, static_cast<unsigned>(M), 128, 0, stream, 1, offsets, G,
+                                            M, static_cast<uint8_t*>(D), static_cast<size_t>(ldd) * elt,
+                                            static_cast<size_t>(n_out) * elt, rt.err));
+  }
   const bool dense = offsets == nullptr && G == 1 && !swiglu;
   const int kernel = dense ? dense_kernel(M, N, (K + kKCols - 1) / kKCols, rt.sm_count) : -1;
   if (kernel == 0)
