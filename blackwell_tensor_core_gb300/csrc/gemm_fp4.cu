@@ -457,7 +457,7 @@ __global__ void __launch_bounds__(kPairThreads, 1) fp4_pair_kernel(const __grid_
     const uint32_t q = warp & 3u;
     const int grp = static_cast<int>((warp - 4u) >> 2);  // SwiGLU: warpgroup 0 or 1
     const uint32_t acc_empty0 = mapa_shared(acc_empty(0), 0);
-    const float ga = p.a_global != nullptr ? __ldg(p.a_global) : 1.f;
+    const float ga = p.a_global != nullptr ? *p.a_global : 1.f;
     const bool out32 = p.out_dtype == kOutF32;
     const bool outbf = p.out_dtype == kOutBF16;
     const uint32_t t_lane = (q * 32u) << 16;
@@ -470,7 +470,7 @@ __global__ void __launch_bounds__(kPairThreads, 1) fp4_pair_kernel(const __grid_
       if (lane == 0) mbar_arrive_cluster_relaxed(acc_empty0 + 8u * slot);
     };
     auto alpha_of = [&](int g) {
-      return p.b_global != nullptr ? ga * __ldg(p.b_global + (p.b_globals > 1 ? g : 0)) : ga;
+      return p.b_global != nullptr ? ga * p.b_global[p.b_globals > 1 ? g : 0] : ga;
     };
     // values of rows c0 .. c0 + 31 of the tile, this lane's column: 32 lanes
     // write 32 adjacent columns of one row at a time
@@ -670,7 +670,7 @@ __device__ __forceinline__ float4 ld_cluster_v4(uint32_t cluster_addr) {
 __device__ __forceinline__ void sum_partials(const Fp4SmallParams& p, uint32_t base, int rank, int row0, int rows,
                                              int col0) {
   const bool out32 = p.out_dtype == kOutF32, outbf = p.out_dtype == kOutBF16;
-  const float alpha = (p.a_global != nullptr ? __ldg(p.a_global) : 1.f) * (p.b_global != nullptr ? __ldg(p.b_global) : 1.f);
+  const float alpha = (p.a_global != nullptr ? *p.a_global : 1.f) * (p.b_global != nullptr ? *p.b_global : 1.f);
   const int ch = static_cast<int>(threadIdx.x & 31u) * 4;
   const int col = col0 + ch;
   const int elt = out32 ? 4 : 2;
@@ -872,7 +872,7 @@ __global__ void __launch_bounds__(kSmallThreads, 1) fp4_small_kernel(const __gri
     // ---- epilogue: TMEM lane = output column, TMEM column = row of D ---------
     const uint32_t q = warp & 3u;
     const bool out32 = p.out_dtype == kOutF32, outbf = p.out_dtype == kOutBF16;
-    const float alpha = (p.a_global != nullptr ? __ldg(p.a_global) : 1.f) * (p.b_global != nullptr ? __ldg(p.b_global) : 1.f);
+    const float alpha = (p.a_global != nullptr ? *p.a_global : 1.f) * (p.b_global != nullptr ? *p.b_global : 1.f);
     int acc = 0;
     uint32_t acc_ph = 0;
     for (int t = first; t < p.tiles; t += stride) {
@@ -971,20 +971,35 @@ __global__ void fp4_zero_rows_kernel(const int* offsets, int G, int M, uint8_t* 
 // SwiGLU of FP32 rows [gate | up], for halves that the fused epilogue cannot
 // pair (it needs both to start on a tile of scales): the groups' rows only.
 template <class T>
-__global__ void fp4_swiglu_kernel(const float* __restrict__ x, const int* __restrict__ offsets, int G, int n_out,
-                                  long long ldd, T* __restrict__ h) {
+__global__ void fp4_swiglu_kernel(const float* x, const int* offsets, int G, int n_out, long long ldd, T* h) {
   grid_dependency_wait();
   const int row = static_cast<int>(blockIdx.x);
-  if (!row_has_group(offsets, G, row)) return;
+  if (row >= offsets[G] && !row_has_group(offsets, G, row)) return;
   const float* r = x + static_cast<long long>(row) * 2 * n_out;
-  for (int c = static_cast<int>(threadIdx.x); c < n_out; c += static_cast<int>(blockDim.x)) {
-    const float y = silu_mul(r[c], r[n_out + c]);
-    if constexpr (std::is_same<T, float>::value)
-      h[row * ldd + c] = y;
-    else if constexpr (std::is_same<T, __half>::value)
-      h[row * ldd + c] = __float2half_rn(y);
-    else
-      h[row * ldd + c] = __float2bfloat16_rn(y);
+  // four columns' loads in flight a thread
+  const int step = static_cast<int>(blockDim.x);
+  for (int c0 = static_cast<int>(threadIdx.x); c0 < n_out; c0 += 4 * step) {
+    float gate[4], up[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int c = c0 + i * step;
+      if (c < n_out) {
+        gate[i] = ld_global(r + c);
+        up[i] = ld_global(r + n_out + c);
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int c = c0 + i * step;
+      if (c >= n_out) break;
+      const float y = silu_mul(gate[i], up[i]);
+      if constexpr (std::is_same<T, float>::value)
+        h[row * ldd + c] = y;
+      else if constexpr (std::is_same<T, __half>::value)
+        h[row * ldd + c] = __float2half_rn(y);
+      else
+        h[row * ldd + c] = __float2bfloat16_rn(y);
+    }
   }
 }
 

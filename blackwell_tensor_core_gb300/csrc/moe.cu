@@ -64,8 +64,7 @@ constexpr int kSortCtas = 16;    // of the cluster, where the device has room fo
 
 template <class ID>
 __global__ void __launch_bounds__(kSortMaxWarps * 32)
-    moe_sort_kernel(const ID* __restrict__ ids, int pairs, int E, int n_cta, int* __restrict__ offsets,
-                    int* __restrict__ order, int* __restrict__ position) {
+    moe_sort_kernel(const ID* ids, int pairs, int E, int n_cta, int* offsets, int* order, int* position) {
   extern __shared__ int sm[];
   grid_dependency_wait();
   grid_dependents_launch();
@@ -249,6 +248,14 @@ union Vec {
   __device__ Vec() {}
 };
 
+// An operand to be read with ld_global in vectors of VB bytes (the narrow loads
+// need no pointer from behind the wait: the gradient of 2049 x 8 rows of 2047 FP32
+// 54.9 us, with one 55.9).
+template <int VB>
+__device__ __forceinline__ const void* input(const void* p) {
+  return VB == 16 ? behind_wait(p) : p;
+}
+
 __device__ __forceinline__ float to_f32(float v) { return v; }
 __device__ __forceinline__ float to_f32(__nv_bfloat16 v) { return __bfloat162float(v); }
 __device__ __forceinline__ float to_f32(__half v) { return __half2float(v); }
@@ -289,12 +296,12 @@ __global__ void __launch_bounds__(256) moe_dispatch_kernel(const __grid_constant
   const int t = static_cast<int>(blockIdx.x / static_cast<unsigned>(chunks));
   const int step = static_cast<int>(blockDim.x);
   const int v0 = static_cast<int>(blockIdx.x % static_cast<unsigned>(chunks)) * step * V + static_cast<int>(threadIdx.x);
-  const R* src = reinterpret_cast<const R*>(static_cast<const char*>(p.src) + t * p.ld_src * elt);
+  const R* src = reinterpret_cast<const R*>(static_cast<const char*>(input<VB>(p.src)) + t * p.ld_src * elt);
   R x[V];
   if constexpr (VB != 4) {
 #pragma unroll
     for (int m = 0; m < V; ++m)
-      if (v0 + m * step < p.vecs) x[m] = __ldg(src + v0 + m * step);
+      if (v0 + m * step < p.vecs) x[m] = ld_global(src + v0 + m * step);
   }
   const int kept = *p.kept;
   const int* pos = p.position + static_cast<long long>(t) * p.k;
@@ -309,7 +316,7 @@ __global__ void __launch_bounds__(256) moe_dispatch_kernel(const __grid_constant
     if constexpr (VB == 4) {
 #pragma unroll
       for (int m = 0; m < V; ++m)
-        if (static_cast<unsigned>(v + m * step) < static_cast<unsigned>(p.vecs)) x[m] = __ldg(src + v + m * step);
+        if (static_cast<unsigned>(v + m * step) < static_cast<unsigned>(p.vecs)) x[m] = ld_global(src + v + m * step);
     }
 #pragma unroll
     for (int m = 0; m < V; ++m)
@@ -325,7 +332,9 @@ __global__ void __launch_bounds__(256) moe_dispatch_kernel(const __grid_constant
 // with 256 threads; the gradient 87.0 us (6.6 TB/s) with 16 loads, 90.7 with 8,
 // 92.3 with 256 threads.  Narrower vectors: 32 loads for the combine (2049 x 8
 // rows of 2047 FP32: 26 us, 30 with 16), 16 for the gradient (51.4, 52.2 with
-// 32).  Checks of the positions between the loads cost the combine 15 us.
+// 32), and for the combine loads that leave no line in L1 (2049 x 8 rows of 2047
+// BF16 21.1 us, 22.3 with them in L1; the gradient and the dispatch lose by it).
+// Checks of the positions between the loads cost the combine 15 us.
 constexpr int kRowThreads = 128;
 template <int VB, int P, bool GRAD>
 constexpr int vectors_of() {
@@ -345,6 +354,7 @@ __global__ void __launch_bounds__(kRowThreads) moe_combine_kernel(const __grid_c
   const int v0 = static_cast<int>(blockIdx.x % static_cast<unsigned>(chunks)) * step * V + static_cast<int>(threadIdx.x);
   const int kept = min(*p.kept, p.pairs);
   const long long p0 = static_cast<long long>(t) * p.k;
+  const T* rows = static_cast<const T*>(input<VB>(p.src));
   float acc[V][N];
 #pragma unroll
   for (int m = 0; m < V; ++m)
@@ -365,10 +375,10 @@ __global__ void __launch_bounds__(kRowThreads) moe_combine_kernel(const __grid_c
     for (int a = 0; a < P; ++a) {
       bad |= j0 + a < p.k && static_cast<unsigned>(row[a]) >= static_cast<unsigned>(p.pairs);
       has[a] = row[a] >= 0 && row[a] < kept;
-      const R* src = reinterpret_cast<const R*>(static_cast<const T*>(p.src) + (has[a] ? row[a] : 0) * p.ld_src);
+      const R* src = reinterpret_cast<const R*>(rows + (has[a] ? row[a] : 0) * p.ld_src);
 #pragma unroll
       for (int m = 0; m < V; ++m)
-        if (has[a] && v0 + m * step < p.vecs) x[a][m].raw = __ldg(src + v0 + m * step);
+        if (has[a] && v0 + m * step < p.vecs) x[a][m].raw = ld_global_once(src + v0 + m * step);
     }
     if (bad && threadIdx.x == 0) record_bad_position(p.err);
 #pragma unroll
@@ -405,7 +415,8 @@ __global__ void __launch_bounds__(kRowThreads) moe_combine_grad_kernel(const __g
   const int step = static_cast<int>(blockDim.x);
   const int kept = min(*p.kept, p.pairs);
   const long long p0 = static_cast<long long>(t) * p.k;
-  const R* dy = reinterpret_cast<const R*>(static_cast<const T*>(p.src) + t * p.ld_src);
+  const R* dy = reinterpret_cast<const R*>(static_cast<const T*>(input<VB>(p.src)) + t * p.ld_src);
+  const T* rows = static_cast<const T*>(input<VB>(p.rows_in));
   for (int j0 = 0; j0 < p.k; j0 += P) {
     int row[P];
     float w[P], dot[P];
@@ -430,7 +441,7 @@ __global__ void __launch_bounds__(kRowThreads) moe_combine_grad_kernel(const __g
 #pragma unroll
     for (int a = 0; a < P; ++a) {
       const int r = max(row[a], 0);
-      from[a] = reinterpret_cast<const R*>(static_cast<const T*>(p.rows_in) + r * p.ld_rows);
+      from[a] = reinterpret_cast<const R*>(rows + r * p.ld_rows);
       to[a] = reinterpret_cast<R*>(static_cast<T*>(p.dst) + r * p.ld_dst);
     }
     for (int v = static_cast<int>(threadIdx.x); v < p.vecs; v += step * V) {
@@ -438,12 +449,12 @@ __global__ void __launch_bounds__(kRowThreads) moe_combine_grad_kernel(const __g
       auto in = [&](int m) { return v + m * step < p.vecs; };
 #pragma unroll
       for (int m = 0; m < V; ++m)
-        if (in(m)) g[m].raw = __ldg(dy + v + m * step);
+        if (in(m)) g[m].raw = ld_global(dy + v + m * step);
 #pragma unroll
       for (int a = 0; a < P; ++a)
 #pragma unroll
         for (int m = 0; m < V; ++m)
-          if (row[a] >= 0 && row[a] < kept && in(m)) x[a][m].raw = __ldg(from[a] + v + m * step);
+          if (row[a] >= 0 && row[a] < kept && in(m)) x[a][m].raw = ld_global(from[a] + v + m * step);
 #pragma unroll
       for (int a = 0; a < P; ++a) {
         if (row[a] < 0) continue;
