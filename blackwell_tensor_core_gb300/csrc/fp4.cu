@@ -529,7 +529,7 @@ bwg_status check_fp4(const void* x, int dtype, int M, int K, int ldx, int format
   if (offsets == nullptr && M % G != 0) return BWG_ERR_INVALID_ARG;
   if (K % 32 != 0) return BWG_ERR_ALIGNMENT;
   if (global != nullptr && (format == kMxfp4 || (n_global != 1 && n_global != G))) return BWG_ERR_INVALID_ARG;
-  if (G > kFp4MaxGroups) return BWG_ERR_UNSUPPORTED;
+  if (G > kFp4MaxGroups || M > kFp4MaxSize || K > kFp4MaxSize) return BWG_ERR_UNSUPPORTED;
   if (M == 0 || K == 0) {
     *empty = true;
     return BWG_OK;
@@ -643,6 +643,7 @@ extern "C" {
 
 long long bwg_fp4_scale_bytes(int M, int K, int format, int G, int ragged) {
   if (M < 0 || K < 0 || G < 1 || (format != kNvfp4 && format != kMxfp4) || (!ragged && M % G != 0)) return -1;
+  if (M > kFp4MaxSize || K > kFp4MaxSize) return -1;
   const long long rows = ragged ? (M + 127LL * std::min(G, M)) / 128 * 128 : static_cast<long long>(G) * pad128(M / G);
   return rows / 128 * fp4_k_tiles(K, format) * kScaleTileBytes;
 }

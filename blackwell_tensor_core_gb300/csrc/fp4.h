@@ -26,6 +26,9 @@ constexpr int kMxfp4 = 1;
 constexpr int kScaleTileRows = 128;
 constexpr int kScaleTileBytes = 512;
 
+// Largest number of rows or columns: rounded up to tiles it is still an int.
+constexpr int kFp4MaxSize = 0x7fffffff - 511;
+
 BWG_HD int fp4_block(int format) { return format == kNvfp4 ? 16 : 32; }
 
 BWG_HD int pad128(int rows) { return (rows + 127) & ~127; }

@@ -1261,7 +1261,7 @@ bwg_status run_fp4_gemm(const Fp4Operand& a, const Fp4Operand& b, void* D, int M
     if (!aligned16(a.codes) || !aligned16(a.scales) || !aligned16(b.codes) || !aligned16(b.scales))
       return BWG_ERR_ALIGNMENT;
   }
-  if (G > kFp4MaxGroups) return BWG_ERR_UNSUPPORTED;
+  if (G > kFp4MaxGroups || M > kFp4MaxSize || N > kFp4MaxSize || K > kFp4MaxSize) return BWG_ERR_UNSUPPORTED;
   Runtime rt;
   bwg_status st = runtime_device(&rt);
   if (st != BWG_OK) return st;

@@ -34,6 +34,7 @@ namespace bwg {
 namespace {
 
 constexpr int kMaxExperts = 1024;
+constexpr int kMaxColumns = 1 << 30;  // the vectors of a row's blocks are counted in an int
 
 // The int at `p` (this CTA's shared memory) in the shared memory of CTA `rank`.
 __device__ __forceinline__ int ld_cluster(const int* p, uint32_t rank) {
@@ -511,7 +512,7 @@ bool elt_aligned(const void* q, int elt) { return (reinterpret_cast<uintptr_t>(q
 bwg_status check_rows(int dtype, int T, int H, int k, int E, const int* position, const int* offsets, bool* empty) {
   *empty = false;
   if (!dtype_ok(dtype) || T < 0 || H < 0 || k < 1 || E < 1) return BWG_ERR_INVALID_ARG;
-  if (E > kMaxExperts || static_cast<long long>(T) * k > 0x7fffffffLL) return BWG_ERR_UNSUPPORTED;
+  if (E > kMaxExperts || H > kMaxColumns || static_cast<long long>(T) * k > 0x7fffffffLL) return BWG_ERR_UNSUPPORTED;
   if (T == 0 || H == 0) {
     *empty = true;
     return BWG_OK;

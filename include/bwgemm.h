@@ -233,9 +233,10 @@ bwg_status gemm_bf16_host(const void* A_host, const void* B_host, void* D_host, 
  *   grouped products for M_total = n.
  *
  * The row operators take X, Y, rows in one element type, `dtype` (a
- * bwg_out_dtype), row-major with leading dimensions in elements.  Any H and
- * any leading dimension >= H; pointers aligned to the element.  Rows whose
- * start and length are multiples of 16 bytes move fastest.
+ * bwg_out_dtype), row-major with leading dimensions in elements.  Any H up to
+ * 2^30 (else BWG_ERR_UNSUPPORTED, as for more than 2^31 - 1 pairs) and any
+ * leading dimension >= H; pointers aligned to the element.  Rows whose start
+ * and length are multiples of 16 bytes move fastest.
  * moe_dispatch:      rows[position[p]] = X[t]; zero where position[p] >= n.
  * moe_dispatch_grad: dX[t] = sum_j d_rows[position[p]] over position[p] < n.
  * moe_combine:       Y[t] = sum_j weights[p] rows[position[p]], the same pairs.
@@ -304,7 +305,8 @@ bwg_status moe_combine_grad(const void* dY, const void* rows, int dtype, int T, 
  *   * up, evaluated in FP32; N must be even.  If N is no multiple of 256, the
  *   up half starts inside a scale tile: the product then goes through
  *   `workspace` (M_total * N * 4 bytes, 16-byte aligned; else unused).
- * Codes and scales must be 16-byte aligned.  K = 0 gives D = 0.
+ * Codes and scales must be 16-byte aligned.  K = 0 gives D = 0.  M, N and K
+ * above 2^31 - 512 are BWG_ERR_UNSUPPORTED.
  * ------------------------------------------------------------------- */
 typedef enum { BWG_NVFP4 = 0, BWG_MXFP4 = 1 } bwg_fp4_format;
 
