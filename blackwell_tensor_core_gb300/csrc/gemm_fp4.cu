@@ -1142,6 +1142,14 @@ int grouped_blocks(int M, int N, int groups, int pairs) {
   return 19 * two <= 10 * one ? 2 : 1;
 }
 
+// Kernel of a product: 0 the few-rows kernel, else pairs of 1 or 2 weight blocks a
+// CTA.  groups: 0 for the dense product.  n_out: columns of the result.
+int product_kernel(int M, int n_out, int K, int groups, bool swiglu, int sm_count) {
+  if (swiglu) return 2;
+  if (groups > 0) return grouped_blocks(M, n_out, groups, sm_count / 2);
+  return dense_kernel(M, n_out, (K + kKCols - 1) / kKCols, sm_count);
+}
+
 struct Fp4Operand {
   const void* codes;
   const void* scales;
@@ -1306,14 +1314,12 @@ bwg_status run_fp4_gemm(const Fp4Operand& a, const Fp4Operand& b, void* D, int M
                                             M, static_cast<uint8_t*>(D), static_cast<size_t>(ldd) * elt,
                                             static_cast<size_t>(n_out) * elt, rt.err));
   }
-  const bool dense = offsets == nullptr && G == 1 && !swiglu;
-  const int kernel = dense ? dense_kernel(M, N, (K + kKCols - 1) / kKCols, rt.sm_count) : -1;
-  if (kernel == 0)
+  const int nc = product_kernel(M, n_out, K, offsets != nullptr ? G : 0, swiglu, rt.sm_count);
+  if (nc == 0)
     return run_small(a, b, D, M, N, K, ldd, format, out_dtype, rt, stream);
   Fp4GemmParams p;
   std::memset(&p, 0, sizeof(p));
   const long long tok_tiles = (M + kTok - 1LL) / kTok + (offsets != nullptr ? G : 0);  // at most
-  const int nc = dense ? kernel : swiglu ? 2 : grouped_blocks(M, n_out, offsets != nullptr ? G : 0, rt.sm_count / 2);
   p.w_blocks = pad128(N) / 128;
   const int a_rows = offsets != nullptr ? static_cast<int>((M + 127LL * std::min(G, M)) / 128) : pad128(M) / 128;
   if (!fp4_maps(&p, a, b, M, N, K, format, G, a_rows)) return BWG_ERR_CUDA;
@@ -1383,6 +1389,11 @@ bwg_status run_swiglu_two_steps(const Fp4Operand& a, const Fp4Operand& b, void* 
 using namespace bwg;
 
 extern "C" {
+
+int bwg_fp4_kernel(int M, int N, int K, int G, int swiglu, int sm_count) {
+  if (M < 1 || N < 1 || K < 1 || G < 0 || sm_count < 2 || M > kFp4MaxSize || N > kFp4MaxSize || K > kFp4MaxSize) return -1;
+  return product_kernel(M, swiglu && N % 256 == 0 ? N / 2 : N, K, G, swiglu && N % 256 == 0, sm_count);
+}
 
 bwg_status gemm_fp4(const void* A, const void* A_scales, const float* A_global, const void* B, const void* B_scales,
                     const float* B_global, int format, void* D, int M, int N, int K, int ldd, int out_dtype,

@@ -142,6 +142,8 @@ def lib() -> ctypes.CDLL:
             L.bwg_fp4_scale_bytes.restype = ctypes.c_longlong
             L.bwg_fp4_scale_offset.argtypes = [ctypes.c_longlong, i, i, i]
             L.bwg_fp4_scale_offset.restype = ctypes.c_longlong
+            L.bwg_fp4_kernel.argtypes = [i, i, i, i, i, i]
+            L.bwg_fp4_kernel.restype = i
             L.bwg_idesc_fp4.argtypes = [i, i, i, i]
             L.bwg_idesc_fp4.restype = u32
             L.bwg_version.argtypes = []

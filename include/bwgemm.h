@@ -514,6 +514,11 @@ long long bwg_fp4_scale_offset(long long row, int block, int K, int format);
  * bwg_fp4_format; scale_id: first of a word's four scales that is used). */
 uint32_t bwg_idesc_fp4(int format, int m, int n, int scale_id);
 
+/* Kernel that a 4-bit product takes: 0 one CTA a tile of 128 columns and up to
+ * 128 rows, 1 or 2 CTA pairs with as many blocks of 128 weight rows a CTA; -1 for
+ * invalid arguments.  G: 0 for gemm_fp4; swiglu and N as for grouped_gemm_fp4. */
+int bwg_fp4_kernel(int M, int N, int K, int G, int swiglu, int sm_count);
+
 /* tcgen05 shared-memory matrix descriptor (swizzle: 0 none, 2 = 128-byte). */
 uint64_t bwg_smem_desc(uint32_t smem_addr, uint32_t lbo_bytes, uint32_t sbo_bytes, int swizzle);
 
