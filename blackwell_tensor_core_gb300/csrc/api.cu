@@ -1120,7 +1120,7 @@ bwg_status runtime_device(Runtime* out) {
     cudaGetLastError();
     return BWG_ERR_CUDA;
   }
-  *out = Runtime{dev, st->sm_count, st->max_smem, st->err, g_timeout_ns.load()};
+  *out = Runtime{dev, st->sm_count, st->max_smem, st->err, g_timeout_ns.load(), g_tx_extra.load()};
   return BWG_OK;
 }
 

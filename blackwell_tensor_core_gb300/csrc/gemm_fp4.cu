@@ -48,6 +48,7 @@ struct Fp4GemmParams {
   CUtensorMap map_as;  // activation scales, the same with a box of 2 row blocks
   unsigned long long* err;
   unsigned long long timeout_ns;
+  uint32_t tx_extra;       // test hook: extra bytes expected per stage (0 normally)
   const int* offsets;      // [G + 1] or nullptr: one group of all M rows
   const float* a_global;   // nullptr: 1
   const float* b_global;   // nullptr: 1
@@ -359,7 +360,7 @@ __global__ void __launch_bounds__(kPairThreads, 1) fp4_pair_kernel(const __grid_
                 // box of two row blocks (the second may lie past the end: zeros)
                 tma_load_3d_pair(st + L::kStageW + kTokBytes + NC * L::kSfBlock, &p.map_as, fb, 0, kb * kTilesK, sf_row);
               } else {
-                if (job == 0 && rank == 0) mbar_arrive_expect_tx(full_bar(s), kStageTx);
+                if (job == 0 && rank == 0) mbar_arrive_expect_tx(full_bar(s), kStageTx + p.tx_extra);
                 tma_load_3d_pair(st + job * kWBytes, &p.map_w, fb, kb * kKBytes, row, tl.g);
                 tma_load_3d_pair(st + L::kStageW + kTokBytes + job * L::kSfBlock, &p.map_ws, fb, 0, kb * kTilesK, sf_row);
               }
@@ -671,6 +672,7 @@ struct Fp4SmallParams {
   CUtensorMap map_w, map_a, map_ws, map_as;  // as above; activations in boxes of n rows, scales of one row block
   unsigned long long* err;
   unsigned long long timeout_ns;
+  uint32_t tx_extra;       // test hook: extra bytes expected per stage (0 normally)
   const float* a_global;
   const float* b_global;
   void* d;
@@ -834,7 +836,7 @@ __global__ void __launch_bounds__(kSmallThreads, 1) fp4_small_kernel(const __gri
           const uint32_t st = base + static_cast<uint32_t>(s) * stage_bytes;
           const uint32_t sf = st + kWBytes + a_bytes;
           if (weights) {
-            mbar_arrive_expect_tx(full_bar(s), kWBytes + a_bytes + 2u * kSfBytes);
+            mbar_arrive_expect_tx(full_bar(s), kWBytes + a_bytes + 2u * kSfBytes + p.tx_extra);
             tma_load_3d_hint(st, &p.map_w, full_bar(s), kb * kKBytes, tile.c * 128, 0, policy);
             tma_load_3d_hint(sf, &p.map_ws, full_bar(s), 0, kb * kTilesK, tile.c, policy);
           } else {
@@ -1262,6 +1264,7 @@ bwg_status run_small(const Fp4Operand& a, const Fp4Operand& b, void* D, int M, i
     return BWG_ERR_CUDA;
   p.err = rt.err;
   p.timeout_ns = rt.timeout_ns;
+  p.tx_extra = rt.tx_extra;
   p.a_global = a.global;
   p.b_global = b.global;
   p.d = D;
@@ -1325,6 +1328,7 @@ bwg_status run_fp4_gemm(const Fp4Operand& a, const Fp4Operand& b, void* D, int M
   if (!fp4_maps(&p, a, b, M, N, K, format, G, a_rows)) return BWG_ERR_CUDA;
   p.err = rt.err;
   p.timeout_ns = rt.timeout_ns;
+  p.tx_extra = rt.tx_extra;
   p.offsets = offsets;
   p.a_global = a.global;
   p.b_global = b.global;

@@ -16,6 +16,7 @@ struct Runtime {
   int max_smem;                   // opt-in shared memory per CTA
   unsigned long long* err;        // device error word
   unsigned long long timeout_ns;  // bound of every barrier wait
+  unsigned tx_extra;              // test hook: extra bytes expected per stage (0 normally)
 };
 
 // State of the current device; BWG_ERR_UNSUPPORTED where it is not sm_103.
