@@ -41,9 +41,20 @@ def quantize_experts(w, fmt):
     return ops.quantize_fp4(stack, fmt, global_scale=g)
 
 
+def calibrated_scales(x, ids, w1, fmt):
+    """The scales of the two products' inputs, x and FC1's output, from a BF16
+    pass over sample tokens.  Each input needs its own: with a scale too small
+    for it values saturate, with one too large they lose their bits."""
+    if fmt != "nvfp4":
+        return None, None
+    r = ops.moe_sort(ids, len(w1))
+    h = ops.grouped_gemm(ops.moe_dispatch(x, r), w1, r.offsets, swiglu=True)
+    return tuple((m.abs().amax().float() / 2688.0).reshape(1) for m in (x, h))
+
+
 def layer_fp4(x, ids, weights, q1, q2, fmt, x_scale=None, h_scale=None):
-    """The same with 4-bit experts; x_scale and h_scale are the calibrated
-    nvfp4 scales of the two products' inputs."""
+    """The same with 4-bit experts; x_scale and h_scale are the nvfp4 scales of
+    the two products' inputs (calibrated_scales)."""
     r = ops.moe_sort(ids, q1.groups)
     rows = ops.quantize_fp4(ops.moe_dispatch(x, r), fmt, global_scale=x_scale, group_offsets=r.offsets)
     h = ops.quantize_fp4(ops.grouped_gemm_fp4(rows, q1, swiglu=True), fmt, global_scale=h_scale,
@@ -90,10 +101,9 @@ def main():
     ids, weights = route(x, router, a.topk)
     y = layer_bf16(x, ids, weights, w1, w2)
     print("bf16 experts: %8.1f us" % timed(lambda: layer_bf16(x, ids, weights, w1, w2)))
-    x_scale = (x.abs().amax().float() / 2688.0).reshape(1)
     for fmt in ("nvfp4", "mxfp4"):
         q1, q2 = quantize_experts(w1, fmt), quantize_experts(w2, fmt)
-        scales = (x_scale, x_scale) if fmt == "nvfp4" else (None, None)
+        scales = calibrated_scales(x, ids, w1, fmt)
         y4 = layer_fp4(x, ids, weights, q1, q2, fmt, *scales)
         err = float((y4.float() - y.float()).norm() / y.float().norm())
         print("%s experts: %8.1f us, relative difference from bf16 %.3f" % (
