@@ -495,7 +495,7 @@ def _rows(t: torch.Tensor, name: str, rows: int) -> int:
         raise ValueError("%s must be a 2-D CUDA tensor" % name)
     have, cols = t.shape
     ld, unit = t.stride()
-    if unit != 1:
+    if unit != 1 and cols > 1:
         raise ValueError("%s must be row-major with unit column stride" % name)
     if have != rows:
         raise ValueError("%s must have %d rows, got %d" % (name, rows, have))

@@ -217,3 +217,14 @@ def test_stacked_weights_without_columns(rec):
     assert q.shape == (24, 0) and q.groups == 3
     (name, args), = rec.calls
     assert name == "quantize_fp4" and args[2:4] == (24, 0) and args[9] == 3
+
+
+def test_a_single_column_has_no_column_stride(rec):
+    """[4, 1] with strides (1, 4), as the transpose of a row is: torch calls it contiguous."""
+    x = cuda(1, 4).t()
+    assert x.is_contiguous() and x.stride() == (1, 4)
+    ops.moe_dispatch(x, routing(4, 2, 3))
+    (name, args), = rec.calls
+    assert name == "moe_dispatch" and args[3:5] == (1, 1)
+    with pytest.raises(ValueError):
+        ops.moe_dispatch(cuda(2, 4).t(), routing(4, 2, 3))
