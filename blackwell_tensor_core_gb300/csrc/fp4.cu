@@ -301,8 +301,10 @@ __device__ __forceinline__ GlobalScale global_scale(const float* p) {
 // nvfp4's quotients are FP32's x / d from an approximate reciprocal r of d:
 // q0 = x r is a few units in the last place off, its remainder x - q0 d is
 // exact in an FMA, and q0 plus the remainder times r rounds to the quotient
-// (Markstein, 1990).  Computed as -q from -r, so that every factor is a constant
-// of the block and a zero gets the sign that a flip of the codes' signs turns
+// (Markstein, 1990; r being approximate, the codes next to every tie were compared
+// with FP32 division for all 2^23 mantissas of d, and the scales for every 6 g).
+// Computed as -q from -r, so that every factor is a constant of the block and a
+// zero gets the sign that a flip of the codes' signs turns
 // into its own, also for a zero scale (r = 0).  What could overflow or lose the
 // remainder's bits goes to slow_block, out of line, which leaves registers for
 // four blocks of threads an SM: 58 us for 32768 x 4096 BF16 (5.9 TB/s) against

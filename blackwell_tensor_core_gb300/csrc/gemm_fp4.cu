@@ -1115,7 +1115,9 @@ bwg_status pair_clusters(PairKernel k, int nc, const Runtime& rt, int* clusters)
 // weight blocks a CTA.  Up to 128 rows the first; above, the one whose rounds of
 // tiles take the least time: a start, and for each round its k-blocks and a
 // tile's switch, or the epilogue where that is longer (in 10 ns, fitted to 132
-// sizes of 200 to 4096 rows, where the fastest is taken but for 0.2% on average).
+// sizes of 200 to 4096 rows, where the fastest is taken but for 0.2% on average;
+// all of them NVFP4 with BF16 output: MXFP4's k-blocks in pairs are a tenth
+// shorter and FP32 output stores twice the bytes).
 // The few-rows kernel is ready sooner and splits tiles: 200 rows of 4096 x 7168
 // 9.1 us against 11.6 and 18.2; 960 rows of 4096 x 2048 8.2, 9.6 and 10.5.  One
 // block has the shorter k-blocks (1900 rows of 4096 x 7168 32.4, 26.5 and 32.3),
@@ -1134,8 +1136,8 @@ int dense_kernel(int M, int N, int kb, int sm_count) {
 
 // Weight blocks a CTA for a plain grouped product.  A tile of two blocks takes
 // 1.9 times as long as one of one block, but a pair's last round of tiles is
-// then twice as coarse (32 experts' FC1 without SwiGLU 217 us with two, 228
-// with one).
+// then twice as coarse (4096 x 4096 NVFP4: 4096 tokens x 8 of 32 experts 183 us
+// with two, 194 with one; 16 tokens 49.4 and 47.4, one token 14.6 and 17.6).
 int grouped_blocks(int M, int N, int groups, int pairs) {
   // a ragged group ends on half a tile on average
   const long long rows = (M + kTok - 1LL) / kTok + groups / 2;

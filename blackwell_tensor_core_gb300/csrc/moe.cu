@@ -57,8 +57,9 @@ __device__ __forceinline__ void record_bad_position(unsigned long long* err) {
 // pair order.
 // What bounds it: latency.  The ids are 0.3 MB for the 4096 x 8 layer; one
 // launch with its counts on chip replaces three passes through global memory.
-// 32768 ids of 32 experts: 6.4 us; with 8 CTAs 8.1, and 11.6 with match.any and with sums over the
-// warps' counts and the CTAs' totals that wait for one load after the other.
+// 32768 ids of 32 experts: 6.0 us, with 8 CTAs 7.6; 131072 of 256 experts 15.4 and
+// 25.4.  Sums over the warps' counts and the CTAs' totals that waited for one load
+// after the other cost the former 5 us.
 constexpr int kSortMaxWarps = 32;
 constexpr int kSortAhead = 4;    // id loads in flight per lane
 constexpr int kSortCtas = 16;    // of the cluster, where the device has room for it; else 8
@@ -92,8 +93,8 @@ __global__ void __launch_bounds__(kSortMaxWarps * 32)
     return v >= 0 && v < static_cast<ID>(E) ? static_cast<int>(v) : E;
   };
   // The lanes with this lane's bucket, bit by bit of the bucket's number: 6
-  // votes for 32 experts take less time than one match.any (131072 pairs
-  // 21 us, with match.any 29).
+  // votes for 32 experts take less time than one match.any (32768 pairs 6.0 us,
+  // with match.any 6.5; 131072 of 256 experts 15.4 and 21.4).
   const int bits = 32 - __clz(E);
   auto same_bucket = [&](int key) -> unsigned {
     unsigned same = __ballot_sync(0xffffffffu, key >= 0);
@@ -267,7 +268,7 @@ __device__ __forceinline__ void from_f32(__half& d, float v) { d = __float2half_
 // Block (t, chunk): V vectors of token t per thread, blockDim.x apart, stored to
 // its k rows.  The stores are the time; one vector of 16 bytes a thread reaches
 // 6.5 TB/s, narrower ones need more of them (2049 x 8 rows of 2047 BF16, 2 bytes
-// at a time: 27.9 us with one, 19.5 with 8).
+// at a time: 29.2 us with one, 19.0 with 8).
 template <int VB>
 constexpr int dispatch_vectors() {
   return VB == 16 ? 1 : VB == 4 ? 4 : 8;
@@ -275,8 +276,8 @@ constexpr int dispatch_vectors() {
 
 // Vectors of 4 bytes: the threads of a warp take those that fill one aligned
 // line of 128 bytes of the row they store to, whatever its start, so that no
-// store splits a sector with another warp's (2049 x 8 rows of 2047 FP32: 29.0 us,
-// 32.1 without; with 2 bytes, or in the combine's gradient, whose vectors of dy
+// store splits a sector with another warp's (2049 x 8 rows of 2047 FP32: 25.9 us,
+// 33.9 without; with 2 bytes, or in the combine's gradient, whose vectors of dy
 // would then be read once a pair, it costs more than it gives).  Vectors to
 // skip at row `dst`.
 template <int VB>
@@ -328,14 +329,15 @@ __global__ void __launch_bounds__(256) moe_dispatch_kernel(const __grid_constant
 // Loads in flight decide how near these two kernels come to the memory's rate,
 // so a thread takes P pairs (k, 5 as 6 and 7 as 8; more in turns of 8) of V
 // vectors and issues all P * V loads before it uses the first.  Measured for
-// 4096 tokens x 8 experts, H = 4096 BF16: the combine 46.9 us (6.4 TB/s) with 8
-// loads of 16 bytes a thread and 128 threads a block, 60 with 16 loads, 47.7
-// with 256 threads; the gradient 87.0 us (6.6 TB/s) with 16 loads, 90.7 with 8,
-// 92.3 with 256 threads.  Narrower vectors: 32 loads for the combine (2049 x 8
-// rows of 2047 FP32: 26 us, 30 with 16), 16 for the gradient (51.4, 52.2 with
-// 32), and for the combine loads that leave no line in L1 (2049 x 8 rows of 2047
-// BF16 21.1 us, 22.3 with them in L1; the gradient and the dispatch lose by it).
-// Checks of the positions between the loads cost the combine 15 us.
+// 4096 tokens x 8 experts, H = 4096 BF16: the combine 46.0 us (6.5 TB/s) with 8
+// loads of 16 bytes a thread and 128 threads a block, 46.9 with 256 threads, 45.2
+// with 16 loads, which take 5003 x 6 of H = 2056 from 23.8 to 29.2; the gradient
+// 86.6 us (6.6 TB/s) with 16 loads, 88.6 with 8, 94.4 with 256 threads.  Narrower
+// vectors: 32 loads for the combine (2049 x 8 rows of 2047 FP32: 25.8 us, 28.7
+// with 16), 16 for the gradient (55.2; 53.1 with 32), and for the combine loads
+// that leave no line in L1 (2049 x 8 rows of 2047 BF16 21.1 us, 22.3 with them in
+// L1; the gradient and the dispatch lose by it).  Checks of the positions between
+// the loads cost the combine 15 us.
 constexpr int kRowThreads = 128;
 template <int VB, int P, bool GRAD>
 constexpr int vectors_of() {
@@ -642,9 +644,9 @@ cudaError_t sort_ctas(int device, int* n) {
 template <class ID>
 cudaError_t launch_sort(const void* ids, int pairs, int E, int* offsets, int* order, int* position, int device,
                         cudaStream_t s) {
-  // One CTA up to 2048 pairs (256 experts: 5.6 us), a warp for each 128 of
+  // One CTA up to 2048 pairs (256 experts: 5.0 us), a warp for each 128 of
   // them; a cluster beyond (8192 pairs with 8 CTAs: 6.2 us, one CTA takes 7.7
-  // for 4096; 32768 pairs with 16 CTAs 6.4 us, with 8 8.1).
+  // for 4096; 32768 pairs with 16 CTAs 6.0 us, with 8 7.6).
   int n_cta = 1;
   const cudaError_t known = sort_ctas<ID>(device, &n_cta);
   if (known != cudaSuccess) return known;

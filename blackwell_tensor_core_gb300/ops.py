@@ -441,6 +441,9 @@ def grouped_gemm_swiglu_fp16_nt(A_ptr, B_ptrs, H_ptr, offsets_ptr, G, M_total, N
 
 # ------------------------------------------------------------ routed rows ---
 
+# Like every call here these are outside automatic differentiation: the
+# gradients are calls of their own, and an output never requires one.
+
 
 class Routing(NamedTuple):
     """What moe_sort makes of the experts' ids: the order of the rows that the
@@ -454,7 +457,11 @@ class Routing(NamedTuple):
 def moe_sort(expert_ids: torch.Tensor, num_experts: int, stream=None) -> Routing:
     """Stable sort of the (token, expert) pairs by expert.  ``expert_ids`` is a
     CUDA int32 or int64 tensor [T, k]; an id outside 0 .. num_experts - 1 marks
-    a pair without an expert, sorted behind all others."""
+    a pair without an expert, sorted behind all others.
+
+    With such pairs the offsets end before T * k: grouped_gemm_fp4 takes them so,
+    grouped_gemm reports it (its contract wants the last offset to be the rows
+    of A, so give it the first offsets[-1] rows)."""
     if expert_ids.dim() != 2 or expert_ids.dtype not in (torch.int32, torch.int64):
         raise ValueError("expert_ids must be an int32 or int64 tensor [T, k]")
     if not expert_ids.is_cuda or not expert_ids.is_contiguous():

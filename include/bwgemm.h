@@ -230,7 +230,7 @@ bwg_status gemm_bf16_host(const void* A_host, const void* B_host, void* D_host, 
  *     its inverse.  Pairs without an expert are sorted behind all others
  *     (rows n ..), so order and position are whole permutations.
  *   E <= 1024, else BWG_ERR_UNSUPPORTED.  offsets honours the contract of the
- *   grouped products for M_total = n.
+ *   grouped products for M_total = n (grouped_gemm_fp4 also for M_total above).
  *
  * The row operators take X, Y, rows in one element type, `dtype` (a
  * bwg_out_dtype), row-major with leading dimensions in elements.  Any H up to
@@ -295,7 +295,8 @@ bwg_status moe_combine_grad(const void* dY, const void* rows, int dtype, int T, 
  * Rows of no group (from group_offsets[G] on) are neither read nor written.
  *
  * gemm_fp4: D[M, N] = A x B^T for A [M, K] and B [N, K] in the same format,
- *   FP32 accumulation, D in out_dtype with any ldd >= N.
+ *   FP32 accumulation, D in out_dtype with any ldd >= N.  The product of the two
+ *   scales may leave FP32's range where the results do not.
  * grouped_gemm_fp4: D[r, :] = A[r, :] x B[g]^T for r in group g.  A is
  *   [M_total, K] in ragged groups, B [G * N, K] in G groups of N rows; B_global
  *   has n_global = 1 or G floats.  group_offsets[G] may be below M_total: D's
