@@ -218,8 +218,10 @@ def _matrix(t: torch.Tensor, name: str) -> int:
         raise ValueError("%s must be row-major with unit column stride" % name)
     if not t.is_cuda:
         raise ValueError("%s must be a CUDA tensor" % name)
-    _fits("size or row stride of " + name, *t.shape, t.stride(0))
-    return t.stride(0)
+    ld = t.stride(0)
+    if ld > _INT_MAX:
+        raise ValueError("row stride of %s: %d is past 2^31 - 1" % (name, ld))
+    return ld
 
 
 def gemm(A: torch.Tensor, B: torch.Tensor, out: torch.Tensor | None = None,
@@ -232,21 +234,24 @@ def gemm(A: torch.Tensor, B: torch.Tensor, out: torch.Tensor | None = None,
     N, K2 = B.shape if b_transposed else (B.shape[1], B.shape[0])
     if K2 != K:
         raise ValueError("inner dimensions differ: %s x %s" % (tuple(A.shape), tuple(B.shape)))
+    if M > _INT_MAX or N > _INT_MAX or K > _INT_MAX:
+        raise ValueError("M, N or K is past 2^31 - 1: %d, %d, %d" % (M, N, K))
+    dev = A.device
     if out is None:
-        out = torch.empty((M, N), dtype=out_dtype, device=A.device)
+        out = torch.empty((M, N), dtype=out_dtype, device=dev)
     if out.dtype not in _OUT_CODES:
         raise TypeError("output dtype must be bfloat16, float16 or float32")
     if tuple(out.shape) != (M, N):
         raise ValueError("out must be [%d, %d], got %s" % (M, N, tuple(out.shape)))
-    if not (A.device == B.device == out.device):
+    if not (dev == B.device == out.device):
         raise ValueError("A, B and out must be on the same device")
     lda, ldb, ldd = _matrix(A, "A"), _matrix(B, "B"), _matrix(out, "out")
     if b_transposed:
         fn = gemm_bf16_nt if A.dtype == torch.bfloat16 else gemm_fp16_nt
     else:
         fn = gemm_bf16 if A.dtype == torch.bfloat16 else gemm_fp16
-    _on(A.device, fn, A.data_ptr(), B.data_ptr(), out.data_ptr(), M, N, K, lda, ldb, ldd, _OUT_CODES[out.dtype],
-        _stream_handle(stream, A.device))
+    _on(dev, fn, A.data_ptr(), B.data_ptr(), out.data_ptr(), M, N, K, lda, ldb, ldd, _OUT_CODES[out.dtype],
+        _stream_handle(stream, dev))
     return out
 
 
@@ -471,7 +476,8 @@ def moe_sort(expert_ids: torch.Tensor, num_experts: int, stream=None) -> Routing
         raise ValueError("num_experts must be at least 1")
     dev = expert_ids.device
     pairs = expert_ids.numel()
-    _fits("pairs or experts", pairs, num_experts)
+    if pairs > _INT_MAX or num_experts > _INT_MAX:
+        raise ValueError("%d pairs of %d experts are past 2^31 - 1" % (pairs, num_experts))
     offsets = _new((num_experts + 1,), torch.int32, dev, stream)
     order = _new((pairs,), torch.int32, dev, stream)
     position = _new(expert_ids.shape, torch.int32, dev, stream)
