@@ -31,6 +31,8 @@ class Recorder:
 def rec(monkeypatch):
     r = Recorder()
     monkeypatch.setattr(ops, "lib", lambda: r)
+    # where there is a GPU, fake tensors would set up their device's context, which may not exist
+    monkeypatch.setattr(torch.cuda, "is_available", lambda: False)
     monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: 0, raising=False)
     monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream", lambda index: 0, raising=False)
     with warnings.catch_warnings():
