@@ -28,6 +28,8 @@
 namespace bwg {
 cudaError_t set_gemm_attributes(size_t smem);
 cudaError_t set_small_m_attributes(size_t smem);
+cudaError_t set_gated_attributes(size_t smem);
+cudaError_t set_tn_attributes(size_t smem);
 }  // namespace bwg
 
 using namespace bwg;
@@ -48,8 +50,6 @@ std::atomic<unsigned> g_tx_extra{0};
 std::atomic<unsigned long long*> g_trace{nullptr};  // unit trace buffer (dense and grouped pair kernels)
 
 constexpr int kMaxDevices = 64;
-constexpr int kBarrierArea = 2048;  // barriers, TMEM address slot, grouped tables
-constexpr int kGroupM = 8;
 
 struct DeviceState {
   bool ready = false;
@@ -215,16 +215,6 @@ int streamk_max_sharers(int tiles, int kb, int grid) {
 
 
 // ------------------------------------------------------------ planning -----
-
-// Per-CTA bytes of one ring stage: nc A blocks of 128 rows and this CTA's
-// share of the B columns, 64 K deep.
-int dense_stage_bytes(int cg, int nc = 1) {
-  return nc * kRowsPerCta * kBK * 2 + (kTileN / cg) * kBK * 2;
-}
-
-int dense_smem(int cg, int stages, bool direct_store = false, int nc = 1) {
-  return 1024 + stages * dense_stage_bytes(cg, nc) + (direct_store ? 0 : kEpiBytes) + kBarrierArea;
-}
 
 // Epilogue choice: "tma" (staged boxes + TMA stores) or "direct" (rows stored
 // from registers, which frees the staging space for one more ring stage).
@@ -565,7 +555,8 @@ bwg_status ensure_device(DeviceState** out) {
     }
     if (st.init_status == BWG_OK) {
       if (set_gemm_attributes(st.max_smem) != cudaSuccess ||
-          set_small_m_attributes(st.max_smem) != cudaSuccess) {
+          set_small_m_attributes(st.max_smem) != cudaSuccess ||
+          set_gated_attributes(st.max_smem) != cudaSuccess || set_tn_attributes(st.max_smem) != cudaSuccess) {
         cudaGetLastError();
         st.init_status = BWG_ERR_CUDA;
       } else {
@@ -1120,7 +1111,8 @@ bwg_status runtime_device(Runtime* out) {
     cudaGetLastError();
     return BWG_ERR_CUDA;
   }
-  *out = Runtime{dev, st->sm_count, st->max_smem, st->err, g_timeout_ns.load(), g_tx_extra.load()};
+  *out = Runtime{dev, st->sm_count, st->max_smem, st->err, g_timeout_ns.load(), g_tx_extra.load(),
+                 st->clusters_2cta, st->clusters_2c, st->clusters_grouped_2c, no_tail_split_from_env(), g_trace.load()};
   return BWG_OK;
 }
 

@@ -1,0 +1,167 @@
+// Products whose left operand is read transposed (gemm_body.cuh, TN):
+// D[g] = A_g^T B_g, the gradient of a weight from a layer's input A and the
+// gradient B of its output, over all rows or over each expert's.
+#include <algorithm>
+#include <cstring>
+
+#include "gemm_body.cuh"
+#include "runtime.h"
+
+using namespace bwg;
+
+namespace bwg {
+namespace {
+
+// 512x256 tiles, sums in TMEM.
+template <bool DYN>
+__global__ void __launch_bounds__(kThreads2C, 1) gemm_tn_2c_kernel(const __grid_constant__ GemmParams p) {
+  gemm_body<2, 1, false, 2, kEpiPlain, DYN, true, false>(p, p);
+}
+
+// 256x256 tiles, sums of kChunkBlocks k-blocks joined in registers.
+template <bool DYN>
+__global__ void __launch_bounds__(kThreads2C, 1) gemm_tn_joined_kernel(const __grid_constant__ GemmParams p) {
+  gemm_body<2, 1, false, 1, kEpiPlain, DYN, true, true>(p, p);
+}
+
+}  // namespace
+
+cudaError_t launch_tn(const GemmParams& p, bool joined, bool dynamic, int grid, size_t smem, cudaStream_t s) {
+  if (joined)
+    return dynamic ? launch_two_consumer(gemm_tn_joined_kernel<true>, p, grid, smem, s)
+                   : launch_two_consumer(gemm_tn_joined_kernel<false>, p, grid, smem, s);
+  return dynamic ? launch_two_consumer(gemm_tn_2c_kernel<true>, p, grid, smem, s)
+                 : launch_two_consumer(gemm_tn_2c_kernel<false>, p, grid, smem, s);
+}
+
+cudaError_t set_tn_attributes(size_t smem) {
+  const void* fns[] = {reinterpret_cast<const void*>(gemm_tn_2c_kernel<false>),
+                       reinterpret_cast<const void*>(gemm_tn_2c_kernel<true>),
+                       reinterpret_cast<const void*>(gemm_tn_joined_kernel<false>),
+                       reinterpret_cast<const void*>(gemm_tn_joined_kernel<true>)};
+  return set_max_smem(fns, smem);
+}
+
+// ---------------------------------------------------------- entry points ---
+
+namespace {
+
+struct TnCall {
+  int dtype, out_dtype;
+  const void* a;       // [rows, M]
+  const void* b;       // [rows, N]
+  void* d;             // G planes [M, N]
+  const int* offsets;  // nullptr: one group of all rows
+  int G, M, N, rows, lda, ldb, ldd;
+};
+
+CUtensorMapDataType map_type(int dtype) {
+  return dtype == BWG_OUT_FP32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32
+         : dtype == BWG_OUT_FP16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+}
+
+bwg_status check_tn(const TnCall& c) {
+  if (c.dtype != BWG_OUT_BF16 && c.dtype != BWG_OUT_FP16) return BWG_ERR_INVALID_ARG;
+  if (c.out_dtype != BWG_OUT_BF16 && c.out_dtype != BWG_OUT_FP16 && c.out_dtype != BWG_OUT_FP32)
+    return BWG_ERR_INVALID_ARG;
+  if (c.G < 0 || c.M < 0 || c.N < 0 || c.rows < 0) return BWG_ERR_INVALID_ARG;
+  if (c.G == 0 || c.M == 0 || c.N == 0) return BWG_OK;
+  if (c.d == nullptr || c.ldd < c.N) return BWG_ERR_INVALID_ARG;
+  const int oe = c.out_dtype == BWG_OUT_FP32 ? 4 : 2;
+  if (!is_aligned(c.d, 16) || static_cast<long long>(c.ldd) * oe % 16 != 0) return BWG_ERR_ALIGNMENT;
+  if (c.rows == 0) return BWG_OK;
+  if (c.a == nullptr || c.b == nullptr || c.lda < c.M || c.ldb < c.N) return BWG_ERR_INVALID_ARG;
+  if (!is_aligned(c.a, 16) || !is_aligned(c.b, 16) || c.lda % 8 != 0 || c.ldb % 8 != 0) return BWG_ERR_ALIGNMENT;
+  return BWG_OK;
+}
+
+// Windows of kBK rows, one for every row that a window can start at (see gemm_body).
+bool window_map(CUtensorMap* m, const void* p, int dtype, int cols, int rows, int ld) {
+  const uint64_t dims[3] = {static_cast<uint64_t>(cols), static_cast<uint64_t>(kBK), static_cast<uint64_t>(rows)};
+  const uint64_t strides[2] = {static_cast<uint64_t>(ld) * 2, static_cast<uint64_t>(ld) * 2};
+  const uint32_t box[3] = {64, kBK, 1};
+  return runtime_map(m, p, map_type(dtype), 3, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B);
+}
+
+bwg_status run_tn(const TnCall& c, cudaStream_t stream) {
+  bwg_status s = check_tn(c);
+  if (s != BWG_OK || c.G == 0 || c.M == 0 || c.N == 0) return s;
+  Runtime rt;
+  if ((s = runtime_device(&rt)) != BWG_OK) return s;
+  const int oe = c.out_dtype == BWG_OUT_FP32 ? 4 : 2;
+  if (c.rows == 0) {
+    const long long all = static_cast<long long>(c.G) * c.M;
+    if (all > 0x7fffffffLL) return BWG_ERR_UNSUPPORTED;
+    return runtime_status(launch_zero_fill(c.d, static_cast<int>(all), c.N, c.ldd, oe, stream));
+  }
+  auto ceil_div = [](int a, int b) { return (a + b - 1) / b; };
+  const int n_tiles = ceil_div(c.N, kTileN);
+  // FP32 results keep what TMEM's sums lose; other results are 16 bits wide
+  const long long tiles_2c = static_cast<long long>(c.G) * ceil_div(c.M, 4 * kRowsPerCta) * n_tiles;
+  const bool joined = c.out_dtype == BWG_OUT_FP32 || tiles_2c < rt.pairs_2c;
+  const int nc = joined ? 1 : 2, stages = joined ? 6 : 4;
+  const int smem = dense_smem(2, stages, false, nc);
+  if (smem > rt.max_smem) return BWG_ERR_UNSUPPORTED;
+  for (int g0 = 0; g0 < c.G; g0 += kMaxGroupsPerLaunch) {
+    GemmParams p;
+    std::memset(&p, 0, sizeof(p));
+    const uint64_t row = static_cast<uint64_t>(c.ldd) * oe;
+    const uint64_t dims[3] = {static_cast<uint64_t>(c.N), static_cast<uint64_t>(c.M), static_cast<uint64_t>(c.G)};
+    const uint64_t strides[2] = {row, row * c.M};
+    const uint32_t box[3] = {oe == 4 ? 32u : 64u, 32, 1};
+    if (!window_map(&p.map_a, c.a, c.dtype, c.M, c.rows, c.lda) ||
+        !window_map(&p.map_b, c.b, c.dtype, c.N, c.rows, c.ldb) ||
+        !runtime_map(&p.map_d, c.d, map_type(c.out_dtype), 3, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B))
+      return BWG_ERR_CUDA;
+    p.err = rt.err;
+    p.d_ptr = c.d;
+    p.group_offsets = c.offsets;
+    p.timeout_ns = rt.timeout_ns;
+    p.M = c.M;
+    p.N = c.N;
+    p.K = c.rows;
+    p.ldd = c.ldd;
+    p.num_m_tiles = ceil_div(c.M, 2 * kRowsPerCta * nc);
+    p.num_n_tiles = n_tiles;
+    p.group_m = kGroupM;
+    p.stages = stages;
+    p.out_dtype = c.out_dtype;
+    p.idesc = make_idesc_f16(c.dtype == BWG_OUT_FP16 ? kFmtF16 : kFmtBF16, true, true, 2 * kRowsPerCta, kTileN);
+    p.tx_extra = rt.tx_extra;
+    p.trace = rt.trace;
+    p.no_tail_split = rt.no_tail_split;
+    p.splits = 1;
+    p.G = std::min(kMaxGroupsPerLaunch, c.G - g0);
+    p.g_begin = g0;
+    p.G_total = c.G;
+    const long long tiles = static_cast<long long>(p.G) * p.num_m_tiles * n_tiles;
+    if (tiles > 0x0fffffff) return BWG_ERR_UNSUPPORTED;
+    p.workers = static_cast<int>(std::min<long long>(tiles, joined ? rt.pairs : rt.pairs_2c));
+    // groups differ in length: units are claimed at run time
+    const bool dynamic = c.offsets != nullptr;
+    const long long pairs = dynamic ? tiles + 3LL * p.workers : p.workers;
+    const cudaError_t e = launch_tn(p, joined, dynamic, static_cast<int>(2 * pairs), smem, stream);
+    if (e != cudaSuccess) return runtime_status(e);
+  }
+  return BWG_OK;
+}
+
+}  // namespace
+}  // namespace bwg
+
+extern "C" {
+
+bwg_status gemm_tn(const void* A, const void* B, void* D, int dtype, int out_dtype, int M, int N, int K, int lda,
+                   int ldb, int ldd, void* stream) {
+  return run_tn(TnCall{dtype, out_dtype, A, B, D, nullptr, 1, M, N, K, lda, ldb, ldd},
+                static_cast<cudaStream_t>(stream));
+}
+
+bwg_status grouped_gemm_tn(const void* A, const void* B, void* D, const int* group_offsets, int dtype, int out_dtype,
+                           int G, int M, int N, int K_total, void* stream) {
+  if (G > 0 && M > 0 && N > 0 && group_offsets == nullptr) return BWG_ERR_INVALID_ARG;
+  return run_tn(TnCall{dtype, out_dtype, A, B, D, group_offsets, G, M, N, K_total, M, N, N},
+                static_cast<cudaStream_t>(stream));
+}
+
+}  // extern "C"

@@ -1,0 +1,444 @@
+// Matrices kept in 8 bits between a training step's passes: put there, read
+// back, and SwiGLU's gradient from gate and up kept so.
+//
+//   a = largest magnitude of a block of 64 columns of a row
+//   scale = a / 127,  code = rint(x * (127 / a)),  value = code * scale
+//
+// Both quotients are rounded to FP32 and the product with the second is rounded
+// once, to the integer.  A matrix in two parts (gate and up) has blocks of its
+// own in each.  A block with an infinity or a NaN in it reads back as NaN; one
+// whose largest magnitude is below 2^-121 as zero.
+//
+// What bounds these kernels: HBM.  One pass; four lanes share a block, 16 columns
+// each, so that its maximum takes two exchanges and a warp reads whole lines.
+#include <algorithm>
+#include <cstdint>
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+#include <type_traits>
+
+#include "../../include/bwgemm.h"
+#include "params.h"
+#include "runtime.h"
+#include "swiglu.cuh"
+
+namespace bwg {
+namespace {
+
+constexpr int kThreadsInt8 = 256;
+constexpr int kRowsPerWarp = 4;   // rows in flight a lane
+
+struct Int8Params {
+  const void* x;        // quantise: the matrix; SwiGLU gradient: H's gradient
+  void* y;              // read back: the matrix; SwiGLU gradient: [dgate | dup]
+  void* h;              // SwiGLU gradient: H, or nullptr
+  int8_t* codes;
+  float* scales;
+  long long ldx, ldy, ldh;  // elements
+  long long rows;       // rows of parts: matrix rows x parts
+  int cols;             // columns of a part
+  int blocks;           // blocks of a part
+  int part_bits;        // 0 or 1: log2 of the parts
+  int segs;             // column segments of a part's row
+};
+
+template <int IN>
+using Elem = std::conditional_t<IN == kOutF32, float, uint16_t>;
+
+template <int IN>
+__device__ __forceinline__ float to_float(Elem<IN> v) {
+  if constexpr (IN == kOutF32)
+    return v;
+  else if constexpr (IN == kOutBF16)
+    return __uint_as_float(static_cast<uint32_t>(v) << 16);
+  else
+    return __half2float(__ushort_as_half(v));
+}
+
+template <int OUT>
+__device__ __forceinline__ Elem<OUT> from_float(float v) {
+  if constexpr (OUT == kOutF32)
+    return v;
+  else
+    return static_cast<uint16_t>(OUT == kOutBF16 ? cvt_rn_bf16(v) : cvt_rn_f16(v));
+}
+
+// 8 values from 16-byte aligned memory.
+template <int IN>
+__device__ __forceinline__ void load8(const Elem<IN>* p, float (&v)[8]) {
+  if constexpr (IN == kOutF32) {
+    const float4 a = reinterpret_cast<const float4*>(p)[0], b = reinterpret_cast<const float4*>(p)[1];
+    v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+  } else {
+    const uint4 a = *reinterpret_cast<const uint4*>(p);
+    unpack_pair(a.x, IN == kOutBF16, &v[0], &v[1]);
+    unpack_pair(a.y, IN == kOutBF16, &v[2], &v[3]);
+    unpack_pair(a.z, IN == kOutBF16, &v[4], &v[5]);
+    unpack_pair(a.w, IN == kOutBF16, &v[6], &v[7]);
+  }
+}
+
+template <int OUT>
+__device__ __forceinline__ void store8(Elem<OUT>* p, const float (&v)[8]) {
+  if constexpr (OUT == kOutF32) {
+    reinterpret_cast<float4*>(p)[0] = make_float4(v[0], v[1], v[2], v[3]);
+    reinterpret_cast<float4*>(p)[1] = make_float4(v[4], v[5], v[6], v[7]);
+  } else {
+    auto pk = [](float a, float b) { return OUT == kOutBF16 ? pack_bf16x2(a, b) : pack_f16x2(a, b); };
+    *reinterpret_cast<uint4*>(p) = make_uint4(pk(v[0], v[1]), pk(v[2], v[3]), pk(v[4], v[5]), pk(v[6], v[7]));
+  }
+}
+
+// The four codes of a word as floats: each byte, its sign bit turned over, as the
+// low mantissa bits of 2^23, less 2^23 + 128.
+__device__ __forceinline__ void codes4(uint32_t w, float* v) {
+  const uint32_t b = w ^ 0x80808080u;
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    v[i] = __uint_as_float(__byte_perm(b, 0x4B000000u, 0x7540u | i)) - 8388736.0f;
+}
+
+// Where part row v of a matrix with row stride ld starts.
+__device__ __forceinline__ long long part_row(const Int8Params& p, long long v, long long ld) {
+  return (v >> p.part_bits) * ld + (v & ((1 << p.part_bits) - 1)) * p.cols;
+}
+
+// VEC: rows, parts and their ends lie on multiples of 8 elements in all buffers.
+// A warp takes 32 / L rows at a time, L lanes a row of 16 columns each.
+template <int IN, int L>
+__global__ void __launch_bounds__(kThreadsInt8) quantize_int8_kernel(const Int8Params p) {
+  constexpr int kR = 32 / L;
+  const int lane = static_cast<int>(threadIdx.x & 31u), sub = lane % L;
+  const long long rb = blockIdx.x / p.segs;
+  const int seg = static_cast<int>(blockIdx.x - rb * p.segs);
+  const int col = (seg * L + sub) * 16;
+  const long long row0 = (rb * (kThreadsInt8 / 32) + (threadIdx.x >> 5)) * (kR * kRowsPerWarp) + lane / L;
+  float v[kRowsPerWarp][16];
+#pragma unroll
+  for (int r = 0; r < kRowsPerWarp; ++r) {
+    const long long row = row0 + r * kR;
+    const Elem<IN>* src = static_cast<const Elem<IN>*>(p.x) + part_row(p, row, p.ldx) + col;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      float t[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+      if (row < p.rows && col + 8 * h < p.cols) load8<IN>(src + 8 * h, t);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[r][8 * h + i] = t[i];
+    }
+  }
+#pragma unroll
+  for (int r = 0; r < kRowsPerWarp; ++r) {
+    const long long row = row0 + r * kR;
+    float a = 0.f, b = 0.f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      a = max_abs_nan(a, v[r][i]);
+      b = max_abs_nan(b, v[r][8 + i]);
+    }
+    a = max_abs_nan(a, b);
+    a = max_abs_nan(a, __shfl_xor_sync(0xffffffffu, a, 1));
+    a = max_abs_nan(a, __shfl_xor_sync(0xffffffffu, a, 2));
+    float scale, inv;
+    int8_scale(a, &scale, &inv);
+    if (row < p.rows && col < p.cols) {
+      uint32_t w[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        w[i] = pack_bytes(int8_code(v[r][4 * i], inv), int8_code(v[r][4 * i + 1], inv),
+                          int8_code(v[r][4 * i + 2], inv), int8_code(v[r][4 * i + 3], inv));
+      int8_t* dst = p.codes + row * p.cols + col;
+      if ((p.cols & 15) == 0) {
+        *reinterpret_cast<uint4*>(dst) = make_uint4(w[0], w[1], w[2], w[3]);
+      } else {
+        reinterpret_cast<uint2*>(dst)[0] = make_uint2(w[0], w[1]);
+        if (col + 8 < p.cols) reinterpret_cast<uint2*>(dst)[1] = make_uint2(w[2], w[3]);
+      }
+      if ((sub & 3) == 0) p.scales[row * p.blocks + (col >> 6)] = scale;
+    }
+  }
+}
+
+// Any width and stride: a warp takes a block, two columns a lane.
+template <int IN>
+__global__ void __launch_bounds__(kThreadsInt8) quantize_int8_odd_kernel(const Int8Params p) {
+  const int lane = static_cast<int>(threadIdx.x & 31u);
+  const long long total = p.rows * p.blocks;
+  const long long step = static_cast<long long>(gridDim.x) * (kThreadsInt8 / 32);
+  for (long long t = static_cast<long long>(blockIdx.x) * (kThreadsInt8 / 32) + (threadIdx.x >> 5); t < total;
+       t += step) {
+    const long long row = t / p.blocks;
+    const int c0 = static_cast<int>(t - row * p.blocks) * kInt8Block + lane;
+    const Elem<IN>* src = static_cast<const Elem<IN>*>(p.x) + part_row(p, row, p.ldx) + c0;
+    const float v0 = c0 < p.cols ? to_float<IN>(src[0]) : 0.f;
+    const float v1 = c0 + 32 < p.cols ? to_float<IN>(src[32]) : 0.f;
+    float a = max_abs_nan(v0, v1);
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) a = max_abs_nan(a, __shfl_xor_sync(0xffffffffu, a, d));
+    float scale, inv;
+    int8_scale(a, &scale, &inv);
+    int8_t* dst = p.codes + row * p.cols + c0;
+    if (c0 < p.cols) dst[0] = static_cast<int8_t>(int8_code(v0, inv) & 0xFFu);
+    if (c0 + 32 < p.cols) dst[32] = static_cast<int8_t>(int8_code(v1, inv) & 0xFFu);
+    if (lane == 0) p.scales[t] = scale;
+  }
+}
+
+template <int OUT, int L>
+__global__ void __launch_bounds__(kThreadsInt8) dequantize_int8_kernel(const Int8Params p) {
+  constexpr int kR = 32 / L;
+  const int lane = static_cast<int>(threadIdx.x & 31u), sub = lane % L;
+  const long long rb = blockIdx.x / p.segs;
+  const int seg = static_cast<int>(blockIdx.x - rb * p.segs);
+  const int col = (seg * L + sub) * 16;
+  const long long row0 = (rb * (kThreadsInt8 / 32) + (threadIdx.x >> 5)) * (kR * kRowsPerWarp) + lane / L;
+  uint32_t w[kRowsPerWarp][4];
+  float scale[kRowsPerWarp];
+#pragma unroll
+  for (int r = 0; r < kRowsPerWarp; ++r) {
+    const long long row = row0 + r * kR;
+    if (row < p.rows && col < p.cols) {
+      const int8_t* src = p.codes + row * p.cols + col;
+      if ((p.cols & 15) == 0) {
+        const uint4 q = *reinterpret_cast<const uint4*>(src);
+        w[r][0] = q.x, w[r][1] = q.y, w[r][2] = q.z, w[r][3] = q.w;
+      } else {
+        const uint2 q = reinterpret_cast<const uint2*>(src)[0];
+        w[r][0] = q.x, w[r][1] = q.y;
+        if (col + 8 < p.cols) {
+          const uint2 q1 = reinterpret_cast<const uint2*>(src)[1];
+          w[r][2] = q1.x, w[r][3] = q1.y;
+        }
+      }
+      scale[r] = p.scales[row * p.blocks + (col >> 6)];
+    }
+  }
+#pragma unroll
+  for (int r = 0; r < kRowsPerWarp; ++r) {
+    const long long row = row0 + r * kR;
+    Elem<OUT>* dst = static_cast<Elem<OUT>*>(p.y) + part_row(p, row, p.ldy) + col;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      if (row < p.rows && col + 8 * h < p.cols) {
+        float v[8];
+        codes4(w[r][2 * h], v);
+        codes4(w[r][2 * h + 1], v + 4);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] *= scale[r];
+        store8<OUT>(dst + 8 * h, v);
+      }
+    }
+  }
+}
+
+template <int OUT>
+__global__ void __launch_bounds__(kThreadsInt8) dequantize_int8_odd_kernel(const Int8Params p) {
+  const int lane = static_cast<int>(threadIdx.x & 31u);
+  const long long total = p.rows * p.blocks;
+  const long long step = static_cast<long long>(gridDim.x) * (kThreadsInt8 / 32);
+  for (long long t = static_cast<long long>(blockIdx.x) * (kThreadsInt8 / 32) + (threadIdx.x >> 5); t < total;
+       t += step) {
+    const long long row = t / p.blocks;
+    const int c0 = static_cast<int>(t - row * p.blocks) * kInt8Block + lane;
+    const float scale = p.scales[t];
+    const int8_t* src = p.codes + row * p.cols + c0;
+    Elem<OUT>* dst = static_cast<Elem<OUT>*>(p.y) + part_row(p, row, p.ldy) + c0;
+    if (c0 < p.cols) dst[0] = from_float<OUT>(static_cast<float>(src[0]) * scale);
+    if (c0 + 32 < p.cols) dst[32] = from_float<OUT>(static_cast<float>(src[32]) * scale);
+  }
+}
+
+// dgate and dup (and H) from H's gradient and gate and up kept in 8 bits: a lane
+// takes 8 columns of a row, a warp 256.
+template <int IO, bool WITH_H>
+__global__ void __launch_bounds__(kThreadsInt8) swiglu_grad_int8_kernel(const Int8Params p) {
+  const int lane = static_cast<int>(threadIdx.x & 31u);
+  const long long rb = blockIdx.x / p.segs;
+  const int seg = static_cast<int>(blockIdx.x - rb * p.segs);
+  const int col = (seg * 32 + lane) * 8;
+  if (col >= p.cols) return;
+  const long long row0 = (rb * (kThreadsInt8 / 32) + (threadIdx.x >> 5)) * kRowsPerWarp;
+  uint2 cg[kRowsPerWarp], cu[kRowsPerWarp];
+  uint4 dh[kRowsPerWarp];
+  float sg[kRowsPerWarp], su[kRowsPerWarp];
+#pragma unroll
+  for (int r = 0; r < kRowsPerWarp; ++r) {
+    const long long row = row0 + r;
+    if (row < p.rows) {
+      dh[r] = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.x) + row * p.ldx + col);
+      cg[r] = *reinterpret_cast<const uint2*>(p.codes + row * 2 * p.cols + col);
+      cu[r] = *reinterpret_cast<const uint2*>(p.codes + row * 2 * p.cols + p.cols + col);
+      const float* sc = p.scales + row * 2 * p.blocks + (col >> 6);
+      sg[r] = sc[0];
+      su[r] = sc[p.blocks];
+    }
+  }
+#pragma unroll
+  for (int r = 0; r < kRowsPerWarp; ++r) {
+    const long long row = row0 + r;
+    if (row < p.rows) {
+      float g[8], u[8], d[8], dg[8], du[8], h[8];
+      codes4(cg[r].x, g);
+      codes4(cg[r].y, g + 4);
+      codes4(cu[r].x, u);
+      codes4(cu[r].y, u + 4);
+      unpack_pair(dh[r].x, IO == kOutBF16, &d[0], &d[1]);
+      unpack_pair(dh[r].y, IO == kOutBF16, &d[2], &d[3]);
+      unpack_pair(dh[r].z, IO == kOutBF16, &d[4], &d[5]);
+      unpack_pair(dh[r].w, IO == kOutBF16, &d[6], &d[7]);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        g[i] *= sg[r];
+        u[i] *= su[r];
+        const float s = rcp_approx(1.0f + __expf(-g[i])), t = d[i] * s;
+        du[i] = t * g[i];
+        dg[i] = t * u[i] * fmaf(g[i], 1.0f - s, 1.0f);
+        if constexpr (WITH_H) h[i] = g[i] * s * u[i];
+      }
+      uint16_t* dst = static_cast<uint16_t*>(p.y) + row * p.ldy + col;
+      store8<IO>(dst, dg);
+      store8<IO>(dst + p.cols, du);
+      if constexpr (WITH_H) store8<IO>(static_cast<uint16_t*>(p.h) + row * p.ldh + col, h);
+    }
+  }
+}
+
+int elt_bytes(int dtype) { return dtype == kOutF32 ? 4 : 2; }
+
+bool known(int dtype) { return dtype == kOutBF16 || dtype == kOutF16 || dtype == kOutF32; }
+
+// Lanes a row of `cols` columns takes, a power of two of 4 .. 32.
+int row_lanes(int cols) {
+  int l = 4;
+  while (l < 32 && l * 16 < cols) l *= 2;
+  return l;
+}
+
+// Grid of a row kernel whose warps take `rows` rows of `cols` columns at a time; 0: too large.
+unsigned row_grid(Int8Params* p, int cols, int rows) {
+  p->segs = (p->cols + cols - 1) / cols;
+  const long long per = static_cast<long long>(kThreadsInt8 / 32) * rows;
+  const long long blocks = (p->rows + per - 1) / per * p->segs;
+  return blocks > 0x7fffffffLL ? 0u : static_cast<unsigned>(blocks);
+}
+
+template <int T, int L>
+bool launch_rows(Int8Params p, bool back, cudaStream_t s) {
+  const unsigned grid = row_grid(&p, 16 * L, 32 / L * kRowsPerWarp);
+  if (grid == 0) return false;
+  if (back)
+    dequantize_int8_kernel<T, L><<<grid, kThreadsInt8, 0, s>>>(p);
+  else
+    quantize_int8_kernel<T, L><<<grid, kThreadsInt8, 0, s>>>(p);
+  return true;
+}
+
+template <int T>
+bool launch_type(const Int8Params& p, bool back, bool vec, int sm_count, cudaStream_t s) {
+  if (!vec) {
+    const long long warps = p.rows * p.blocks;
+    const unsigned grid = static_cast<unsigned>(
+        std::min<long long>((warps + kThreadsInt8 / 32 - 1) / (kThreadsInt8 / 32), 64LL * sm_count));
+    if (back)
+      dequantize_int8_odd_kernel<T><<<grid, kThreadsInt8, 0, s>>>(p);
+    else
+      quantize_int8_odd_kernel<T><<<grid, kThreadsInt8, 0, s>>>(p);
+    return true;
+  }
+  switch (row_lanes(p.cols)) {
+    case 4: return launch_rows<T, 4>(p, back, s);
+    case 8: return launch_rows<T, 8>(p, back, s);
+    case 16: return launch_rows<T, 16>(p, back, s);
+    default: return launch_rows<T, 32>(p, back, s);
+  }
+}
+
+// Shared by both directions: m [M, N] with row stride ld in `dtype`.
+bwg_status run_int8(bool back, const void* m, int dtype, int M, int N, int ld, int parts, void* codes, float* scales,
+                    cudaStream_t stream) {
+  if (!known(dtype) || M < 0 || N < 0 || (parts != 1 && parts != 2) || N % parts != 0) return BWG_ERR_INVALID_ARG;
+  if (M == 0 || N == 0) return BWG_OK;
+  if (m == nullptr || codes == nullptr || scales == nullptr || ld < N) return BWG_ERR_INVALID_ARG;
+  if (!is_aligned(m, elt_bytes(dtype)) || !is_aligned(scales, 4)) return BWG_ERR_ALIGNMENT;
+  Runtime rt;
+  const bwg_status s = runtime_device(&rt);
+  if (s != BWG_OK) return s;
+  Int8Params p = {};
+  p.x = m;
+  p.y = const_cast<void*>(m);
+  p.codes = static_cast<int8_t*>(codes);
+  p.scales = scales;
+  p.ldx = p.ldy = ld;
+  p.rows = static_cast<long long>(M) * parts;
+  p.cols = N / parts;
+  p.blocks = (p.cols + kInt8Block - 1) / kInt8Block;
+  p.part_bits = parts - 1;
+  const bool vec = p.cols % 8 == 0 && is_aligned(m, 16) && is_aligned(codes, 16) &&
+                   static_cast<long long>(ld) * elt_bytes(dtype) % 16 == 0;
+  const bool ok = dtype == kOutBF16  ? launch_type<kOutBF16>(p, back, vec, rt.sm_count, stream)
+                  : dtype == kOutF16 ? launch_type<kOutF16>(p, back, vec, rt.sm_count, stream)
+                                     : launch_type<kOutF32>(p, back, vec, rt.sm_count, stream);
+  return ok ? runtime_status(cudaGetLastError()) : BWG_ERR_UNSUPPORTED;
+}
+
+}  // namespace
+}  // namespace bwg
+
+using namespace bwg;
+
+extern "C" {
+
+bwg_status quantize_int8(const void* x, int dtype, int M, int N, int ldx, int parts, void* codes, float* scales,
+                         void* stream) {
+  return run_int8(false, x, dtype, M, N, ldx, parts, codes, scales, static_cast<cudaStream_t>(stream));
+}
+
+bwg_status dequantize_int8(const void* codes, const float* scales, int parts, void* y, int dtype, int M, int N,
+                           int ldy, void* stream) {
+  return run_int8(true, y, dtype, M, N, ldy, parts, const_cast<void*>(codes), const_cast<float*>(scales),
+                  static_cast<cudaStream_t>(stream));
+}
+
+bwg_status swiglu_grad_int8(const void* dH, const void* codes, const float* scales, void* dGU, void* H, int dtype,
+                            int M, int I, int lddh, int ldd, int ldh, void* stream) {
+  if ((dtype != BWG_OUT_BF16 && dtype != BWG_OUT_FP16) || M < 0 || I < 0 || I > 0x3fffffff) return BWG_ERR_INVALID_ARG;
+  if (M == 0 || I == 0) return BWG_OK;
+  if (dH == nullptr || codes == nullptr || scales == nullptr || dGU == nullptr || lddh < I || ldd < 2 * I ||
+      (H != nullptr && ldh < I))
+    return BWG_ERR_INVALID_ARG;
+  if (I % 8 != 0 || !is_aligned(dH, 16) || !is_aligned(codes, 16) || !is_aligned(scales, 4) || !is_aligned(dGU, 16) ||
+      lddh % 8 != 0 || ldd % 8 != 0 || (H != nullptr && (!is_aligned(H, 16) || ldh % 8 != 0)))
+    return BWG_ERR_ALIGNMENT;
+  Runtime rt;
+  const bwg_status s = runtime_device(&rt);
+  if (s != BWG_OK) return s;
+  Int8Params p = {};
+  p.x = dH;
+  p.y = dGU;
+  p.h = H;
+  p.codes = static_cast<int8_t*>(const_cast<void*>(codes));
+  p.scales = const_cast<float*>(scales);
+  p.ldx = lddh;
+  p.ldy = ldd;
+  p.ldh = ldh;
+  p.rows = M;
+  p.cols = I;
+  p.blocks = (I + kInt8Block - 1) / kInt8Block;
+  const unsigned grid = row_grid(&p, 256, kRowsPerWarp);
+  if (grid == 0) return BWG_ERR_UNSUPPORTED;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  if (dtype == BWG_OUT_BF16) {
+    if (H != nullptr)
+      swiglu_grad_int8_kernel<kOutBF16, true><<<grid, kThreadsInt8, 0, st>>>(p);
+    else
+      swiglu_grad_int8_kernel<kOutBF16, false><<<grid, kThreadsInt8, 0, st>>>(p);
+  } else {
+    if (H != nullptr)
+      swiglu_grad_int8_kernel<kOutF16, true><<<grid, kThreadsInt8, 0, st>>>(p);
+    else
+      swiglu_grad_int8_kernel<kOutF16, false><<<grid, kThreadsInt8, 0, st>>>(p);
+  }
+  return runtime_status(cudaGetLastError());
+}
+
+}  // extern "C"

@@ -29,6 +29,19 @@ constexpr int kMaxGroupsPerLaunch = 64;
 constexpr int kSmallMMaxM = 128;     // swapped kernel handles up to 128 rows of A
 constexpr int kMaxSplit = 8;         // largest cluster of the small-M split (portable size)
 
+constexpr int kBarrierArea = 2048;   // barriers, TMEM address slot, grouped tables
+constexpr int kGroupM = 8;           // raster: tile rows per group
+
+// Per-CTA bytes of one ring stage: nc A blocks of 128 rows and this CTA's
+// share of the B columns, 64 K deep.
+constexpr int dense_stage_bytes(int cg, int nc = 1) {
+  return nc * kRowsPerCta * kBK * 2 + (kTileN / cg) * kBK * 2;
+}
+
+constexpr int dense_smem(int cg, int stages, bool direct_store = false, int nc = 1) {
+  return 1024 + stages * dense_stage_bytes(cg, nc) + (direct_store ? 0 : kEpiBytes) + kBarrierArea;
+}
+
 // Output element type codes (same values as the C ABI).
 constexpr int kOutBF16 = 0;
 constexpr int kOutF32 = 1;
@@ -81,6 +94,7 @@ struct GemmParams {
   int ws_slots;              // partial slots per stream-K tile (most pairs sharing one)
   float* ws;                 // partials [sk_tiles][ws_slots][16 warp slices][32 rows][256] FP32
   int* ws_counters;          // arrivals [sk_tiles][16 warp slices], zero between calls
+  int splits;                // transposed A: slices of each group's k-blocks (planes of D per group)
   // Optional unit trace (nullptr: off): per CTA, kTraceUnits records of
   // kTraceWords words (global timer, ns).
   unsigned long long* trace;
@@ -92,6 +106,25 @@ constexpr int kTraceWords = 5;  // unit, producer start, epilogue end, accumulat
 struct GroupedParams {
   GemmParams base;
   CUtensorMap map_b[kMaxGroupsPerLaunch];
+};
+
+// What the gated kernels' epilogues read and write beside D (see gemm_body):
+// the codes and scales of gate and up, [rows, 2 I] and [rows, 2 blocks], or the
+// gradient of H.
+struct GatedExtra {
+  uint8_t* codes;
+  float* scales;
+  int blocks;    // blocks of 64 columns of gate (and of up)
+  int wide;      // 1: every block of 64 codes starts on a 16-byte boundary
+  const void* dh;
+  int ld_dh;
+};
+
+struct DenseGatedParams : GemmParams {
+  GatedExtra x;
+};
+struct GroupedGatedParams : GroupedParams {
+  GatedExtra x;
 };
 
 struct SmallMParams {
@@ -157,6 +190,14 @@ cudaError_t launch_grouped_2c(const GroupedParams& p, int grid, size_t smem, cud
 int max_active_clusters_grouped_2c(size_t smem);
 cudaError_t launch_grouped_2cta(const GroupedParams& p, int grid, size_t smem, cudaStream_t s,
                                 bool swiglu = false);
+// Gated kernels (gemm_gated.cu): epi = 1 H, 2 H and gate and up in 8 bits, 3 the
+// gradients of gate and up; two = two consumers.  Grouped: 2 and 3, two
+// consumers, cluster launch control.
+cudaError_t launch_gated_dense(const DenseGatedParams& p, int epi, bool two, int grid, size_t smem, cudaStream_t s);
+cudaError_t launch_gated_grouped(const GroupedGatedParams& p, int epi, int grid, size_t smem, cudaStream_t s);
+// Transposed A (gemm_tn.cu): two consumers with sums in TMEM, or one (joined)
+// whose sums are joined in registers; dynamic as above.
+cudaError_t launch_tn(const GemmParams& p, bool joined, bool dynamic, int grid, size_t smem, cudaStream_t s);
 cudaError_t launch_small_m(const SmallMParams& p, int grid, size_t smem, cudaStream_t s);
 // Co-resident clusters of `cluster` small-M CTAs with `smem` bytes each (0 on error).
 int max_active_clusters_small_m(int cluster, size_t smem);

@@ -82,6 +82,17 @@ def lib() -> ctypes.CDLL:
                                ("gemm_fp4", [vp, vp, vp, vp, vp, vp, i, vp, i, i, i, i, i, vp]),
                                ("grouped_gemm_fp4", [vp, vp, vp, vp, vp, vp, i, i, vp, vp, i, i, i, i, i, i, i, vp,
                                                      vp]),
+                               ("gemm_swiglu", [vp, vp, vp, vp, vp, i, i, i, i, i, i, i, i, vp]),
+                               ("gemm_swiglu_grad", [vp, vp, vp, vp, i, i, i, i, i, i, i, i, i, vp]),
+                               ("grouped_gemm_swiglu_keep", [vp, ctypes.POINTER(vp), vp, vp, vp, vp, i, i, i, i, i, i,
+                                                             vp]),
+                               ("grouped_gemm_swiglu_grad", [vp, vp, ctypes.POINTER(vp), vp, vp, i, i, i, i, i, i,
+                                                             vp]),
+                               ("quantize_int8", [vp, i, i, i, i, i, vp, vp, vp]),
+                               ("dequantize_int8", [vp, vp, i, vp, i, i, i, i, vp]),
+                               ("swiglu_grad_int8", [vp, vp, vp, vp, vp, i, i, i, i, i, i, vp]),
+                               ("gemm_tn", [vp, vp, vp, i, i, i, i, i, i, i, i, vp]),
+                               ("grouped_gemm_tn", [vp, vp, vp, vp, i, i, i, i, i, i, vp]),
                                ("moe_combine_grad", [vp, vp, i, i, i, i, i, i, vp, vp, vp, i, vp, i, vp, vp])):
                 f = getattr(L, name)
                 f.argtypes = args
@@ -225,9 +236,14 @@ def _matrix(t: torch.Tensor, name: str) -> int:
 
 
 def gemm(A: torch.Tensor, B: torch.Tensor, out: torch.Tensor | None = None,
-         out_dtype: torch.dtype = torch.bfloat16, stream=None, b_transposed: bool = False) -> torch.Tensor:
+         out_dtype: torch.dtype = torch.bfloat16, stream=None, b_transposed: bool = False,
+         a_transposed: bool = False) -> torch.Tensor:
     """D = A @ B through gemm_bf16 / gemm_fp16 (chosen by A's dtype); with
-    ``b_transposed`` B is given as [N, K] and D = A @ B.T (gemm_*_nt)."""
+    ``b_transposed`` B is given as [N, K] and D = A @ B.T (gemm_*_nt); with
+    ``a_transposed`` A is given as [K, M] and D = A.T @ B (gemm_tn), the gradient
+    of a weight from a layer's input A and its output's gradient B."""
+    if a_transposed:
+        return _gemm_tn(A, B, out, out_dtype, stream, b_transposed)
     if A.dtype != B.dtype or A.dtype not in (torch.bfloat16, torch.float16):
         raise TypeError("A and B must both be bfloat16 or both float16")
     M, K = A.shape
@@ -278,14 +294,8 @@ def gemm_fp16_nt(A_ptr: int, B_ptr: int, D_ptr: int, M: int, N: int, K: int, lda
            "gemm_fp16_nt")
 
 
-def grouped_gemm(A: torch.Tensor, Bs: list, group_offsets: torch.Tensor,
-                 out: torch.Tensor | None = None, stream=None, swiglu: bool = False,
-                 b_transposed: bool = False) -> torch.Tensor:
-    """Grouped expert product through grouped_gemm_bf16 / grouped_gemm_fp16.
-
-    With ``swiglu`` each weight is [gate | up] ([K, N]) and the result is
-    silu(gate) * up, [M_total, N/2], through grouped_gemm_swiglu_bf16/_fp16.
-    With ``b_transposed`` every weight is given as [N, K] (the *_nt entry points)."""
+def _grouped_operands(A: torch.Tensor, Bs: list, group_offsets: torch.Tensor, b_transposed: bool) -> tuple:
+    """(M_total, K, N, G) of a grouped product's checked operands."""
     if A.dtype not in (torch.bfloat16, torch.float16):
         raise TypeError("A must be bfloat16 or float16")
     M_total, K = A.shape
@@ -301,6 +311,24 @@ def grouped_gemm(A: torch.Tensor, Bs: list, group_offsets: torch.Tensor,
     if not A.is_contiguous():
         raise ValueError("A must be dense [M_total, K]")
     _fits("rows, columns or groups", M_total, K, N, G)
+    return M_total, K, N, G
+
+
+def grouped_gemm(A: torch.Tensor, Bs: list, group_offsets: torch.Tensor,
+                 out: torch.Tensor | None = None, stream=None, swiglu: bool = False,
+                 b_transposed: bool = False, keep_int8: bool = False):
+    """Grouped expert product through grouped_gemm_bf16 / grouped_gemm_fp16.
+
+    With ``swiglu`` each weight is [gate | up] ([K, N]) and the result is
+    silu(gate) * up, [M_total, N/2], through grouped_gemm_swiglu_bf16/_fp16.
+    With ``b_transposed`` every weight is given as [N, K] (the *_nt entry points).
+    With ``keep_int8`` (and swiglu) the result is (H, kept): kept is the Int8Matrix
+    of [gate | up] that grouped_gemm_swiglu_grad takes."""
+    M_total, K, N, G = _grouped_operands(A, Bs, group_offsets, b_transposed)
+    if keep_int8:
+        if not swiglu:
+            raise ValueError("keep_int8 keeps the gate and up of a swiglu product")
+        return _grouped_keep(A, Bs, group_offsets, out, stream, b_transposed, M_total, K, N, G)
     n_out = N // 2 if swiglu else N
     if out is None:
         out = torch.empty((M_total, n_out), dtype=A.dtype, device=A.device)
@@ -791,3 +819,310 @@ def grouped_gemm_fp4(A: Fp4Matrix, B: Fp4Matrix, swiglu: bool = False, out: torc
                1 if swiglu else 0, None if work is None else work.data_ptr(), _stream_handle(stream, dev)),
            "grouped_gemm_fp4")
     return out
+
+
+# --------------------------------------- gated feed-forward block, training ---
+
+# As above: the gradients are calls of their own.
+
+_INT8_BLOCK = 64
+
+
+class Int8Matrix:
+    """A matrix [rows, cols] kept in 8 bits between a training step's passes.
+
+    codes   int8 [rows, cols]
+    scales  float32 [rows, parts * ceil(cols / parts / 64)], one for each block of
+            64 columns of a part's row: a value is code * scale
+    parts   1, or 2 for [gate | up], whose halves have blocks of their own
+    """
+
+    __slots__ = ("codes", "scales", "parts")
+
+    def __init__(self, codes, scales, parts=1):
+        self.codes = codes
+        self.scales = scales
+        self.parts = parts
+
+    @property
+    def shape(self):
+        return self.codes.shape
+
+    @property
+    def device(self):
+        return self.codes.device
+
+
+def _int8_blocks(cols: int, parts: int) -> int:
+    return parts * -(-(cols // parts) // _INT8_BLOCK)
+
+
+def _int8_check(q: Int8Matrix, name: str, parts: int | None = None) -> tuple[int, int]:
+    """(rows, cols) of an Int8Matrix whose buffers are as large as the kernels take them."""
+    codes, scales = q.codes, q.scales
+    if q.parts not in (1, 2) or (parts is not None and q.parts != parts):
+        raise ValueError("%s must have %s, got %r" % (name, "1 or 2 parts" if parts is None else "parts=%d" % parts,
+                                                      q.parts))
+    if codes.dtype != torch.int8 or codes.dim() != 2 or not codes.is_contiguous() or not codes.is_cuda:
+        raise ValueError("%s.codes must be a dense CUDA int8 tensor [rows, cols]" % name)
+    rows, cols = codes.shape
+    _fits("rows or columns of " + name, rows, cols)
+    if cols % q.parts:
+        raise ValueError("%s: %d columns do not make %d parts" % (name, cols, q.parts))
+    want = (rows, _int8_blocks(cols, q.parts))
+    if scales.dtype != torch.float32 or scales.shape != want or not scales.is_contiguous() \
+            or scales.device != codes.device:
+        raise ValueError("%s.scales must be a dense float32 tensor [%d, %d] on %s" % (name, *want, codes.device))
+    return rows, cols
+
+
+def _new_int8(rows: int, cols: int, parts: int, dev, stream) -> Int8Matrix:
+    return Int8Matrix(_new((rows, cols), torch.int8, dev, stream),
+                      _new((rows, _int8_blocks(cols, parts)), torch.float32, dev, stream), parts)
+
+
+def quantize_int8(x: torch.Tensor, parts: int = 1, stream=None) -> Int8Matrix:
+    """x [rows, cols] in 8 bits, with a float32 scale for every 64 columns of a
+    row; parts=2 for [gate | up], whose halves have blocks of their own."""
+    rows, cols = x.shape
+    ldx = _rows(x, "x", rows)
+    _fits("columns of x", cols)
+    if parts not in (1, 2) or cols % parts:
+        raise ValueError("parts must be 1 or 2 and divide the columns, got %r for %d" % (parts, cols))
+    q = _new_int8(rows, cols, parts, x.device, stream)
+    _check(_on(x.device, lib().quantize_int8, x.data_ptr(), _OUT_CODES[x.dtype], rows, cols, ldx, parts,
+               q.codes.data_ptr(), q.scales.data_ptr(), _stream_handle(stream, x.device)), "quantize_int8")
+    return q
+
+
+def dequantize_int8(q: Int8Matrix, out_dtype: torch.dtype = torch.bfloat16, out: torch.Tensor | None = None,
+                    stream=None) -> torch.Tensor:
+    """The values of q, [rows, cols], each rounded once."""
+    rows, cols = _int8_check(q, "q")
+    dev = q.codes.device
+    out, ldo = _fp4_out(out, out_dtype, rows, cols, dev, stream)
+    _check(_on(dev, lib().dequantize_int8, q.codes.data_ptr(), q.scales.data_ptr(), q.parts, out.data_ptr(),
+               _OUT_CODES[out.dtype], rows, cols, ldo, _stream_handle(stream, dev)), "dequantize_int8")
+    return out
+
+
+def _half(t: torch.Tensor, name: str) -> None:
+    if t.dtype not in (torch.bfloat16, torch.float16):
+        raise TypeError("%s must be bfloat16 or float16" % name)
+
+
+def _like(t: torch.Tensor, name: str, dtype, dev) -> None:
+    if t.dtype is not dtype or t.device != dev:
+        raise ValueError("%s must be a %s tensor on %s" % (name, dtype, dev))
+
+
+def _gemm_tn(A, B, out, out_dtype, stream, b_transposed) -> torch.Tensor:
+    if b_transposed:
+        raise ValueError("a_transposed takes B as [K, N]")
+    _half(A, "A")
+    dev = A.device
+    _like(B, "B", A.dtype, dev)
+    (K, M), N = A.shape, B.shape[1]
+    lda, ldb = _rows(A, "A", K), _rows(B, "B", K)
+    _fits("M or N", M, N)
+    out, ldd = _fp4_out(out, out_dtype, M, N, dev, stream)
+    _check(_on(dev, lib().gemm_tn, A.data_ptr(), B.data_ptr(), out.data_ptr(), _OUT_CODES[A.dtype],
+               _OUT_CODES[out.dtype], M, N, K, lda, ldb, ldd, _stream_handle(stream, dev)), "gemm_tn")
+    return out
+
+
+def grouped_gemm_wgrad(A: torch.Tensor, B: torch.Tensor, group_offsets: torch.Tensor,
+                       out: torch.Tensor | None = None, out_dtype: torch.dtype | None = None,
+                       stream=None) -> torch.Tensor:
+    """Gradients of the experts' weights: out[g] = A_g.T @ B_g over group g's rows
+    of A [rows, M] (the layer's input) and B [rows, N] (its output's gradient),
+    [G, M, N] in out_dtype (default: A's); zeros for a group without rows."""
+    _half(A, "A")
+    dev = A.device
+    _like(B, "B", A.dtype, dev)
+    if not A.is_contiguous() or not B.is_contiguous() or A.dim() != 2 or B.dim() != 2 or A.shape[0] != B.shape[0]:
+        raise ValueError("A and B must be dense [rows, M] and [rows, N]")
+    _like(group_offsets, "group_offsets", torch.int32, dev)
+    if group_offsets.dim() != 1 or group_offsets.shape[0] < 2 or not group_offsets.is_contiguous():
+        raise ValueError("group_offsets must be a dense int32 tensor [G + 1]")
+    (rows, M), N, G = A.shape, B.shape[1], group_offsets.shape[0] - 1
+    _fits("rows, columns or groups", rows, M, N, G)
+    if out is None:
+        out = _new((G, M, N), A.dtype if out_dtype is None else out_dtype, dev, stream)
+    elif out.shape != (G, M, N) or not out.is_contiguous() or out.device != dev or \
+            (out_dtype is not None and out.dtype is not out_dtype):
+        raise ValueError("out must be a dense [%d, %d, %d] tensor on %s" % (G, M, N, dev))
+    if out.dtype not in _OUT_CODES:
+        raise TypeError("output dtype must be bfloat16, float16 or float32")
+    _check(_on(dev, lib().grouped_gemm_tn, A.data_ptr(), B.data_ptr(), out.data_ptr(), group_offsets.data_ptr(),
+               _OUT_CODES[A.dtype], _OUT_CODES[out.dtype], G, M, N, rows, _stream_handle(stream, dev)),
+           "grouped_gemm_tn")
+    return out
+
+
+def _gated_weight(w: torch.Tensor, dtype, dev, K: int, b_transposed: bool) -> tuple[int, int]:
+    """(N, leading dimension) of a gated block's weight [K, N], or [N, K]."""
+    _like(w, "w", dtype, dev)
+    ldw = _rows(w, "w", w.shape[0])
+    N, K2 = w.shape if b_transposed else (w.shape[1], w.shape[0])
+    if K2 != K:
+        raise ValueError("inner dimensions differ: x has %d columns, w %s" % (K, tuple(w.shape)))
+    _fits("columns of w", N, K)
+    if N % 2:
+        raise ValueError("w must hold gate and up: an even number of columns, got %d" % N)
+    return N, ldw
+
+
+def gemm_swiglu(x: torch.Tensor, w: torch.Tensor, out: torch.Tensor | None = None, stream=None,
+                b_transposed: bool = False, keep_int8: bool = False):
+    """The gated feed-forward block, silu(x @ gate) * (x @ up) for w = [gate | up]
+    ([K, N], or [N, K] with ``b_transposed``): [M, N / 2] in x's dtype.  With
+    ``keep_int8`` the result is (h, kept): kept is the Int8Matrix of [gate | up]
+    that gemm_swiglu_grad takes."""
+    _half(x, "x")
+    dev, dtype = x.device, x.dtype
+    M, K = x.shape
+    ldx = _rows(x, "x", M)
+    N, ldw = _gated_weight(w, dtype, dev, K, b_transposed)
+    out, ldh = _out_rows(out, M, N // 2, dtype, dev, stream)
+    kept = _new_int8(M, N, 2, dev, stream) if keep_int8 else None
+    _check(_on(dev, lib().gemm_swiglu, x.data_ptr(), w.data_ptr(), out.data_ptr(),
+               kept.codes.data_ptr() if keep_int8 else None, kept.scales.data_ptr() if keep_int8 else None,
+               _OUT_CODES[dtype], 1 if b_transposed else 0, M, N, K, ldx, ldw, ldh, _stream_handle(stream, dev)),
+           "gemm_swiglu")
+    return (out, kept) if keep_int8 else out
+
+
+def _grouped_keep(A, Bs, group_offsets, out, stream, b_transposed, M_total, K, N, G) -> tuple:
+    dev = A.device
+    if N % 2:
+        raise ValueError("swiglu needs an even number of weight columns, got %d" % N)
+    if out is None:
+        out = _new((M_total, N // 2), A.dtype, dev, stream)
+    elif out.shape != (M_total, N // 2) or out.dtype != A.dtype or not out.is_contiguous() or out.device != dev:
+        raise ValueError("out must be a dense [M_total, %d] tensor of A's dtype" % (N // 2))
+    kept = _new_int8(M_total, N, 2, dev, stream)
+    p, keep = _ptr_array([b.data_ptr() for b in Bs])
+    _check(_on(dev, lib().grouped_gemm_swiglu_keep, A.data_ptr(), p, out.data_ptr(), kept.codes.data_ptr(),
+               kept.scales.data_ptr(), group_offsets.data_ptr(), _OUT_CODES[A.dtype], 1 if b_transposed else 0, G,
+               M_total, N, K, _stream_handle(stream, dev)), "grouped_gemm_swiglu_keep")
+    del keep
+    return out, kept
+
+
+class SwigluGrad(NamedTuple):
+    """Gradients of a gated block."""
+
+    dx: torch.Tensor | None   # [M, K]; None where it was not asked for
+    dw: torch.Tensor | None   # like w, or [G, *w.shape] of the experts; None likewise
+    h: torch.Tensor | None    # the block's output once more, with with_h
+
+
+def swiglu_grad(dh: torch.Tensor, kept: Int8Matrix, with_h: bool = False, stream=None):
+    """[dgate | dup] ([M, N]) from the gradient of h = silu(gate) * up and
+    [gate | up] kept in 8 bits; with ``with_h`` also h, as (dgu, h)."""
+    _half(dh, "dh")
+    M, N = _int8_check(kept, "kept", 2)
+    dev, dtype, inner = dh.device, dh.dtype, N // 2
+    if kept.device != dev or dh.shape != (M, inner):
+        raise ValueError("dh must be [%d, %d] on %s" % (M, inner, kept.device))
+    lddh = _rows(dh, "dh", M)
+    dgu = _new((M, N), dtype, dev, stream)
+    h = _new((M, inner), dtype, dev, stream) if with_h else None
+    _check(_on(dev, lib().swiglu_grad_int8, dh.data_ptr(), kept.codes.data_ptr(), kept.scales.data_ptr(),
+               dgu.data_ptr(), h.data_ptr() if with_h else None, _OUT_CODES[dtype], M, inner, lddh, N, inner,
+               _stream_handle(stream, dev)), "swiglu_grad_int8")
+    return (dgu, h) if with_h else dgu
+
+
+def _block_input(x, dh, stream) -> torch.Tensor:
+    """The block's input in dh's dtype, read back where it was kept in 8 bits."""
+    if isinstance(x, Int8Matrix):
+        return dequantize_int8(x, out_dtype=dh.dtype, stream=stream)
+    _like(x, "x", dh.dtype, dh.device)
+    return x
+
+
+def gemm_swiglu_grad(dh: torch.Tensor, x, w: torch.Tensor, kept: Int8Matrix | None = None, with_h: bool = False,
+                     b_transposed: bool = False, need_dx: bool = True, need_dw: bool = True,
+                     stream=None) -> SwigluGrad:
+    """Gradients of gemm_swiglu(x, w) from that of its output: dx [M, K] and dw
+    (like w), in dh's dtype.  x is the block's input, or the Int8Matrix it was kept
+    in.  With ``kept`` gate and up are read from 8 bits and ``with_h`` gives h too
+    (for the gradient of the weight that follows); without it they are multiplied
+    out again.  [dgate | dup] is rounded to dh's dtype on the way."""
+    _half(dh, "dh")
+    dev, dtype = dh.device, dh.dtype
+    if isinstance(x, Int8Matrix):
+        _int8_check(x, "x")
+    if x.device != dev:
+        raise ValueError("x must be on %s" % dev)
+    M, K = x.shape
+    N, ldw = _gated_weight(w, dtype, dev, K, b_transposed)
+    if dh.shape != (M, N // 2):
+        raise ValueError("dh must be [%d, %d], got %s" % (M, N // 2, tuple(dh.shape)))
+    lddh = _rows(dh, "dh", M)
+    xv = _block_input(x, dh, stream) if need_dw or kept is None else None
+    if kept is not None:
+        if kept.shape != (M, N):
+            raise ValueError("kept must be [%d, %d], got %s" % (M, N, tuple(kept.shape)))
+        dgu, h = swiglu_grad(dh, kept, True, stream) if with_h else (swiglu_grad(dh, kept, False, stream), None)
+    elif with_h:
+        raise ValueError("with_h reads h from kept")
+    else:
+        h = None
+        dgu = _new((M, N), dtype, dev, stream)
+        _check(_on(dev, lib().gemm_swiglu_grad, dh.data_ptr(), xv.data_ptr(), w.data_ptr(), dgu.data_ptr(),
+                   _OUT_CODES[dtype], 1 if b_transposed else 0, M, N, K, lddh, _rows(xv, "x", M), ldw, N,
+                   _stream_handle(stream, dev)), "gemm_swiglu_grad")
+    dx = dw = None
+    if need_dx:  # w is [K, N]: the second operand as [out, in]
+        dx = gemm(dgu, w, _new((M, K), dtype, dev, stream), stream=stream, b_transposed=not b_transposed)
+    if need_dw:
+        a, b = (dgu, xv) if b_transposed else (xv, dgu)
+        dw = gemm(a, b, out_dtype=dtype, stream=stream, a_transposed=True)
+    return SwigluGrad(dx, dw, h)
+
+
+def grouped_gemm_swiglu_grad(dh: torch.Tensor, x, ws: list, group_offsets: torch.Tensor,
+                             kept: Int8Matrix | None = None, with_h: bool = False, b_transposed: bool = False,
+                             need_dx: bool = True, need_dw: bool = True, stream=None) -> SwigluGrad:
+    """The same for the experts' blocks, grouped_gemm(x, ws, group_offsets,
+    swiglu=True): dx [rows, K] and dw [G, *w.shape]."""
+    _half(dh, "dh")
+    dev, dtype = dh.device, dh.dtype
+    if isinstance(x, Int8Matrix):
+        _int8_check(x, "x")
+    if x.device != dev:
+        raise ValueError("x must be on %s" % dev)
+    xv = _block_input(x, dh, stream) if need_dw or kept is None else None
+    M, K = x.shape
+    G = len(ws)
+    if xv is not None:
+        _, _, N, _ = _grouped_operands(xv, ws, group_offsets, b_transposed)
+    else:
+        N = (ws[0].shape[0] if b_transposed else ws[0].shape[1]) if G else 0
+    if N % 2 or dh.shape != (M, N // 2) or not dh.is_contiguous():
+        raise ValueError("dh must be dense [%d, %d], got %s" % (M, N // 2, tuple(dh.shape)))
+    if kept is not None:
+        if kept.shape != (M, N):
+            raise ValueError("kept must be [%d, %d], got %s" % (M, N, tuple(kept.shape)))
+        dgu, h = swiglu_grad(dh, kept, True, stream) if with_h else (swiglu_grad(dh, kept, False, stream), None)
+    elif with_h:
+        raise ValueError("with_h reads h from kept")
+    else:
+        h = None
+        dgu = _new((M, N), dtype, dev, stream)
+        p, keep = _ptr_array([w.data_ptr() for w in ws])
+        _check(_on(dev, lib().grouped_gemm_swiglu_grad, dh.data_ptr(), xv.data_ptr(), p, dgu.data_ptr(),
+                   group_offsets.data_ptr(), _OUT_CODES[dtype], 1 if b_transposed else 0, G, M, N, K,
+                   _stream_handle(stream, dev)), "grouped_gemm_swiglu_grad")
+        del keep
+    dx = dw = None
+    if need_dx:
+        dx = grouped_gemm(dgu, ws, group_offsets, out=_new((M, K), dtype, dev, stream), stream=stream,
+                          b_transposed=not b_transposed)
+    if need_dw:
+        a, b = (dgu, xv) if b_transposed else (xv, dgu)
+        dw = grouped_gemm_wgrad(a, b, group_offsets, stream=stream)
+    return SwigluGrad(dx, dw, h)

@@ -329,6 +329,80 @@ bwg_status grouped_gemm_fp4(const void* A, const void* A_scales, const float* A_
 const char* bwg_status_string(int status);
 
 /*
+ * The gated feed-forward block: gate = X Wg, up = X Wu, H = silu(gate) * up with
+ * silu(x) = x / (1 + e^-x), X [M, K], W = [Wg | Wu] [K, N] (N = 2 I; w_transposed:
+ * [N, K], gate's rows first), H [M, I].  Both projections, the activation and the
+ * product are one kernel; the projections do not reach memory unless they are
+ * kept.  dtype: BWG_OUT_BF16 or BWG_OUT_FP16, of X, W and H.  Accumulation,
+ * activation and product are FP32, with one rounding to dtype.
+ *   codes, scales: NULL, or both: gate and up are also kept in 8 bits, as
+ *   quantize_int8 of [gate | up] (FP32, parts = 2) would: codes int8 [M, N] dense,
+ *   16-byte aligned, scales FP32 [M, 2 ceil(I / 64)] dense.
+ * Leading dimensions in elements, multiples of 8; N a multiple of 16 and every
+ * base 16-byte aligned, else BWG_ERR_ALIGNMENT.  M, N = 0: nothing is done; K = 0
+ * writes zeros.
+ * gemm_swiglu_grad: from dH [M, I] the gradients of the projections,
+ *   dGU = [dgate | dup] [M, N], dgate = dH * up * s (1 + gate (1 - s)) with
+ *   s = 1 / (1 + e^-gate), dup = dH * silu(gate); gate and up are multiplied out
+ *   again and only dGU is written.  The gradients of X and W are the products
+ *   dGU W^T (gemm_*_nt) and X^T dGU (gemm_tn).  dGU overlaps none of the inputs.
+ * The grouped forms take expert e's rows (group_offsets as for grouped_gemm_bf16,
+ * with its contract and its report of broken ones) with W[e] (a host array of G
+ * device pointers); all matrices are dense.  Rows of no group are left as they are.
+ */
+bwg_status gemm_swiglu(const void* X, const void* W, void* H, void* codes, float* scales, int dtype, int w_transposed,
+                       int M, int N, int K, int ldx, int ldw, int ldh, void* stream);
+bwg_status gemm_swiglu_grad(const void* dH, const void* X, const void* W, void* dGU, int dtype, int w_transposed,
+                            int M, int N, int K, int lddh, int ldx, int ldw, int ldd, void* stream);
+bwg_status grouped_gemm_swiglu_keep(const void* X, const void* const* W, void* H, void* codes, float* scales,
+                                    const int* group_offsets, int dtype, int w_transposed, int G, int M_total, int N,
+                                    int K, void* stream);
+bwg_status grouped_gemm_swiglu_grad(const void* dH, const void* X, const void* const* W, void* dGU,
+                                    const int* group_offsets, int dtype, int w_transposed, int G, int M_total, int N,
+                                    int K, void* stream);
+
+/*
+ * Matrices kept in 8 bits.  Each row of a part (parts = 1: the matrix; 2: its
+ * left and right half) is cut into blocks of 64 columns, the last one shorter:
+ *   scale = a / 127, code = rint(x * (127 / a)), value = code * scale
+ * with a the block's largest magnitude, both quotients rounded to FP32 and the
+ * code rounded once, ties to even.  A block with an infinity or a NaN in it reads
+ * back as NaN; one whose a is below 2^-121 as zeros.
+ *   quantize_int8: x [M, N] of dtype (BF16, FP16 or FP32; any N that the parts
+ *     divide, any ldx >= N) into codes int8 [M, N] and scales FP32
+ *     [M, parts * ceil(N / parts / 64)], both dense.
+ *   dequantize_int8: back to y [M, N] of dtype, each value rounded once.
+ *     Columns, strides and bases on multiples of 8 elements and 16 bytes are
+ *     faster; others are taken too.
+ *   swiglu_grad_int8: gemm_swiglu_grad's dGU [M, 2 I] from dH [M, I] (dtype BF16
+ *     or FP16) and [gate | up] kept in 8 bits (parts = 2); with H not NULL also
+ *     H = silu(gate) * up [M, I].  I and the leading dimensions are multiples of
+ *     8, the bases 16-byte aligned.  The outputs overlap none of the inputs.
+ */
+bwg_status quantize_int8(const void* x, int dtype, int M, int N, int ldx, int parts, void* codes, float* scales,
+                         void* stream);
+bwg_status dequantize_int8(const void* codes, const float* scales, int parts, void* y, int dtype, int M, int N,
+                           int ldy, void* stream);
+bwg_status swiglu_grad_int8(const void* dH, const void* codes, const float* scales, void* dGU, void* H, int dtype,
+                            int M, int I, int lddh, int ldd, int ldh, void* stream);
+
+/*
+ * Products whose left operand is read transposed, the gradients of weights:
+ * gemm_tn: D [M, N] = A^T B with A [K, M] and B [K, N] of dtype (BF16 or FP16) and
+ *   D in out_dtype.  lda, ldb multiples of 8, ldd's rows of 16 bytes, bases 16-byte
+ *   aligned; M, N and K any.  K = 0 writes zeros.
+ * grouped_gemm_tn: D[g] [M, N] = A_g^T B_g over each group's rows of A [K_total, M]
+ *   and B [K_total, N] (all dense, M and N multiples of 8), D [G, M, N]; zeros for a
+ *   group without rows.  group_offsets as for grouped_gemm_bf16.
+ * FP32 results are sums of 512 rows each, joined with rounding to nearest: a sum
+ * that stays on the tensor cores loses bits towards zero at every step.
+ */
+bwg_status gemm_tn(const void* A, const void* B, void* D, int dtype, int out_dtype, int M, int N, int K, int lda,
+                   int ldb, int ldd, void* stream);
+bwg_status grouped_gemm_tn(const void* A, const void* B, void* D, const int* group_offsets, int dtype, int out_dtype,
+                           int G, int M, int N, int K_total, void* stream);
+
+/*
  * Synchronises `stream`, then reads and clears the device error word of the
  * current device.  *info receives the raw word (0 if no fault):
  *   bits 56..63 kind (1 barrier wait timed out, 2 invalid group offsets or
