@@ -78,8 +78,8 @@ EncodeTiledFn g_encode = nullptr;
 
 struct MapKey {
   const void* ptr;
-  uint64_t dims[4], strides[3];
-  uint32_t box[4];
+  uint64_t dims[5], strides[4];
+  uint32_t box[5];
   int rank, dtype, swizzle, device;
   bool operator==(const MapKey& o) const { return std::memcmp(this, &o, sizeof(MapKey)) == 0; }
 };
@@ -583,7 +583,7 @@ bwg_status ensure_device(DeviceState** out) {
   return st.init_status;
 }
 
-// Tensor map of a rank-`rank` view (2 to 4 dimensions, innermost first;
+// Tensor map of a rank-`rank` view (2 to 5 dimensions, innermost first;
 // strides in bytes for dimensions 1.., box in elements), cached by its
 // arguments.
 bool get_map_nd(CUtensorMap* m, const void* ptr, CUtensorMapDataType dtype, int rank,
@@ -609,8 +609,8 @@ bool get_map_nd(CUtensorMap* m, const void* ptr, CUtensorMapDataType dtype, int 
     *m = it->second;
     return true;
   }
-  cuuint64_t gdim[4], gstride[3];
-  cuuint32_t bx[4], estride[4] = {1, 1, 1, 1};
+  cuuint64_t gdim[5], gstride[4];
+  cuuint32_t bx[5], estride[5] = {1, 1, 1, 1, 1};
   for (int d = 0; d < rank; ++d) {
     gdim[d] = dims[d];
     bx[d] = box[d];
@@ -1123,6 +1123,82 @@ bool runtime_map(CUtensorMap* m, const void* ptr, CUtensorMapDataType dtype, int
 }
 
 bwg_status runtime_status(cudaError_t e) { return launch_status(e); }
+
+// Few rows of a gated block: the small-M kernel on tiles of 64 columns of gate and
+// the same of up.  Whole tiles, or a cluster's shares of one; no workspace, so
+// that calls on any streams and in any graphs may overlap.
+bwg_status run_small_m_gated(const void* X, const void* W, void* H, int dtype, bool w_nt, int M, int N, int K, int ldx,
+                             int ldw, int ldh, cudaStream_t stream) {
+  DeviceState* st = nullptr;
+  const bwg_status s = ensure_device(&st);
+  if (s != BWG_OK) return s;
+  const int I = N / 2, m_pad = small_m_pad(M);
+  const bool fp16 = dtype == BWG_OUT_FP16;
+  const CUtensorMapDataType t = fp16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+  SmallMParams p;
+  std::memset(&p, 0, sizeof(p));
+  p.gated = 1;
+  p.tile_n = 64;
+  p.num_tiles = ceil_div(I, 64);
+  p.num_k_blocks = ceil_div(K, kBK);
+  p.split = small_m_split(p.num_tiles, p.num_k_blocks, st->sm_count, st->clusters_small);
+  const int exchange = 4096 + 16;
+  const bool in_ring = p.split > 1 || p.num_tiles <= st->sm_count;
+  const int fixed = small_m_smem(m_pad, dtype, 0, in_ring) + exchange;
+  p.stages = std::min(8, (st->max_smem - fixed) / small_m_stage_bytes(m_pad));
+  if (p.stages < 2) return BWG_ERR_UNSUPPORTED;
+  // a CTA's partial and the rows that it receives fit in its idle ring
+  if (p.split > 1 && (static_cast<long long>(m_pad) + static_cast<long long>(p.split) * ceil_div(M, p.split)) * 512 >
+                         static_cast<long long>(p.stages) * small_m_stage_bytes(m_pad))
+    p.split = 1;
+  p.staging_in_ring = p.split > 1 || p.num_tiles <= st->sm_count ? 1 : 0;
+  const int smem = small_m_smem(m_pad, dtype, p.stages, p.staging_in_ring != 0) + exchange;
+  if (smem > st->max_smem) return BWG_ERR_UNSUPPORTED;
+  const uint64_t row = static_cast<uint64_t>(ldw) * 2, gap = static_cast<uint64_t>(I);
+  const uint64_t In = static_cast<uint64_t>(I), Kn = static_cast<uint64_t>(K), kb = Kn / 64;
+  const auto sw = CU_TENSOR_MAP_SWIZZLE_128B;
+  bool ok;
+  p.bt_boxes = w_nt || I % 64 == 0 ? 1 : 2;
+  p.pair_loads = K % 64 == 0 && p.bt_boxes == 1 ? 1 : 0;
+  if (w_nt) {
+    const uint64_t d1[3] = {Kn, In, 2}, s1[2] = {row, gap * row};
+    const uint64_t d2[4] = {64, In, 2, kb}, s2[3] = {row, gap * row, 128};
+    const uint32_t b1[3] = {64, 64, 2}, b2[4] = {64, 64, 2, 2};
+    ok = get_map_nd(&p.map_bt, W, t, 3, d1, s1, b1, sw) &&
+         (!p.pair_loads || get_map_nd(&p.map_bt2, W, t, 4, d2, s2, b2, sw));
+  } else if (p.bt_boxes == 1) {
+    const uint64_t d1[4] = {64, Kn, 2, In / 64}, s1[3] = {row, gap * 2, 128};
+    const uint64_t d2[5] = {64, 64, 2, In / 64, kb}, s2[4] = {row, gap * 2, 128, 64 * row};
+    const uint32_t b1[4] = {64, 64, 2, 1}, b2[5] = {64, 64, 2, 1, 2};
+    ok = get_map_nd(&p.map_bt, W, t, 4, d1, s1, b1, sw) &&
+         (!p.pair_loads || get_map_nd(&p.map_bt2, W, t, 5, d2, s2, b2, sw));
+  } else {
+    ok = get_map(&p.map_bt, W, t, N, Kn, row, 64, 64, sw);
+  }
+  if (ok && p.pair_loads) {
+    const uint64_t d[3] = {64, static_cast<uint64_t>(M), kb}, s3[2] = {static_cast<uint64_t>(ldx) * 2, 128};
+    const uint32_t b[3] = {64, static_cast<uint32_t>(m_pad), 2};
+    ok = get_map_nd(&p.map_at2, X, t, 3, d, s3, b, sw);
+  }
+  if (!ok || !get_map(&p.map_at, X, t, K, M, static_cast<uint64_t>(ldx) * 2, kBK, m_pad, sw) ||
+      !get_map(&p.map_d, H, t, I, M, static_cast<uint64_t>(ldh) * 2, 64, m_pad, CU_TENSOR_MAP_SWIZZLE_NONE))
+    return BWG_ERR_CUDA;
+  p.err = st->err;
+  p.timeout_ns = g_timeout_ns.load();
+  p.M = M;
+  p.N = I;
+  p.K = K;
+  p.m_pad = m_pad;
+  p.out_dtype = dtype;
+  p.idesc = make_idesc_f16(fp16 ? kFmtF16 : kFmtBF16, !w_nt, false, 128, m_pad);
+  p.tx_extra = g_tx_extra.load();
+  p.b_kmajor = w_nt ? 1 : 0;
+  p.l2hint = p.split > 1 ? 0 : 2;  // as in gemm_bf16
+  p.d = H;
+  p.ldd = ldh;
+  const int grid = p.split > 1 ? p.num_tiles * p.split : std::min(p.num_tiles, st->sm_count);
+  return launch_status(launch_small_m(p, grid, static_cast<size_t>(smem), stream));
+}
 
 }  // namespace bwg
 

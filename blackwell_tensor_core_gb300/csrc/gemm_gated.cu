@@ -235,6 +235,9 @@ bwg_status run_gated(const GatedCall& c, cudaStream_t stream) {
     }
     return runtime_status(e);
   }
+  // few rows: W streams through once, as in gemm_bf16
+  if (c.offsets == nullptr && c.epi == kEpiSwiglu && c.M <= kSmallMMaxM)
+    return run_small_m_gated(c.x, c.w[0], c.d, c.dtype, c.w_nt != 0, c.M, c.N, c.K, c.ldx, c.ldw, c.ldd, stream);
   return c.offsets == nullptr ? run_gated_dense(c, rt, stream) : run_gated_grouped(c, rt, stream);
 }
 

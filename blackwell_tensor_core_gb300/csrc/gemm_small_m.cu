@@ -49,9 +49,16 @@
 // in rank order and stores them.  The partials never leave the chip and no workspace is needed; CTAs
 // of one cluster are co-scheduled, so waiting for one another is safe (the
 // waits are bounded all the same).
+//
+// Gated (SW): W = [gate | up], a tile's 128 channels are 64 columns of gate and
+// the same 64 of up (loaded as one box: the step from gate to up is a dimension
+// of the maps), and silu(gate) * up is stored.  Threads of up's columns hand
+// their sums to those of gate's through shared memory, 16 rows at a time; in the
+// cluster split every thread sums gate and up of its rows itself.
 #include "layout.h"
 #include "params.h"
 #include "ptx.cuh"
+#include "swiglu.cuh"
 
 namespace bwg {
 namespace {
@@ -116,6 +123,7 @@ struct Segments {
   }
 };
 
+template <bool SW>
 __global__ void __launch_bounds__(kThreads, 1) small_m_kernel(const __grid_constant__ SmallMParams p) {
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
@@ -145,6 +153,7 @@ __global__ void __launch_bounds__(kThreads, 1) small_m_kernel(const __grid_const
   const uint32_t last_flag = tmem_slot + 4u;  // "this CTA finishes the tile" broadcast
   const uint32_t ready_bar = tmem_slot + 8u;   // split: every CTA of the cluster has its partial
   const uint32_t recv_bar = tmem_slot + 16u;   // split: the other CTAs' rows have landed here
+  const uint32_t exch = (recv_bar + 23u) & ~15u;  // gated: up's sums of 16 rows, [16][64] FP32
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < S; ++s) {
@@ -222,7 +231,11 @@ __global__ void __launch_bounds__(kThreads, 1) small_m_kernel(const __grid_const
         const uint32_t sat = smem_at + s * at_stage_bytes;
         if (pair) {
           mbar_arrive_expect_tx(full, 2u * (tx - p.tx_extra) + p.tx_extra);
-          if (p.b_kmajor)
+          if (SW && p.b_kmajor)
+            tma_load_4d_hint(sbt, &p.map_bt2, full, 0, n0, 0, kb, pol_b);
+          else if (SW)
+            tma_load_5d_hint(sbt, &p.map_bt2, full, 0, 0, 0, n0 >> 6, kb, pol_b);
+          else if (p.b_kmajor)
             tma_load_3d_hint(sbt, &p.map_bt2, full, 0, n0, kb, pol_b);
           else
             tma_load_4d_hint(sbt, &p.map_bt2, full, 0, 0, n0 >> 6, kb, pol_b);
@@ -240,7 +253,14 @@ __global__ void __launch_bounds__(kThreads, 1) small_m_kernel(const __grid_const
         // B^T's 128 channels x 64 K: row-major B [K, N] is addressed
         // (channel, k) or (channel in group, k, group), B stored as [N, K]
         // (k, channel)
-        if (p.b_kmajor) {
+        if (SW && p.b_kmajor) {
+          tma_load_3d_hint(sbt, &p.map_bt, full, k0, n0, 0, pol_b);
+        } else if (SW && p.bt_boxes == 1) {
+          tma_load_4d_hint(sbt, &p.map_bt, full, 0, k0, 0, n0 >> 6, pol_b);
+        } else if (SW) {
+          tma_load_2d_hint(sbt, &p.map_bt, full, n0, k0, pol_b);
+          tma_load_2d_hint(sbt + kBtChunkBytes, &p.map_bt, full, p.N + n0, k0, pol_b);
+        } else if (p.b_kmajor) {
           tma_load_2d_hint(sbt, &p.map_bt, full, k0, n0, pol_b);
         } else if (p.bt_boxes == 1) {
           tma_load_3d_hint(sbt, &p.map_bt, full, 0, k0, n0 >> 6, pol_b);
@@ -374,7 +394,22 @@ __global__ void __launch_bounds__(kThreads, 1) small_m_kernel(const __grid_const
     // body that the row loops below reuse.
     const uint32_t row_bytes = pitch * static_cast<uint32_t>(out_elt);
     const uint32_t col_addr = smem_d + half * half_bytes + col_in_half * static_cast<uint32_t>(out_elt);
-    auto stage16 = [&](int r0, const uint32_t (&v)[16]) {
+    auto stage16 = [&](int r0, uint32_t (&v)[16]) {
+      if constexpr (SW) {
+        // all 128 threads: up's hand their sums over, gate's take them
+        const uint32_t at = exch + col_in_half * 4u;
+        if (half == 1) {
+#pragma unroll
+          for (int r = 0; r < 16; ++r) st_shared_u32(at + r * 256u, v[r]);
+        }
+        named_bar_sync(1, 128);
+        if (half == 0) {
+#pragma unroll
+          for (int r = 0; r < 16; ++r)
+            v[r] = __float_as_uint(swiglu_f32(__uint_as_float(v[r]), __uint_as_float(ld_shared_u32(at + r * 256u))));
+        }
+        named_bar_sync(1, 128);  // read before the next rows are written
+      }
       if (!stores) return;
       const int n = min(16, p.M - r0);
       const uint32_t a = col_addr + static_cast<uint32_t>(r0) * row_bytes;
@@ -476,8 +511,40 @@ __global__ void __launch_bounds__(kThreads, 1) small_m_kernel(const __grid_const
         // 5. Sum the partials in rank order (this CTA's own from its local
         //    copy) and store this CTA's rows of D, four rows at a time so the
         //    shared-memory loads of a row group are independent.
-        const int col = n0 + static_cast<int>(ch);
-        if (stores && col < p.N) {
+        const int col = n0 + static_cast<int>(SW ? col_in_half : ch);
+        if constexpr (SW) {
+          // every second row a thread, gate and up of its column
+          if (col < p.N) {
+            const int r0 = static_cast<int>(me) * rpc;
+            const float* own = reinterpret_cast<const float*>(smem_raw + (base - smem_u32(smem_raw))) +
+                               static_cast<size_t>(r0) * 128u + col_in_half;
+            const float* slots = reinterpret_cast<const float*>(smem_raw + (recv - smem_u32(smem_raw))) + col_in_half;
+#pragma unroll 1
+            for (int r = static_cast<int>(half); r < my_rows; r += 4) {
+              float g[2] = {0.f, 0.f}, u[2] = {0.f, 0.f};
+#pragma unroll 1
+              for (int src = 0; src < F; ++src) {
+                const float* q4 = (src == static_cast<int>(me) ? own : slots + static_cast<size_t>(src) * rpc * 128u) +
+                                  static_cast<size_t>(r) * 128u;
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                  if (r + 2 * j < my_rows) {
+                    g[j] += q4[j * 256];
+                    u[j] += q4[j * 256 + 64];
+                  }
+                }
+              }
+#pragma unroll
+              for (int j = 0; j < 2; ++j) {
+                if (r + 2 * j < my_rows) {
+                  const float y = swiglu_f32(g[j], u[j]);
+                  static_cast<uint16_t*>(p.d)[static_cast<size_t>(r0 + r + 2 * j) * p.ldd + col] =
+                      outbf ? cvt_rn_bf16(y) : cvt_rn_f16(y);
+                }
+              }
+            }
+          }
+        } else if (stores && col < p.N) {
           const int r0 = static_cast<int>(me) * rpc;
           const float* own = reinterpret_cast<const float*>(smem_raw + (base - smem_u32(smem_raw))) +
                              static_cast<size_t>(r0) * 128u + ch;
@@ -636,8 +703,12 @@ __global__ void zero_fill_kernel(uint8_t* d, int rows, int row_bytes, size_t ld_
 }  // namespace
 
 cudaError_t launch_small_m(const SmallMParams& p, int grid, size_t smem, cudaStream_t s) {
+  const bool gated = p.gated != 0;
   if (p.split <= 1) {
-    small_m_kernel<<<grid, kThreads, smem, s>>>(p);
+    if (gated)
+      small_m_kernel<true><<<grid, kThreads, smem, s>>>(p);
+    else
+      small_m_kernel<false><<<grid, kThreads, smem, s>>>(p);
     return cudaGetLastError();
   }
   cudaLaunchConfig_t cfg = {};
@@ -652,7 +723,7 @@ cudaError_t launch_small_m(const SmallMParams& p, int grid, size_t smem, cudaStr
   attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, small_m_kernel, p);
+  return gated ? cudaLaunchKernelEx(&cfg, small_m_kernel<true>, p) : cudaLaunchKernelEx(&cfg, small_m_kernel<false>, p);
 }
 
 int max_active_clusters_small_m(int cluster, size_t smem) {
@@ -668,7 +739,7 @@ int max_active_clusters_small_m(int cluster, size_t smem) {
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   int n = 0;
-  if (cudaOccupancyMaxActiveClusters(&n, reinterpret_cast<const void*>(small_m_kernel), &cfg) !=
+  if (cudaOccupancyMaxActiveClusters(&n, reinterpret_cast<const void*>(small_m_kernel<false>), &cfg) !=
       cudaSuccess) {
     cudaGetLastError();
     return 0;
@@ -687,7 +758,7 @@ cudaError_t launch_zero_fill(void* d, int rows, int cols, int ld, int elt_bytes,
 
 int max_active_ctas_small_m(size_t smem) {
   int n = 0;
-  if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, small_m_kernel, kThreads, smem) !=
+  if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, small_m_kernel<false>, kThreads, smem) !=
       cudaSuccess) {
     cudaGetLastError();
     return 0;
@@ -696,7 +767,10 @@ int max_active_ctas_small_m(size_t smem) {
 }
 
 cudaError_t set_small_m_attributes(size_t smem) {
-  return cudaFuncSetAttribute(small_m_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+  const cudaError_t e = cudaFuncSetAttribute(small_m_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                             static_cast<int>(smem));
+  if (e != cudaSuccess) return e;
+  return cudaFuncSetAttribute(small_m_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                               static_cast<int>(smem));
 }
 

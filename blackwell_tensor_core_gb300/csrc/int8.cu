@@ -28,6 +28,8 @@ namespace {
 
 constexpr int kThreadsInt8 = 256;
 constexpr int kRowsPerWarp = 4;   // rows in flight a lane
+constexpr int kOddRows = 2;       // the same where nothing is aligned
+constexpr int kOddCols = 256;     // and the columns that a warp takes
 
 struct Int8Params {
   const void* x;        // quantise: the matrix; SwiGLU gradient: H's gradient
@@ -41,6 +43,7 @@ struct Int8Params {
   int blocks;           // blocks of a part
   int part_bits;        // 0 or 1: log2 of the parts
   int segs;             // column segments of a part's row
+  int wide;             // 16-bit matrix: 16 columns start on 32 bytes wherever a lane's do
 };
 
 template <int IN>
@@ -62,6 +65,18 @@ __device__ __forceinline__ Elem<OUT> from_float(float v) {
     return v;
   else
     return static_cast<uint16_t>(OUT == kOutBF16 ? cvt_rn_bf16(v) : cvt_rn_f16(v));
+}
+
+// 32 bytes at once (sm_100 on), 32-byte aligned.
+__device__ __forceinline__ void load32(const void* p, uint32_t (&w)[8]) {
+  asm("ld.global.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+      : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]), "=r"(w[4]), "=r"(w[5]), "=r"(w[6]), "=r"(w[7])
+      : "l"(p));
+}
+__device__ __forceinline__ void store32(void* p, const uint32_t (&w)[8]) {
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(w[0]), "r"(w[1]), "r"(w[2]),
+               "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+               : "memory");
 }
 
 // 8 values from 16-byte aligned memory.
@@ -119,6 +134,13 @@ __global__ void __launch_bounds__(kThreadsInt8) quantize_int8_kernel(const Int8P
   for (int r = 0; r < kRowsPerWarp; ++r) {
     const long long row = row0 + r * kR;
     const Elem<IN>* src = static_cast<const Elem<IN>*>(p.x) + part_row(p, row, p.ldx) + col;
+    if (IN != kOutF32 && p.wide) {
+      uint32_t w[8] = {0u, 0u, 0u, 0u, 0u, 0u, 0u, 0u};
+      if (row < p.rows && col < p.cols) load32(src, w);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) unpack_pair(w[i], IN == kOutBF16, &v[r][2 * i], &v[r][2 * i + 1]);
+      continue;
+    }
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       float t[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
@@ -159,28 +181,46 @@ __global__ void __launch_bounds__(kThreadsInt8) quantize_int8_kernel(const Int8P
   }
 }
 
-// Any width and stride: a warp takes a block, two columns a lane.
+// Any width and stride: a warp takes four blocks of a row, two columns of each a
+// lane, so that neighbouring lanes read neighbouring elements.
 template <int IN>
 __global__ void __launch_bounds__(kThreadsInt8) quantize_int8_odd_kernel(const Int8Params p) {
   const int lane = static_cast<int>(threadIdx.x & 31u);
-  const long long total = p.rows * p.blocks;
-  const long long step = static_cast<long long>(gridDim.x) * (kThreadsInt8 / 32);
-  for (long long t = static_cast<long long>(blockIdx.x) * (kThreadsInt8 / 32) + (threadIdx.x >> 5); t < total;
-       t += step) {
-    const long long row = t / p.blocks;
-    const int c0 = static_cast<int>(t - row * p.blocks) * kInt8Block + lane;
-    const Elem<IN>* src = static_cast<const Elem<IN>*>(p.x) + part_row(p, row, p.ldx) + c0;
-    const float v0 = c0 < p.cols ? to_float<IN>(src[0]) : 0.f;
-    const float v1 = c0 + 32 < p.cols ? to_float<IN>(src[32]) : 0.f;
-    float a = max_abs_nan(v0, v1);
+  const long long rb = blockIdx.x / p.segs;
+  const int seg = static_cast<int>(blockIdx.x - rb * p.segs);
+  const int col = seg * kOddCols + lane;
+  const long long row0 = (rb * (kThreadsInt8 / 32) + (threadIdx.x >> 5)) * kOddRows;
+  float v[kOddRows][8];
 #pragma unroll
-    for (int d = 1; d < 32; d <<= 1) a = max_abs_nan(a, __shfl_xor_sync(0xffffffffu, a, d));
+  for (int r = 0; r < kOddRows; ++r) {
+    const Elem<IN>* src = static_cast<const Elem<IN>*>(p.x) + part_row(p, row0 + r, p.ldx) + col;
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      v[r][i] = row0 + r < p.rows && col + 32 * i < p.cols ? to_float<IN>(src[32 * i]) : 0.f;
+  }
+#pragma unroll
+  for (int r = 0; r < kOddRows; ++r) {
+    if (row0 + r >= p.rows) break;  // the whole warp
+    float a[4];
+#pragma unroll
+    for (int b = 0; b < 4; ++b) a[b] = max_abs_nan(v[r][2 * b], v[r][2 * b + 1]);
+    // lanes 8 b .. 8 b + 7 come to hold block b's maximum
+    const bool hi = (lane & 16) != 0, mid = (lane & 8) != 0;
+    float m0 = max_abs_nan(hi ? a[2] : a[0], __shfl_xor_sync(0xffffffffu, hi ? a[0] : a[2], 16));
+    const float m1 = max_abs_nan(hi ? a[3] : a[1], __shfl_xor_sync(0xffffffffu, hi ? a[1] : a[3], 16));
+    m0 = max_abs_nan(mid ? m1 : m0, __shfl_xor_sync(0xffffffffu, mid ? m0 : m1, 8));
+#pragma unroll
+    for (int d = 4; d > 0; d >>= 1) m0 = max_abs_nan(m0, __shfl_xor_sync(0xffffffffu, m0, d));
     float scale, inv;
-    int8_scale(a, &scale, &inv);
-    int8_t* dst = p.codes + row * p.cols + c0;
-    if (c0 < p.cols) dst[0] = static_cast<int8_t>(int8_code(v0, inv) & 0xFFu);
-    if (c0 + 32 < p.cols) dst[32] = static_cast<int8_t>(int8_code(v1, inv) & 0xFFu);
-    if (lane == 0) p.scales[t] = scale;
+    int8_scale(m0, &scale, &inv);
+    const int block = seg * (kOddCols / kInt8Block) + (lane >> 3);
+    if ((lane & 7) == 0 && block < p.blocks) p.scales[(row0 + r) * p.blocks + block] = scale;
+    int8_t* dst = p.codes + (row0 + r) * p.cols + col;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const float f = __shfl_sync(0xffffffffu, inv, (i >> 1) * 8);
+      if (col + 32 * i < p.cols) dst[32 * i] = static_cast<int8_t>(int8_code(v[r][i], f) & 0xFFu);
+    }
   }
 }
 
@@ -217,6 +257,20 @@ __global__ void __launch_bounds__(kThreadsInt8) dequantize_int8_kernel(const Int
   for (int r = 0; r < kRowsPerWarp; ++r) {
     const long long row = row0 + r * kR;
     Elem<OUT>* dst = static_cast<Elem<OUT>*>(p.y) + part_row(p, row, p.ldy) + col;
+    if (OUT != kOutF32 && p.wide) {
+      uint32_t o[8];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        float v[4];
+        codes4(w[r][i], v);
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+          o[2 * i + j] = OUT == kOutBF16 ? pack_bf16x2(v[2 * j] * scale[r], v[2 * j + 1] * scale[r])
+                                         : pack_f16x2(v[2 * j] * scale[r], v[2 * j + 1] * scale[r]);
+      }
+      if (row < p.rows && col < p.cols) store32(dst, o);
+      continue;
+    }
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       if (row < p.rows && col + 8 * h < p.cols) {
@@ -234,17 +288,29 @@ __global__ void __launch_bounds__(kThreadsInt8) dequantize_int8_kernel(const Int
 template <int OUT>
 __global__ void __launch_bounds__(kThreadsInt8) dequantize_int8_odd_kernel(const Int8Params p) {
   const int lane = static_cast<int>(threadIdx.x & 31u);
-  const long long total = p.rows * p.blocks;
-  const long long step = static_cast<long long>(gridDim.x) * (kThreadsInt8 / 32);
-  for (long long t = static_cast<long long>(blockIdx.x) * (kThreadsInt8 / 32) + (threadIdx.x >> 5); t < total;
-       t += step) {
-    const long long row = t / p.blocks;
-    const int c0 = static_cast<int>(t - row * p.blocks) * kInt8Block + lane;
-    const float scale = p.scales[t];
-    const int8_t* src = p.codes + row * p.cols + c0;
-    Elem<OUT>* dst = static_cast<Elem<OUT>*>(p.y) + part_row(p, row, p.ldy) + c0;
-    if (c0 < p.cols) dst[0] = from_float<OUT>(static_cast<float>(src[0]) * scale);
-    if (c0 + 32 < p.cols) dst[32] = from_float<OUT>(static_cast<float>(src[32]) * scale);
+  const long long rb = blockIdx.x / p.segs;
+  const int seg = static_cast<int>(blockIdx.x - rb * p.segs);
+  const int col = seg * kOddCols + lane, block = seg * (kOddCols / kInt8Block);
+  const long long row0 = (rb * (kThreadsInt8 / 32) + (threadIdx.x >> 5)) * kOddRows;
+  int8_t c[kOddRows][8];
+  float scale[kOddRows][4];
+#pragma unroll
+  for (int r = 0; r < kOddRows; ++r) {
+    const int8_t* src = p.codes + (row0 + r) * p.cols + col;
+    const float* sc = p.scales + (row0 + r) * p.blocks + block;
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (row0 + r < p.rows && col + 32 * i < p.cols) c[r][i] = src[32 * i];
+#pragma unroll
+    for (int b = 0; b < 4; ++b) scale[r][b] = row0 + r < p.rows && block + b < p.blocks ? sc[b] : 0.f;
+  }
+#pragma unroll
+  for (int r = 0; r < kOddRows; ++r) {
+    Elem<OUT>* dst = static_cast<Elem<OUT>*>(p.y) + part_row(p, row0 + r, p.ldy) + col;
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (row0 + r < p.rows && col + 32 * i < p.cols)
+        dst[32 * i] = from_float<OUT>(static_cast<float>(c[r][i]) * scale[r][i >> 1]);
   }
 }
 
@@ -334,15 +400,15 @@ bool launch_rows(Int8Params p, bool back, cudaStream_t s) {
 }
 
 template <int T>
-bool launch_type(const Int8Params& p, bool back, bool vec, int sm_count, cudaStream_t s) {
+bool launch_type(const Int8Params& p, bool back, bool vec, cudaStream_t s) {
   if (!vec) {
-    const long long warps = p.rows * p.blocks;
-    const unsigned grid = static_cast<unsigned>(
-        std::min<long long>((warps + kThreadsInt8 / 32 - 1) / (kThreadsInt8 / 32), 64LL * sm_count));
+    Int8Params q = p;
+    const unsigned grid = row_grid(&q, kOddCols, kOddRows);
+    if (grid == 0) return false;
     if (back)
-      dequantize_int8_odd_kernel<T><<<grid, kThreadsInt8, 0, s>>>(p);
+      dequantize_int8_odd_kernel<T><<<grid, kThreadsInt8, 0, s>>>(q);
     else
-      quantize_int8_odd_kernel<T><<<grid, kThreadsInt8, 0, s>>>(p);
+      quantize_int8_odd_kernel<T><<<grid, kThreadsInt8, 0, s>>>(q);
     return true;
   }
   switch (row_lanes(p.cols)) {
@@ -375,9 +441,10 @@ bwg_status run_int8(bool back, const void* m, int dtype, int M, int N, int ld, i
   p.part_bits = parts - 1;
   const bool vec = p.cols % 8 == 0 && is_aligned(m, 16) && is_aligned(codes, 16) &&
                    static_cast<long long>(ld) * elt_bytes(dtype) % 16 == 0;
-  const bool ok = dtype == kOutBF16  ? launch_type<kOutBF16>(p, back, vec, rt.sm_count, stream)
-                  : dtype == kOutF16 ? launch_type<kOutF16>(p, back, vec, rt.sm_count, stream)
-                                     : launch_type<kOutF32>(p, back, vec, rt.sm_count, stream);
+  p.wide = p.cols % 16 == 0 && is_aligned(m, 32) && ld % 16 == 0 ? 1 : 0;
+  const bool ok = dtype == kOutBF16  ? launch_type<kOutBF16>(p, back, vec, stream)
+                  : dtype == kOutF16 ? launch_type<kOutF16>(p, back, vec, stream)
+                                     : launch_type<kOutF32>(p, back, vec, stream);
   return ok ? runtime_status(cudaGetLastError()) : BWG_ERR_UNSUPPORTED;
 }
 

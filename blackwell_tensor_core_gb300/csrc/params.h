@@ -169,6 +169,12 @@ struct SmallMParams {
                         // k-blocks of the segment remain
   int l2hint;           // L2 policies: bit 1 loads B^T evict-first (the default), bit 0
                         // loads A evict-last; evict-normal where a bit is clear
+  int gated;            // 1: B = [gate | up], D = silu(gate) * up [M, N], tile_n = 64.  Maps
+                        // of B: 2-D {2N, K}, box {64, 64} (bt_boxes 2); else, with gate and
+                        // up as a dimension: {64, K, 2, N/64}, box {64, 64, 2, 1}, two stages
+                        // {64, 64, 2, N/64, K/64}, box {64, 64, 2, 1, 2}; stored [2N, K]:
+                        // {K, N, 2}, box {64, 64, 2}, two stages {64, N, 2, K/64}, box
+                        // {64, 64, 2, 2}
   void* d;            // D (split mode stores its rows directly)
   long long ldd;      // D's leading dimension, elements
   // Optional trace (nullptr: off): per CTA eight global-timer stamps (ns),

@@ -329,6 +329,15 @@ BWG_DEV void tma_load_4d_hint(uint32_t dst, const CUtensorMap* map, uint32_t bar
       : "memory");
 }
 
+BWG_DEV void tma_load_5d_hint(uint32_t dst, const CUtensorMap* map, uint32_t bar, int32_t c0, int32_t c1,
+                              int32_t c2, int32_t c3, int32_t c4, uint64_t pol) {
+  asm volatile(
+      "cp.async.bulk.tensor.5d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.L2::cache_hint"
+      " [%0], [%1, {%3, %4, %5, %6, %7}], [%2], %8;" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(c4), "l"(pol)
+      : "memory");
+}
+
 // Same, for a CTA pair: the completing barrier may live in the peer CTA
 // (`bar` is a shared::cluster address, e.g. from mapa_shared).
 BWG_DEV void tma_load_2d_pair(uint32_t dst, const CUtensorMap* map, uint32_t bar, int32_t c0,

@@ -43,6 +43,10 @@ inline bool runtime_map_2d(CUtensorMap* m, const void* ptr, CUtensorMapDataType 
 
 inline bool is_aligned(const void* p, uintptr_t bytes) { return (reinterpret_cast<uintptr_t>(p) & (bytes - 1)) == 0; }
 
+// H = silu(X gate) * (X up) of at most kSmallMMaxM rows, arguments checked (see gemm_swiglu).
+bwg_status run_small_m_gated(const void* X, const void* W, void* H, int dtype, bool w_nt, int M, int N, int K, int ldx,
+                             int ldw, int ldh, cudaStream_t stream);
+
 // BWG_OK, or BWG_ERR_CUDA with the runtime's error state cleared.
 bwg_status runtime_status(cudaError_t e);
 
