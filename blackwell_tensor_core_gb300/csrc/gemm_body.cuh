@@ -347,11 +347,15 @@ template <int CG, int MC, bool GROUPED, int NC, int EPI, bool DYN, bool TN = fal
 __device__ void gemm_body(const PT& P, const GemmParams& p) {
   constexpr bool SW = EPI != kEpiPlain;
   static_assert(!SW || (CG == 2 && MC == 1), "SwiGLU runs on the pair kernels");
-  static_assert(!DYN || (CG == 2 && MC == 1 && (NC == 2 || CH)), "dynamic scheduling: 12-warp pairs");
+  static_assert(!DYN || (CG == 2 && MC == 1 && (NC == 2 || CH || EPI >= kEpiSwigluKeep)), "dynamic scheduling: 12-warp pairs");
   static_assert(!TN || (CG == 2 && MC == 1 && !SW && !GROUPED), "transposed A runs on plain pairs");
   static_assert(!CH || (TN && NC == 1), "sums in registers: one consumer, transposed A");
   constexpr bool kTables = GROUPED || TN;              // row ranges of groups in shared memory
-  constexpr bool kWide = NC == 2 || CH;                // two epilogue warpgroups
+  // two epilogue warpgroups: one a consumer, or (kHalves) one for each half of
+  // the columns of a single consumer's tile
+  constexpr bool kHalves = CH || EPI >= kEpiSwigluKeep;
+  constexpr bool kWide = NC == 2 || kHalves;
+  static_assert(!kHalves || NC == 1, "halves of the columns: one consumer");
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
   const uint32_t warp = threadIdx.x >> 5;
@@ -396,7 +400,7 @@ __device__ void gemm_body(const PT& P, const GemmParams& p) {
     }
     for (int a = 0; a < 2; ++a) {
       mbar_init(acc_full_bar(a), 1);
-      mbar_init(acc_empty_bar(a), CG * (CH ? 8 : 4));
+      mbar_init(acc_empty_bar(a), CG * (kHalves ? 8 : 4));
     }
     if constexpr (DYN) {
       for (uint32_t s = 0; s < kClcSlots; ++s) {
@@ -567,12 +571,21 @@ __device__ void gemm_body(const PT& P, const GemmParams& p) {
             for (int c = 0; c < NC; ++c) {
               if ((tl.cmask >> c) & 1) {
                 const int col = a_row + c * 2 * kRowsPerCta;  // columns of A: rows of D
-                tma_load_3d_pair(sa + c * kAStageBytes, &p.map_a, fb, col, w0, wr);
-                tma_load_3d_pair(sa + c * kAStageBytes + kAStageBytes / 2, &p.map_a, fb, col + 64, w0, wr);
+                const uint32_t dst = sa + c * kAStageBytes;
+                if (p.a_one_box) {
+                  tma_load_4d_pair(dst, &p.map_a, fb, 0, w0, wr, col / 64);
+                } else {
+                  tma_load_3d_pair(dst, &p.map_a, fb, col, w0, wr);
+                  tma_load_3d_pair(dst + kAStageBytes / 2, &p.map_a, fb, col + 64, w0, wr);
+                }
               }
             }
-            for (uint32_t j = 0; j < b_chunks; ++j)
-              tma_load_3d_pair(sb + j * kBChunkBytes, mb, fb, b_col + 64 * static_cast<int>(j), w0, wr);
+            if (p.b_one_box && b_chunks == 2) {
+              tma_load_4d_pair(sb, &p.map_b1, fb, 0, w0, wr, b_col / 64);
+            } else {
+              for (uint32_t j = 0; j < b_chunks; ++j)
+                tma_load_3d_pair(sb + j * kBChunkBytes, mb, fb, b_col + 64 * static_cast<int>(j), w0, wr);
+            }
           } else if constexpr (CG == 2) {
             if (rank == 0) mbar_arrive_expect_tx(full_bar(s), stage_tx);
             const uint32_t fb = mapa_shared(full_bar(s), leader);
@@ -748,7 +761,7 @@ __device__ void gemm_body(const PT& P, const GemmParams& p) {
     // ---- epilogue: TMEM -> registers -> convert -> swizzled SMEM -> TMA -----
     const uint32_t q = warp & 3u;  // TMEM lane quarter this warp may read
     const int cons = NC == 1 ? 0 : static_cast<int>((warp - kEpiWarp0) >> 2);  // accumulator owner
-    const int wg = CH ? static_cast<int>((warp - kEpiWarp0) >> 2) : 0;  // its half of the columns (CH)
+    const int wg = kHalves ? static_cast<int>((warp - kEpiWarp0) >> 2) : 0;  // its half of the columns
     const uint32_t ebuf = smem_epi + (warp - kEpiWarp0) * kEpiBufs * kEpiBufBytes;
     const uint32_t acc_empty_leader0 =
         (CG == 2) ? mapa_shared(acc_empty_bar(0), leader) : acc_empty_bar(0);
@@ -881,18 +894,16 @@ __device__ void gemm_body(const PT& P, const GemmParams& p) {
         }
         continue;
       }
-      // This lane's row of H's gradient (128 columns of a whole unit), read
-      // while the accumulator is still being filled.
-      uint4 dh[EPI == kEpiSwigluGrad ? 16 : 1];
+      // This lane's row of H's gradient (this warp's 64 columns), read while the
+      // accumulator is still being filled.
+      uint4 dh[EPI == kEpiSwigluGrad ? 8 : 1];
       if constexpr (EPI == kEpiSwigluGrad) {
-        const int row = row_w + static_cast<int>(lane);
+        const int row = row_w + static_cast<int>(lane), col = tl.n0 + wg * 64;
         const uint4* src = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(P.x.dh) +
-                                                          static_cast<size_t>(row) * P.x.ld_dh + tl.n0);
+                                                          static_cast<size_t>(row) * P.x.ld_dh + col);
+        const bool mine = row < tl.row_end && wg * 128 < tl.width;
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          const bool in = row < tl.row_end && i * 16 < tl.width && tl.n0 + i * 8 < p.N;
-          dh[i] = in ? src[i] : make_uint4(0u, 0u, 0u, 0u);
-        }
+        for (int i = 0; i < 8; ++i) dh[i] = mine && col + i * 8 < p.N ? src[i] : make_uint4(0u, 0u, 0u, 0u);
       }
       if (!warp_wait(acc_full_bar(acc), acc_ph, p.timeout_ns)) {
         if (lane == 0) record_fault(p.err, kFaultTimeout, kRoleEpilogue, kBarAccFull, acc, acc_ph);
@@ -1017,72 +1028,54 @@ __device__ void gemm_body(const PT& P, const GemmParams& p) {
       // first (packed to 16 bits: 128 registers), releases the accumulator,
       // and only then stages and stores it, while the next tile's MMAs run.
       const bool early = EPI >= kEpiSwigluKeep || (NC == 2 && !out32 && fix == nullptr && store_slice);
-      if constexpr (EPI == kEpiSwigluKeep) {
-        // H as below; gate and up, block by block of 64 columns, to 8 bits.
-        // The accumulator goes back once its last columns are in registers.
-        uint32_t hk[2][32];
-        const int row = row_w + static_cast<int>(lane);
-        const bool in = row < tl.row_end;
-        uint8_t* const code_row = P.x.codes + static_cast<size_t>(row) * 2u * static_cast<uint32_t>(p.N);
-        float* const scale_row = P.x.scales + static_cast<size_t>(row) * 2u * P.x.blocks;
+      if constexpr (EPI >= kEpiSwigluKeep) {
+        // This warp's 32 rows x 64 columns of gate and of up, out of TMEM at once;
+        // a unit of half width has columns for the first warpgroup only.
+        const int c0 = wg * 64, col = tl.n0 + c0;
+        uint32_t g[64], u[64];
+        if (c0 < out_cols) {
 #pragma unroll
-        for (int sub = 0; sub < 2; ++sub) {
-          if (sub < nsub) {
-            uint32_t g[64], u[64];
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              tmem_ld_32x32b_x32(t_acc + sub * 64 + h * 32, reinterpret_cast<uint32_t (&)[32]>(g[h * 32]));
-              tmem_ld_32x32b_x32(t_acc + out_cols + sub * 64 + h * 32, reinterpret_cast<uint32_t (&)[32]>(u[h * 32]));
-            }
-            tmem_wait_ld();
-            if (sub == nsub - 1) release_acc();
+          for (int h = 0; h < 2; ++h) {
+            tmem_ld_32x32b_x32(t_acc + c0 + h * 32, reinterpret_cast<uint32_t (&)[32]>(g[h * 32]));
+            tmem_ld_32x32b_x32(t_acc + out_cols + c0 + h * 32, reinterpret_cast<uint32_t (&)[32]>(u[h * 32]));
+          }
+          tmem_wait_ld();
+        }
+        release_acc();
+        if (c0 < out_cols && col < p.N) {
+          uint32_t pk[32];
+          if constexpr (EPI == kEpiSwigluKeep) {
+            // H, and gate and up of this row put into 8 bits, a block each
 #pragma unroll
             for (int i = 0; i < 32; ++i) {
               const float y0 = swiglu_f32(__uint_as_float(g[2 * i]), __uint_as_float(u[2 * i]));
               const float y1 = swiglu_f32(__uint_as_float(g[2 * i + 1]), __uint_as_float(u[2 * i + 1]));
-              hk[sub][i] = outbf ? pack_bf16x2(y0, y1) : pack_f16x2(y0, y1);
+              pk[i] = outbf ? pack_bf16x2(y0, y1) : pack_f16x2(y0, y1);
             }
-            const int col = tl.n0 + sub * 64;
-            if (in && col < p.N) {
+            emit(col, pk, 0);
+            const int row = row_w + static_cast<int>(lane);
+            if (row < tl.row_end) {
               const int n = min(64, p.N - col);
-              float* const sc = scale_row + (col >> 6);
-              *sc = keep_block(g, n, code_row + col, P.x.wide);
-              sc[P.x.blocks] = keep_block(u, n, code_row + p.N + col, P.x.wide);
+              uint8_t* const codes = P.x.codes + static_cast<size_t>(row) * 2u * static_cast<uint32_t>(p.N) + col;
+              float* const scale = P.x.scales + static_cast<size_t>(row) * 2u * P.x.blocks + (col >> 6);
+              scale[0] = keep_block(g, n, codes, P.x.wide);
+              scale[P.x.blocks] = keep_block(u, n, codes + p.N, P.x.wide);
             }
-          }
-        }
+          } else {
+            // gradients of gate and up from that of H
+            uint32_t pu[32];
+            const uint32_t* dw = reinterpret_cast<const uint32_t*>(dh);
 #pragma unroll
-        for (int sub = 0; sub < 2; ++sub)
-          if (sub < nsub) emit(tl.n0 + sub * 64, hk[sub], 0);
-      } else if constexpr (EPI == kEpiSwigluGrad) {
-        // gradients of gate and up from that of H, 32 columns at a time
-        uint32_t dgk[2][32], duk[2][32];
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          if (c < 2 * nsub) {
-            uint32_t g[32], u[32];
-            tmem_ld_32x32b_x32(t_acc + c * 32, g);
-            tmem_ld_32x32b_x32(t_acc + out_cols + c * 32, u);
-            tmem_wait_ld();
-            if (c == 2 * nsub - 1) release_acc();
-            const uint32_t* dw = reinterpret_cast<const uint32_t*>(&dh[c * 4]);
-#pragma unroll
-            for (int i = 0; i < 16; ++i) {
-              float d0, d1;
+            for (int i = 0; i < 32; ++i) {
+              float d0, d1, dg0, dg1, du0, du1;
               unpack_pair(dw[i], outbf, &d0, &d1);
-              float dg0, dg1, du0, du1;
               swiglu_grad_f32(__uint_as_float(g[2 * i]), __uint_as_float(u[2 * i]), d0, &dg0, &du0);
               swiglu_grad_f32(__uint_as_float(g[2 * i + 1]), __uint_as_float(u[2 * i + 1]), d1, &dg1, &du1);
-              dgk[c >> 1][16 * (c & 1) + i] = outbf ? pack_bf16x2(dg0, dg1) : pack_f16x2(dg0, dg1);
-              duk[c >> 1][16 * (c & 1) + i] = outbf ? pack_bf16x2(du0, du1) : pack_f16x2(du0, du1);
+              pk[i] = outbf ? pack_bf16x2(dg0, dg1) : pack_f16x2(dg0, dg1);
+              pu[i] = outbf ? pack_bf16x2(du0, du1) : pack_f16x2(du0, du1);
             }
-          }
-        }
-#pragma unroll
-        for (int sub = 0; sub < 2; ++sub) {
-          if (sub < nsub) {
-            emit(tl.n0 + sub * 64, dgk[sub], 0);
-            emit(tl.n0 + sub * 64, duk[sub], 1);
+            emit(col, pk, 0);
+            emit(col, pu, 1);
           }
         }
       } else if constexpr (NC == 2) {

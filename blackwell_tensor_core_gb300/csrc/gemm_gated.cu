@@ -12,49 +12,50 @@ using namespace bwg;
 namespace bwg {
 namespace {
 
-template <int EPI>
+// H alone: 256x256 tiles, or 512x256 with two consumers.
 __global__ void __launch_bounds__(kThreads, 1) gated_kernel(const __grid_constant__ DenseGatedParams p) {
+  gemm_body<2, 1, false, 1, kEpiSwiglu, false>(p, p);
+}
+
+__global__ void __launch_bounds__(kThreads2C, 1) gated_2c_kernel(const __grid_constant__ DenseGatedParams p) {
+  gemm_body<2, 1, false, 2, kEpiSwiglu, false>(p, p);
+}
+
+// The epilogues that read or write more: 256x256 tiles, whose accumulator is one of
+// two, so that eight epilogue warps work on one tile while the next is summed up.
+// With 512x256 tiles the tensor cores wait for the epilogue's reads of TMEM:
+// 8192 x 4096 x 8192 with gate and up kept in 8 bits took 341 us, its gradient 356.
+template <int EPI>
+__global__ void __launch_bounds__(kThreads2C, 1) gated_wide_kernel(const __grid_constant__ DenseGatedParams p) {
   gemm_body<2, 1, false, 1, EPI, false>(p, p);
 }
 
 template <int EPI>
-__global__ void __launch_bounds__(kThreads2C, 1) gated_2c_kernel(const __grid_constant__ DenseGatedParams p) {
-  gemm_body<2, 1, false, 2, EPI, false>(p, p);
-}
-
-template <int EPI>
-__global__ void __launch_bounds__(kThreads2C, 1)
-    gated_grouped_2c_kernel(const __grid_constant__ GroupedGatedParams p) {
-  gemm_body<2, 1, true, 2, EPI, true>(p, p.base);
+__global__ void __launch_bounds__(kThreads2C, 1) gated_grouped_kernel(const __grid_constant__ GroupedGatedParams p) {
+  gemm_body<2, 1, true, 1, EPI, true>(p, p.base);
 }
 
 }  // namespace
 
 cudaError_t launch_gated_dense(const DenseGatedParams& p, int epi, bool two, int grid, size_t smem, cudaStream_t s) {
-  if (two) {
-    if (epi == kEpiSwiglu) return launch_two_consumer(gated_2c_kernel<kEpiSwiglu>, p, grid, smem, s);
-    if (epi == kEpiSwigluKeep) return launch_two_consumer(gated_2c_kernel<kEpiSwigluKeep>, p, grid, smem, s);
-    return launch_two_consumer(gated_2c_kernel<kEpiSwigluGrad>, p, grid, smem, s);
-  }
-  if (epi == kEpiSwiglu) return launch_cluster(gated_kernel<kEpiSwiglu>, p, 2, grid, smem, s);
-  if (epi == kEpiSwigluKeep) return launch_cluster(gated_kernel<kEpiSwigluKeep>, p, 2, grid, smem, s);
-  return launch_cluster(gated_kernel<kEpiSwigluGrad>, p, 2, grid, smem, s);
+  if (epi == kEpiSwigluKeep) return launch_two_consumer(gated_wide_kernel<kEpiSwigluKeep>, p, grid, smem, s);
+  if (epi == kEpiSwigluGrad) return launch_two_consumer(gated_wide_kernel<kEpiSwigluGrad>, p, grid, smem, s);
+  return two ? launch_two_consumer(gated_2c_kernel, p, grid, smem, s)
+             : launch_cluster(gated_kernel, p, 2, grid, smem, s);
 }
 
 cudaError_t launch_gated_grouped(const GroupedGatedParams& p, int epi, int grid, size_t smem, cudaStream_t s) {
-  return epi == kEpiSwigluKeep ? launch_two_consumer(gated_grouped_2c_kernel<kEpiSwigluKeep>, p, grid, smem, s)
-                               : launch_two_consumer(gated_grouped_2c_kernel<kEpiSwigluGrad>, p, grid, smem, s);
+  return epi == kEpiSwigluKeep ? launch_two_consumer(gated_grouped_kernel<kEpiSwigluKeep>, p, grid, smem, s)
+                               : launch_two_consumer(gated_grouped_kernel<kEpiSwigluGrad>, p, grid, smem, s);
 }
 
 cudaError_t set_gated_attributes(size_t smem) {
-  const void* fns[] = {reinterpret_cast<const void*>(gated_kernel<kEpiSwiglu>),
-                       reinterpret_cast<const void*>(gated_kernel<kEpiSwigluKeep>),
-                       reinterpret_cast<const void*>(gated_kernel<kEpiSwigluGrad>),
-                       reinterpret_cast<const void*>(gated_2c_kernel<kEpiSwiglu>),
-                       reinterpret_cast<const void*>(gated_2c_kernel<kEpiSwigluKeep>),
-                       reinterpret_cast<const void*>(gated_2c_kernel<kEpiSwigluGrad>),
-                       reinterpret_cast<const void*>(gated_grouped_2c_kernel<kEpiSwigluKeep>),
-                       reinterpret_cast<const void*>(gated_grouped_2c_kernel<kEpiSwigluGrad>)};
+  const void* fns[] = {reinterpret_cast<const void*>(gated_kernel),
+                       reinterpret_cast<const void*>(gated_2c_kernel),
+                       reinterpret_cast<const void*>(gated_wide_kernel<kEpiSwigluKeep>),
+                       reinterpret_cast<const void*>(gated_wide_kernel<kEpiSwigluGrad>),
+                       reinterpret_cast<const void*>(gated_grouped_kernel<kEpiSwigluKeep>),
+                       reinterpret_cast<const void*>(gated_grouped_kernel<kEpiSwigluGrad>)};
   return set_max_smem(fns, smem);
 }
 
@@ -156,7 +157,7 @@ bwg_status run_gated_dense(const GatedCall& c, const Runtime& rt, cudaStream_t s
   const int I = c.N / 2, n_tiles = (I + kTileN / 2 - 1) / (kTileN / 2);
   // two consumers while their tiles still give every pair one, as in gemm_bf16
   const long long tiles_2c = static_cast<long long>((c.M + 4 * kRowsPerCta - 1) / (4 * kRowsPerCta)) * n_tiles;
-  const bool two = tiles_2c >= rt.pairs_2c;
+  const bool two = c.epi == kEpiSwiglu && tiles_2c >= rt.pairs_2c;
   const int stages = two ? 4 : 6, nc = two ? 2 : 1;
   const int smem = dense_smem(2, stages, false, nc);
   if (smem > rt.max_smem) return BWG_ERR_UNSUPPORTED;
@@ -191,7 +192,8 @@ bwg_status run_gated_dense(const GatedCall& c, const Runtime& rt, cudaStream_t s
 }
 
 bwg_status run_gated_grouped(const GatedCall& c, const Runtime& rt, cudaStream_t stream) {
-  const int smem = dense_smem(2, 4, false, 2);
+  constexpr int kStages = 6;
+  const int smem = dense_smem(2, kStages, false, 1);
   if (smem > rt.max_smem) return BWG_ERR_UNSUPPORTED;
   for (int g0 = 0; g0 < c.G; g0 += kMaxGroupsPerLaunch) {
     const int gn = std::min(kMaxGroupsPerLaunch, c.G - g0);
@@ -201,16 +203,16 @@ bwg_status run_gated_grouped(const GatedCall& c, const Runtime& rt, cudaStream_t
     if (!gated_maps(c, &p)) return BWG_ERR_CUDA;
     for (int i = 0; i < gn; ++i)
       if (!gated_weight_map(c, &P.map_b[i], c.w[g0 + i])) return BWG_ERR_CUDA;
-    gated_params(c, rt, 4, &p, &P.x);
+    gated_params(c, rt, kStages, &p, &P.x);
     p.group_offsets = c.offsets;
     p.G = gn;
     p.g_begin = g0;
     p.G_total = c.G;
     // as in the grouped products: at most one partial row tile a group, and a
     // pair for every unit that the last wave's cut can make
-    const int tile_m = 4 * kRowsPerCta;
+    const int tile_m = 2 * kRowsPerCta;
     const long long max_tiles = (static_cast<long long>((c.M + tile_m - 1) / tile_m) + gn) * p.num_n_tiles;
-    p.workers = static_cast<int>(std::min<long long>(max_tiles, rt.pairs_grouped_2c));
+    p.workers = static_cast<int>(std::min<long long>(max_tiles, rt.pairs));
     const long long pairs = max_tiles + 3LL * p.workers;
     if (2 * pairs > 0x7fffffffLL) return BWG_ERR_UNSUPPORTED;
     const cudaError_t e = launch_gated_grouped(P, c.epi, static_cast<int>(2 * pairs), smem, stream);

@@ -75,12 +75,15 @@ bwg_status check_tn(const TnCall& c) {
   return BWG_OK;
 }
 
-// Windows of kBK rows, one for every row that a window can start at (see gemm_body).
-bool window_map(CUtensorMap* m, const void* p, int dtype, int cols, int rows, int ld) {
-  const uint64_t dims[3] = {static_cast<uint64_t>(cols), static_cast<uint64_t>(kBK), static_cast<uint64_t>(rows)};
-  const uint64_t strides[2] = {static_cast<uint64_t>(ld) * 2, static_cast<uint64_t>(ld) * 2};
-  const uint32_t box[3] = {64, kBK, 1};
-  return runtime_map(m, p, map_type(dtype), 3, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B);
+// Windows of kBK rows, one for every row that a window can start at (see
+// gemm_body): boxes of 64 columns, or (pair) of 128 as two groups of 64.
+bool window_map(CUtensorMap* m, const void* p, int dtype, int cols, int rows, int ld, bool pair) {
+  const uint64_t row = static_cast<uint64_t>(ld) * 2;
+  const uint64_t dims[4] = {pair ? 64 : static_cast<uint64_t>(cols), static_cast<uint64_t>(kBK),
+                            static_cast<uint64_t>(rows), static_cast<uint64_t>(cols / 64)};
+  const uint64_t strides[3] = {row, row, 128};
+  const uint32_t box[4] = {64, kBK, 1, 2};
+  return runtime_map(m, p, map_type(dtype), pair ? 4 : 3, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B);
 }
 
 bwg_status run_tn(const TnCall& c, cudaStream_t stream) {
@@ -109,8 +112,12 @@ bwg_status run_tn(const TnCall& c, cudaStream_t stream) {
     const uint64_t dims[3] = {static_cast<uint64_t>(c.N), static_cast<uint64_t>(c.M), static_cast<uint64_t>(c.G)};
     const uint64_t strides[2] = {row, row * c.M};
     const uint32_t box[3] = {oe == 4 ? 32u : 64u, 32, 1};
-    if (!window_map(&p.map_a, c.a, c.dtype, c.M, c.rows, c.lda) ||
-        !window_map(&p.map_b, c.b, c.dtype, c.N, c.rows, c.ldb) ||
+    // one load for a CTA's 128 columns where 64 divides the matrix's
+    p.a_one_box = c.M % 64 == 0 ? 1 : 0;
+    p.b_one_box = c.N % 64 == 0 ? 1 : 0;
+    if (!window_map(&p.map_a, c.a, c.dtype, c.M, c.rows, c.lda, p.a_one_box != 0) ||
+        !window_map(&p.map_b, c.b, c.dtype, c.N, c.rows, c.ldb, false) ||
+        (p.b_one_box && !window_map(&p.map_b1, c.b, c.dtype, c.N, c.rows, c.ldb, true)) ||
         !runtime_map(&p.map_d, c.d, map_type(c.out_dtype), 3, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B))
       return BWG_ERR_CUDA;
     p.err = rt.err;

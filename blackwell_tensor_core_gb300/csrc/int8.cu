@@ -27,7 +27,8 @@ namespace bwg {
 namespace {
 
 constexpr int kThreadsInt8 = 256;
-constexpr int kRowsPerWarp = 4;   // rows in flight a lane
+constexpr int kRowsPerWarp = 2;   // rows in flight a lane
+constexpr int kGradRows = 1;      // the same in SwiGLU's gradient
 constexpr int kOddRows = 2;       // the same where nothing is aligned
 constexpr int kOddCols = 256;     // and the columns that a warp takes
 
@@ -323,12 +324,12 @@ __global__ void __launch_bounds__(kThreadsInt8) swiglu_grad_int8_kernel(const In
   const int seg = static_cast<int>(blockIdx.x - rb * p.segs);
   const int col = (seg * 32 + lane) * 8;
   if (col >= p.cols) return;
-  const long long row0 = (rb * (kThreadsInt8 / 32) + (threadIdx.x >> 5)) * kRowsPerWarp;
-  uint2 cg[kRowsPerWarp], cu[kRowsPerWarp];
-  uint4 dh[kRowsPerWarp];
-  float sg[kRowsPerWarp], su[kRowsPerWarp];
+  const long long row0 = (rb * (kThreadsInt8 / 32) + (threadIdx.x >> 5)) * kGradRows;
+  uint2 cg[kGradRows], cu[kGradRows];
+  uint4 dh[kGradRows];
+  float sg[kGradRows], su[kGradRows];
 #pragma unroll
-  for (int r = 0; r < kRowsPerWarp; ++r) {
+  for (int r = 0; r < kGradRows; ++r) {
     const long long row = row0 + r;
     if (row < p.rows) {
       dh[r] = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.x) + row * p.ldx + col);
@@ -340,7 +341,7 @@ __global__ void __launch_bounds__(kThreadsInt8) swiglu_grad_int8_kernel(const In
     }
   }
 #pragma unroll
-  for (int r = 0; r < kRowsPerWarp; ++r) {
+  for (int r = 0; r < kGradRows; ++r) {
     const long long row = row0 + r;
     if (row < p.rows) {
       float g[8], u[8], d[8], dg[8], du[8], h[8];
@@ -491,7 +492,7 @@ bwg_status swiglu_grad_int8(const void* dH, const void* codes, const float* scal
   p.rows = M;
   p.cols = I;
   p.blocks = (I + kInt8Block - 1) / kInt8Block;
-  const unsigned grid = row_grid(&p, 256, kRowsPerWarp);
+  const unsigned grid = row_grid(&p, 256, kGradRows);
   if (grid == 0) return BWG_ERR_UNSUPPORTED;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   if (dtype == BWG_OUT_BF16) {

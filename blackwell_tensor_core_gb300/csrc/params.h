@@ -94,6 +94,7 @@ struct GemmParams {
   int ws_slots;              // partial slots per stream-K tile (most pairs sharing one)
   float* ws;                 // partials [sk_tiles][ws_slots][16 warp slices][32 rows][256] FP32
   int* ws_counters;          // arrivals [sk_tiles][16 warp slices], zero between calls
+  int a_one_box;             // transposed A: map_a is 4-D, a CTA's 128 columns in one load
   int splits;                // transposed A: slices of each group's k-blocks (planes of D per group)
   // Optional unit trace (nullptr: off): per CTA, kTraceUnits records of
   // kTraceWords words (global timer, ns).
@@ -196,9 +197,9 @@ cudaError_t launch_grouped_2c(const GroupedParams& p, int grid, size_t smem, cud
 int max_active_clusters_grouped_2c(size_t smem);
 cudaError_t launch_grouped_2cta(const GroupedParams& p, int grid, size_t smem, cudaStream_t s,
                                 bool swiglu = false);
-// Gated kernels (gemm_gated.cu): epi = 1 H, 2 H and gate and up in 8 bits, 3 the
-// gradients of gate and up; two = two consumers.  Grouped: 2 and 3, two
-// consumers, cluster launch control.
+// Gated kernels (gemm_gated.cu): epi = 1 H (two: two consumers), 2 H and gate and
+// up in 8 bits, 3 the gradients of gate and up.  Grouped: 2 and 3, cluster launch
+// control.
 cudaError_t launch_gated_dense(const DenseGatedParams& p, int epi, bool two, int grid, size_t smem, cudaStream_t s);
 cudaError_t launch_gated_grouped(const GroupedGatedParams& p, int epi, int grid, size_t smem, cudaStream_t s);
 // Transposed A (gemm_tn.cu): two consumers with sums in TMEM, or one (joined)
