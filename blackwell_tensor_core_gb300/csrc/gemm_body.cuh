@@ -374,19 +374,23 @@ __device__ void gemm_body(const PT& P, const GemmParams& p) {
   const uint32_t smem_a = base;
   const uint32_t smem_b = smem_a + S * kAStage;
   const uint32_t smem_epi = smem_b + S * kBStageBytes;
-  const uint32_t smem_bar = smem_epi + (p.direct_store ? 0u : static_cast<uint32_t>(kEpiBytes));
+  // gradient of SwiGLU: a box of H's gradient for every epilogue warp
+  const uint32_t smem_dh = smem_epi + (p.direct_store ? 0u : static_cast<uint32_t>(kEpiBytes));
+  const uint32_t smem_bar = smem_dh + (EPI == kEpiSwigluGrad ? 8u * kEpiBufBytes : 0u);
   auto full_bar = [&](int s) { return smem_bar + 8u * s; };
   auto empty_bar = [&](int s) { return smem_bar + 8u * (S + s); };
   auto acc_full_bar = [&](int a) { return smem_bar + 8u * (2 * S + a); };
   auto acc_empty_bar = [&](int a) { return smem_bar + 8u * (2 * S + 2 + a); };
   const uint32_t tmem_slot = smem_bar + 8u * (2 * S + 4);
-  const uint32_t tables = tmem_slot + 16u;
+  const uint32_t tables = tmem_slot + (EPI == kEpiSwigluGrad ? 80u : 16u);
   // CLC responses (16 bytes each, 16-byte aligned) and their barriers, after
   // the grouped tables
   const uint32_t clc = (tables + 4u * (3u * kMaxGroupsPerLaunch + 1u) + 15u) & ~15u;
   auto clc_resp = [&](uint32_t s) { return clc + 16u * s; };
   auto clc_full = [&](uint32_t s) { return clc + 16u * kClcSlots + 8u * s; };
   auto clc_empty = [&](uint32_t s) { return clc + 16u * kClcSlots + 8u * (kClcSlots + s); };
+  // (before the tables, for kEpiSwigluGrad) a barrier for every warp's box
+  const uint32_t dh_bars = tmem_slot + 16u;
   // readers of each response: the producer of each CTA, the leader's MMA
   // threads, and every epilogue warp of both CTAs
   constexpr uint32_t kClcReaders = 2u + NC + (kWide ? 16u : 8u);
@@ -401,6 +405,9 @@ __device__ void gemm_body(const PT& P, const GemmParams& p) {
     for (int a = 0; a < 2; ++a) {
       mbar_init(acc_full_bar(a), 1);
       mbar_init(acc_empty_bar(a), CG * (kHalves ? 8 : 4));
+    }
+    if constexpr (EPI == kEpiSwigluGrad) {
+      for (uint32_t w = 0; w < 8; ++w) mbar_init(dh_bars + 8u * w, 1);
     }
     if constexpr (DYN) {
       for (uint32_t s = 0; s < kClcSlots; ++s) {
@@ -772,6 +779,9 @@ __device__ void gemm_body(const PT& P, const GemmParams& p) {
     uint32_t buf = 0;
     uint32_t k = 0;
     int n_traced = 0;
+    const uint32_t dh_bar = dh_bars + 8u * (warp - kEpiWarp0);
+    const uint32_t dh_buf = smem_dh + (warp - kEpiWarp0) * kEpiBufBytes;
+    uint32_t dh_ph = 0;
     for (int t = first; DYN ? t >= 0 : t < total;
          t = next_unit(t, k, kRoleEpilogue, /*arm=*/false, /*warp_wide=*/true)) {
       if (t >= total) continue;
@@ -894,16 +904,14 @@ __device__ void gemm_body(const PT& P, const GemmParams& p) {
         }
         continue;
       }
-      // This lane's row of H's gradient (this warp's 64 columns), read while the
-      // accumulator is still being filled.
-      uint4 dh[EPI == kEpiSwigluGrad ? 8 : 1];
+      // This warp's box of H's gradient comes in while the accumulator is still
+      // being filled (rows past a group's end are read and not used).
       if constexpr (EPI == kEpiSwigluGrad) {
-        const int row = row_w + static_cast<int>(lane), col = tl.n0 + wg * 64;
-        const uint4* src = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(P.x.dh) +
-                                                          static_cast<size_t>(row) * P.x.ld_dh + col);
-        const bool mine = row < tl.row_end && wg * 128 < tl.width;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) dh[i] = mine && col + i * 8 < p.N ? src[i] : make_uint4(0u, 0u, 0u, 0u);
+        const int col = tl.n0 + wg * 64;
+        if (lane == 0 && wg * 128 < tl.width && col < p.N) {
+          mbar_arrive_expect_tx(dh_bar, kEpiBufBytes + p.tx_extra);
+          tma_load_2d(dh_buf, &P.x.map_x, dh_bar, col, row_w);
+        }
       }
       if (!warp_wait(acc_full_bar(acc), acc_ph, p.timeout_ns)) {
         if (lane == 0) record_fault(p.err, kFaultTimeout, kRoleEpilogue, kBarAccFull, acc, acc_ph);
@@ -1054,17 +1062,57 @@ __device__ void gemm_body(const PT& P, const GemmParams& p) {
             }
             emit(col, pk, 0);
             const int row = row_w + static_cast<int>(lane);
+            const int n = min(64, p.N - col);
+            uint32_t cg[16], cu[16];
+            const float sg = keep_block(g, n, cg), su = keep_block(u, n, cu);
             if (row < tl.row_end) {
-              const int n = min(64, p.N - col);
-              uint8_t* const codes = P.x.codes + static_cast<size_t>(row) * 2u * static_cast<uint32_t>(p.N) + col;
               float* const scale = P.x.scales + static_cast<size_t>(row) * 2u * P.x.blocks + (col >> 6);
-              scale[0] = keep_block(g, n, codes, P.x.wide);
-              scale[P.x.blocks] = keep_block(u, n, codes + p.N, P.x.wide);
+              scale[0] = sg;
+              scale[P.x.blocks] = su;
+            }
+            if (P.x.wide && (!GROUPED || row_w + 32 <= tl.row_end)) {
+              // gate's and up's 32 x 64 codes as two boxes of the staging
+              // buffer; stored from registers, 16 bytes a row, they cost the
+              // tensor cores' operand reads 32 cycles an instruction
+              if (lane == 0) bulk_wait_group_read<0>();
+              __syncwarp();
+#pragma unroll
+              for (uint32_t j = 0; j < 4; ++j) {
+                const uint32_t at = ebuf + swizzle64_offset(lane, j);
+                st_shared_v4(at, cg[4 * j], cg[4 * j + 1], cg[4 * j + 2], cg[4 * j + 3]);
+                st_shared_v4(at + 2048u, cu[4 * j], cu[4 * j + 1], cu[4 * j + 2], cu[4 * j + 3]);
+              }
+              fence_proxy_async_shared();
+              __syncwarp();
+              if (lane == 0) {
+                tma_store_3d(&P.x.map_x, ebuf, col, row_w, 0);
+                tma_store_3d(&P.x.map_x, ebuf + 2048u, col, row_w, 1);
+                bulk_commit_group();
+              }
+            } else if (row < tl.row_end) {
+              uint8_t* const codes = P.x.codes + static_cast<size_t>(row) * 2u * static_cast<uint32_t>(p.N) + col;
+#pragma unroll
+              for (int j = 0; j < 8; ++j) {
+                if (8 * j < n) {
+                  reinterpret_cast<uint2*>(codes)[j] = make_uint2(cg[2 * j], cg[2 * j + 1]);
+                  reinterpret_cast<uint2*>(codes + p.N)[j] = make_uint2(cu[2 * j], cu[2 * j + 1]);
+                }
+              }
             }
           } else {
             // gradients of gate and up from that of H
             uint32_t pu[32];
-            const uint32_t* dw = reinterpret_cast<const uint32_t*>(dh);
+            if (!warp_wait(dh_bar, dh_ph, p.timeout_ns)) {
+              if (lane == 0) record_fault(p.err, kFaultTimeout, kRoleEpilogue, kBarFull, warp, dh_ph);
+              aborted = true;
+              break;
+            }
+            dh_ph ^= 1u;
+            uint32_t dw[32];
+#pragma unroll
+            for (uint32_t j = 0; j < 8; ++j)
+              ld_shared_v4(dh_buf + swizzle128_offset(lane, j), &dw[4 * j]);
+            __syncwarp();  // read before the next box comes in
 #pragma unroll
             for (int i = 0; i < 32; ++i) {
               float d0, d1, dg0, dg1, du0, du1;

@@ -105,13 +105,21 @@ bwg_status check_gated(const GatedCall& c) {
   return BWG_OK;
 }
 
-bool gated_maps(const GatedCall& c, GemmParams* p) {
+bool gated_maps(const GatedCall& c, GemmParams* p, GatedExtra* x) {
   const CUtensorMapDataType t =
       c.dtype == BWG_OUT_FP16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
   const uint64_t I = static_cast<uint64_t>(c.N / 2), M = static_cast<uint64_t>(c.M);
   const uint64_t row = static_cast<uint64_t>(c.ldd) * 2;
   if (!runtime_map_2d(&p->map_a, c.x, t, c.K, M, static_cast<uint64_t>(c.ldx) * 2, kBK, kRowsPerCta)) return false;
+  if (c.epi == kEpiSwigluKeep && c.N / 2 % 16 == 0) {
+    const uint64_t dims[3] = {I, M, 2}, strides[2] = {2 * I, I};
+    const uint32_t box[3] = {64, 32, 1};
+    if (!runtime_map(&x->map_x, c.codes, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, dims, strides, box,
+                     CU_TENSOR_MAP_SWIZZLE_64B))
+      return false;
+  }
   if (c.epi != kEpiSwigluGrad) return runtime_map_2d(&p->map_d, c.d, t, I, M, row, 64, 32);
+  if (!runtime_map_2d(&x->map_x, c.dh, t, I, M, static_cast<uint64_t>(c.lddh) * 2, 64, 32)) return false;
   // gate's and up's gradients as two planes of I columns, so that a box at
   // the end of gate's columns stops there
   const uint64_t dims[3] = {I, M, 2}, strides[2] = {row, I * 2};
@@ -149,8 +157,13 @@ void gated_params(const GatedCall& c, const Runtime& rt, int stages, GemmParams*
   x->scales = c.scales;
   x->blocks = (I + kInt8Block - 1) / kInt8Block;
   x->wide = I % 16 == 0 ? 1 : 0;
-  x->dh = c.dh;
-  x->ld_dh = c.lddh;
+}
+
+// The gradient's boxes of dH, 32 KiB, take the place of a stage.
+int gated_stages(int epi, bool two) { return two ? 4 : epi == kEpiSwigluGrad ? 5 : 6; }
+
+int gated_smem(int epi, int stages, int nc) {
+  return dense_smem(2, stages, false, nc) + (epi == kEpiSwigluGrad ? 8 * kEpiBufBytes : 0);
 }
 
 bwg_status run_gated_dense(const GatedCall& c, const Runtime& rt, cudaStream_t stream) {
@@ -158,12 +171,12 @@ bwg_status run_gated_dense(const GatedCall& c, const Runtime& rt, cudaStream_t s
   // two consumers while their tiles still give every pair one, as in gemm_bf16
   const long long tiles_2c = static_cast<long long>((c.M + 4 * kRowsPerCta - 1) / (4 * kRowsPerCta)) * n_tiles;
   const bool two = c.epi == kEpiSwiglu && tiles_2c >= rt.pairs_2c;
-  const int stages = two ? 4 : 6, nc = two ? 2 : 1;
-  const int smem = dense_smem(2, stages, false, nc);
+  const int nc = two ? 2 : 1, stages = gated_stages(c.epi, two);
+  const int smem = gated_smem(c.epi, stages, nc);
   if (smem > rt.max_smem) return BWG_ERR_UNSUPPORTED;
   DenseGatedParams p;
   std::memset(&p, 0, sizeof(p));
-  if (!gated_maps(c, &p) || !gated_weight_map(c, &p.map_b, c.w[0])) return BWG_ERR_CUDA;
+  if (!gated_maps(c, &p, &p.x) || !gated_weight_map(c, &p.map_b, c.w[0])) return BWG_ERR_CUDA;
   // a pair CTA's 128 columns of a stage in one load: [K, N] as 64-column
   // groups, where gate and up both start on one; [N, K] as rows
   if (c.w_nt || I % 64 == 0) {
@@ -192,18 +205,18 @@ bwg_status run_gated_dense(const GatedCall& c, const Runtime& rt, cudaStream_t s
 }
 
 bwg_status run_gated_grouped(const GatedCall& c, const Runtime& rt, cudaStream_t stream) {
-  constexpr int kStages = 6;
-  const int smem = dense_smem(2, kStages, false, 1);
+  const int stages = gated_stages(c.epi, false);
+  const int smem = gated_smem(c.epi, stages, 1);
   if (smem > rt.max_smem) return BWG_ERR_UNSUPPORTED;
   for (int g0 = 0; g0 < c.G; g0 += kMaxGroupsPerLaunch) {
     const int gn = std::min(kMaxGroupsPerLaunch, c.G - g0);
     GroupedGatedParams P;
     std::memset(&P, 0, sizeof(P));
     GemmParams& p = P.base;
-    if (!gated_maps(c, &p)) return BWG_ERR_CUDA;
+    if (!gated_maps(c, &p, &P.x)) return BWG_ERR_CUDA;
     for (int i = 0; i < gn; ++i)
       if (!gated_weight_map(c, &P.map_b[i], c.w[g0 + i])) return BWG_ERR_CUDA;
-    gated_params(c, rt, kStages, &p, &P.x);
+    gated_params(c, rt, stages, &p, &P.x);
     p.group_offsets = c.offsets;
     p.G = gn;
     p.g_begin = g0;

@@ -24,6 +24,44 @@ __global__ void __launch_bounds__(kThreads2C, 1) gemm_tn_joined_kernel(const __g
   gemm_body<2, 1, false, 1, kEpiPlain, DYN, true, true>(p, p);
 }
 
+// D[g] = the sum of its slices' planes, FP32 [G * splits][M][pitch], in order.
+template <int OUT>
+__global__ void __launch_bounds__(256) tn_join_kernel(const float* planes, void* d, int M, int N, int pitch, int splits,
+                                                      long long rows, int ldd) {
+  const int quads = pitch / 4;
+  for (long long i = blockIdx.x * 256LL + threadIdx.x; i < rows * quads; i += gridDim.x * 256LL) {
+    const long long row = i / quads;  // of all groups' rows of D
+    const int col = static_cast<int>(i - row * quads) * 4;
+    const long long g = row / M;
+    const float* src = planes + (g * splits * M + (row - g * M)) * pitch + col;
+    float4 s = *reinterpret_cast<const float4*>(src);
+    for (int k = 1; k < splits; ++k) {
+      const float4 v = *reinterpret_cast<const float4*>(src + static_cast<long long>(k) * M * pitch);
+      s.x += v.x, s.y += v.y, s.z += v.z, s.w += v.w;
+    }
+    const float v[4] = {s.x, s.y, s.z, s.w};
+    if constexpr (OUT == kOutF32) {
+      float* dst = static_cast<float*>(d) + row * ldd + col;
+      if (col + 4 <= N) {
+        *reinterpret_cast<float4*>(dst) = s;
+      } else {
+        for (int j = 0; col + j < N; ++j) dst[j] = v[j];
+      }
+    } else {
+      uint16_t* dst = static_cast<uint16_t*>(d) + row * ldd + col;
+      uint16_t w[4];
+      for (int j = 0; j < 4; ++j)
+        w[j] = static_cast<uint16_t>(OUT == kOutBF16 ? cvt_rn_bf16(v[j]) : cvt_rn_f16(v[j]));
+      if (col + 4 <= N) {
+        *reinterpret_cast<uint2*>(dst) = make_uint2(w[0] | (static_cast<uint32_t>(w[1]) << 16),
+                                                    w[2] | (static_cast<uint32_t>(w[3]) << 16));
+      } else {
+        for (int j = 0; col + j < N; ++j) dst[j] = w[j];
+      }
+    }
+  }
+}
+
 }  // namespace
 
 cudaError_t launch_tn(const GemmParams& p, bool joined, bool dynamic, int grid, size_t smem, cudaStream_t s) {
@@ -53,7 +91,43 @@ struct TnCall {
   void* d;             // G planes [M, N]
   const int* offsets;  // nullptr: one group of all rows
   int G, M, N, rows, lda, ldb, ldd;
+  float* workspace;
+  long long workspace_bytes;
 };
+
+int ceil_div(int a, int b) { return (a + b - 1) / b; }
+
+// Slices of each group's rows: where D has few tiles, pairs would stand idle.
+// Estimated in k-blocks of a 256x256 tile (0.27 us): a unit costs its blocks and
+// kUnit for filling the ring and storing the tile, the join of S > 1 planes a
+// launch and its traffic.
+int tn_splits(int M, int N, int rows, int G, int pairs) {
+  constexpr double kUnit = 10, kJoin = 12;
+  const double tiles = static_cast<double>(G) * ceil_div(M, 256) * ceil_div(N, 256);
+  const double blocks = static_cast<double>(ceil_div(rows, kBK)) / G;
+  if (tiles * 2 > pairs * 3) return 1;  // two waves, a slice would save less than it costs
+  int best = 1;
+  double least = 0;
+  for (int s = 1; s <= 32 && (s == 1 || blocks >= 8.0 * s); ++s) {
+    const double units = tiles * s;
+    const double waves = static_cast<double>((static_cast<long long>(units) + pairs - 1) / pairs);
+    double t = waves * (blocks / s + kUnit);
+    // 8 bytes an element of every plane at 6 TB/s
+    if (s > 1) t += kJoin + static_cast<double>(G) * s * M * N * 8 / 6.0e6 / 0.27;
+    if (s == 1 || t < least) {
+      least = t;
+      best = s;
+    }
+  }
+  return best;
+}
+
+int tn_pitch(int N) { return (N + 3) / 4 * 4; }
+
+long long tn_workspace(int M, int N, int rows, int G, int pairs) {
+  const int s = tn_splits(M, N, rows, G, pairs);
+  return s == 1 ? 0 : 4LL * G * s * M * tn_pitch(N);
+}
 
 CUtensorMapDataType map_type(int dtype) {
   return dtype == BWG_OUT_FP32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32
@@ -97,51 +171,61 @@ bwg_status run_tn(const TnCall& c, cudaStream_t stream) {
     if (all > 0x7fffffffLL) return BWG_ERR_UNSUPPORTED;
     return runtime_status(launch_zero_fill(c.d, static_cast<int>(all), c.N, c.ldd, oe, stream));
   }
-  auto ceil_div = [](int a, int b) { return (a + b - 1) / b; };
   const int n_tiles = ceil_div(c.N, kTileN);
   // FP32 results keep what TMEM's sums lose; other results are 16 bits wide
   const long long tiles_2c = static_cast<long long>(c.G) * ceil_div(c.M, 4 * kRowsPerCta) * n_tiles;
   const bool joined = c.out_dtype == BWG_OUT_FP32 || tiles_2c < rt.pairs_2c;
+  const int splits = joined ? tn_splits(c.M, c.N, c.rows, c.G, rt.pairs) : 1;
+  const int pitch = tn_pitch(c.N);
+  if (splits > 1) {
+    if (c.workspace == nullptr || c.workspace_bytes < tn_workspace(c.M, c.N, c.rows, c.G, rt.pairs))
+      return BWG_ERR_INVALID_ARG;
+    if (!is_aligned(c.workspace, 16)) return BWG_ERR_ALIGNMENT;
+  }
+  void* const planes = splits > 1 ? c.workspace : c.d;  // what the product writes
+  const int plane_type = splits > 1 ? BWG_OUT_FP32 : c.out_dtype;
+  const int plane_ld = splits > 1 ? pitch : c.ldd, pe = splits > 1 ? 4 : oe;
   const int nc = joined ? 1 : 2, stages = joined ? 6 : 4;
   const int smem = dense_smem(2, stages, false, nc);
   if (smem > rt.max_smem) return BWG_ERR_UNSUPPORTED;
   for (int g0 = 0; g0 < c.G; g0 += kMaxGroupsPerLaunch) {
     GemmParams p;
     std::memset(&p, 0, sizeof(p));
-    const uint64_t row = static_cast<uint64_t>(c.ldd) * oe;
-    const uint64_t dims[3] = {static_cast<uint64_t>(c.N), static_cast<uint64_t>(c.M), static_cast<uint64_t>(c.G)};
+    const uint64_t row = static_cast<uint64_t>(plane_ld) * pe;
+    const uint64_t dims[3] = {static_cast<uint64_t>(c.N), static_cast<uint64_t>(c.M),
+                              static_cast<uint64_t>(c.G) * splits};
     const uint64_t strides[2] = {row, row * c.M};
-    const uint32_t box[3] = {oe == 4 ? 32u : 64u, 32, 1};
+    const uint32_t box[3] = {pe == 4 ? 32u : 64u, 32, 1};
     // one load for a CTA's 128 columns where 64 divides the matrix's
     p.a_one_box = c.M % 64 == 0 ? 1 : 0;
     p.b_one_box = c.N % 64 == 0 ? 1 : 0;
     if (!window_map(&p.map_a, c.a, c.dtype, c.M, c.rows, c.lda, p.a_one_box != 0) ||
         !window_map(&p.map_b, c.b, c.dtype, c.N, c.rows, c.ldb, false) ||
         (p.b_one_box && !window_map(&p.map_b1, c.b, c.dtype, c.N, c.rows, c.ldb, true)) ||
-        !runtime_map(&p.map_d, c.d, map_type(c.out_dtype), 3, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B))
+        !runtime_map(&p.map_d, planes, map_type(plane_type), 3, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B))
       return BWG_ERR_CUDA;
     p.err = rt.err;
-    p.d_ptr = c.d;
+    p.d_ptr = planes;
     p.group_offsets = c.offsets;
     p.timeout_ns = rt.timeout_ns;
     p.M = c.M;
     p.N = c.N;
     p.K = c.rows;
-    p.ldd = c.ldd;
+    p.ldd = plane_ld;
     p.num_m_tiles = ceil_div(c.M, 2 * kRowsPerCta * nc);
     p.num_n_tiles = n_tiles;
     p.group_m = kGroupM;
     p.stages = stages;
-    p.out_dtype = c.out_dtype;
+    p.out_dtype = plane_type;
     p.idesc = make_idesc_f16(c.dtype == BWG_OUT_FP16 ? kFmtF16 : kFmtBF16, true, true, 2 * kRowsPerCta, kTileN);
     p.tx_extra = rt.tx_extra;
     p.trace = rt.trace;
     p.no_tail_split = rt.no_tail_split;
-    p.splits = 1;
+    p.splits = splits;
     p.G = std::min(kMaxGroupsPerLaunch, c.G - g0);
     p.g_begin = g0;
     p.G_total = c.G;
-    const long long tiles = static_cast<long long>(p.G) * p.num_m_tiles * n_tiles;
+    const long long tiles = static_cast<long long>(p.G) * splits * p.num_m_tiles * n_tiles;
     if (tiles > 0x0fffffff) return BWG_ERR_UNSUPPORTED;
     p.workers = static_cast<int>(std::min<long long>(tiles, joined ? rt.pairs : rt.pairs_2c));
     // groups differ in length: units are claimed at run time
@@ -150,7 +234,17 @@ bwg_status run_tn(const TnCall& c, cudaStream_t stream) {
     const cudaError_t e = launch_tn(p, joined, dynamic, static_cast<int>(2 * pairs), smem, stream);
     if (e != cudaSuccess) return runtime_status(e);
   }
-  return BWG_OK;
+  if (splits == 1) return BWG_OK;
+  const long long rows = static_cast<long long>(c.G) * c.M;
+  const unsigned grid =
+      static_cast<unsigned>(std::min<long long>((rows * (pitch / 4) + 255) / 256, 16LL * rt.sm_count));
+  if (c.out_dtype == BWG_OUT_FP32)
+    tn_join_kernel<kOutF32><<<grid, 256, 0, stream>>>(c.workspace, c.d, c.M, c.N, pitch, splits, rows, c.ldd);
+  else if (c.out_dtype == BWG_OUT_BF16)
+    tn_join_kernel<kOutBF16><<<grid, 256, 0, stream>>>(c.workspace, c.d, c.M, c.N, pitch, splits, rows, c.ldd);
+  else
+    tn_join_kernel<kOutF16><<<grid, 256, 0, stream>>>(c.workspace, c.d, c.M, c.N, pitch, splits, rows, c.ldd);
+  return runtime_status(cudaGetLastError());
 }
 
 }  // namespace
@@ -158,16 +252,25 @@ bwg_status run_tn(const TnCall& c, cudaStream_t stream) {
 
 extern "C" {
 
+long long bwg_tn_workspace(int M, int N, int K_total, int G) {
+  if (M < 1 || N < 1 || K_total < 1 || G < 1) return 0;
+  Runtime rt;
+  return runtime_device(&rt) == BWG_OK ? tn_workspace(M, N, K_total, G, rt.pairs) : 0;
+}
+
 bwg_status gemm_tn(const void* A, const void* B, void* D, int dtype, int out_dtype, int M, int N, int K, int lda,
-                   int ldb, int ldd, void* stream) {
-  return run_tn(TnCall{dtype, out_dtype, A, B, D, nullptr, 1, M, N, K, lda, ldb, ldd},
+                   int ldb, int ldd, void* workspace, long long workspace_bytes, void* stream) {
+  return run_tn(TnCall{dtype, out_dtype, A, B, D, nullptr, 1, M, N, K, lda, ldb, ldd, static_cast<float*>(workspace),
+                       workspace_bytes},
                 static_cast<cudaStream_t>(stream));
 }
 
 bwg_status grouped_gemm_tn(const void* A, const void* B, void* D, const int* group_offsets, int dtype, int out_dtype,
-                           int G, int M, int N, int K_total, void* stream) {
+                           int G, int M, int N, int K_total, void* workspace, long long workspace_bytes,
+                           void* stream) {
   if (G > 0 && M > 0 && N > 0 && group_offsets == nullptr) return BWG_ERR_INVALID_ARG;
-  return run_tn(TnCall{dtype, out_dtype, A, B, D, group_offsets, G, M, N, K_total, M, N, N},
+  return run_tn(TnCall{dtype, out_dtype, A, B, D, group_offsets, G, M, N, K_total, M, N, N,
+                       static_cast<float*>(workspace), workspace_bytes},
                 static_cast<cudaStream_t>(stream));
 }
 

@@ -56,6 +56,12 @@ BWG_HD uint32_t swizzle128_offset(uint32_t row, uint32_t chunk) {
   return row * 128u + ((chunk ^ (row & 7u)) << 4);
 }
 
+// The same for rows of 64 bytes and 64-byte swizzle: the chunk (0..3) is XOR-ed
+// with the row pair's index modulo 4.
+BWG_HD uint32_t swizzle64_offset(uint32_t row, uint32_t chunk) {
+  return row * 64u + ((chunk ^ ((row >> 1) & 3u)) << 4);
+}
+
 // Grouped raster order of output tiles ("GEMM优化（三）", section 3.2-3.4):
 // tiles are taken in groups of `group_m` tile rows; inside a group the row
 // index runs fastest, so the tiles in flight at one time share a few B column

@@ -113,12 +113,12 @@ struct GroupedParams {
 // the codes and scales of gate and up, [rows, 2 I] and [rows, 2 blocks], or the
 // gradient of H.
 struct GatedExtra {
+  CUtensorMap map_x;  // codes as {I, rows, 2 parts}, box {64, 32, 1}, 64-byte swizzle (wide); or
+                      // H's gradient {I, rows}, box {64, 32}, 128-byte swizzle
   uint8_t* codes;
   float* scales;
   int blocks;    // blocks of 64 columns of gate (and of up)
-  int wide;      // 1: every block of 64 codes starts on a 16-byte boundary
-  const void* dh;
-  int ld_dh;
+  int wide;      // 1: codes of up start on a 16-byte boundary (map_x)
 };
 
 struct DenseGatedParams : GemmParams {

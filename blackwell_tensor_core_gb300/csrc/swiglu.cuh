@@ -71,9 +71,9 @@ BWG_DEV uint32_t pack_bytes(uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
   return __byte_perm(__byte_perm(a, b, 0x0040), __byte_perm(c, d, 0x0040), 0x5410);
 }
 
-// One block of n (1 .. 64) values, n a multiple of 8, in registers: its codes to
-// dst (8-byte aligned; 16 with `wide`), its scale returned.
-BWG_DEV float keep_block(uint32_t (&v)[64], int n, uint8_t* dst, bool wide) {
+// One block of n (1 .. 64) values in registers: its codes, zero past n, and its
+// scale.
+BWG_DEV float keep_block(uint32_t (&v)[64], int n, uint32_t (&codes)[16]) {
   if (n < 64) {
 #pragma unroll
     for (int i = 0; i < 64; ++i)
@@ -85,20 +85,10 @@ BWG_DEV float keep_block(uint32_t (&v)[64], int n, uint8_t* dst, bool wide) {
   for (int i = 0; i < 64; ++i) a[i & 3] = max_abs_nan(a[i & 3], __uint_as_float(v[i]));
   float scale, inv;
   int8_scale(max_abs_nan(max_abs_nan(a[0], a[1]), max_abs_nan(a[2], a[3])), &scale, &inv);
-  uint32_t w[16];
 #pragma unroll
   for (int i = 0; i < 16; ++i)
-    w[i] = pack_bytes(int8_code(__uint_as_float(v[4 * i]), inv), int8_code(__uint_as_float(v[4 * i + 1]), inv),
-                      int8_code(__uint_as_float(v[4 * i + 2]), inv), int8_code(__uint_as_float(v[4 * i + 3]), inv));
-  if (wide && n == 64) {
-#pragma unroll
-    for (int j = 0; j < 4; ++j)
-      reinterpret_cast<uint4*>(dst)[j] = make_uint4(w[4 * j], w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]);
-  } else {
-#pragma unroll
-    for (int j = 0; j < 8; ++j)
-      if (8 * j < n) reinterpret_cast<uint2*>(dst)[j] = make_uint2(w[2 * j], w[2 * j + 1]);
-  }
+    codes[i] = pack_bytes(int8_code(__uint_as_float(v[4 * i]), inv), int8_code(__uint_as_float(v[4 * i + 1]), inv),
+                          int8_code(__uint_as_float(v[4 * i + 2]), inv), int8_code(__uint_as_float(v[4 * i + 3]), inv));
   return scale;
 }
 

@@ -91,8 +91,9 @@ def lib() -> ctypes.CDLL:
                                ("quantize_int8", [vp, i, i, i, i, i, vp, vp, vp]),
                                ("dequantize_int8", [vp, vp, i, vp, i, i, i, i, vp]),
                                ("swiglu_grad_int8", [vp, vp, vp, vp, vp, i, i, i, i, i, i, vp]),
-                               ("gemm_tn", [vp, vp, vp, i, i, i, i, i, i, i, i, vp]),
-                               ("grouped_gemm_tn", [vp, vp, vp, vp, i, i, i, i, i, i, vp]),
+                               ("gemm_tn", [vp, vp, vp, i, i, i, i, i, i, i, i, vp, ctypes.c_longlong, vp]),
+                               ("grouped_gemm_tn", [vp, vp, vp, vp, i, i, i, i, i, i, vp, ctypes.c_longlong,
+                                                    vp]),
                                ("moe_combine_grad", [vp, vp, i, i, i, i, i, i, vp, vp, vp, i, vp, i, vp, vp])):
                 f = getattr(L, name)
                 f.argtypes = args
@@ -157,6 +158,8 @@ def lib() -> ctypes.CDLL:
             L.bwg_fp4_kernel.restype = i
             L.bwg_idesc_fp4.argtypes = [i, i, i, i]
             L.bwg_idesc_fp4.restype = u32
+            L.bwg_tn_workspace.argtypes = [i, i, i, i]
+            L.bwg_tn_workspace.restype = ctypes.c_longlong
             L.bwg_version.argtypes = []
             L.bwg_version.restype = ctypes.c_char_p
             _lib = L
@@ -916,6 +919,12 @@ def _like(t: torch.Tensor, name: str, dtype, dev) -> None:
         raise ValueError("%s must be a %s tensor on %s" % (name, dtype, dev))
 
 
+def _tn_work(M: int, N: int, rows: int, G: int, dev, stream) -> tuple:
+    """(bytes, tensor or None) of the workspace of a product with transposed A."""
+    need = _on(dev, lib().bwg_tn_workspace, M, N, rows, G)
+    return need, _new((need,), torch.uint8, dev, stream) if need > 0 else None
+
+
 def _gemm_tn(A, B, out, out_dtype, stream, b_transposed) -> torch.Tensor:
     if b_transposed:
         raise ValueError("a_transposed takes B as [K, N]")
@@ -926,8 +935,10 @@ def _gemm_tn(A, B, out, out_dtype, stream, b_transposed) -> torch.Tensor:
     lda, ldb = _rows(A, "A", K), _rows(B, "B", K)
     _fits("M or N", M, N)
     out, ldd = _fp4_out(out, out_dtype, M, N, dev, stream)
+    need, work = _tn_work(M, N, K, 1, dev, stream)
     _check(_on(dev, lib().gemm_tn, A.data_ptr(), B.data_ptr(), out.data_ptr(), _OUT_CODES[A.dtype],
-               _OUT_CODES[out.dtype], M, N, K, lda, ldb, ldd, _stream_handle(stream, dev)), "gemm_tn")
+               _OUT_CODES[out.dtype], M, N, K, lda, ldb, ldd, None if work is None else work.data_ptr(), need,
+               _stream_handle(stream, dev)), "gemm_tn")
     return out
 
 
@@ -954,9 +965,10 @@ def grouped_gemm_wgrad(A: torch.Tensor, B: torch.Tensor, group_offsets: torch.Te
         raise ValueError("out must be a dense [%d, %d, %d] tensor on %s" % (G, M, N, dev))
     if out.dtype not in _OUT_CODES:
         raise TypeError("output dtype must be bfloat16, float16 or float32")
+    need, work = _tn_work(M, N, rows, G, dev, stream)
     _check(_on(dev, lib().grouped_gemm_tn, A.data_ptr(), B.data_ptr(), out.data_ptr(), group_offsets.data_ptr(),
-               _OUT_CODES[A.dtype], _OUT_CODES[out.dtype], G, M, N, rows, _stream_handle(stream, dev)),
-           "grouped_gemm_tn")
+               _OUT_CODES[A.dtype], _OUT_CODES[out.dtype], G, M, N, rows, None if work is None else work.data_ptr(),
+               need, _stream_handle(stream, dev)), "grouped_gemm_tn")
     return out
 
 
