@@ -353,7 +353,8 @@ __device__ void gemm_body(const PT& P, const GemmParams& p) {
   constexpr bool kTables = GROUPED || TN;              // row ranges of groups in shared memory
   // two epilogue warpgroups: one a consumer, or (kHalves) one for each half of
   // the columns of a single consumer's tile
-  constexpr bool kHalves = CH || EPI >= kEpiSwigluKeep;
+  constexpr bool kHalves = CH || EPI >= kEpiSwigluKeep || (EPI == kEpiSwiglu && NC == 1 && !GROUPED);
+  constexpr bool kGated = SW && kHalves;
   constexpr bool kWide = NC == 2 || kHalves;
   static_assert(!kHalves || NC == 1, "halves of the columns: one consumer");
   extern __shared__ __align__(1024) uint8_t smem_raw[];
@@ -579,15 +580,15 @@ __device__ void gemm_body(const PT& P, const GemmParams& p) {
               if ((tl.cmask >> c) & 1) {
                 const int col = a_row + c * 2 * kRowsPerCta;  // columns of A: rows of D
                 const uint32_t dst = sa + c * kAStageBytes;
-                if (p.a_one_box) {
-                  tma_load_4d_pair(dst, &p.map_a, fb, 0, w0, wr, col / 64);
+                if (col + kRowsPerCta <= P.a_grouped) {
+                  tma_load_4d_pair(dst, &P.map_a1, fb, 0, w0, wr, col / 64);
                 } else {
                   tma_load_3d_pair(dst, &p.map_a, fb, col, w0, wr);
                   tma_load_3d_pair(dst + kAStageBytes / 2, &p.map_a, fb, col + 64, w0, wr);
                 }
               }
             }
-            if (p.b_one_box && b_chunks == 2) {
+            if (b_chunks == 2 && b_col + 128 <= P.b_grouped) {
               tma_load_4d_pair(sb, &p.map_b1, fb, 0, w0, wr, b_col / 64);
             } else {
               for (uint32_t j = 0; j < b_chunks; ++j)
@@ -1035,8 +1036,8 @@ __device__ void gemm_body(const PT& P, const GemmParams& p) {
       // output the warp therefore reads its whole 32 x 256 slice out of TMEM
       // first (packed to 16 bits: 128 registers), releases the accumulator,
       // and only then stages and stores it, while the next tile's MMAs run.
-      const bool early = EPI >= kEpiSwigluKeep || (NC == 2 && !out32 && fix == nullptr && store_slice);
-      if constexpr (EPI >= kEpiSwigluKeep) {
+      const bool early = kGated || (NC == 2 && !out32 && fix == nullptr && store_slice);
+      if constexpr (kGated) {
         // This warp's 32 rows x 64 columns of gate and of up, out of TMEM at once;
         // a unit of half width has columns for the first warpgroup only.
         const int c0 = wg * 64, col = tl.n0 + c0;
@@ -1052,8 +1053,7 @@ __device__ void gemm_body(const PT& P, const GemmParams& p) {
         release_acc();
         if (c0 < out_cols && col < p.N) {
           uint32_t pk[32];
-          if constexpr (EPI == kEpiSwigluKeep) {
-            // H, and gate and up of this row put into 8 bits, a block each
+          if constexpr (EPI != kEpiSwigluGrad) {
 #pragma unroll
             for (int i = 0; i < 32; ++i) {
               const float y0 = swiglu_f32(__uint_as_float(g[2 * i]), __uint_as_float(u[2 * i]));
@@ -1061,6 +1061,9 @@ __device__ void gemm_body(const PT& P, const GemmParams& p) {
               pk[i] = outbf ? pack_bf16x2(y0, y1) : pack_f16x2(y0, y1);
             }
             emit(col, pk, 0);
+          }
+          if constexpr (EPI == kEpiSwigluKeep) {
+            // gate and up of this row put into 8 bits, a block each
             const int row = row_w + static_cast<int>(lane);
             const int n = min(64, p.N - col);
             uint32_t cg[16], cu[16];
@@ -1099,7 +1102,7 @@ __device__ void gemm_body(const PT& P, const GemmParams& p) {
                 }
               }
             }
-          } else {
+          } else if constexpr (EPI == kEpiSwigluGrad) {
             // gradients of gate and up from that of H
             uint32_t pu[32];
             if (!warp_wait(dh_bar, dh_ph, p.timeout_ns)) {

@@ -12,19 +12,16 @@ using namespace bwg;
 namespace bwg {
 namespace {
 
-// H alone: 256x256 tiles, or 512x256 with two consumers.
-__global__ void __launch_bounds__(kThreads, 1) gated_kernel(const __grid_constant__ DenseGatedParams p) {
-  gemm_body<2, 1, false, 1, kEpiSwiglu, false>(p, p);
-}
-
+// H alone, 512x256 tiles.
 __global__ void __launch_bounds__(kThreads2C, 1) gated_2c_kernel(const __grid_constant__ DenseGatedParams p) {
   gemm_body<2, 1, false, 2, kEpiSwiglu, false>(p, p);
 }
 
-// The epilogues that read or write more: 256x256 tiles, whose accumulator is one of
-// two, so that eight epilogue warps work on one tile while the next is summed up.
-// With 512x256 tiles the tensor cores wait for the epilogue's reads of TMEM:
-// 8192 x 4096 x 8192 with gate and up kept in 8 bits took 341 us, its gradient 356.
+// 256x256 tiles, whose accumulator is one of two, so that eight epilogue warps work
+// on one tile while the next is summed up: H alone where 512x256 tiles would be
+// too few, and the epilogues that read or write more, for which the tensor cores
+// would wait with 512x256 tiles (8192 x 4096 x 8192 with gate and up kept in 8
+// bits took 341 us with them, its gradient 356).
 template <int EPI>
 __global__ void __launch_bounds__(kThreads2C, 1) gated_wide_kernel(const __grid_constant__ DenseGatedParams p) {
   gemm_body<2, 1, false, 1, EPI, false>(p, p);
@@ -41,7 +38,7 @@ cudaError_t launch_gated_dense(const DenseGatedParams& p, int epi, bool two, int
   if (epi == kEpiSwigluKeep) return launch_two_consumer(gated_wide_kernel<kEpiSwigluKeep>, p, grid, smem, s);
   if (epi == kEpiSwigluGrad) return launch_two_consumer(gated_wide_kernel<kEpiSwigluGrad>, p, grid, smem, s);
   return two ? launch_two_consumer(gated_2c_kernel, p, grid, smem, s)
-             : launch_cluster(gated_kernel, p, 2, grid, smem, s);
+             : launch_two_consumer(gated_wide_kernel<kEpiSwiglu>, p, grid, smem, s);
 }
 
 cudaError_t launch_gated_grouped(const GroupedGatedParams& p, int epi, int grid, size_t smem, cudaStream_t s) {
@@ -50,8 +47,8 @@ cudaError_t launch_gated_grouped(const GroupedGatedParams& p, int epi, int grid,
 }
 
 cudaError_t set_gated_attributes(size_t smem) {
-  const void* fns[] = {reinterpret_cast<const void*>(gated_kernel),
-                       reinterpret_cast<const void*>(gated_2c_kernel),
+  const void* fns[] = {reinterpret_cast<const void*>(gated_2c_kernel),
+                       reinterpret_cast<const void*>(gated_wide_kernel<kEpiSwiglu>),
                        reinterpret_cast<const void*>(gated_wide_kernel<kEpiSwigluKeep>),
                        reinterpret_cast<const void*>(gated_wide_kernel<kEpiSwigluGrad>),
                        reinterpret_cast<const void*>(gated_grouped_kernel<kEpiSwigluKeep>),
@@ -200,7 +197,9 @@ bwg_status run_gated_dense(const GatedCall& c, const Runtime& rt, cudaStream_t s
   p.num_m_tiles = (c.M + tile_m - 1) / tile_m;
   const long long tiles = static_cast<long long>(p.num_m_tiles) * n_tiles;
   if (tiles > 0x3fffffff) return BWG_ERR_UNSUPPORTED;
-  p.workers = static_cast<int>(std::min<long long>(tiles, two ? rt.pairs_2c : rt.pairs));
+  // with pairs for all their halves, few tiles are cut in two
+  const int all = two ? rt.pairs_2c : rt.pairs;
+  p.workers = static_cast<int>(2 * tiles <= all ? 2 * tiles : std::min<long long>(tiles, all));
   return runtime_status(launch_gated_dense(p, c.epi, two, 2 * p.workers, smem, stream));
 }
 

@@ -14,13 +14,13 @@ namespace {
 
 // 512x256 tiles, sums in TMEM.
 template <bool DYN>
-__global__ void __launch_bounds__(kThreads2C, 1) gemm_tn_2c_kernel(const __grid_constant__ GemmParams p) {
+__global__ void __launch_bounds__(kThreads2C, 1) gemm_tn_2c_kernel(const __grid_constant__ TnParams p) {
   gemm_body<2, 1, false, 2, kEpiPlain, DYN, true, false>(p, p);
 }
 
 // 256x256 tiles, sums of kChunkBlocks k-blocks joined in registers.
 template <bool DYN>
-__global__ void __launch_bounds__(kThreads2C, 1) gemm_tn_joined_kernel(const __grid_constant__ GemmParams p) {
+__global__ void __launch_bounds__(kThreads2C, 1) gemm_tn_joined_kernel(const __grid_constant__ TnParams p) {
   gemm_body<2, 1, false, 1, kEpiPlain, DYN, true, true>(p, p);
 }
 
@@ -64,7 +64,7 @@ __global__ void __launch_bounds__(256) tn_join_kernel(const float* planes, void*
 
 }  // namespace
 
-cudaError_t launch_tn(const GemmParams& p, bool joined, bool dynamic, int grid, size_t smem, cudaStream_t s) {
+cudaError_t launch_tn(const TnParams& p, bool joined, bool dynamic, int grid, size_t smem, cudaStream_t s) {
   if (joined)
     return dynamic ? launch_two_consumer(gemm_tn_joined_kernel<true>, p, grid, smem, s)
                    : launch_two_consumer(gemm_tn_joined_kernel<false>, p, grid, smem, s);
@@ -189,19 +189,20 @@ bwg_status run_tn(const TnCall& c, cudaStream_t stream) {
   const int smem = dense_smem(2, stages, false, nc);
   if (smem > rt.max_smem) return BWG_ERR_UNSUPPORTED;
   for (int g0 = 0; g0 < c.G; g0 += kMaxGroupsPerLaunch) {
-    GemmParams p;
+    TnParams p;
     std::memset(&p, 0, sizeof(p));
     const uint64_t row = static_cast<uint64_t>(plane_ld) * pe;
     const uint64_t dims[3] = {static_cast<uint64_t>(c.N), static_cast<uint64_t>(c.M),
                               static_cast<uint64_t>(c.G) * splits};
     const uint64_t strides[2] = {row, row * c.M};
     const uint32_t box[3] = {pe == 4 ? 32u : 64u, 32, 1};
-    // one load for a CTA's 128 columns where 64 divides the matrix's
-    p.a_one_box = c.M % 64 == 0 ? 1 : 0;
-    p.b_one_box = c.N % 64 == 0 ? 1 : 0;
-    if (!window_map(&p.map_a, c.a, c.dtype, c.M, c.rows, c.lda, p.a_one_box != 0) ||
+    // whole groups of 64 columns; what is left of a row takes plain boxes
+    p.a_grouped = c.M / 64 * 64;
+    p.b_grouped = c.N / 64 * 64;
+    if (!window_map(&p.map_a, c.a, c.dtype, c.M, c.rows, c.lda, false) ||
         !window_map(&p.map_b, c.b, c.dtype, c.N, c.rows, c.ldb, false) ||
-        (p.b_one_box && !window_map(&p.map_b1, c.b, c.dtype, c.N, c.rows, c.ldb, true)) ||
+        (p.a_grouped > 0 && !window_map(&p.map_a1, c.a, c.dtype, c.M, c.rows, c.lda, true)) ||
+        (p.b_grouped > 0 && !window_map(&p.map_b1, c.b, c.dtype, c.N, c.rows, c.ldb, true)) ||
         !runtime_map(&p.map_d, planes, map_type(plane_type), 3, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B))
       return BWG_ERR_CUDA;
     p.err = rt.err;
@@ -227,7 +228,9 @@ bwg_status run_tn(const TnCall& c, cudaStream_t stream) {
     p.G_total = c.G;
     const long long tiles = static_cast<long long>(p.G) * splits * p.num_m_tiles * n_tiles;
     if (tiles > 0x0fffffff) return BWG_ERR_UNSUPPORTED;
-    p.workers = static_cast<int>(std::min<long long>(tiles, joined ? rt.pairs : rt.pairs_2c));
+    // with pairs for all their halves, few tiles are cut in two
+    const int all = joined ? rt.pairs : rt.pairs_2c;
+    p.workers = static_cast<int>(2 * tiles <= all ? 2 * tiles : std::min<long long>(tiles, all));
     // groups differ in length: units are claimed at run time
     const bool dynamic = c.offsets != nullptr;
     const long long pairs = dynamic ? tiles + 3LL * p.workers : p.workers;

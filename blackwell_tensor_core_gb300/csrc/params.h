@@ -94,7 +94,6 @@ struct GemmParams {
   int ws_slots;              // partial slots per stream-K tile (most pairs sharing one)
   float* ws;                 // partials [sk_tiles][ws_slots][16 warp slices][32 rows][256] FP32
   int* ws_counters;          // arrivals [sk_tiles][16 warp slices], zero between calls
-  int a_one_box;             // transposed A: map_a is 4-D, a CTA's 128 columns in one load
   int splits;                // transposed A: slices of each group's k-blocks (planes of D per group)
   // Optional unit trace (nullptr: off): per CTA, kTraceUnits records of
   // kTraceWords words (global timer, ns).
@@ -107,6 +106,14 @@ constexpr int kTraceWords = 5;  // unit, producer start, epilogue end, accumulat
 struct GroupedParams {
   GemmParams base;
   CUtensorMap map_b[kMaxGroupsPerLaunch];
+};
+
+// Transposed A: columns of A and B below a_grouped and b_grouped (multiples of 64)
+// are loaded 128 at a time, through windows of 64-column groups: 4-D maps {64, kBK,
+// rows, groups}, box {64, kBK, 1, 2} (map_a1, and the base's map_b1).
+struct TnParams : GemmParams {
+  CUtensorMap map_a1;
+  int a_grouped, b_grouped;
 };
 
 // What the gated kernels' epilogues read and write beside D (see gemm_body):
@@ -204,7 +211,7 @@ cudaError_t launch_gated_dense(const DenseGatedParams& p, int epi, bool two, int
 cudaError_t launch_gated_grouped(const GroupedGatedParams& p, int epi, int grid, size_t smem, cudaStream_t s);
 // Transposed A (gemm_tn.cu): two consumers with sums in TMEM, or one (joined)
 // whose sums are joined in registers; dynamic as above.
-cudaError_t launch_tn(const GemmParams& p, bool joined, bool dynamic, int grid, size_t smem, cudaStream_t s);
+cudaError_t launch_tn(const TnParams& p, bool joined, bool dynamic, int grid, size_t smem, cudaStream_t s);
 cudaError_t launch_small_m(const SmallMParams& p, int grid, size_t smem, cudaStream_t s);
 // Co-resident clusters of `cluster` small-M CTAs with `smem` bytes each (0 on error).
 int max_active_clusters_small_m(int cluster, size_t smem);

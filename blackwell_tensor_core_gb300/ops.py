@@ -1030,29 +1030,49 @@ class SwigluGrad(NamedTuple):
     h: torch.Tensor | None    # the block's output once more, with with_h
 
 
+def _kept_grad(dh, lddh: int, kept: Int8Matrix, with_h: bool, M: int, N: int, dev, stream, handle) -> tuple:
+    """(dgu, h or None) from checked operands."""
+    dtype, inner = dh.dtype, N // 2
+    dgu = _new((M, N), dtype, dev, stream)
+    h = _new((M, inner), dtype, dev, stream) if with_h else None
+    _check(lib().swiglu_grad_int8(dh.data_ptr(), kept.codes.data_ptr(), kept.scales.data_ptr(), dgu.data_ptr(),
+                                  h.data_ptr() if with_h else None, _OUT_CODES[dtype], M, inner, lddh, N, inner,
+                                  handle), "swiglu_grad_int8")
+    return dgu, h
+
+
 def swiglu_grad(dh: torch.Tensor, kept: Int8Matrix, with_h: bool = False, stream=None):
     """[dgate | dup] ([M, N]) from the gradient of h = silu(gate) * up and
     [gate | up] kept in 8 bits; with ``with_h`` also h, as (dgu, h)."""
     _half(dh, "dh")
     M, N = _int8_check(kept, "kept", 2)
-    dev, dtype, inner = dh.device, dh.dtype, N // 2
-    if kept.device != dev or dh.shape != (M, inner):
-        raise ValueError("dh must be [%d, %d] on %s" % (M, inner, kept.device))
-    lddh = _rows(dh, "dh", M)
-    dgu = _new((M, N), dtype, dev, stream)
-    h = _new((M, inner), dtype, dev, stream) if with_h else None
-    _check(_on(dev, lib().swiglu_grad_int8, dh.data_ptr(), kept.codes.data_ptr(), kept.scales.data_ptr(),
-               dgu.data_ptr(), h.data_ptr() if with_h else None, _OUT_CODES[dtype], M, inner, lddh, N, inner,
-               _stream_handle(stream, dev)), "swiglu_grad_int8")
+    dev = dh.device
+    if kept.codes.device != dev or dh.shape != (M, N // 2):
+        raise ValueError("dh must be [%d, %d] on %s" % (M, N // 2, kept.device))
+    dgu, h = _on(dev, _kept_grad, dh, _rows(dh, "dh", M), kept, with_h, M, N, dev, stream,
+                 _stream_handle(stream, dev))
     return (dgu, h) if with_h else dgu
 
 
-def _block_input(x, dh, stream) -> torch.Tensor:
-    """The block's input in dh's dtype, read back where it was kept in 8 bits."""
-    if isinstance(x, Int8Matrix):
-        return dequantize_int8(x, out_dtype=dh.dtype, stream=stream)
-    _like(x, "x", dh.dtype, dh.device)
-    return x
+def _block_operands(dh, x, kept, with_h: bool, N: int) -> tuple[int, int]:
+    """(M, K) of a gated block's backward pass, its operands checked."""
+    dev, kept_x = dh.device, isinstance(x, Int8Matrix)
+    if kept_x:
+        M, K = _int8_check(x, "x", 1)
+    else:
+        M, K = x.shape
+    if (x.codes if kept_x else x).device != dev:
+        raise ValueError("x must be on %s" % dev)
+    if not kept_x and x.dtype is not dh.dtype:
+        raise TypeError("x must have the dtype of dh, %s" % dh.dtype)
+    if dh.shape != (M, N // 2):
+        raise ValueError("dh must be [%d, %d], got %s" % (M, N // 2, tuple(dh.shape)))
+    if kept is None:
+        if with_h:
+            raise ValueError("with_h reads h from kept")
+    elif _int8_check(kept, "kept", 2) != (M, N) or kept.codes.device != dev:
+        raise ValueError("kept must be [%d, %d] on %s, got %s" % (M, N, dev, tuple(kept.shape)))
+    return M, K
 
 
 def gemm_swiglu_grad(dh: torch.Tensor, x, w: torch.Tensor, kept: Int8Matrix | None = None, with_h: bool = False,
@@ -1062,37 +1082,40 @@ def gemm_swiglu_grad(dh: torch.Tensor, x, w: torch.Tensor, kept: Int8Matrix | No
     (like w), in dh's dtype.  x is the block's input, or the Int8Matrix it was kept
     in.  With ``kept`` gate and up are read from 8 bits and ``with_h`` gives h too
     (for the gradient of the weight that follows); without it they are multiplied
-    out again.  [dgate | dup] is rounded to dh's dtype on the way."""
+    out again.  [dgate | dup], and x read back, are rounded to dh's dtype on the way."""
     _half(dh, "dh")
-    dev, dtype = dh.device, dh.dtype
-    if isinstance(x, Int8Matrix):
-        _int8_check(x, "x")
-    if x.device != dev:
-        raise ValueError("x must be on %s" % dev)
-    M, K = x.shape
-    N, ldw = _gated_weight(w, dtype, dev, K, b_transposed)
-    if dh.shape != (M, N // 2):
-        raise ValueError("dh must be [%d, %d], got %s" % (M, N // 2, tuple(dh.shape)))
+    dev = dh.device
+    N, ldw = _gated_weight(w, dh.dtype, dev, x.shape[1], b_transposed)
+    M, K = _block_operands(dh, x, kept, with_h, N)
     lddh = _rows(dh, "dh", M)
-    xv = _block_input(x, dh, stream) if need_dw or kept is None else None
+    if isinstance(x, Int8Matrix):
+        x = dequantize_int8(x, out_dtype=dh.dtype, stream=stream) if need_dw or kept is None else None
+    ldx = _rows(x, "x", M) if x is not None else 0
+    return _on(dev, _block_grad, dh, lddh, x, ldx, w, ldw, kept, with_h, b_transposed, need_dx, need_dw, M, N, K, dev,
+               stream)
+
+
+def _block_grad(dh, lddh, x, ldx, w, ldw, kept, with_h, b_transposed, need_dx, need_dw, M, N, K, dev,
+                stream) -> SwigluGrad:
+    dtype, L, handle = dh.dtype, lib(), _stream_handle(stream, dev)
+    code = _OUT_CODES[dtype]
     if kept is not None:
-        if kept.shape != (M, N):
-            raise ValueError("kept must be [%d, %d], got %s" % (M, N, tuple(kept.shape)))
-        dgu, h = swiglu_grad(dh, kept, True, stream) if with_h else (swiglu_grad(dh, kept, False, stream), None)
-    elif with_h:
-        raise ValueError("with_h reads h from kept")
+        dgu, h = _kept_grad(dh, lddh, kept, with_h, M, N, dev, stream, handle)
     else:
-        h = None
-        dgu = _new((M, N), dtype, dev, stream)
-        _check(_on(dev, lib().gemm_swiglu_grad, dh.data_ptr(), xv.data_ptr(), w.data_ptr(), dgu.data_ptr(),
-                   _OUT_CODES[dtype], 1 if b_transposed else 0, M, N, K, lddh, _rows(xv, "x", M), ldw, N,
-                   _stream_handle(stream, dev)), "gemm_swiglu_grad")
+        dgu, h = _new((M, N), dtype, dev, stream), None
+        _check(L.gemm_swiglu_grad(dh.data_ptr(), x.data_ptr(), w.data_ptr(), dgu.data_ptr(), code,
+                                  1 if b_transposed else 0, M, N, K, lddh, ldx, ldw, N, handle), "gemm_swiglu_grad")
     dx = dw = None
-    if need_dx:  # w is [K, N]: the second operand as [out, in]
-        dx = gemm(dgu, w, _new((M, K), dtype, dev, stream), stream=stream, b_transposed=not b_transposed)
+    if need_dx:  # w [K, N] is the second operand as [out, in]
+        dx = _new((M, K), dtype, dev, stream)
+        name = ("gemm_bf16" if code == OUT_BF16 else "gemm_fp16") + ("" if b_transposed else "_nt")
+        _check(getattr(L, name)(dgu.data_ptr(), w.data_ptr(), dx.data_ptr(), M, K, N, N, ldw, K, code, handle), name)
     if need_dw:
-        a, b = (dgu, xv) if b_transposed else (xv, dgu)
-        dw = gemm(a, b, out_dtype=dtype, stream=stream, a_transposed=True)
+        rows, cols, a, lda, b, ldb = (N, K, dgu, N, x, ldx) if b_transposed else (K, N, x, ldx, dgu, N)
+        dw = _new((rows, cols), dtype, dev, stream)
+        need, work = _tn_work(rows, cols, M, 1, dev, stream)
+        _check(L.gemm_tn(a.data_ptr(), b.data_ptr(), dw.data_ptr(), code, code, rows, cols, M, lda, ldb, cols,
+                         None if work is None else work.data_ptr(), need, handle), "gemm_tn")
     return SwigluGrad(dx, dw, h)
 
 
@@ -1102,39 +1125,50 @@ def grouped_gemm_swiglu_grad(dh: torch.Tensor, x, ws: list, group_offsets: torch
     """The same for the experts' blocks, grouped_gemm(x, ws, group_offsets,
     swiglu=True): dx [rows, K] and dw [G, *w.shape]."""
     _half(dh, "dh")
-    dev, dtype = dh.device, dh.dtype
+    dev, dtype, G = dh.device, dh.dtype, len(ws)
+    _like(group_offsets, "group_offsets", torch.int32, dev)
+    if G == 0 or group_offsets.shape != (G + 1,) or not group_offsets.is_contiguous():
+        raise ValueError("group_offsets must be a dense int32 tensor [G + 1], with a weight for each of G >= 1 groups")
+    shape = ws[0].shape
+    for w in ws:
+        if w.shape != shape or w.dtype != dtype or not w.is_contiguous() or w.device != dev or w.dim() != 2:
+            raise ValueError("every weight must be a dense [K, N] (or [N, K]) tensor of dh's dtype on %s" % dev)
+    N, K = shape if b_transposed else (shape[1], shape[0])
+    if N % 2 or K != x.shape[1]:
+        raise ValueError("weights of %s do not fit x with %d columns" % (tuple(shape), x.shape[1]))
+    M, K = _block_operands(dh, x, kept, with_h, N)
+    _fits("rows, columns or groups", M, K, N, G)
     if isinstance(x, Int8Matrix):
-        _int8_check(x, "x")
-    if x.device != dev:
-        raise ValueError("x must be on %s" % dev)
-    xv = _block_input(x, dh, stream) if need_dw or kept is None else None
-    M, K = x.shape
-    G = len(ws)
-    if xv is not None:
-        _, _, N, _ = _grouped_operands(xv, ws, group_offsets, b_transposed)
-    else:
-        N = (ws[0].shape[0] if b_transposed else ws[0].shape[1]) if G else 0
-    if N % 2 or dh.shape != (M, N // 2) or not dh.is_contiguous():
-        raise ValueError("dh must be dense [%d, %d], got %s" % (M, N // 2, tuple(dh.shape)))
+        x = dequantize_int8(x, out_dtype=dtype, stream=stream) if need_dw or kept is None else None
+    if not dh.is_contiguous() or (x is not None and not x.is_contiguous()):
+        raise ValueError("dh and x must be dense")
+    return _on(dev, _experts_grad, dh, x, ws, group_offsets, kept, with_h, b_transposed, need_dx, need_dw, G, M, N, K,
+               dev, stream)
+
+
+def _experts_grad(dh, x, ws, group_offsets, kept, with_h, b_transposed, need_dx, need_dw, G, M, N, K, dev,
+                  stream) -> SwigluGrad:
+    dtype, L, handle = dh.dtype, lib(), _stream_handle(stream, dev)
+    code = _OUT_CODES[dtype]
+    p, keep = _ptr_array([w.data_ptr() for w in ws])
     if kept is not None:
-        if kept.shape != (M, N):
-            raise ValueError("kept must be [%d, %d], got %s" % (M, N, tuple(kept.shape)))
-        dgu, h = swiglu_grad(dh, kept, True, stream) if with_h else (swiglu_grad(dh, kept, False, stream), None)
-    elif with_h:
-        raise ValueError("with_h reads h from kept")
+        dgu, h = _kept_grad(dh, N // 2, kept, with_h, M, N, dev, stream, handle)
     else:
-        h = None
-        dgu = _new((M, N), dtype, dev, stream)
-        p, keep = _ptr_array([w.data_ptr() for w in ws])
-        _check(_on(dev, lib().grouped_gemm_swiglu_grad, dh.data_ptr(), xv.data_ptr(), p, dgu.data_ptr(),
-                   group_offsets.data_ptr(), _OUT_CODES[dtype], 1 if b_transposed else 0, G, M, N, K,
-                   _stream_handle(stream, dev)), "grouped_gemm_swiglu_grad")
-        del keep
+        dgu, h = _new((M, N), dtype, dev, stream), None
+        _check(L.grouped_gemm_swiglu_grad(dh.data_ptr(), x.data_ptr(), p, dgu.data_ptr(), group_offsets.data_ptr(),
+                                          code, 1 if b_transposed else 0, G, M, N, K, handle),
+               "grouped_gemm_swiglu_grad")
     dx = dw = None
     if need_dx:
-        dx = grouped_gemm(dgu, ws, group_offsets, out=_new((M, K), dtype, dev, stream), stream=stream,
-                          b_transposed=not b_transposed)
+        dx = _new((M, K), dtype, dev, stream)
+        name = ("grouped_gemm_bf16" if code == OUT_BF16 else "grouped_gemm_fp16") + ("" if b_transposed else "_nt")
+        _check(getattr(L, name)(dgu.data_ptr(), p, dx.data_ptr(), group_offsets.data_ptr(), G, M, K, N, handle), name)
     if need_dw:
-        a, b = (dgu, xv) if b_transposed else (xv, dgu)
-        dw = grouped_gemm_wgrad(a, b, group_offsets, stream=stream)
+        rows, cols, a, b = (N, K, dgu, x) if b_transposed else (K, N, x, dgu)
+        dw = _new((G, rows, cols), dtype, dev, stream)
+        need, work = _tn_work(rows, cols, M, G, dev, stream)
+        _check(L.grouped_gemm_tn(a.data_ptr(), b.data_ptr(), dw.data_ptr(), group_offsets.data_ptr(), code, code, G,
+                                 rows, cols, M, None if work is None else work.data_ptr(), need, handle),
+               "grouped_gemm_tn")
+    del keep
     return SwigluGrad(dx, dw, h)
