@@ -79,8 +79,8 @@ bwg_status check_gated(const GatedCall& c) {
   if (c.dtype != BWG_OUT_BF16 && c.dtype != BWG_OUT_FP16) return BWG_ERR_INVALID_ARG;
   if (c.G < 0 || c.M < 0 || c.N < 0 || c.K < 0) return BWG_ERR_INVALID_ARG;
   if (c.G == 0 || c.M == 0 || c.N == 0) return BWG_OK;
+  if (c.M > kMaxSize || c.N > kMaxSize || c.K > kMaxSize) return BWG_ERR_UNSUPPORTED;
   if (c.N % 16 != 0) return BWG_ERR_ALIGNMENT;
-  // columns of kept codes and of gate's gradient are counted in ints
   const int d_cols = c.epi == kEpiSwigluGrad ? c.N : c.N / 2;
   if (c.d == nullptr || c.ldd < d_cols) return BWG_ERR_INVALID_ARG;
   if (!rows16(c.d, c.ldd)) return BWG_ERR_ALIGNMENT;

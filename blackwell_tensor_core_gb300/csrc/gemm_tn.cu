@@ -140,6 +140,7 @@ bwg_status check_tn(const TnCall& c) {
     return BWG_ERR_INVALID_ARG;
   if (c.G < 0 || c.M < 0 || c.N < 0 || c.rows < 0) return BWG_ERR_INVALID_ARG;
   if (c.G == 0 || c.M == 0 || c.N == 0) return BWG_OK;
+  if (c.M > kMaxSize || c.N > kMaxSize || c.rows > kMaxSize) return BWG_ERR_UNSUPPORTED;
   if (c.d == nullptr || c.ldd < c.N) return BWG_ERR_INVALID_ARG;
   const int oe = c.out_dtype == BWG_OUT_FP32 ? 4 : 2;
   if (!is_aligned(c.d, 16) || static_cast<long long>(c.ldd) * oe % 16 != 0) return BWG_ERR_ALIGNMENT;
@@ -168,7 +169,7 @@ bwg_status run_tn(const TnCall& c, cudaStream_t stream) {
   const int oe = c.out_dtype == BWG_OUT_FP32 ? 4 : 2;
   if (c.rows == 0) {
     const long long all = static_cast<long long>(c.G) * c.M;
-    if (all > 0x7fffffffLL) return BWG_ERR_UNSUPPORTED;
+    if (all > 0x7fffffffLL || static_cast<long long>(c.N) * oe > 0x7fffffffLL) return BWG_ERR_UNSUPPORTED;
     return runtime_status(launch_zero_fill(c.d, static_cast<int>(all), c.N, c.ldd, oe, stream));
   }
   const int n_tiles = ceil_div(c.N, kTileN);

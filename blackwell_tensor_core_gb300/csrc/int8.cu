@@ -425,6 +425,7 @@ bwg_status run_int8(bool back, const void* m, int dtype, int M, int N, int ld, i
                     cudaStream_t stream) {
   if (!known(dtype) || M < 0 || N < 0 || (parts != 1 && parts != 2) || N % parts != 0) return BWG_ERR_INVALID_ARG;
   if (M == 0 || N == 0) return BWG_OK;
+  if (N > kMaxSize) return BWG_ERR_UNSUPPORTED;
   if (m == nullptr || codes == nullptr || scales == nullptr || ld < N) return BWG_ERR_INVALID_ARG;
   if (!is_aligned(m, elt_bytes(dtype)) || !is_aligned(scales, 4)) return BWG_ERR_ALIGNMENT;
   Runtime rt;
@@ -469,8 +470,9 @@ bwg_status dequantize_int8(const void* codes, const float* scales, int parts, vo
 
 bwg_status swiglu_grad_int8(const void* dH, const void* codes, const float* scales, void* dGU, void* H, int dtype,
                             int M, int I, int lddh, int ldd, int ldh, void* stream) {
-  if ((dtype != BWG_OUT_BF16 && dtype != BWG_OUT_FP16) || M < 0 || I < 0 || I > 0x3fffffff) return BWG_ERR_INVALID_ARG;
+  if ((dtype != BWG_OUT_BF16 && dtype != BWG_OUT_FP16) || M < 0 || I < 0) return BWG_ERR_INVALID_ARG;
   if (M == 0 || I == 0) return BWG_OK;
+  if (I > kMaxSize / 2) return BWG_ERR_UNSUPPORTED;
   if (dH == nullptr || codes == nullptr || scales == nullptr || dGU == nullptr || lddh < I || ldd < 2 * I ||
       (H != nullptr && ldh < I))
     return BWG_ERR_INVALID_ARG;

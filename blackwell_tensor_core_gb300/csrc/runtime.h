@@ -41,6 +41,10 @@ inline bool runtime_map_2d(CUtensorMap* m, const void* ptr, CUtensorMapDataType 
   return runtime_map(m, ptr, dtype, 2, dims, &row_bytes, box, CU_TENSOR_MAP_SWIZZLE_128B);
 }
 
+// Largest rows, columns and depths that the tiled kernels take: rounding up to
+// tiles, and the first element past a tile, stay in an int.
+constexpr int kMaxSize = 0x7fffffff - 1024;
+
 inline bool is_aligned(const void* p, uintptr_t bytes) { return (reinterpret_cast<uintptr_t>(p) & (bytes - 1)) == 0; }
 
 // H = silu(X gate) * (X up) of at most kSmallMMaxM rows, arguments checked (see gemm_swiglu).

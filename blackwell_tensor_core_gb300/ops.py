@@ -909,6 +909,15 @@ def dequantize_int8(q: Int8Matrix, out_dtype: torch.dtype = torch.bfloat16, out:
     return out
 
 
+def _lead(t: torch.Tensor, name: str) -> int:
+    """Leading dimension of a matrix for the TMA engine: a single row keeps the
+    stride that it has, where that is one."""
+    ld = _rows(t, name, t.shape[0])
+    if t.shape[0] == 1 and ld < t.stride(0) <= _INT_MAX:
+        return t.stride(0)
+    return ld
+
+
 def _half(t: torch.Tensor, name: str) -> None:
     if t.dtype not in (torch.bfloat16, torch.float16):
         raise TypeError("%s must be bfloat16 or float16" % name)
@@ -932,7 +941,9 @@ def _gemm_tn(A, B, out, out_dtype, stream, b_transposed) -> torch.Tensor:
     dev = A.device
     _like(B, "B", A.dtype, dev)
     (K, M), N = A.shape, B.shape[1]
-    lda, ldb = _rows(A, "A", K), _rows(B, "B", K)
+    if B.shape[0] != K:
+        raise ValueError("inner dimensions differ: %s x %s" % (tuple(A.shape), tuple(B.shape)))
+    lda, ldb = _lead(A, "A"), _lead(B, "B")
     _fits("M or N", M, N)
     out, ldd = _fp4_out(out, out_dtype, M, N, dev, stream)
     need, work = _tn_work(M, N, K, 1, dev, stream)
@@ -975,7 +986,7 @@ def grouped_gemm_wgrad(A: torch.Tensor, B: torch.Tensor, group_offsets: torch.Te
 def _gated_weight(w: torch.Tensor, dtype, dev, K: int, b_transposed: bool) -> tuple[int, int]:
     """(N, leading dimension) of a gated block's weight [K, N], or [N, K]."""
     _like(w, "w", dtype, dev)
-    ldw = _rows(w, "w", w.shape[0])
+    ldw = _lead(w, "w")
     N, K2 = w.shape if b_transposed else (w.shape[1], w.shape[0])
     if K2 != K:
         raise ValueError("inner dimensions differ: x has %d columns, w %s" % (K, tuple(w.shape)))
@@ -994,7 +1005,7 @@ def gemm_swiglu(x: torch.Tensor, w: torch.Tensor, out: torch.Tensor | None = Non
     _half(x, "x")
     dev, dtype = x.device, x.dtype
     M, K = x.shape
-    ldx = _rows(x, "x", M)
+    ldx = _lead(x, "x")
     N, ldw = _gated_weight(w, dtype, dev, K, b_transposed)
     out, ldh = _out_rows(out, M, N // 2, dtype, dev, stream)
     kept = _new_int8(M, N, 2, dev, stream) if keep_int8 else None
@@ -1049,7 +1060,7 @@ def swiglu_grad(dh: torch.Tensor, kept: Int8Matrix, with_h: bool = False, stream
     dev = dh.device
     if kept.codes.device != dev or dh.shape != (M, N // 2):
         raise ValueError("dh must be [%d, %d] on %s" % (M, N // 2, kept.device))
-    dgu, h = _on(dev, _kept_grad, dh, _rows(dh, "dh", M), kept, with_h, M, N, dev, stream,
+    dgu, h = _on(dev, _kept_grad, dh, _lead(dh, "dh"), kept, with_h, M, N, dev, stream,
                  _stream_handle(stream, dev))
     return (dgu, h) if with_h else dgu
 
@@ -1087,10 +1098,10 @@ def gemm_swiglu_grad(dh: torch.Tensor, x, w: torch.Tensor, kept: Int8Matrix | No
     dev = dh.device
     N, ldw = _gated_weight(w, dh.dtype, dev, x.shape[1], b_transposed)
     M, K = _block_operands(dh, x, kept, with_h, N)
-    lddh = _rows(dh, "dh", M)
+    lddh = _lead(dh, "dh")
     if isinstance(x, Int8Matrix):
         x = dequantize_int8(x, out_dtype=dh.dtype, stream=stream) if need_dw or kept is None else None
-    ldx = _rows(x, "x", M) if x is not None else 0
+    ldx = _lead(x, "x") if x is not None else 0
     return _on(dev, _block_grad, dh, lddh, x, ldx, w, ldw, kept, with_h, b_transposed, need_dx, need_dw, M, N, K, dev,
                stream)
 
