@@ -28,6 +28,7 @@
 // in time and reports a fault word instead of hanging.
 #pragma once
 
+#include "launch.h"
 #include "layout.h"
 #include "params.h"
 #include "ptx.cuh"
@@ -350,6 +351,8 @@ __device__ void gemm_body(const PT& P, const GemmParams& p) {
   static_assert(!DYN || (CG == 2 && MC == 1 && (NC == 2 || CH || EPI >= kEpiSwigluKeep)), "dynamic scheduling: 12-warp pairs");
   static_assert(!TN || (CG == 2 && MC == 1 && !SW && !GROUPED), "transposed A runs on plain pairs");
   static_assert(!CH || (TN && NC == 1), "sums in registers: one consumer, transposed A");
+  // launched while the work before may still be running (launch_behind)
+  constexpr bool kBehind = TN || EPI >= kEpiSwigluKeep || (SW && !GROUPED);
   constexpr bool kTables = GROUPED || TN;              // row ranges of groups in shared memory
   // two epilogue warpgroups: one a consumer, or (kHalves) one for each half of
   // the columns of a single consumer's tile
@@ -425,6 +428,7 @@ __device__ void gemm_body(const PT& P, const GemmParams& p) {
   int* t_hi = t_lo + kMaxGroupsPerLaunch;
   if constexpr (kTables) {
     if (warp == 2) {  // a warp with no set-up duty
+      if constexpr (kBehind) grid_dependency_wait();
       if (TN && p.group_offsets == nullptr) {  // one group of all rows
         if (lane == 0) {
           t_lo[0] = 0;
@@ -452,6 +456,11 @@ __device__ void gemm_body(const PT& P, const GemmParams& p) {
   else
     __syncthreads();
   tc_fence_after();
+  if constexpr (kBehind) {
+    grid_dependency_wait();
+    // every CTA of a static grid is resident by now; a claimed grid's are not
+    if constexpr (!DYN) grid_dependents_launch();
+  }
   const uint32_t tmem_base = ld_shared_u32(tmem_slot);
 
   const int first = static_cast<int>((CG == 2) ? cluster_id_x() : blockIdx.x);
@@ -1340,6 +1349,13 @@ template <class K, class P>
 cudaError_t launch_two_consumer(K kernel, const P& p, int grid, size_t smem, cudaStream_t s) {
   if (!two_consumer_regs_ok(kernel)) return cudaErrorLaunchOutOfResources;
   return launch_cluster(kernel, p, 2, grid, smem, s, kThreads2C);
+}
+
+// The same for kernels that wait for the work before by themselves (kBehind).
+template <class P>
+cudaError_t launch_pair_behind(void (*kernel)(P), const P& p, int grid, size_t smem, cudaStream_t s) {
+  if (!two_consumer_regs_ok(kernel)) return cudaErrorLaunchOutOfResources;
+  return launch_behind(kernel, static_cast<unsigned>(grid), kThreads2C, smem, s, 2, p);
 }
 
 inline int occupancy_clusters(const void* fn, int cg, size_t smem, int threads = kThreads) {

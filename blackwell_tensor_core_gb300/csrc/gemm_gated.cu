@@ -35,15 +35,15 @@ __global__ void __launch_bounds__(kThreads2C, 1) gated_grouped_kernel(const __gr
 }  // namespace
 
 cudaError_t launch_gated_dense(const DenseGatedParams& p, int epi, bool two, int grid, size_t smem, cudaStream_t s) {
-  if (epi == kEpiSwigluKeep) return launch_two_consumer(gated_wide_kernel<kEpiSwigluKeep>, p, grid, smem, s);
-  if (epi == kEpiSwigluGrad) return launch_two_consumer(gated_wide_kernel<kEpiSwigluGrad>, p, grid, smem, s);
-  return two ? launch_two_consumer(gated_2c_kernel, p, grid, smem, s)
-             : launch_two_consumer(gated_wide_kernel<kEpiSwiglu>, p, grid, smem, s);
+  if (epi == kEpiSwigluKeep) return launch_pair_behind(gated_wide_kernel<kEpiSwigluKeep>, p, grid, smem, s);
+  if (epi == kEpiSwigluGrad) return launch_pair_behind(gated_wide_kernel<kEpiSwigluGrad>, p, grid, smem, s);
+  return two ? launch_pair_behind(gated_2c_kernel, p, grid, smem, s)
+             : launch_pair_behind(gated_wide_kernel<kEpiSwiglu>, p, grid, smem, s);
 }
 
 cudaError_t launch_gated_grouped(const GroupedGatedParams& p, int epi, int grid, size_t smem, cudaStream_t s) {
-  return epi == kEpiSwigluKeep ? launch_two_consumer(gated_grouped_kernel<kEpiSwigluKeep>, p, grid, smem, s)
-                               : launch_two_consumer(gated_grouped_kernel<kEpiSwigluGrad>, p, grid, smem, s);
+  return epi == kEpiSwigluKeep ? launch_pair_behind(gated_grouped_kernel<kEpiSwigluKeep>, p, grid, smem, s)
+                               : launch_pair_behind(gated_grouped_kernel<kEpiSwigluGrad>, p, grid, smem, s);
 }
 
 cudaError_t set_gated_attributes(size_t smem) {

@@ -55,6 +55,7 @@
 // of the maps), and silu(gate) * up is stored.  Threads of up's columns hand
 // their sums to those of gate's through shared memory, 16 rows at a time; in the
 // cluster split every thread sums gate and up of its rows itself.
+#include "launch.h"
 #include "layout.h"
 #include "params.h"
 #include "ptx.cuh"
@@ -285,6 +286,10 @@ __global__ void __launch_bounds__(kThreads, 1) small_m_kernel(const __grid_const
   if (threadIdx.x == 0) {
     producer.pol_b = (p.l2hint & 2) ? l2_policy_evict_first() : l2_policy_evict_normal();
     producer.pol_a = (p.l2hint & 1) ? l2_policy_evict_last() : l2_policy_evict_normal();
+  }
+  if constexpr (SW) {  // launched while the work before may still be running
+    grid_dependency_wait();
+    grid_dependents_launch();
   }
   if (threadIdx.x == 0) producer.issue(S, &aborted);
   if (warp == 1) {
@@ -703,12 +708,11 @@ __global__ void zero_fill_kernel(uint8_t* d, int rows, int row_bytes, size_t ld_
 }  // namespace
 
 cudaError_t launch_small_m(const SmallMParams& p, int grid, size_t smem, cudaStream_t s) {
-  const bool gated = p.gated != 0;
+  if (p.gated)
+    return launch_behind(small_m_kernel<true>, static_cast<unsigned>(grid), kThreads, smem, s,
+                         p.split > 1 ? static_cast<unsigned>(p.split) : 1u, p);
   if (p.split <= 1) {
-    if (gated)
-      small_m_kernel<true><<<grid, kThreads, smem, s>>>(p);
-    else
-      small_m_kernel<false><<<grid, kThreads, smem, s>>>(p);
+    small_m_kernel<false><<<grid, kThreads, smem, s>>>(p);
     return cudaGetLastError();
   }
   cudaLaunchConfig_t cfg = {};
@@ -723,7 +727,7 @@ cudaError_t launch_small_m(const SmallMParams& p, int grid, size_t smem, cudaStr
   attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return gated ? cudaLaunchKernelEx(&cfg, small_m_kernel<true>, p) : cudaLaunchKernelEx(&cfg, small_m_kernel<false>, p);
+  return cudaLaunchKernelEx(&cfg, small_m_kernel<false>, p);
 }
 
 int max_active_clusters_small_m(int cluster, size_t smem) {

@@ -25,10 +25,21 @@ __global__ void __launch_bounds__(kThreads2C, 1) gemm_tn_joined_kernel(const __g
 }
 
 // D[g] = the sum of its slices' planes, FP32 [G * splits][M][pitch], in order.
+struct JoinParams {
+  const float* planes;
+  void* d;
+  int M, N, pitch, splits, ldd;
+  long long rows;  // of all groups' D
+};
+
 template <int OUT>
-__global__ void __launch_bounds__(256) tn_join_kernel(const float* planes, void* d, int M, int N, int pitch, int splits,
-                                                      long long rows, int ldd) {
-  const int quads = pitch / 4;
+__global__ void __launch_bounds__(256) tn_join_kernel(const __grid_constant__ JoinParams p) {
+  grid_dependency_wait();
+  grid_dependents_launch();
+  const float* const planes = p.planes;
+  void* const d = p.d;
+  const int M = p.M, N = p.N, pitch = p.pitch, splits = p.splits, ldd = p.ldd, quads = pitch / 4;
+  const long long rows = p.rows;
   for (long long i = blockIdx.x * 256LL + threadIdx.x; i < rows * quads; i += gridDim.x * 256LL) {
     const long long row = i / quads;  // of all groups' rows of D
     const int col = static_cast<int>(i - row * quads) * 4;
@@ -66,10 +77,10 @@ __global__ void __launch_bounds__(256) tn_join_kernel(const float* planes, void*
 
 cudaError_t launch_tn(const TnParams& p, bool joined, bool dynamic, int grid, size_t smem, cudaStream_t s) {
   if (joined)
-    return dynamic ? launch_two_consumer(gemm_tn_joined_kernel<true>, p, grid, smem, s)
-                   : launch_two_consumer(gemm_tn_joined_kernel<false>, p, grid, smem, s);
-  return dynamic ? launch_two_consumer(gemm_tn_2c_kernel<true>, p, grid, smem, s)
-                 : launch_two_consumer(gemm_tn_2c_kernel<false>, p, grid, smem, s);
+    return dynamic ? launch_pair_behind(gemm_tn_joined_kernel<true>, p, grid, smem, s)
+                   : launch_pair_behind(gemm_tn_joined_kernel<false>, p, grid, smem, s);
+  return dynamic ? launch_pair_behind(gemm_tn_2c_kernel<true>, p, grid, smem, s)
+                 : launch_pair_behind(gemm_tn_2c_kernel<false>, p, grid, smem, s);
 }
 
 cudaError_t set_tn_attributes(size_t smem) {
@@ -242,13 +253,12 @@ bwg_status run_tn(const TnCall& c, cudaStream_t stream) {
   const long long rows = static_cast<long long>(c.G) * c.M;
   const unsigned grid =
       static_cast<unsigned>(std::min<long long>((rows * (pitch / 4) + 255) / 256, 16LL * rt.sm_count));
-  if (c.out_dtype == BWG_OUT_FP32)
-    tn_join_kernel<kOutF32><<<grid, 256, 0, stream>>>(c.workspace, c.d, c.M, c.N, pitch, splits, rows, c.ldd);
-  else if (c.out_dtype == BWG_OUT_BF16)
-    tn_join_kernel<kOutBF16><<<grid, 256, 0, stream>>>(c.workspace, c.d, c.M, c.N, pitch, splits, rows, c.ldd);
-  else
-    tn_join_kernel<kOutF16><<<grid, 256, 0, stream>>>(c.workspace, c.d, c.M, c.N, pitch, splits, rows, c.ldd);
-  return runtime_status(cudaGetLastError());
+  const JoinParams j{c.workspace, c.d, c.M, c.N, pitch, splits, c.ldd, rows};
+  return runtime_status(
+      launch_behind(c.out_dtype == BWG_OUT_FP32   ? tn_join_kernel<kOutF32>
+                    : c.out_dtype == BWG_OUT_BF16 ? tn_join_kernel<kOutBF16>
+                                                  : tn_join_kernel<kOutF16>,
+                    grid, 256, 0, stream, 1, j));
 }
 
 }  // namespace

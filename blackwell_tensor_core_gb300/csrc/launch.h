@@ -63,6 +63,28 @@ __device__ __forceinline__ uint16_t ld_global_once(const uint16_t* p) {
   return v;
 }
 
+// Launch of a grid of clusters whose kernel waits so, for kernels that take their
+// parameters as one block.
+template <class P>
+cudaError_t launch_behind(void (*kernel)(P), unsigned grid, unsigned threads, size_t smem, cudaStream_t s,
+                          unsigned cluster, const P& p) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid, 1, 1);
+  cfg.blockDim = dim3(threads, 1, 1);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = cluster;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = cluster > 1 ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, kernel, p);
+}
+
 template <class... Params, class... Args>
 cudaError_t launch_overlapped(void (*kernel)(Params...), unsigned grid, unsigned threads, size_t smem, cudaStream_t s,
                               unsigned cluster, Args&&... args) {
