@@ -184,9 +184,14 @@ bwg_status run_tn(const TnCall& c, cudaStream_t stream) {
     return runtime_status(launch_zero_fill(c.d, static_cast<int>(all), c.N, c.ldd, oe, stream));
   }
   const int n_tiles = ceil_div(c.N, kTileN);
-  // FP32 results keep what TMEM's sums lose; other results are 16 bits wide
+  // FP32 results keep what TMEM's sums lose (nothing over kChunkBlocks k-blocks);
+  // other results are 16 bits wide.  With both operands MN-major the 256x256
+  // tiles of joined sums run at 1.5 times the cycles of a K-major A (8192^3: 1.25
+  // M cycles against 0.95 M, with or without joining), 512x256 tiles at the same
+  // (0.92 M): shared memory serves the operands' reads and the ring's writes.
   const long long tiles_2c = static_cast<long long>(c.G) * ceil_div(c.M, 4 * kRowsPerCta) * n_tiles;
-  const bool joined = c.out_dtype == BWG_OUT_FP32 || tiles_2c < rt.pairs_2c;
+  const bool exact = c.out_dtype == BWG_OUT_FP32 && (c.offsets != nullptr || c.rows > kChunkBlocks * kBK);
+  const bool joined = exact || tiles_2c < rt.pairs_2c;
   const int splits = joined ? tn_splits(c.M, c.N, c.rows, c.G, rt.pairs) : 1;
   const int pitch = tn_pitch(c.N);
   if (splits > 1) {
