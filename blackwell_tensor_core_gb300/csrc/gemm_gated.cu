@@ -197,9 +197,8 @@ bwg_status run_gated_dense(const GatedCall& c, const Runtime& rt, cudaStream_t s
   p.num_m_tiles = (c.M + tile_m - 1) / tile_m;
   const long long tiles = static_cast<long long>(p.num_m_tiles) * n_tiles;
   if (tiles > 0x3fffffff) return BWG_ERR_UNSUPPORTED;
-  // with pairs for all their halves, few tiles are cut in two
-  const int all = two ? rt.pairs_2c : rt.pairs;
-  p.workers = static_cast<int>(2 * tiles <= all ? 2 * tiles : std::min<long long>(tiles, all));
+  // with pairs for all their parts, few tiles are cut
+  p.workers = static_cast<int>(std::min<long long>(tiles * (two ? 4 : 2), two ? rt.pairs_2c : rt.pairs));
   return runtime_status(launch_gated_dense(p, c.epi, two, 2 * p.workers, smem, stream));
 }
 

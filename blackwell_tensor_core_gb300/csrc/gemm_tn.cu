@@ -108,26 +108,47 @@ struct TnCall {
 
 int ceil_div(int a, int b) { return (a + b - 1) / b; }
 
-// Slices of each group's rows: where D has few tiles, pairs would stand idle.
-// Estimated in k-blocks of a 256x256 tile (0.27 us): a unit costs its blocks and
-// kUnit for filling the ring and storing the tile, the join of S > 1 planes a
-// launch and its traffic.
-int tn_splits(int M, int N, int rows, int G, int pairs) {
-  constexpr double kUnit = 10, kJoin = 12;
-  const double tiles = static_cast<double>(G) * ceil_div(M, 256) * ceil_div(N, 256);
+// How a product is cut up: tiles of 256x256 whose sums are joined in registers, or
+// of 512x256 (the faster for each element, see gemm_body), and slices of each
+// group's rows where D has few tiles.
+struct TnPlan {
+  bool joined;
+  int splits;
+};
+
+// Waves of T tiles on C pairs, the last one cut as the schedule cuts it.
+double tn_waves(long long T, int C, int nc) {
+  const int workers = static_cast<int>(std::min<long long>(C, T * (nc == 2 ? 4 : 2)));
+  const long long full = T / workers, R = T % workers;
+  if (R == 0) return static_cast<double>(full);
+  auto part = [&](int f, double cost) { return static_cast<double>((f * R + workers - 1) / workers) * cost; };
+  const double last = nc == 2 ? std::min(part(2, kCostHalf2 / 1000.0), part(4, kCostQuarter2 / 1000.0))
+                              : part(2, kCostHalf1 / 1000.0);
+  return static_cast<double>(full) + std::min(1.0, last);
+}
+
+// The cheapest by an estimate in us: k-blocks of a tile at the rates measured on
+// 8192^3, filling the ring and storing a tile, and for slices a launch and 8 bytes
+// an element of every plane at 6 TB/s.  20011 rows of 1000 x 1416: 256x256 tiles in
+// one slice 158 us, three slices 60, 512x256 tiles in six 54.
+TnPlan tn_plan(int M, int N, int rows, int G, int out_dtype, int pairs, int pairs_2c) {
+  // FP32 results keep what TMEM's sums lose (nothing over kChunkBlocks k-blocks)
+  const bool exact = out_dtype == BWG_OUT_FP32 && rows > kChunkBlocks * kBK;
   const double blocks = static_cast<double>(ceil_div(rows, kBK)) / G;
-  if (tiles * 2 > pairs * 3) return 1;  // two waves, a slice would save less than it costs
-  int best = 1;
+  TnPlan best{true, 1};
   double least = 0;
-  for (int s = 1; s <= 32 && (s == 1 || blocks >= 8.0 * s); ++s) {
-    const double units = tiles * s;
-    const double waves = static_cast<double>((static_cast<long long>(units) + pairs - 1) / pairs);
-    double t = waves * (blocks / s + kUnit);
-    // 8 bytes an element of every plane at 6 TB/s
-    if (s > 1) t += kJoin + static_cast<double>(G) * s * M * N * 8 / 6.0e6 / 0.27;
-    if (s == 1 || t < least) {
-      least = t;
-      best = s;
+  for (int nc = 1; nc <= (exact ? 1 : 2); ++nc) {
+    const long long tiles =
+        static_cast<long long>(G) * ceil_div(M, 2 * kRowsPerCta * nc) * ceil_div(N, kTileN);
+    const int all = nc == 2 ? pairs_2c : pairs;
+    for (int s : {1, 2, 3, 4, 5, 6, 8, 10, 12, 16, 20, 24, 32}) {
+      if (s > 1 && (blocks < 8.0 * s || tiles >= 2 * all)) break;
+      double t = tn_waves(tiles * s, all, nc) * (blocks / s * (nc == 2 ? 0.56 : 0.40) + (nc == 2 ? 4.5 : 3.0));
+      if (s > 1) t += 3.0 + static_cast<double>(G) * s * M * N * 8 / 6.0e6;
+      if ((nc == 1 && s == 1) || t < least) {
+        least = t;
+        best = TnPlan{nc == 1, s};
+      }
     }
   }
   return best;
@@ -135,9 +156,8 @@ int tn_splits(int M, int N, int rows, int G, int pairs) {
 
 int tn_pitch(int N) { return (N + 3) / 4 * 4; }
 
-long long tn_workspace(int M, int N, int rows, int G, int pairs) {
-  const int s = tn_splits(M, N, rows, G, pairs);
-  return s == 1 ? 0 : 4LL * G * s * M * tn_pitch(N);
+long long tn_workspace(const TnPlan& plan, int M, int N, int G) {
+  return plan.splits == 1 ? 0 : 4LL * G * plan.splits * M * tn_pitch(N);
 }
 
 CUtensorMapDataType map_type(int dtype) {
@@ -184,18 +204,12 @@ bwg_status run_tn(const TnCall& c, cudaStream_t stream) {
     return runtime_status(launch_zero_fill(c.d, static_cast<int>(all), c.N, c.ldd, oe, stream));
   }
   const int n_tiles = ceil_div(c.N, kTileN);
-  // FP32 results keep what TMEM's sums lose (nothing over kChunkBlocks k-blocks);
-  // other results are 16 bits wide.  With both operands MN-major the 256x256
-  // tiles of joined sums run at 1.5 times the cycles of a K-major A (8192^3: 1.25
-  // M cycles against 0.95 M, with or without joining), 512x256 tiles at the same
-  // (0.92 M): shared memory serves the operands' reads and the ring's writes.
-  const long long tiles_2c = static_cast<long long>(c.G) * ceil_div(c.M, 4 * kRowsPerCta) * n_tiles;
-  const bool exact = c.out_dtype == BWG_OUT_FP32 && (c.offsets != nullptr || c.rows > kChunkBlocks * kBK);
-  const bool joined = exact || tiles_2c < rt.pairs_2c;
-  const int splits = joined ? tn_splits(c.M, c.N, c.rows, c.G, rt.pairs) : 1;
+  const TnPlan plan = tn_plan(c.M, c.N, c.rows, c.G, c.out_dtype, rt.pairs, rt.pairs_2c);
+  const bool joined = plan.joined;
+  const int splits = plan.splits;
   const int pitch = tn_pitch(c.N);
   if (splits > 1) {
-    if (c.workspace == nullptr || c.workspace_bytes < tn_workspace(c.M, c.N, c.rows, c.G, rt.pairs))
+    if (c.workspace == nullptr || c.workspace_bytes < tn_workspace(plan, c.M, c.N, c.G))
       return BWG_ERR_INVALID_ARG;
     if (!is_aligned(c.workspace, 16)) return BWG_ERR_ALIGNMENT;
   }
@@ -245,9 +259,8 @@ bwg_status run_tn(const TnCall& c, cudaStream_t stream) {
     p.G_total = c.G;
     const long long tiles = static_cast<long long>(p.G) * splits * p.num_m_tiles * n_tiles;
     if (tiles > 0x0fffffff) return BWG_ERR_UNSUPPORTED;
-    // with pairs for all their halves, few tiles are cut in two
-    const int all = joined ? rt.pairs : rt.pairs_2c;
-    p.workers = static_cast<int>(2 * tiles <= all ? 2 * tiles : std::min<long long>(tiles, all));
+    // with pairs for all their parts, few tiles are cut
+    p.workers = static_cast<int>(std::min<long long>(tiles * (joined ? 2 : 4), joined ? rt.pairs : rt.pairs_2c));
     // groups differ in length: units are claimed at run time
     const bool dynamic = c.offsets != nullptr;
     const long long pairs = dynamic ? tiles + 3LL * p.workers : p.workers;
@@ -271,10 +284,11 @@ bwg_status run_tn(const TnCall& c, cudaStream_t stream) {
 
 extern "C" {
 
-long long bwg_tn_workspace(int M, int N, int K_total, int G) {
-  if (M < 1 || N < 1 || K_total < 1 || G < 1) return 0;
+long long bwg_tn_workspace(int M, int N, int K_total, int G, int out_dtype) {
+  if (M < 1 || N < 1 || K_total < 1 || G < 1 || M > kMaxSize || N > kMaxSize || K_total > kMaxSize) return 0;
   Runtime rt;
-  return runtime_device(&rt) == BWG_OK ? tn_workspace(M, N, K_total, G, rt.pairs) : 0;
+  if (runtime_device(&rt) != BWG_OK) return 0;
+  return tn_workspace(tn_plan(M, N, K_total, G, out_dtype, rt.pairs, rt.pairs_2c), M, N, G);
 }
 
 bwg_status gemm_tn(const void* A, const void* B, void* D, int dtype, int out_dtype, int M, int N, int K, int lda,

@@ -158,7 +158,7 @@ def lib() -> ctypes.CDLL:
             L.bwg_fp4_kernel.restype = i
             L.bwg_idesc_fp4.argtypes = [i, i, i, i]
             L.bwg_idesc_fp4.restype = u32
-            L.bwg_tn_workspace.argtypes = [i, i, i, i]
+            L.bwg_tn_workspace.argtypes = [i, i, i, i, i]
             L.bwg_tn_workspace.restype = ctypes.c_longlong
             L.bwg_version.argtypes = []
             L.bwg_version.restype = ctypes.c_char_p
@@ -928,9 +928,9 @@ def _like(t: torch.Tensor, name: str, dtype, dev) -> None:
         raise ValueError("%s must be a %s tensor on %s" % (name, dtype, dev))
 
 
-def _tn_work(M: int, N: int, rows: int, G: int, dev, stream) -> tuple:
+def _tn_work(M: int, N: int, rows: int, G: int, out_code: int, dev, stream) -> tuple:
     """(bytes, tensor or None) of the workspace of a product with transposed A."""
-    need = _on(dev, lib().bwg_tn_workspace, M, N, rows, G)
+    need = _on(dev, lib().bwg_tn_workspace, M, N, rows, G, out_code)
     return need, _new((need,), torch.uint8, dev, stream) if need > 0 else None
 
 
@@ -946,7 +946,7 @@ def _gemm_tn(A, B, out, out_dtype, stream, b_transposed) -> torch.Tensor:
     lda, ldb = _lead(A, "A"), _lead(B, "B")
     _fits("M or N", M, N)
     out, ldd = _fp4_out(out, out_dtype, M, N, dev, stream)
-    need, work = _tn_work(M, N, K, 1, dev, stream)
+    need, work = _tn_work(M, N, K, 1, _OUT_CODES[out.dtype], dev, stream)
     _check(_on(dev, lib().gemm_tn, A.data_ptr(), B.data_ptr(), out.data_ptr(), _OUT_CODES[A.dtype],
                _OUT_CODES[out.dtype], M, N, K, lda, ldb, ldd, None if work is None else work.data_ptr(), need,
                _stream_handle(stream, dev)), "gemm_tn")
@@ -976,7 +976,7 @@ def grouped_gemm_wgrad(A: torch.Tensor, B: torch.Tensor, group_offsets: torch.Te
         raise ValueError("out must be a dense [%d, %d, %d] tensor on %s" % (G, M, N, dev))
     if out.dtype not in _OUT_CODES:
         raise TypeError("output dtype must be bfloat16, float16 or float32")
-    need, work = _tn_work(M, N, rows, G, dev, stream)
+    need, work = _tn_work(M, N, rows, G, _OUT_CODES[out.dtype], dev, stream)
     _check(_on(dev, lib().grouped_gemm_tn, A.data_ptr(), B.data_ptr(), out.data_ptr(), group_offsets.data_ptr(),
                _OUT_CODES[A.dtype], _OUT_CODES[out.dtype], G, M, N, rows, None if work is None else work.data_ptr(),
                need, _stream_handle(stream, dev)), "grouped_gemm_tn")
@@ -1124,7 +1124,7 @@ def _block_grad(dh, lddh, x, ldx, w, ldw, kept, with_h, b_transposed, need_dx, n
     if need_dw:
         rows, cols, a, lda, b, ldb = (N, K, dgu, N, x, ldx) if b_transposed else (K, N, x, ldx, dgu, N)
         dw = _new((rows, cols), dtype, dev, stream)
-        need, work = _tn_work(rows, cols, M, 1, dev, stream)
+        need, work = _tn_work(rows, cols, M, 1, code, dev, stream)
         _check(L.gemm_tn(a.data_ptr(), b.data_ptr(), dw.data_ptr(), code, code, rows, cols, M, lda, ldb, cols,
                          None if work is None else work.data_ptr(), need, handle), "gemm_tn")
     return SwigluGrad(dx, dw, h)
@@ -1177,7 +1177,7 @@ def _experts_grad(dh, x, ws, group_offsets, kept, with_h, b_transposed, need_dx,
     if need_dw:
         rows, cols, a, b = (N, K, dgu, x) if b_transposed else (K, N, x, dgu)
         dw = _new((G, rows, cols), dtype, dev, stream)
-        need, work = _tn_work(rows, cols, M, G, dev, stream)
+        need, work = _tn_work(rows, cols, M, G, code, dev, stream)
         _check(L.grouped_gemm_tn(a.data_ptr(), b.data_ptr(), dw.data_ptr(), group_offsets.data_ptr(), code, code, G,
                                  rows, cols, M, None if work is None else work.data_ptr(), need, handle),
                "grouped_gemm_tn")

@@ -395,8 +395,8 @@ bwg_status swiglu_grad_int8(const void* dH, const void* codes, const float* scal
  *   and B [K_total, N] (all dense, M and N multiples of 8), D [G, M, N]; zeros for a
  *   group without rows.  group_offsets as for grouped_gemm_bf16.
  * Where D has few tiles the rows are shared out over more of the GPU and the
- * shares' sums joined from `workspace`: at least bwg_tn_workspace(M, N, K, G)
- * bytes (0: none is used; G = 1 for gemm_tn), 16-byte aligned device memory that
+ * shares' sums joined from `workspace`: at least bwg_tn_workspace(M, N, K, G,
+ * out_dtype) bytes (0: none is used; G = 1 for gemm_tn), 16-byte aligned device memory that
  * nothing else touches until the call's work is done, BWG_ERR_INVALID_ARG without.
  * The sums' order is fixed: equal calls on one kind of GPU give equal results.
  * FP32 results are sums of 512 rows each, joined with rounding to nearest: a sum
@@ -407,7 +407,7 @@ bwg_status gemm_tn(const void* A, const void* B, void* D, int dtype, int out_dty
 bwg_status grouped_gemm_tn(const void* A, const void* B, void* D, const int* group_offsets, int dtype, int out_dtype,
                            int G, int M, int N, int K_total, void* workspace, long long workspace_bytes,
                            void* stream);
-long long bwg_tn_workspace(int M, int N, int K_total, int G);
+long long bwg_tn_workspace(int M, int N, int K_total, int G, int out_dtype);
 
 /*
  * Synchronises `stream`, then reads and clears the device error word of the
