@@ -5,9 +5,10 @@
 The router's choices are sorted by expert, the tokens' rows dispatched into that
 order, multiplied by their experts' weights (FC1 with SwiGLU, then FC2) and
 combined back with the router's weights.  With the experts in 4 bits each
-product's input rows are quantised on the way.  The backward pass shown is that
-of a layer with frozen experts: gradients of the tokens and of the router's
-weights through a linear expert.
+product's input rows are quantised on the way.  Two backward passes: that of the
+whole layer in training, which keeps what it needs in 8 bits and gives the
+gradients of the tokens, of the router's weights and of both experts' weights;
+and that of a layer with frozen linear experts.
 """
 import argparse
 import os
@@ -62,6 +63,27 @@ def layer_fp4(x, ids, weights, q1, q2, fmt, x_scale=None, h_scale=None):
     return ops.moe_combine(ops.grouped_gemm_fp4(h, q2), r, weights)
 
 
+def training_forward(x, ids, weights, w1, w2):
+    """layer_bf16's y, and what training_backward needs of it: the routing, and in 8
+    bits the routed rows, FC1's gate and up and FC2's rows.  Every token's pairs
+    have an expert here; rows without one would have to be cut off first."""
+    r = ops.moe_sort(ids, len(w1))
+    rows = ops.moe_dispatch(x, r)
+    h, gate_up = ops.grouped_gemm(rows, w1, r.offsets, swiglu=True, keep_int8=True)
+    out = ops.grouped_gemm(h, w2, r.offsets)
+    return ops.moe_combine(out, r, weights), (r, ops.quantize_int8(rows), gate_up, ops.quantize_int8(out))
+
+
+def training_backward(kept, weights, w1, w2, d_y):
+    """(d_x, d_weights, d_w1 [experts, H, 2 I], d_w2 [experts, I, H])."""
+    r, rows, gate_up, out = kept
+    d_out, d_weights = ops.moe_combine_grad(d_y, ops.dequantize_int8(out), r, weights)
+    d_h = ops.grouped_gemm(d_out, w2, r.offsets, b_transposed=True)
+    g = ops.grouped_gemm_swiglu_grad(d_h, rows, w1, r.offsets, kept=gate_up, with_h=True)
+    d_w2 = ops.grouped_gemm_wgrad(g.h, d_out, r.offsets)
+    return ops.moe_dispatch_grad(g.dx, r), d_weights, g.dw, d_w2
+
+
 def linear_layer_backward(x, ids, weights, w, d_y):
     """y = combine(rows W): (y, d_x, d_weights) for frozen experts W [H, H]."""
     r = ops.moe_sort(ids, len(w))
@@ -108,6 +130,11 @@ def main():
         err = float((y4.float() - y.float()).norm() / y.float().norm())
         print("%s experts: %8.1f us, relative difference from bf16 %.3f" % (
             fmt, timed(lambda: layer_fp4(x, ids, weights, q1, q2, fmt, *scales)), err))
+    def step():
+        _, kept = training_forward(x, ids, weights, w1, w2)
+        return training_backward(kept, weights, w1, w2, x)
+
+    print("bf16 experts, forward and backward: %8.1f us" % timed(step))
     w = [m[:, :a.hidden].contiguous() for m in w1] if 2 * a.inner >= a.hidden else None
     if w is not None:
         print("linear experts, forward and backward: %8.1f us" % timed(lambda: linear_layer_backward(x, ids, weights, w, x)))
