@@ -352,8 +352,8 @@ def grouped_gemm(A: torch.Tensor, Bs: list, group_offsets: torch.Tensor,
 
 
 def _ptr_array(ptrs):
-    arr = (ctypes.c_void_p * max(len(ptrs), 1))(*[ctypes.c_void_p(p) for p in ptrs])
-    return ctypes.cast(arr, ctypes.POINTER(ctypes.c_void_p)), arr
+    arr = (ctypes.c_void_p * max(len(ptrs), 1))(*ptrs)
+    return arr, arr
 
 
 def grouped_gemm_bf16(A_ptr: int, B_ptrs: list, D_ptr: int, offsets_ptr: int, G: int, M_total: int,
