@@ -677,8 +677,13 @@ __global__ void __launch_bounds__(kThreads, 1) small_m_kernel(const __grid_const
     }
     // The CTA may exit once the TMA stores have read the staging tile; their
     // global writes complete on their own before the grid is done.
+    // (A kernel launched behind this one waits for the grid, so the gated form
+    // sees its stores through.)
     if (store_thread) {
-      bulk_wait_group_read<0>();
+      if constexpr (SW)
+        bulk_wait_group<0>();
+      else
+        bulk_wait_group_read<0>();
       if (trace != nullptr) trace[3] = globaltimer_ns();
     }
     __syncwarp();

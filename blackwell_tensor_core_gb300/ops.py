@@ -1068,6 +1068,8 @@ def swiglu_grad(dh: torch.Tensor, kept: Int8Matrix, with_h: bool = False, stream
 def _block_operands(dh, x, kept, with_h: bool, N: int) -> tuple[int, int]:
     """(M, K) of a gated block's backward pass, its operands checked."""
     dev, kept_x = dh.device, isinstance(x, Int8Matrix)
+    if len(x.shape) != 2 or dh.dim() != 2:
+        raise ValueError("dh and x must be 2-D")
     if kept_x:
         M, K = _int8_check(x, "x", 1)
     else:
@@ -1096,7 +1098,7 @@ def gemm_swiglu_grad(dh: torch.Tensor, x, w: torch.Tensor, kept: Int8Matrix | No
     out again.  [dgate | dup], and x read back, are rounded to dh's dtype on the way."""
     _half(dh, "dh")
     dev = dh.device
-    N, ldw = _gated_weight(w, dh.dtype, dev, x.shape[1], b_transposed)
+    N, ldw = _gated_weight(w, dh.dtype, dev, x.shape[-1], b_transposed)
     M, K = _block_operands(dh, x, kept, with_h, N)
     lddh = _lead(dh, "dh")
     if isinstance(x, Int8Matrix):
@@ -1145,8 +1147,8 @@ def grouped_gemm_swiglu_grad(dh: torch.Tensor, x, ws: list, group_offsets: torch
         if w.shape != shape or w.dtype != dtype or not w.is_contiguous() or w.device != dev or w.dim() != 2:
             raise ValueError("every weight must be a dense [K, N] (or [N, K]) tensor of dh's dtype on %s" % dev)
     N, K = shape if b_transposed else (shape[1], shape[0])
-    if N % 2 or K != x.shape[1]:
-        raise ValueError("weights of %s do not fit x with %d columns" % (tuple(shape), x.shape[1]))
+    if N % 2 or K != x.shape[-1]:
+        raise ValueError("weights of %s do not fit x with %d columns" % (tuple(shape), x.shape[-1]))
     M, K = _block_operands(dh, x, kept, with_h, N)
     _fits("rows, columns or groups", M, K, N, G)
     if isinstance(x, Int8Matrix):

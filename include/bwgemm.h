@@ -345,7 +345,8 @@ const char* bwg_status_string(int status);
  *   dGU = [dgate | dup] [M, N], dgate = dH * up * s (1 + gate (1 - s)) with
  *   s = 1 / (1 + e^-gate), dup = dH * silu(gate); gate and up are multiplied out
  *   again and only dGU is written.  The gradients of X and W are the products
- *   dGU W^T (gemm_*_nt) and X^T dGU (gemm_tn).  dGU overlaps none of the inputs.
+ *   dGU W^T (gemm_*_nt) and X^T dGU (gemm_tn).
+ * No output overlaps an input or another output.
  * The grouped forms take expert e's rows (group_offsets as for grouped_gemm_bf16,
  * with its contract and its report of broken ones) with W[e] (a host array of G
  * device pointers); all matrices are dense.  Rows of no group are left as they are.
