@@ -353,6 +353,10 @@ __device__ void gemm_body(const PT& P, const GemmParams& p) {
   static_assert(!CH || (TN && NC == 1), "sums in registers: one consumer, transposed A");
   // launched while the work before may still be running (launch_behind)
   constexpr bool kBehind = TN || EPI >= kEpiSwigluKeep || (SW && !GROUPED);
+  // The producer warp stays together and elects a lane for a stage's loads: from
+  // one lane of a diverged warp two to four loads and their wait take 700 to 800
+  // clocks, more than a 256x256 tile's MMAs (512).
+  constexpr bool kWarpLoads = kBehind;
   constexpr bool kTables = GROUPED || TN;              // row ranges of groups in shared memory
   // two epilogue warpgroups: one a consumer, or (kHalves) one for each half of
   // the columns of a single consumer's tile
@@ -492,7 +496,7 @@ __device__ void gemm_body(const PT& P, const GemmParams& p) {
       }
       uint32_t x = 0;
       const bool ok = clc_query(clc_resp(s), &x);
-      if (ok && arm) mbar_arrive_expect_tx(clc_full(s), 16);
+      if (ok && arm && (!warp_wide || lane == 0)) mbar_arrive_expect_tx(clc_full(s), 16);
       if (warp_wide) __syncwarp();
       // relaxed: the response was read into registers (the query consumed
       // the load) before the arrive issues, which is all the slot's next
@@ -515,33 +519,36 @@ __device__ void gemm_body(const PT& P, const GemmParams& p) {
 
   if (warp == 0) {
     // ---- TMA producer: one thread streams A and B k-blocks into the ring ----
-    if (lane == 0) {
+    if (kWarpLoads || lane == 0) {
       int s = 0;
       uint32_t ph = 0;
       uint32_t k = 0;  // CLC responses read so far
       int n_traced = 0;
       if constexpr (DYN) {
-        for (uint32_t c = 0; c < kClcSlots; ++c) mbar_arrive_expect_tx(clc_full(c), 16);
+        if (lane == 0)
+          for (uint32_t c = 0; c < kClcSlots; ++c) mbar_arrive_expect_tx(clc_full(c), 16);
+        if constexpr (kWarpLoads) __syncwarp();
       }
       for (int t = first; DYN ? t >= 0 : t < total;
-           t = next_unit(t, k, kRoleProducer, /*arm=*/true, /*warp_wide=*/false)) {
+           t = next_unit(t, k, kRoleProducer, /*arm=*/true, /*warp_wide=*/kWarpLoads)) {
         if constexpr (DYN) {
           if (rank == 0) {
             // ask for the unit after this one (response k), once its slot is free
             const uint32_t cs = k % kClcSlots;
             const uint32_t cph = ((k / kClcSlots) & 1u) ^ 1u;
-            if (!mbar_wait(clc_empty(cs), cph, p.timeout_ns)) {
-              record_fault(p.err, kFaultTimeout, kRoleProducer, kBarClcEmpty, cs, cph);
+            if (!(kWarpLoads ? warp_wait(clc_empty(cs), cph, p.timeout_ns)
+                             : mbar_wait(clc_empty(cs), cph, p.timeout_ns))) {
+              if (lane == 0) record_fault(p.err, kFaultTimeout, kRoleProducer, kBarClcEmpty, cs, cph);
               aborted = true;
               break;
             }
-            clc_try_cancel_multicast(clc_resp(cs), clc_full(cs));
+            if (lane == 0) clc_try_cancel_multicast(clc_resp(cs), clc_full(cs));
           }
         }
         if (t >= total) continue;  // a unit past the end (grid rounding): nothing to load
         const Tile tl = sched.at(t);
         if (tl.width == 0) continue;
-        if (p.trace != nullptr && n_traced < kTraceUnits) {
+        if (p.trace != nullptr && lane == 0 && n_traced < kTraceUnits) {
           unsigned long long* r = p.trace + (static_cast<size_t>(blockIdx.x) * kTraceUnits + n_traced) * kTraceWords;
           r[0] = static_cast<unsigned long long>(t);
           r[1] = globaltimer_ns();
@@ -568,79 +575,98 @@ __device__ void gemm_body(const PT& P, const GemmParams& p) {
         // operand) is addressed (column, k); B stored as [N, K] (K-major, the
         // layout of the pages' kernels) is addressed (k, column).
         const bool bk = p.b_kmajor != 0;
+        // transposed A: whether every box of the unit lies in whole 64-column
+        // groups, and where its groups start
+        int a_cols = 0, a_group = 0, b_group = 0;
+        bool b_cols2 = false;
+        uint32_t full0 = 0;
+        if constexpr (TN) {
+          full0 = mapa_shared(full_bar(0), leader);
+          a_cols = a_row + (NC - 1) * 2 * kRowsPerCta + kRowsPerCta > P.a_grouped;
+          a_group = a_row >> 6;
+          b_group = b_col >> 6;
+          b_cols2 = b_chunks == 2 && b_col + 128 <= P.b_grouped;
+        }
         for (int kb = tl.kb0; kb < tl.kb1; ++kb) {
-          if (!mbar_wait(empty_bar(s), ph ^ 1u, p.timeout_ns)) {
-            record_fault(p.err, kFaultTimeout, kRoleProducer, kBarEmpty, s, ph ^ 1u);
+          if (!(kWarpLoads ? warp_wait_cta(empty_bar(s), ph ^ 1u, p.timeout_ns)
+                           : mbar_wait(empty_bar(s), ph ^ 1u, p.timeout_ns))) {
+            if (lane == 0) record_fault(p.err, kFaultTimeout, kRoleProducer, kBarEmpty, s, ph ^ 1u);
             aborted = true;
             break;
           }
-          const uint32_t sa = smem_a + s * kAStage;
-          const uint32_t sb = smem_b + s * kBStageBytes;
-          const int k0 = kb * kBK;
-          if constexpr (TN) {
-            // windows start at the group's first row for its short first
-            // block, which fills the end of the box, and follow it from there
-            const int w0 = kb == 0 ? tl.k_first - kBK : 0;
-            const int wr = kb == 0 ? tl.k_row : tl.k_row + tl.k_first + (kb - 1) * kBK;
-            if (rank == 0) mbar_arrive_expect_tx(full_bar(s), stage_tx);
-            const uint32_t fb = mapa_shared(full_bar(s), leader);
+          if (!kWarpLoads || elect_one()) {
+            const uint32_t sa = smem_a + s * kAStage;
+            const uint32_t sb = smem_b + s * kBStageBytes;
+            const int k0 = kb * kBK;
+            if constexpr (TN) {
+              // windows start at the group's first row for its short first
+              // block, which fills the end of the box, and follow it from there
+              const int w0 = kb == 0 ? tl.k_first - kBK : 0;
+              const int wr = kb == 0 ? tl.k_row : tl.k_row + tl.k_first + (kb - 1) * kBK;
+              if (rank == 0) mbar_arrive_expect_tx(full_bar(s), stage_tx);
+              const uint32_t fb = full0 + 8u * s;
+              if (a_cols == 0) {
 #pragma unroll
-            for (int c = 0; c < NC; ++c) {
-              if ((tl.cmask >> c) & 1) {
-                const int col = a_row + c * 2 * kRowsPerCta;  // columns of A: rows of D
-                const uint32_t dst = sa + c * kAStageBytes;
-                if (col + kRowsPerCta <= P.a_grouped) {
-                  tma_load_4d_pair(dst, &P.map_a1, fb, 0, w0, wr, col / 64);
-                } else {
-                  tma_load_3d_pair(dst, &p.map_a, fb, col, w0, wr);
-                  tma_load_3d_pair(dst + kAStageBytes / 2, &p.map_a, fb, col + 64, w0, wr);
-                }
-              }
-            }
-            if (b_chunks == 2 && b_col + 128 <= P.b_grouped) {
-              tma_load_4d_pair(sb, &p.map_b1, fb, 0, w0, wr, b_col / 64);
-            } else {
-              for (uint32_t j = 0; j < b_chunks; ++j)
-                tma_load_3d_pair(sb + j * kBChunkBytes, mb, fb, b_col + 64 * static_cast<int>(j), w0, wr);
-            }
-          } else if constexpr (CG == 2) {
-            if (rank == 0) mbar_arrive_expect_tx(full_bar(s), stage_tx);
-            const uint32_t fb = mapa_shared(full_bar(s), leader);
-#pragma unroll
-            for (int c = 0; c < NC; ++c)  // consumer c's rows start 256 rows further
-              if ((tl.cmask >> c) & 1)
-                tma_load_2d_pair(sa + c * kAStageBytes, &p.map_a, fb, k0, a_row + c * 2 * kRowsPerCta);
-            if constexpr (MC == 1) {
-              if (!GROUPED && p.b_one_box && b_chunks == 2) {
-                // both 64-column chunks in one load
-                if (bk)
-                  tma_load_2d_pair(sb, &p.map_b1, fb, k0, b_col);
-                else
-                  tma_load_3d_pair(sb, &p.map_b1, fb, 0, k0, b_col / 64);
+                for (int c = 0; c < NC; ++c)
+                  if ((tl.cmask >> c) & 1)
+                    tma_load_4d_pair(sa + c * kAStageBytes, &P.map_a1, fb, 0, w0, wr, a_group + 4 * c);
               } else {
-                for (uint32_t j = 0; j < b_chunks; ++j) {
+#pragma unroll
+                for (int c = 0; c < NC; ++c) {
+                  if ((tl.cmask >> c) & 1) {
+                    const int col = a_row + c * 2 * kRowsPerCta;
+                    const uint32_t dst = sa + c * kAStageBytes;
+                    tma_load_3d_pair(dst, &p.map_a, fb, col, w0, wr);
+                    tma_load_3d_pair(dst + kAStageBytes / 2, &p.map_a, fb, col + 64, w0, wr);
+                  }
+                }
+              }
+              if (b_cols2) {
+                tma_load_4d_pair(sb, &p.map_b1, fb, 0, w0, wr, b_group);
+              } else {
+                for (uint32_t j = 0; j < b_chunks; ++j)
+                  tma_load_3d_pair(sb + j * kBChunkBytes, mb, fb, b_col + 64 * static_cast<int>(j), w0, wr);
+              }
+            } else if constexpr (CG == 2) {
+              if (rank == 0) mbar_arrive_expect_tx(full_bar(s), stage_tx);
+              const uint32_t fb = mapa_shared(full_bar(s), leader);
+#pragma unroll
+              for (int c = 0; c < NC; ++c)  // consumer c's rows start 256 rows further
+                if ((tl.cmask >> c) & 1)
+                  tma_load_2d_pair(sa + c * kAStageBytes, &p.map_a, fb, k0, a_row + c * 2 * kRowsPerCta);
+              if constexpr (MC == 1) {
+                if (!GROUPED && p.b_one_box && b_chunks == 2) {
+                  // both 64-column chunks in one load
+                  if (bk)
+                    tma_load_2d_pair(sb, &p.map_b1, fb, k0, b_col);
+                  else
+                    tma_load_3d_pair(sb, &p.map_b1, fb, 0, k0, b_col / 64);
+                } else {
+                  for (uint32_t j = 0; j < b_chunks; ++j) {
+                    const int c = b_col + 64 * static_cast<int>(j);
+                    tma_load_2d_pair(sb + j * kBChunkBytes, mb, fb, bk ? k0 : c, bk ? c : k0);
+                  }
+                }
+              } else {
+                // The pairs share B: box j of this CTA's columns is fetched once, by
+                // pair j, and multicast to the same-rank CTA of every pair; each
+                // destination's bytes complete on its own pair leader's barrier.
+                const uint16_t mask = static_cast<uint16_t>((1u << rank) | (1u << (rank + 2)));
+                for (uint32_t j = pair; j < b_chunks; j += MC) {
                   const int c = b_col + 64 * static_cast<int>(j);
-                  tma_load_2d_pair(sb + j * kBChunkBytes, mb, fb, bk ? k0 : c, bk ? c : k0);
+                  tma_load_2d_pair_mc(sb + j * kBChunkBytes, mb, fb, bk ? k0 : c, bk ? c : k0, mask);
                 }
               }
             } else {
-              // The pairs share B: box j of this CTA's columns is fetched once, by
-              // pair j, and multicast to the same-rank CTA of every pair; each
-              // destination's bytes complete on its own pair leader's barrier.
-              const uint16_t mask = static_cast<uint16_t>((1u << rank) | (1u << (rank + 2)));
-              for (uint32_t j = pair; j < b_chunks; j += MC) {
+              mbar_arrive_expect_tx(full_bar(s), stage_tx);
+              tma_load_2d(sa, &p.map_a, full_bar(s), k0, a_row);
+              for (uint32_t j = 0; j < b_chunks; ++j) {
                 const int c = b_col + 64 * static_cast<int>(j);
-                tma_load_2d_pair_mc(sb + j * kBChunkBytes, mb, fb, bk ? k0 : c, bk ? c : k0, mask);
+                tma_load_2d(sb + j * kBChunkBytes, mb, full_bar(s), bk ? k0 : c, bk ? c : k0);
               }
-            }
-          } else {
-            mbar_arrive_expect_tx(full_bar(s), stage_tx);
-            tma_load_2d(sa, &p.map_a, full_bar(s), k0, a_row);
-            for (uint32_t j = 0; j < b_chunks; ++j) {
-              const int c = b_col + 64 * static_cast<int>(j);
-              tma_load_2d(sb + j * kBChunkBytes, mb, full_bar(s), bk ? k0 : c, bk ? c : k0);
             }
           }
+          if constexpr (kWarpLoads) __syncwarp();
           if (++s == S) {
             s = 0;
             ph ^= 1u;
@@ -715,7 +741,8 @@ __device__ void gemm_body(const PT& P, const GemmParams& p) {
           tc_fence_after();
           const uint32_t d_tmem = tmem_base + static_cast<uint32_t>(acc) * kTileN;
           for (int kb = kc; kb < ke; ++kb) {
-            if (!warp_wait(full_bar(s), ph, p.timeout_ns)) {
+            if (!(kBehind ? warp_wait_cta(full_bar(s), ph, p.timeout_ns)
+                          : warp_wait(full_bar(s), ph, p.timeout_ns))) {
               if (lane == 0) record_fault(p.err, kFaultTimeout, kRoleMma, kBarFull, s, ph);
               aborted = true;
               break;
