@@ -382,9 +382,7 @@ __device__ void gemm_body(const PT& P, const GemmParams& p) {
   const uint32_t smem_a = base;
   const uint32_t smem_b = smem_a + S * kAStage;
   const uint32_t smem_epi = smem_b + S * kBStageBytes;
-  // gradient of SwiGLU: a box of H's gradient for every epilogue warp
-  const uint32_t smem_dh = smem_epi + (p.direct_store ? 0u : static_cast<uint32_t>(kEpiBytes));
-  const uint32_t smem_bar = smem_dh + (EPI == kEpiSwigluGrad ? 8u * kEpiBufBytes : 0u);
+  const uint32_t smem_bar = smem_epi + (p.direct_store ? 0u : static_cast<uint32_t>(kEpiBytes));
   auto full_bar = [&](int s) { return smem_bar + 8u * s; };
   auto empty_bar = [&](int s) { return smem_bar + 8u * (S + s); };
   auto acc_full_bar = [&](int a) { return smem_bar + 8u * (2 * S + a); };
@@ -817,7 +815,6 @@ __device__ void gemm_body(const PT& P, const GemmParams& p) {
     uint32_t k = 0;
     int n_traced = 0;
     const uint32_t dh_bar = dh_bars + 8u * (warp - kEpiWarp0);
-    const uint32_t dh_buf = smem_dh + (warp - kEpiWarp0) * kEpiBufBytes;
     uint32_t dh_ph = 0;
     for (int t = first; DYN ? t >= 0 : t < total;
          t = next_unit(t, k, kRoleEpilogue, /*arm=*/false, /*warp_wide=*/true)) {
@@ -941,13 +938,15 @@ __device__ void gemm_body(const PT& P, const GemmParams& p) {
         }
         continue;
       }
-      // This warp's box of H's gradient comes in while the accumulator is still
-      // being filled (rows past a group's end are read and not used).
+      // This warp's box of H's gradient comes into its staging buffer while the
+      // accumulator is still being filled, once the stores of the unit before have
+      // read it (rows past a group's end are loaded and not used).
       if constexpr (EPI == kEpiSwigluGrad) {
         const int col = tl.n0 + wg * 64;
         if (lane == 0 && wg * 128 < tl.width && col < p.N) {
+          bulk_wait_group_read<0>();
           mbar_arrive_expect_tx(dh_bar, kEpiBufBytes + p.tx_extra);
-          tma_load_2d(dh_buf, &P.x.map_x, dh_bar, col, row_w);
+          tma_load_2d(ebuf, &P.x.map_x, dh_bar, col, row_w);
         }
       }
       if (!warp_wait(acc_full_bar(acc), acc_ph, p.timeout_ns)) {
@@ -1150,8 +1149,8 @@ __device__ void gemm_body(const PT& P, const GemmParams& p) {
             uint32_t dw[32];
 #pragma unroll
             for (uint32_t j = 0; j < 8; ++j)
-              ld_shared_v4(dh_buf + swizzle128_offset(lane, j), &dw[4 * j]);
-            __syncwarp();  // read before the next box comes in
+              ld_shared_v4(ebuf + swizzle128_offset(lane, j), &dw[4 * j]);
+            // (emit's __syncwarp lies between these reads and its writes)
 #pragma unroll
             for (int i = 0; i < 32; ++i) {
               float d0, d1, dg0, dg1, du0, du1;

@@ -156,20 +156,13 @@ void gated_params(const GatedCall& c, const Runtime& rt, int stages, GemmParams*
   x->wide = I % 16 == 0 ? 1 : 0;
 }
 
-// The gradient's boxes of dH, 32 KiB, take the place of a stage.
-int gated_stages(int epi, bool two) { return two ? 4 : epi == kEpiSwigluGrad ? 5 : 6; }
-
-int gated_smem(int epi, int stages, int nc) {
-  return dense_smem(2, stages, false, nc) + (epi == kEpiSwigluGrad ? 8 * kEpiBufBytes : 0);
-}
-
 bwg_status run_gated_dense(const GatedCall& c, const Runtime& rt, cudaStream_t stream) {
   const int I = c.N / 2, n_tiles = (I + kTileN / 2 - 1) / (kTileN / 2);
   // two consumers while their tiles still give every pair one, as in gemm_bf16
   const long long tiles_2c = static_cast<long long>((c.M + 4 * kRowsPerCta - 1) / (4 * kRowsPerCta)) * n_tiles;
   const bool two = c.epi == kEpiSwiglu && tiles_2c >= rt.pairs_2c;
-  const int nc = two ? 2 : 1, stages = gated_stages(c.epi, two);
-  const int smem = gated_smem(c.epi, stages, nc);
+  const int nc = two ? 2 : 1, stages = two ? 4 : 6;
+  const int smem = dense_smem(2, stages, false, nc);
   if (smem > rt.max_smem) return BWG_ERR_UNSUPPORTED;
   DenseGatedParams p;
   std::memset(&p, 0, sizeof(p));
@@ -203,8 +196,8 @@ bwg_status run_gated_dense(const GatedCall& c, const Runtime& rt, cudaStream_t s
 }
 
 bwg_status run_gated_grouped(const GatedCall& c, const Runtime& rt, cudaStream_t stream) {
-  const int stages = gated_stages(c.epi, false);
-  const int smem = gated_smem(c.epi, stages, 1);
+  constexpr int kStages = 6;
+  const int smem = dense_smem(2, kStages, false, 1);
   if (smem > rt.max_smem) return BWG_ERR_UNSUPPORTED;
   for (int g0 = 0; g0 < c.G; g0 += kMaxGroupsPerLaunch) {
     const int gn = std::min(kMaxGroupsPerLaunch, c.G - g0);
@@ -214,7 +207,7 @@ bwg_status run_gated_grouped(const GatedCall& c, const Runtime& rt, cudaStream_t
     if (!gated_maps(c, &p, &P.x)) return BWG_ERR_CUDA;
     for (int i = 0; i < gn; ++i)
       if (!gated_weight_map(c, &P.map_b[i], c.w[g0 + i])) return BWG_ERR_CUDA;
-    gated_params(c, rt, stages, &p, &P.x);
+    gated_params(c, rt, kStages, &p, &P.x);
     p.group_offsets = c.offsets;
     p.G = gn;
     p.g_begin = g0;
