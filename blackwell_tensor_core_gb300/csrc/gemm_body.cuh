@@ -348,14 +348,16 @@ template <int CG, int MC, bool GROUPED, int NC, int EPI, bool DYN, bool TN = fal
 __device__ void gemm_body(const PT& P, const GemmParams& p) {
   constexpr bool SW = EPI != kEpiPlain;
   static_assert(!SW || (CG == 2 && MC == 1), "SwiGLU runs on the pair kernels");
-  static_assert(!DYN || (CG == 2 && MC == 1 && (NC == 2 || CH || EPI >= kEpiSwigluKeep)), "dynamic scheduling: 12-warp pairs");
+  static_assert(!DYN || (CG == 2 && MC == 1 && (NC == 2 || CH || EPI >= kEpiSwigluKeep)),
+                "dynamic scheduling: 12-warp pairs");
   static_assert(!TN || (CG == 2 && MC == 1 && !SW && !GROUPED), "transposed A runs on plain pairs");
   static_assert(!CH || (TN && NC == 1), "sums in registers: one consumer, transposed A");
   // launched while the work before may still be running (launch_behind)
   constexpr bool kBehind = TN || EPI >= kEpiSwigluKeep || (SW && !GROUPED);
   // The producer warp stays together and elects a lane for a stage's loads: from
-  // one lane of a diverged warp two to four loads and their wait take 700 to 800
-  // clocks, more than a 256x256 tile's MMAs (512).
+  // one lane of a diverged warp two to four loads and their wait take 550 to 800
+  // clocks, more than a 256x256 tile's MMAs (512): 4096 x 8192 x 8192 transposed and
+  // joined took 619 thousand cycles so, 477 with an elected lane.
   constexpr bool kWarpLoads = kBehind;
   constexpr bool kTables = GROUPED || TN;              // row ranges of groups in shared memory
   // two epilogue warpgroups: one a consumer, or (kHalves) one for each half of
@@ -1110,8 +1112,7 @@ __device__ void gemm_body(const PT& P, const GemmParams& p) {
             }
             if (P.x.wide && (!GROUPED || row_w + 32 <= tl.row_end)) {
               // gate's and up's 32 x 64 codes as two boxes of the staging
-              // buffer; stored from registers, 16 bytes a row, they cost the
-              // tensor cores' operand reads 32 cycles an instruction
+              // buffer: a store from registers would touch 32 lines at a time
               if (lane == 0) bulk_wait_group_read<0>();
               __syncwarp();
 #pragma unroll

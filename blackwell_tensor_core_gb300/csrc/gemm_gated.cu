@@ -20,8 +20,9 @@ __global__ void __launch_bounds__(kThreads2C, 1) gated_2c_kernel(const __grid_co
 // 256x256 tiles, whose accumulator is one of two, so that eight epilogue warps work
 // on one tile while the next is summed up: H alone where 512x256 tiles would be
 // too few, and the epilogues that read or write more, for which the tensor cores
-// would wait with 512x256 tiles (8192 x 4096 x 8192 with gate and up kept in 8
-// bits took 341 us with them, its gradient 356).
+// would wait with 512x256 tiles.  8192 x 4096 x 8192, back to back: H 278 us; with
+// gate and up kept in 8 bits 302 (341 with 512x256 tiles), their gradient 325
+// (356).  What bounds them: tensor cores and the power limit.
 template <int EPI>
 __global__ void __launch_bounds__(kThreads2C, 1) gated_wide_kernel(const __grid_constant__ DenseGatedParams p) {
   gemm_body<2, 1, false, 1, EPI, false>(p, p);

@@ -1,6 +1,11 @@
 // Products whose left operand is read transposed (gemm_body.cuh, TN):
 // D[g] = A_g^T B_g, the gradient of a weight from a layer's input A and the
 // gradient B of its output, over all rows or over each expert's.
+//
+// Both operands are summed over their rows, so both enter MN-major, as stored: no
+// transpose.  What bounds them: tensor cores and the power limit (8192^3 in BF16
+// 605 us back to back, 1.82 PFLOP/s; FP32 results 643), and where D is small
+// the rate at which a slice's rows come from L2.
 #include <algorithm>
 #include <cstring>
 
@@ -109,7 +114,7 @@ struct TnCall {
 int ceil_div(int a, int b) { return (a + b - 1) / b; }
 
 // How a product is cut up: tiles of 256x256 whose sums are joined in registers, or
-// of 512x256 (the faster for each element, see gemm_body), and slices of each
+// of 512x256, which load a quarter less for each element, and slices of each
 // group's rows where D has few tiles.
 struct TnPlan {
   bool joined;
@@ -127,10 +132,11 @@ double tn_waves(long long T, int C, int nc) {
   return static_cast<double>(full) + std::min(1.0, last);
 }
 
-// The cheapest by an estimate in us: k-blocks of a tile at the rates measured on
-// 8192^3, filling the ring and storing a tile, and for slices a launch and 8 bytes
-// an element of every plane at 6 TB/s.  20011 rows of 1000 x 1416: 256x256 tiles in
-// one slice 158 us, three slices 60, 512x256 tiles in six 54.
+// The cheapest by an estimate in us: a tile's k-blocks, filling the ring and storing
+// the tile, and for slices a launch and 8 bytes an element of every plane at 6 TB/s.
+// 20011 rows of 1000 x 1416: 256x256 tiles in one slice 106 us, in three 58, 512x256
+// tiles in six 50.  At 13 sizes from 256 x 256 to 4096 x 8192 the chosen form is at
+// most 8% slower than the best of twenty (2.5% on average).
 TnPlan tn_plan(int M, int N, int rows, int G, int out_dtype, int pairs, int pairs_2c) {
   // FP32 results keep what TMEM's sums lose (nothing over kChunkBlocks k-blocks)
   const bool exact = out_dtype == BWG_OUT_FP32 && rows > kChunkBlocks * kBK;
