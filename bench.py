@@ -47,7 +47,7 @@ TRAFFIC_FILE = os.path.join(ROOT, "profiles", "traffic_gemm_8192.txt")
 # Sources of the benchmark's kernel (the dense two-consumer pair kernel and
 # the host code that launches it): the committed DRAM traffic figure is
 # reported only while their code-only hash matches the one it was taken on.
-KERNEL_SOURCES = ["gemm_tc.cu", "ptx.cuh", "layout.h", "params.h", "api.cu"]
+KERNEL_SOURCES = ["gemm_tc.cu", "gemm_body.cuh", "swiglu.cuh", "launch.h", "ptx.cuh", "layout.h", "params.h", "api.cu"]
 KERNEL_NAMES = {2: "persistent 1-CTA", 3: "persistent CTA pair (cta_group::2)",
                 4: "swapped small-M", 5: "two pairs sharing B by TMA multicast",
                 6: "persistent CTA pair, two MMA consumers (cta_group::2)"}
