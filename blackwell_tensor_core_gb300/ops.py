@@ -1100,6 +1100,8 @@ def gemm_swiglu_grad(dh: torch.Tensor, x, w: torch.Tensor, kept: Int8Matrix | No
     dev = dh.device
     N, ldw = _gated_weight(w, dh.dtype, dev, x.shape[-1], b_transposed)
     M, K = _block_operands(dh, x, kept, with_h, N)
+    if K % 8 and (need_dx or (need_dw and b_transposed)):
+        raise ValueError("gradients of %d columns: their rows must be whole 16 bytes, multiples of 8" % K)
     lddh = _lead(dh, "dh")
     if isinstance(x, Int8Matrix):
         x = dequantize_int8(x, out_dtype=dh.dtype, stream=stream) if need_dw or kept is None else None

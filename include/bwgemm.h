@@ -509,6 +509,7 @@ void bwg_debug_set_trace(void* buffer);
  *                      evict-last (default 2; 0 with the cluster split)
  *   BWG_GROUPED_1C     1: grouped kernels with one MMA consumer (256-row units)
  *   BWG_GROUPED_SWAP   1: swapped-operand group ends (one-consumer grouped kernel)
+ * The gated, transposed and 8-bit calls go by BWG_NO_TAIL_SPLIT alone.
  *   BWG_B_ONE_BOX      0: dense pair kernels load a CTA's B stage as two
  *                      64-column boxes (default: one load where N % 64 == 0
  *                      or B is [N, K])

@@ -350,6 +350,70 @@ def test_a_training_step_captured_twice_and_replayed_at_once(ops):
             assert torch.equal(x, y)
 
 
+def test_captured_behind_copies_and_on_forked_streams(ops):
+    """Kernels that set up while the work before ends, behind a copy, behind each
+    other and behind a fork's join, replayed with new inputs each time."""
+    x, w, dh = data(300, 264, 528, torch.bfloat16, 25)
+    xs, main, side = torch.empty_like(x), torch.cuda.Stream(), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g, stream=main):
+        xs.copy_(x)
+        a = ops.gemm_swiglu(xs, w)
+        side.wait_stream(main)
+        with torch.cuda.stream(side):
+            b = ops.gemm_swiglu(xs[:64], w)
+            c = ops.gemm(xs, dh, a_transposed=True, out_dtype=torch.float32)
+        d = ops.gemm_swiglu_grad(dh, xs, w)
+        main.wait_stream(side)
+        e = ops.gemm(a, c.to(torch.bfloat16), b_transposed=True)
+    for seed in (26, 27, 28):
+        x.copy_(data(300, 264, 528, torch.bfloat16, seed)[0])
+        g.replay()
+        torch.cuda.synchronize()
+        want = ops.gemm_swiglu_grad(dh, x, w)
+        h = ops.gemm_swiglu(x, w)
+        t = ops.gemm(x, dh, a_transposed=True, out_dtype=torch.float32)
+        for got, ref in ((a, h), (b, ops.gemm_swiglu(x[:64], w)), (c, t), (d.dx, want.dx), (d.dw, want.dw),
+                         (e, ops.gemm(h, t.to(torch.bfloat16), b_transposed=True))):
+            assert torch.equal(got, ref)
+
+
+def test_more_elements_than_an_int(ops):
+    """70000 x 32768: 2.3e9 codes and gradients; the first and last rows are right."""
+    M, K, N = 70000, 64, 32768
+    x, w, _ = data(M, K, N, torch.bfloat16, 33)
+    h, kept = ops.gemm_swiglu(x, w, keep_int8=True)
+    dgu = ops.swiglu_grad(h, kept)
+    from_x = torch.empty(M, N, dtype=torch.bfloat16, device="cuda")
+    assert ops.lib().gemm_swiglu_grad(h.data_ptr(), x.data_ptr(), w.data_ptr(), from_x.data_ptr(), 0, 0, M, N, K, N // 2,
+                                      K, N, N, torch.cuda.current_stream().cuda_stream) == 0
+    for rows in (slice(0, 40), slice(M - 300, M)):
+        g = gu.gated(x[rows], w)
+        gu.assert_close(h[rows], *gu.forward(*g, torch.bfloat16), "h")
+        part = ops.Int8Matrix(kept.codes[rows], kept.scales[rows], 2)
+        check_kept(part, *g)
+        gu.assert_close(from_x[rows], *gu.backward(h[rows], *g, torch.bfloat16), "dgu")
+        v = gu.value(part)
+        gate, up = v[:, :N // 2], v[:, N // 2:]
+        e = 2.0 ** -23
+        gu.assert_close(dgu[rows], *gu.backward(h[rows], gate, up, e * gate.abs(), e * up.abs(), torch.bfloat16), "dgu")
+
+
+def test_columns_that_end_inside_16_bytes(ops):
+    """x of 100 columns in rows of 104: the block and dw are taken, dx is refused."""
+    x, w, dh = data(300, 104, 144, torch.bfloat16, 34)
+    x[:, 100:] = float("nan")
+    x, w = x[:, :100], w[:100]
+    gu.assert_close(ops.gemm_swiglu(x, w), *gu.forward(*gu.gated(x, w), x.dtype), "h")
+    gu.assert_close(ops.gemm_swiglu(x[:9], w), *gu.forward(*gu.gated(x[:9], w), x.dtype), "h of few rows")
+    with pytest.raises(ValueError):
+        ops.gemm_swiglu_grad(dh, x, w)
+    got = ops.gemm_swiglu_grad(dh, x, w, need_dx=False)
+    d, e = gu.backward(dh, *gu.gated(x, w), x.dtype)
+    gu.assert_close(got.dw, *gu.through(x.double().t(), 0.0, d, e, x.dtype), "dw")
+
+
 def test_a_stream_of_its_own(ops):
     x, w, dh = data(300, 72, 400, torch.bfloat16, 30)
     want = step(ops, x, w, dh)

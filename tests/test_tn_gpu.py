@@ -84,6 +84,20 @@ def test_long_sums_keep_their_bits(ops):
     assert float((d - ref).norm() / ref.norm()) < 2e-6
 
 
+def test_more_elements_than_an_int(ops):
+    """560000 rows of 4096: what the last rows add arrives, and nothing else."""
+    rows, M = 560000, 4096
+    a = torch.zeros(rows, M, dtype=torch.bfloat16, device="cuda")
+    b = torch.zeros(rows, 64, dtype=torch.bfloat16, device="cuda")
+    a[-70:], b[-70:] = draw(70, M, torch.bfloat16, 20, True), draw(70, 64, torch.bfloat16, 21, True)
+    want_d = a[-70:].double().t() @ b[-70:].double()
+    for out in (torch.float32, torch.bfloat16):
+        assert torch.equal(ops.gemm(a, b, out_dtype=out, a_transposed=True), want_d.to(out))
+    off = gu.offsets([rows - 70, 70])
+    d = ops.grouped_gemm_wgrad(a, b, off)
+    assert bool((d[0] == 0).all()) and torch.equal(d[1], want_d.to(torch.bfloat16))
+
+
 def test_strides_and_what_lies_between_rows(ops):
     K, M, N = 777, 136, 200
     a, b = draw(K, M, torch.bfloat16, 5), draw(K, N, torch.bfloat16, 6)
