@@ -14,7 +14,8 @@
 // reads whole lines; two rows in flight a lane (four: 77 us in place of 68, one:
 // 70).  32768 x 4096 BF16: in 68 us (6.0 TB/s), back 63 (6.6); SwiGLU's gradient
 // of 32768 x 2048 83 (6.6), with H 104.  Rows that start off 16 bytes: 8192 x 4095
-// in 34, back 29 (3.0 and 3.4 TB/s; a value a lane and load).
+// in 34, back 28 (3.0 and 3.7 TB/s; a value a lane and load), 8192 x 4094 in 30 and
+// 21 (two).
 #include <algorithm>
 #include <cstdint>
 #include <cuda_bf16.h>
@@ -187,21 +188,32 @@ __global__ void __launch_bounds__(kThreadsInt8) quantize_int8_kernel(const Int8P
 }
 
 // Any width and stride: a warp takes four blocks of a row, two columns of each a
-// lane, so that neighbouring lanes read neighbouring elements.
-template <int IN>
+// lane, so that neighbouring lanes read neighbouring elements, V = 1 or 2 at a time
+// (2: columns, strides and bases are even).
+template <class T, int V>
+struct alignas(sizeof(T) * V) Few {
+  T v[V];
+};
+
+template <int IN, int V>
 __global__ void __launch_bounds__(kThreadsInt8) quantize_int8_odd_kernel(const Int8Params p) {
   const int lane = static_cast<int>(threadIdx.x & 31u);
   const long long rb = blockIdx.x / p.segs;
   const int seg = static_cast<int>(blockIdx.x - rb * p.segs);
-  const int col = seg * kOddCols + lane;
+  const int col = seg * kOddCols + lane * V;
   const long long row0 = (rb * (kThreadsInt8 / 32) + (threadIdx.x >> 5)) * kOddRows;
-  float v[kOddRows][8];
+  float v[kOddRows][8];  // of block b: 2 b and 2 b + 1
 #pragma unroll
   for (int r = 0; r < kOddRows; ++r) {
     const Elem<IN>* src = static_cast<const Elem<IN>*>(p.x) + part_row(p, row0 + r, p.ldx) + col;
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
-      v[r][i] = row0 + r < p.rows && col + 32 * i < p.cols ? to_float<IN>(src[32 * i]) : 0.f;
+    for (int i = 0; i < 8 / V; ++i) {
+      Few<Elem<IN>, V> t = {};
+      if (row0 + r < p.rows && col + 32 * V * i < p.cols)
+        t = *reinterpret_cast<const Few<Elem<IN>, V>*>(src + 32 * V * i);
+#pragma unroll
+      for (int j = 0; j < V; ++j) v[r][V * i + j] = to_float<IN>(t.v[j]);
+    }
   }
 #pragma unroll
   for (int r = 0; r < kOddRows; ++r) {
@@ -222,9 +234,12 @@ __global__ void __launch_bounds__(kThreadsInt8) quantize_int8_odd_kernel(const I
     if ((lane & 7) == 0 && block < p.blocks) p.scales[(row0 + r) * p.blocks + block] = scale;
     int8_t* dst = p.codes + (row0 + r) * p.cols + col;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const float f = __shfl_sync(0xffffffffu, inv, (i >> 1) * 8);
-      if (col + 32 * i < p.cols) dst[32 * i] = static_cast<int8_t>(int8_code(v[r][i], f) & 0xFFu);
+    for (int i = 0; i < 8 / V; ++i) {
+      const float f = __shfl_sync(0xffffffffu, inv, (V * i >> 1) * 8);
+      Few<uint8_t, V> t;
+#pragma unroll
+      for (int j = 0; j < V; ++j) t.v[j] = static_cast<uint8_t>(int8_code(v[r][V * i + j], f));
+      if (col + 32 * V * i < p.cols) *reinterpret_cast<Few<uint8_t, V>*>(dst + 32 * V * i) = t;
     }
   }
 }
@@ -290,22 +305,23 @@ __global__ void __launch_bounds__(kThreadsInt8) dequantize_int8_kernel(const Int
   }
 }
 
-template <int OUT>
+template <int OUT, int V>
 __global__ void __launch_bounds__(kThreadsInt8) dequantize_int8_odd_kernel(const Int8Params p) {
   const int lane = static_cast<int>(threadIdx.x & 31u);
   const long long rb = blockIdx.x / p.segs;
   const int seg = static_cast<int>(blockIdx.x - rb * p.segs);
-  const int col = seg * kOddCols + lane, block = seg * (kOddCols / kInt8Block);
+  const int col = seg * kOddCols + lane * V, block = seg * (kOddCols / kInt8Block);
   const long long row0 = (rb * (kThreadsInt8 / 32) + (threadIdx.x >> 5)) * kOddRows;
-  int8_t c[kOddRows][8];
+  Few<int8_t, V> c[kOddRows][8 / V];
   float scale[kOddRows][4];
 #pragma unroll
   for (int r = 0; r < kOddRows; ++r) {
     const int8_t* src = p.codes + (row0 + r) * p.cols + col;
     const float* sc = p.scales + (row0 + r) * p.blocks + block;
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
-      if (row0 + r < p.rows && col + 32 * i < p.cols) c[r][i] = src[32 * i];
+    for (int i = 0; i < 8 / V; ++i)
+      if (row0 + r < p.rows && col + 32 * V * i < p.cols)
+        c[r][i] = *reinterpret_cast<const Few<int8_t, V>*>(src + 32 * V * i);
 #pragma unroll
     for (int b = 0; b < 4; ++b) scale[r][b] = row0 + r < p.rows && block + b < p.blocks ? sc[b] : 0.f;
   }
@@ -313,9 +329,14 @@ __global__ void __launch_bounds__(kThreadsInt8) dequantize_int8_odd_kernel(const
   for (int r = 0; r < kOddRows; ++r) {
     Elem<OUT>* dst = static_cast<Elem<OUT>*>(p.y) + part_row(p, row0 + r, p.ldy) + col;
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
-      if (row0 + r < p.rows && col + 32 * i < p.cols)
-        dst[32 * i] = from_float<OUT>(static_cast<float>(c[r][i]) * scale[r][i >> 1]);
+    for (int i = 0; i < 8 / V; ++i) {
+      Few<Elem<OUT>, V> t;
+#pragma unroll
+      for (int j = 0; j < V; ++j)
+        t.v[j] = from_float<OUT>(static_cast<float>(c[r][i].v[j]) * scale[r][V * i >> 1]);
+      if (row0 + r < p.rows && col + 32 * V * i < p.cols)
+        *reinterpret_cast<Few<Elem<OUT>, V>*>(dst + 32 * V * i) = t;
+    }
   }
 }
 
@@ -410,10 +431,14 @@ bool launch_type(const Int8Params& p, bool back, bool vec, cudaStream_t s) {
     Int8Params q = p;
     const unsigned grid = row_grid(&q, kOddCols, kOddRows);
     if (grid == 0) return false;
+    // two at a time: every row, part and code starts on an even element
+    const bool two = p.cols % 2 == 0 && p.ldx % 2 == 0 && is_aligned(p.x, 2 * elt_bytes(T)) && is_aligned(p.codes, 2);
     if (back)
-      dequantize_int8_odd_kernel<T><<<grid, kThreadsInt8, 0, s>>>(q);
+      two ? dequantize_int8_odd_kernel<T, 2><<<grid, kThreadsInt8, 0, s>>>(q)
+          : dequantize_int8_odd_kernel<T, 1><<<grid, kThreadsInt8, 0, s>>>(q);
     else
-      quantize_int8_odd_kernel<T><<<grid, kThreadsInt8, 0, s>>>(q);
+      two ? quantize_int8_odd_kernel<T, 2><<<grid, kThreadsInt8, 0, s>>>(q)
+          : quantize_int8_odd_kernel<T, 1><<<grid, kThreadsInt8, 0, s>>>(q);
     return true;
   }
   switch (row_lanes(p.cols)) {
