@@ -840,32 +840,71 @@ class Int8Matrix:
     parts   1, or 2 for [gate | up], whose halves have blocks of their own
     """
 
-    __slots__ = ("codes", "scales", "parts")
+    __slots__ = ("_codes", "_scales", "parts", "_buffer", "_shape")
 
     def __init__(self, codes, scales, parts=1):
-        self.codes = codes
-        self.scales = scales
+        self._codes = codes
+        self._scales = scales
         self.parts = parts
+        self._buffer = None
+        self._shape = None
+
+    @classmethod
+    def _new(cls, rows: int, cols: int, parts: int, dev, stream):
+        """One whose codes and scales share a buffer, which they become views of
+        when they are asked for: a tensor costs a small call 4 us."""
+        q = cls(None, None, parts)
+        q._shape = rows, cols
+        q._buffer = _new((_int8_scales_at(rows, cols) + 4 * rows * _int8_blocks(cols, parts),), torch.int8, dev, stream)
+        return q
+
+    @property
+    def codes(self):
+        if self._codes is None:
+            rows, cols = self._shape
+            self._codes = self._buffer[:rows * cols].view(rows, cols)
+        return self._codes
+
+    @property
+    def scales(self):
+        if self._scales is None:
+            rows, cols = self._shape
+            self._scales = self._buffer[_int8_scales_at(rows, cols):].view(torch.float32).view(
+                rows, _int8_blocks(cols, self.parts))
+        return self._scales
 
     @property
     def shape(self):
-        return self.codes.shape
+        return tuple(self._codes.shape) if self._buffer is None else self._shape
 
     @property
     def device(self):
-        return self.codes.device
+        return (self._codes if self._buffer is None else self._buffer).device
+
+    def _pointers(self) -> tuple[int, int]:
+        if self._buffer is None:
+            return self._codes.data_ptr(), self._scales.data_ptr()
+        at = self._buffer.data_ptr()
+        return at, at + _int8_scales_at(*self._shape)
 
 
 def _int8_blocks(cols: int, parts: int) -> int:
     return parts * -(-(cols // parts) // _INT8_BLOCK)
 
 
+def _int8_scales_at(rows: int, cols: int) -> int:
+    """Where the scales start behind the codes."""
+    return (rows * cols + 255) // 256 * 256
+
+
 def _int8_check(q: Int8Matrix, name: str, parts: int | None = None) -> tuple[int, int]:
     """(rows, cols) of an Int8Matrix whose buffers are as large as the kernels take them."""
-    codes, scales = q.codes, q.scales
     if q.parts not in (1, 2) or (parts is not None and q.parts != parts):
         raise ValueError("%s must have %s, got %r" % (name, "1 or 2 parts" if parts is None else "parts=%d" % parts,
                                                       q.parts))
+    if q._buffer is not None:
+        return q._shape
+    codes, scales = q._codes, q._scales
     if codes.dtype != torch.int8 or codes.dim() != 2 or not codes.is_contiguous() or not codes.is_cuda:
         raise ValueError("%s.codes must be a dense CUDA int8 tensor [rows, cols]" % name)
     rows, cols = codes.shape
@@ -879,11 +918,6 @@ def _int8_check(q: Int8Matrix, name: str, parts: int | None = None) -> tuple[int
     return rows, cols
 
 
-def _new_int8(rows: int, cols: int, parts: int, dev, stream) -> Int8Matrix:
-    return Int8Matrix(_new((rows, cols), torch.int8, dev, stream),
-                      _new((rows, _int8_blocks(cols, parts)), torch.float32, dev, stream), parts)
-
-
 def quantize_int8(x: torch.Tensor, parts: int = 1, stream=None) -> Int8Matrix:
     """x [rows, cols] in 8 bits, with a float32 scale for every 64 columns of a
     row; parts=2 for [gate | up], whose halves have blocks of their own."""
@@ -892,9 +926,10 @@ def quantize_int8(x: torch.Tensor, parts: int = 1, stream=None) -> Int8Matrix:
     _fits("columns of x", cols)
     if parts not in (1, 2) or cols % parts:
         raise ValueError("parts must be 1 or 2 and divide the columns, got %r for %d" % (parts, cols))
-    q = _new_int8(rows, cols, parts, x.device, stream)
-    _check(_on(x.device, lib().quantize_int8, x.data_ptr(), _OUT_CODES[x.dtype], rows, cols, ldx, parts,
-               q.codes.data_ptr(), q.scales.data_ptr(), _stream_handle(stream, x.device)), "quantize_int8")
+    dev = x.device
+    q = Int8Matrix._new(rows, cols, parts, dev, stream)
+    _check(_on(dev, lib().quantize_int8, x.data_ptr(), _OUT_CODES[x.dtype], rows, cols, ldx, parts, *q._pointers(),
+               _stream_handle(stream, dev)), "quantize_int8")
     return q
 
 
@@ -902,10 +937,9 @@ def dequantize_int8(q: Int8Matrix, out_dtype: torch.dtype = torch.bfloat16, out:
                     stream=None) -> torch.Tensor:
     """The values of q, [rows, cols], each rounded once."""
     rows, cols = _int8_check(q, "q")
-    dev = q.codes.device
+    dev = q.device
     out, ldo = _fp4_out(out, out_dtype, rows, cols, dev, stream)
-    _check(_on(dev, lib().dequantize_int8, q.codes.data_ptr(), q.scales.data_ptr(), q.parts, out.data_ptr(),
-               _OUT_CODES[out.dtype], rows, cols, ldo, _stream_handle(stream, dev)), "dequantize_int8")
+    _check(_on(dev, lib().dequantize_int8, *q._pointers(), q.parts, out.data_ptr(), _OUT_CODES[out.dtype], rows, cols, ldo, _stream_handle(stream, dev)), "dequantize_int8")
     return out
 
 
@@ -1008,10 +1042,9 @@ def gemm_swiglu(x: torch.Tensor, w: torch.Tensor, out: torch.Tensor | None = Non
     ldx = _lead(x, "x")
     N, ldw = _gated_weight(w, dtype, dev, K, b_transposed)
     out, ldh = _out_rows(out, M, N // 2, dtype, dev, stream)
-    kept = _new_int8(M, N, 2, dev, stream) if keep_int8 else None
-    _check(_on(dev, lib().gemm_swiglu, x.data_ptr(), w.data_ptr(), out.data_ptr(),
-               kept.codes.data_ptr() if keep_int8 else None, kept.scales.data_ptr() if keep_int8 else None,
-               _OUT_CODES[dtype], 1 if b_transposed else 0, M, N, K, ldx, ldw, ldh, _stream_handle(stream, dev)),
+    kept = Int8Matrix._new(M, N, 2, dev, stream) if keep_int8 else None
+    codes, scales = kept._pointers() if keep_int8 else (None, None)
+    _check(_on(dev, lib().gemm_swiglu, x.data_ptr(), w.data_ptr(), out.data_ptr(), codes, scales, _OUT_CODES[dtype], 1 if b_transposed else 0, M, N, K, ldx, ldw, ldh, _stream_handle(stream, dev)),
            "gemm_swiglu")
     return (out, kept) if keep_int8 else out
 
@@ -1024,10 +1057,10 @@ def _grouped_keep(A, Bs, group_offsets, out, stream, b_transposed, M_total, K, N
         out = _new((M_total, N // 2), A.dtype, dev, stream)
     elif out.shape != (M_total, N // 2) or out.dtype != A.dtype or not out.is_contiguous() or out.device != dev:
         raise ValueError("out must be a dense [M_total, %d] tensor of A's dtype" % (N // 2))
-    kept = _new_int8(M_total, N, 2, dev, stream)
+    kept = Int8Matrix._new(M_total, N, 2, dev, stream)
     p, keep = _ptr_array([b.data_ptr() for b in Bs])
-    _check(_on(dev, lib().grouped_gemm_swiglu_keep, A.data_ptr(), p, out.data_ptr(), kept.codes.data_ptr(),
-               kept.scales.data_ptr(), group_offsets.data_ptr(), _OUT_CODES[A.dtype], 1 if b_transposed else 0, G,
+    _check(_on(dev, lib().grouped_gemm_swiglu_keep, A.data_ptr(), p, out.data_ptr(), *kept._pointers(),
+               group_offsets.data_ptr(), _OUT_CODES[A.dtype], 1 if b_transposed else 0, G,
                M_total, N, K, _stream_handle(stream, dev)), "grouped_gemm_swiglu_keep")
     del keep
     return out, kept
@@ -1046,9 +1079,8 @@ def _kept_grad(dh, lddh: int, kept: Int8Matrix, with_h: bool, M: int, N: int, de
     dtype, inner = dh.dtype, N // 2
     dgu = _new((M, N), dtype, dev, stream)
     h = _new((M, inner), dtype, dev, stream) if with_h else None
-    _check(lib().swiglu_grad_int8(dh.data_ptr(), kept.codes.data_ptr(), kept.scales.data_ptr(), dgu.data_ptr(),
-                                  h.data_ptr() if with_h else None, _OUT_CODES[dtype], M, inner, lddh, N, inner,
-                                  handle), "swiglu_grad_int8")
+    _check(lib().swiglu_grad_int8(dh.data_ptr(), *kept._pointers(), dgu.data_ptr(), h.data_ptr() if with_h else None,
+                                  _OUT_CODES[dtype], M, inner, lddh, N, inner, handle), "swiglu_grad_int8")
     return dgu, h
 
 
@@ -1058,7 +1090,7 @@ def swiglu_grad(dh: torch.Tensor, kept: Int8Matrix, with_h: bool = False, stream
     _half(dh, "dh")
     M, N = _int8_check(kept, "kept", 2)
     dev = dh.device
-    if kept.codes.device != dev or dh.shape != (M, N // 2):
+    if kept.device != dev or dh.shape != (M, N // 2):
         raise ValueError("dh must be [%d, %d] on %s" % (M, N // 2, kept.device))
     dgu, h = _on(dev, _kept_grad, dh, _lead(dh, "dh"), kept, with_h, M, N, dev, stream,
                  _stream_handle(stream, dev))
@@ -1074,7 +1106,7 @@ def _block_operands(dh, x, kept, with_h: bool, N: int) -> tuple[int, int]:
         M, K = _int8_check(x, "x", 1)
     else:
         M, K = x.shape
-    if (x.codes if kept_x else x).device != dev:
+    if x.device != dev:
         raise ValueError("x must be on %s" % dev)
     if not kept_x and x.dtype is not dh.dtype:
         raise TypeError("x must have the dtype of dh, %s" % dh.dtype)
@@ -1083,7 +1115,7 @@ def _block_operands(dh, x, kept, with_h: bool, N: int) -> tuple[int, int]:
     if kept is None:
         if with_h:
             raise ValueError("with_h reads h from kept")
-    elif _int8_check(kept, "kept", 2) != (M, N) or kept.codes.device != dev:
+    elif _int8_check(kept, "kept", 2) != (M, N) or kept.device != dev:
         raise ValueError("kept must be [%d, %d] on %s, got %s" % (M, N, dev, tuple(kept.shape)))
     return M, K
 

@@ -266,6 +266,19 @@ def test_sizes_and_strides_past_32_bits_are_refused(rec):  # noqa: F811
     assert [n for n, _ in rec.calls if not n.startswith("bwg_")] == []
 
 
+def test_a_kept_matrix_shares_a_buffer(rec):  # noqa: F811
+    """Codes and scales of a call's own matrix are views, the scales on 256 bytes."""
+    for parts, blocks in ((1, 3), (2, 4)):
+        q = ops.quantize_int8(cuda(5, 130), parts=parts)
+        at, scales_at = rec.calls[-1][1][-3:-1]
+        assert q.shape == (5, 130) and scales_at - at == 768
+        assert q.codes.shape == (5, 130) and q.codes.dtype == torch.int8
+        assert q.scales.shape == (5, blocks) and q.scales.dtype == torch.float32
+        assert ops._int8_check(q, "q") == (5, 130)
+    with pytest.raises(ValueError):
+        ops.swiglu_grad(cuda(5, 65), ops.quantize_int8(cuda(5, 130)))
+
+
 def test_a_single_row_keeps_its_stride(rec):  # noqa: F811
     """One row of 60 columns in a buffer of 64: the TMA engine wants the 64."""
     ops.gemm_swiglu(wide(1, 60, 64), cuda(60, 128))
