@@ -12,17 +12,12 @@ using namespace bwg;
 namespace bwg {
 namespace {
 
-// H alone, 512x256 tiles.
-__global__ void __launch_bounds__(kThreads2C, 1) gated_2c_kernel(const __grid_constant__ DenseGatedParams p) {
-  gemm_body<2, 1, false, 2, kEpiSwiglu, false>(p, p);
-}
-
 // 256x256 tiles, whose accumulator is one of two, so that eight epilogue warps work
-// on one tile while the next is summed up: H alone where 512x256 tiles would be
-// too few, and the epilogues that read or write more, for which the tensor cores
-// would wait with 512x256 tiles.  8192 x 4096 x 8192, back to back: H 278 us; with
-// gate and up kept in 8 bits 302 (341 with 512x256 tiles), their gradient 325
-// (356).  What bounds them: tensor cores and the power limit.
+// on one tile while the next is summed up.  With 512x256 tiles, which load a quarter
+// less, the tensor cores wait for the epilogue at each tile's end: 8192 x 4096 x
+// 8192, back to back in turn, H 300 for 322 us (K = 512: 24.6 for 30.2; K = 8192:
+// 607 for 632); of another run, with gate and up kept in 8 bits 302 for 341, their
+// gradient 325 for 356.  What bounds them: tensor cores and the power limit.
 template <int EPI>
 __global__ void __launch_bounds__(kThreads2C, 1) gated_wide_kernel(const __grid_constant__ DenseGatedParams p) {
   gemm_body<2, 1, false, 1, EPI, false>(p, p);
@@ -35,11 +30,10 @@ __global__ void __launch_bounds__(kThreads2C, 1) gated_grouped_kernel(const __gr
 
 }  // namespace
 
-cudaError_t launch_gated_dense(const DenseGatedParams& p, int epi, bool two, int grid, size_t smem, cudaStream_t s) {
+cudaError_t launch_gated_dense(const DenseGatedParams& p, int epi, int grid, size_t smem, cudaStream_t s) {
   if (epi == kEpiSwigluKeep) return launch_pair_behind(gated_wide_kernel<kEpiSwigluKeep>, p, grid, smem, s);
   if (epi == kEpiSwigluGrad) return launch_pair_behind(gated_wide_kernel<kEpiSwigluGrad>, p, grid, smem, s);
-  return two ? launch_pair_behind(gated_2c_kernel, p, grid, smem, s)
-             : launch_pair_behind(gated_wide_kernel<kEpiSwiglu>, p, grid, smem, s);
+  return launch_pair_behind(gated_wide_kernel<kEpiSwiglu>, p, grid, smem, s);
 }
 
 cudaError_t launch_gated_grouped(const GroupedGatedParams& p, int epi, int grid, size_t smem, cudaStream_t s) {
@@ -48,8 +42,7 @@ cudaError_t launch_gated_grouped(const GroupedGatedParams& p, int epi, int grid,
 }
 
 cudaError_t set_gated_attributes(size_t smem) {
-  const void* fns[] = {reinterpret_cast<const void*>(gated_2c_kernel),
-                       reinterpret_cast<const void*>(gated_wide_kernel<kEpiSwiglu>),
+  const void* fns[] = {reinterpret_cast<const void*>(gated_wide_kernel<kEpiSwiglu>),
                        reinterpret_cast<const void*>(gated_wide_kernel<kEpiSwigluKeep>),
                        reinterpret_cast<const void*>(gated_wide_kernel<kEpiSwigluGrad>),
                        reinterpret_cast<const void*>(gated_grouped_kernel<kEpiSwigluKeep>),
@@ -159,11 +152,8 @@ void gated_params(const GatedCall& c, const Runtime& rt, int stages, GemmParams*
 
 bwg_status run_gated_dense(const GatedCall& c, const Runtime& rt, cudaStream_t stream) {
   const int I = c.N / 2, n_tiles = (I + kTileN / 2 - 1) / (kTileN / 2);
-  // two consumers while their tiles still give every pair one, as in gemm_bf16
-  const long long tiles_2c = static_cast<long long>((c.M + 4 * kRowsPerCta - 1) / (4 * kRowsPerCta)) * n_tiles;
-  const bool two = c.epi == kEpiSwiglu && tiles_2c >= rt.pairs_2c;
-  const int nc = two ? 2 : 1, stages = two ? 4 : 6;
-  const int smem = dense_smem(2, stages, false, nc);
+  constexpr int kStages = 6;
+  const int smem = dense_smem(2, kStages, false, 1);
   if (smem > rt.max_smem) return BWG_ERR_UNSUPPORTED;
   DenseGatedParams p;
   std::memset(&p, 0, sizeof(p));
@@ -186,14 +176,14 @@ bwg_status run_gated_dense(const GatedCall& c, const Runtime& rt, cudaStream_t s
     if (!ok) return BWG_ERR_CUDA;
     p.b_one_box = 1;
   }
-  gated_params(c, rt, stages, &p, &p.x);
-  const int tile_m = 2 * kRowsPerCta * nc;
+  gated_params(c, rt, kStages, &p, &p.x);
+  const int tile_m = 2 * kRowsPerCta;
   p.num_m_tiles = (c.M + tile_m - 1) / tile_m;
   const long long tiles = static_cast<long long>(p.num_m_tiles) * n_tiles;
   if (tiles > 0x3fffffff) return BWG_ERR_UNSUPPORTED;
   // with pairs for all their parts, few tiles are cut
-  p.workers = static_cast<int>(std::min<long long>(tiles * (two ? 4 : 2), two ? rt.pairs_2c : rt.pairs));
-  return runtime_status(launch_gated_dense(p, c.epi, two, 2 * p.workers, smem, stream));
+  p.workers = static_cast<int>(std::min<long long>(tiles * 2, rt.pairs));
+  return runtime_status(launch_gated_dense(p, c.epi, 2 * p.workers, smem, stream));
 }
 
 bwg_status run_gated_grouped(const GatedCall& c, const Runtime& rt, cudaStream_t stream) {

@@ -207,7 +207,7 @@ cudaError_t launch_grouped_2cta(const GroupedParams& p, int grid, size_t smem, c
 // Gated kernels (gemm_gated.cu): epi = 1 H (two: two consumers), 2 H and gate and
 // up in 8 bits, 3 the gradients of gate and up.  Grouped: 2 and 3, cluster launch
 // control.
-cudaError_t launch_gated_dense(const DenseGatedParams& p, int epi, bool two, int grid, size_t smem, cudaStream_t s);
+cudaError_t launch_gated_dense(const DenseGatedParams& p, int epi, int grid, size_t smem, cudaStream_t s);
 cudaError_t launch_gated_grouped(const GroupedGatedParams& p, int epi, int grid, size_t smem, cudaStream_t s);
 // Transposed A (gemm_tn.cu): two consumers with sums in TMEM, or one (joined)
 // whose sums are joined in registers; dynamic as above.
