@@ -701,7 +701,8 @@ __global__ void __launch_bounds__(kThreads, 1) small_m_kernel(const __grid_const
   }
 }
 
-__global__ void zero_fill_kernel(uint8_t* d, int rows, int row_bytes, size_t ld_bytes) {
+// (a row may be longer than 2^31 bytes)
+__global__ void zero_fill_kernel(uint8_t* d, int rows, size_t row_bytes, size_t ld_bytes) {
   const size_t total = static_cast<size_t>(rows) * row_bytes;
   for (size_t i = blockIdx.x * static_cast<size_t>(blockDim.x) + threadIdx.x; i < total;
        i += static_cast<size_t>(gridDim.x) * blockDim.x) {
@@ -757,10 +758,11 @@ int max_active_clusters_small_m(int cluster, size_t smem) {
 }
 
 cudaError_t launch_zero_fill(void* d, int rows, int cols, int ld, int elt_bytes, cudaStream_t s) {
-  const size_t total = static_cast<size_t>(rows) * cols * elt_bytes;
+  const size_t row_bytes = static_cast<size_t>(cols) * elt_bytes;
+  const size_t total = static_cast<size_t>(rows) * row_bytes;
   if (total == 0) return cudaSuccess;
   const int grid = static_cast<int>(std::min<size_t>((total + 255) / 256, 4096));
-  zero_fill_kernel<<<grid, 256, 0, s>>>(static_cast<uint8_t*>(d), rows, cols * elt_bytes,
+  zero_fill_kernel<<<grid, 256, 0, s>>>(static_cast<uint8_t*>(d), rows, row_bytes,
                                         static_cast<size_t>(ld) * elt_bytes);
   return cudaGetLastError();
 }

@@ -206,7 +206,7 @@ bwg_status run_tn(const TnCall& c, cudaStream_t stream) {
   const int oe = c.out_dtype == BWG_OUT_FP32 ? 4 : 2;
   if (c.rows == 0) {
     const long long all = static_cast<long long>(c.G) * c.M;
-    if (all > 0x7fffffffLL || static_cast<long long>(c.N) * oe > 0x7fffffffLL) return BWG_ERR_UNSUPPORTED;
+    if (all > 0x7fffffffLL) return BWG_ERR_UNSUPPORTED;
     return runtime_status(launch_zero_fill(c.d, static_cast<int>(all), c.N, c.ldd, oe, stream));
   }
   const int n_tiles = ceil_div(c.N, kTileN);
