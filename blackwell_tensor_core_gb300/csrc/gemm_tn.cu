@@ -132,14 +132,23 @@ double tn_waves(long long T, int C, int nc) {
   return static_cast<double>(full) + std::min(1.0, last);
 }
 
+// Rows that one sum in TMEM may take.  Every step of 16 rows cuts up to 2^-23 of the
+// sum, towards zero, so that sums of equal signs end short by up to rows / 16 2^-23
+// (measured: 0.85 of that, 1.3e-3 at 200000 rows): at most an eighth of the result's
+// rounding, 2^-11 in FP16 and 2^-8 in BF16.  FP32 results are joined at once.
+int tn_max_rows(int out_dtype) {
+  return out_dtype == BWG_OUT_FP32 ? kChunkBlocks * kBK : out_dtype == BWG_OUT_FP16 ? 8192 : 65536;
+}
+
 // The cheapest by an estimate in us: a tile's k-blocks, filling the ring and storing
 // the tile, and for slices a launch and 8 bytes an element of every plane at 6 TB/s.
 // 20011 rows of 1000 x 1416: 256x256 tiles in one slice 106 us, in three 58, 512x256
 // tiles in six 50.  At 13 sizes from 256 x 256 to 4096 x 8192 the chosen form is at
 // most 8% slower than the best of twenty (2.5% on average).
 TnPlan tn_plan(int M, int N, int rows, int G, int out_dtype, int pairs, int pairs_2c) {
-  // FP32 results keep what TMEM's sums lose (nothing over kChunkBlocks k-blocks)
-  const bool exact = out_dtype == BWG_OUT_FP32 && rows > kChunkBlocks * kBK;
+  // all rows may be one group's
+  const int max_rows = tn_max_rows(out_dtype);
+  const bool exact = out_dtype == BWG_OUT_FP32 && rows > max_rows;
   const double blocks = static_cast<double>(ceil_div(rows, kBK)) / G;
   TnPlan best{true, 1};
   double least = 0;
@@ -149,6 +158,7 @@ TnPlan tn_plan(int M, int N, int rows, int G, int out_dtype, int pairs, int pair
     const int all = nc == 2 ? pairs_2c : pairs;
     for (int s : {1, 2, 3, 4, 5, 6, 8, 10, 12, 16, 20, 24, 32}) {
       if (s > 1 && (blocks < 8.0 * s || tiles >= 2 * all)) break;
+      if (nc == 2 && ceil_div(ceil_div(rows, kBK), s) > max_rows / kBK) continue;
       double t = tn_waves(tiles * s, all, nc) * (blocks / s * (nc == 2 ? 0.56 : 0.40) + (nc == 2 ? 4.5 : 3.0));
       if (s > 1) t += 3.0 + static_cast<double>(G) * s * M * N * 8 / 6.0e6;
       if ((nc == 1 && s == 1) || t < least) {

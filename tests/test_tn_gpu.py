@@ -199,3 +199,29 @@ def test_stalled_calls_give_up(ops, shape, grouped, out):
     d = run()
     ref = a[:100].double().t() @ b[:100].double() if grouped else a.double().t() @ b.double()
     assert torch.equal((d[0] if grouped else d), ref.to(DT[out]))
+
+
+@pytest.mark.parametrize("grouped", [False, True])
+@pytest.mark.parametrize("dtype,rows", [("fp16", 8192), ("fp16", 8256), ("fp16", 200000), ("bf16", 65536),
+                                        ("bf16", 600000)])
+def test_long_sums_of_one_sign(ops, dtype, rows, grouped):
+    """16-bit results of wide products.  A sum on the tensor cores is cut towards
+    zero at every step of 16 rows, by up to 2^-23 of itself: however many rows, the
+    results are on average less than an eighth of a rounding short.  (The roundings
+    themselves, over 64 columns of 4096 spread over half a binade, average to less
+    than u / 128.)"""
+    M, N, dt = 4096, 8192, DT[dtype]
+    g = torch.Generator(device="cuda").manual_seed(rows)
+    a = torch.empty(rows, M, dtype=dt, device="cuda").uniform_(0.5, 1.5, generator=g)
+    a *= torch.empty(M, device="cuda").uniform_(0.5, 1.0, generator=g).to(dt)
+    b = torch.empty(rows, N, dtype=dt, device="cuda").uniform_(0.05, 0.15, generator=g)
+    if grouped:
+        d = ops.grouped_gemm_wgrad(a, b, gu.offsets([0, rows]))[1]
+    else:
+        d = ops.gemm(a, b, out_dtype=dt, a_transposed=True)
+    cols = torch.arange(64, device="cuda") * (N // 64) + 5
+    ref = torch.zeros(M, 64, dtype=torch.float64, device="cuda")
+    for at in range(0, rows, 50000):
+        ref += a[at:at + 50000].double().t() @ b[at:at + 50000, cols].double()
+    short = float(((d[:, cols].double() - ref) / ref).mean())
+    assert abs(short) <= gu.u(dt) * (1 / 8 + 1 / 128), short
