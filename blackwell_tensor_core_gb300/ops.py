@@ -840,7 +840,7 @@ class Int8Matrix:
     parts   1, or 2 for [gate | up], whose halves have blocks of their own
     """
 
-    __slots__ = ("_codes", "_scales", "parts", "_buffer", "_shape")
+    __slots__ = ("_codes", "_scales", "parts", "_buffer", "_shape", "_blocks")
 
     def __init__(self, codes, scales, parts=1):
         self._codes = codes
@@ -848,6 +848,7 @@ class Int8Matrix:
         self.parts = parts
         self._buffer = None
         self._shape = None
+        self._blocks = None
 
     @classmethod
     def _new(cls, rows: int, cols: int, parts: int, dev, stream):
@@ -855,7 +856,8 @@ class Int8Matrix:
         when they are asked for: a tensor costs a small call 4 us."""
         q = cls(None, None, parts)
         q._shape = rows, cols
-        q._buffer = _new((_int8_scales_at(rows, cols) + 4 * rows * _int8_blocks(cols, parts),), torch.int8, dev, stream)
+        q._blocks = _int8_blocks(cols, parts)
+        q._buffer = _new((_int8_scales_at(rows, cols) + 4 * rows * q._blocks,), torch.int8, dev, stream)
         return q
 
     @property
@@ -869,8 +871,7 @@ class Int8Matrix:
     def scales(self):
         if self._scales is None:
             rows, cols = self._shape
-            self._scales = self._buffer[_int8_scales_at(rows, cols):].view(torch.float32).view(
-                rows, _int8_blocks(cols, self.parts))
+            self._scales = self._buffer[_int8_scales_at(rows, cols):].view(torch.float32).view(rows, self._blocks)
         return self._scales
 
     @property
@@ -903,6 +904,9 @@ def _int8_check(q: Int8Matrix, name: str, parts: int | None = None) -> tuple[int
         raise ValueError("%s must have %s, got %r" % (name, "1 or 2 parts" if parts is None else "parts=%d" % parts,
                                                       q.parts))
     if q._buffer is not None:
+        cols = q._shape[1]
+        if cols % q.parts or _int8_blocks(cols, q.parts) != q._blocks:
+            raise ValueError("%s was not kept in %d parts" % (name, q.parts))
         return q._shape
     codes, scales = q._codes, q._scales
     if codes.dtype != torch.int8 or codes.dim() != 2 or not codes.is_contiguous() or not codes.is_cuda:

@@ -286,3 +286,23 @@ def test_a_single_row_keeps_its_stride(rec):  # noqa: F811
     assert rec.calls[0][1][10] == 64 and rec.calls[-1][1][8] == 64
     ops.gemm_swiglu(wide(1, 64, BIG + 64), cuda(64, 128))
     assert rec.calls[-1][1][10] == 64
+
+
+def test_parts_that_do_not_fit_the_scales(rec):  # noqa: F811
+    """Parts that are changed afterwards would have scales read behind their end;
+    halves of whole blocks have the same ones."""
+    q = ops.quantize_int8(cuda(5, 130))
+    q.parts = 2
+    odd = ops.quantize_int8(cuda(5, 65))
+    odd.parts = 2
+    del rec.calls[:]
+    for m in (q, odd):
+        with pytest.raises(ValueError):
+            ops.dequantize_int8(m)
+    with pytest.raises(ValueError):
+        ops.swiglu_grad(cuda(5, 65), q)
+    assert rec.calls == []
+    whole = ops.quantize_int8(cuda(5, 128))
+    whole.parts = 2
+    ops.swiglu_grad(cuda(5, 64), whole)
+    assert [n for n, _ in rec.calls] == ["quantize_int8", "swiglu_grad_int8"]
