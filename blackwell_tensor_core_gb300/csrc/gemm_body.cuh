@@ -34,7 +34,9 @@
 #include "ptx.cuh"
 #include "swiglu.cuh"
 
+#include <mutex>
 #include <type_traits>
+#include <unordered_map>
 
 namespace bwg {
 namespace {
@@ -1356,19 +1358,24 @@ cudaError_t launch_cluster(K kernel, const P& p, int cg, int grid, size_t smem, 
   return cudaLaunchKernelEx(&cfg, kernel, p);
 }
 
-// The two-consumer kernels split their registers with setmaxnreg after
-// set-up; the epilogue warpgroups' increase only completes if the CTA was
-// launched with at least the registers the split hands out.  Checked once
-// per kernel from the compiled register count: a smaller allocation would
-// leave the increase waiting for registers that never come free, so such a
-// kernel is not launched.
+// The kernels of 12 warps split their registers with setmaxnreg after set-up; the
+// epilogue warpgroups' increase only completes if the CTA was launched with at
+// least the registers the split hands out.  Checked once per kernel, which its
+// address tells apart (many share a type), from the compiled register count: a
+// smaller allocation would leave the increase waiting for registers that never
+// come free, so such a kernel is not launched.
 template <class K>
 bool two_consumer_regs_ok(K kernel) {
-  static const bool ok = [kernel] {
-    cudaFuncAttributes a;
-    if (cudaFuncGetAttributes(&a, kernel) != cudaSuccess) return false;
-    return static_cast<uint32_t>(a.numRegs) * kThreads2C >= kRegsControl2C * 128u + kRegsEpilogue2C * 256u;
-  }();
+  static std::mutex mu;
+  static std::unordered_map<const void*, bool> known;
+  const void* const fn = reinterpret_cast<const void*>(kernel);
+  std::lock_guard<std::mutex> lock(mu);
+  const auto it = known.find(fn);
+  if (it != known.end()) return it->second;
+  cudaFuncAttributes a;
+  if (cudaFuncGetAttributes(&a, fn) != cudaSuccess) return false;
+  const bool ok = static_cast<uint32_t>(a.numRegs) * kThreads2C >= kRegsControl2C * 128u + kRegsEpilogue2C * 256u;
+  known.emplace(fn, ok);
   return ok;
 }
 
