@@ -289,7 +289,6 @@ __global__ void __launch_bounds__(kThreads, 1) small_m_kernel(const __grid_const
   }
   if constexpr (SW) {  // launched while the work before may still be running
     grid_dependency_wait();
-    grid_dependents_launch();
   }
   if (threadIdx.x == 0) producer.issue(S, &aborted);
   if (warp == 1) {
@@ -303,6 +302,8 @@ __global__ void __launch_bounds__(kThreads, 1) small_m_kernel(const __grid_const
   else
     __syncthreads();
   tc_fence_after();
+  // this CTA holds its TMEM: a kernel let in before could take it and wait for this grid
+  if constexpr (SW) grid_dependents_launch();
   const uint32_t tmem_base = ld_shared_u32(tmem_slot);
 
   if (warp == 0) {

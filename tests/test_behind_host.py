@@ -46,3 +46,19 @@ def test_the_shared_body_waits():
     assert offsets < body.index("grouped_tables_warp(p.group_offsets", behind)  # the warp that reads the offsets
     roles = body.index("if constexpr (kBehind) {\n    grid_dependency_wait();", offsets)
     assert roles < body.index("tma_load_", behind) and roles < body.index("emit = [&]", behind)
+
+
+def test_dependents_are_let_in_after_the_kernels_own_tmem():
+    """A kernel that allocates TMEM without a limit on its wait must hold it before it
+    lets the kernel behind it become resident: that one could take it first, and then
+    wait for this grid to end."""
+    for name in sources():
+        text = read(name)
+        for kernel in re.split(r"__global__|__device__ void gemm_body", text)[1:]:
+            alloc = [m.start() for m in re.finditer(r"\btmem_alloc<", kernel)]
+            trigger = [m.start() for m in re.finditer(r"\bgrid_dependents_launch\(\)", kernel)]
+            if not alloc or not trigger:
+                continue
+            assert len(alloc) == 1
+            barrier = re.compile(r"\b(cluster_sync_all|__syncthreads)\(\)").search(kernel, alloc[0])
+            assert barrier and barrier.start() < min(trigger), name
