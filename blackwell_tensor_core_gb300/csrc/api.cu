@@ -307,7 +307,7 @@ bwg_status plan_dense(int M, int N, int K, int out_dtype, bool fp16_in, int sm_c
                       int force_kernel, int force_stages, int max_clusters_2cta, int max_ctas_1cta,
                       int max_clusters_mc, int max_clusters_2c, bwg_plan_info* o,
                       const int* small_clusters = nullptr, bool force_streamk = false,
-                      bool b_kmajor = false) {
+                      bool b_kmajor = false, bool no_workspace = false) {
   std::memset(o, 0, sizeof(*o));
   if (M == 0 || N == 0) {
     o->kernel = BWG_KERNEL_NONE;
@@ -379,6 +379,7 @@ bwg_status plan_dense(int M, int N, int K, int out_dtype, bool fp16_in, int sm_c
       streamk = 1;
       split = 1;
     }
+    if (no_workspace) streamk = 0;
     // With one tile per CTA the stage ring is idle when the epilogue runs, so
     // the output staging tile lives in it and the ring gets one stage deeper.
     const bool in_ring = !streamk && (split > 1 || o->tiles <= sm_count);
@@ -466,7 +467,7 @@ bwg_status plan_dense(int M, int N, int K, int out_dtype, bool fp16_in, int sm_c
       const char* env = std::getenv("BWG_STREAMK_DENSE");
       int segs = 0;
       int sk = 0;
-      if (env != nullptr && env[0] == '1')
+      if (env != nullptr && env[0] == '1' && !no_workspace)
         sk = streamk_tiles(base_units, C, o->k_blocks, 1 << 30, &segs);
       (void)cut_cost;
       if (sk > 0) {
@@ -731,6 +732,8 @@ bwg_status launch_status(cudaError_t e) {
 bwg_status run_dense(bool fp16_in, const void* A, const void* B, void* D, int M, int N, int K,
                      int lda, int ldb, int ldd, int out_dtype, cudaStream_t stream,
                      bool b_kmajor = false) {
+  const bool no_workspace = (out_dtype & BWG_NO_WORKSPACE) != 0;
+  out_dtype &= ~BWG_NO_WORKSPACE;
   bwg_status s = check_args(A, B, D, M, N, K, lda, ldb, ldd, out_dtype, b_kmajor);
   if (s != BWG_OK) return s;
   if (M == 0 || N == 0) return BWG_OK;
@@ -739,7 +742,7 @@ bwg_status run_dense(bool fp16_in, const void* A, const void* B, void* D, int M,
   bwg_plan_info pl;
   s = plan_dense(M, N, K, out_dtype, fp16_in, st->sm_count, st->max_smem, force_kernel_from_env(),
                  force_stages_from_env(), st->clusters_2cta, st->ctas_1cta, st->clusters_mc,
-                 st->clusters_2c, &pl, st->clusters_small, false, b_kmajor);
+                 st->clusters_2c, &pl, st->clusters_small, false, b_kmajor, no_workspace);
   if (s != BWG_OK) return s;
   if (pl.kernel == BWG_KERNEL_ZERO)
     return launch_status(launch_zero_fill(D, M, N, ldd, out_elt(out_dtype), stream));

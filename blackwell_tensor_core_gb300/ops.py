@@ -21,6 +21,7 @@ LIB_PATH = os.path.join(_HERE, "libbwgemm.so")
 OUT_BF16 = 0
 OUT_FP32 = 1
 OUT_FP16 = 2
+NO_WORKSPACE = 0x100  # or-ed into the output type of a dense product
 _OUT_CODES = {torch.bfloat16: OUT_BF16, torch.float32: OUT_FP32, torch.float16: OUT_FP16}
 
 KERNEL_NONE, KERNEL_ZERO, KERNEL_1CTA, KERNEL_2CTA, KERNEL_SMALL_M, KERNEL_2CTA_MC, KERNEL_2CTA_2C = range(7)
@@ -1160,7 +1161,9 @@ def _block_grad(dh, lddh, x, ldx, w, ldw, kept, with_h, b_transposed, need_dx, n
     if need_dx:  # w [K, N] is the second operand as [out, in]
         dx = _new((M, K), dtype, dev, stream)
         name = ("gemm_bf16" if code == OUT_BF16 else "gemm_fp16") + ("" if b_transposed else "_nt")
-        _check(getattr(L, name)(dgu.data_ptr(), w.data_ptr(), dx.data_ptr(), M, K, N, N, ldw, K, code, handle), name)
+        # no scratch of the stream's: captured steps of one stream may run at once
+        _check(getattr(L, name)(dgu.data_ptr(), w.data_ptr(), dx.data_ptr(), M, K, N, N, ldw, K, code | NO_WORKSPACE,
+                                handle), name)
     if need_dw:
         rows, cols, a, lda, b, ldb = (N, K, dgu, N, x, ldx) if b_transposed else (K, N, x, ldx, dgu, N)
         dw = _new((rows, cols), dtype, dev, stream)

@@ -47,6 +47,11 @@ typedef enum {
 
 typedef enum { BWG_OUT_BF16 = 0, BWG_OUT_FP32 = 1, BWG_OUT_FP16 = 2 } bwg_out_dtype;
 
+/* Or-ed into the out_dtype of gemm_bf16, gemm_fp16 and their _nt forms: the call
+ * uses no workspace of the library (see gemm_bf16), so that it can be the first of
+ * its stream in a capture and graphs that hold it can run at once. */
+#define BWG_NO_WORKSPACE 0x100
+
 /*
  * D[M,N] = A[M,K] x B[K,N]; A and B BF16; FP32 accumulation; D in out_dtype.
  * "使用 Warp Specialization 和 Cluster 扩展 GEMM" (steps 7-8) describes the
@@ -66,8 +71,10 @@ typedef enum { BWG_OUT_BF16 = 0, BWG_OUT_FP32 = 1, BWG_OUT_FP16 = 2 } bwg_out_dt
  *   default stream of each host thread has its own).  A call that would have
  *   to grow that workspace while its stream is being captured into a CUDA
  *   graph returns BWG_ERR_UNSUPPORTED: make one eager call of the largest
- *   shape on the stream first, from the host thread that captures.  Callers that must never see the library
- *   allocate can use gemm_bf16_small_m_noalloc below.
+ *   shape on the stream first, from the host thread that captures.  Graphs
+ *   captured on one stream share its workspace and must not run at once.
+ *   BWG_NO_WORKSPACE takes whole tiles instead.  Callers that must never see the
+ *   library allocate can use gemm_bf16_small_m_noalloc below.
  *   The library also holds a TMA-multicast variant of the pair kernel (two
  *   CTA pairs receive every box of B), selected only by the environment
  *   override BWG_FORCE_KERNEL=2cta_mc; it reads only device memory of the
@@ -345,7 +352,7 @@ const char* bwg_status_string(int status);
  *   dGU = [dgate | dup] [M, N], dgate = dH * up * s (1 + gate (1 - s)) with
  *   s = 1 / (1 + e^-gate), dup = dH * silu(gate); gate and up are multiplied out
  *   again and only dGU is written.  The gradients of X and W are the products
- *   dGU W^T (gemm_*_nt) and X^T dGU (gemm_tn).
+ *   dGU W^T (gemm_*_nt, in a capture with BWG_NO_WORKSPACE) and X^T dGU (gemm_tn).
  * No output overlaps an input or another output.
  * The grouped forms take expert e's rows (group_offsets as for grouped_gemm_bf16,
  * with its contract and its report of broken ones) with W[e] (a host array of G

@@ -463,3 +463,36 @@ def test_stalled_calls_give_up(ops, call):
     assert st == 5 and (word >> 56) == 1, (st, hex(word))
     h = ops.gemm_swiglu(x, w)
     gu.assert_close(h, *gu.forward(*gu.gated(x, w), x.dtype), "h after the stall")
+
+
+# few rows and a wide dX: 76 tiles of 2 k-blocks and 160 tiles on 152 SMs, where the product's
+# k-blocks would be shared out through a workspace of the stream's
+@pytest.mark.parametrize("transposed", [False, True])
+@pytest.mark.parametrize("M,K,N", [(72, 9728, 128), (17, 20480, 256)])
+def test_captured_steps_of_few_rows(ops, M, K, N, transposed):
+    """The first calls of a stream, in captures; the two graphs then run at once."""
+    sets = []
+    for i in range(2):
+        x, w, dh = data(M, K, N, torch.bfloat16, 60 + i)
+        sets.append((dh, x, w.t().contiguous() if transposed else w))
+    want = []
+    for dh, x, w in sets:
+        r = ops.gemm_swiglu_grad(dh, x, w, b_transposed=transposed)
+        want.append((r.dx.clone(), r.dw.clone()))
+        d, e = gu.backward(dh, *gu.gated(x, w.t() if transposed else w), x.dtype)
+        gu.assert_close(r.dx, *gu.through(d, e, w.double() if transposed else w.double().t(), 0.0, x.dtype), "dx")
+    torch.cuda.synchronize()
+    graphs, outs, side = [], [], torch.cuda.Stream()
+    for dh, x, w in sets:
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, stream=side):
+            outs.append(ops.gemm_swiglu_grad(dh, x, w, b_transposed=transposed))
+        graphs.append(g)
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    for _ in range(50):
+        for st, g in zip(streams, graphs):
+            with torch.cuda.stream(st):
+                g.replay()
+    torch.cuda.synchronize()
+    for r, (dx, dw) in zip(outs, want):
+        assert torch.equal(r.dx, dx) and torch.equal(r.dw, dw)

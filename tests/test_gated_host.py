@@ -306,3 +306,23 @@ def test_parts_that_do_not_fit_the_scales(rec):  # noqa: F811
     whole.parts = 2
     ops.swiglu_grad(cuda(5, 64), whole)
     assert [n for n, _ in rec.calls] == ["quantize_int8", "swiglu_grad_int8"]
+
+
+def test_dx_uses_no_workspace_of_the_library(rec, lib):  # noqa: F811
+    """The flag goes with every dX; the dense products take it beside a type, no other call does."""
+    for transposed, w in ((False, cuda(64, 128)), (True, cuda(128, 64))):
+        for dtype, name in ((torch.bfloat16, "gemm_bf16"), (torch.float16, "gemm_fp16")):
+            del rec.calls[:]
+            ops.gemm_swiglu_grad(cuda(4, 64, dtype=dtype), cuda(4, 64, dtype=dtype), w.to(dtype),
+                                 b_transposed=transposed)
+            (args,) = [a for n, a in rec.calls if n == name + ("" if transposed else "_nt")]
+            assert args[9] == ops._OUT_CODES[dtype] | ops.NO_WORKSPACE
+
+    def dense(fn, out, M=0, a=A):
+        return fn(a, B, C, M, 128, 64, 64, 128, 128, out, None)
+
+    for fn in (lib.gemm_bf16, lib.gemm_fp16, lib.gemm_bf16_nt, lib.gemm_fp16_nt):
+        assert dense(fn, 0x100) == dense(fn, 0x101) == dense(fn, 0x102) == OK
+        assert dense(fn, 0x103) == dense(fn, 0x200) == dense(fn, 0x100, 4, None) == INVALID
+        assert dense(fn, 0x100, 4, A + 8) == ALIGNMENT
+    assert dense(lib.gemm_bf16_small_m_noalloc, 0x100) == INVALID
