@@ -1125,6 +1125,28 @@ def _block_operands(dh, x, kept, with_h: bool, N: int) -> tuple[int, int]:
     return M, K
 
 
+def _block_sizes(M: int, N: int, K: int, whole_rows: bool) -> None:
+    """What the chain's later calls would refuse after its first ones have run."""
+    if N % 16 and M:
+        raise ValueError("w must hold gate and up in multiples of 8 columns each, got %d" % N)
+    if K % 8 and whole_rows:
+        raise ValueError("gradients of %d columns: their rows must be whole 16 bytes, multiples of 8" % K)
+
+
+def _rows16(what: str, *matrices) -> None:
+    """The same of matrices that the TMA engine reads: (tensor, row stride) of each."""
+    for t, ld in matrices:
+        if (ld % 8 or t.data_ptr() % 16) and t.numel():
+            raise BwgError(2, what)
+
+
+def _read_back(q: Int8Matrix, K: int, dtype, dev, stream) -> torch.Tensor:
+    """The values of q in rows of whole 16 bytes."""
+    if K % 8 == 0:
+        return dequantize_int8(q, out_dtype=dtype, stream=stream)
+    return dequantize_int8(q, out=_new((q.shape[0], -(-K // 8) * 8), dtype, dev, stream)[:, :K], stream=stream)
+
+
 def gemm_swiglu_grad(dh: torch.Tensor, x, w: torch.Tensor, kept: Int8Matrix | None = None, with_h: bool = False,
                      b_transposed: bool = False, need_dx: bool = True, need_dw: bool = True,
                      stream=None) -> SwigluGrad:
@@ -1137,12 +1159,18 @@ def gemm_swiglu_grad(dh: torch.Tensor, x, w: torch.Tensor, kept: Int8Matrix | No
     dev = dh.device
     N, ldw = _gated_weight(w, dh.dtype, dev, x.shape[-1], b_transposed)
     M, K = _block_operands(dh, x, kept, with_h, N)
-    if K % 8 and (need_dx or (need_dw and b_transposed)):
-        raise ValueError("gradients of %d columns: their rows must be whole 16 bytes, multiples of 8" % K)
+    _block_sizes(M, N, K, need_dx or (need_dw and b_transposed))
     lddh = _lead(dh, "dh")
-    if isinstance(x, Int8Matrix):
-        x = dequantize_int8(x, out_dtype=dh.dtype, stream=stream) if need_dw or kept is None else None
-    ldx = _lead(x, "x") if x is not None else 0
+    if M:
+        _rows16("gemm_swiglu_grad", (dh, lddh), *([(w, ldw)] if need_dx or kept is None else []))
+    if not need_dw and kept is not None:
+        x, ldx = None, 0
+    elif isinstance(x, Int8Matrix):
+        x = _read_back(x, K, dh.dtype, dev, stream)
+        ldx = _lead(x, "x")
+    else:
+        ldx = _lead(x, "x")
+        _rows16("gemm_swiglu_grad", (x, ldx))
     return _on(dev, _block_grad, dh, lddh, x, ldx, w, ldw, kept, with_h, b_transposed, need_dx, need_dw, M, N, K, dev,
                stream)
 
@@ -1192,19 +1220,28 @@ def grouped_gemm_swiglu_grad(dh: torch.Tensor, x, ws: list, group_offsets: torch
         raise ValueError("weights of %s do not fit x with %d columns" % (tuple(shape), x.shape[-1]))
     M, K = _block_operands(dh, x, kept, with_h, N)
     _fits("rows, columns or groups", M, K, N, G)
-    if isinstance(x, Int8Matrix):
-        x = dequantize_int8(x, out_dtype=dtype, stream=stream) if need_dw or kept is None else None
-    if not dh.is_contiguous() or (x is not None and not x.is_contiguous()):
+    reads_x, reads_w = need_dw or kept is None, need_dx or kept is None
+    _block_sizes(M, N, K, M > 0 and (reads_x or reads_w))
+    kept_x = isinstance(x, Int8Matrix)
+    if not dh.is_contiguous() or (reads_x and not kept_x and not x.is_contiguous()):
         raise ValueError("dh and x must be dense")
-    return _on(dev, _experts_grad, dh, x, ws, group_offsets, kept, with_h, b_transposed, need_dx, need_dw, G, M, N, K,
+    at = [w.data_ptr() for w in ws]
+    if M and (dh.data_ptr() % 16 or (reads_x and not kept_x and x.data_ptr() % 16) or
+              (reads_w and any(p % 16 for p in at))):
+        raise BwgError(2, "grouped_gemm_swiglu_grad")
+    if not reads_x:
+        x = None
+    elif kept_x:
+        x = dequantize_int8(x, out_dtype=dtype, stream=stream)
+    return _on(dev, _experts_grad, dh, x, at, group_offsets, kept, with_h, b_transposed, need_dx, need_dw, G, M, N, K,
                dev, stream)
 
 
-def _experts_grad(dh, x, ws, group_offsets, kept, with_h, b_transposed, need_dx, need_dw, G, M, N, K, dev,
+def _experts_grad(dh, x, at, group_offsets, kept, with_h, b_transposed, need_dx, need_dw, G, M, N, K, dev,
                   stream) -> SwigluGrad:
     dtype, L, handle = dh.dtype, lib(), _stream_handle(stream, dev)
     code = _OUT_CODES[dtype]
-    p, keep = _ptr_array([w.data_ptr() for w in ws])
+    p, keep = _ptr_array(at)
     if kept is not None:
         dgu, h = _kept_grad(dh, N // 2, kept, with_h, M, N, dev, stream, handle)
     else:

@@ -496,3 +496,22 @@ def test_captured_steps_of_few_rows(ops, M, K, N, transposed):
     torch.cuda.synchronize()
     for r, (dx, dw) in zip(outs, want):
         assert torch.equal(r.dx, dx) and torch.equal(r.dw, dw)
+
+
+@pytest.mark.parametrize("from_8_bits", [False, True])
+@pytest.mark.parametrize("M", [1, 300])
+def test_a_kept_input_of_columns_that_end_inside_16_bytes(ops, M, from_8_bits):
+    """x of 100 columns in rows of 104, kept in 8 bits: dw is that of the values that were kept."""
+    x, w, dh = data(M, 104, 144, torch.bfloat16, 35)
+    x, w = x[:, :100], w[:100]
+    q = ops.quantize_int8(x)
+    kept = ops.gemm_swiglu(x, w, keep_int8=True)[1] if from_8_bits else None
+    got = ops.gemm_swiglu_grad(dh, q, w, kept=kept, need_dx=False)
+    rows = torch.full((M, 104), float("nan"), dtype=x.dtype, device="cuda")[:, :100]
+    want = ops.gemm_swiglu_grad(dh, ops.dequantize_int8(q, out=rows), w, kept=kept, need_dx=False)
+    assert torch.equal(got.dw, want.dw) and got.dx is None
+    if not from_8_bits:
+        d, e = gu.backward(dh, *gu.gated(rows, w), x.dtype)
+        gu.assert_close(got.dw, *gu.through(rows.double().t(), 0.0, d, e, x.dtype), "dw")
+    with pytest.raises(ValueError):
+        ops.gemm_swiglu_grad(dh, q, w, kept=kept)

@@ -326,3 +326,63 @@ def test_dx_uses_no_workspace_of_the_library(rec, lib):  # noqa: F811
         assert dense(fn, 0x103) == dense(fn, 0x200) == dense(fn, 0x100, 4, None) == INVALID
         assert dense(fn, 0x100, 4, A + 8) == ALIGNMENT
     assert dense(lib.gemm_bf16_small_m_noalloc, 0x100) == INVALID
+
+
+def off16(rows, cols):
+    """A matrix that starts 2 bytes behind an aligned address."""
+    return cuda(rows * cols + 8)[1:rows * cols + 1].view(rows, cols)
+
+
+def test_gradients_are_refused_before_anything_runs(rec, monkeypatch):  # noqa: F811
+    """Sizes and addresses that a later call of the chain would refuse."""
+    # fake tensors have no address: the offset in their storage stands for it
+    monkeypatch.setattr(torch.Tensor, "data_ptr", lambda t: 4096 + 2 * t.storage_offset())
+    off = cuda(3, dtype=torch.int32)
+    x8, kept = int8(4, 64), int8(4, 128, 2)
+    w, dh, x = cuda(64, 128), cuda(4, 64), cuda(4, 64)
+    for call in (
+        # K no multiple of 8
+        lambda: ops.grouped_gemm_swiglu_grad(dh, int8(4, 60), [cuda(60, 128)] * 2, off, kept=kept),
+        lambda: ops.grouped_gemm_swiglu_grad(dh, cuda(4, 60), [cuda(60, 128)] * 2, off),
+        lambda: ops.grouped_gemm_swiglu_grad(dh, cuda(4, 60), [cuda(128, 60)] * 2, off, b_transposed=True),
+        lambda: ops.gemm_swiglu_grad(dh, int8(4, 60), cuda(60, 128), kept=kept),
+        # halves of w that start off 16 bytes
+        lambda: ops.gemm_swiglu_grad(cuda(4, 60), x8, cuda(64, 120), kept=int8(4, 120, 2)),
+        lambda: ops.grouped_gemm_swiglu_grad(cuda(4, 60), x8, [cuda(64, 120)] * 2, off, kept=int8(4, 120, 2)),
+        # rows of dh that are no rows of its experts' matrix
+        lambda: ops.grouped_gemm_swiglu_grad(wide(4, 64, 72), x8, [w, w], off, kept=kept),
+        # addresses and row strides off 16 bytes
+        lambda: ops.gemm_swiglu_grad(dh, x8, off16(64, 128), kept=kept),
+        lambda: ops.gemm_swiglu_grad(dh, x8, wide(64, 128, 132), kept=kept),
+        lambda: ops.gemm_swiglu_grad(dh, off16(4, 64), w, kept=kept),
+        lambda: ops.gemm_swiglu_grad(dh, wide(4, 64, 68), w, kept=kept),
+        lambda: ops.gemm_swiglu_grad(off16(4, 64), x8, w, kept=kept),
+        lambda: ops.gemm_swiglu_grad(wide(4, 64, 68), x8, w, kept=kept),
+        lambda: ops.grouped_gemm_swiglu_grad(dh, x8, [w, off16(64, 128)], off, kept=kept),
+        lambda: ops.grouped_gemm_swiglu_grad(dh, off16(4, 64), [w, w], off, kept=kept),
+        lambda: ops.grouped_gemm_swiglu_grad(off16(4, 64), x8, [w, w], off, kept=kept),
+    ):
+        with pytest.raises((ValueError, ops.BwgError)):
+            call()
+        assert [n for n, _ in rec.calls if not n.startswith("bwg_")] == []
+    # what is not read may lie anywhere, and so may matrices without rows
+    del rec.calls[:]
+    ops.gemm_swiglu_grad(dh, off16(4, 64), w, kept=kept, need_dw=False)
+    ops.gemm_swiglu_grad(dh, x, off16(64, 128), kept=kept, need_dx=False, need_dw=False)
+    ops.grouped_gemm_swiglu_grad(dh, off16(4, 60), [off16(60, 128)] * 2, off, kept=kept, need_dx=False, need_dw=False)
+    assert [n for n, _ in rec.calls] == ["swiglu_grad_int8", "gemm_bf16_nt", "swiglu_grad_int8", "swiglu_grad_int8"]
+    ops.gemm_swiglu_grad(cuda(0, 60), cuda(0, 64), off16(64, 120), need_dw=False)
+    ops.grouped_gemm_swiglu_grad(cuda(0, 64), cuda(0, 60), [cuda(60, 128)] * 2, off)
+
+
+def test_a_kept_input_is_read_back_into_whole_16_bytes(rec):  # noqa: F811
+    """x of 60 columns kept in 8 bits: its rows come back 64 apart, and dw is taken as
+    it is of the x that it was kept from."""
+    for kept in (None, int8(4, 128, 2)):
+        del rec.calls[:]
+        ops.gemm_swiglu_grad(cuda(4, 64), int8(4, 60), cuda(60, 128), kept=kept, need_dx=False)
+        args = dict(rec.calls)
+        assert args["dequantize_int8"][5:8] == (4, 60, 64)
+        assert args["gemm_tn"][5:9] == (60, 128, 4, 64)
+        if kept is None:
+            assert args["gemm_swiglu_grad"][6:11] == (4, 128, 60, 64, 64)
