@@ -949,12 +949,10 @@ def dequantize_int8(q: Int8Matrix, out_dtype: torch.dtype = torch.bfloat16, out:
 
 
 def _lead(t: torch.Tensor, name: str) -> int:
-    """Leading dimension of a matrix for the TMA engine: a single row keeps the
-    stride that it has, where that is one."""
+    """Leading dimension of a matrix of 16-bit elements for the TMA engine: for a
+    single row, which torch gives any stride, its end rounded up to 16 bytes."""
     ld = _rows(t, name, t.shape[0])
-    if t.shape[0] == 1 and ld < t.stride(0) <= _INT_MAX:
-        return t.stride(0)
-    return ld
+    return -(-ld // 8) * 8 if t.shape[0] == 1 else ld
 
 
 def _half(t: torch.Tensor, name: str) -> None:

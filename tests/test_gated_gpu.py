@@ -515,3 +515,18 @@ def test_a_kept_input_of_columns_that_end_inside_16_bytes(ops, M, from_8_bits):
         gu.assert_close(got.dw, *gu.through(rows.double().t(), 0.0, d, e, x.dtype), "dw")
     with pytest.raises(ValueError):
         ops.gemm_swiglu_grad(dh, q, w, kept=kept)
+
+
+@pytest.mark.parametrize("K", [64, 60])
+def test_a_single_row_of_any_stride(ops, K):
+    """One row whose stride is no multiple of 8, or less than the row, gives what a dense one does."""
+    x, w, dh = data(1, K, 144, torch.bfloat16, 36)
+    want = ops.gemm_swiglu_grad(dh, padded(x, 4 if K == 60 else 8)[1], w, need_dx=K == 64)
+    h = ops.gemm_swiglu(padded(x, 4 if K == 60 else 8)[1], w)
+    for ld in (61, 1):
+        xs, ds = x.as_strided(x.shape, (ld, 1)), dh.as_strided(dh.shape, (ld, 1))
+        assert torch.equal(ops.gemm_swiglu(xs, w), h)
+        got = ops.gemm_swiglu_grad(ds, xs, w, need_dx=K == 64)
+        assert torch.equal(got.dw, want.dw) and (K == 60 or torch.equal(got.dx, want.dx))
+        d = ops.gemm(xs, ds, a_transposed=True, out_dtype=torch.float32)
+        gu.assert_close(d, x.double().t() @ dh.double(), 2.0 ** -22 * (x.double().abs().t() @ dh.double().abs()), "d")

@@ -386,3 +386,15 @@ def test_a_kept_input_is_read_back_into_whole_16_bytes(rec):  # noqa: F811
         assert args["gemm_tn"][5:9] == (60, 128, 4, 64)
         if kept is None:
             assert args["gemm_swiglu_grad"][6:11] == (4, 128, 60, 64, 64)
+
+
+def test_a_single_row_has_a_stride_that_fits(rec):  # noqa: F811
+    """One row may come with any stride, or with none that the TMA engine takes: its
+    end rounded up to 16 bytes stands for it."""
+    for ld in (61, 60, 1, 4099):
+        ops.gemm_swiglu(wide(1, 60, ld), cuda(60, 128))
+        assert rec.calls[-1][1][10] == 64
+        ops.gemm(wide(1, 64, ld), wide(1, 128, ld), a_transposed=True)
+        assert rec.calls[-1][1][8:10] == (64, 128)
+        ops.swiglu_grad(wide(1, 64, ld), int8(1, 128, 2))
+        assert rec.calls[-1][1][8] == 64
