@@ -7,7 +7,7 @@
 // Both quotients are rounded to FP32 and the product with the second is rounded
 // once, to the integer.  A matrix in two parts (gate and up) has blocks of its
 // own in each.  A block with an infinity or a NaN in it reads back as NaN; one
-// whose largest magnitude is below 2^-121 as zero.
+// whose largest magnitude is at most 127 * 2^-128 (0.992 * 2^-121) as zero.
 //
 // What bounds these kernels: HBM.  One pass; four lanes share a block, 16 columns
 // each (32 bytes, one load), so that its maximum takes two exchanges and a warp

@@ -49,8 +49,8 @@ BWG_DEV float max_abs_nan(float a, float b) {
 }
 
 // Scale and reciprocal of a block whose largest magnitude is `amax`: a / 127 and
-// 127 / a, each rounded once.  Below 2^-121, where 127 / a passes FP32's range,
-// the block is zero; with an infinity or a NaN in it it reads back as NaN.
+// 127 / a, each rounded once.  Up to a = 127 * 2^-128, where 127 / a passes FP32's
+// range, the block is zero; with an infinity or a NaN in it it reads back as NaN.
 BWG_DEV void int8_scale(float amax, float* scale, float* inv) {
   *inv = 127.0f / amax;
   *scale = amax / 127.0f;

@@ -375,7 +375,7 @@ bwg_status grouped_gemm_swiglu_grad(const void* dH, const void* X, const void* c
  *   scale = a / 127, code = rint(x * (127 / a)), value = code * scale
  * with a the block's largest magnitude, both quotients rounded to FP32 and the
  * code rounded once, ties to even.  A block with an infinity or a NaN in it reads
- * back as NaN; one whose a is below 2^-121 as zeros.
+ * back as NaN; one whose a is at most 127 * 2^-128 as zeros.
  *   quantize_int8: x [M, N] of dtype (BF16, FP16 or FP32; any N that the parts
  *     divide, any ldx >= N) into codes int8 [M, N] and scales FP32
  *     [M, parts * ceil(N / parts / 64)], both dense.

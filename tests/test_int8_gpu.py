@@ -110,3 +110,20 @@ def test_more_elements_than_an_int(ops):
     codes, scales = gu.keep(x[-1:].float())
     assert torch.equal(q.codes[-1:].double(), codes) and torch.equal(q.scales[-1:], scales)
     assert bool((q.scales[:-1] == 0).all())
+
+
+@pytest.mark.parametrize("cols", [64, 77])
+def test_where_a_block_becomes_zero(ops, cols):
+    """127 / a passes FP32's range from a = 127 * 2^-128 down: those blocks are zero, the
+    next number above is kept (its scale has 21 bits: half a code and 2^-21)."""
+    edge = 127 * 2.0 ** -128
+    x = torch.zeros(4, cols, device="cuda")
+    for r, a in enumerate((edge * (1 - 2.0 ** -20), edge, edge * (1 + 2.0 ** -22), 0.995 * 2.0 ** -121)):
+        x[r] = a
+        x[r, ::3] = -a / 3
+    q = ops.quantize_int8(x)
+    y = ops.dequantize_int8(q, out_dtype=torch.float32)
+    assert not q.scales[:2].any() and not y[:2].any()
+    off = (y[2:].double() - x[2:].double()).abs()
+    a = x[2:].double().abs().amax(1, keepdim=True)
+    assert bool((off <= (0.5 / 127 + 2.0 ** -20) * a).all())
