@@ -225,3 +225,25 @@ def test_long_sums_of_one_sign(ops, dtype, rows, grouped):
         ref += a[at:at + 50000].double().t() @ b[at:at + 50000, cols].double()
     short = float(((d[:, cols].double() - ref) / ref).mean())
     assert abs(short) <= gu.u(dt) * (1 / 8 + 1 / 128), short
+
+
+@pytest.mark.parametrize("out", ["bf16", "fp32"])
+@pytest.mark.parametrize("counts", [[7, 0] * 40, [64, 1, 0] * 30, [130, 3] * 35], ids=lambda c: "x".join(map(str, c[:3])))
+def test_every_one_of_many_groups(ops, counts, out):
+    """More groups than a launch takes: each of them within its bound, but for four
+    that hold NaN, on both sides of the launches' border, and those alone hold NaN."""
+    rows, M, N = sum(counts), 136, 200
+    a, b = draw(rows, M, torch.bfloat16, 40), draw(rows, N, torch.bfloat16, 41)
+    bounds = gu.offsets(counts).tolist()
+    full = [g for g, c in enumerate(counts) if c]
+    bad = {full[0], max(g for g in full if g < 64), min(g for g in full if g >= 64), full[-1]}
+    for g in bad:
+        a[bounds[g]:bounds[g + 1]] = float("nan")
+    d = ops.grouped_gemm_wgrad(a, b, gu.offsets(counts), out_dtype=DT[out])
+    for g, (lo, hi) in enumerate(zip(bounds, bounds[1:])):
+        if g in bad:
+            assert bool(d[g].isnan().all()), g
+        elif lo == hi:
+            assert bool((d[g] == 0).all()), g
+        else:
+            gu.assert_close(d[g], *want(a[lo:hi], b[lo:hi], DT[out]), "group %d" % g)
