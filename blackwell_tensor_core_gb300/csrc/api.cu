@@ -1115,7 +1115,7 @@ bwg_status runtime_device(Runtime* out) {
     return BWG_ERR_CUDA;
   }
   *out = Runtime{dev, st->sm_count, st->max_smem, st->err, g_timeout_ns.load(), g_tx_extra.load(),
-                 st->clusters_2cta, st->clusters_2c, st->clusters_grouped_2c, no_tail_split_from_env(), g_trace.load()};
+                 st->clusters_2cta, st->clusters_2c, no_tail_split_from_env(), g_trace.load()};
   return BWG_OK;
 }
 

@@ -9,8 +9,8 @@
 namespace bwg {
 
 constexpr int kThreads = 192;        // warp 0 TMA, warp 1 MMA, warps 2..5 epilogue
-constexpr int kThreads2C = 384;      // two-consumer pair kernel: 12 warps
-// Registers per thread of the two-consumer kernel: at launch (one CTA per SM,
+constexpr int kThreads2C = 384;      // pair kernels of 12 warps: two consumers, or eight epilogue warps
+// Registers per thread of these kernels: at launch (one CTA per SM,
 // 65,536 / 384 rounded down to a multiple of 8), and the split after set-up
 // between warpgroup 0 (TMA, MMA) and the two epilogue warpgroups.
 constexpr uint32_t kRegsLaunch2C = 168;
@@ -204,9 +204,8 @@ cudaError_t launch_grouped_2c(const GroupedParams& p, int grid, size_t smem, cud
 int max_active_clusters_grouped_2c(size_t smem);
 cudaError_t launch_grouped_2cta(const GroupedParams& p, int grid, size_t smem, cudaStream_t s,
                                 bool swiglu = false);
-// Gated kernels (gemm_gated.cu): epi = 1 H (two: two consumers), 2 H and gate and
-// up in 8 bits, 3 the gradients of gate and up.  Grouped: 2 and 3, cluster launch
-// control.
+// Gated kernels (gemm_gated.cu): epi = 1 H, 2 H and gate and up in 8 bits, 3 the
+// gradients of gate and up.  Grouped: 2 and 3, cluster launch control.
 cudaError_t launch_gated_dense(const DenseGatedParams& p, int epi, int grid, size_t smem, cudaStream_t s);
 cudaError_t launch_gated_grouped(const GroupedGatedParams& p, int epi, int grid, size_t smem, cudaStream_t s);
 // Transposed A (gemm_tn.cu): two consumers with sums in TMEM, or one (joined)

@@ -19,7 +19,6 @@ struct Runtime {
   unsigned tx_extra;              // test hook: extra bytes expected per stage (0 normally)
   int pairs;                      // CTA pairs of the one-consumer kernels that run at once
   int pairs_2c;                   // of the two-consumer kernels
-  int pairs_grouped_2c;           // of the grouped two-consumer kernels
   int no_tail_split;              // 1: never cut the tiles of the last wave
   unsigned long long* trace;      // unit trace of the pair kernels, or nullptr
 };

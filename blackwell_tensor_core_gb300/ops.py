@@ -413,7 +413,8 @@ def set_watchdog_ns(ns: int) -> None:
 
 def debug_set_trace(buffer: "torch.Tensor | None") -> None:
     """Profiling hook: per-CTA unit timestamps into `buffer` (int64 CUDA
-    tensor of at least grid * 64 * 3 entries), or None to switch off."""
+    tensor of at least grid * 64 * 5 entries, for the largest grid of the pair
+    kernels launched meanwhile), or None to switch off."""
     lib().bwg_debug_set_trace(None if buffer is None else buffer.data_ptr())
 
 
@@ -944,7 +945,8 @@ def dequantize_int8(q: Int8Matrix, out_dtype: torch.dtype = torch.bfloat16, out:
     rows, cols = _int8_check(q, "q")
     dev = q.device
     out, ldo = _fp4_out(out, out_dtype, rows, cols, dev, stream)
-    _check(_on(dev, lib().dequantize_int8, *q._pointers(), q.parts, out.data_ptr(), _OUT_CODES[out.dtype], rows, cols, ldo, _stream_handle(stream, dev)), "dequantize_int8")
+    _check(_on(dev, lib().dequantize_int8, *q._pointers(), q.parts, out.data_ptr(), _OUT_CODES[out.dtype], rows, cols,
+               ldo, _stream_handle(stream, dev)), "dequantize_int8")
     return out
 
 
@@ -1047,8 +1049,8 @@ def gemm_swiglu(x: torch.Tensor, w: torch.Tensor, out: torch.Tensor | None = Non
     out, ldh = _out_rows(out, M, N // 2, dtype, dev, stream)
     kept = Int8Matrix._new(M, N, 2, dev, stream) if keep_int8 else None
     codes, scales = kept._pointers() if keep_int8 else (None, None)
-    _check(_on(dev, lib().gemm_swiglu, x.data_ptr(), w.data_ptr(), out.data_ptr(), codes, scales, _OUT_CODES[dtype], 1 if b_transposed else 0, M, N, K, ldx, ldw, ldh, _stream_handle(stream, dev)),
-           "gemm_swiglu")
+    _check(_on(dev, lib().gemm_swiglu, x.data_ptr(), w.data_ptr(), out.data_ptr(), codes, scales, _OUT_CODES[dtype],
+               1 if b_transposed else 0, M, N, K, ldx, ldw, ldh, _stream_handle(stream, dev)), "gemm_swiglu")
     return (out, kept) if keep_int8 else out
 
 

@@ -480,13 +480,15 @@ void bwg_debug_set_tx_extra(unsigned int bytes);
 
 /*
  * Profiling hook: while `buffer` (device memory, or NULL to switch off) is
- * set, every launch of the dense and grouped pair kernels records, for each
+ * set, every launch of the pair kernels (dense, grouped, gated and transposed;
+ * those that join sums in registers record only the first two words) records, for each
  * CTA b and each of its first 64 work units i, five 64-bit words at
  * buffer[(b * 64 + i) * 5]: the unit's index in the schedule, the global
  * time (ns) when the TMA producer started it, the global time when the
  * first epilogue warp finished it, and when that warp saw the accumulator
  * full and handed it back to the MMA issuer.  The buffer needs
- * grid x 64 x 40 bytes;
+ * grid x 64 x 40 bytes for the largest grid launched meanwhile (grids whose
+ * units are claimed at run time have a CTA pair for every unit);
  * the caller owns it and reads it after synchronising.  Launches of the
  * small-M kernel through gemm_bf16 / gemm_fp16 record instead eight words per
  * CTA b at buffer[8 * b] (grid x 64 bytes), global times in ns (0: not
@@ -516,10 +518,10 @@ void bwg_debug_set_trace(void* buffer);
  *                      evict-last (default 2; 0 with the cluster split)
  *   BWG_GROUPED_1C     1: grouped kernels with one MMA consumer (256-row units)
  *   BWG_GROUPED_SWAP   1: swapped-operand group ends (one-consumer grouped kernel)
- * The gated, transposed and 8-bit calls go by BWG_NO_TAIL_SPLIT alone.
  *   BWG_B_ONE_BOX      0: dense pair kernels load a CTA's B stage as two
  *                      64-column boxes (default: one load where N % 64 == 0
  *                      or B is [N, K])
+ * The gated, transposed and 8-bit calls go by BWG_NO_TAIL_SPLIT alone.
  * ------------------------------------------------------------------- */
 
 /* ---------------------------------------------------------------------
