@@ -142,9 +142,10 @@ int tn_max_rows(int out_dtype) {
 
 // The cheapest by an estimate in us: a tile's k-blocks, filling the ring and storing
 // the tile, and for slices a launch and 8 bytes an element of every plane at 6 TB/s.
-// 20011 rows of 1000 x 1416: 256x256 tiles in one slice 106 us, in three 58, 512x256
-// tiles in six 50.  At 13 sizes from 256 x 256 to 4096 x 8192 the chosen form is at
-// most 8% slower than the best of twenty (2.5% on average).
+// 20011 rows of 1000 x 1416: 256x256 tiles in one slice 106 us, in three 57, 512x256
+// tiles in six 50.  At 16 sizes from 256 x 256 to 4096 x 8192 the chosen form is at
+// most 15% slower than the best of up to 26 (4% on average; 300 to 1500 rows are
+// where it misses).
 TnPlan tn_plan(int M, int N, int rows, int G, int out_dtype, int pairs, int pairs_2c) {
   // all rows may be one group's
   const int max_rows = tn_max_rows(out_dtype);
