@@ -64,7 +64,7 @@ typedef enum { BWG_OUT_BF16 = 0, BWG_OUT_FP32 = 1, BWG_OUT_FP16 = 2 } bwg_out_dt
  *   The small-M kernel may share a tile's k-blocks among several CTAs.  With
  *   few column tiles (at most half the SMs' worth) the CTAs form clusters and
  *   sum their partials in shared memory; with more tiles than SMs and a ragged
- *   last wave they share k-blocks stream-K style through a device workspace
+ *   last wave, or too few k-blocks for a cluster, they share k-blocks stream-K style through a device workspace
  *   that the library allocates (cudaMalloc) on the first such call on a
  *   stream and keeps, until the process exits, for later calls on that
  *   stream (streams are told apart by their runtime id, so the per-thread
@@ -347,7 +347,7 @@ const char* bwg_status_string(int status);
  *   16-byte aligned, scales FP32 [M, 2 ceil(I / 64)] dense.
  * Leading dimensions in elements, multiples of 8; N a multiple of 16 and every
  * base 16-byte aligned, else BWG_ERR_ALIGNMENT.  M, N = 0: nothing is done; K = 0
- * writes zeros.
+ * writes zeros (the grouped forms too, to every row).
  * gemm_swiglu_grad: from dH [M, I] the gradients of the projections,
  *   dGU = [dgate | dup] [M, N], dgate = dH * up * s (1 + gate (1 - s)) with
  *   s = 1 / (1 + e^-gate), dup = dH * silu(gate); gate and up are multiplied out
@@ -408,7 +408,8 @@ bwg_status swiglu_grad_int8(const void* dH, const void* codes, const float* scal
  * nothing else touches until the call's work is done, BWG_ERR_INVALID_ARG without.
  * The sums' order is fixed: equal calls on one kind of GPU give equal results.
  * FP32 results are sums of 512 rows each, joined with rounding to nearest: a sum
- * that stays on the tensor cores loses bits towards zero at every step.
+ * that stays on the tensor cores loses bits towards zero at every step.  For FP16
+ * and BF16 results at most 8192 and 65536 rows stay there (an eighth of a rounding).
  */
 bwg_status gemm_tn(const void* A, const void* B, void* D, int dtype, int out_dtype, int M, int N, int K, int lda,
                    int ldb, int ldd, void* workspace, long long workspace_bytes, void* stream);
