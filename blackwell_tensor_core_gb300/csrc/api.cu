@@ -855,6 +855,7 @@ bwg_status run_dense(bool fp16_in, const void* A, const void* B, void* D, int M,
   p.tx_extra = g_tx_extra.load();
   p.trace = g_trace.load();
   p.no_tail_split = no_tail_split_from_env();
+  p.box_cols = box_columns(N, oe);
   p.direct_store = direct_store_from_env() ? 1 : 0;
   if (pl.kernel == BWG_KERNEL_2CTA)
     return launch_status(launch_gemm_2cta(p, pl.grid, pl.smem_total, stream));
@@ -937,6 +938,7 @@ bwg_status run_grouped(bool fp16, const void* A, const void* const* B, void* D,
     p.N = n_out;
     p.K = K;
     p.ldd = n_out;
+    p.box_cols = n_out;  // rows of whole 16 bytes
     p.num_n_tiles = ceil_div(n_out, swiglu ? kTileN / 2 : kTileN);
     p.swiglu_up = swiglu ? n_out : 0;
     p.num_m_tiles = 0;

@@ -832,7 +832,8 @@ __device__ void gemm_body(const PT& P, const GemmParams& p) {
       // column col0 (of the gate or up block `part`, or of plane `part`).
       auto emit = [&](int col0, const uint32_t (&pk)[32], int part) __attribute__((always_inline)) {
         if (col0 >= p.N) return;
-        const bool whole_box = TN || (!p.direct_store && (!GROUPED || (row_w + 32 <= tl.row_end)));
+        const bool whole_box =
+            (TN || (!p.direct_store && (!GROUPED || (row_w + 32 <= tl.row_end)))) && col0 < p.box_cols;
         if (whole_box) {
           if (lane == 0) bulk_wait_group_read<kEpiBufs - 1>();
           __syncwarp();
@@ -852,29 +853,30 @@ __device__ void gemm_body(const PT& P, const GemmParams& p) {
           }
           buf = (buf + 1u) % kEpiBufs;
         } else {
-          // Ragged end of a group, or the register-store epilogue: each
-          // thread stores its own row (64 or 32 columns), if inside.
+          // Ragged end of a group, rows that end inside 16 bytes, or the
+          // register-store epilogue: each thread stores its own row (64 or 32
+          // columns), if inside.
           const int row = row_w + static_cast<int>(lane);
           if (row < tl.row_end) {
             const int elt = out32 ? 4 : 2;
-            uint8_t* drow = static_cast<uint8_t*>(p.d_ptr) +
-                            (static_cast<size_t>(row) * p.ldd + static_cast<size_t>(part) * p.N + col0) * elt;
-            const int ncols = min(sub_cols, p.N - col0);
-            if (ncols == sub_cols) {
+            const size_t at = TN ? (static_cast<size_t>(part) * p.M + row) * p.ldd + col0
+                                 : static_cast<size_t>(row) * p.ldd + static_cast<size_t>(part) * p.N + col0;
+            uint8_t* drow = static_cast<uint8_t*>(p.d_ptr) + at * elt;
+            const int words = min(sub_cols, p.N - col0) * elt / 4;  // whole words of this row
 #pragma unroll
-              for (int j = 0; j < 8; ++j)
+            for (int j = 0; j < 8; ++j) {
+              if (4 * j + 4 <= words) {
                 reinterpret_cast<uint4*>(drow)[j] =
                     make_uint4(pk[4 * j], pk[4 * j + 1], pk[4 * j + 2], pk[4 * j + 3]);
-            } else if (out32) {
+              } else if (4 * j <= words) {  // the last, partial 16 bytes
 #pragma unroll
-              for (int c = 0; c < 32; ++c)
-                if (c < ncols) reinterpret_cast<uint32_t*>(drow)[c] = pk[c];
-            } else {
-#pragma unroll
-              for (int c = 0; c < 64; ++c)
-                if (c < ncols)
-                  reinterpret_cast<uint16_t*>(drow)[c] =
-                      static_cast<uint16_t>(pk[c >> 1] >> ((c & 1) * 16));
+                for (int i = 0; i < 4; ++i) {
+                  if (4 * j + i < words)
+                    reinterpret_cast<uint32_t*>(drow)[4 * j + i] = pk[4 * j + i];
+                  else if (4 * j + i == words && !out32 && ((p.N - col0) & 1) != 0)
+                    reinterpret_cast<uint16_t*>(drow)[2 * (4 * j + i)] = static_cast<uint16_t>(pk[4 * j + i]);
+                }
+              }
             }
           }
         }

@@ -133,6 +133,7 @@ void gated_params(const GatedCall& c, const Runtime& rt, int stages, GemmParams*
   p->N = I;
   p->K = c.K;
   p->ldd = c.ldd;
+  p->box_cols = I;  // rows of whole 16 bytes
   p->num_n_tiles = (I + kTileN / 2 - 1) / (kTileN / 2);
   p->num_k_blocks = (c.K + kBK - 1) / kBK;
   p->group_m = kGroupM;

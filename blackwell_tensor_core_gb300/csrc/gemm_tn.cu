@@ -261,6 +261,7 @@ bwg_status run_tn(const TnCall& c, cudaStream_t stream) {
     p.N = c.N;
     p.K = c.rows;
     p.ldd = plane_ld;
+    p.box_cols = splits > 1 ? c.N : box_columns(c.N, oe);  // a plane's rows end in whole 16 bytes
     p.num_m_tiles = ceil_div(c.M, 2 * kRowsPerCta * nc);
     p.num_n_tiles = n_tiles;
     p.group_m = kGroupM;

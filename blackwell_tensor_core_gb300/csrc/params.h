@@ -42,6 +42,14 @@ constexpr int dense_smem(int cg, int stages, bool direct_store = false, int nc =
   return 1024 + stages * dense_stage_bytes(cg, nc) + (direct_store ? 0 : kEpiBytes) + kBarrierArea;
 }
 
+// Columns of D [.., N] that may be stored as boxes.  A TMA store is cut off at D's
+// last column rounded up to 16 bytes and writes zeros up to there: where rows end
+// inside 16 bytes, the columns of the last box are stored from registers.
+constexpr int box_columns(int N, int elt_bytes) {
+  const int box = 128 / elt_bytes;
+  return N % (16 / elt_bytes) == 0 ? N : N / box * box;
+}
+
 // Output element type codes (same values as the C ABI).
 constexpr int kOutBF16 = 0;
 constexpr int kOutF32 = 1;
@@ -79,6 +87,7 @@ struct GemmParams {
   uint32_t tx_extra;         // test hook: extra bytes expected per stage (0 normally)
   int G, g_begin, G_total;   // grouped only: groups in this launch, first group, all groups
   int no_tail_split;         // 1: never split last-wave tiles (tests and measurements)
+  int box_cols;              // columns of D stored as boxes (see box_columns)
   int direct_store;          // 1: epilogue stores rows from registers (no staging, one more stage)
   int swap_ends;             // grouped: 1 = compute group ends of <= 128 rows with swapped operands
   uint32_t idesc_swap;       // grouped: descriptor of the swapped MMA (A MN-major, B K-major)

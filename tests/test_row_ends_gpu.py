@@ -1,0 +1,76 @@
+"""Rows of D that end inside 16 bytes: a product writes its columns and nothing of
+what lies between them and the next row, by every kernel that stores boxes of D.
+Integers of magnitude 2: every sum is exact."""
+import pytest
+import torch
+
+from gpu_util import forced_kernel
+
+pytestmark = pytest.mark.gpu
+
+DT = {"bf16": torch.bfloat16, "fp16": torch.float16, "fp32": torch.float32}
+COLS = [1, 7, 113, 114, 190, 250, 257, 383, 516, 1030]
+
+
+@pytest.fixture(scope="module")
+def ops():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    from blackwell_tensor_core_gb300 import build, ops
+    build.build()
+    return ops
+
+
+@pytest.fixture(autouse=True)
+def no_device_error(ops):
+    yield
+    assert ops.last_device_error() == (0, 0)
+
+
+def ints(rows, cols, dtype, seed, most=2):
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    ld = -(-cols // 8) * 8
+    return torch.randint(-most, most + 1, (rows, ld), generator=g, device="cuda").to(dtype)[:, :cols]
+
+
+def between(M, N, dtype):
+    """(buffer, D): rows of 16 bytes with 7s around D, which ends where the last row does."""
+    ld = -(-N // 8) * 8
+    buf = torch.full((M * ld + 64,), 7.0, dtype=dtype, device="cuda")
+    return buf, buf[:M * ld].view(M, ld)[:, :N]
+
+
+def check(buf, d, want, what):
+    assert torch.equal(d.double(), want), what
+    d.fill_(7.0)
+    assert bool((buf == 7.0).all()), what
+
+
+@pytest.mark.parametrize("out", list(DT))
+@pytest.mark.parametrize("kind,M", [("2cta_2c", 700), ("2cta", 300), ("1cta", 300), ("2cta_mc", 600)])
+def test_dense(ops, kind, M, out):
+    dtype = torch.float16 if out == "fp16" else torch.bfloat16
+    for transposed in (False, True):
+        for N in COLS:
+            a, b = ints(M, 200, dtype, N), ints(200, N, dtype, N + 1, 1)
+            want = a.double() @ b.double()
+            if out != "fp32":
+                want = want.to(DT[out]).double()
+            w = torch.zeros(N, 200, dtype=dtype, device="cuda").copy_(b.t()) if transposed else b
+            buf, d = between(M, N, DT[out])
+            with forced_kernel(kind):
+                ops.gemm(a, w, out=d, b_transposed=transposed)
+            check(buf, d, want, (kind, M, N, out, transposed))
+
+
+@pytest.mark.parametrize("out", list(DT))
+@pytest.mark.parametrize("K,M", [(70, 40), (153, 300), (700, 1000), (9000, 300), (100, 4400)])
+def test_transposed(ops, K, M, out):
+    """Both tile forms, with and without slices."""
+    dtype = torch.float16 if out == "fp16" else torch.bfloat16
+    for N in COLS + [4397]:
+        a, b = ints(K, M, dtype, N), ints(K, N, dtype, N + 1, 1)
+        want = (a.float().t() @ b.float()).to(DT[out]).double()
+        buf, d = between(M, N, DT[out])
+        ops.gemm(a, b, out=d, a_transposed=True)
+        check(buf, d, want, (K, M, N, out))
