@@ -788,6 +788,7 @@ bwg_status run_dense(bool fp16_in, const void* A, const void* B, void* D, int M,
     if (const char* v = std::getenv("BWG_SMALL_M_L2HINT")) p.l2hint = std::atoi(v) & 3;
     p.d = D;
     p.ldd = ldd;
+    p.odd_rows = box_columns(N, oe) != N ? 1 : 0;
     p.trace = g_trace.load();
     if (pl.streamk) {
       p.ws_slots = streamk_max_sharers(pl.tiles, pl.k_blocks, pl.grid);
@@ -1097,6 +1098,9 @@ bwg_status run_small_m_noalloc(const void* A, const void* B, void* D, int M, int
   p.tx_extra = g_tx_extra.load();
   p.streamk = 1;
   p.l2hint = 2;  // B^T evict-first, as in gemm_bf16
+  p.d = D;
+  p.ldd = ldd;
+  p.odd_rows = box_columns(N, oe) != N ? 1 : 0;
   p.ws_slots = slots;
   p.ws_counters = static_cast<int*>(scratch);
   p.ws = reinterpret_cast<float*>(static_cast<unsigned char*>(scratch) + kNoAllocCounterBytes);

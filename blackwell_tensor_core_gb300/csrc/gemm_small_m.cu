@@ -124,6 +124,27 @@ struct Segments {
   }
 };
 
+// The last tile of a D whose rows end inside 16 bytes, out of the staging tile by the
+// 128 epilogue threads.  (The barrier before the next tile is staged, or the end of
+// the kernel, lies behind these reads.)
+__device__ __noinline__ void store_odd_tile(const SmallMParams& p, const uint8_t* staged, uint32_t half_bytes, int n0) {
+  const int elt = p.out_dtype == kOutF32 ? 4 : 2;
+  for (int h = 0; h < 2; ++h) {
+    const int pitch = h == 0 ? min(64, p.tile_n) : p.tile_n - 64;
+    const int col0 = n0 + 64 * h, cols = min(pitch, p.N - col0);
+    if (cols <= 0) break;
+    const uint8_t* src = staged + h * half_bytes;
+    for (int i = static_cast<int>(threadIdx.x) - 64; i < p.M * cols; i += 128) {
+      const int r = i / cols, c = i - r * cols;
+      const size_t from = static_cast<size_t>(r) * pitch + c, to = static_cast<size_t>(r) * p.ldd + col0 + c;
+      if (elt == 4)
+        static_cast<uint32_t*>(p.d)[to] = reinterpret_cast<const uint32_t*>(src)[from];
+      else
+        static_cast<uint16_t*>(p.d)[to] = reinterpret_cast<const uint16_t*>(src)[from];
+    }
+  }
+}
+
 template <bool SW>
 __global__ void __launch_bounds__(kThreads, 1) small_m_kernel(const __grid_constant__ SmallMParams p) {
   extern __shared__ __align__(1024) uint8_t smem_raw[];
@@ -436,6 +457,12 @@ __global__ void __launch_bounds__(kThreads, 1) small_m_kernel(const __grid_const
     auto store_staged = [&](int n0) {
       fence_proxy_async_shared();
       named_bar_sync(1, 128);
+      if constexpr (!SW) {
+        if (p.odd_rows != 0 && n0 + p.tile_n > p.N) {
+          store_odd_tile(p, smem_raw + (smem_d - smem_u32(smem_raw)), half_bytes, n0);
+          return;
+        }
+      }
       if (store_thread) {
         tma_store_2d(&p.map_d, smem_d, n0, 0);
         if (p.tile_n > 64 && n0 + 64 < p.N) tma_store_2d(&p.map_d2, smem_d + half_bytes, n0 + 64, 0);

@@ -192,6 +192,8 @@ struct SmallMParams {
                         // {64, 64, 2, N/64, K/64}, box {64, 64, 2, 1, 2}; stored [2N, K]:
                         // {K, N, 2}, box {64, 64, 2}, two stages {64, N, 2, K/64}, box
                         // {64, 64, 2, 2}
+  int odd_rows;         // 1: rows of D end inside 16 bytes (see box_columns): their last box
+                        // is stored without TMA
   void* d;            // D (split mode stores its rows directly)
   long long ldd;      // D's leading dimension, elements
   // Optional trace (nullptr: off): per CTA eight global-timer stamps (ns),

@@ -1,6 +1,8 @@
 """Rows of D that end inside 16 bytes: a product writes its columns and nothing of
 what lies between them and the next row, by every kernel that stores boxes of D.
 Integers of magnitude 2: every sum is exact."""
+import ctypes
+
 import pytest
 import torch
 
@@ -47,7 +49,7 @@ def check(buf, d, want, what):
 
 
 @pytest.mark.parametrize("out", list(DT))
-@pytest.mark.parametrize("kind,M", [("2cta_2c", 700), ("2cta", 300), ("1cta", 300), ("2cta_mc", 600)])
+@pytest.mark.parametrize("kind,M", [("2cta_2c", 700), ("2cta", 300), ("1cta", 300), ("2cta_mc", 600), (None, 40), (None, 128)])
 def test_dense(ops, kind, M, out):
     dtype = torch.float16 if out == "fp16" else torch.bfloat16
     for transposed in (False, True):
@@ -61,6 +63,38 @@ def test_dense(ops, kind, M, out):
             with forced_kernel(kind):
                 ops.gemm(a, w, out=d, b_transposed=transposed)
             check(buf, d, want, (kind, M, N, out, transposed))
+
+
+@pytest.mark.parametrize("out", list(DT))
+def test_few_rows_of_every_schedule(ops, out, monkeypatch):
+    """The small-M kernel: whole tiles (one and several a CTA), cluster split, stream-K, other tile widths."""
+    dtype = torch.float16 if out == "fp16" else torch.bfloat16
+    for env, N, K in (({}, 113, 4096), ({"BWG_SMALL_M_SPLIT": "0"}, 113, 640), ({}, 19463, 640), ({}, 24999, 128),
+                      ({"BWG_STREAMK": "0"}, 24999, 640),
+                      ({"BWG_STREAMK": "1"}, 1001, 2048), ({"BWG_SMALL_M_TILE_N": "80"}, 250, 640),
+                      ({"BWG_SMALL_M_TILE_N": "48"}, 250, 640)):
+        for M in (1, 17, 72):
+            for k, v in env.items():
+                monkeypatch.setenv(k, v)
+            a, b = ints(M, K, dtype, N), ints(K, N, dtype, N + 1, 1)
+            want = (a.float() @ b.float()).to(DT[out]).double()  # integers below 2^24
+            buf, d = between(M, N, DT[out])
+            ops.gemm(a, b, out=d)
+            for k in env:
+                monkeypatch.delenv(k)
+            check(buf, d, want, (env, M, N, K, out))
+
+
+def test_few_rows_without_allocation(ops):
+    L = ctypes.CDLL(ops.LIB_PATH)  # (the Python calls have no such form)
+    f, vp, i = L.gemm_bf16_small_m_noalloc, ctypes.c_void_p, ctypes.c_int
+    f.argtypes, f.restype = [vp, vp, vp, i, i, i, i, i, i, i, vp], i
+    for N in (1, 113, 1001):
+        a, b = ints(17, 640, torch.bfloat16, N), ints(640, N, torch.bfloat16, N + 1, 1)
+        buf, d = between(17, N, torch.float32)
+        assert f(a.data_ptr(), b.data_ptr(), d.data_ptr(), 17, N, 640, 640, b.stride(0), d.stride(0), 1,
+                 torch.cuda.current_stream().cuda_stream) == 0
+        check(buf, d, a.double() @ b.double(), N)
 
 
 @pytest.mark.parametrize("out", list(DT))
