@@ -985,6 +985,8 @@ def _gemm_tn(A, B, out, out_dtype, stream, b_transposed) -> torch.Tensor:
     lda, ldb = _lead(A, "A"), _lead(B, "B")
     _fits("M or N", M, N)
     out, ldd = _fp4_out(out, out_dtype, M, N, dev, stream)
+    if M == 1:
+        ldd = -(-N // 8) * 8  # of no matter to a single row, but the library wants rows of 16 bytes
     need, work = _tn_work(M, N, K, 1, _OUT_CODES[out.dtype], dev, stream)
     _check(_on(dev, lib().gemm_tn, A.data_ptr(), B.data_ptr(), out.data_ptr(), _OUT_CODES[A.dtype],
                _OUT_CODES[out.dtype], M, N, K, lda, ldb, ldd, None if work is None else work.data_ptr(), need,

@@ -398,3 +398,12 @@ def test_a_single_row_has_a_stride_that_fits(rec):  # noqa: F811
         assert rec.calls[-1][1][8:10] == (64, 128)
         ops.swiglu_grad(wide(1, 64, ld), int8(1, 128, 2))
         assert rec.calls[-1][1][8] == 64
+
+
+def test_a_result_of_one_row_has_a_stride_that_fits(rec):  # noqa: F811
+    """D of one row of 113 columns: rows of 16 bytes are of no matter to it."""
+    for out in (None, wide(1, 113, 120), wide(1, 113, 113)):
+        ops.gemm(wide(4, 1, 8), wide(4, 113, 120), out=out, a_transposed=True)
+        assert rec.calls[-1][1][10] == 120
+    ops.gemm(wide(4, 2, 8), wide(4, 113, 120), out=wide(2, 113, 128), a_transposed=True)
+    assert rec.calls[-1][1][10] == 128

@@ -108,3 +108,16 @@ def test_transposed(ops, K, M, out):
         buf, d = between(M, N, DT[out])
         ops.gemm(a, b, out=d, a_transposed=True)
         check(buf, d, want, (K, M, N, out))
+
+
+@pytest.mark.parametrize("out", list(DT))
+def test_transposed_one_row(ops, out):
+    """D of one row, new and in a buffer that ends with it."""
+    for N in (1, 113, 257):
+        a, b = ints(700, 1, torch.bfloat16, N), ints(700, N, torch.bfloat16, N + 1, 1)
+        want = (a.float().t() @ b.float()).to(DT[out]).double()
+        assert torch.equal(ops.gemm(a, b, out_dtype=DT[out], a_transposed=True).double(), want)
+        buf = torch.full((N + 64,), 7.0, dtype=DT[out], device="cuda")
+        d = buf[:N].view(1, N)
+        ops.gemm(a, b, out=d, a_transposed=True)
+        check(buf, d, want, (N, out))
