@@ -14,7 +14,9 @@
  *     owns every buffer; the library keeps no pointer after the call returns.
  *   - Every base pointer must be 16-byte aligned and every leading dimension
  *     times the element size a multiple of 16 bytes (the TMA engine's rule);
- *     otherwise the call returns BWG_ERR_ALIGNMENT and does nothing.
+ *     otherwise the call returns BWG_ERR_ALIGNMENT and does nothing.  Of an
+ *     output nothing is written but its columns, also where they end inside
+ *     16 bytes.
  *   - Calls are asynchronous: work is enqueued on `stream` (a cudaStream_t
  *     passed as void*, NULL = legacy default stream) and the call never
  *     synchronises.  The return value reports host-detectable errors and
