@@ -842,7 +842,7 @@ class Int8Matrix:
     parts   1, or 2 for [gate | up], whose halves have blocks of their own
     """
 
-    __slots__ = ("_codes", "_scales", "parts", "_buffer", "_shape", "_blocks")
+    __slots__ = ("_codes", "_scales", "parts", "_buffer", "_shape", "_kept_parts")
 
     def __init__(self, codes, scales, parts=1):
         self._codes = codes
@@ -850,7 +850,7 @@ class Int8Matrix:
         self.parts = parts
         self._buffer = None
         self._shape = None
-        self._blocks = None
+        self._kept_parts = parts
 
     @classmethod
     def _new(cls, rows: int, cols: int, parts: int, dev, stream):
@@ -858,8 +858,7 @@ class Int8Matrix:
         when they are asked for: a tensor costs a small call 4 us."""
         q = cls(None, None, parts)
         q._shape = rows, cols
-        q._blocks = _int8_blocks(cols, parts)
-        q._buffer = _new((_int8_scales_at(rows, cols) + 4 * rows * q._blocks,), torch.int8, dev, stream)
+        q._buffer = _new((_int8_scales_at(rows, cols) + 4 * rows * _int8_blocks(cols, parts),), torch.int8, dev, stream)
         return q
 
     @property
@@ -873,7 +872,8 @@ class Int8Matrix:
     def scales(self):
         if self._scales is None:
             rows, cols = self._shape
-            self._scales = self._buffer[_int8_scales_at(rows, cols):].view(torch.float32).view(rows, self._blocks)
+            self._scales = self._buffer[_int8_scales_at(rows, cols):].view(torch.float32).view(
+                rows, _int8_blocks(cols, self._kept_parts))
         return self._scales
 
     @property
@@ -906,9 +906,10 @@ def _int8_check(q: Int8Matrix, name: str, parts: int | None = None) -> tuple[int
         raise ValueError("%s must have %s, got %r" % (name, "1 or 2 parts" if parts is None else "parts=%d" % parts,
                                                       q.parts))
     if q._buffer is not None:
-        cols = q._shape[1]
-        if cols % q.parts or _int8_blocks(cols, q.parts) != q._blocks:
-            raise ValueError("%s was not kept in %d parts" % (name, q.parts))
+        if q.parts != q._kept_parts:  # the same blocks where they do not cross the halves
+            cols = q._shape[1]
+            if cols % q.parts or _int8_blocks(cols, q.parts) != _int8_blocks(cols, q._kept_parts):
+                raise ValueError("%s was not kept in %d parts" % (name, q.parts))
         return q._shape
     codes, scales = q._codes, q._scales
     if codes.dtype != torch.int8 or codes.dim() != 2 or not codes.is_contiguous() or not codes.is_cuda:
@@ -1135,11 +1136,10 @@ def _block_sizes(M: int, N: int, K: int, whole_rows: bool) -> None:
         raise ValueError("gradients of %d columns: their rows must be whole 16 bytes, multiples of 8" % K)
 
 
-def _rows16(what: str, *matrices) -> None:
-    """The same of matrices that the TMA engine reads: (tensor, row stride) of each."""
-    for t, ld in matrices:
-        if (ld % 8 or t.data_ptr() % 16) and t.numel():
-            raise BwgError(2, what)
+def _rows16(what: str, t: torch.Tensor, ld: int) -> None:
+    """The same of a matrix that the TMA engine reads."""
+    if (ld % 8 or t.data_ptr() % 16) and t.numel():
+        raise BwgError(2, what)
 
 
 def _read_back(q: Int8Matrix, K: int, dtype, dev, stream) -> torch.Tensor:
@@ -1163,8 +1163,10 @@ def gemm_swiglu_grad(dh: torch.Tensor, x, w: torch.Tensor, kept: Int8Matrix | No
     M, K = _block_operands(dh, x, kept, with_h, N)
     _block_sizes(M, N, K, need_dx or (need_dw and b_transposed))
     lddh = _lead(dh, "dh")
-    if M:
-        _rows16("gemm_swiglu_grad", (dh, lddh), *([(w, ldw)] if need_dx or kept is None else []))
+    if M and (lddh % 8 or dh.data_ptr() % 16):
+        _rows16("gemm_swiglu_grad", dh, lddh)
+    if M and (ldw % 8 or w.data_ptr() % 16) and (need_dx or kept is None):
+        _rows16("gemm_swiglu_grad", w, ldw)
     if not need_dw and kept is not None:
         x, ldx = None, 0
     elif isinstance(x, Int8Matrix):
@@ -1172,7 +1174,7 @@ def gemm_swiglu_grad(dh: torch.Tensor, x, w: torch.Tensor, kept: Int8Matrix | No
         ldx = _lead(x, "x")
     else:
         ldx = _lead(x, "x")
-        _rows16("gemm_swiglu_grad", (x, ldx))
+        _rows16("gemm_swiglu_grad", x, ldx)
     return _on(dev, _block_grad, dh, lddh, x, ldx, w, ldw, kept, with_h, b_transposed, need_dx, need_dw, M, N, K, dev,
                stream)
 
